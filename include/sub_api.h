@@ -265,6 +265,121 @@ int32_t sub_kv_compact(const sub_kv_cache* kv, int64_t root_pos, const int32_t* 
                        const int32_t* n_accepted, int32_t max_accept, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* Batches of sequences over one paged cache.  The calls below serve the same
+ * draft-and-verify step for many sequences at once, with the lengths on the
+ * device (a captured graph replays with new ones) and chains of drafted
+ * tokens ("Low-Bit Shadow" report 6.2, Leviathan et al.) in place of one tree.
+ *
+ * Sequence b owns rows [start[b], start[b+1]) of the caller's row tensors; its
+ * row i stands at position pos[b] + i.  Rows before start[0] and from
+ * start[n_seqs] on (padding) belong to no sequence: no call reads or writes
+ * them.  start must not decrease; entries outside [0, n_rows] are clamped.
+ * A cache used here has one page-table row per sequence:
+ * page_table[b * P + t / page_size], P = ceil(capacity / page_size), and
+ * n_pages * n_layers pages of any sequence in one pool.  An entry outside
+ * [0, n_pages) is no page: its positions hold no keys, are not written, and
+ * read as zeros.  The same goes for positions outside [0, capacity). */
+typedef struct {
+  const int32_t* start;   /* device [n_seqs + 1] */
+  const int32_t* pos;     /* device [n_seqs] */
+  int32_t n_seqs;         /* 1 .. SUB_MAX_SEQS */
+  int32_t n_rows;         /* rows of the row tensors */
+  int64_t max_keys;       /* about the largest pos[b] + rows of b, 0 = capacity: how the
+                             work is split; only speed depends on it */
+} sub_batch;
+#define SUB_MAX_SEQS 1024
+
+/* An 8-bit paged cache.  The D values x of one (position, KV head) row are
+ * kept as codes with one fp32 scale, in IEEE fp32 operations:
+ *   a = max |x|,  scale = a / 127,  code = 128 + rint_even(x * (127 / a));
+ * a < 2^-100: scale 1, codes 128; a row that is not finite: scale NaN, codes
+ * 128.  The value is (code - 128) * scale.
+ * Codes lie like the values of sub_kv_cache ([layer][page][head][page_size]
+ * [head_dim]), scales like them without the last axis. */
+typedef struct {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* page_table;   /* device */
+  int32_t n_layers;
+  int32_t n_heads_kv;
+  int32_t head_dim;            /* 64 or 128 */
+  int32_t page_size;           /* multiple of 16 */
+  int32_t n_pages;
+  int64_t capacity;            /* positions covered by one page-table row */
+} sub_kv8_cache;
+
+/* Write the batch's new rows K, V ([n_rows, Hkv, head_dim] bf16; consecutive
+ * rows ldk, ldv elements apart, multiples of 8, so that they may be a part of a
+ * q/k/v product) at their positions in one layer of the cache: copied
+ * (sub_kv_append), or quantised as they are written (sub_kv8_append).  Two rows
+ * of a batch must not stand at the same place of the pool. */
+int32_t sub_kv_append(const sub_bf16* K, int64_t ldk, const sub_bf16* V, int64_t ldv,
+                      const sub_kv_cache* kv, int32_t layer, const sub_batch* batch,
+                      void* stream);
+int32_t sub_kv8_append(const sub_bf16* K, int64_t ldk, const sub_bf16* V, int64_t ldv,
+                       const sub_kv8_cache* kv, int32_t layer, const sub_batch* batch,
+                       void* stream);
+/* Read rows back: K, V [n_rows, Hkv, head_dim] bf16 (contiguous) get the
+ * values at the batch's positions, rounded once to bf16. */
+int32_t sub_kv8_read(const sub_kv8_cache* kv, int32_t layer, const sub_batch* batch, sub_bf16* K,
+                     sub_bf16* V, void* stream);
+
+/* Attention of the batch's new rows over the paged cache, which already holds
+ * their own K and V: row i of sequence b (Q [n_rows, Hq, head_dim] bf16, rows
+ * ldq elements apart, a multiple of 8) reads the keys at positions
+ * 0 .. pos[b] + i of its sequence.  O [n_rows, Hq, head_dim] bf16 (contiguous,
+ * not overlapping Q) = softmax(q K^T * softmax_scale) V, sums in fp32; a row
+ * with no key gives zeros; what a row does not read (later keys, other pages,
+ * whatever they hold) does not change it.
+ * Hq % Hkv == 0, Hq / Hkv <= 64; head_dim 64 or 128.  Which sequences share
+ * the batch, and max_keys, move a row's result by rounding only; the same call
+ * gives the same bits.  workspace: sub_chunk_attn_workspace(...) bytes of
+ * device memory, 16-byte aligned, used by this call alone until it is done
+ * (its contents do not matter); NULL: drawn from the stream's memory pool. */
+int32_t sub_chunk_attn(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q, const sub_kv_cache* kv,
+                       int32_t layer, const sub_batch* batch, float softmax_scale, sub_bf16* O,
+                       void* workspace, int64_t workspace_bytes, void* stream);
+int32_t sub_chunk_attn8(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q,
+                        const sub_kv8_cache* kv, int32_t layer, const sub_batch* batch,
+                        float softmax_scale, sub_bf16* O, void* workspace,
+                        int64_t workspace_bytes, void* stream);
+/* *bytes = workspace that one sub_chunk_attn / sub_chunk_attn8 call of these
+ * sizes may need (0: none). */
+int32_t sub_chunk_attn_workspace(int32_t n_heads_q, int32_t n_heads_kv, int32_t head_dim,
+                                 int32_t n_seqs, int32_t n_rows, int64_t* bytes);
+
+/* probs[r, v] = exp(z[r, v] / T) / sum_w exp(z[r, w] / T) for fp32 logits z
+ * [rows, V], sums in fp32; probs [rows, V] may be the logits themselves.
+ * -infinity entries get 0, a row of nothing else gets zeros.  1 <= V <= 2^20,
+ * temperature in [1e-6, 1e6]; logits and probs 16-byte aligned. */
+int32_t sub_probs(const float* logits, int64_t rows, int64_t V, float temperature, float* probs,
+                  void* stream);
+
+/* Verify chains of drafted tokens against the target's probabilities from
+ * given random numbers ("Low-Bit Shadow" report 6.2, Leviathan et al.: the
+ * emitted tokens are distributed as the target's).  Sequence b has drafted
+ * tokens x_i = draft[b, i], i < n_draft; the first entry outside [0, V) ends
+ * its draft.  p [n_seqs, n_draft + 1, V] are the target's probabilities before
+ * each of them and after the last, q [n_seqs, n_draft, V] the draft's that x_i
+ * was sampled from (NULL: x_i was certain), u [n_seqs, n_draft + 1] numbers in
+ * [0, 1).  Token i is accepted while u[b, i] q_i(x_i) < p_i(x_i) (decided
+ * exactly).  Then one more token is sampled with u[b, n_draft]: from
+ * max(p_a - q_a, 0) (one fp32 subtraction) after a rejection at a, from p_a
+ * where the draft ended: the smallest v whose running sum exceeds u times the
+ * whole sum.  The weights, clamped to [0, 1], are summed exactly as multiples
+ * of 2^-43; a rejection whose weights sum to 0 samples p_a, and a row that sums
+ * to 0 gives token 0.
+ * tokens [n_seqs, n_draft + 1] gets the accepted tokens, the sampled one, then
+ * -1; n_accepted [n_seqs] how many were accepted.  n_draft >= 0 (0: plain
+ * sampling from p, draft and q may be NULL), 1 <= V <= 2^20; p and q 16-byte
+ * aligned. */
+int32_t sub_verify_sample(const float* p, const float* q, const int32_t* draft, const float* u,
+                          int32_t n_seqs, int32_t n_draft, int64_t V, int32_t* tokens,
+                          int32_t* n_accepted, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Model.  Layers [0, n_resident) keep bf16 weights on the device; layers
  * [n_resident, n_layers) are offloaded: their bf16 originals live in pinned
  * host memory and stream over the host link into a device staging ring for

@@ -41,6 +41,17 @@ class KVCache(C.Structure):
                 ("n_pages", _i32), ("capacity", _i64)]
 
 
+class KV8Cache(C.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("page_table", _vp),
+                ("n_layers", _i32), ("n_heads_kv", _i32), ("head_dim", _i32),
+                ("page_size", _i32), ("n_pages", _i32), ("capacity", _i64)]
+
+
+class Batch(C.Structure):
+    _fields_ = [("start", _vp), ("pos", _vp), ("n_seqs", _i32), ("n_rows", _i32),
+                ("max_keys", _i64)]
+
+
 class Tree(C.Structure):
     _fields_ = [("token", _vp), ("parent", _vp), ("depth", _vp), ("score", _vp), ("anc", _vp),
                 ("width", _i32), ("max_depth", _i32)]
@@ -110,6 +121,18 @@ _verify_accept_static = _decl("sub_verify_accept_static",
                               [_vp, C.POINTER(Tree), _i32, _i64, _i32, _f32, _u64, _i64, _vp, _vp,
                                _vp, _vp, _vp])
 _kv_compact = _decl("sub_kv_compact", [C.POINTER(KVCache), _i64, _vp, _vp, _i32, _vp])
+_KV, _KV8, _BATCH = C.POINTER(KVCache), C.POINTER(KV8Cache), C.POINTER(Batch)
+_kv_append = _decl("sub_kv_append", [_vp, _i64, _vp, _i64, _KV, _i32, _BATCH, _vp])
+_kv8_append = _decl("sub_kv8_append", [_vp, _i64, _vp, _i64, _KV8, _i32, _BATCH, _vp])
+_kv8_read = _decl("sub_kv8_read", [_KV8, _i32, _BATCH, _vp, _vp, _vp])
+_chunk_attn = _decl("sub_chunk_attn", [_vp, _i64, _i32, _KV, _i32, _BATCH, _f32, _vp, _vp, _i64,
+                                       _vp])
+_chunk_attn8 = _decl("sub_chunk_attn8", [_vp, _i64, _i32, _KV8, _i32, _BATCH, _f32, _vp, _vp,
+                                         _i64, _vp])
+_chunk_attn_workspace = _decl("sub_chunk_attn_workspace", [_i32, _i32, _i32, _i32, _i32,
+                                                           C.POINTER(_i64)])
+_probs = _decl("sub_probs", [_vp, _i64, _i64, _f32, _vp, _vp])
+_verify_sample = _decl("sub_verify_sample", [_vp, _vp, _vp, _vp, _i32, _i32, _i64, _vp, _vp, _vp])
 _model_create = _decl("sub_model_create", [C.POINTER(ModelDesc), C.POINTER(_vp)])
 _model_destroy = _decl("sub_model_destroy", [_vp])
 _model_memory = _decl("sub_model_memory", [_vp, C.POINTER(_i64)])
@@ -129,7 +152,9 @@ EXPORTED = ["sub_last_error", "sub_version", "sub_pipeline_timeouts", "sub_bound
             "sub_wq_pack", "sub_wq_dequant", "sub_wq_gemm", "sub_wq_pack_hqq",
             "sub_bf16_gemm", "sub_tree_attn", "sub_draft_expand", "sub_verify_accept",
             "sub_verify_accept_static",
-            "sub_kv_compact", "sub_model_create", "sub_model_destroy", "sub_model_memory",
+            "sub_kv_compact", "sub_kv_append", "sub_kv8_append", "sub_kv8_read", "sub_chunk_attn",
+            "sub_chunk_attn8", "sub_chunk_attn_workspace", "sub_probs", "sub_verify_sample",
+            "sub_model_create", "sub_model_destroy", "sub_model_memory",
             "sub_model_forward", "sub_model_kv", "sub_generate", "sub_prefill",
             "sub_decode_cycles", "sub_decode_read", "sub_cycle_info"]
 
@@ -331,6 +356,234 @@ def make_kv(n_layers, n_heads_kv, head_dim, capacity, page_size=64, device="cuda
     st = KVCache(k.data_ptr(), v.data_ptr(), pt.data_ptr(), n_layers, n_heads_kv, head_dim,
                  page_size, n_pages, n_pages * page_size)
     return st, (k, v, pt)
+
+
+# ----------------------------------------------- batches of sequences --
+def _need(ok, msg):
+    if not ok:
+        raise SubError(SUB_EINVAL, msg)
+
+
+def _on(t, dtype, name, device=None):
+    """A tensor of this type on the GPU (that of the other tensors)."""
+    _need(isinstance(t, torch.Tensor) and t.dtype == dtype, f"{name}: a {dtype} tensor is needed")
+    _need(t.is_cuda and (device is None or t.device == device),
+          f"{name}: must be on {device or 'the GPU'}")
+    return t
+
+
+def _dense(t, dtype, shape, name, device):
+    _need(tuple(_on(t, dtype, name, device).shape) == tuple(shape) and t.is_contiguous(),
+          f"{name}: must be contiguous, of shape {tuple(shape)}")
+    return t
+
+
+def _rows(t, shape, name, device):
+    """[rows, heads, head_dim] bf16 whose rows may lie apart -> row stride."""
+    _on(t, torch.bfloat16, name, device)
+    _need(tuple(t.shape) == tuple(shape), f"{name}: must have shape {tuple(shape)}")
+    n, h, d = t.shape
+    _need((d == 1 or t.stride(2) == 1) and (h == 1 or t.stride(1) == d),
+          f"{name}: the heads of a row must be contiguous")
+    return t.stride(0) if n > 1 else h * d
+
+
+class _at:
+    """The device of the call's tensors as the current one, if it is not."""
+
+    def __init__(self, device):
+        self.device = device
+
+    def __enter__(self):
+        self.back = torch.cuda.current_device()
+        if self.back != self.device.index:
+            torch.cuda.set_device(self.device)
+
+    def __exit__(self, *exc):
+        if self.back != self.device.index:
+            torch.cuda.set_device(self.back)
+
+
+def paged_kv(k, v, page_table) -> KVCache:
+    """A cache of sequences on torch tensors: pools k, v bf16 [n_layers, n_pages,
+    n_heads_kv, page_size, head_dim], page_table int32 [n_seqs, pages per
+    sequence] (entries outside the pool: no page).  Keeps the tensors."""
+    dev = _on(k, torch.bfloat16, "k").device
+    _need(k.dim() == 5, "k: must be [n_layers, n_pages, n_heads_kv, page_size, head_dim]")
+    _dense(k, torch.bfloat16, k.shape, "k", dev)
+    _dense(v, torch.bfloat16, k.shape, "v", dev)
+    _need(page_table.dim() == 2 and page_table.shape[1] >= 1, "page_table: must be [n_seqs, pages]")
+    _dense(page_table, torch.int32, page_table.shape, "page_table", dev)
+    nl, npg, h, ps, d = k.shape
+    kv = KVCache(k.data_ptr(), v.data_ptr(), page_table.data_ptr(), nl, h, d, ps, npg,
+                 page_table.shape[1] * ps)
+    kv.keep, kv.device, kv.n_seqs = (k, v, page_table), dev, page_table.shape[0]
+    return kv
+
+
+def paged_kv8(k, v, k_scale, v_scale, page_table) -> KV8Cache:
+    """An 8-bit cache of sequences: codes uint8 shaped as paged_kv's pools, scales
+    fp32 without the last axis."""
+    dev = _on(k, torch.uint8, "k").device
+    _need(k.dim() == 5, "k: must be [n_layers, n_pages, n_heads_kv, page_size, head_dim]")
+    _dense(k, torch.uint8, k.shape, "k", dev)
+    _dense(v, torch.uint8, k.shape, "v", dev)
+    _dense(k_scale, torch.float32, k.shape[:4], "k_scale", dev)
+    _dense(v_scale, torch.float32, k.shape[:4], "v_scale", dev)
+    _need(page_table.dim() == 2 and page_table.shape[1] >= 1, "page_table: must be [n_seqs, pages]")
+    _dense(page_table, torch.int32, page_table.shape, "page_table", dev)
+    nl, npg, h, ps, d = k.shape
+    kv = KV8Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                  page_table.data_ptr(), nl, h, d, ps, npg, page_table.shape[1] * ps)
+    kv.keep, kv.device = (k, v, k_scale, v_scale, page_table), dev
+    kv.n_seqs = page_table.shape[0]
+    return kv
+
+
+def batch(start, pos, n_rows: int, max_keys: int = 0) -> Batch:
+    """New rows of a batch: sequence b has rows start[b] .. start[b+1] - 1 of the
+    row tensors (n_rows of them), the first at position pos[b]; int32 device
+    tensors [n_seqs + 1] and [n_seqs].  max_keys: about the most keys a sequence has
+    (0: the cache's capacity); only the split of the work depends on it."""
+    _need(start.dim() == 1 and start.shape[0] >= 2, "start: must be [n_seqs + 1]")
+    _dense(start, torch.int32, start.shape, "start", None)
+    _dense(pos, torch.int32, (start.shape[0] - 1,), "pos", start.device)
+    b = Batch(start.data_ptr(), pos.data_ptr(), pos.shape[0], n_rows, max_keys)
+    b.keep, b.device = (start, pos), start.device
+    return b
+
+
+def _same(kv, b):
+    _need(kv.device == b.device, "the batch and the cache must be on one device")
+    _need(kv.n_seqs == b.n_seqs, "page_table and batch must have the same number of sequences")
+
+
+def kv_append(k, v, kv: KVCache, layer: int, batch: Batch, stream=None):
+    """Copy the batch's new rows (bf16 [n_rows, n_heads_kv, head_dim], rows may
+    be strided) into one layer of a paged_kv cache."""
+    _append(_kv_append, k, v, kv, layer, batch, stream)
+
+
+def kv8_append(k, v, kv: KV8Cache, layer: int, batch: Batch, stream=None):
+    """Quantise the batch's new rows into one layer of a paged_kv8 cache."""
+    _append(_kv8_append, k, v, kv, layer, batch, stream)
+
+
+def _append(fn, k, v, kv, layer, batch, stream):
+    _same(kv, batch)
+    shape = (batch.n_rows, kv.n_heads_kv, kv.head_dim)
+    ldk, ldv = _rows(k, shape, "k", kv.device), _rows(v, shape, "v", kv.device)
+    with _at(kv.device):
+        _check(fn(k.data_ptr(), ldk, v.data_ptr(), ldv, C.byref(kv), layer, C.byref(batch),
+                  _stream(stream)))
+
+
+def kv8_read(kv: KV8Cache, layer: int, batch: Batch, out=None, stream=None):
+    """The values at the batch's positions -> (k, v) bf16 [n_rows, n_heads_kv,
+    head_dim].  Rows of no sequence are left as they are in `out`, zero without."""
+    _same(kv, batch)
+    shape = (batch.n_rows, kv.n_heads_kv, kv.head_dim)
+    with _at(kv.device):
+        if out is None:
+            out = tuple(_new(shape, torch.bfloat16, kv.device, stream) for _ in range(2))
+        k, v = out
+        _dense(k, torch.bfloat16, shape, "out[0]", kv.device)
+        _dense(v, torch.bfloat16, shape, "out[1]", kv.device)
+        _check(_kv8_read(C.byref(kv), layer, C.byref(batch), k.data_ptr(), v.data_ptr(),
+                         _stream(stream)))
+    return k, v
+
+
+def _new(shape, dtype, device, stream, zero=True):
+    """A tensor allocated (and zeroed) on the call's stream."""
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
+
+
+def chunk_attn_workspace(n_heads_q: int, n_heads_kv: int, head_dim: int, n_seqs: int,
+                         n_rows: int) -> int:
+    """Bytes of workspace that a chunk_attn call of these sizes may need."""
+    n = _i64()
+    _check(_chunk_attn_workspace(n_heads_q, n_heads_kv, head_dim, n_seqs, n_rows, C.byref(n)))
+    return n.value
+
+
+def chunk_attn(q, kv, layer: int, batch: Batch, scale=None, out=None, workspace=None,
+               stream=None):
+    """Causal attention of the batch's new rows (bf16 [n_rows, n_heads_q,
+    head_dim], rows may be strided) over a paged_kv or paged_kv8 cache that holds
+    their own keys already -> bf16 [n_rows, n_heads_q, head_dim].  Rows of no
+    sequence are left as they are in `out`, zero without.  workspace: a uint8
+    tensor of chunk_attn_workspace bytes; allocated by torch if not given."""
+    _same(kv, batch)
+    dev = kv.device
+    _need(q.dim() == 3, "q: must be [n_rows, n_heads_q, head_dim]")
+    hq = q.shape[1]
+    shape = (batch.n_rows, hq, kv.head_dim)
+    ldq = _rows(q, shape, "q", dev)
+    scale = scale if scale is not None else kv.head_dim ** -0.5
+    with _at(dev):
+        if out is None:
+            out = _new(shape, torch.bfloat16, dev, stream)
+        _dense(out, torch.bfloat16, shape, "out", dev)
+        if workspace is None:
+            n = chunk_attn_workspace(hq, kv.n_heads_kv, kv.head_dim, batch.n_seqs, batch.n_rows)
+            workspace = _new(n, torch.uint8, dev, stream, zero=False)
+        _on(workspace, torch.uint8, "workspace", dev)
+        fn = _chunk_attn8 if isinstance(kv, KV8Cache) else _chunk_attn
+        _check(fn(q.data_ptr(), ldq, hq, C.byref(kv), layer, C.byref(batch), scale,
+                  out.data_ptr(), workspace.data_ptr() or None, workspace.numel(),
+                  _stream(stream)))
+    return out
+
+
+def probs(logits, temperature: float = 1.0, out=None, stream=None):
+    """softmax(logits / temperature) of fp32 [rows, V]; `out` may be the logits."""
+    dev = _on(logits, torch.float32, "logits").device
+    _need(logits.dim() == 2, "logits: must be [rows, V]")
+    _dense(logits, torch.float32, logits.shape, "logits", dev)
+    with _at(dev):
+        if out is None:
+            out = _new(logits.shape, torch.float32, dev, stream, zero=False)
+        _dense(out, torch.float32, logits.shape, "out", dev)
+        _check(_probs(logits.data_ptr(), logits.shape[0], logits.shape[1], temperature,
+                      out.data_ptr(), _stream(stream)))
+    return out
+
+
+def verify_sample(p, q, draft, u, out=None, stream=None):
+    """Verify drafted tokens against probabilities from given random numbers:
+    p fp32 [n_seqs, n_draft + 1, V] the target's, q fp32 [n_seqs, n_draft, V] the
+    draft's (None: its tokens were certain), draft int32 [n_seqs, n_draft] (the first
+    entry outside [0, V) ends a sequence's draft), u fp32 [n_seqs, n_draft + 1] in
+    [0, 1) -> (tokens int32 [n_seqs, n_draft + 1]: the accepted ones, the sampled one,
+    then -1; n_accepted int32 [n_seqs]).  draft None: plain sampling from p."""
+    dev = _on(p, torch.float32, "p").device
+    _need(p.dim() == 3 and p.shape[1] >= 1, "p: must be [n_seqs, n_draft + 1, V]")
+    b, n, v = p.shape[0], p.shape[1] - 1, p.shape[2]
+    _dense(p, torch.float32, p.shape, "p", dev)
+    _need(draft is not None or n == 0, "draft: must be [n_seqs, n_draft]")
+    if draft is not None:
+        _dense(draft, torch.int32, (b, n), "draft", dev)
+    if q is not None:
+        _dense(q, torch.float32, (b, n, v), "q", dev)
+    _dense(u, torch.float32, (b, n + 1), "u", dev)
+    with _at(dev):
+        if out is None:
+            out = (_new((b, n + 1), torch.int32, dev, stream, zero=False),
+                   _new((b,), torch.int32, dev, stream, zero=False))
+        tokens, n_accepted = out
+        _dense(tokens, torch.int32, (b, n + 1), "out[0]", dev)
+        _dense(n_accepted, torch.int32, (b,), "out[1]", dev)
+        has_q = q is not None and n > 0
+        _check(_verify_sample(p.data_ptr(), q.data_ptr() if has_q else None,
+                              draft.data_ptr() if draft is not None and n > 0 else None,
+                              u.data_ptr(), b, n, v, tokens.data_ptr(), n_accepted.data_ptr(),
+                              _stream(stream)))
+    return tokens, n_accepted
 
 
 # -------------------------------------------------------------------- model --

@@ -42,25 +42,6 @@ int32_t check_launch(const char* what) {
   return SUB_OK;
 }
 
-// Temporary device memory on a stream (freed in stream order).
-struct StreamScratch {
-  void* p = nullptr;
-  cudaStream_t st;
-  explicit StreamScratch(cudaStream_t s) : st(s) {}
-  int32_t alloc(size_t bytes) {
-    if (bytes == 0) return SUB_OK;
-    const cudaError_t e = cudaMallocAsync(&p, bytes, st);
-    if (e != cudaSuccess) {
-      p = nullptr;
-      return fail(SUB_ENOMEM, std::string("cudaMallocAsync: ") + cudaGetErrorString(e));
-    }
-    return SUB_OK;
-  }
-  ~StreamScratch() {
-    if (p) cudaFreeAsync(p, st);
-  }
-};
-
 }  // namespace sub
 
 using namespace sub;

@@ -1,0 +1,749 @@
+// Attention of new rows over a paged cache, few rows per sequence: the decode
+// step (one row per sequence) and short chunks of drafted tokens.
+//
+// o_i = sum_j e_ij v_j / sum_j e_ij, e_ij = 2^(s_ij - m_i), s_ij = q_i . k_j *
+// scale * log2(e), over the keys at positions 0 .. pos + i, in one pass with a
+// running maximum m_i.  The Hq / Hkv query heads of a KV head are rows of the
+// same tile, so a key is read once for all of them.
+//
+// Bound by HBM: a row tile of 16 does 64 flops per byte of a bf16 cache,
+// mma.sync covers that many times over, and what counts is bytes in flight.
+// So every warp streams blocks of 32 keys on its own, through a private ring
+// of shared memory that its lanes fill with cp.async and read themselves: a
+// lane copies exactly the 16-byte pieces that it will use as matrix operands,
+// so there is no barrier, no swizzle and no ldmatrix in the loop.  That works
+// because a dot product may take its terms in any order, if Q is laid out the
+// same way: lane (g, tig) holds, of key g of an 8-key group, the 16-byte chunks
+// tig, tig + 4, .. of the row, and of V, for its four keys of a 16-key step, the
+// columns that make its B fragments for the n tiles of eight chunk-wise
+// permuted columns.
+//
+// 8-bit codes c stand for (c - 128) * scale.  (c - 128) is exact in fp16 (the
+// bytes 0x64, c are 1024 + c), so both products take the codes themselves: the
+// scale of k_j multiplies the score, and the scale of v_j goes into e_ij before it is
+// rounded to fp16.  The running maximum is taken of s_ij + log2(vscale_j) - 15, so
+// that what is rounded reaches 2^15 at most, and fp16's smallest step, 2^-24, is
+// 2^-39 of the largest; the sum takes the unscaled e_ij, in fp32, relative to the
+// same maximum (log2(vscale_j) counts as at least -80, which keeps it in range).  Q enters in fp16 scaled by a power of two
+// of its row's largest value: bf16 has three bits fewer, so only values below 2^-15 of
+// the largest lose any.  With a bf16 cache P = hi + lo, two bf16 products, keeps
+// it to 2^-17; in fp16 one product keeps 2^-12.
+//
+// A key that a row must not read can still hold anything.  Its score is replaced,
+// and where its value is infinite or NaN (bf16 only, and only in blocks that
+// not all rows read to the end), the block's products with V are formed one by
+// one without the keys of weight zero.
+#include <mutex>
+#include <type_traits>
+#include "chunk_attn.cuh"
+
+namespace sub {
+namespace {
+
+constexpr int KB = 32;          // keys per block of a warp
+constexpr int WARPS = 4;
+constexpr int NT = WARPS * 32;
+constexpr int STAGES = 3;
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
+}
+template <int N>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool pred) {
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src),
+                 "r"(pred ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;\n" ::"r"(dst), "l"(src), "n"(N),
+                 "r"(pred ? N : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+// Codes in two bytes of w (picked by sel, 0x64 above each) to fp16 code - 128.
+__device__ __forceinline__ uint32_t codes2(uint32_t w, uint32_t sel) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(__byte_perm(w, 0x64646464u, sel)), "r"(0x64806480u));
+  return r;
+}
+__device__ __forceinline__ float log2_fast(float x) {
+  float r;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float exp2_fast(float x) {   // 2 ulp; flushes below 2^-126
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+template <int D, bool Q8>
+struct Ring {
+  static constexpr int ESZ = Q8 ? 1 : 2;
+  static constexpr int KI = D * ESZ / 64;            // 16-byte chunks of a key per lane
+  static constexpr int VB = Q8 ? D / 8 : 16;         // bytes of a V piece
+  static constexpr int VH = Q8 ? 1 : D / 64;         // pieces per key and lane
+  static constexpr int K_BYTES = KB * D * ESZ;
+  static constexpr int STAGE = 2 * K_BYTES + (Q8 ? 2 * KB * 4 : 0);
+  static constexpr int BYTES = STAGES * STAGE;       // of one warp
+};
+
+template <int D, bool Q8, int MT>
+constexpr int decode_smem() {
+  // a warp's partial result (MT * 16 rows of D floats, maxima and sums) reuses its ring
+  static_assert(Ring<D, Q8>::BYTES >= MT * 16 * (D + 2) * 4, "the ring holds the partial result");
+  return WARPS * Ring<D, Q8>::BYTES;
+}
+
+// ------------------------------------------------------------------ kernel --
+template <int D, bool Q8, int MT>
+__global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
+  using R = Ring<D, Q8>;
+  constexpr int RT = MT * 16, KS = D / 16, ON = D / 8;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int64_t s_pre[SUB_MAX_SEQS + 1], s_warp[WARPS];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, tig = lane & 3;
+  const int G = a.group;
+  const ChunkPlan<RT, KB> plan(a.t, G, a.n_heads_kv);
+  plan.template scan<NT>(s_pre, s_warp);
+  const int64_t total = s_pre[a.t.n_seqs];
+  const int64_t per = blocks_per_cta(total, gridDim.x, WARPS);
+  const int64_t line_lo = blockIdx.x * per, line_hi = min(total, line_lo + per);
+  uint8_t* const ring = smem + warp * R::BYTES;
+  const uint32_t ring_s = smem_u32(ring);
+  const uint8_t* const kp = reinterpret_cast<const uint8_t*>(a.k);
+  const uint8_t* const vp = reinterpret_cast<const uint8_t*>(a.v);
+
+  for (int64_t at = line_lo; at < line_hi;) {
+    const auto u = plan.find(s_pre, at);
+    const int kb0 = (int)(at - u.begin);
+    const int kb1 = (int)min((int64_t)u.n_blocks, line_hi - u.begin);
+    const int n_mine = (kb1 - kb0 - warp + WARPS - 1) / WARPS;   // blocks kb0 + warp + i * WARPS
+    const int32_t* const pages = a.t.pages + (int64_t)u.b * a.t.width;
+
+    // page (or -1) of each 16-key half of a block
+    auto load_pages = [&](int i, int (&pg)[2]) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int key = (kb0 + warp + i * WARPS) * KB + s * 16;
+        pg[s] = i < n_mine && key < u.n_keys
+                    ? pages[(uint32_t)key / (uint32_t)a.t.page_size] : -1;
+      }
+    };
+    uint32_t missing = 0;   // bits 2 * stage + half: no page there
+    auto issue = [&](int i, int stage, const int (&pg)[2]) {
+      const uint32_t dst = ring_s + stage * R::STAGE;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int key0 = (kb0 + warp + i * WARPS) * KB + s * 16;
+        const bool have = (unsigned)pg[s] < (unsigned)a.t.n_pages;
+        missing = (missing & ~(1u << (2 * stage + s))) | ((have ? 0u : 1u) << (2 * stage + s));
+        const int64_t row0 =
+            pool_row(a.t, a.layer, a.n_heads_kv, have ? pg[s] : 0, u.head,
+                     (int)((uint32_t)key0 % (uint32_t)a.t.page_size));
+        const uint8_t* const k0 = kp + row0 * (D * R::ESZ);
+        const uint8_t* const v0 = vp + row0 * (D * R::ESZ);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int key = h * 8 + g;
+          const bool ok = have && key0 + key < u.n_keys;
+#pragma unroll
+          for (int c = 0; c < R::KI; ++c)
+            cp_async<16>(dst + (((s * 2 + h) * R::KI + c) * 32 + lane) * 16,
+                         ok ? k0 + key * (D * R::ESZ) + (tig + 4 * c) * 16 : kp, ok);
+        }
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          const int key = (kk >> 1) * 8 + 2 * tig + (kk & 1);
+          const bool ok = have && key0 + key < u.n_keys;
+#pragma unroll
+          for (int c = 0; c < R::VH; ++c)
+            cp_async<R::VB>(dst + R::K_BYTES + (((s * 4 + kk) * R::VH + c) * 32 + lane) * R::VB,
+                            ok ? v0 + key * (D * R::ESZ) + (c * 8 + g) * R::VB : vp, ok);
+        }
+        if constexpr (Q8) {
+          // 16 scales of K, 16 of V
+          const int key = lane & 15;
+          const bool ok = have && key0 + key < u.n_keys;
+          const float* src = (lane < 16 ? a.ks : a.vs) + row0 + key;
+          cp_async<4>(dst + 2 * R::K_BYTES + ((lane >> 4) * KB + s * 16 + key) * 4,
+                      ok ? src : a.ks, ok);
+        }
+      }
+    };
+    int pg[2];
+#pragma unroll
+    for (int i = 0; i < STAGES; ++i) {
+      load_pages(i, pg);
+      if (i < n_mine) issue(i, i, pg);
+      cp_commit();
+    }
+    load_pages(STAGES, pg);   // one block ahead of their use
+
+    // ---- Q fragments, and the rows' last visible key ----
+    uint32_t qf[MT][KS][4];
+    float qs[MT][2];    // factor of the row's scores
+    int lim[MT][2];     // keys 0 .. lim are read
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      uint4 w[2][Q8 ? KS / 2 : KS / 2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = u.tile * RT + m * 16 + h * 8 + g;
+        const int q = r / G;
+        const bool ok = q < u.rows;
+        lim[m][h] = ok ? min(u.pos + q, u.n_keys - 1) : -1;
+        const uint16_t* src = a.Q + (int64_t)(u.row0 + (ok ? q : 0)) * a.ldq +
+                              (int64_t)(u.head * G + r % G) * D;
+#pragma unroll
+        for (int c = 0; c < KS / 2; ++c) {
+          // bf16 cache: chunk tig + 4 c of 8 values; codes: half c & 1 of chunk tig + 4 (c / 2) of 16
+          const int d = Q8 ? ((tig + 4 * (c >> 1)) * 16 + (c & 1) * 8) : (tig + 4 * c) * 8;
+          w[h][c] = ok ? *reinterpret_cast<const uint4*>(src + d) : make_uint4(0, 0, 0, 0);
+        }
+      }
+      if constexpr (!Q8) {
+#pragma unroll
+        for (int c = 0; c < KS / 2; ++c) {
+          qf[m][2 * c][0] = w[0][c].x;
+          qf[m][2 * c][1] = w[1][c].x;
+          qf[m][2 * c][2] = w[0][c].y;
+          qf[m][2 * c][3] = w[1][c].y;
+          qf[m][2 * c + 1][0] = w[0][c].z;
+          qf[m][2 * c + 1][1] = w[1][c].z;
+          qf[m][2 * c + 1][2] = w[0][c].w;
+          qf[m][2 * c + 1][3] = w[1][c].w;
+        }
+        qs[m][0] = qs[m][1] = a.sl2;
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          // the row's largest value to [1, 2): an exponent in [-126, 126]
+          float big = 0.f;
+#pragma unroll
+          for (int c = 0; c < KS / 2; ++c) {
+            const uint32_t x[4] = {w[h][c].x, w[h][c].y, w[h][c].z, w[h][c].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              big = fmaxf(big, fmaxf(fabsf(bf16lo(x[i])), fabsf(bf16hi(x[i]))));
+          }
+          big = fmaxf(big, __shfl_xor_sync(~0u, big, 1));
+          big = fmaxf(big, __shfl_xor_sync(~0u, big, 2));
+          const int e = min(126, max(-126, (int)(__float_as_uint(big) >> 23) - 127));
+          const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+          qs[m][h] = a.sl2 * __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+          for (int c = 0; c < KS / 2; ++c) {
+            const uint32_t x[4] = {w[h][c].x, w[h][c].y, w[h][c].z, w[h][c].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              qf[m][2 * c + (i >> 1)][(i & 1) * 2 + h] =
+                  pack_f16x2(bf16lo(x[i]) * down, bf16hi(x[i]) * down);
+          }
+        }
+      }
+    }
+    const int lim_min = min(u.pos + u.tile * RT / G, u.n_keys - 1);   // of the tile's first row
+
+    float o[MT][ON][4], mx[MT][2], l[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      mx[m][0] = mx[m][1] = -INFINITY;
+      l[m][0] = l[m][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < ON; ++i) o[m][i][0] = o[m][i][1] = o[m][i][2] = o[m][i][3] = 0.f;
+    }
+
+    int stage = 0;
+    for (int i = 0; i < n_mine; ++i) {
+      cp_wait<STAGES - 1>();
+      __syncwarp();
+      const int key0 = (kb0 + warp + i * WARPS) * KB;
+      const uint8_t* const st = ring + stage * R::STAGE;
+      const uint32_t miss = (missing >> (2 * stage)) & 3u;
+      const bool edge = key0 + KB - 1 > lim_min || miss;
+
+      // ---- S = Q K^T: n tile t holds keys key0 + 8 t .. + 7 ----
+      float s[MT][4][4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) s[m][t][0] = s[m][t][1] = s[m][t][2] = s[m][t][3] = 0.f;
+#pragma unroll
+        for (int c = 0; c < R::KI; ++c) {
+          const uint4 w = *reinterpret_cast<const uint4*>(st + ((t * R::KI + c) * 32 + lane) * 16);
+          if constexpr (!Q8) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              mma_bf16_16816(s[m][t], qf[m][2 * c], w.x, w.y);
+              mma_bf16_16816(s[m][t], qf[m][2 * c + 1], w.z, w.w);
+            }
+          } else {
+            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t b0 = codes2(x[k], 0x4140u), b1 = codes2(x[k], 0x4342u);
+#pragma unroll
+              for (int m = 0; m < MT; ++m) mma_f16(s[m][t], qf[m][4 * c + k], b0, b1);
+            }
+          }
+        }
+      }
+
+      // ---- weights of the lane's keys 8 t + 2 tig + {0, 1} ----
+      float vsc[4][2], lv[4][2];
+      if constexpr (Q8) {
+        const float* const sc = reinterpret_cast<const float*>(st + 2 * R::K_BYTES);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const float2 kq = *reinterpret_cast<const float2*>(sc + t * 8 + 2 * tig);
+          const float2 vq = *reinterpret_cast<const float2*>(sc + KB + t * 8 + 2 * tig);
+          vsc[t][0] = vq.x;
+          vsc[t][1] = vq.y;
+          lv[t][0] = fmaxf(log2_fast(vq.x), -80.f) - 15.f;
+          lv[t][1] = fmaxf(log2_fast(vq.y), -80.f) - 15.f;
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[m][t][e] *= (e & 1 ? kq.y : kq.x) * qs[m][e >> 1];
+        }
+      } else {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[m][t][e] *= a.sl2;
+      }
+      if (edge) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int key = key0 + t * 8 + 2 * tig + (e & 1);
+            const bool gone = (miss >> (t >> 1)) & 1u;
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+              if (gone || key > lim[m][e >> 1]) s[m][t][e] = -INFINITY;
+          }
+      }
+      uint32_t pf[MT][2][4], pl[MT][2][4];   // P of the two 16-key steps (bf16: high and low part)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            top[e >> 1] = fmaxf(top[e >> 1], Q8 ? s[m][t][e] + lv[t][e & 1] : s[m][t][e]);
+        if (__any_sync(~0u, top[0] > mx[m][0] || top[1] > mx[m][1])) {
+          float corr[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            top[h] = fmaxf(top[h], __shfl_xor_sync(~0u, top[h], 1));
+            top[h] = fmaxf(top[h], __shfl_xor_sync(~0u, top[h], 2));
+            const float now = fmaxf(mx[m][h], top[h]);
+            corr[h] = now == -INFINITY ? 1.f : exp2_fast(mx[m][h] - now);
+            mx[m][h] = now;
+            l[m][h] *= corr[h];
+          }
+#pragma unroll
+          for (int n = 0; n < ON; ++n) {
+            o[m][n][0] *= corr[0];
+            o[m][n][1] *= corr[0];
+            o[m][n][2] *= corr[1];
+            o[m][n][3] *= corr[1];
+          }
+        }
+        // a row without a key so far keeps -infinity: subtract 0 there
+        const float ref[2] = {mx[m][0] == -INFINITY ? 0.f : mx[m][0],
+                              mx[m][1] == -INFINITY ? 0.f : mx[m][1]};
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          float p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            p[e] = exp2_fast(s[m][t][e] - ref[e >> 1]);
+            l[m][e >> 1] += p[e];
+            if constexpr (Q8) {
+              // a masked key's scale may be anything
+              p[e] = edge && s[m][t][e] == -INFINITY ? 0.f : p[e] * vsc[t][e & 1];
+            }
+          }
+          const int step = t >> 1, r0 = (t & 1) * 2;
+          if constexpr (Q8) {
+            pf[m][step][r0] = pack_f16x2(p[0], p[1]);
+            pf[m][step][r0 + 1] = pack_f16x2(p[2], p[3]);
+          } else {
+            const uint32_t a01 = pack_bf16x2(p[0], p[1]), a23 = pack_bf16x2(p[2], p[3]);
+            pf[m][step][r0] = a01;
+            pf[m][step][r0 + 1] = a23;
+            pl[m][step][r0] = pack_bf16x2(p[0] - bf16lo(a01), p[1] - bf16hi(a01));
+            pl[m][step][r0 + 1] = pack_bf16x2(p[2] - bf16lo(a23), p[3] - bf16hi(a23));
+          }
+        }
+      }
+
+      // ---- O += P V: n tile n, column g is column d(g, n) of the head ----
+      const uint8_t* const sv = st + R::K_BYTES;
+#pragma unroll
+      for (int step = 0; step < 2; ++step) {
+        if constexpr (!Q8) {
+#pragma unroll
+          for (int c = 0; c < R::VH; ++c) {   // d(g, 8 c + j) = 64 c + 8 g + j
+            uint32_t w[4][4];
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint4 x =
+                  *reinterpret_cast<const uint4*>(sv + (((step * 4 + kk) * R::VH + c) * 32 + lane) * 16);
+              w[kk][0] = x.x;
+              w[kk][1] = x.y;
+              w[kk][2] = x.z;
+              w[kk][3] = x.w;
+            }
+            bool odd = false;
+            if (edge) {   // an exponent of all ones somewhere
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  odd |= (w[kk][j] & 0x7f80u) == 0x7f80u || (w[kk][j] & 0x7f800000u) == 0x7f800000u;
+              odd = __any_sync(~0u, odd);
+            }
+            if (!odd) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t b0 = __byte_perm(w[0][j], w[1][j], 0x5410u);
+                const uint32_t b1 = __byte_perm(w[2][j], w[3][j], 0x5410u);
+                const uint32_t d0 = __byte_perm(w[0][j], w[1][j], 0x7632u);
+                const uint32_t d1 = __byte_perm(w[2][j], w[3][j], 0x7632u);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                  mma_bf16_16816(o[m][c * 8 + 2 * j], pf[m][step], b0, b1);
+                  mma_bf16_16816(o[m][c * 8 + 2 * j + 1], pf[m][step], d0, d1);
+                  mma_bf16_16816(o[m][c * 8 + 2 * j], pl[m][step], b0, b1);
+                  mma_bf16_16816(o[m][c * 8 + 2 * j + 1], pl[m][step], d0, d1);
+                }
+              }
+            } else {
+              // element by element: output columns 2 tig + e of n tile 8 c + 2 j + x
+#pragma unroll 1
+              for (int key = 0; key < 16; ++key) {
+                const int kt = (key & 7) >> 1, kk = (key >> 3) * 2 + (key & 1);   // its lanes, its piece
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                  float pr[2];
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) {
+                    const uint32_t hi = __shfl_sync(~0u, pf[m][step][(key >> 3) * 2 + h], g * 4 + kt);
+                    const uint32_t lo = __shfl_sync(~0u, pl[m][step][(key >> 3) * 2 + h], g * 4 + kt);
+                    pr[h] = key & 1 ? bf16hi(hi) + bf16hi(lo) : bf16lo(hi) + bf16lo(lo);
+                  }
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) {
+                    const uint32_t mine = kk == 0 ? w[0][j] : kk == 1 ? w[1][j] : kk == 2 ? w[2][j] : w[3][j];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                      const uint32_t x = __shfl_sync(~0u, mine, (2 * tig + e) * 4 + kt);
+#pragma unroll
+                      for (int h = 0; h < 2; ++h) {
+                        if (pr[h] == 0.f) continue;
+                        o[m][c * 8 + 2 * j][2 * h + e] += pr[h] * bf16lo(x);
+                        o[m][c * 8 + 2 * j + 1][2 * h + e] += pr[h] * bf16hi(x);
+                      }
+                    }
+                  }
+                }
+              }
+            }
+          }
+        } else {
+          constexpr int WN = R::VB / 4;   // d(g, n) = g * (D / 8) + n
+          uint32_t w[4][WN];
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint8_t* const src = sv + ((step * 4 + kk) * 32 + lane) * R::VB;
+            if constexpr (WN == 4) {
+              const uint4 x = *reinterpret_cast<const uint4*>(src);
+              w[kk][0] = x.x;
+              w[kk][1] = x.y;
+              w[kk][2] = x.z;
+              w[kk][3] = x.w;
+            } else {
+              const uint2 x = *reinterpret_cast<const uint2*>(src);
+              w[kk][0] = x.x;
+              w[kk][1] = x.y;
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < WN; ++j) {
+            const uint32_t a0 = __byte_perm(w[0][j], w[1][j], 0x5140u);
+            const uint32_t a1 = __byte_perm(w[0][j], w[1][j], 0x7362u);
+            const uint32_t c0 = __byte_perm(w[2][j], w[3][j], 0x5140u);
+            const uint32_t c1 = __byte_perm(w[2][j], w[3][j], 0x7362u);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t sel = x & 1 ? 0x4342u : 0x4140u;
+              const uint32_t b0 = codes2(x < 2 ? a0 : a1, sel), b1 = codes2(x < 2 ? c0 : c1, sel);
+#pragma unroll
+              for (int m = 0; m < MT; ++m) mma_f16(o[m][4 * j + x], pf[m][step], b0, b1);
+            }
+          }
+        }
+      }
+      __syncwarp();   // the stage's scales were read by other lanes
+      if (i + STAGES < n_mine) issue(i + STAGES, stage, pg);
+      cp_commit();
+      load_pages(i + STAGES + 1, pg);
+      stage = stage + 1 == STAGES ? 0 : stage + 1;
+    }
+    cp_wait<0>();
+    __syncwarp();
+
+    // ---- the warps' results into their rings, then joined in warp order ----
+    constexpr int WSTRIDE = R::BYTES / 4;
+    float* const wo = reinterpret_cast<float*>(ring);   // [RT][D], maxima [RT], sums [RT]
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = m * 16 + h * 8 + g;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int gg = 2 * tig + e;
+#pragma unroll
+          for (int n = 0; n < ON; n += 4) {
+            const int d = Q8 ? gg * (D / 8) + n : (n >> 3) * 64 + gg * 8 + (n & 7);
+            *reinterpret_cast<float4*>(wo + r * D + d) =
+                make_float4(o[m][n][2 * h + e], o[m][n + 1][2 * h + e], o[m][n + 2][2 * h + e],
+                            o[m][n + 3][2 * h + e]);
+          }
+        }
+        float ls = l[m][h];
+        ls += __shfl_xor_sync(~0u, ls, 1);
+        ls += __shfl_xor_sync(~0u, ls, 2);
+        if (tig == 0) {
+          wo[RT * D + r] = mx[m][h];
+          wo[RT * D + RT + r] = ls;
+        }
+      }
+    __syncthreads();
+    const bool whole = kb0 == 0 && kb1 == u.n_blocks;
+    // a CTA's first piece goes to its slot 0, its last to slot 1
+    const int64_t slot = 2 * (int64_t)blockIdx.x + (at == line_lo ? 0 : 1);
+    const float* const all = reinterpret_cast<const float*>(smem);
+    for (int idx = tid; idx < RT * (D / 4); idx += NT) {
+      const int r = idx / (D / 4), d = (idx % (D / 4)) * 4;
+      const int row = u.tile * RT + r, q = row / G;
+      if (q >= u.rows) continue;
+      float big = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) big = fmaxf(big, all[w * WSTRIDE + RT * D + r]);
+      float sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        const float* const pw = all + w * WSTRIDE;
+        const float mw = pw[RT * D + r];
+        if (mw == -INFINITY) continue;
+        const float f = exp2_fast(mw - big);
+        const float4 v = *reinterpret_cast<const float4*>(pw + r * D + d);
+        sum = fmaf(f, pw[RT * D + RT + r], sum);
+        x[0] = fmaf(f, v.x, x[0]);
+        x[1] = fmaf(f, v.y, x[1]);
+        x[2] = fmaf(f, v.z, x[2]);
+        x[3] = fmaf(f, v.w, x[3]);
+      }
+      if (whole) {
+        const float inv = big == -INFINITY ? 0.f : 1.f / sum;
+        *reinterpret_cast<uint2*>(a.O + ((int64_t)(u.row0 + q) * a.n_heads_q + u.head * G + row % G) * D + d) =
+            make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
+      } else {
+        __stcg(reinterpret_cast<float4*>(a.part_o + (slot * RT + r) * D + d),
+               make_float4(x[0], x[1], x[2], x[3]));
+        if (d == 0) __stcg(a.part_ml + slot * RT + r, make_float2(big, sum));
+      }
+    }
+    __syncthreads();
+    at = u.begin + kb1;
+  }
+}
+
+// ------------------------------------------------------------------- joins --
+// CTA x joins the unit that is cut at the end of CTA x's part of the line, if
+// that is its first cut: pieces x, x + 1, .. in order.  The rows are shared
+// over grid.y.
+constexpr int JOIN_NT = 128, JOIN_ROWS = 4;
+
+template <int D, int RT>
+__global__ void __launch_bounds__(JOIN_NT) chunk_join_kernel(ChunkArgs a, int n_ctas, int least) {
+  __shared__ int64_t s_pre[SUB_MAX_SEQS + 1], s_warp[JOIN_NT / 32];
+  const ChunkPlan<RT, KB> plan(a.t, a.group, a.n_heads_kv);
+  plan.template scan<JOIN_NT>(s_pre, s_warp);
+  const int64_t total = s_pre[a.t.n_seqs];
+  const int64_t per = blocks_per_cta(total, n_ctas, least);
+  const int64_t cut = (blockIdx.x + 1) * per;
+  pdl_wait();   // lengths are older than the kernel before; its partial results are not
+  pdl_trigger();
+  if (cut >= total) return;
+  const auto u = plan.find(s_pre, cut);
+  if (u.begin == cut || u.begin < cut - per) return;   // not cut here, or first cut earlier
+  const int64_t first = 2 * (int64_t)blockIdx.x + (u.begin == cut - per ? 0 : 1);
+  const int n = (int)((u.begin + u.n_blocks - 1) / per) - (int)blockIdx.x + 1;
+  auto slot = [&](int i) { return i == 0 ? first : 2 * ((int64_t)blockIdx.x + i); };
+  const int G = a.group;
+  for (int idx = threadIdx.x; idx < JOIN_ROWS * (D / 4); idx += JOIN_NT) {
+    const int r = blockIdx.y * JOIN_ROWS + idx / (D / 4), d = (idx % (D / 4)) * 4;
+    const int row = u.tile * RT + r, q = row / G;
+    if (q >= u.rows) continue;
+    float big = -INFINITY;
+    for (int i = 0; i < n; ++i) big = fmaxf(big, __ldcg(a.part_ml + slot(i) * RT + r).x);
+    float sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float2 ml = __ldcg(a.part_ml + slot(i) * RT + r);
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + (slot(i) * RT + r) * D + d));
+      const float f = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - big);
+      sum = fmaf(f, ml.y, sum);
+      x[0] = fmaf(f, v.x, x[0]);
+      x[1] = fmaf(f, v.y, x[1]);
+      x[2] = fmaf(f, v.z, x[2]);
+      x[3] = fmaf(f, v.w, x[3]);
+    }
+    const float inv = big == -INFINITY ? 0.f : 1.f / sum;
+    *reinterpret_cast<uint2*>(a.O + ((int64_t)(u.row0 + q) * a.n_heads_q + u.head * G + row % G) * D + d) =
+        make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
+  }
+}
+
+// -------------------------------------------------------------------- host --
+int sm_count() {
+  static int n = 0;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+      n = 152;
+  });
+  return n;
+}
+
+template <int D, bool Q8, int MT>
+int32_t launch_decode(const ChunkArgs& a, int n_ctas, cudaStream_t st) {
+  static std::once_flag once;
+  static cudaError_t err = cudaSuccess;
+  constexpr int SMEM = decode_smem<D, Q8, MT>();
+  std::call_once(once, [] {
+    err = cudaFuncSetAttribute(chunk_attn_kernel<D, Q8, MT>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  });
+  SUB_CUDA_TRY(err);
+  SUB_CUDA_TRY(launch_k(chunk_attn_kernel<D, Q8, MT>, dim3(n_ctas), dim3(NT), SMEM, st, a));
+  SUB_CUDA_TRY(launch_k(chunk_join_kernel<D, MT * 16>, dim3(n_ctas, MT * 16 / JOIN_ROWS),
+                        dim3(JOIN_NT), 0, st, a, n_ctas, WARPS));
+  return SUB_OK;
+}
+
+// Partial results: two per CTA.
+int64_t part_bytes(int n_ctas, int rows, int d) {
+  return (int64_t)n_ctas * 2 * rows * (d + 2) * 4;
+}
+
+template <class Cache>
+int32_t chunk_attn(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q, const Cache* kv,
+                   const float* ks, const float* vs, int32_t layer, const sub_batch* batch,
+                   float softmax_scale, sub_bf16* O, void* workspace, int64_t workspace_bytes,
+                   void* stream) {
+  constexpr bool Q8 = std::is_same<Cache, sub_kv8_cache>::value;
+  ChunkArgs a{};
+  SUB_TRY(make_seq_table(kv, layer, batch, &a.t));
+  SUB_CHECK_ARG(n_heads_q >= 1 && n_heads_q % kv->n_heads_kv == 0 &&
+                    n_heads_q / kv->n_heads_kv <= 64,
+                "Hq must be a multiple of Hkv, at most 64 times");
+  SUB_CHECK_ARG(softmax_scale >= 0.f && softmax_scale <= 1e6f, "softmax_scale out of range");
+  if (a.t.n_rows == 0) return SUB_OK;
+  SUB_CHECK_ARG(Q && O, "null pointer");
+  SUB_CHECK_ARG(aligned16(Q) && aligned16(O) && ldq % 8 == 0, "rows must be 16-byte aligned");
+  SUB_CHECK_ARG(ldq >= (int64_t)n_heads_q * kv->head_dim, "row stride below Hq * head_dim");
+  a.Q = Q;
+  a.ldq = ldq;
+  a.O = O;
+  a.k = kv->k;
+  a.v = kv->v;
+  a.ks = ks;
+  a.vs = vs;
+  a.layer = layer;
+  a.n_heads_q = n_heads_q;
+  a.n_heads_kv = kv->n_heads_kv;
+  a.group = n_heads_q / kv->n_heads_kv;
+  a.sl2 = softmax_scale * 1.4426950408889634f;
+  const cudaStream_t st = as_stream(stream);
+  int64_t need = 0;
+  SUB_TRY(sub_chunk_attn_workspace(n_heads_q, kv->n_heads_kv, kv->head_dim, a.t.n_seqs, a.t.n_rows,
+                                   &need));
+  StreamScratch scratch(st);
+  if (workspace) {
+    SUB_CHECK_ARG(aligned16(workspace) && workspace_bytes >= need, "workspace too small");
+  } else {
+    SUB_TRY(scratch.alloc((size_t)need));
+    workspace = scratch.p;
+  }
+  const int n_ctas = sm_count();
+  a.part_o = reinterpret_cast<float*>(workspace);
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + (int64_t)n_ctas * 2 * 16 * kv->head_dim);
+  return kv->head_dim == 128 ? launch_decode<128, Q8, 1>(a, n_ctas, st)
+                             : launch_decode<64, Q8, 1>(a, n_ctas, st);
+}
+
+}  // namespace
+}  // namespace sub
+
+using namespace sub;
+
+extern "C" int32_t sub_chunk_attn_workspace(int32_t n_heads_q, int32_t n_heads_kv,
+                                            int32_t head_dim, int32_t n_seqs, int32_t n_rows,
+                                            int64_t* bytes) {
+  SUB_CHECK_ARG(bytes, "null pointer");
+  SUB_CHECK_ARG(head_dim == 64 || head_dim == 128, "head_dim must be 64 or 128");
+  SUB_CHECK_ARG(n_heads_kv >= 1 && n_heads_q >= 1 && n_heads_q % n_heads_kv == 0,
+                "Hq must be a multiple of Hkv");
+  SUB_CHECK_ARG(n_seqs >= 1 && n_seqs <= SUB_MAX_SEQS && n_rows >= 0, "bad batch sizes");
+  *bytes = n_rows ? part_bytes(sm_count(), 16, head_dim) : 0;
+  return SUB_OK;
+}
+
+extern "C" int32_t sub_chunk_attn(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q,
+                                  const sub_kv_cache* kv, int32_t layer, const sub_batch* batch,
+                                  float softmax_scale, sub_bf16* O, void* workspace,
+                                  int64_t workspace_bytes, void* stream) {
+  return chunk_attn(Q, ldq, n_heads_q, kv, nullptr, nullptr, layer, batch, softmax_scale, O,
+                    workspace, workspace_bytes, stream);
+}
+
+extern "C" int32_t sub_chunk_attn8(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q,
+                                   const sub_kv8_cache* kv, int32_t layer, const sub_batch* batch,
+                                   float softmax_scale, sub_bf16* O, void* workspace,
+                                   int64_t workspace_bytes, void* stream) {
+  SUB_CHECK_ARG(kv && kv->k_scale && kv->v_scale, "null pointer");
+  return chunk_attn(Q, ldq, n_heads_q, kv, kv->k_scale, kv->v_scale, layer, batch, softmax_scale,
+                    O, workspace, workspace_bytes, stream);
+}

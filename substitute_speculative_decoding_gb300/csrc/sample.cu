@@ -1,0 +1,403 @@
+// Probabilities from logits, and the verification of chains of drafted tokens
+// against them ("SubSpec: Using the Target Model's Own Low-Bit Shadow as Its
+// Draft Model", 6.2, Leviathan et al.).
+//
+// Both pass once over rows of V values.  A row belongs to one thread-block
+// cluster, so that a single row still streams through several SMs, and the
+// CTAs agree on the row's sums through distributed shared memory: one launch,
+// no scratch.  Rows are read in aligned groups of four values whatever V is:
+// a row that starts `mis` values past a 16-byte boundary has groups
+// [4 g - mis, 4 g - mis + 4), of which the first and last may be partial.
+#include <algorithm>
+#include <cooperative_groups.h>
+#include "common.cuh"
+
+namespace sub {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int MAX_CLUSTER = 8;        // the portable size
+constexpr int64_t MAX_V = 1 << 20;
+
+struct Row {
+  int64_t V;
+  int mis;
+  __device__ Row(const float* z, int64_t v)
+      : V(v), mis((int)((reinterpret_cast<uintptr_t>(z) >> 2) & 3)) {}
+  __device__ int groups() const { return (int)((V + mis + 3) / 4); }
+  __device__ int64_t first(int g) const { return (int64_t)g * 4 - mis; }   // may be < 0 in group 0
+  __device__ bool whole(int g) const { return first(g) >= 0 && first(g) + 4 <= V; }
+};
+
+// Group g of row z; `none` where the row has no value.
+template <bool VEC = true>
+__device__ __forceinline__ float4 load_group(const float* z, const Row& r, int g, float none) {
+  const int64_t e = r.first(g);
+  if (VEC && r.whole(g)) return *reinterpret_cast<const float4*>(z + e);
+  float4 x;
+  x.x = e >= 0 && e < r.V ? z[e] : none;
+  x.y = e + 1 >= 0 && e + 1 < r.V ? z[e + 1] : none;
+  x.z = e + 2 >= 0 && e + 2 < r.V ? z[e + 2] : none;
+  x.w = e + 3 < r.V ? z[e + 3] : none;
+  return x;
+}
+
+// A CTA's share of a row's groups.
+__device__ __forceinline__ void share(int groups, int rank, int size, int& lo, int& hi) {
+  const int per = (groups + size - 1) / size;
+  lo = min(groups, rank * per);
+  hi = min(groups, lo + per);
+}
+
+// ------------------------------------------------------------- softmax --
+// p = exp((z - m) / T) / sum, with m the largest logit.  Bound by HBM: 4 bytes
+// in, 4 out.  A thread keeps NV groups in registers between the two passes
+// (groups past them, in rows longer than the cluster holds, are read again).
+// Each CTA sums relative to its own largest logit, so one cluster barrier
+// exchanges both, and a value is scaled by exp((m_cta - m) / T) / sum.
+template <int THREADS, int NV>
+__global__ void __launch_bounds__(THREADS) probs_kernel(const float* logits, int64_t V, float c_hi,
+                                                        float c_lo, float* probs) {
+  constexpr int WARPS = THREADS / 32;
+  __shared__ float s_m[WARPS], s_s[WARPS];
+  __shared__ float2 s_cta;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int size = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int64_t row = blockIdx.x / size;
+  pdl_wait();
+  pdl_trigger();
+  const float* z = logits + row * V;
+  float* out = probs + row * V;
+  const Row r(z, V);
+  int lo, hi;
+  share(r.groups(), rank, size, lo, hi);
+  // exp(d / T) = 2^(d c), c = log2(e) / T in two parts: one rounding of d c
+  auto expo = [&](float d) { return d == -INFINITY ? 0.f : exp2f(fmaf(d, c_hi, d * c_lo)); };
+  float4 x[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int g = lo + threadIdx.x + j * THREADS;
+    x[j] = g < hi ? load_group(z, r, g, -INFINITY)
+                  : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+  }
+  auto max4 = [](const float4& v) { return fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)); };
+  float m = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) m = fmaxf(m, max4(x[j]));
+  for (int g = lo + threadIdx.x + NV * THREADS; g < hi; g += THREADS)
+    m = fmaxf(m, max4(load_group(z, r, g, -INFINITY)));
+  m = warp_max(m);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (lane == 0) s_m[warp] = m;
+  __syncthreads();
+  m = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) m = fmaxf(m, s_m[w]);
+  // no logit above -infinity here: every value is 0 whatever the reference
+  const float ref = m == -INFINITY ? 0.f : m;
+  auto exp4 = [&](const float4& v) {
+    return make_float4(expo(v.x - ref), expo(v.y - ref), expo(v.z - ref), expo(v.w - ref));
+  };
+  float s = 0.f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    x[j] = exp4(x[j]);
+    s += (x[j].x + x[j].y) + (x[j].z + x[j].w);
+  }
+  for (int g = lo + threadIdx.x + NV * THREADS; g < hi; g += THREADS) {
+    const float4 e = exp4(load_group(z, r, g, -INFINITY));
+    s += (e.x + e.y) + (e.z + e.w);
+  }
+  s = warp_sum(s);
+  if (lane == 0) s_s[warp] = s;
+  __syncthreads();
+  s = 0.f;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) s += s_s[w];
+  float f;
+  if (size == 1) {
+    f = s == 0.f ? 0.f : 1.f / s;
+  } else {
+    if (threadIdx.x == 0) s_cta = make_float2(m, s);
+    cluster.sync();
+    float2 peer[MAX_CLUSTER];
+    float big = -INFINITY, all = 0.f;
+#pragma unroll
+    for (int i = 0; i < MAX_CLUSTER; ++i) {
+      peer[i] = i < size ? *cluster.map_shared_rank(&s_cta, i) : make_float2(-INFINITY, 0.f);
+      big = fmaxf(big, peer[i].x);
+    }
+#pragma unroll
+    for (int i = 0; i < MAX_CLUSTER; ++i)
+      if (peer[i].x != -INFINITY || peer[i].y != 0.f) all += peer[i].y * expo(peer[i].x - big);
+    f = all == 0.f ? 0.f : expo(m - big) / all;
+  }
+  auto put = [&](int g, const float4& v) {
+    const int64_t e = r.first(g);
+    if (r.whole(g)) {
+      *reinterpret_cast<float4*>(out + e) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+      return;
+    }
+    const float w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (e + i >= 0 && e + i < V) out[e + i] = w[i] * f;
+  };
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int g = lo + threadIdx.x + j * THREADS;
+    if (g < hi) put(g, x[j]);
+  }
+  for (int g = lo + threadIdx.x + NV * THREADS; g < hi; g += THREADS)
+    put(g, exp4(load_group(z, r, g, -INFINITY)));
+  if (size > 1) cluster.sync();   // peers may still be reading s_cta
+}
+
+// ------------------------------------------------- draft verification --
+constexpr int VER_THREADS = 512, VER_WARPS = VER_THREADS / 32;
+// segments of a CTA's share: one warp's 32 groups of four values each
+constexpr int VER_SEGS = (int)((MAX_V + 3) / 4 + 1 + 31) / 32 / MAX_CLUSTER + VER_WARPS + 1;
+
+struct VerifyArgs {
+  const float* p;
+  const float* q;
+  const int32_t* draft;
+  const float* u;
+  int n_draft;
+  int64_t V;
+  int32_t* tokens;
+  int32_t* n_accepted;
+};
+
+__device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+  return v;
+}
+
+// One cluster per sequence.  Every CTA repeats the acceptance tests (a few
+// numbers each), which name the row to sample from; then the row is read
+// once: weights as whole multiples of 2^-43, so that their sums do not depend
+// on the order and the sampled token is the same on any split.  A sum per warp
+// segment (128 values) stays in shared memory; the CTA whose part of the
+// running sum holds the number reads that one segment again.  Bound by the
+// latency of the three dependent rounds of reads at few sequences, by HBM
+// (one row of p and of q per sequence) at many.
+__global__ void __launch_bounds__(VER_THREADS) verify_kernel(VerifyArgs a) {
+  __shared__ uint64_t s_seg[VER_SEGS];
+  __shared__ uint64_t s_warp[VER_WARPS], s_cta;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int size = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int64_t b = blockIdx.x / size;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n = a.n_draft;
+  pdl_wait();
+  pdl_trigger();
+
+  // ---- the longest accepted prefix (every warp by itself) ----
+  int acc = n;
+  bool refused = false;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const int i = i0 + lane;
+    bool stop = i < n, bad = false;
+    if (i < n) {
+      const int x = a.draft[b * n + i];
+      if (x >= 0 && x < a.V) {
+        const double pv = a.p[(b * (n + 1) + i) * a.V + x];
+        const double qv = a.q ? a.q[(b * n + i) * a.V + x] : 1.f;
+        bad = !((double)a.u[b * (n + 1) + i] * qv < pv);   // 48-bit product: exact
+        stop = bad;
+      }
+    }
+    const unsigned stops = __ballot_sync(~0u, stop);
+    if (stops) {
+      const int first = __ffs(stops) - 1;
+      acc = i0 + first;
+      refused = (__ballot_sync(~0u, bad) >> first) & 1u;
+      break;
+    }
+  }
+  if (rank == 0) {
+    for (int i = threadIdx.x; i <= n; i += VER_THREADS)
+      if (i != acc) a.tokens[b * (n + 1) + i] = i < acc ? a.draft[b * n + i] : -1;
+    if (threadIdx.x == 0) a.n_accepted[b] = acc;
+  }
+
+  const float* p = a.p + (b * (n + 1) + acc) * a.V;
+  const float* q = a.q ? a.q + (b * n + acc) * a.V : nullptr;   // read after a rejection only
+  const int64_t x = refused ? a.draft[b * n + acc] : -1;
+  const Row r(p, a.V);
+  const bool q_vec = q && ((reinterpret_cast<uintptr_t>(q) >> 2) & 3) == (unsigned)r.mis;
+  int lo, hi;
+  share(r.groups(), rank, size, lo, hi);
+  auto weights = [&](int g, bool diff, uint64_t (&w)[4]) {
+    float4 pv = load_group(p, r, g, 0.f), qv = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (diff) {
+      if (q) {
+        qv = q_vec ? load_group(q, r, g, 0.f) : load_group<false>(q, r, g, 0.f);
+      } else {
+        const int64_t e = x - r.first(g);
+        qv = make_float4(e == 0, e == 1, e == 2, e == 3);
+      }
+    }
+    const float d[4] = {pv.x - qv.x, pv.y - qv.y, pv.z - qv.z, pv.w - qv.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = __float2ull_rn(fminf(fmaxf(d[i], 0.f), 1.f) * 0x1p43f);   // NaN counts as 0
+  };
+  const float uf = a.u[b * (n + 1) + n];
+  const uint64_t u64 = __float2ull_rz(fminf(fmaxf(uf, 0.f), 0x1.fffffep-1f) * 0x1p64f);
+
+  for (bool diff = refused;; diff = false) {
+    // ---- segment sums, this CTA's sum ----
+    uint64_t mine = 0;
+    const int segs = (hi - lo + 31) / 32;
+    for (int s0 = warp; s0 < segs; s0 += 4 * VER_WARPS) {
+      uint64_t v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int g = lo + (s0 + k * VER_WARPS) * 32 + lane;
+        uint64_t w[4] = {0, 0, 0, 0};
+        if (g < hi) weights(g, diff, w);
+        v[k] = (w[0] + w[1]) + (w[2] + w[3]);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint64_t t = warp_sum64(v[k]);
+        if (lane == 0 && s0 + k * VER_WARPS < segs) s_seg[s0 + k * VER_WARPS] = t;
+        mine += t;
+      }
+    }
+    if (lane == 0) s_warp[warp] = mine;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      uint64_t t = 0;
+      for (int i = 0; i < VER_WARPS; ++i) t += s_warp[i];
+      s_cta = t;
+    }
+    if (size > 1) cluster.sync();
+    else __syncthreads();
+    uint64_t total = 0, before = 0;
+    for (int i = 0; i < size; ++i) {
+      const uint64_t t = *cluster.map_shared_rank(&s_cta, i);
+      if (i < rank) before += t;
+      total += t;
+    }
+    const uint64_t own = s_cta;
+    if (total == 0) {
+      if (size > 1) cluster.sync();
+      else __syncthreads();
+      if (diff) continue;   // nothing left after the rejection: sample p itself
+      if (rank == 0 && threadIdx.x == 0) a.tokens[b * (n + 1) + acc] = 0;
+      return;
+    }
+    // ---- the value whose running sum first exceeds u * total ----
+    const uint64_t target = __umul64hi(total, u64);   // floor: sums are whole numbers
+    if (target >= before && target - before < own && warp == 0) {
+      uint64_t rest = target - before;   // within this CTA's share
+      int seg = 0;
+      for (int s0 = 0; s0 < segs; s0 += 32) {
+        const uint64_t t = s0 + lane < segs ? s_seg[s0 + lane] : 0;
+        uint64_t run = t;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint64_t up = __shfl_up_sync(~0u, run, o);
+          if (lane >= o) run += up;
+        }
+        const unsigned over = __ballot_sync(~0u, run > rest);
+        if (over) {
+          const int l = __ffs(over) - 1;
+          seg = s0 + l;
+          rest -= __shfl_sync(~0u, run - t, l);
+          break;
+        }
+        rest -= __shfl_sync(~0u, run, 31);
+      }
+      const int g = lo + seg * 32 + lane;
+      uint64_t w[4] = {0, 0, 0, 0};
+      if (g < hi) weights(g, diff, w);
+      const uint64_t t = (w[0] + w[1]) + (w[2] + w[3]);
+      uint64_t run = t;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t up = __shfl_up_sync(~0u, run, o);
+        if (lane >= o) run += up;
+      }
+      const unsigned over = __ballot_sync(~0u, run > rest);
+      if (lane == __ffs(over) - 1) {
+        uint64_t at = run - t;
+        int i = 0;
+        while (i < 3 && (at += w[i]) <= rest) ++i;
+        a.tokens[b * (n + 1) + acc] = (int32_t)(r.first(g) + i);
+      }
+    }
+    if (size > 1) cluster.sync();   // peers may still be reading s_cta
+    return;
+  }
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_clusters(void (*kern)(KArgs...), int64_t rows, int size, int threads,
+                            cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(rows * size));
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = size;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+}
+
+}  // namespace
+}  // namespace sub
+
+using namespace sub;
+
+extern "C" int32_t sub_probs(const float* logits, int64_t rows, int64_t V, float temperature,
+                             float* probs, void* stream) {
+  SUB_CHECK_ARG(rows >= 0 && rows <= (1 << 24), "rows out of range");
+  SUB_CHECK_ARG(V >= 1 && V <= MAX_V, "V must be in [1, 2^20]");
+  SUB_CHECK_ARG(temperature >= 1e-6f && temperature <= 1e6f,
+                "temperature must be in [1e-6, 1e6]");
+  if (rows == 0) return SUB_OK;
+  SUB_CHECK_ARG(logits && probs, "null pointer");
+  SUB_CHECK_ARG(aligned16(logits) && aligned16(probs), "logits and probs must be 16-byte aligned");
+  const double c = 1.4426950408889634074 / (double)temperature;
+  const float c_hi = (float)c, c_lo = (float)(c - (double)c_hi);
+  const cudaStream_t st = as_stream(stream);
+  if (V <= 2048) {
+    SUB_CUDA_TRY(
+        launch_clusters(probs_kernel<128, 4>, rows, 1, 128, st, logits, V, c_hi, c_lo, probs));
+    return SUB_OK;
+  }
+  // a CTA keeps 512 * 10 groups; few rows spread over more CTAs (two per SM)
+  int size = 1;
+  while (size < MAX_CLUSTER && (V > (int64_t)size * 512 * 40 - 4 || rows * size < 152)) size *= 2;
+  SUB_CUDA_TRY(
+      launch_clusters(probs_kernel<512, 10>, rows, size, 512, st, logits, V, c_hi, c_lo, probs));
+  return SUB_OK;
+}
+
+extern "C" int32_t sub_verify_sample(const float* p, const float* q, const int32_t* draft,
+                                     const float* u, int32_t n_seqs, int32_t n_draft, int64_t V,
+                                     int32_t* tokens, int32_t* n_accepted, void* stream) {
+  SUB_CHECK_ARG(n_seqs >= 0 && n_seqs <= (1 << 24), "n_seqs out of range");
+  SUB_CHECK_ARG(n_draft >= 0 && n_draft <= (1 << 20), "n_draft out of range");
+  SUB_CHECK_ARG(V >= 1 && V <= MAX_V, "V must be in [1, 2^20]");
+  if (n_seqs == 0) return SUB_OK;
+  SUB_CHECK_ARG(p && u && tokens && n_accepted && (draft || n_draft == 0), "null pointer");
+  SUB_CHECK_ARG(aligned16(p) && aligned16(q), "p and q must be 16-byte aligned");
+  VerifyArgs a{p, q, draft, u, n_draft, V, tokens, n_accepted};
+  // rows one CTA reads in a few rounds need no cluster
+  const int size = V <= 8192 ? 1 : MAX_CLUSTER;
+  SUB_CUDA_TRY(launch_clusters(verify_kernel, n_seqs, size, VER_THREADS, as_stream(stream), a));
+  return SUB_OK;
+}

@@ -4,6 +4,7 @@
 #include <cstdlib>
 #include <mutex>
 #include "attn.cuh"
+#include "chunk_attn.cuh"
 #include "gemm.cuh"
 #include "tree.cuh"
 
@@ -51,10 +52,11 @@ extern "C" const char* sub_version(void) { return "0.1 sm_103a"; }
 
 extern "C" int32_t sub_pipeline_timeouts(uint32_t* out) {
   SUB_CHECK_ARG(out, "null pointer");
-  unsigned int a = 0, b = 0;
+  unsigned int a = 0, b = 0, c = 0;
   SUB_TRY(gemv_tma_timeouts(&a));
   SUB_TRY(gemm_tc_timeouts(&b));
-  *out = a + b;
+  SUB_TRY(chunk_tc_timeouts(&c));
+  *out = a + b + c;
   return SUB_OK;
 }
 

@@ -591,12 +591,14 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
 // CTA x joins the unit that is cut at the end of CTA x's part of the line, if
 // that is its first cut: pieces x, x + 1, .. in order.  The rows are shared
 // over grid.y.
-constexpr int JOIN_NT = 128, JOIN_ROWS = 4;
+constexpr int JOIN_NT = 128;
+constexpr int join_rows(int rt) { return rt <= 32 ? 4 : 32; }
 
-template <int D, int RT>
+template <int D, int RT, int KEYS>
 __global__ void __launch_bounds__(JOIN_NT) chunk_join_kernel(ChunkArgs a, int n_ctas, int least) {
+  constexpr int JOIN_ROWS = join_rows(RT);
   __shared__ int64_t s_pre[SUB_MAX_SEQS + 1], s_warp[JOIN_NT / 32];
-  const ChunkPlan<RT, KB> plan(a.t, a.group, a.n_heads_kv);
+  const ChunkPlan<RT, KEYS> plan(a.t, a.group, a.n_heads_kv);
   plan.template scan<JOIN_NT>(s_pre, s_warp);
   const int64_t total = s_pre[a.t.n_seqs];
   const int64_t per = blocks_per_cta(total, n_ctas, least);
@@ -647,6 +649,13 @@ int sm_count() {
   return n;
 }
 
+template <int D, int RT, int KEYS>
+int32_t launch_join(const ChunkArgs& a, int n_ctas, int least, cudaStream_t st) {
+  SUB_CUDA_TRY(launch_k(chunk_join_kernel<D, RT, KEYS>, dim3(n_ctas, RT / join_rows(RT)),
+                        dim3(JOIN_NT), 0, st, a, n_ctas, least));
+  return SUB_OK;
+}
+
 template <int D, bool Q8, int MT>
 int32_t launch_decode(const ChunkArgs& a, int n_ctas, cudaStream_t st) {
   static std::once_flag once;
@@ -658,9 +667,16 @@ int32_t launch_decode(const ChunkArgs& a, int n_ctas, cudaStream_t st) {
   });
   SUB_CUDA_TRY(err);
   SUB_CUDA_TRY(launch_k(chunk_attn_kernel<D, Q8, MT>, dim3(n_ctas), dim3(NT), SMEM, st, a));
-  SUB_CUDA_TRY(launch_k(chunk_join_kernel<D, MT * 16>, dim3(n_ctas, MT * 16 / JOIN_ROWS),
-                        dim3(JOIN_NT), 0, st, a, n_ctas, WARPS));
-  return SUB_OK;
+  return launch_join<D, MT * 16, KB>(a, n_ctas, WARPS, st);
+}
+
+// Many rows per sequence: the tensor-core kernel.  (Rows and sequences are known
+// here, lengths only on the device.)
+bool many_rows(int group, int n_seqs, int n_rows) {
+  return (int64_t)n_rows * group > 32 * (int64_t)n_seqs;
+}
+int tile_rows(int group, int n_seqs, int n_rows) {
+  return many_rows(group, n_seqs, n_rows) ? CHUNK_TC_ROWS : 16;
 }
 
 // Partial results: two per CTA.
@@ -695,7 +711,8 @@ int32_t chunk_attn(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q, const Cach
   a.n_heads_q = n_heads_q;
   a.n_heads_kv = kv->n_heads_kv;
   a.group = n_heads_q / kv->n_heads_kv;
-  a.sl2 = softmax_scale * 1.4426950408889634f;
+  // (a scale of 0 must not meet the masked scores' -infinity)
+  a.sl2 = fmaxf(softmax_scale, 1e-30f) * 1.4426950408889634f;
   const cudaStream_t st = as_stream(stream);
   int64_t need = 0;
   SUB_TRY(sub_chunk_attn_workspace(n_heads_q, kv->n_heads_kv, kv->head_dim, a.t.n_seqs, a.t.n_rows,
@@ -709,7 +726,16 @@ int32_t chunk_attn(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q, const Cach
   }
   const int n_ctas = sm_count();
   a.part_o = reinterpret_cast<float*>(workspace);
-  a.part_ml = reinterpret_cast<float2*>(a.part_o + (int64_t)n_ctas * 2 * 16 * kv->head_dim);
+  const int rt = tile_rows(a.group, a.t.n_seqs, a.t.n_rows);
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + (int64_t)n_ctas * 2 * rt * kv->head_dim);
+  const int64_t pool_rows =
+      (int64_t)kv->n_layers * kv->n_pages * kv->n_heads_kv * kv->page_size;
+  if (rt == CHUNK_TC_ROWS && chunk_tc_fits(pool_rows)) {
+    SUB_TRY(launch_chunk_tc(a, Q8, kv->head_dim, pool_rows, n_ctas, st));
+    return kv->head_dim == 128
+               ? launch_join<128, CHUNK_TC_ROWS, CHUNK_TC_KEYS>(a, n_ctas, CHUNK_TC_LEAST, st)
+               : launch_join<64, CHUNK_TC_ROWS, CHUNK_TC_KEYS>(a, n_ctas, CHUNK_TC_LEAST, st);
+  }
   return kv->head_dim == 128 ? launch_decode<128, Q8, 1>(a, n_ctas, st)
                              : launch_decode<64, Q8, 1>(a, n_ctas, st);
 }
@@ -727,7 +753,8 @@ extern "C" int32_t sub_chunk_attn_workspace(int32_t n_heads_q, int32_t n_heads_k
   SUB_CHECK_ARG(n_heads_kv >= 1 && n_heads_q >= 1 && n_heads_q % n_heads_kv == 0,
                 "Hq must be a multiple of Hkv");
   SUB_CHECK_ARG(n_seqs >= 1 && n_seqs <= SUB_MAX_SEQS && n_rows >= 0, "bad batch sizes");
-  *bytes = n_rows ? part_bytes(sm_count(), 16, head_dim) : 0;
+  *bytes = n_rows ? part_bytes(sm_count(), tile_rows(n_heads_q / n_heads_kv, n_seqs, n_rows),
+                               head_dim) : 0;
   return SUB_OK;
 }
 

@@ -124,4 +124,12 @@ __device__ __forceinline__ int64_t blocks_per_cta(int64_t total, int n_ctas, int
   return per < least ? least : per;
 }
 
+// The kernel for many rows per sequence (chunk_attn_tc.cu): its tiles, and the
+// fewest blocks a CTA takes.
+constexpr int CHUNK_TC_ROWS = 256, CHUNK_TC_KEYS = 128, CHUNK_TC_LEAST = 2;
+bool chunk_tc_fits(int64_t pool_rows);   // rows of head_dim values in a pool
+int32_t launch_chunk_tc(const ChunkArgs& a, bool q8, int head_dim, int64_t pool_rows, int n_ctas,
+                        cudaStream_t st);
+int32_t chunk_tc_timeouts(unsigned int* out);
+
 }  // namespace sub

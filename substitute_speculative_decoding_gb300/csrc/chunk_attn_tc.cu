@@ -1,0 +1,829 @@
+// Attention of new rows over a paged cache, many rows per sequence: chunks of a
+// prompt, on the 5th-generation tensor cores.
+//
+// The same sums as chunk_attn.cu, in tiles of 256 (row, head in group) pairs x
+// 128 keys.  Bound by the tensor cores and, close behind, by the exponentials: a
+// tile pair costs 4 * 512 cycles of tcgen05.mma, and 2 * 128 * 128 exponentials.
+// So two groups of 128 rows alternate: while the tensor cores form one group's
+// scores or output, the four warps of the other turn scores into weights.
+//   warps 0-3, 4-7   softmax of rows 0-127 and 128-255, one row per thread (a
+//                    row's maximum and sum need no exchange between threads),
+//                    the Q tile's way into shared memory, and the results
+//   a producer       K and V blocks of 128 keys, one after the other, into a
+//                    ring: a TMA warp for a bf16 cache (boxes of as many keys
+//                    as a page holds together), or four warps that turn 8-bit
+//                    codes into fp16 code - 128 on the way
+//   one MMA thread   S = Q K^T into tensor memory; then, once the group's weights
+//                    are there, O += P V with P read from tensor memory (in
+//                    place of S, as bf16 or fp16 pairs) and S of the next block
+// O stays in tensor memory.  It is rescaled only when a row's maximum has grown
+// by more than 2^8 since the weights' reference was set: until then the weights
+// exceed 1 by at most that factor, which costs a floating-point value nothing.
+// P is rounded once, to bf16 (half a step 2^-8 relative, random over the keys; the
+// sum takes the unrounded weights) or fp16 for codes; a second product with
+// the rest would make the tensor cores half as slow again.
+//
+// The scale of v_j goes into the weights of codes (see chunk_attn.cu), as
+// 2^(s_ij + log2 vscale_j); the sum takes them divided by it.
+//
+// V rows past the tile's last key hold anything, and so may keys of the chunk
+// that only later rows read.  In blocks that not all rows read to the end the first
+// group's warps look through V: rows past the end and values that are not
+// finite become 0, and if there were any of these, each row adds those that it does
+// read to its result (whatever is added to them, it stays infinite or NaN).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <mutex>
+#include "chunk_attn.cuh"
+#include "tma.cuh"
+
+namespace sub {
+namespace {
+
+using namespace tmah;
+
+constexpr int RT = CHUNK_TC_ROWS, KB = CHUNK_TC_KEYS;
+static_assert(RT == 256 && KB == 128, "two groups of 128 rows, blocks of 128 keys");
+constexpr int GROUP_ROWS = 128;
+constexpr float GROWTH = 8.f;        // log2 of how far weights may exceed 1
+
+__device__ unsigned int g_chunk_timeouts;   // waits that ran out (never expected)
+
+template <int D, bool Q8>
+struct Cfg {
+  static constexpr int STAGE = KB * D * 2;               // K or V of a block, 16-bit values
+  static constexpr int STAGES = D == 128 ? 4 : 6;
+  static constexpr int Q_BYTES = GROUP_ROWS * D * 2;     // of one group
+  static constexpr int N_PROD = Q8 ? 4 : 1;              // producer warps
+  static constexpr int MMA_WARP = 8 + (Q8 ? 4 : 1);
+  static constexpr int THREADS = Q8 ? 512 : 384;         // whole groups of four warps
+  // registers by group of four warps, out of 65536 / THREADS each at the launch
+  // (bf16: the producer and the MMA warp share one)
+  static constexpr int REGS_SOFTMAX = Q8 ? 192 : 208;
+  static constexpr int REGS_PROD = Q8 ? 96 : 80;
+  static constexpr int REGS_MMA = Q8 ? 32 : 80;
+  static_assert((2 * REGS_SOFTMAX + REGS_PROD + (Q8 ? REGS_MMA : 0)) * 128 <=
+                    65536 / THREADS / 8 * 8 * THREADS,
+                "the shares fit what the block is launched with");
+  static constexpr int SCALES = Q8 ? 4 * 3 * KB * 4 : 0; // four blocks' column factors
+  static constexpr int QSCALES = Q8 ? RT * 4 : 0;
+  static constexpr int TAIL = 512;                       // barriers, flags, TMEM address
+  static constexpr int SMEM =
+      1024 + 2 * Q_BYTES + STAGES * STAGE + SCALES + QSCALES + TAIL;
+};
+
+// ---------------------------------------------------------------- tcgen05 --
+// Shared-memory descriptors of operands in the 128-byte swizzle.  K-major (Q, K:
+// rows of 64 values): stride 1024 between groups of 8 rows.  MN-major (V: a key
+// is a row of 64 columns): 1024 between groups of 8 keys, and the next 64 columns a
+// whole block of keys further.
+__device__ __forceinline__ uint64_t desc_k(uint32_t addr) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024u >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)((KB * 128u) >> 4) << 16 |
+         (uint64_t)(1024u >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// kind::f16, fp32 accumulator, M = 128; both operands bf16 (1) or fp16 (0).
+__device__ constexpr uint32_t idesc(int n, bool bf16, bool b_mn) {
+  return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((b_mn ? 1u : 0u) << 16) |
+         ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// 32 columns of the warp's 32 lanes, one lane per thread; wait_ld before use.
+__device__ __forceinline__ void tc_ld32(uint32_t t, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(t)
+      : "memory");
+}
+__device__ __forceinline__ void tc_st32(uint32_t t, const float* v) {
+  const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(t),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+      "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t t, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(t),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// Two fp32 operations in one instruction.
+union F2 {
+  float2 f;
+  uint64_t u;
+};
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  F2 x{a}, y{b}, z{c}, d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.u) : "l"(x.u), "l"(y.u), "l"(z.u));
+  return d.f;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  F2 x{a}, y{b}, d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.u) : "l"(x.u), "l"(y.u));
+  return d.f;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  F2 x{a}, y{b}, d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.u) : "l"(x.u), "l"(y.u));
+  return d.f;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t codes2(uint32_t w, uint32_t sel) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;"
+      : "=r"(r)
+      : "r"(__byte_perm(w, 0x64646464u, sel)), "r"(0x64806480u));
+  return r;
+}
+__device__ __forceinline__ void fence_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Bounded wait.  One that runs out is counted and ends the CTA's work: every
+// later wait returns at once, nothing more is issued, and the results are not valid.
+struct Gate {
+  volatile int* dead;
+  __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) const {
+    for (uint32_t i = 0; i < (1u << 20); ++i) {
+      if (mbar_try_wait(bar, parity)) return true;
+      if ((i & 63) == 63 && *dead) return false;
+    }
+    if (!*dead) {
+      *dead = 1;
+      atomicAdd(&g_chunk_timeouts, 1u);
+    }
+    return false;
+  }
+  // by a whole warp, which goes on or stops together
+  __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) const {
+    return __all_sync(~0u, wait(bar, parity));
+  }
+};
+
+// Bit of a block's 16-key part in its word of missing pages: the TMA warp writes
+// the word, the four converter warps a byte each.
+template <bool Q8>
+__device__ constexpr int miss_bit(int part) {
+  return Q8 ? 8 * (part >> 1) + (part & 1) : part;
+}
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+struct Maps {
+  CUtensorMap k, v;   // pool rows [all rows, D] bf16, boxes of 64 columns x box keys
+};
+
+// ------------------------------------------------------------------ kernel --
+template <int D, bool Q8>
+__global__ void __launch_bounds__(Cfg<D, Q8>::THREADS, 1)
+chunk_tc_kernel(const __grid_constant__ Maps maps, const ChunkArgs a, const int box,
+                const int pool_rows) {
+  using C = Cfg<D, Q8>;
+  constexpr int STAGES = C::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int64_t s_pre[SUB_MAX_SEQS + 1], s_warp[C::THREADS / 32];
+  __shared__ int s_rows[2][Q8 ? KB : 1];   // pool rows of two blocks' keys (converters)
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* const base_p = smem_raw + (base - smem_u32(smem_raw));
+  const uint32_t q_s = base, ring_s = base + 2 * C::Q_BYTES;
+  uint8_t* const after = base_p + 2 * C::Q_BYTES + STAGES * C::STAGE;
+  float* const s_scale = reinterpret_cast<float*>(after);                  // [4][3][KB]
+  float* const s_qs = reinterpret_cast<float*>(after + C::SCALES);         // [RT]
+  uint8_t* const tail = after + C::SCALES + C::QSCALES;
+  const uint32_t bars = smem_u32(tail);
+  auto kv_full = [&](int s) { return bars + 8u * s; };
+  auto kv_empty = [&](int s) { return bars + 8u * (STAGES + s); };
+  auto q_full = [&](int t) { return bars + 8u * (2 * STAGES + t); };
+  auto s_full = [&](int t) { return bars + 8u * (2 * STAGES + 2 + t); };
+  auto p_full = [&](int t) { return bars + 8u * (2 * STAGES + 4 + t); };
+  auto o_full = [&](int t) { return bars + 8u * (2 * STAGES + 6 + t); };
+  int* const flags = reinterpret_cast<int*>(tail + 8 * (2 * STAGES + 8));
+  volatile int* const s_dead = flags;            // a wait ran out
+  volatile int* const s_odd = flags + 1;         // [2] piece (by parity) that met infinite values or NaN
+  volatile uint32_t* const s_miss = reinterpret_cast<uint32_t*>(flags + 3);   // [8] blocks' missing 16-key parts
+  uint32_t* const s_tmem = reinterpret_cast<uint32_t*>(flags + 11);
+  static_assert(8 * (2 * STAGES + 8) + 12 * 4 <= C::TAIL, "tail");
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(s_tmem)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (tid == 32) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(kv_full(s), Q8 ? C::N_PROD * 32 : 1);
+      mbar_init(kv_empty(s), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(q_full(t), GROUP_ROWS);
+      mbar_init(s_full(t), 1);
+      mbar_init(p_full(t), GROUP_ROWS);
+      mbar_init(o_full(t), 1);
+    }
+    *s_dead = 0;
+    s_odd[0] = s_odd[1] = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  pdl_wait();
+  pdl_trigger();
+  const ChunkPlan<RT, KB> plan(a.t, a.group, a.n_heads_kv);
+  tc_fence_before();
+  plan.template scan<C::THREADS>(s_pre, s_warp);   // ends with a barrier
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  const int64_t total = s_pre[a.t.n_seqs];
+  const int64_t per = blocks_per_cta(total, gridDim.x, CHUNK_TC_LEAST);
+  const int64_t line_lo = blockIdx.x * per, line_hi = min(total, line_lo + per);
+  const Gate gate{s_dead};
+  const int G = a.group;
+
+  if (warp < 8) more_registers<C::REGS_SOFTMAX>();
+  else if (!Q8 || warp < 12) fewer_registers<C::REGS_PROD>();
+  else fewer_registers<C::REGS_MMA>();
+
+  if (warp < 8) {
+    // ------------------------------------------------ softmax, Q, results
+    const int t = warp >> 2, r = (warp & 3) * 32 + lane;   // group, row in it
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + t * 128 + lanes, tO = tmem + 256 + t * 128 + lanes;
+    uint32_t n_s = 0, n_o = 0;      // blocks and pieces seen by this group
+    uint32_t items = 0;             // ring items before this piece
+    int piece = 0;
+    for (int64_t at = line_lo; at < line_hi; ++piece) {
+      const auto u = plan.find(s_pre, at);
+      const int kb0 = (int)(at - u.begin), kb1 = (int)min((int64_t)u.n_blocks, line_hi - u.begin);
+      const int row0 = u.tile * RT + t * GROUP_ROWS;       // the group's first row
+      const int64_t slot = 2 * (int64_t)blockIdx.x + (at == line_lo ? 0 : 1);
+      at = u.begin + kb1;
+      const uint32_t first_item = items;
+      items += 2 * (kb1 - kb0);
+      if (row0 >= u.rows * G) continue;                    // an empty second group
+
+      // ---- Q: 16-byte chunks c of a row at c ^ (row % 8) of its 128-byte line ----
+      {
+        // (each warp its own threads' rows)
+        constexpr int CH = D / 8, RP = 32 / CH;            // chunks of a row, rows per pass
+        const int c = lane % CH;
+        const uint32_t dst0 = q_s + t * C::Q_BYTES + (c >> 3) * (GROUP_ROWS * 128);
+#pragma unroll 4
+        for (int i = 0; i < CH; ++i) {
+          const int rr = (warp & 3) * 32 + i * RP + lane / CH, q = (row0 + rr) / G;
+          uint4 w = make_uint4(0, 0, 0, 0);
+          if (q < u.rows)
+            w = ldg_nc_v4(a.Q + (int64_t)(u.row0 + q) * a.ldq +
+                          (int64_t)(u.head * G + (row0 + rr) % G) * D + c * 8);
+          if constexpr (Q8) {
+            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+            float big = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              big = fmaxf(big, fmaxf(fabsf(bf16lo(x[k])), fabsf(bf16hi(x[k]))));
+#pragma unroll
+            for (int o = CH / 2; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, o));
+            const int e = min(126, max(-126, (int)(__float_as_uint(big) >> 23) - 127));
+            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+            if (c == 0)
+              s_qs[t * GROUP_ROWS + rr] = a.sl2 * __uint_as_float((uint32_t)(127 + e) << 23);
+            w.x = pack_f16x2(bf16lo(x[0]) * down, bf16hi(x[0]) * down);
+            w.y = pack_f16x2(bf16lo(x[1]) * down, bf16hi(x[1]) * down);
+            w.z = pack_f16x2(bf16lo(x[2]) * down, bf16hi(x[2]) * down);
+            w.w = pack_f16x2(bf16lo(x[3]) * down, bf16hi(x[3]) * down);
+          }
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
+                           dst0 + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)),
+                       "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w)
+                       : "memory");
+        }
+        fence_async();
+        mbar_arrive(q_full(t));
+        __syncwarp();   // s_qs
+      }
+      const int q = (row0 + r) / G;
+      const bool real = q < u.rows;
+      const int lim = real ? min(u.pos + q, u.n_keys - 1) : -1;             // keys 0 .. lim are read
+      const int lim_first = min(u.pos + u.tile * RT / G, u.n_keys - 1);     // by every row of the tile
+      float factor = a.sl2;
+      if constexpr (Q8) factor = s_qs[t * GROUP_ROWS + r];
+
+      float ref = 0.f, l = 0.f;    // weights are 2^(score - ref)
+      bool any = false;            // a key has been read
+      for (int kb = kb0; kb < kb1; ++kb) {
+        const int key0 = kb * KB;
+        const uint32_t item = first_item + 2 * (kb - kb0);
+        if (!gate.wait_warp(s_full(t), n_s & 1)) break;
+        ++n_s;
+        tc_fence_after();
+        float s[KB];
+#pragma unroll
+        for (int c = 0; c < KB; c += 32) tc_ld32(tS + c, s + c);
+        const uint32_t miss = s_miss[(item >> 1) & 7];
+        const bool behind = key0 + KB - 1 > lim_first;   // the same for all rows of the tile
+        const bool edge = behind || miss;
+        const float* const sc = s_scale + ((item >> 1) & 3) * (3 * KB);
+        wait_ld();
+        if constexpr (Q8) {
+          // scores in base 2, plus log2 of the value's scale
+          const float2 f2 = make_float2(factor, factor);
+#pragma unroll
+          for (int c = 0; c < KB; c += 4) {
+            const float4 k4 = *reinterpret_cast<const float4*>(sc + c);
+            const float4 l4 = *reinterpret_cast<const float4*>(sc + KB + c);
+            const float2 x = fma2(mul2(make_float2(s[c], s[c + 1]), f2), make_float2(k4.x, k4.y),
+                                  make_float2(l4.x, l4.y));
+            const float2 y = fma2(mul2(make_float2(s[c + 2], s[c + 3]), f2),
+                                  make_float2(k4.z, k4.w), make_float2(l4.z, l4.w));
+            s[c] = x.x;
+            s[c + 1] = x.y;
+            s[c + 2] = y.x;
+            s[c + 3] = y.y;
+          }
+        }
+        if (edge) {
+          const int last = lim - key0;   // columns past it are not read
+#pragma unroll
+          for (int c = 0; c < KB; ++c)
+            if (c > last || ((miss >> miss_bit<Q8>(c >> 4)) & 1u)) s[c] = -INFINITY;
+        }
+        float top = s[0];
+#pragma unroll
+        for (int c = 1; c < KB; ++c) top = fmaxf(top, s[c]);
+        if constexpr (!Q8) top = top == -INFINITY ? top : top * factor;
+        // ---- the reference, and the output that was formed with another ----
+        const bool grow = top > ref + GROWTH || (!any && top != -INFINITY);
+        if (__any_sync(~0u, grow)) {
+          const float f = grow && any ? exp2_fast(ref - top) : 1.f;
+          if (grow) {
+            ref = top;
+            any = true;
+          }
+          l *= f;
+          if (kb > kb0 && __any_sync(~0u, f != 1.f)) {
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+              float o[32];
+              __syncwarp();
+              tc_ld32(tO + c, o);
+              wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= f;
+              tc_st32(tO + c, o);
+            }
+          }
+        }
+        // ---- weights, in place of the scores' first columns ----
+        // codes: times 2^7, so that they reach fp16's range (2^15) but not past it
+        const float shift = Q8 ? 7.f - ref : -ref;
+        const float2 f2 = make_float2(Q8 ? 1.f : factor, Q8 ? 1.f : factor);
+        const float2 d2 = make_float2(shift, shift);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int c0 = 0; c0 < KB; c0 += 32) {
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int c = c0 + 2 * i;
+            float2 e = make_float2(s[c], s[c + 1]);
+            e = Q8 ? add2(e, d2) : fma2(e, f2, d2);
+            e.x = exp2_fast(e.x);
+            e.y = exp2_fast(e.y);
+            if constexpr (Q8) {
+              const float2 inv = *reinterpret_cast<const float2*>(sc + 2 * KB + c);
+              if (edge) {   // a key that is not read may have any scale
+                sum[i & 1].x += s[c] == -INFINITY ? 0.f : e.x * inv.x;
+                sum[i & 1].y += s[c + 1] == -INFINITY ? 0.f : e.y * inv.y;
+              } else {
+                sum[i & 1] = fma2(e, inv, sum[i & 1]);
+              }
+              w[i] = pack_f16x2(e.x, e.y);
+            } else {
+              sum[i & 1] = add2(sum[i & 1], e);
+              w[i] = pack_bf16x2(e.x, e.y);
+            }
+          }
+          tc_st16(tS + c0 / 2, w);
+        }
+        l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
+        if (!Q8 && behind && t == 0) {
+          // V of the block: row r of it is this thread's
+          const uint32_t st = (item + 1) % STAGES;
+          if (!gate.wait_warp(kv_full(st), ((item + 1) / STAGES) & 1)) break;
+          const uint32_t v0 = ring_s + st * C::STAGE + r * 128;
+          const bool past = key0 + r >= u.n_keys;
+          bool odd = false;
+#pragma unroll 4
+          for (int i = 0; i < D / 8; ++i) {
+            const uint32_t at16 = v0 + (i >> 3) * (KB * 128) + (((i ^ r) & 7) << 4);
+            uint4 w = lds128(at16);
+            uint32_t x[4] = {w.x, w.y, w.z, w.w};
+            bool hit = past;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const bool lo = (x[k] & 0x7f80u) == 0x7f80u, hi = (x[k] & 0x7f800000u) == 0x7f800000u;
+              odd |= (lo || hi) && !past;
+              hit |= lo || hi;
+              if (past || lo) x[k] &= 0xffff0000u;
+              if (past || hi) x[k] &= 0x0000ffffu;
+            }
+            if (hit)
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at16), "r"(x[0]),
+                           "r"(x[1]), "r"(x[2]), "r"(x[3])
+                           : "memory");
+          }
+          if (odd) s_odd[piece & 1] = piece + 1;
+          fence_async();
+        }
+        wait_st();
+        tc_fence_before();
+        mbar_arrive(p_full(t));
+      }
+      // ---- the piece's result ----
+      if (!gate.wait_warp(o_full(t), n_o & 1)) break;
+      ++n_o;
+      tc_fence_after();
+      const bool whole = kb0 == 0 && kb1 == u.n_blocks;
+      const bool odd = !Q8 && s_odd[piece & 1] == piece + 1;
+      const float mul = whole ? (any ? 1.f / l : 0.f) : 1.f;
+      uint16_t* const out = a.O + ((int64_t)(u.row0 + q) * a.n_heads_q + u.head * G + (row0 + r) % G) * D;
+      float* const part = a.part_o + (slot * RT + t * GROUP_ROWS + r) * D;
+#pragma unroll
+      for (int c = 0; c < D; c += 32) {
+        float o[32];
+        __syncwarp();
+        tc_ld32(tO + c, o);
+        wait_ld();
+        if (odd && real) {
+          // values that are not finite, of the keys this row reads in the blocks looked through
+          const uint16_t* const vp = reinterpret_cast<const uint16_t*>(a.v);
+          const int from = max(kb0, max(0, lim_first + 1) / KB) * KB;
+          for (int key = from; key <= min(lim, kb1 * KB - 1); ++key) {
+            const int page = page_of(a.t, u.b, key);
+            if (page < 0) continue;
+            const uint16_t* const x =
+                vp + pool_row(a.t, a.layer, a.n_heads_kv, page, u.head,
+                              (int)((uint32_t)key % (uint32_t)a.t.page_size)) * D + c;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if ((x[i] & 0x7f80u) == 0x7f80u) o[i] += bf16_bits_to_f32(x[i]);
+          }
+        }
+        if (real && whole) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 8)
+            *reinterpret_cast<uint4*>(out + c + i) =
+                make_uint4(pack_bf16x2(o[i] * mul, o[i + 1] * mul),
+                           pack_bf16x2(o[i + 2] * mul, o[i + 3] * mul),
+                           pack_bf16x2(o[i + 4] * mul, o[i + 5] * mul),
+                           pack_bf16x2(o[i + 6] * mul, o[i + 7] * mul));
+        } else if (real) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            __stcg(reinterpret_cast<float4*>(part + c + i),
+                   make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]));
+        }
+      }
+      if (!whole && real)
+        __stcg(a.part_ml + slot * RT + t * GROUP_ROWS + r,
+               make_float2(any ? ref : -INFINITY, l));
+      __syncwarp();
+      tc_fence_before();   // O is read before the next piece's first weights are announced
+      if (*s_dead) break;
+    }
+  } else if (warp >= 8 + (Q8 ? 4 : 0) && warp != 8) {
+    if (warp == C::MMA_WARP && lane == 0) {
+      // -------------------------------------------------------- MMA issuer
+      constexpr uint32_t id_s = idesc(KB, !Q8, false), id_o = idesc(D, !Q8, true);
+      uint32_t it = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
+      bool ok = true;
+      auto scores = [&](int t, uint32_t item) {
+        const uint32_t qb = q_s + t * C::Q_BYTES, kb = ring_s + (item % STAGES) * C::STAGE;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k >> 2) * (KB * 128) + (k & 3) * 32;
+          mma_ss(tmem + t * 128, desc_k(qb + off), desc_k(kb + off), id_s, k > 0);
+        }
+        tc_commit(s_full(t));
+      };
+      for (int64_t at = line_lo; at < line_hi && ok;) {
+        const auto u = plan.find(s_pre, at);
+        const int kb0 = (int)(at - u.begin), kb1 = (int)min((int64_t)u.n_blocks, line_hi - u.begin);
+        at = u.begin + kb1;
+        const int n = kb1 - kb0;
+        const int groups = u.tile * RT + GROUP_ROWS < u.rows * G ? 2 : 1;
+        ok = gate.wait(kv_full(it % STAGES), (it / STAGES) & 1);
+        for (int t = 0; t < groups && ok; ++t) {
+          ok = gate.wait(q_full(t), n_q[t]++ & 1);
+          tc_fence_after();
+          if (ok) scores(t, it);
+        }
+        if (!ok) break;
+        tc_commit(kv_empty(it % STAGES));
+        for (int i = 0; i < n && ok; ++i, it += 2) {
+          const uint32_t vi = it + 1, ki = it + 2;
+          for (int t = 0; t < groups && ok; ++t) {
+            if (t == 0) ok = gate.wait(kv_full(vi % STAGES), (vi / STAGES) & 1);
+            ok = ok && gate.wait(p_full(t), n_p[t]++ & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t vb = ring_s + (vi % STAGES) * C::STAGE;
+#pragma unroll
+            for (int k = 0; k < KB / 16; ++k)
+              mma_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8, desc_mn(vb + k * 2048), id_o,
+                     i > 0 || k > 0);
+            if (t == groups - 1) tc_commit(kv_empty(vi % STAGES));
+            if (i + 1 < n) {
+              if (t == 0) ok = gate.wait(kv_full(ki % STAGES), (ki / STAGES) & 1);
+              if (!ok) break;
+              tc_fence_after();
+              scores(t, ki);
+              if (t == groups - 1) tc_commit(kv_empty(ki % STAGES));
+            } else {
+              tc_commit(o_full(t));
+            }
+          }
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ producers
+    uint32_t it = 0;
+    bool ok = true;
+    for (int64_t at = line_lo; at < line_hi && ok;) {
+      const auto u = plan.find(s_pre, at);
+      const int kb0 = (int)(at - u.begin), kb1 = (int)min((int64_t)u.n_blocks, line_hi - u.begin);
+      at = u.begin + kb1;
+      const int32_t* const pages = a.t.pages + (int64_t)u.b * a.t.width;
+      if constexpr (!Q8) {
+        // lanes 0..15 move K, 16..31 V: 64 columns (lane & 1) of the boxes (lane & 15) / 2, ..
+        const int half = lane & 1, side = lane >> 4, b0 = (lane & 15) >> 1;
+        const int n_box = KB / box;
+        for (int kb = kb0; kb < kb1 && ok; ++kb, it += 2) {
+          // rows of the pool, one per box; past the pool (zeros) where there is no page
+          const int key = kb * KB + b0 * box;
+          int y = pool_rows;
+          bool here = false;
+          if (b0 < n_box && key < u.n_keys) {
+            const int page = pages[(uint32_t)key / (uint32_t)a.t.page_size];
+            here = (unsigned)page < (unsigned)a.t.n_pages;
+            if (here)
+              y = (int)pool_row(a.t, a.layer, a.n_heads_kv, page, u.head,
+                                (int)((uint32_t)key % (uint32_t)a.t.page_size));
+          }
+          // 16-key parts without a page (those past the last key count as read past the end)
+          const unsigned gone = __ballot_sync(~0u, side == 0 && half == 0 && b0 < n_box && !here &&
+                                                       key < u.n_keys);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {   // K, then V
+            const uint32_t item = it + x, st = item % STAGES;
+            if (item >= STAGES) ok = ok && gate.wait(kv_empty(st), ((item / STAGES) - 1) & 1);
+            ok = __all_sync(~0u, ok);
+            if (!ok) break;
+            if (lane == 0) {
+              if (x == 0) {
+                uint32_t miss = 0;
+                for (int b = 0; b < n_box; ++b)
+                  if ((gone >> (2 * b)) & 1u) miss |= ((1u << (box / 16)) - 1u) << (b * box / 16);
+                s_miss[(item >> 1) & 7] = miss;
+              }
+              mbar_expect_tx(kv_full(st), C::STAGE);
+            }
+            __syncwarp();
+            if (side == x && b0 < n_box && half < D / 64)
+              tma_load_2d(ring_s + st * C::STAGE + half * (KB * 128) + b0 * box * 128,
+                          x ? &maps.v : &maps.k, half * 64, y, kv_full(st));
+          }
+        }
+      } else {
+        // CH lanes per key, 16 codes each; thread ptid looks up the pool row of key ptid
+        constexpr int CH = D / 16, PASS = 128 / CH, N = KB / PASS;
+        const int ptid = tid - 256, c = ptid % CH, k0 = ptid / CH;
+        uint4 w[N];
+        auto look_up = [&](int kb) {
+          const int key = kb * KB + ptid;
+          int row = -1;
+          if (key < u.n_keys) {
+            const int page = pages[(uint32_t)key / (uint32_t)a.t.page_size];
+            if ((unsigned)page < (unsigned)a.t.n_pages)
+              row = (int)pool_row(a.t, a.layer, a.n_heads_kv, page, u.head,
+                                  (int)((uint32_t)key % (uint32_t)a.t.page_size));
+          }
+          s_rows[kb & 1][ptid] = row;
+          return row;
+        };
+        auto load = [&](const void* pool, int kb) {
+          const uint8_t* const p = reinterpret_cast<const uint8_t*>(pool) + c * 16;
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const int row = s_rows[kb & 1][i * PASS + k0];
+            w[i] = row >= 0 ? ldg_nc_v4(p + (int64_t)row * D)
+                            : make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
+          }
+        };
+        auto meet = [] { asm volatile("bar.sync 3, 128;" ::: "memory"); };
+        int row = look_up(kb0), next = -1;
+        meet();
+        load(a.k, kb0);
+        // no thread leaves this loop early (they meet in it): after a wait ran out
+        // they only go on writing to their own shared memory
+        for (int kb = kb0; kb < kb1; ++kb, it += 2, row = next) {
+          float ksc = 0.f, vsc = 1.f;
+          if (row >= 0) {
+            ksc = a.ks[row];
+            vsc = a.vs[row];
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t item = it + x, st = item % STAGES;
+            if (x == 0) next = kb + 1 < kb1 ? look_up(kb + 1) : -1;
+            if (item >= STAGES) gate.wait(kv_empty(st), ((item / STAGES) - 1) & 1);
+            if (x == 0) {
+              float* const sc = s_scale + ((item >> 1) & 3) * (3 * KB) + ptid;
+              sc[0] = ksc;
+              sc[KB] = log2f(vsc);
+              sc[2 * KB] = __fdiv_rn(1.f, vsc);
+              const unsigned gone = __ballot_sync(~0u, row < 0 && kb * KB + ptid < u.n_keys);
+              // 16-key parts: bits 0 and 16 of the warp's 32 keys
+              if (lane == 0)
+                reinterpret_cast<volatile uint8_t*>(s_miss + ((item >> 1) & 7))[warp - 8] =
+                    (uint8_t)((gone & 1u) | ((gone >> 16) & 1u) << 1);
+            }
+            const uint32_t dst = ring_s + st * C::STAGE;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+              const int key = i * PASS + k0;
+              const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+              uint32_t h[8];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                h[2 * k] = codes2(v[k], 0x4140u);
+                h[2 * k + 1] = codes2(v[k], 0x4342u);
+              }
+              // 16 values are chunks 2 c, 2 c + 1 of the row; lanes of the second half of the
+              // row store theirs in the other order, so that eight lanes meet all banks
+              const uint32_t line = dst + (c >> 2) * (KB * 128) + key * 128;
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const int z = y ^ ((c >> 2) & 1);
+                const uint32_t p = line + ((((c & 3) * 2 + z) ^ (key & 7)) << 4);
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(p),
+                             "r"(z ? h[4] : h[0]), "r"(z ? h[5] : h[1]), "r"(z ? h[6] : h[2]),
+                             "r"(z ? h[7] : h[3])
+                             : "memory");
+              }
+            }
+            // the next item's codes are on their way while this one is used
+            if (x == 0) load(a.v, kb);
+            meet();
+            if (x == 1 && kb + 1 < kb1) load(a.k, kb + 1);
+            fence_async();
+            mbar_arrive(kv_full(st));
+          }
+        }
+      }
+    }
+    if constexpr (!Q8) {
+      // after a wait ran out: copies of the last stages may still be under way
+      if (!ok && lane == 0)
+        for (int s = 0; s < STAGES; ++s)
+          for (uint32_t i = 0; i < (1u << 16) && !mbar_try_wait(kv_full(s), 0) && !mbar_try_wait(kv_full(s), 1); ++i) {
+          }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
+                 : "memory");
+}
+
+// -------------------------------------------------------------------- host --
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+bool pool_map(CUtensorMap* m, const void* pool, int64_t rows, int d, int box) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)d * 2};
+  const cuuint32_t boxes[2] = {64, (cuuint32_t)box}, es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(pool), dims, strides, boxes,
+            es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool Q8>
+int32_t launch(const ChunkArgs& a, int64_t rows, int n_ctas, cudaStream_t st) {
+  using C = Cfg<D, Q8>;
+  static std::once_flag once;
+  static cudaError_t err = cudaSuccess;
+  std::call_once(once, [] {
+    err = cudaFuncSetAttribute(chunk_tc_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               C::SMEM);
+  });
+  SUB_CUDA_TRY(err);
+  Maps maps;
+  memset(&maps, 0, sizeof(maps));
+  int box = 16;
+  while (box < KB && a.t.page_size % (2 * box) == 0) box *= 2;
+  if (!Q8 && (!pool_map(&maps.k, a.k, rows, D, box) || !pool_map(&maps.v, a.v, rows, D, box)))
+    return fail(SUB_ECUDA, "chunk_attn: the cache's tensor map was refused");
+  SUB_CUDA_TRY(launch_k(chunk_tc_kernel<D, Q8>, dim3(n_ctas), dim3(C::THREADS), C::SMEM, st, maps, a,
+                        box, (int)rows));
+  return SUB_OK;
+}
+
+}  // namespace
+
+bool chunk_tc_fits(int64_t pool_rows) { return pool_rows < (1ll << 31) - 4096; }
+
+int32_t launch_chunk_tc(const ChunkArgs& a, bool q8, int head_dim, int64_t pool_rows, int n_ctas,
+                        cudaStream_t st) {
+  if (q8) return head_dim == 128 ? launch<128, true>(a, pool_rows, n_ctas, st)
+                                 : launch<64, true>(a, pool_rows, n_ctas, st);
+  return head_dim == 128 ? launch<128, false>(a, pool_rows, n_ctas, st)
+                         : launch<64, false>(a, pool_rows, n_ctas, st);
+}
+
+int32_t chunk_tc_timeouts(unsigned int* out) {
+  SUB_CUDA_TRY(cudaMemcpyFromSymbol(out, g_chunk_timeouts, sizeof(unsigned int)));
+  return SUB_OK;
+}
+
+}  // namespace sub

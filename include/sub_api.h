@@ -272,8 +272,8 @@ int32_t sub_kv_compact(const sub_kv_cache* kv, int64_t root_pos, const int32_t* 
  *
  * Sequence b owns rows [start[b], start[b+1]) of the caller's row tensors; its
  * row i stands at position pos[b] + i.  Rows before start[0] and from
- * start[n_seqs] on (padding) belong to no sequence: no call reads or writes
- * them.  start must not decrease; entries outside [0, n_rows] are clamped.
+ * start[n_seqs] on (padding) belong to no sequence: no call writes them, and
+ * what they hold has no effect.  start must not decrease; entries outside [0, n_rows] are clamped.
  * A cache used here has one page-table row per sequence:
  * page_table[b * P + t / page_size], P = ceil(capacity / page_size), and
  * n_pages * n_layers pages of any sequence in one pool.  An entry outside

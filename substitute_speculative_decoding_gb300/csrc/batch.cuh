@@ -36,9 +36,11 @@ __device__ __forceinline__ int seq_rows(const SeqTable& t, int b) {
 __device__ __forceinline__ int row_seq(const SeqTable& t, int row, int lane) {
   static_assert(SUB_MAX_SEQS <= 1024, "two rounds of 32");
   const int n = t.n_seqs;
-  // entries 32, 64, ..: how many whole groups of 32 lie at or below the row
-  const int e = (lane + 1) * 32;
-  const int groups = __popc(__ballot_sync(~0u, e <= n && t.start[min(e, n)] <= row));
+  int groups = 0;
+  if (n > 32) {   // entries 32, 64, ..: how many whole groups of 32 lie at or below the row
+    const int e = (lane + 1) * 32;
+    groups = __popc(__ballot_sync(~0u, e <= n && t.start[min(e, n)] <= row));
+  }
   const int f = groups * 32 + lane + 1;
   const int b = groups * 32 + __popc(__ballot_sync(~0u, f <= n && t.start[min(f, n)] <= row));
   return b < n && t.start[0] <= row ? b : -1;

@@ -584,55 +584,77 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
     }
     __syncthreads();
     at = u.begin + kb1;
+    if (tid == 0 && at >= line_hi) a.cuts[blockIdx.x] = make_cut(u, kb1, line_lo, per);
   }
+  if (tid == 0 && line_lo >= line_hi) a.cuts[blockIdx.x].pieces = 0;
 }
 
 // ------------------------------------------------------------------- joins --
-// CTA x joins the unit that is cut at the end of CTA x's part of the line, if
-// that is its first cut: pieces x, x + 1, .. in order.  The rows are shared
-// over grid.y.
-constexpr int JOIN_NT = 128;
-constexpr int join_rows(int rt) { return rt <= 32 ? 4 : 32; }
+// The rows of a cut unit from their pieces, in order: one warp per row, whose
+// lanes hold the pieces' maxima and sums, then four columns each.  A few dependent
+// rounds of reads from L2, at the end of every call: what it needs to know
+// lies ready in the list of cuts.
+constexpr int JOIN_WARPS = 4, JOIN_MAX = 5;   // warps per CTA; 32 * JOIN_MAX pieces at most
+constexpr int join_rows(int rt) { return rt <= 32 ? JOIN_WARPS : 4 * JOIN_WARPS; }   // per CTA
 
-template <int D, int RT, int KEYS>
-__global__ void __launch_bounds__(JOIN_NT) chunk_join_kernel(ChunkArgs a, int n_ctas, int least) {
-  constexpr int JOIN_ROWS = join_rows(RT);
-  __shared__ int64_t s_pre[SUB_MAX_SEQS + 1], s_warp[JOIN_NT / 32];
-  const ChunkPlan<RT, KEYS> plan(a.t, a.group, a.n_heads_kv);
-  plan.template scan<JOIN_NT>(s_pre, s_warp);
-  const int64_t total = s_pre[a.t.n_seqs];
-  const int64_t per = blocks_per_cta(total, n_ctas, least);
-  const int64_t cut = (blockIdx.x + 1) * per;
-  pdl_wait();   // lengths are older than the kernel before; its partial results are not
+template <int D, int RT>
+__global__ void __launch_bounds__(JOIN_WARPS * 32) chunk_join_kernel(ChunkArgs a) {
+  pdl_wait();
   pdl_trigger();
-  if (cut >= total) return;
-  const auto u = plan.find(s_pre, cut);
-  if (u.begin == cut || u.begin < cut - per) return;   // not cut here, or first cut earlier
-  const int64_t first = 2 * (int64_t)blockIdx.x + (u.begin == cut - per ? 0 : 1);
-  const int n = (int)((u.begin + u.n_blocks - 1) / per) - (int)blockIdx.x + 1;
-  auto slot = [&](int i) { return i == 0 ? first : 2 * ((int64_t)blockIdx.x + i); };
-  const int G = a.group;
-  for (int idx = threadIdx.x; idx < JOIN_ROWS * (D / 4); idx += JOIN_NT) {
-    const int r = blockIdx.y * JOIN_ROWS + idx / (D / 4), d = (idx % (D / 4)) * 4;
-    const int row = u.tile * RT + r, q = row / G;
-    if (q >= u.rows) continue;
+  const ChunkCut c = a.cuts[blockIdx.x];
+  if (c.pieces == 0) return;
+  constexpr int LANES = D / 4, PER = 32 / LANES;   // lanes per piece, pieces per load
+  const int lane = threadIdx.x & 31, n = c.pieces;
+  const int d = (lane % LANES) * 4, part = lane / LANES;
+  auto slot = [&](int i) { return i == 0 ? c.first : 2 * ((int)blockIdx.x + i); };
+  for (int r = blockIdx.y * join_rows(RT) + (threadIdx.x >> 5); r < (int)(blockIdx.y + 1) * join_rows(RT);
+       r += JOIN_WARPS) {
+    const int row = c.tile * RT + r, q = row / a.group;
+    if (q >= c.rows) break;
+    float2 ml[JOIN_MAX];
     float big = -INFINITY;
-    for (int i = 0; i < n; ++i) big = fmaxf(big, __ldcg(a.part_ml + slot(i) * RT + r).x);
-    float sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float2 ml = __ldcg(a.part_ml + slot(i) * RT + r);
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + (slot(i) * RT + r) * D + d));
-      const float f = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - big);
-      sum = fmaf(f, ml.y, sum);
-      x[0] = fmaf(f, v.x, x[0]);
-      x[1] = fmaf(f, v.y, x[1]);
-      x[2] = fmaf(f, v.z, x[2]);
-      x[3] = fmaf(f, v.w, x[3]);
+#pragma unroll
+    for (int k = 0; k < JOIN_MAX; ++k) {
+      const int i = k * 32 + lane;
+      ml[k] = i < n ? __ldcg(a.part_ml + (int64_t)slot(i) * RT + r) : make_float2(-INFINITY, 0.f);
+      big = fmaxf(big, ml[k].x);
+    }
+    big = warp_max(big);
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < JOIN_MAX; ++k) {
+      ml[k].x = ml[k].x == -INFINITY ? 0.f : exp2_fast(ml[k].x - big);   // the piece's weight
+      sum = fmaf(ml[k].x, ml[k].y, sum);
+    }
+    sum = warp_sum(sum);
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < JOIN_MAX; ++k) {
+      if (k * 32 >= n) break;
+#pragma unroll 8
+      for (int i0 = 0; i0 < 32; i0 += PER) {
+        if (k * 32 + i0 >= n) break;
+        const int i = k * 32 + i0 + part;
+        const float f = __shfl_sync(~0u, ml[k].x, i0 + part);
+        if (i < n) {
+          const float4 v =
+              __ldcg(reinterpret_cast<const float4*>(a.part_o + ((int64_t)slot(i) * RT + r) * D + d));
+          x[0] = fmaf(f, v.x, x[0]);
+          x[1] = fmaf(f, v.y, x[1]);
+          x[2] = fmaf(f, v.z, x[2]);
+          x[3] = fmaf(f, v.w, x[3]);
+        }
+      }
+    }
+    if constexpr (PER == 2) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] += __shfl_xor_sync(~0u, x[e], 16);
     }
     const float inv = big == -INFINITY ? 0.f : 1.f / sum;
-    *reinterpret_cast<uint2*>(a.O + ((int64_t)(u.row0 + q) * a.n_heads_q + u.head * G + row % G) * D + d) =
-        make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
+    if (part == 0)
+      *reinterpret_cast<uint2*>(
+          a.O + ((int64_t)(c.row0 + q) * a.n_heads_q + c.head * a.group + row % a.group) * D + d) =
+          make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
   }
 }
 
@@ -649,10 +671,11 @@ int sm_count() {
   return n;
 }
 
-template <int D, int RT, int KEYS>
-int32_t launch_join(const ChunkArgs& a, int n_ctas, int least, cudaStream_t st) {
-  SUB_CUDA_TRY(launch_k(chunk_join_kernel<D, RT, KEYS>, dim3(n_ctas, RT / join_rows(RT)),
-                        dim3(JOIN_NT), 0, st, a, n_ctas, least));
+template <int D, int RT>
+int32_t launch_join(const ChunkArgs& a, int n_ctas, cudaStream_t st) {
+  SUB_CHECK_ARG(n_ctas <= 32 * JOIN_MAX, "chunk_attn: more SMs than the join was built for");
+  SUB_CUDA_TRY(launch_k(chunk_join_kernel<D, RT>, dim3(n_ctas, RT / join_rows(RT)),
+                        dim3(JOIN_WARPS * 32), 0, st, a));
   return SUB_OK;
 }
 
@@ -667,7 +690,7 @@ int32_t launch_decode(const ChunkArgs& a, int n_ctas, cudaStream_t st) {
   });
   SUB_CUDA_TRY(err);
   SUB_CUDA_TRY(launch_k(chunk_attn_kernel<D, Q8, MT>, dim3(n_ctas), dim3(NT), SMEM, st, a));
-  return launch_join<D, MT * 16, KB>(a, n_ctas, WARPS, st);
+  return launch_join<D, MT * 16>(a, n_ctas, st);
 }
 
 // Many rows per sequence: the tensor-core kernel.  (Rows and sequences are known
@@ -679,9 +702,9 @@ int tile_rows(int group, int n_seqs, int n_rows) {
   return many_rows(group, n_seqs, n_rows) ? CHUNK_TC_ROWS : 16;
 }
 
-// Partial results: two per CTA.
+// Partial results, two per CTA, and the list of cuts.
 int64_t part_bytes(int n_ctas, int rows, int d) {
-  return (int64_t)n_ctas * 2 * rows * (d + 2) * 4;
+  return (int64_t)n_ctas * (2 * rows * (d + 2) * 4 + (int64_t)sizeof(ChunkCut));
 }
 
 template <class Cache>
@@ -728,13 +751,13 @@ int32_t chunk_attn(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q, const Cach
   a.part_o = reinterpret_cast<float*>(workspace);
   const int rt = tile_rows(a.group, a.t.n_seqs, a.t.n_rows);
   a.part_ml = reinterpret_cast<float2*>(a.part_o + (int64_t)n_ctas * 2 * rt * kv->head_dim);
+  a.cuts = reinterpret_cast<ChunkCut*>(a.part_ml + (int64_t)n_ctas * 2 * rt);
   const int64_t pool_rows =
       (int64_t)kv->n_layers * kv->n_pages * kv->n_heads_kv * kv->page_size;
   if (rt == CHUNK_TC_ROWS && chunk_tc_fits(pool_rows)) {
     SUB_TRY(launch_chunk_tc(a, Q8, kv->head_dim, pool_rows, n_ctas, st));
-    return kv->head_dim == 128
-               ? launch_join<128, CHUNK_TC_ROWS, CHUNK_TC_KEYS>(a, n_ctas, CHUNK_TC_LEAST, st)
-               : launch_join<64, CHUNK_TC_ROWS, CHUNK_TC_KEYS>(a, n_ctas, CHUNK_TC_LEAST, st);
+    return kv->head_dim == 128 ? launch_join<128, CHUNK_TC_ROWS>(a, n_ctas, st)
+                               : launch_join<64, CHUNK_TC_ROWS>(a, n_ctas, st);
   }
   return kv->head_dim == 128 ? launch_decode<128, Q8, 1>(a, n_ctas, st)
                              : launch_decode<64, Q8, 1>(a, n_ctas, st);

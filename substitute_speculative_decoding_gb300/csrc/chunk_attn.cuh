@@ -18,7 +18,23 @@ struct ChunkArgs {
   // partial results of key ranges cut between CTAs: two per CTA
   float* part_o;         // [2 n_ctas][rows][D], relative to the maxima of
   float2* part_ml;       // [2 n_ctas][rows] (largest score, sum)
+  struct ChunkCut* cuts; // [n_ctas]
 };
+
+// The unit of work (below) that is cut first at the end of a CTA's part, for the
+// kernel that joins its pieces: written by each CTA, pieces 0 where none is.
+struct __align__(16) ChunkCut {
+  int row0, rows, tile, head;   // as in ChunkPlan::Unit
+  int pieces, first;            // the first piece's slot; piece i > 0 of CTA x lies in slot 2 (x + i)
+  int pad[2];
+};
+
+// Quotients of line positions, nearly always of 32 bits (a 64-bit division
+// takes a few hundred cycles, in every CTA before its first load).
+__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
 
 // ---------------------------------------------------------------- work plan --
 // A unit of work is one tile of RT rows -- (row, head in group) pairs of one
@@ -104,8 +120,8 @@ struct ChunkPlan {
     u.row0 = seq_first(t, lo);
     u.rows = seq_rows(t, lo);
     u.pos = t.pos[lo];
-    const int64_t per_head = (pre[lo + 1] - pre[lo]) / heads;
-    u.head = (int)((at - pre[lo]) / per_head);
+    const int64_t per_head = quot(pre[lo + 1] - pre[lo], heads);
+    u.head = (int)quot(at - pre[lo], per_head);
     u.begin = pre[lo] + u.head * per_head;
     u.tile = 0;
     u.n_blocks = blocks(u.pos, u.rows, 0);
@@ -120,8 +136,19 @@ struct ChunkPlan {
 
 // Blocks per CTA of a line of `total`, at least `least`.
 __device__ __forceinline__ int64_t blocks_per_cta(int64_t total, int n_ctas, int least) {
-  const int64_t per = (total + n_ctas - 1) / n_ctas;
+  const int64_t per = quot(total + n_ctas - 1, n_ctas);
   return per < least ? least : per;
+}
+// A CTA's entry in the list of cuts, from its last piece (blocks [.., kb1) of u;
+// the CTA's part of the line begins at lo).
+template <class Unit>
+__device__ __forceinline__ ChunkCut make_cut(const Unit& u, int kb1, int64_t lo, int64_t per) {
+  ChunkCut c{u.row0, u.rows, u.tile, u.head, 0, 0, {0, 0}};
+  if (kb1 < u.n_blocks && u.begin >= lo) {
+    c.pieces = (int)(quot(u.begin + u.n_blocks - 1, per) - blockIdx.x) + 1;
+    c.first = 2 * blockIdx.x + (u.begin == lo ? 0 : 1);
+  }
+  return c;
 }
 
 // The kernel for many rows per sequence (chunk_attn_tc.cu): its tiles, and the

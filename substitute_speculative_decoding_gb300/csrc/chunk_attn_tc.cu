@@ -59,9 +59,9 @@ struct Cfg {
   static constexpr int THREADS = Q8 ? 512 : 384;         // whole groups of four warps
   // registers by group of four warps, out of 65536 / THREADS each at the launch
   // (bf16: the producer and the MMA warp share one)
-  static constexpr int REGS_SOFTMAX = Q8 ? 192 : 208;
-  static constexpr int REGS_PROD = Q8 ? 96 : 80;
-  static constexpr int REGS_MMA = Q8 ? 32 : 80;
+  static constexpr int REGS_SOFTMAX = Q8 ? 192 : 216;
+  static constexpr int REGS_PROD = Q8 ? 64 : 72;
+  static constexpr int REGS_MMA = Q8 ? 64 : 72;
   static_assert((2 * REGS_SOFTMAX + REGS_PROD + (Q8 ? REGS_MMA : 0)) * 128 <=
                     65536 / THREADS / 8 * 8 * THREADS,
                 "the shares fit what the block is launched with");
@@ -315,12 +315,14 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const ChunkArgs a, const int 
     uint32_t n_s = 0, n_o = 0;      // blocks and pieces seen by this group
     uint32_t items = 0;             // ring items before this piece
     int piece = 0;
+    if (tid == 0 && line_lo >= line_hi) a.cuts[blockIdx.x].pieces = 0;
     for (int64_t at = line_lo; at < line_hi; ++piece) {
       const auto u = plan.find(s_pre, at);
       const int kb0 = (int)(at - u.begin), kb1 = (int)min((int64_t)u.n_blocks, line_hi - u.begin);
       const int row0 = u.tile * RT + t * GROUP_ROWS;       // the group's first row
       const int64_t slot = 2 * (int64_t)blockIdx.x + (at == line_lo ? 0 : 1);
       at = u.begin + kb1;
+      if (tid == 0 && at >= line_hi) a.cuts[blockIdx.x] = make_cut(u, kb1, line_lo, per);
       const uint32_t first_item = items;
       items += 2 * (kb1 - kb0);
       if (row0 >= u.rows * G) continue;                    // an empty second group

@@ -72,17 +72,23 @@ __global__ void __launch_bounds__(ROW_WARPS * 32) append_kernel(RowArgs a) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, side = blockIdx.y;
-  const Place p = find_place(a.t, blockIdx.x * ROW_WARPS + (threadIdx.x >> 5), lane);
-  if (p.page < 0) return;
+  const int row = blockIdx.x * ROW_WARPS + (threadIdx.x >> 5);
+  if (row >= a.t.n_rows) return;
   const int sub = lane / LANES, l = lane % LANES;
-  const uint16_t* src = a.src[side] + p.row * a.ld[side];
-  for (int h0 = 0; h0 < a.n_heads_kv; h0 += U * PER) {
-    uint4 w[U];
+  const uint16_t* src = a.src[side] + row * a.ld[side];
+  uint4 w[U];
+  auto load = [&](int h0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int h = h0 + u * PER + sub;
       w[u] = h < a.n_heads_kv ? ldg_nc_v4(src + h * D + l * 8) : make_uint4(0, 0, 0, 0);
     }
+  };
+  load(0);   // on its way while the row's place is looked up
+  const Place p = find_place(a.t, row, lane);
+  if (p.page < 0) return;
+  for (int h0 = 0; h0 < a.n_heads_kv; h0 += U * PER) {
+    if (h0) load(h0);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int h = h0 + u * PER + sub;

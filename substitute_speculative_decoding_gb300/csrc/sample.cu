@@ -57,7 +57,7 @@ __device__ __forceinline__ void share(int groups, int rank, int size, int& lo, i
 // Each CTA sums relative to its own largest logit, so one cluster barrier
 // exchanges both, and a value is scaled by exp((m_cta - m) / T) / sum.
 template <int THREADS, int NV>
-__global__ void __launch_bounds__(THREADS) probs_kernel(const float* logits, int64_t V, float c_hi,
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) probs_kernel(const float* logits, int64_t V, float c_hi,
                                                         float c_lo, float* probs) {
   constexpr int WARPS = THREADS / 32;
   __shared__ float s_m[WARPS], s_s[WARPS];

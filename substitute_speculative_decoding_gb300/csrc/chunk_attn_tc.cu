@@ -46,6 +46,7 @@ constexpr int RT = CHUNK_TC_ROWS, KB = CHUNK_TC_KEYS;
 static_assert(RT == 256 && KB == 128, "two groups of 128 rows, blocks of 128 keys");
 constexpr int GROUP_ROWS = 128;
 constexpr float GROWTH = 8.f;        // log2 of how far weights may exceed 1
+constexpr float Q8_SHIFT = 7.f;      // fp16 weights times scales: 2^7 at the reference, 2^15 at most
 
 __device__ unsigned int g_chunk_timeouts;   // waits that ran out (never expected)
 
@@ -59,13 +60,15 @@ struct Cfg {
   static constexpr int THREADS = Q8 ? 512 : 384;         // whole groups of four warps
   // registers by group of four warps, out of 65536 / THREADS each at the launch
   // (bf16: the producer and the MMA warp share one)
-  static constexpr int REGS_SOFTMAX = Q8 ? 192 : 216;
-  static constexpr int REGS_PROD = Q8 ? 64 : 72;
-  static constexpr int REGS_MMA = Q8 ? 64 : 72;
+  static constexpr int REGS_SOFTMAX = Q8 ? 176 : 192;
+  static constexpr int REGS_PROD = Q8 ? 80 : 120;
+  static constexpr int REGS_MMA = Q8 ? 80 : 120;
   static_assert((2 * REGS_SOFTMAX + REGS_PROD + (Q8 ? REGS_MMA : 0)) * 128 <=
                     65536 / THREADS / 8 * 8 * THREADS,
                 "the shares fit what the block is launched with");
-  static constexpr int SCALES = Q8 ? 4 * 3 * KB * 4 : 0; // four blocks' column factors
+  // four blocks' scales of K, of V, and log2 of the largest of V by converter warp
+  static constexpr int SCALE_SLOT = 2 * KB + 4;
+  static constexpr int SCALES = Q8 ? 4 * SCALE_SLOT * 4 : 0;
   static constexpr int QSCALES = Q8 ? RT * 4 : 0;
   static constexpr int TAIL = 512;                       // barriers, flags, TMEM address
   static constexpr int SMEM =
@@ -135,15 +138,15 @@ __device__ __forceinline__ void tc_ld32(uint32_t t, float* v) {
       : "r"(t)
       : "memory");
 }
-__device__ __forceinline__ void tc_st32(uint32_t t, const float* v) {
-  const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
+__device__ __forceinline__ void tc_ld16(uint32_t t, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(t),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
-      "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(t)
       : "memory");
 }
 __device__ __forceinline__ void tc_st16(uint32_t t, const uint32_t* r) {
@@ -250,7 +253,7 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const ChunkArgs a, const int 
   uint8_t* const base_p = smem_raw + (base - smem_u32(smem_raw));
   const uint32_t q_s = base, ring_s = base + 2 * C::Q_BYTES;
   uint8_t* const after = base_p + 2 * C::Q_BYTES + STAGES * C::STAGE;
-  float* const s_scale = reinterpret_cast<float*>(after);                  // [4][3][KB]
+  float* const s_scale = reinterpret_cast<float*>(after);                  // [4][SCALE_SLOT]
   float* const s_qs = reinterpret_cast<float*>(after + C::SCALES);         // [RT]
   uint8_t* const tail = after + C::SCALES + C::QSCALES;
   const uint32_t bars = smem_u32(tail);
@@ -258,14 +261,14 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const ChunkArgs a, const int 
   auto kv_empty = [&](int s) { return bars + 8u * (STAGES + s); };
   auto q_full = [&](int t) { return bars + 8u * (2 * STAGES + t); };
   auto s_full = [&](int t) { return bars + 8u * (2 * STAGES + 2 + t); };
-  auto p_full = [&](int t) { return bars + 8u * (2 * STAGES + 4 + t); };
-  auto o_full = [&](int t) { return bars + 8u * (2 * STAGES + 6 + t); };
-  int* const flags = reinterpret_cast<int*>(tail + 8 * (2 * STAGES + 8));
+  auto p_full = [&](int t, int h) { return bars + 8u * (2 * STAGES + 4 + 2 * h + t); };
+  auto o_full = [&](int t) { return bars + 8u * (2 * STAGES + 8 + t); };
+  int* const flags = reinterpret_cast<int*>(tail + 8 * (2 * STAGES + 10));
   volatile int* const s_dead = flags;            // a wait ran out
   volatile int* const s_odd = flags + 1;         // [2] piece (by parity) that met infinite values or NaN
   volatile uint32_t* const s_miss = reinterpret_cast<uint32_t*>(flags + 3);   // [8] blocks' missing 16-key parts
   uint32_t* const s_tmem = reinterpret_cast<uint32_t*>(flags + 11);
-  static_assert(8 * (2 * STAGES + 8) + 12 * 4 <= C::TAIL, "tail");
+  static_assert(8 * (2 * STAGES + 10) + 12 * 4 <= C::TAIL, "tail");
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (warp == 0) {
@@ -283,7 +286,8 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const ChunkArgs a, const int 
     for (int t = 0; t < 2; ++t) {
       mbar_init(q_full(t), GROUP_ROWS);
       mbar_init(s_full(t), 1);
-      mbar_init(p_full(t), GROUP_ROWS);
+      mbar_init(p_full(t, 0), GROUP_ROWS);
+      mbar_init(p_full(t, 1), GROUP_ROWS);
       mbar_init(o_full(t), 1);
     }
     *s_dead = 0;
@@ -317,31 +321,40 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const ChunkArgs a, const int 
     int piece = 0;
     if (tid == 0 && line_lo >= line_hi) a.cuts[blockIdx.x].pieces = 0;
     for (int64_t at = line_lo; at < line_hi; ++piece) {
-      const auto u = plan.find(s_pre, at);
-      const int kb0 = (int)(at - u.begin), kb1 = (int)min((int64_t)u.n_blocks, line_hi - u.begin);
-      const int row0 = u.tile * RT + t * GROUP_ROWS;       // the group's first row
-      const int64_t slot = 2 * (int64_t)blockIdx.x + (at == line_lo ? 0 : 1);
-      at = u.begin + kb1;
-      if (tid == 0 && at >= line_hi) a.cuts[blockIdx.x] = make_cut(u, kb1, line_lo, per);
-      const uint32_t first_item = items;
-      items += 2 * (kb1 - kb0);
-      if (row0 >= u.rows * G) continue;                    // an empty second group
-
-      // ---- Q: 16-byte chunks c of a row at c ^ (row % 8) of its 128-byte line ----
+      const int64_t begin = at;
+      int kb0, kb1, lim, lim_first, n_keys;
+      float factor = a.sl2;        // of the row's scores, to base 2
       {
+        const auto u = plan.find(s_pre, at);
+        kb0 = (int)(at - u.begin);
+        kb1 = (int)min((int64_t)u.n_blocks, line_hi - u.begin);
+        at = u.begin + kb1;
+        if (tid == 0 && at >= line_hi) a.cuts[blockIdx.x] = make_cut(u, kb1, line_lo, per);
+        const int row0 = u.tile * RT + t * GROUP_ROWS;     // the group's first row
+        if (row0 >= u.rows * G) {                          // an empty second group
+          items += 2 * (kb1 - kb0);
+          continue;
+        }
+        // ---- Q: 16-byte chunks c of a row at c ^ (row % 8) of its 128-byte line ----
         // (each warp its own threads' rows)
         constexpr int CH = D / 8, RP = 32 / CH;            // chunks of a row, rows per pass
         const int c = lane % CH;
         const uint32_t dst0 = q_s + t * C::Q_BYTES + (c >> 3) * (GROUP_ROWS * 128);
-#pragma unroll 4
+        uint4 w[CH];
+#pragma unroll
         for (int i = 0; i < CH; ++i) {
-          const int rr = (warp & 3) * 32 + i * RP + lane / CH, q = (row0 + rr) / G;
-          uint4 w = make_uint4(0, 0, 0, 0);
+          const int row = row0 + (warp & 3) * 32 + i * RP + lane / CH, q = row / G;
+          w[i] = make_uint4(0, 0, 0, 0);
           if (q < u.rows)
-            w = ldg_nc_v4(a.Q + (int64_t)(u.row0 + q) * a.ldq +
-                          (int64_t)(u.head * G + (row0 + rr) % G) * D + c * 8);
+            w[i] = ldg_nc_v4(a.Q + (int64_t)(u.row0 + q) * a.ldq + (int64_t)(u.head * G + row % G) * D +
+                             c * 8);
+        }
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+          const int rr = (warp & 3) * 32 + i * RP + lane / CH;
           if constexpr (Q8) {
-            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+            // the row's largest value to [1, 2), for fp16
+            const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
             float big = 0.f;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -352,54 +365,47 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const ChunkArgs a, const int 
             const float down = __uint_as_float((uint32_t)(127 - e) << 23);
             if (c == 0)
               s_qs[t * GROUP_ROWS + rr] = a.sl2 * __uint_as_float((uint32_t)(127 + e) << 23);
-            w.x = pack_f16x2(bf16lo(x[0]) * down, bf16hi(x[0]) * down);
-            w.y = pack_f16x2(bf16lo(x[1]) * down, bf16hi(x[1]) * down);
-            w.z = pack_f16x2(bf16lo(x[2]) * down, bf16hi(x[2]) * down);
-            w.w = pack_f16x2(bf16lo(x[3]) * down, bf16hi(x[3]) * down);
+            w[i].x = pack_f16x2(bf16lo(x[0]) * down, bf16hi(x[0]) * down);
+            w[i].y = pack_f16x2(bf16lo(x[1]) * down, bf16hi(x[1]) * down);
+            w[i].z = pack_f16x2(bf16lo(x[2]) * down, bf16hi(x[2]) * down);
+            w[i].w = pack_f16x2(bf16lo(x[3]) * down, bf16hi(x[3]) * down);
           }
           asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
                            dst0 + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)),
-                       "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w)
+                       "r"(w[i].x), "r"(w[i].y), "r"(w[i].z), "r"(w[i].w)
                        : "memory");
         }
         fence_async();
         mbar_arrive(q_full(t));
         __syncwarp();   // s_qs
+        const int q = (row0 + r) / G;
+        n_keys = u.n_keys;
+        lim = q < u.rows ? min(u.pos + q, n_keys - 1) : -1;            // keys 0 .. lim are read
+        lim_first = min(u.pos + u.tile * RT / G, n_keys - 1);          // by every row of the tile
+        // (not 0: it meets the masked scores' -infinity)
+        if constexpr (Q8) factor = fmaxf(s_qs[t * GROUP_ROWS + r], 1e-37f);
       }
-      const int q = (row0 + r) / G;
-      const bool real = q < u.rows;
-      const int lim = real ? min(u.pos + q, u.n_keys - 1) : -1;             // keys 0 .. lim are read
-      const int lim_first = min(u.pos + u.tile * RT / G, u.n_keys - 1);     // by every row of the tile
-      float factor = a.sl2;
-      if constexpr (Q8) factor = s_qs[t * GROUP_ROWS + r];
-
       float ref = 0.f, l = 0.f;    // weights are 2^(score - ref)
       bool any = false;            // a key has been read
-      for (int kb = kb0; kb < kb1; ++kb) {
+      for (int kb = kb0; kb < kb1; ++kb, items += 2) {
         const int key0 = kb * KB;
-        const uint32_t item = first_item + 2 * (kb - kb0);
         if (!gate.wait_warp(s_full(t), n_s & 1)) break;
         ++n_s;
         tc_fence_after();
         float s[KB];
 #pragma unroll
         for (int c = 0; c < KB; c += 32) tc_ld32(tS + c, s + c);
-        const uint32_t miss = s_miss[(item >> 1) & 7];
+        const uint32_t miss = s_miss[(items >> 1) & 7];
         const bool behind = key0 + KB - 1 > lim_first;   // the same for all rows of the tile
         const bool edge = behind || miss;
-        const float* const sc = s_scale + ((item >> 1) & 3) * (3 * KB);
+        const float* const sc = s_scale + ((items >> 1) & 3) * C::SCALE_SLOT;
         wait_ld();
         if constexpr (Q8) {
-          // scores in base 2, plus log2 of the value's scale
-          const float2 f2 = make_float2(factor, factor);
 #pragma unroll
           for (int c = 0; c < KB; c += 4) {
             const float4 k4 = *reinterpret_cast<const float4*>(sc + c);
-            const float4 l4 = *reinterpret_cast<const float4*>(sc + KB + c);
-            const float2 x = fma2(mul2(make_float2(s[c], s[c + 1]), f2), make_float2(k4.x, k4.y),
-                                  make_float2(l4.x, l4.y));
-            const float2 y = fma2(mul2(make_float2(s[c + 2], s[c + 3]), f2),
-                                  make_float2(k4.z, k4.w), make_float2(l4.z, l4.w));
+            const float2 x = mul2(make_float2(s[c], s[c + 1]), make_float2(k4.x, k4.y));
+            const float2 y = mul2(make_float2(s[c + 2], s[c + 3]), make_float2(k4.z, k4.w));
             s[c] = x.x;
             s[c + 1] = x.y;
             s[c + 2] = y.x;
@@ -412,10 +418,22 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const ChunkArgs a, const int 
           for (int c = 0; c < KB; ++c)
             if (c > last || ((miss >> miss_bit<Q8>(c >> 4)) & 1u)) s[c] = -INFINITY;
         }
-        float top = s[0];
+        // eight chains: a single one would wait for itself 128 times
+        float top8[8];
 #pragma unroll
-        for (int c = 1; c < KB; ++c) top = fmaxf(top, s[c]);
-        if constexpr (!Q8) top = top == -INFINITY ? top : top * factor;
+        for (int c = 0; c < 8; ++c) top8[c] = fmaxf(s[c], s[c + 8]);
+#pragma unroll
+        for (int c = 16; c < KB; c += 16)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) top8[i] = fmaxf(fmaxf(top8[i], s[c + i]), s[c + 8 + i]);
+        float top = fmaxf(fmaxf(fmaxf(top8[0], top8[1]), fmaxf(top8[2], top8[3])),
+                          fmaxf(fmaxf(top8[4], top8[5]), fmaxf(top8[6], top8[7])));
+        top = top == -INFINITY ? top : top * factor;
+        if constexpr (Q8) {
+          // what is rounded to fp16 is the weight times the key's scale of V
+          const float4 lv = *reinterpret_cast<const float4*>(sc + 2 * KB);
+          top += fmaxf(fmaxf(lv.x, lv.y), fmaxf(lv.z, lv.w));
+        }
         // ---- the reference, and the output that was formed with another ----
         const bool grow = top > ref + GROWTH || (!any && top != -INFINITY);
         if (__any_sync(~0u, grow)) {
@@ -427,56 +445,23 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const ChunkArgs a, const int 
           l *= f;
           if (kb > kb0 && __any_sync(~0u, f != 1.f)) {
 #pragma unroll
-            for (int c = 0; c < D; c += 32) {
-              float o[32];
+            for (int c = 0; c < D; c += 16) {
+              float o[16];
               __syncwarp();
-              tc_ld32(tO + c, o);
+              tc_ld16(tO + c, o);
               wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] *= f;
-              tc_st32(tO + c, o);
+              for (int i = 0; i < 16; ++i) o[i] *= f;
+              tc_st16(tO + c, reinterpret_cast<const uint32_t*>(o));
             }
           }
         }
-        // ---- weights, in place of the scores' first columns ----
-        // codes: times 2^7, so that they reach fp16's range (2^15) but not past it
-        const float shift = Q8 ? 7.f - ref : -ref;
-        const float2 f2 = make_float2(Q8 ? 1.f : factor, Q8 ? 1.f : factor);
-        const float2 d2 = make_float2(shift, shift);
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-        for (int c0 = 0; c0 < KB; c0 += 32) {
-          uint32_t w[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int c = c0 + 2 * i;
-            float2 e = make_float2(s[c], s[c + 1]);
-            e = Q8 ? add2(e, d2) : fma2(e, f2, d2);
-            e.x = exp2_fast(e.x);
-            e.y = exp2_fast(e.y);
-            if constexpr (Q8) {
-              const float2 inv = *reinterpret_cast<const float2*>(sc + 2 * KB + c);
-              if (edge) {   // a key that is not read may have any scale
-                sum[i & 1].x += s[c] == -INFINITY ? 0.f : e.x * inv.x;
-                sum[i & 1].y += s[c + 1] == -INFINITY ? 0.f : e.y * inv.y;
-              } else {
-                sum[i & 1] = fma2(e, inv, sum[i & 1]);
-              }
-              w[i] = pack_f16x2(e.x, e.y);
-            } else {
-              sum[i & 1] = add2(sum[i & 1], e);
-              w[i] = pack_bf16x2(e.x, e.y);
-            }
-          }
-          tc_st16(tS + c0 / 2, w);
-        }
-        l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
         if (!Q8 && behind && t == 0) {
           // V of the block: row r of it is this thread's
-          const uint32_t st = (item + 1) % STAGES;
-          if (!gate.wait_warp(kv_full(st), ((item + 1) / STAGES) & 1)) break;
+          const uint32_t st = (items + 1) % STAGES;
+          if (!gate.wait_warp(kv_full(st), ((items + 1) / STAGES) & 1)) break;
           const uint32_t v0 = ring_s + st * C::STAGE + r * 128;
-          const bool past = key0 + r >= u.n_keys;
+          const bool past = key0 + r >= n_keys;
           bool odd = false;
 #pragma unroll 4
           for (int i = 0; i < D / 8; ++i) {
@@ -500,19 +485,58 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const ChunkArgs a, const int 
           if (odd) s_odd[piece & 1] = piece + 1;
           fence_async();
         }
-        wait_st();
-        tc_fence_before();
-        mbar_arrive(p_full(t));
+        // ---- weights, in place of the scores' first columns; the products with
+        // the first half of V start while the second half is still here ----
+        const float shift = Q8 ? Q8_SHIFT - ref : -ref;
+        const float2 f2 = make_float2(factor, factor), d2 = make_float2(shift, shift);
+        float2 sum[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[i] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int c0 = 0; c0 < KB; c0 += 32) {
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int c = c0 + 2 * i;
+            float2 e = fma2(make_float2(s[c], s[c + 1]), f2, d2);
+            e.x = exp2_fast(e.x);
+            e.y = exp2_fast(e.y);
+            sum[i & 3] = add2(sum[i & 3], e);
+            if constexpr (Q8) {
+              e = mul2(e, *reinterpret_cast<const float2*>(sc + KB + c));
+              if (edge) {   // a key that is not read may have any scale
+                if (s[c] == -INFINITY) e.x = 0.f;
+                if (s[c + 1] == -INFINITY) e.y = 0.f;
+              }
+              w[i] = pack_f16x2(e.x, e.y);
+            } else {
+              w[i] = pack_bf16x2(e.x, e.y);
+            }
+          }
+          tc_st16(tS + c0 / 2, w);
+          if (c0 == KB / 2 - 32 || c0 == KB - 32) {
+            wait_st();
+            tc_fence_before();
+            mbar_arrive(p_full(t, c0 >= KB / 2));
+          }
+        }
+        sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+        l += sum[0].x + sum[0].y;
       }
       // ---- the piece's result ----
       if (!gate.wait_warp(o_full(t), n_o & 1)) break;
       ++n_o;
       tc_fence_after();
+      asm volatile("" ::: "memory");   // the unit's figures are looked up again, not kept through the loop
+      const auto u = plan.find(s_pre, begin);
+      const int row = u.tile * RT + t * GROUP_ROWS + r, q = row / G;
+      const bool real = q < u.rows;
       const bool whole = kb0 == 0 && kb1 == u.n_blocks;
       const bool odd = !Q8 && s_odd[piece & 1] == piece + 1;
       const float mul = whole ? (any ? 1.f / l : 0.f) : 1.f;
-      uint16_t* const out = a.O + ((int64_t)(u.row0 + q) * a.n_heads_q + u.head * G + (row0 + r) % G) * D;
-      float* const part = a.part_o + (slot * RT + t * GROUP_ROWS + r) * D;
+      uint16_t* const out = a.O + ((int64_t)(u.row0 + q) * a.n_heads_q + u.head * G + row % G) * D;
+      const int64_t part_row =
+          (2 * (int64_t)blockIdx.x + (begin == line_lo ? 0 : 1)) * RT + t * GROUP_ROWS + r;
 #pragma unroll
       for (int c = 0; c < D; c += 32) {
         float o[32];
@@ -545,13 +569,12 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const ChunkArgs a, const int 
         } else if (real) {
 #pragma unroll
           for (int i = 0; i < 32; i += 4)
-            __stcg(reinterpret_cast<float4*>(part + c + i),
+            __stcg(reinterpret_cast<float4*>(a.part_o + part_row * D + c + i),
                    make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]));
         }
       }
       if (!whole && real)
-        __stcg(a.part_ml + slot * RT + t * GROUP_ROWS + r,
-               make_float2(any ? ref : -INFINITY, l));
+        __stcg(a.part_ml + part_row, make_float2(any ? ref : -INFINITY, l));
       __syncwarp();
       tc_fence_before();   // O is read before the next piece's first weights are announced
       if (*s_dead) break;
@@ -562,12 +585,15 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const ChunkArgs a, const int 
       constexpr uint32_t id_s = idesc(KB, !Q8, false), id_o = idesc(D, !Q8, true);
       uint32_t it = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
       bool ok = true;
-      auto scores = [&](int t, uint32_t item) {
-        const uint32_t qb = q_s + t * C::Q_BYTES, kb = ring_s + (item % STAGES) * C::STAGE;
+      // descriptors of the first step; a step further is a constant in the address field
+      const uint64_t q_desc[2] = {desc_k(q_s), desc_k(q_s + C::Q_BYTES)};
+      const uint64_t k_desc = desc_k(ring_s), v_desc = desc_mn(ring_s);
+      auto scores = [&](int t, uint32_t stage) {
+        const uint64_t qd = q_desc[t], kd = k_desc + stage * (C::STAGE >> 4);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k >> 2) * (KB * 128) + (k & 3) * 32;
-          mma_ss(tmem + t * 128, desc_k(qb + off), desc_k(kb + off), id_s, k > 0);
+          const uint32_t off = ((k >> 2) * (KB * 128) + (k & 3) * 32) >> 4;
+          mma_ss(tmem + t * 128, qd + off, kd + off, id_s, k > 0);
         }
         tc_commit(s_full(t));
       };
@@ -581,7 +607,7 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const ChunkArgs a, const int 
         for (int t = 0; t < groups && ok; ++t) {
           ok = gate.wait(q_full(t), n_q[t]++ & 1);
           tc_fence_after();
-          if (ok) scores(t, it);
+          if (ok) scores(t, it % STAGES);
         }
         if (!ok) break;
         tc_commit(kv_empty(it % STAGES));
@@ -589,20 +615,25 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const ChunkArgs a, const int 
           const uint32_t vi = it + 1, ki = it + 2;
           for (int t = 0; t < groups && ok; ++t) {
             if (t == 0) ok = gate.wait(kv_full(vi % STAGES), (vi / STAGES) & 1);
-            ok = ok && gate.wait(p_full(t), n_p[t]++ & 1);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t vb = ring_s + (vi % STAGES) * C::STAGE;
+            const uint64_t vd = v_desc + (vi % STAGES) * (C::STAGE >> 4);
 #pragma unroll
-            for (int k = 0; k < KB / 16; ++k)
-              mma_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8, desc_mn(vb + k * 2048), id_o,
+            for (int k = 0; k < KB / 16; ++k) {
+              if (k % (KB / 32) == 0) {   // half of the weights
+                ok = ok && gate.wait(p_full(t, k >= KB / 32), n_p[t] & 1);
+                if (!ok) break;
+                tc_fence_after();
+              }
+              mma_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8, vd + k * (2048 >> 4), id_o,
                      i > 0 || k > 0);
+            }
+            if (!ok) break;
+            ++n_p[t];
             if (t == groups - 1) tc_commit(kv_empty(vi % STAGES));
             if (i + 1 < n) {
               if (t == 0) ok = gate.wait(kv_full(ki % STAGES), (ki / STAGES) & 1);
               if (!ok) break;
               tc_fence_after();
-              scores(t, ki);
+              scores(t, ki % STAGES);
               if (t == groups - 1) tc_commit(kv_empty(ki % STAGES));
             } else {
               tc_commit(o_full(t));
@@ -704,10 +735,12 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const ChunkArgs a, const int 
             if (x == 0) next = kb + 1 < kb1 ? look_up(kb + 1) : -1;
             if (item >= STAGES) gate.wait(kv_empty(st), ((item / STAGES) - 1) & 1);
             if (x == 0) {
-              float* const sc = s_scale + ((item >> 1) & 3) * (3 * KB) + ptid;
-              sc[0] = ksc;
-              sc[KB] = log2f(vsc);
-              sc[2 * KB] = __fdiv_rn(1.f, vsc);
+              float* const sc = s_scale + ((item >> 1) & 3) * C::SCALE_SLOT;
+              sc[ptid] = ksc;
+              sc[KB + ptid] = vsc;
+              // (at least 2^-80: the sums of weights stay in range)
+              const float big = warp_max(row >= 0 ? fmaxf(log2f(vsc), -80.f) : -80.f);
+              if (lane == 0) sc[2 * KB + warp - 8] = big;
               const unsigned gone = __ballot_sync(~0u, row < 0 && kb * KB + ptid < u.n_keys);
               // 16-key parts: bits 0 and 16 of the warp's 32 keys
               if (lane == 0)

@@ -9,6 +9,7 @@ or ``__graft_entry__.build()``).
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 
 import torch
@@ -359,142 +360,36 @@ def make_kv(n_layers, n_heads_kv, head_dim, capacity, page_size=64, device="cuda
 
 
 # ----------------------------------------------- batches of sequences --
-def _need(ok, msg):
-    if not ok:
-        raise SubError(SUB_EINVAL, msg)
+# These calls are made once per layer or token, so their checks cost little on
+# the way that is taken: messages are formed only when one fails.
+def _refuse(msg):
+    raise SubError(SUB_EINVAL, msg)
 
 
-def _on(t, dtype, name, device=None):
-    """A tensor of this type on the GPU (that of the other tensors)."""
-    _need(isinstance(t, torch.Tensor) and t.dtype == dtype, f"{name}: a {dtype} tensor is needed")
-    _need(t.is_cuda and (device is None or t.device == device),
-          f"{name}: must be on {device or 'the GPU'}")
-    return t
+def _gpu(t, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        _refuse(f"{name}: a tensor on the GPU is needed")
+    return t.device
 
 
 def _dense(t, dtype, shape, name, device):
-    _need(tuple(_on(t, dtype, name, device).shape) == tuple(shape) and t.is_contiguous(),
-          f"{name}: must be contiguous, of shape {tuple(shape)}")
-    return t
+    """Address of a contiguous tensor of this type and shape on the device."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
+        _refuse(f"{name}: must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return t.data_ptr()
 
 
-def _rows(t, shape, name, device):
-    """[rows, heads, head_dim] bf16 whose rows may lie apart -> row stride."""
-    _on(t, torch.bfloat16, name, device)
-    _need(tuple(t.shape) == tuple(shape), f"{name}: must have shape {tuple(shape)}")
-    n, h, d = t.shape
-    _need((d == 1 or t.stride(2) == 1) and (h == 1 or t.stride(1) == d),
-          f"{name}: the heads of a row must be contiguous")
-    return t.stride(0) if n > 1 else h * d
+def _rows(t, rows, heads, d, name, device):
+    """Row stride of a bf16 tensor [rows, heads, d] whose rows may lie apart."""
+    if t.dtype is not torch.bfloat16 or t.shape != (rows, heads, d) or t.device != device:
+        _refuse(f"{name}: must be a bf16 tensor of shape {(rows, heads, d)} on {device}")
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and d > 1) or (s1 != d and heads > 1):
+        _refuse(f"{name}: the heads of a row must be contiguous")
+    return s0 if rows > 1 else heads * d
 
 
-class _at:
-    """The device of the call's tensors as the current one, if it is not."""
-
-    def __init__(self, device):
-        self.device = device
-
-    def __enter__(self):
-        self.back = torch.cuda.current_device()
-        if self.back != self.device.index:
-            torch.cuda.set_device(self.device)
-
-    def __exit__(self, *exc):
-        if self.back != self.device.index:
-            torch.cuda.set_device(self.back)
-
-
-def paged_kv(k, v, page_table) -> KVCache:
-    """A cache of sequences on torch tensors: pools k, v bf16 [n_layers, n_pages,
-    n_heads_kv, page_size, head_dim], page_table int32 [n_seqs, pages per
-    sequence] (entries outside the pool: no page).  Keeps the tensors."""
-    dev = _on(k, torch.bfloat16, "k").device
-    _need(k.dim() == 5, "k: must be [n_layers, n_pages, n_heads_kv, page_size, head_dim]")
-    _dense(k, torch.bfloat16, k.shape, "k", dev)
-    _dense(v, torch.bfloat16, k.shape, "v", dev)
-    _need(page_table.dim() == 2 and page_table.shape[1] >= 1, "page_table: must be [n_seqs, pages]")
-    _dense(page_table, torch.int32, page_table.shape, "page_table", dev)
-    nl, npg, h, ps, d = k.shape
-    kv = KVCache(k.data_ptr(), v.data_ptr(), page_table.data_ptr(), nl, h, d, ps, npg,
-                 page_table.shape[1] * ps)
-    kv.keep, kv.device, kv.n_seqs = (k, v, page_table), dev, page_table.shape[0]
-    return kv
-
-
-def paged_kv8(k, v, k_scale, v_scale, page_table) -> KV8Cache:
-    """An 8-bit cache of sequences: codes uint8 shaped as paged_kv's pools, scales
-    fp32 without the last axis."""
-    dev = _on(k, torch.uint8, "k").device
-    _need(k.dim() == 5, "k: must be [n_layers, n_pages, n_heads_kv, page_size, head_dim]")
-    _dense(k, torch.uint8, k.shape, "k", dev)
-    _dense(v, torch.uint8, k.shape, "v", dev)
-    _dense(k_scale, torch.float32, k.shape[:4], "k_scale", dev)
-    _dense(v_scale, torch.float32, k.shape[:4], "v_scale", dev)
-    _need(page_table.dim() == 2 and page_table.shape[1] >= 1, "page_table: must be [n_seqs, pages]")
-    _dense(page_table, torch.int32, page_table.shape, "page_table", dev)
-    nl, npg, h, ps, d = k.shape
-    kv = KV8Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                  page_table.data_ptr(), nl, h, d, ps, npg, page_table.shape[1] * ps)
-    kv.keep, kv.device = (k, v, k_scale, v_scale, page_table), dev
-    kv.n_seqs = page_table.shape[0]
-    return kv
-
-
-def batch(start, pos, n_rows: int, max_keys: int = 0) -> Batch:
-    """New rows of a batch: sequence b has rows start[b] .. start[b+1] - 1 of the
-    row tensors (n_rows of them), the first at position pos[b]; int32 device
-    tensors [n_seqs + 1] and [n_seqs].  max_keys: about the most keys a sequence has
-    (0: the cache's capacity); only the split of the work depends on it."""
-    _need(start.dim() == 1 and start.shape[0] >= 2, "start: must be [n_seqs + 1]")
-    _dense(start, torch.int32, start.shape, "start", None)
-    _dense(pos, torch.int32, (start.shape[0] - 1,), "pos", start.device)
-    b = Batch(start.data_ptr(), pos.data_ptr(), pos.shape[0], n_rows, max_keys)
-    b.keep, b.device = (start, pos), start.device
-    return b
-
-
-def _same(kv, b):
-    _need(kv.device == b.device, "the batch and the cache must be on one device")
-    _need(kv.n_seqs == b.n_seqs, "page_table and batch must have the same number of sequences")
-
-
-def kv_append(k, v, kv: KVCache, layer: int, batch: Batch, stream=None):
-    """Copy the batch's new rows (bf16 [n_rows, n_heads_kv, head_dim], rows may
-    be strided) into one layer of a paged_kv cache."""
-    _append(_kv_append, k, v, kv, layer, batch, stream)
-
-
-def kv8_append(k, v, kv: KV8Cache, layer: int, batch: Batch, stream=None):
-    """Quantise the batch's new rows into one layer of a paged_kv8 cache."""
-    _append(_kv8_append, k, v, kv, layer, batch, stream)
-
-
-def _append(fn, k, v, kv, layer, batch, stream):
-    _same(kv, batch)
-    shape = (batch.n_rows, kv.n_heads_kv, kv.head_dim)
-    ldk, ldv = _rows(k, shape, "k", kv.device), _rows(v, shape, "v", kv.device)
-    with _at(kv.device):
-        _check(fn(k.data_ptr(), ldk, v.data_ptr(), ldv, C.byref(kv), layer, C.byref(batch),
-                  _stream(stream)))
-
-
-def kv8_read(kv: KV8Cache, layer: int, batch: Batch, out=None, stream=None):
-    """The values at the batch's positions -> (k, v) bf16 [n_rows, n_heads_kv,
-    head_dim].  Rows of no sequence are left as they are in `out`, zero without."""
-    _same(kv, batch)
-    shape = (batch.n_rows, kv.n_heads_kv, kv.head_dim)
-    with _at(kv.device):
-        if out is None:
-            out = tuple(_new(shape, torch.bfloat16, kv.device, stream) for _ in range(2))
-        k, v = out
-        _dense(k, torch.bfloat16, shape, "out[0]", kv.device)
-        _dense(v, torch.bfloat16, shape, "out[1]", kv.device)
-        _check(_kv8_read(C.byref(kv), layer, C.byref(batch), k.data_ptr(), v.data_ptr(),
-                         _stream(stream)))
-    return k, v
-
-
-def _new(shape, dtype, device, stream, zero=True):
+def _new(shape, dtype, device, stream, zero):
     """A tensor allocated (and zeroed) on the call's stream."""
     make = torch.zeros if zero else torch.empty
     if stream is None:
@@ -503,6 +398,107 @@ def _new(shape, dtype, device, stream, zero=True):
         return make(shape, dtype=dtype, device=device)
 
 
+def _run(fn, device, stream, *args):
+    """The library's call on the tensors' device, on the given or current stream."""
+    i = device.index
+    if torch._C._cuda_getDevice() != i:
+        with torch.cuda.device(i):
+            return _run(fn, device, stream, *args)
+    code = fn(*args, torch._C._cuda_getCurrentRawStream(i) if stream is None
+              else stream.cuda_stream)
+    if code != SUB_OK:
+        _check(code)
+
+
+def _paged(struct, dtype, k, v, page_table, scales=()):
+    dev = _gpu(k, "k")
+    if k.dim() != 5:
+        _refuse("k: must be [n_layers, n_pages, n_heads_kv, page_size, head_dim]")
+    if page_table.dim() != 2 or page_table.shape[1] < 1:
+        _refuse("page_table: must be [n_seqs, pages per sequence]")
+    shape = k.shape
+    nl, npg, h, ps, d = shape
+    at = [_dense(k, dtype, shape, "k", dev), _dense(v, dtype, shape, "v", dev)]
+    at += [_dense(x, torch.float32, shape[:4], n, dev) for x, n in scales]
+    at.append(_dense(page_table, torch.int32, page_table.shape, "page_table", dev))
+    kv = struct(*at, nl, h, d, ps, npg, page_table.shape[1] * ps)
+    kv.keep, kv.device, kv.n_seqs = (k, v, page_table, *scales), dev, page_table.shape[0]
+    kv.ref = C.byref(kv)
+    return kv
+
+
+def paged_kv(k, v, page_table) -> KVCache:
+    """A cache of sequences on torch tensors: pools k, v bf16 [n_layers, n_pages,
+    n_heads_kv, page_size, head_dim], page_table int32 [n_seqs, pages per
+    sequence] (entries outside the pool: no page).  Keeps the tensors."""
+    return _paged(KVCache, torch.bfloat16, k, v, page_table)
+
+
+def paged_kv8(k, v, k_scale, v_scale, page_table) -> KV8Cache:
+    """An 8-bit cache of sequences: codes uint8 shaped as paged_kv's pools, scales
+    fp32 without the last axis."""
+    return _paged(KV8Cache, torch.uint8, k, v, page_table,
+                  ((k_scale, "k_scale"), (v_scale, "v_scale")))
+
+
+def batch(start, pos, n_rows: int, max_keys: int = 0) -> Batch:
+    """New rows of a batch: sequence b has rows start[b] .. start[b+1] - 1 of the
+    row tensors (n_rows of them), the first at position pos[b]; int32 device
+    tensors [n_seqs + 1] and [n_seqs].  max_keys: about the most keys a sequence has
+    (0: the cache's capacity); only the split of the work depends on it."""
+    dev = _gpu(start, "start")
+    n = start.shape[0] - 1 if start.dim() == 1 else 0
+    if n < 1:
+        _refuse("start: must be [n_seqs + 1]")
+    b = Batch(_dense(start, torch.int32, (n + 1,), "start", dev),
+              _dense(pos, torch.int32, (n,), "pos", dev), n, n_rows, max_keys)
+    b.keep, b.device = (start, pos), dev
+    b.ref = C.byref(b)
+    return b
+
+
+def _same(kv, b):
+    if kv.device != b.device:
+        _refuse("the batch and the cache must be on one device")
+    if kv.n_seqs != b.n_seqs:
+        _refuse("page_table and batch must have the same number of sequences")
+    return kv.device
+
+
+def kv_append(k, v, kv: KVCache, layer: int, batch: Batch, stream=None):
+    """Copy the batch's new rows (bf16 [n_rows, n_heads_kv, head_dim], rows may
+    be strided) into one layer of a paged_kv cache."""
+    _append_rows(_kv_append, k, v, kv, layer, batch, stream)
+
+
+def kv8_append(k, v, kv: KV8Cache, layer: int, batch: Batch, stream=None):
+    """Quantise the batch's new rows into one layer of a paged_kv8 cache."""
+    _append_rows(_kv8_append, k, v, kv, layer, batch, stream)
+
+
+def _append_rows(fn, k, v, kv, layer, batch, stream):
+    dev = _same(kv, batch)
+    n, h, d = batch.n_rows, kv.n_heads_kv, kv.head_dim
+    ldk, ldv = _rows(k, n, h, d, "k", dev), _rows(v, n, h, d, "v", dev)
+    _run(fn, dev, stream, k.data_ptr(), ldk, v.data_ptr(), ldv, kv.ref, layer, batch.ref)
+
+
+def kv8_read(kv: KV8Cache, layer: int, batch: Batch, out=None, stream=None):
+    """The values at the batch's positions -> (k, v) bf16 [n_rows, n_heads_kv,
+    head_dim].  Rows of no sequence are left as they are in `out`, zero without."""
+    dev = _same(kv, batch)
+    shape = (batch.n_rows, kv.n_heads_kv, kv.head_dim)
+    if out is None:
+        out = (_new(shape, torch.bfloat16, dev, stream, True),
+               _new(shape, torch.bfloat16, dev, stream, True))
+    k, v = out
+    _run(_kv8_read, dev, stream, kv.ref, layer, batch.ref,
+         _dense(k, torch.bfloat16, shape, "out[0]", dev),
+         _dense(v, torch.bfloat16, shape, "out[1]", dev))
+    return k, v
+
+
+@functools.lru_cache(maxsize=4096)
 def chunk_attn_workspace(n_heads_q: int, n_heads_kv: int, head_dim: int, n_seqs: int,
                          n_rows: int) -> int:
     """Bytes of workspace that a chunk_attn call of these sizes may need."""
@@ -518,39 +514,37 @@ def chunk_attn(q, kv, layer: int, batch: Batch, scale=None, out=None, workspace=
     their own keys already -> bf16 [n_rows, n_heads_q, head_dim].  Rows of no
     sequence are left as they are in `out`, zero without.  workspace: a uint8
     tensor of chunk_attn_workspace bytes; allocated by torch if not given."""
-    _same(kv, batch)
-    dev = kv.device
-    _need(q.dim() == 3, "q: must be [n_rows, n_heads_q, head_dim]")
-    hq = q.shape[1]
-    shape = (batch.n_rows, hq, kv.head_dim)
-    ldq = _rows(q, shape, "q", dev)
-    scale = scale if scale is not None else kv.head_dim ** -0.5
-    with _at(dev):
-        if out is None:
-            out = _new(shape, torch.bfloat16, dev, stream)
-        _dense(out, torch.bfloat16, shape, "out", dev)
-        if workspace is None:
-            n = chunk_attn_workspace(hq, kv.n_heads_kv, kv.head_dim, batch.n_seqs, batch.n_rows)
-            workspace = _new(n, torch.uint8, dev, stream, zero=False)
-        _on(workspace, torch.uint8, "workspace", dev)
-        fn = _chunk_attn8 if isinstance(kv, KV8Cache) else _chunk_attn
-        _check(fn(q.data_ptr(), ldq, hq, C.byref(kv), layer, C.byref(batch), scale,
-                  out.data_ptr(), workspace.data_ptr() or None, workspace.numel(),
-                  _stream(stream)))
+    dev = _same(kv, batch)
+    if q.dim() != 3:
+        _refuse("q: must be [n_rows, n_heads_q, head_dim]")
+    n, hq, d = batch.n_rows, q.shape[1], kv.head_dim
+    ldq = _rows(q, n, hq, d, "q", dev)
+    if out is None:
+        out = _new((n, hq, d), torch.bfloat16, dev, stream, True)
+    at = _dense(out, torch.bfloat16, (n, hq, d), "out", dev)
+    if workspace is None:
+        size = chunk_attn_workspace(hq, kv.n_heads_kv, d, batch.n_seqs, n)
+        workspace = _new(size, torch.uint8, dev, stream, False)
+    else:
+        size = workspace.numel()
+        _dense(workspace, torch.uint8, workspace.shape, "workspace", dev)
+    _run(_chunk_attn8 if type(kv) is KV8Cache else _chunk_attn, dev, stream, q.data_ptr(), ldq, hq,
+         kv.ref, layer, batch.ref, d ** -0.5 if scale is None else scale, at,
+         workspace.data_ptr() or None, size)
     return out
 
 
 def probs(logits, temperature: float = 1.0, out=None, stream=None):
     """softmax(logits / temperature) of fp32 [rows, V]; `out` may be the logits."""
-    dev = _on(logits, torch.float32, "logits").device
-    _need(logits.dim() == 2, "logits: must be [rows, V]")
-    _dense(logits, torch.float32, logits.shape, "logits", dev)
-    with _at(dev):
-        if out is None:
-            out = _new(logits.shape, torch.float32, dev, stream, zero=False)
-        _dense(out, torch.float32, logits.shape, "out", dev)
-        _check(_probs(logits.data_ptr(), logits.shape[0], logits.shape[1], temperature,
-                      out.data_ptr(), _stream(stream)))
+    dev = _gpu(logits, "logits")
+    if logits.dim() != 2:
+        _refuse("logits: must be [rows, V]")
+    shape = logits.shape
+    z = _dense(logits, torch.float32, shape, "logits", dev)
+    if out is None:
+        out = _new(shape, torch.float32, dev, stream, False)
+    _run(_probs, dev, stream, z, shape[0], shape[1], temperature,
+         _dense(out, torch.float32, shape, "out", dev))
     return out
 
 
@@ -561,28 +555,24 @@ def verify_sample(p, q, draft, u, out=None, stream=None):
     entry outside [0, V) ends a sequence's draft), u fp32 [n_seqs, n_draft + 1] in
     [0, 1) -> (tokens int32 [n_seqs, n_draft + 1]: the accepted ones, the sampled one,
     then -1; n_accepted int32 [n_seqs]).  draft None: plain sampling from p."""
-    dev = _on(p, torch.float32, "p").device
-    _need(p.dim() == 3 and p.shape[1] >= 1, "p: must be [n_seqs, n_draft + 1, V]")
-    b, n, v = p.shape[0], p.shape[1] - 1, p.shape[2]
-    _dense(p, torch.float32, p.shape, "p", dev)
-    _need(draft is not None or n == 0, "draft: must be [n_seqs, n_draft]")
-    if draft is not None:
-        _dense(draft, torch.int32, (b, n), "draft", dev)
-    if q is not None:
-        _dense(q, torch.float32, (b, n, v), "q", dev)
-    _dense(u, torch.float32, (b, n + 1), "u", dev)
-    with _at(dev):
-        if out is None:
-            out = (_new((b, n + 1), torch.int32, dev, stream, zero=False),
-                   _new((b,), torch.int32, dev, stream, zero=False))
-        tokens, n_accepted = out
-        _dense(tokens, torch.int32, (b, n + 1), "out[0]", dev)
-        _dense(n_accepted, torch.int32, (b,), "out[1]", dev)
-        has_q = q is not None and n > 0
-        _check(_verify_sample(p.data_ptr(), q.data_ptr() if has_q else None,
-                              draft.data_ptr() if draft is not None and n > 0 else None,
-                              u.data_ptr(), b, n, v, tokens.data_ptr(), n_accepted.data_ptr(),
-                              _stream(stream)))
+    dev = _gpu(p, "p")
+    if p.dim() != 3 or p.shape[1] < 1:
+        _refuse("p: must be [n_seqs, n_draft + 1, V]")
+    b, n, v = p.shape
+    n -= 1
+    if draft is None and n > 0:
+        _refuse("draft: must be [n_seqs, n_draft]")
+    pa = _dense(p, torch.float32, p.shape, "p", dev)
+    qa = None if q is None else _dense(q, torch.float32, (b, n, v), "q", dev)
+    da = None if draft is None else _dense(draft, torch.int32, (b, n), "draft", dev)
+    ua = _dense(u, torch.float32, (b, n + 1), "u", dev)
+    if out is None:
+        out = (_new((b, n + 1), torch.int32, dev, stream, False),
+               _new((b,), torch.int32, dev, stream, False))
+    tokens, n_accepted = out
+    _run(_verify_sample, dev, stream, pa, qa if n else None, da if n else None, ua, b, n, v,
+         _dense(tokens, torch.int32, (b, n + 1), "out[0]", dev),
+         _dense(n_accepted, torch.int32, (b,), "out[1]", dev))
     return tokens, n_accepted
 
 

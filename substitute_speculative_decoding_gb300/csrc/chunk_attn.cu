@@ -7,27 +7,29 @@
 // same tile, so a key is read once for all of them.
 //
 // Bound by HBM: a row tile of 16 does 64 flops per byte of a bf16 cache,
-// mma.sync covers that many times over, and what counts is bytes in flight.
-// So every warp streams blocks of 32 keys on its own, through a private ring
-// of shared memory that its lanes fill with cp.async and read themselves: a
-// lane copies exactly the 16-byte pieces that it will use as matrix operands,
-// so there is no barrier, no swizzle and no ldmatrix in the loop.  That works
-// because a dot product may take its terms in any order, if Q is laid out the
-// same way: lane (g, tig) holds, of key g of an 8-key group, the 16-byte chunks
-// tig, tig + 4, .. of the row, and of V, for its four keys of a 16-key step, the
-// columns that make its B fragments for the n tiles of eight chunk-wise
-// permuted columns.
+// mma.sync covers that many times over, and what counts is bytes in flight and
+// instructions per key.  So each of eight warps streams blocks of 16 or 32 keys (8
+// KB) on its own, through a private ring of shared memory that its lanes fill with
+// cp.async and read themselves: a lane copies exactly the 16-byte pieces that it will
+// use as matrix operands, so there is no barrier, no swizzle and no ldmatrix in
+// the loop.  That works because a dot product may take its terms in any order, if
+// Q is laid out the same way: lane (g, tig) holds, of key g of an 8-key group, the
+// 16-byte chunks tig, tig + 4, .. of the row, and of V, for its four keys of a
+// 16-key step, the columns that make its B fragments for the n tiles of eight
+// chunk-wise permuted columns.
 //
-// 8-bit codes c stand for (c - 128) * scale.  (c - 128) is exact in fp16 (the
-// bytes 0x64, c are 1024 + c), so both products take the codes themselves: the
-// scale of k_j multiplies the score, and the scale of v_j goes into e_ij before it is
-// rounded to fp16.  The running maximum is taken of s_ij + log2(vscale_j) - 15, so
+// 8-bit codes c stand for (c - 128) * scale, and both products take c - 128 in
+// fp16, exactly: the bytes 0x64, c are 1024 + c, a byte permute and a subtraction
+// for two of them.  The scale of k_j multiplies the score, and the scale of v_j
+// goes into e_ij before it is rounded to fp16.
+// The running maximum includes log2 of the largest vscale in reach, minus 15, so
 // that what is rounded reaches 2^15 at most, and fp16's smallest step, 2^-24, is
 // 2^-39 of the largest; the sum takes the unscaled e_ij, in fp32, relative to the
-// same maximum (log2(vscale_j) counts as at least -80, which keeps it in range).  Q enters in fp16 scaled by a power of two
-// of its row's largest value: bf16 has three bits fewer, so only values below 2^-15 of
-// the largest lose any.  With a bf16 cache P = hi + lo, two bf16 products, keeps
-// it to 2^-17; in fp16 one product keeps 2^-12.
+// same maximum (log2(vscale) counts as at least -80, which keeps it in range).  Q
+// enters in fp16 scaled by a power of two of its row's largest value: bf16 has three
+// bits fewer, so only values below 2^-15 of the largest lose any.  With a bf16
+// cache P = hi + lo, two bf16 products, keeps it to 2^-17; in fp16 one product keeps
+// 2^-12.
 //
 // A key that a row must not read can still hold anything.  Its score is replaced,
 // and where its value is infinite or NaN (bf16 only, and only in blocks that
@@ -40,22 +42,30 @@
 namespace sub {
 namespace {
 
-constexpr int KB = 32;          // keys per block of a warp
-constexpr int WARPS = 4;
+constexpr int WARPS = 8;
 constexpr int NT = WARPS * 32;
 constexpr int STAGES = 3;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
 }
+// 16, 8 or 4 bytes; `_if`: zeros if not, with `any` an address that may be read.
 template <int N>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool pred) {
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
   if constexpr (N == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src),
-                 "r"(pred ? 16 : 0) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;\n" ::"r"(dst), "l"(src), "n"(N),
-                 "r"(pred ? N : 0) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(dst), "l"(src), "n"(N)
+                 : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_if(uint32_t dst, const void* src, const void* any, bool yes) {
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(yes ? src : any),
+                 "r"(yes ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;\n" ::"r"(dst),
+                 "l"(yes ? src : any), "n"(N), "r"(yes ? N : 0) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
 template <int N>
@@ -76,7 +86,7 @@ __device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
   return r;
 }
-// Codes in two bytes of w (picked by sel, 0x64 above each) to fp16 code - 128.
+// Codes in two bytes of w as fp16 code - 128.
 __device__ __forceinline__ uint32_t codes2(uint32_t w, uint32_t sel) {
   uint32_t r;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(__byte_perm(w, 0x64646464u, sel)), "r"(0x64806480u));
@@ -95,13 +105,15 @@ __device__ __forceinline__ float exp2_fast(float x) {   // 2 ulp; flushes below 
 
 template <int D, bool Q8>
 struct Ring {
-  static constexpr int ESZ = Q8 ? 1 : 2;
-  static constexpr int KI = D * ESZ / 64;            // 16-byte chunks of a key per lane
-  static constexpr int VB = Q8 ? D / 8 : 16;         // bytes of a V piece
-  static constexpr int VH = Q8 ? 1 : D / 64;         // pieces per key and lane
-  static constexpr int K_BYTES = KB * D * ESZ;
+  static constexpr int KB = !Q8 && D == 128 ? 16 : 32;   // keys per block of a warp
+  static constexpr int SUBS = KB / 16;                   // 16-key steps; a step lies in one page
+  static constexpr int ROW = D * (Q8 ? 1 : 2);           // bytes of a row
+  static constexpr int KI = ROW / 64;                    // 16-byte chunks of a key per lane
+  static constexpr int VB = Q8 ? D / 8 : 16;             // bytes of a V piece
+  static constexpr int VH = Q8 ? 1 : D / 64;             // pieces per key and lane
+  static constexpr int K_BYTES = KB * ROW;
   static constexpr int STAGE = 2 * K_BYTES + (Q8 ? 2 * KB * 4 : 0);
-  static constexpr int BYTES = STAGES * STAGE;       // of one warp
+  static constexpr int BYTES = STAGES * STAGE;           // of one warp
 };
 
 template <int D, bool Q8, int MT>
@@ -115,14 +127,14 @@ constexpr int decode_smem() {
 template <int D, bool Q8, int MT>
 __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
   using R = Ring<D, Q8>;
-  constexpr int RT = MT * 16, KS = D / 16, ON = D / 8;
+  constexpr int RT = MT * 16, KS = D / 16, ON = D / 8, KB = R::KB, SUBS = R::SUBS, TILES = KB / 8;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t s_pre[SUB_MAX_SEQS + 1], s_warp[WARPS];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, tig = lane & 3;
-  const int G = a.group;
+  const int G = a.group, ps = a.t.page_size;
   const ChunkPlan<RT, KB> plan(a.t, G, a.n_heads_kv);
   plan.template scan<NT>(s_pre, s_warp);
   const int64_t total = s_pre[a.t.n_seqs];
@@ -130,8 +142,11 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
   const int64_t line_lo = blockIdx.x * per, line_hi = min(total, line_lo + per);
   uint8_t* const ring = smem + warp * R::BYTES;
   const uint32_t ring_s = smem_u32(ring);
-  const uint8_t* const kp = reinterpret_cast<const uint8_t*>(a.k);
-  const uint8_t* const vp = reinterpret_cast<const uint8_t*>(a.v);
+  // a lane's place in the first key of a step, of K and of V
+  const uint8_t* const kp = reinterpret_cast<const uint8_t*>(a.k) + g * R::ROW + tig * 16;
+  const uint8_t* const vp = reinterpret_cast<const uint8_t*>(a.v) + 2 * tig * R::ROW + g * R::VB;
+  const int64_t page_rows = (int64_t)a.n_heads_kv * ps;
+  const int step_pages = WARPS * KB / ps, step_at = WARPS * KB % ps;   // from block to block of a warp
 
   for (int64_t at = line_lo; at < line_hi;) {
     const auto u = plan.find(s_pre, at);
@@ -139,65 +154,87 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
     const int kb1 = (int)min((int64_t)u.n_blocks, line_hi - u.begin);
     const int n_mine = (kb1 - kb0 - warp + WARPS - 1) / WARPS;   // blocks kb0 + warp + i * WARPS
     const int32_t* const pages = a.t.pages + (int64_t)u.b * a.t.width;
+    const int64_t row_base = ((int64_t)a.layer * a.t.n_pages * a.n_heads_kv + u.head) * ps;
 
-    // page (or -1) of each 16-key half of a block
-    auto load_pages = [&](int i, int (&pg)[2]) {
+    // the next block to copy: first key, page-table entry and place in the page, and
+    // the pages of its steps (-1: none), read one block ahead of their use
+    struct {
+      int key, entry, at, page[SUBS];
+    } nx;
+    nx.key = (kb0 + warp) * KB;
+    nx.entry = (uint32_t)nx.key / (uint32_t)ps;
+    nx.at = nx.key - nx.entry * ps;
+    auto look_up = [&] {
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const int key = (kb0 + warp + i * WARPS) * KB + s * 16;
-        pg[s] = i < n_mine && key < u.n_keys
-                    ? pages[(uint32_t)key / (uint32_t)a.t.page_size] : -1;
-      }
+      for (int s = 0; s < SUBS; ++s)
+        nx.page[s] = nx.key + 16 * s < u.n_keys ? pages[nx.entry + (nx.at + 16 * s >= ps ? 1 : 0)] : -1;
     };
-    uint32_t missing = 0;   // bits 2 * stage + half: no page there
-    auto issue = [&](int i, int stage, const int (&pg)[2]) {
+    uint32_t missing = 0;   // bits SUBS * stage + step: no page there
+    auto issue = [&](int stage) {
       const uint32_t dst = ring_s + stage * R::STAGE;
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const int key0 = (kb0 + warp + i * WARPS) * KB + s * 16;
-        const bool have = (unsigned)pg[s] < (unsigned)a.t.n_pages;
-        missing = (missing & ~(1u << (2 * stage + s))) | ((have ? 0u : 1u) << (2 * stage + s));
-        const int64_t row0 =
-            pool_row(a.t, a.layer, a.n_heads_kv, have ? pg[s] : 0, u.head,
-                     (int)((uint32_t)key0 % (uint32_t)a.t.page_size));
-        const uint8_t* const k0 = kp + row0 * (D * R::ESZ);
-        const uint8_t* const v0 = vp + row0 * (D * R::ESZ);
+      for (int s = 0; s < SUBS; ++s) {
+        const int place = nx.at + 16 * s - (nx.at + 16 * s >= ps ? ps : 0);
+        const bool have = (unsigned)nx.page[s] < (unsigned)a.t.n_pages;
+        const int left = have ? u.n_keys - (nx.key + 16 * s) : 0;   // keys of the step
+        const int bit = SUBS * stage + s;
+        missing = (missing & ~(1u << bit)) | ((have ? 0u : 1u) << bit);
+        const int64_t row0 = row_base + (int64_t)(have ? nx.page[s] : 0) * page_rows + place;
+        const uint8_t* const k0 = kp + row0 * R::ROW;
+        const uint8_t* const v0 = vp + row0 * R::ROW;
+        const uint32_t kd = dst + s * (2 * R::KI * 512) + lane * 16;
+        const uint32_t vd = dst + R::K_BYTES + s * (4 * R::VH * 32 * R::VB) + lane * R::VB;
+        if (left >= 16) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int key = h * 8 + g;
-          const bool ok = have && key0 + key < u.n_keys;
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int c = 0; c < R::KI; ++c)
-            cp_async<16>(dst + (((s * 2 + h) * R::KI + c) * 32 + lane) * 16,
-                         ok ? k0 + key * (D * R::ESZ) + (tig + 4 * c) * 16 : kp, ok);
+            for (int c = 0; c < R::KI; ++c)
+              cp_async<16>(kd + (h * R::KI + c) * 512, k0 + h * 8 * R::ROW + c * 64);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+            for (int c = 0; c < R::VH; ++c)
+              cp_async<R::VB>(vd + (kk * R::VH + c) * (32 * R::VB),
+                              v0 + ((kk >> 1) * 8 + (kk & 1)) * R::ROW + c * 8 * R::VB);
+        } else {   // zeros past the last key
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int c = 0; c < R::KI; ++c)
+              cp_async_if<16>(kd + (h * R::KI + c) * 512, k0 + h * 8 * R::ROW + c * 64, a.k,
+                              h * 8 + g < left);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+            for (int c = 0; c < R::VH; ++c)
+              cp_async_if<R::VB>(vd + (kk * R::VH + c) * (32 * R::VB),
+                                 v0 + ((kk >> 1) * 8 + (kk & 1)) * R::ROW + c * 8 * R::VB, a.k,
+                                 (kk >> 1) * 8 + 2 * tig + (kk & 1) < left);
         }
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          const int key = (kk >> 1) * 8 + 2 * tig + (kk & 1);
-          const bool ok = have && key0 + key < u.n_keys;
-#pragma unroll
-          for (int c = 0; c < R::VH; ++c)
-            cp_async<R::VB>(dst + R::K_BYTES + (((s * 4 + kk) * R::VH + c) * 32 + lane) * R::VB,
-                            ok ? v0 + key * (D * R::ESZ) + (c * 8 + g) * R::VB : vp, ok);
-        }
-        if constexpr (Q8) {
-          // 16 scales of K, 16 of V
+        if constexpr (Q8) {   // 16 scales of K, 16 of V
           const int key = lane & 15;
-          const bool ok = have && key0 + key < u.n_keys;
-          const float* src = (lane < 16 ? a.ks : a.vs) + row0 + key;
-          cp_async<4>(dst + 2 * R::K_BYTES + ((lane >> 4) * KB + s * 16 + key) * 4,
-                      ok ? src : a.ks, ok);
+          cp_async_if<4>(dst + 2 * R::K_BYTES + ((lane >> 4) * KB + s * 16 + key) * 4,
+                         (lane < 16 ? a.ks : a.vs) + row0 + key, a.ks, key < left);
         }
       }
     };
-    int pg[2];
+    auto advance = [&] {
+      nx.key += WARPS * KB;
+      nx.entry += step_pages;
+      nx.at += step_at;
+      if (nx.at >= ps) {
+        nx.at -= ps;
+        ++nx.entry;
+      }
+      look_up();
+    };
+    look_up();
 #pragma unroll
     for (int i = 0; i < STAGES; ++i) {
-      load_pages(i, pg);
-      if (i < n_mine) issue(i, i, pg);
+      if (i < n_mine) issue(i);
       cp_commit();
+      advance();
     }
-    load_pages(STAGES, pg);   // one block ahead of their use
 
     // ---- Q fragments, and the rows' last visible key ----
     uint32_t qf[MT][KS][4];
@@ -205,7 +242,7 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
     int lim[MT][2];     // keys 0 .. lim are read
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      uint4 w[2][Q8 ? KS / 2 : KS / 2];
+      uint4 w[2][KS / 2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int r = u.tile * RT + m * 16 + h * 8 + g;
@@ -250,7 +287,8 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
           big = fmaxf(big, __shfl_xor_sync(~0u, big, 2));
           const int e = min(126, max(-126, (int)(__float_as_uint(big) >> 23) - 127));
           const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-          qs[m][h] = a.sl2 * __uint_as_float((uint32_t)(127 + e) << 23);
+          // (not 0: it meets the masked scores' -infinity)
+          qs[m][h] = fmaxf(a.sl2 * __uint_as_float((uint32_t)(127 + e) << 23), 1e-37f);
 #pragma unroll
           for (int c = 0; c < KS / 2; ++c) {
             const uint32_t x[4] = {w[h][c].x, w[h][c].y, w[h][c].z, w[h][c].w};
@@ -279,13 +317,13 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
       __syncwarp();
       const int key0 = (kb0 + warp + i * WARPS) * KB;
       const uint8_t* const st = ring + stage * R::STAGE;
-      const uint32_t miss = (missing >> (2 * stage)) & 3u;
+      const uint32_t miss = (missing >> (SUBS * stage)) & ((1u << SUBS) - 1u);
       const bool edge = key0 + KB - 1 > lim_min || miss;
 
       // ---- S = Q K^T: n tile t holds keys key0 + 8 t .. + 7 ----
-      float s[MT][4][4];
+      float s[MT][TILES][4];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
+      for (int t = 0; t < TILES; ++t) {
 #pragma unroll
         for (int m = 0; m < MT; ++m) s[m][t][0] = s[m][t][1] = s[m][t][2] = s[m][t][3] = 0.f;
 #pragma unroll
@@ -310,33 +348,28 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
       }
 
       // ---- weights of the lane's keys 8 t + 2 tig + {0, 1} ----
-      float vsc[4][2], lv[4][2];
+      float vsc[TILES][2], lv = 0.f;
       if constexpr (Q8) {
         const float* const sc = reinterpret_cast<const float*>(st + 2 * R::K_BYTES);
+        float vmax = 0.f;
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
+        for (int t = 0; t < TILES; ++t) {
           const float2 kq = *reinterpret_cast<const float2*>(sc + t * 8 + 2 * tig);
           const float2 vq = *reinterpret_cast<const float2*>(sc + KB + t * 8 + 2 * tig);
           vsc[t][0] = vq.x;
           vsc[t][1] = vq.y;
-          lv[t][0] = fmaxf(log2_fast(vq.x), -80.f) - 15.f;
-          lv[t][1] = fmaxf(log2_fast(vq.y), -80.f) - 15.f;
+          vmax = fmaxf(vmax, fmaxf(vq.x, vq.y));
 #pragma unroll
           for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[m][t][e] *= (e & 1 ? kq.y : kq.x) * qs[m][e >> 1];
+            for (int e = 0; e < 4; ++e)
+              s[m][t][e] *= e & 1 ? kq.y : kq.x;
         }
-      } else {
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[m][t][e] *= a.sl2;
+        lv = fmaxf(log2_fast(vmax), -80.f) - 15.f;
       }
       if (edge) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < TILES; ++t)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int key = key0 + t * 8 + 2 * tig + (e & 1);
@@ -346,15 +379,16 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
               if (gone || key > lim[m][e >> 1]) s[m][t][e] = -INFINITY;
           }
       }
-      uint32_t pf[MT][2][4], pl[MT][2][4];   // P of the two 16-key steps (bf16: high and low part)
+      uint32_t pf[MT][SUBS][4], pl[MT][SUBS][4];   // P of the 16-key steps (bf16: high and low part)
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < TILES; ++t)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            top[e >> 1] = fmaxf(top[e >> 1], Q8 ? s[m][t][e] + lv[t][e & 1] : s[m][t][e]);
+          for (int e = 0; e < 4; ++e) top[e >> 1] = fmaxf(top[e >> 1], s[m][t][e]);
+        top[0] = fmaf(top[0], qs[m][0], lv);
+        top[1] = fmaf(top[1], qs[m][1], lv);
         if (__any_sync(~0u, top[0] > mx[m][0] || top[1] > mx[m][1])) {
           float corr[2];
 #pragma unroll
@@ -378,11 +412,11 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
         const float ref[2] = {mx[m][0] == -INFINITY ? 0.f : mx[m][0],
                               mx[m][1] == -INFINITY ? 0.f : mx[m][1]};
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
+        for (int t = 0; t < TILES; ++t) {
           float p[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            p[e] = exp2_fast(s[m][t][e] - ref[e >> 1]);
+            p[e] = exp2_fast(fmaf(s[m][t][e], qs[m][e >> 1], -ref[e >> 1]));
             l[m][e >> 1] += p[e];
             if constexpr (Q8) {
               // a masked key's scale may be anything
@@ -406,7 +440,7 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
       // ---- O += P V: n tile n, column g is column d(g, n) of the head ----
       const uint8_t* const sv = st + R::K_BYTES;
 #pragma unroll
-      for (int step = 0; step < 2; ++step) {
+      for (int step = 0; step < SUBS; ++step) {
         if constexpr (!Q8) {
 #pragma unroll
           for (int c = 0; c < R::VH; ++c) {   // d(g, 8 c + j) = 64 c + 8 g + j
@@ -454,8 +488,10 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
                   float pr[2];
 #pragma unroll
                   for (int h = 0; h < 2; ++h) {
-                    const uint32_t hi = __shfl_sync(~0u, pf[m][step][(key >> 3) * 2 + h], g * 4 + kt);
-                    const uint32_t lo = __shfl_sync(~0u, pl[m][step][(key >> 3) * 2 + h], g * 4 + kt);
+                    const uint32_t hi =
+                        __shfl_sync(~0u, key & 8 ? pf[m][step][2 + h] : pf[m][step][h], g * 4 + kt);
+                    const uint32_t lo =
+                        __shfl_sync(~0u, key & 8 ? pl[m][step][2 + h] : pl[m][step][h], g * 4 + kt);
                     pr[h] = key & 1 ? bf16hi(hi) + bf16hi(lo) : bf16lo(hi) + bf16lo(lo);
                   }
 #pragma unroll
@@ -511,9 +547,9 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
         }
       }
       __syncwarp();   // the stage's scales were read by other lanes
-      if (i + STAGES < n_mine) issue(i + STAGES, stage, pg);
+      if (i + STAGES < n_mine) issue(stage);
       cp_commit();
-      load_pages(i + STAGES + 1, pg);
+      advance();
       stage = stage + 1 == STAGES ? 0 : stage + 1;
     }
     cp_wait<0>();
@@ -693,18 +729,17 @@ int32_t launch_decode(const ChunkArgs& a, int n_ctas, cudaStream_t st) {
   return launch_join<D, MT * 16>(a, n_ctas, st);
 }
 
-// Many rows per sequence: the tensor-core kernel.  (Rows and sequences are known
-// here, lengths only on the device.)
-bool many_rows(int group, int n_seqs, int n_rows) {
-  return (int64_t)n_rows * group > 32 * (int64_t)n_seqs;
-}
-int tile_rows(int group, int n_seqs, int n_rows) {
-  return many_rows(group, n_seqs, n_rows) ? CHUNK_TC_ROWS : 16;
-}
-
 // Partial results, two per CTA, and the list of cuts.
 int64_t part_bytes(int n_ctas, int rows, int d) {
   return (int64_t)n_ctas * (2 * rows * (d + 2) * 4 + (int64_t)sizeof(ChunkCut));
+}
+
+// Rows of a tile, by the rows that a sequence has on average (rows and
+// sequences are known here, lengths only on the device): the smallest that
+// holds them, since a tile streams all its keys.
+int tile_rows(int group, int n_seqs, int n_rows) {
+  const int64_t rows = (int64_t)n_rows * group;
+  return rows <= 16 * (int64_t)n_seqs ? 16 : rows <= 32 * (int64_t)n_seqs ? 32 : CHUNK_TC_ROWS;
 }
 
 template <class Cache>
@@ -759,8 +794,11 @@ int32_t chunk_attn(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q, const Cach
     return kv->head_dim == 128 ? launch_join<128, CHUNK_TC_ROWS>(a, n_ctas, st)
                                : launch_join<64, CHUNK_TC_ROWS>(a, n_ctas, st);
   }
-  return kv->head_dim == 128 ? launch_decode<128, Q8, 1>(a, n_ctas, st)
-                             : launch_decode<64, Q8, 1>(a, n_ctas, st);
+  if (rt == 16)
+    return kv->head_dim == 128 ? launch_decode<128, Q8, 1>(a, n_ctas, st)
+                               : launch_decode<64, Q8, 1>(a, n_ctas, st);
+  return kv->head_dim == 128 ? launch_decode<128, Q8, 2>(a, n_ctas, st)
+                             : launch_decode<64, Q8, 2>(a, n_ctas, st);
 }
 
 }  // namespace

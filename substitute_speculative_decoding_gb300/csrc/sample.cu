@@ -43,6 +43,15 @@ __device__ __forceinline__ float4 load_group(const float* z, const Row& r, int g
   return x;
 }
 
+// The CTAs of a cluster write into each other's shared memory once all of them
+// run: each says so at its start, and asks before its first write.
+__device__ __forceinline__ void cluster_here() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_all_here() {
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+
 // A CTA's share of a row's groups.
 __device__ __forceinline__ void share(int groups, int rank, int size, int& lo, int& hi) {
   const int per = (groups + size - 1) / size;
@@ -61,10 +70,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) probs_kernel(const fl
                                                         float c_lo, float* probs) {
   constexpr int WARPS = THREADS / 32;
   __shared__ float s_m[WARPS], s_s[WARPS];
-  __shared__ float2 s_cta;
+  __shared__ float2 s_peer[MAX_CLUSTER];   // each CTA's (largest logit, sum), written by it
   cg::cluster_group cluster = cg::this_cluster();
   const int size = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int64_t row = blockIdx.x / size;
+  if (size > 1) cluster_here();
   pdl_wait();
   pdl_trigger();
   const float* z = logits + row * V;
@@ -119,18 +129,17 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) probs_kernel(const fl
   if (size == 1) {
     f = s == 0.f ? 0.f : 1.f / s;
   } else {
-    if (threadIdx.x == 0) s_cta = make_float2(m, s);
+    // every CTA writes its own into all of them, so that one barrier is enough:
+    // nobody reads the memory of a CTA that may have ended
+    cluster_all_here();
+    if ((int)threadIdx.x < size) *cluster.map_shared_rank(&s_peer[rank], threadIdx.x) = make_float2(m, s);
     cluster.sync();
-    float2 peer[MAX_CLUSTER];
     float big = -INFINITY, all = 0.f;
-#pragma unroll
-    for (int i = 0; i < MAX_CLUSTER; ++i) {
-      peer[i] = i < size ? *cluster.map_shared_rank(&s_cta, i) : make_float2(-INFINITY, 0.f);
-      big = fmaxf(big, peer[i].x);
+    for (int i = 0; i < size; ++i) big = fmaxf(big, s_peer[i].x);
+    for (int i = 0; i < size; ++i) {
+      const float2 o = s_peer[i];
+      if (o.x != -INFINITY || o.y != 0.f) all += o.y * expo(o.x - big);
     }
-#pragma unroll
-    for (int i = 0; i < MAX_CLUSTER; ++i)
-      if (peer[i].x != -INFINITY || peer[i].y != 0.f) all += peer[i].y * expo(peer[i].x - big);
     f = all == 0.f ? 0.f : expo(m - big) / all;
   }
   auto put = [&](int g, const float4& v) {
@@ -151,13 +160,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) probs_kernel(const fl
   }
   for (int g = lo + threadIdx.x + NV * THREADS; g < hi; g += THREADS)
     put(g, exp4(load_group(z, r, g, -INFINITY)));
-  if (size > 1) cluster.sync();   // peers may still be reading s_cta
 }
 
 // ------------------------------------------------- draft verification --
-constexpr int VER_THREADS = 512, VER_WARPS = VER_THREADS / 32;
-// segments of a CTA's share: one warp's 32 groups of four values each
-constexpr int VER_SEGS = (int)((MAX_V + 3) / 4 + 1 + 31) / 32 / MAX_CLUSTER + VER_WARPS + 1;
+constexpr int VER_THREADS = 256, VER_WARPS = VER_THREADS / 32, VER_MLP = 4;
 
 struct VerifyArgs {
   const float* p;
@@ -175,27 +181,36 @@ __device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
   return v;
 }
+__device__ __forceinline__ uint64_t warp_scan64(uint64_t v, int lane) {   // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t up = __shfl_up_sync(~0u, v, o);
+    if (lane >= o) v += up;
+  }
+  return v;
+}
 
-// One cluster per sequence.  Every CTA repeats the acceptance tests (a few
+// One cluster per sequence.  Every warp repeats the acceptance tests (a few
 // numbers each), which name the row to sample from; then the row is read
 // once: weights as whole multiples of 2^-43, so that their sums do not depend
-// on the order and the sampled token is the same on any split.  A sum per warp
-// segment (128 values) stays in shared memory; the CTA whose part of the
-// running sum holds the number reads that one segment again.  Bound by the
-// latency of the three dependent rounds of reads at few sequences, by HBM
-// (one row of p and of q per sequence) at many.
-__global__ void __launch_bounds__(VER_THREADS) verify_kernel(VerifyArgs a) {
-  __shared__ uint64_t s_seg[VER_SEGS];
-  __shared__ uint64_t s_warp[VER_WARPS], s_cta;
+// on the order and the sampled token is the same on any split.  Each warp sums
+// a contiguous part; the sums of all warps of the cluster name the one warp
+// whose part holds the number, and that warp alone reads its part again (from
+// L2) to find the token.  Bound by the latency of four dependent rounds of
+// reads at few sequences, by HBM (one row of p and of q per sequence) at many.
+__global__ void __launch_bounds__(VER_THREADS, 4) verify_kernel(VerifyArgs a) {
+  __shared__ uint64_t s_sum[MAX_CLUSTER * VER_WARPS];   // every warp of the cluster writes its own
   cg::cluster_group cluster = cg::this_cluster();
   const int size = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int64_t b = blockIdx.x / size;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int n = a.n_draft;
+  const int n = a.n_draft, me = rank * VER_WARPS + warp;
+  if (size > 1) cluster_here();
   pdl_wait();
   pdl_trigger();
+  const float uf = a.u[b * (n + 1) + n];
 
-  // ---- the longest accepted prefix (every warp by itself) ----
+  // ---- the longest accepted prefix ----
   int acc = n;
   bool refused = false;
   for (int i0 = 0; i0 < n; i0 += 32) {
@@ -204,9 +219,10 @@ __global__ void __launch_bounds__(VER_THREADS) verify_kernel(VerifyArgs a) {
     if (i < n) {
       const int x = a.draft[b * n + i];
       if (x >= 0 && x < a.V) {
+        const float ui = a.u[b * (n + 1) + i];
         const double pv = a.p[(b * (n + 1) + i) * a.V + x];
         const double qv = a.q ? a.q[(b * n + i) * a.V + x] : 1.f;
-        bad = !((double)a.u[b * (n + 1) + i] * qv < pv);   // 48-bit product: exact
+        bad = !((double)ui * qv < pv);   // 48-bit product: exact
         stop = bad;
       }
     }
@@ -230,109 +246,99 @@ __global__ void __launch_bounds__(VER_THREADS) verify_kernel(VerifyArgs a) {
   const Row r(p, a.V);
   const bool q_vec = q && ((reinterpret_cast<uintptr_t>(q) >> 2) & 3) == (unsigned)r.mis;
   int lo, hi;
-  share(r.groups(), rank, size, lo, hi);
-  auto weights = [&](int g, bool diff, uint64_t (&w)[4]) {
-    float4 pv = load_group(p, r, g, 0.f), qv = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (diff) {
-      if (q) {
-        qv = q_vec ? load_group(q, r, g, 0.f) : load_group<false>(q, r, g, 0.f);
-      } else {
-        const int64_t e = x - r.first(g);
-        qv = make_float4(e == 0, e == 1, e == 2, e == 3);
-      }
-    }
+  share(r.groups(), me, size * VER_WARPS, lo, hi);
+  auto weights = [&](const float4& pv, const float4& qv, uint64_t (&w)[4]) {
     const float d[4] = {pv.x - qv.x, pv.y - qv.y, pv.z - qv.z, pv.w - qv.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       w[i] = __float2ull_rn(fminf(fmaxf(d[i], 0.f), 1.f) * 0x1p43f);   // NaN counts as 0
   };
-  const float uf = a.u[b * (n + 1) + n];
+  auto load_q = [&](int g, bool diff) {
+    if (!diff) return make_float4(0.f, 0.f, 0.f, 0.f);
+    if (q) return q_vec ? load_group(q, r, g, 0.f) : load_group<false>(q, r, g, 0.f);
+    const int64_t e = x - r.first(g);
+    return make_float4(e == 0, e == 1, e == 2, e == 3);
+  };
   const uint64_t u64 = __float2ull_rz(fminf(fmaxf(uf, 0.f), 0x1.fffffep-1f) * 0x1p64f);
 
+  bool alone = size > 1;   // the others may not run yet
   for (bool diff = refused;; diff = false) {
-    // ---- segment sums, this CTA's sum ----
     uint64_t mine = 0;
-    const int segs = (hi - lo + 31) / 32;
-    for (int s0 = warp; s0 < segs; s0 += 4 * VER_WARPS) {
-      uint64_t v[4];
+    for (int g0 = lo + lane; g0 < hi; g0 += 32 * VER_MLP) {
+      float4 pv[VER_MLP], qv[VER_MLP];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int g = lo + (s0 + k * VER_WARPS) * 32 + lane;
-        uint64_t w[4] = {0, 0, 0, 0};
-        if (g < hi) weights(g, diff, w);
-        v[k] = (w[0] + w[1]) + (w[2] + w[3]);
+      for (int k = 0; k < VER_MLP; ++k) {
+        const int g = g0 + 32 * k;
+        pv[k] = qv[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (g < hi) {
+          pv[k] = load_group(p, r, g, 0.f);
+          qv[k] = load_q(g, diff);
+        }
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint64_t t = warp_sum64(v[k]);
-        if (lane == 0 && s0 + k * VER_WARPS < segs) s_seg[s0 + k * VER_WARPS] = t;
-        mine += t;
+      for (int k = 0; k < VER_MLP; ++k) {
+        uint64_t w[4];
+        weights(pv[k], qv[k], w);
+        mine += (w[0] + w[1]) + (w[2] + w[3]);
       }
     }
-    if (lane == 0) s_warp[warp] = mine;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      uint64_t t = 0;
-      for (int i = 0; i < VER_WARPS; ++i) t += s_warp[i];
-      s_cta = t;
-    }
+    mine = warp_sum64(mine);
+    if (alone) cluster_all_here();
+    alone = false;
+    if (lane < size) *cluster.map_shared_rank(&s_sum[me], lane) = mine;
     if (size > 1) cluster.sync();
     else __syncthreads();
     uint64_t total = 0, before = 0;
-    for (int i = 0; i < size; ++i) {
-      const uint64_t t = *cluster.map_shared_rank(&s_cta, i);
-      if (i < rank) before += t;
+    for (int i = lane; i < size * VER_WARPS; i += 32) {
+      const uint64_t t = s_sum[i];
       total += t;
+      before += i < me ? t : 0;
     }
-    const uint64_t own = s_cta;
+    total = warp_sum64(total);
+    before = warp_sum64(before);
     if (total == 0) {
-      if (size > 1) cluster.sync();
-      else __syncthreads();
-      if (diff) continue;   // nothing left after the rejection: sample p itself
-      if (rank == 0 && threadIdx.x == 0) a.tokens[b * (n + 1) + acc] = 0;
+      if (diff) {   // nothing left after the rejection: sample p itself
+        if (size > 1) cluster.sync();   // everyone has read the sums
+        else __syncthreads();
+        continue;
+      }
+      if (me == 0 && lane == 0) a.tokens[b * (n + 1) + acc] = 0;
       return;
     }
     // ---- the value whose running sum first exceeds u * total ----
     const uint64_t target = __umul64hi(total, u64);   // floor: sums are whole numbers
-    if (target >= before && target - before < own && warp == 0) {
-      uint64_t rest = target - before;   // within this CTA's share
-      int seg = 0;
-      for (int s0 = 0; s0 < segs; s0 += 32) {
-        const uint64_t t = s0 + lane < segs ? s_seg[s0 + lane] : 0;
-        uint64_t run = t;
+    if (target < before || target - before >= mine) return;
+    uint64_t rest = target - before;   // within this warp's part
+    for (int g0 = lo; g0 < hi; g0 += 32 * VER_MLP) {
+      float4 pv[VER_MLP], qv[VER_MLP];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint64_t up = __shfl_up_sync(~0u, run, o);
-          if (lane >= o) run += up;
+      for (int k = 0; k < VER_MLP; ++k) {
+        const int g = g0 + 32 * k + lane;
+        pv[k] = qv[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (g < hi) {
+          pv[k] = load_group(p, r, g, 0.f);
+          qv[k] = load_q(g, diff);
         }
+      }
+#pragma unroll
+      for (int k = 0; k < VER_MLP; ++k) {
+        uint64_t w[4];
+        weights(pv[k], qv[k], w);
+        const uint64_t t = (w[0] + w[1]) + (w[2] + w[3]);
+        const uint64_t run = warp_scan64(t, lane);
         const unsigned over = __ballot_sync(~0u, run > rest);
         if (over) {
-          const int l = __ffs(over) - 1;
-          seg = s0 + l;
-          rest -= __shfl_sync(~0u, run - t, l);
-          break;
+          if (lane == __ffs(over) - 1) {
+            uint64_t at = run - t;
+            int i = 0;
+            while (i < 3 && (at += w[i]) <= rest) ++i;
+            a.tokens[b * (n + 1) + acc] = (int32_t)(r.first(g0 + 32 * k + lane) + i);
+          }
+          return;
         }
         rest -= __shfl_sync(~0u, run, 31);
       }
-      const int g = lo + seg * 32 + lane;
-      uint64_t w[4] = {0, 0, 0, 0};
-      if (g < hi) weights(g, diff, w);
-      const uint64_t t = (w[0] + w[1]) + (w[2] + w[3]);
-      uint64_t run = t;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t up = __shfl_up_sync(~0u, run, o);
-        if (lane >= o) run += up;
-      }
-      const unsigned over = __ballot_sync(~0u, run > rest);
-      if (lane == __ffs(over) - 1) {
-        uint64_t at = run - t;
-        int i = 0;
-        while (i < 3 && (at += w[i]) <= rest) ++i;
-        a.tokens[b * (n + 1) + acc] = (int32_t)(r.first(g) + i);
-      }
     }
-    if (size > 1) cluster.sync();   // peers may still be reading s_cta
     return;
   }
 }

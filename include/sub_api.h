@@ -336,7 +336,7 @@ int32_t sub_kv8_read(const sub_kv8_cache* kv, int32_t layer, const sub_batch* ba
  * Hq % Hkv == 0, Hq / Hkv <= 64; head_dim 64 or 128.  Which sequences share
  * the batch, and max_keys, move a row's result by rounding only; the same call
  * gives the same bits.  workspace: sub_chunk_attn_workspace(...) bytes of
- * device memory, 16-byte aligned, used by this call alone until it is done
+ * device memory, 32-byte aligned, used by this call alone until it is done
  * (its contents do not matter); NULL: drawn from the stream's memory pool. */
 int32_t sub_chunk_attn(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q, const sub_kv_cache* kv,
                        int32_t layer, const sub_batch* batch, float softmax_scale, sub_bf16* O,

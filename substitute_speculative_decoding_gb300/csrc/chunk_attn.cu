@@ -129,14 +129,15 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
   using R = Ring<D, Q8>;
   constexpr int RT = MT * 16, KS = D / 16, ON = D / 8, KB = R::KB, SUBS = R::SUBS, TILES = KB / 8;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t s_pre[SUB_MAX_SEQS + 1], s_warp[WARPS];
+  int64_t* const s_pre = reinterpret_cast<int64_t*>(smem);   // until the first copies
+  static_assert(decode_smem<D, Q8, MT>() >= (SUB_MAX_SEQS + 1) * 8, "the running sums fit");
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, tig = lane & 3;
   const int G = a.group, ps = a.t.page_size;
-  const ChunkPlan<RT, KB> plan(a.t, G, a.n_heads_kv);
-  plan.template scan<NT>(s_pre, s_warp);
+  const ChunkPlan<RT, KB> plan(a);
+  plan.template scan<NT>(s_pre);
   const int64_t total = s_pre[a.t.n_seqs];
   const int64_t per = blocks_per_cta(total, gridDim.x, WARPS);
   const int64_t line_lo = blockIdx.x * per, line_hi = min(total, line_lo + per);
@@ -146,10 +147,13 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
   const uint8_t* const kp = reinterpret_cast<const uint8_t*>(a.k) + g * R::ROW + tig * 16;
   const uint8_t* const vp = reinterpret_cast<const uint8_t*>(a.v) + 2 * tig * R::ROW + g * R::VB;
   const int64_t page_rows = (int64_t)a.n_heads_kv * ps;
-  const int step_pages = WARPS * KB / ps, step_at = WARPS * KB % ps;   // from block to block of a warp
+  // from block to block of a warp
+  const int step_pages = a.by_page.quot(WARPS * KB), step_at = WARPS * KB - step_pages * ps;
+  ChunkUnit u;
+  if (line_lo < line_hi) u = plan.find(s_pre, line_lo);
+  __syncthreads();
 
-  for (int64_t at = line_lo; at < line_hi;) {
-    const auto u = plan.find(s_pre, at);
+  for (int64_t at = line_lo; at < line_hi; plan.next(u)) {
     const int kb0 = (int)(at - u.begin);
     const int kb1 = (int)min((int64_t)u.n_blocks, line_hi - u.begin);
     const int n_mine = (kb1 - kb0 - warp + WARPS - 1) / WARPS;   // blocks kb0 + warp + i * WARPS
@@ -162,7 +166,7 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
       int key, entry, at, page[SUBS];
     } nx;
     nx.key = (kb0 + warp) * KB;
-    nx.entry = (uint32_t)nx.key / (uint32_t)ps;
+    nx.entry = a.by_page.quot(nx.key);
     nx.at = nx.key - nx.entry * ps;
     auto look_up = [&] {
 #pragma unroll
@@ -218,7 +222,7 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
         }
       }
     };
-    auto advance = [&] {
+    auto forward = [&] {
       nx.key += WARPS * KB;
       nx.entry += step_pages;
       nx.at += step_at;
@@ -226,14 +230,29 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
         nx.at -= ps;
         ++nx.entry;
       }
-      look_up();
     };
-    look_up();
+    {
+      // the first blocks' pages are all asked for before the first is used
+      int page[STAGES + 1][SUBS], key = nx.key, entry = nx.entry, place = nx.at;
 #pragma unroll
-    for (int i = 0; i < STAGES; ++i) {
-      if (i < n_mine) issue(i);
-      cp_commit();
-      advance();
+      for (int i = 0; i <= STAGES; ++i) {
+        look_up();
+#pragma unroll
+        for (int s = 0; s < SUBS; ++s) page[i][s] = nx.page[s];
+        forward();
+      }
+      nx.key = key;
+      nx.entry = entry;
+      nx.at = place;
+#pragma unroll
+      for (int i = 0; i <= STAGES; ++i) {
+#pragma unroll
+        for (int s = 0; s < SUBS; ++s) nx.page[s] = page[i][s];
+        if (i == STAGES) break;
+        if (i < n_mine) issue(i);
+        cp_commit();
+        forward();
+      }
     }
 
     // ---- Q fragments, and the rows' last visible key ----
@@ -246,11 +265,11 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int r = u.tile * RT + m * 16 + h * 8 + g;
-        const int q = r / G;
+        const int q = a.by_group.quot(r);
         const bool ok = q < u.rows;
         lim[m][h] = ok ? min(u.pos + q, u.n_keys - 1) : -1;
         const uint16_t* src = a.Q + (int64_t)(u.row0 + (ok ? q : 0)) * a.ldq +
-                              (int64_t)(u.head * G + r % G) * D;
+                              (int64_t)(u.head * G + r - q * G) * D;
 #pragma unroll
         for (int c = 0; c < KS / 2; ++c) {
           // bf16 cache: chunk tig + 4 c of 8 values; codes: half c & 1 of chunk tig + 4 (c / 2) of 16
@@ -300,7 +319,7 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
         }
       }
     }
-    const int lim_min = min(u.pos + u.tile * RT / G, u.n_keys - 1);   // of the tile's first row
+    const int lim_min = min(u.pos + a.by_group.quot(u.tile * RT), u.n_keys - 1);   // of the tile's first row
 
     float o[MT][ON][4], mx[MT][2], l[MT][2];
 #pragma unroll
@@ -455,13 +474,14 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
               w[kk][3] = x.w;
             }
             bool odd = false;
-            if (edge) {   // an exponent of all ones somewhere
+            if (edge) {   // 0 * x is NaN for what is not finite
+              uint32_t z = 0;
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                  odd |= (w[kk][j] & 0x7f80u) == 0x7f80u || (w[kk][j] & 0x7f800000u) == 0x7f800000u;
-              odd = __any_sync(~0u, odd);
+                  asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(z) : "r"(w[kk][j]), "r"(0u));
+              odd = __any_sync(~0u, (z & 0x7fff7fffu) != 0);
             }
             if (!odd) {
 #pragma unroll
@@ -549,7 +569,8 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
       __syncwarp();   // the stage's scales were read by other lanes
       if (i + STAGES < n_mine) issue(stage);
       cp_commit();
-      advance();
+      forward();
+      look_up();
       stage = stage + 1 == STAGES ? 0 : stage + 1;
     }
     cp_wait<0>();
@@ -589,7 +610,7 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
     const float* const all = reinterpret_cast<const float*>(smem);
     for (int idx = tid; idx < RT * (D / 4); idx += NT) {
       const int r = idx / (D / 4), d = (idx % (D / 4)) * 4;
-      const int row = u.tile * RT + r, q = row / G;
+      const int row = u.tile * RT + r, q = a.by_group.quot(row);
       if (q >= u.rows) continue;
       float big = -INFINITY;
 #pragma unroll
@@ -610,7 +631,7 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
       }
       if (whole) {
         const float inv = big == -INFINITY ? 0.f : 1.f / sum;
-        *reinterpret_cast<uint2*>(a.O + ((int64_t)(u.row0 + q) * a.n_heads_q + u.head * G + row % G) * D + d) =
+        *reinterpret_cast<uint2*>(a.O + ((int64_t)(u.row0 + q) * a.n_heads_q + u.head * G + row - q * G) * D + d) =
             make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
       } else {
         __stcg(reinterpret_cast<float4*>(a.part_o + (slot * RT + r) * D + d),
@@ -643,10 +664,20 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) chunk_join_kernel(ChunkArgs a
   const int lane = threadIdx.x & 31, n = c.pieces;
   const int d = (lane % LANES) * 4, part = lane / LANES;
   auto slot = [&](int i) { return i == 0 ? c.first : 2 * ((int)blockIdx.x + i); };
+  const FastDiv by = a.by_group;
   for (int r = blockIdx.y * join_rows(RT) + (threadIdx.x >> 5); r < (int)(blockIdx.y + 1) * join_rows(RT);
        r += JOIN_WARPS) {
-    const int row = c.tile * RT + r, q = row / a.group;
+    const int row = c.tile * RT + r, q = by.quot(row);
     if (q >= c.rows) break;
+    auto piece = [&](int i) {
+      return __ldcg(reinterpret_cast<const float4*>(a.part_o + ((int64_t)slot(i) * RT + r) * D + d));
+    };
+    // the first pieces' columns are on their way with the maxima
+    constexpr int AHEAD = 8;
+    float4 v[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+      v[i] = i * PER + part < n ? piece(i * PER + part) : make_float4(0.f, 0.f, 0.f, 0.f);
     float2 ml[JOIN_MAX];
     float big = -INFINITY;
 #pragma unroll
@@ -664,22 +695,24 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) chunk_join_kernel(ChunkArgs a
     }
     sum = warp_sum(sum);
     float x[4] = {0.f, 0.f, 0.f, 0.f};
+    auto add = [&](float f, const float4& y) {
+      x[0] = fmaf(f, y.x, x[0]);
+      x[1] = fmaf(f, y.y, x[1]);
+      x[2] = fmaf(f, y.z, x[2]);
+      x[3] = fmaf(f, y.w, x[3]);
+    };
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)   // a piece that is not there has weight 0
+      add(__shfl_sync(~0u, ml[0].x, i * PER + part), v[i]);
 #pragma unroll
     for (int k = 0; k < JOIN_MAX; ++k) {
       if (k * 32 >= n) break;
 #pragma unroll 8
-      for (int i0 = 0; i0 < 32; i0 += PER) {
+      for (int i0 = k == 0 ? AHEAD * PER : 0; i0 < 32; i0 += PER) {
         if (k * 32 + i0 >= n) break;
         const int i = k * 32 + i0 + part;
         const float f = __shfl_sync(~0u, ml[k].x, i0 + part);
-        if (i < n) {
-          const float4 v =
-              __ldcg(reinterpret_cast<const float4*>(a.part_o + ((int64_t)slot(i) * RT + r) * D + d));
-          x[0] = fmaf(f, v.x, x[0]);
-          x[1] = fmaf(f, v.y, x[1]);
-          x[2] = fmaf(f, v.z, x[2]);
-          x[3] = fmaf(f, v.w, x[3]);
-        }
+        if (i < n) add(f, piece(i));
       }
     }
     if constexpr (PER == 2) {
@@ -689,7 +722,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) chunk_join_kernel(ChunkArgs a
     const float inv = big == -INFINITY ? 0.f : 1.f / sum;
     if (part == 0)
       *reinterpret_cast<uint2*>(
-          a.O + ((int64_t)(c.row0 + q) * a.n_heads_q + c.head * a.group + row % a.group) * D + d) =
+          a.O + ((int64_t)(c.row0 + q) * a.n_heads_q + c.head * a.group + row - q * a.group) * D + d) =
           make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
   }
 }
@@ -769,6 +802,8 @@ int32_t chunk_attn(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q, const Cach
   a.n_heads_q = n_heads_q;
   a.n_heads_kv = kv->n_heads_kv;
   a.group = n_heads_q / kv->n_heads_kv;
+  a.by_group = make_fast_div(a.group);
+  a.by_page = make_fast_div(kv->page_size);
   // (a scale of 0 must not meet the masked scores' -infinity)
   a.sl2 = fmaxf(softmax_scale, 1e-30f) * 1.4426950408889634f;
   const cudaStream_t st = as_stream(stream);
@@ -777,7 +812,8 @@ int32_t chunk_attn(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q, const Cach
                                    &need));
   StreamScratch scratch(st);
   if (workspace) {
-    SUB_CHECK_ARG(aligned16(workspace) && workspace_bytes >= need, "workspace too small");
+    SUB_CHECK_ARG((reinterpret_cast<uintptr_t>(workspace) & 31) == 0 && workspace_bytes >= need,
+                  "workspace too small or not 32-byte aligned");
   } else {
     SUB_TRY(scratch.alloc((size_t)need));
     workspace = scratch.p;

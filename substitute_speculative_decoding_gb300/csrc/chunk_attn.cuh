@@ -4,6 +4,23 @@
 
 namespace sub {
 
+// Division by a number that the host knows: n / d for 0 <= n < 2^31 is the high
+// word of n * ceil(2^(31 + s) / d), shifted, with 2^s >= d.  (The error of the
+// reciprocal, below 2^-(31 + s), stays below 1 / d even times 2^31.)  A division
+// instruction sequence costs some 100 cycles, a dozen of them before a CTA's first load.
+struct FastDiv {
+  uint32_t d, mul, shift;
+  __device__ __forceinline__ int quot(int n) const {
+    return d == 1 ? n : (int)(__umulhi((uint32_t)n, mul) >> shift);
+  }
+};
+inline FastDiv make_fast_div(uint32_t d) {
+  uint32_t s = 0;
+  while ((1ull << s) < d) ++s;
+  if (d == 1) return {1, 0, 0};
+  return {d, (uint32_t)(((1ull << (31 + s)) + d - 1) / d), s - 1};
+}
+
 struct ChunkArgs {
   SeqTable t;
   const uint16_t* Q;     // [n_rows, Hq, D] bf16, rows ldq elements apart
@@ -14,6 +31,7 @@ struct ChunkArgs {
   const float* ks;       // scales of the codes
   const float* vs;
   int layer, n_heads_q, n_heads_kv, group;   // group = Hq / Hkv
+  FastDiv by_group, by_page;
   float sl2;             // softmax scale * log2(e): scores in base 2
   // partial results of key ranges cut between CTAs: two per CTA
   float* part_o;         // [2 n_ctas][rows][D], relative to the maxima of
@@ -24,7 +42,7 @@ struct ChunkArgs {
 // The unit of work (below) that is cut first at the end of a CTA's part, for the
 // kernel that joins its pieces: written by each CTA, pieces 0 where none is.
 struct __align__(16) ChunkCut {
-  int row0, rows, tile, head;   // as in ChunkPlan::Unit
+  int row0, rows, tile, head;   // as in ChunkUnit
   int pieces, first;            // the first piece's slot; piece i > 0 of CTA x lies in slot 2 (x + i)
   int pad[2];
 };
@@ -42,95 +60,123 @@ __device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
 // KB keys.  All units' blocks, sequence by sequence, KV head by KV head, tile by
 // tile, form one line that the CTAs share evenly, so that any mix of lengths
 // fills the GPU; a unit cut between CTAs is joined afterwards from their
-// partial results, in order.  Every CTA works the plan out by itself from
-// the lengths on the device.
+// partial results, in order.  Every CTA works its part out by itself from
+// the lengths on the device: the place of its first unit from running sums over the
+// sequences, the others one after the other.
+struct ChunkUnit {
+  int b, head, tile;      // sequence, KV head, tile
+  int row0, rows, pos;    // the sequence's first row, its rows, position of the first
+  int n_keys, n_blocks;   // of this tile
+  int64_t begin;          // its first block on the line
+};
+
 template <int RT, int KB>
 struct ChunkPlan {
-  const SeqTable& t;
-  int group, heads;
-  __device__ ChunkPlan(const SeqTable& t_, int g, int h) : t(t_), group(g), heads(h) {}
+  const ChunkArgs& a;
+  __device__ explicit ChunkPlan(const ChunkArgs& a_) : a(a_) {}
 
   // rows of one head-group of a sequence, tiles of them
-  __device__ int tiles(int rows) const { return (rows * group + RT - 1) / RT; }
-  // keys that tile j of sequence b (rows new rows from position pos on) reads
+  __device__ int tiles(int rows) const { return (rows * a.group + RT - 1) / RT; }
+  // keys that tile j of a sequence (rows new rows from position pos on) reads
   __device__ int keys(int pos, int rows, int j) const {
-    const int last = min(rows, (j * RT + RT - 1) / group + 1);
-    return (int)max((int64_t)0, min((int64_t)pos + last, t.capacity));
+    const int last = min(rows, a.by_group.quot(j * RT + RT - 1) + 1);
+    return (int)max((int64_t)0, min((int64_t)pos + last, a.t.capacity));
   }
   __device__ int blocks(int pos, int rows, int j) const {
     return max(1, (keys(pos, rows, j) + KB - 1) / KB);   // a tile without keys still writes zeros
   }
-  __device__ int64_t seq_blocks(int b) const {   // of one KV head
-    const int rows = seq_rows(t, b), pos = t.pos[b], n = tiles(rows);
-    int64_t s = 0;
-    for (int j = 0; j < n; ++j) s += blocks(pos, rows, j);
-    return s;
+  __device__ void load(ChunkUnit& u) const {
+    u.row0 = seq_first(a.t, u.b);
+    u.rows = seq_rows(a.t, u.b);
+    u.pos = a.t.pos[u.b];
+  }
+  __device__ void measure(ChunkUnit& u) const {
+    u.n_keys = keys(u.pos, u.rows, u.tile);
+    u.n_blocks = max(1, (u.n_keys + KB - 1) / KB);
   }
 
-  // pre[b] = blocks of all sequences before b (all KV heads), pre[n_seqs] = all
+  // pre[b] = blocks of all sequences before b (all KV heads), pre[n_seqs] = all; by NT
+  // threads.  A warp takes a sequence, its lanes the tiles.
   template <int NT>
-  __device__ void scan(int64_t* pre, int64_t* warp_sums) const {
-    constexpr int PER = (SUB_MAX_SEQS + NT - 1) / NT;
-    const int per = (t.n_seqs + NT - 1) / NT, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t mine[PER], sum = 0;
+  __device__ void scan(int64_t* pre) const {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = a.t.n_seqs;
+    for (int b = warp; b < n; b += NT / 32) {
+      const int rows = seq_rows(a.t, b), pos = a.t.pos[b], nt = tiles(rows);
+      int64_t s = 0;
+      for (int j = lane; j < nt; j += 32) s += blocks(pos, rows, j);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int b = threadIdx.x * per + i;
-      mine[i] = i < per && b < t.n_seqs ? seq_blocks(b) * heads : 0;
-      sum += mine[i];
+      for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+      if (lane == 0) pre[b + 1] = s * a.n_heads_kv;
     }
-    int64_t run = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t up = __shfl_up_sync(~0u, run, o);
-      if (lane >= o) run += up;
-    }
-    if (lane == 31) warp_sums[warp] = run;
     __syncthreads();
-    int64_t at = run - sum;
-    for (int w = 0; w < warp; ++w) at += warp_sums[w];
+    if (warp == 0) {   // running sums, 32 sequences at a time
+      int64_t at = 0;
+      if (lane == 0) pre[0] = 0;
+      for (int b0 = 0; b0 < n; b0 += 32) {
+        int64_t v = b0 + lane < n ? pre[b0 + lane + 1] : 0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int b = threadIdx.x * per + i;
-      if (i < per && b < t.n_seqs) {
-        pre[b] = at;
-        at += mine[i];
-        if (b == t.n_seqs - 1) pre[t.n_seqs] = at;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t up = __shfl_up_sync(~0u, v, o);
+          if (lane >= o) v += up;
+        }
+        if (b0 + lane < n) pre[b0 + lane + 1] = at + v;
+        at += __shfl_sync(~0u, v, 31);
       }
     }
     __syncthreads();
   }
 
-  struct Unit {
-    int b, head, tile;      // sequence, KV head, tile
-    int row0, rows, pos;    // the sequence's first row, its rows, position of the first
-    int n_keys, n_blocks;   // of this tile
-    int64_t begin;          // its first block on the line
-  };
-  // the unit that block `at` of the line belongs to
-  __device__ Unit find(const int64_t* pre, int64_t at) const {
-    int lo = 0, hi = t.n_seqs - 1;   // last sequence that begins at or before it
+  // the unit that block `at` (< pre[n_seqs]) of the line belongs to; by a whole warp
+  __device__ ChunkUnit find(const int64_t* pre, int64_t at) const {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = a.t.n_seqs - 1;   // last sequence that begins at or before it
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (pre[mid] <= at) lo = mid;
       else hi = mid - 1;
     }
-    Unit u;
+    ChunkUnit u;
     u.b = lo;
-    u.row0 = seq_first(t, lo);
-    u.rows = seq_rows(t, lo);
-    u.pos = t.pos[lo];
-    const int64_t per_head = quot(pre[lo + 1] - pre[lo], heads);
+    load(u);
+    const int64_t per_head = quot(pre[lo + 1] - pre[lo], a.n_heads_kv);
     u.head = (int)quot(at - pre[lo], per_head);
     u.begin = pre[lo] + u.head * per_head;
-    u.tile = 0;
-    u.n_blocks = blocks(u.pos, u.rows, 0);
-    while (at - u.begin >= u.n_blocks) {
-      u.begin += u.n_blocks;
-      u.n_blocks = blocks(u.pos, u.rows, ++u.tile);
+    const int nt = tiles(u.rows);
+    for (int j0 = 0;; j0 += 32) {   // 32 tiles at a time
+      const int v = j0 + lane < nt ? blocks(u.pos, u.rows, j0 + lane) : 0;
+      int64_t run = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t up = __shfl_up_sync(~0u, run, o);
+        if (lane >= o) run += up;
+      }
+      const unsigned over = __ballot_sync(~0u, at - u.begin < run);
+      if (over || j0 + 32 >= nt) {
+        const int l = over ? __ffs(over) - 1 : 0;
+        u.tile = j0 + l;
+        u.begin += __shfl_sync(~0u, run - v, l);
+        break;
+      }
+      u.begin += __shfl_sync(~0u, run, 31);
     }
-    u.n_keys = keys(u.pos, u.rows, u.tile);
+    measure(u);
     return u;
+  }
+
+  // the unit after u (past the last one: undefined, but harmless)
+  __device__ void next(ChunkUnit& u) const {
+    u.begin += u.n_blocks;
+    if (++u.tile >= tiles(u.rows)) {
+      u.tile = 0;
+      if (++u.head == a.n_heads_kv) {
+        u.head = 0;
+        do {
+          if (++u.b >= a.t.n_seqs) return;
+          load(u);
+        } while (u.rows == 0);
+      }
+    }
+    measure(u);
   }
 };
 
@@ -141,8 +187,7 @@ __device__ __forceinline__ int64_t blocks_per_cta(int64_t total, int n_ctas, int
 }
 // A CTA's entry in the list of cuts, from its last piece (blocks [.., kb1) of u;
 // the CTA's part of the line begins at lo).
-template <class Unit>
-__device__ __forceinline__ ChunkCut make_cut(const Unit& u, int kb1, int64_t lo, int64_t per) {
+__device__ __forceinline__ ChunkCut make_cut(const ChunkUnit& u, int kb1, int64_t lo, int64_t per) {
   ChunkCut c{u.row0, u.rows, u.tile, u.head, 0, 0, {0, 0}};
   if (kb1 < u.n_blocks && u.begin >= lo) {
     c.pieces = (int)(quot(u.begin + u.n_blocks - 1, per) - blockIdx.x) + 1;

@@ -17,8 +17,8 @@
 //                    are there, O += P V with P read from tensor memory (in
 //                    place of S, as bf16 or fp16 pairs) and S of the next block
 // O stays in tensor memory.  It is rescaled only when a row's maximum has grown
-// by more than 2^8 since the weights' reference was set: until then the weights
-// exceed 1 by at most that factor, which costs a floating-point value nothing.
+// by more than 2^8 (codes: 2^4) since the weights' reference was set: until then the
+// weights exceed 1 by at most that factor, which costs a floating-point value nothing.
 // P is rounded once, to bf16 (half a step 2^-8 relative, random over the keys; the
 // sum takes the unrounded weights) or fp16 for codes; a second product with
 // the rest would make the tensor cores half as slow again.
@@ -45,17 +45,18 @@ using namespace tmah;
 constexpr int RT = CHUNK_TC_ROWS, KB = CHUNK_TC_KEYS;
 static_assert(RT == 256 && KB == 128, "two groups of 128 rows, blocks of 128 keys");
 constexpr int GROUP_ROWS = 128;
-constexpr float GROWTH = 8.f;        // log2 of how far weights may exceed 1
-constexpr float Q8_SHIFT = 7.f;      // fp16 weights times scales: 2^7 at the reference, 2^15 at most
+// log2 of how far weights may exceed 1; fp16 weights times scales of V are 2^11 at
+// the reference and 2^15 at most, so that fp16's smallest step is 2^-35 of the former
+constexpr float growth(bool q8) { return q8 ? 4.f : 8.f; }
+constexpr float Q8_SHIFT = 11.f;
 
 __device__ unsigned int g_chunk_timeouts;   // waits that ran out (never expected)
 
 template <int D, bool Q8>
 struct Cfg {
   static constexpr int STAGE = KB * D * 2;               // K or V of a block, 16-bit values
-  static constexpr int STAGES = D == 128 ? 4 : 6;
+  static constexpr int STAGES = D == 64 ? 6 : Q8 ? 4 : 5;
   static constexpr int Q_BYTES = GROUP_ROWS * D * 2;     // of one group
-  static constexpr int N_PROD = Q8 ? 4 : 1;              // producer warps
   static constexpr int MMA_WARP = 8 + (Q8 ? 4 : 1);
   static constexpr int THREADS = Q8 ? 512 : 384;         // whole groups of four warps
   // registers by group of four warps, out of 65536 / THREADS each at the launch
@@ -70,9 +71,12 @@ struct Cfg {
   static constexpr int SCALE_SLOT = 2 * KB + 4;
   static constexpr int SCALES = Q8 ? 4 * SCALE_SLOT * 4 : 0;
   static constexpr int QSCALES = Q8 ? RT * 4 : 0;
-  static constexpr int TAIL = 512;                       // barriers, flags, TMEM address
+  static constexpr int ROWS = Q8 ? 4 * KB * 4 : 0;       // pool rows of four blocks' keys
+  static constexpr int TAIL = 256;                       // barriers, flags, TMEM address
   static constexpr int SMEM =
-      1024 + 2 * Q_BYTES + STAGES * STAGE + SCALES + QSCALES + TAIL;
+      1024 + 2 * Q_BYTES + STAGES * STAGE + SCALES + QSCALES + ROWS + TAIL;
+  static_assert(SMEM <= 227 * 1024, "one CTA's shared memory");
+  static_assert(STAGES * STAGE >= (SUB_MAX_SEQS + 1) * 8, "the ring holds the running sums first");
 };
 
 // ---------------------------------------------------------------- tcgen05 --
@@ -239,23 +243,34 @@ struct Maps {
   CUtensorMap k, v;   // pool rows [all rows, D] bf16, boxes of 64 columns x box keys
 };
 
+__device__ __forceinline__ void st_shared(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+// 32 bytes at once: a row is written by one thread, and this fills whole sectors.
+__device__ __forceinline__ void st_global32(void* p, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 // ------------------------------------------------------------------ kernel --
 template <int D, bool Q8>
 __global__ void __launch_bounds__(Cfg<D, Q8>::THREADS, 1)
-chunk_tc_kernel(const __grid_constant__ Maps maps, const ChunkArgs a, const int box,
+chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ChunkArgs a, const int box,
                 const int pool_rows) {
   using C = Cfg<D, Q8>;
   constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ int64_t s_pre[SUB_MAX_SEQS + 1], s_warp[C::THREADS / 32];
-  __shared__ int s_rows[2][Q8 ? KB : 1];   // pool rows of two blocks' keys (converters)
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* const base_p = smem_raw + (base - smem_u32(smem_raw));
   const uint32_t q_s = base, ring_s = base + 2 * C::Q_BYTES;
+  int64_t* const s_pre = reinterpret_cast<int64_t*>(base_p + 2 * C::Q_BYTES);   // until the first copies
   uint8_t* const after = base_p + 2 * C::Q_BYTES + STAGES * C::STAGE;
-  float* const s_scale = reinterpret_cast<float*>(after);                  // [4][SCALE_SLOT]
-  float* const s_qs = reinterpret_cast<float*>(after + C::SCALES);         // [RT]
-  uint8_t* const tail = after + C::SCALES + C::QSCALES;
+  float* const s_scale = reinterpret_cast<float*>(after);                   // [4][SCALE_SLOT]
+  float* const s_qs = reinterpret_cast<float*>(after + C::SCALES);          // [RT]
+  int* const s_rows = reinterpret_cast<int*>(after + C::SCALES + C::QSCALES);   // [4][KB]
+  uint8_t* const tail = after + C::SCALES + C::QSCALES + C::ROWS;
   const uint32_t bars = smem_u32(tail);
   auto kv_full = [&](int s) { return bars + 8u * s; };
   auto kv_empty = [&](int s) { return bars + 8u * (STAGES + s); };
@@ -280,7 +295,7 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const ChunkArgs a, const int 
   }
   if (tid == 32) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(kv_full(s), Q8 ? C::N_PROD * 32 : 1);
+      mbar_init(kv_full(s), Q8 ? 128 : 1);
       mbar_init(kv_empty(s), 1);
     }
     for (int t = 0; t < 2; ++t) {
@@ -294,19 +309,26 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const ChunkArgs a, const int 
     s_odd[0] = s_odd[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (!Q8 && tid == 64) {
+    tma_prefetch_desc(&maps.k);
+    tma_prefetch_desc(&maps.v);
+  }
   pdl_wait();
   pdl_trigger();
-  const ChunkPlan<RT, KB> plan(a.t, a.group, a.n_heads_kv);
+  const ChunkPlan<RT, KB> plan(a);
   tc_fence_before();
-  plan.template scan<C::THREADS>(s_pre, s_warp);   // ends with a barrier
+  plan.template scan<C::THREADS>(s_pre);   // ends with a barrier
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
   const int64_t total = s_pre[a.t.n_seqs];
   const int64_t per = blocks_per_cta(total, gridDim.x, CHUNK_TC_LEAST);
   const int64_t line_lo = blockIdx.x * per, line_hi = min(total, line_lo + per);
+  ChunkUnit u;
+  if (line_lo < line_hi) u = plan.find(s_pre, line_lo);
+  fence_async();     // the ring is written by copies from here on
+  __syncthreads();
   const Gate gate{s_dead};
   const int G = a.group;
-
   if (warp < 8) more_registers<C::REGS_SOFTMAX>();
   else if (!Q8 || warp < 12) fewer_registers<C::REGS_PROD>();
   else fewer_registers<C::REGS_MMA>();
@@ -318,73 +340,79 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const ChunkArgs a, const int 
     const uint32_t tS = tmem + t * 128 + lanes, tO = tmem + 256 + t * 128 + lanes;
     uint32_t n_s = 0, n_o = 0;      // blocks and pieces seen by this group
     uint32_t items = 0;             // ring items before this piece
-    int piece = 0;
-    if (tid == 0 && line_lo >= line_hi) a.cuts[blockIdx.x].pieces = 0;
-    for (int64_t at = line_lo; at < line_hi; ++piece) {
-      const int64_t begin = at;
-      int kb0, kb1, lim, lim_first, n_keys;
-      float factor = a.sl2;        // of the row's scores, to base 2
-      {
-        const auto u = plan.find(s_pre, at);
-        kb0 = (int)(at - u.begin);
-        kb1 = (int)min((int64_t)u.n_blocks, line_hi - u.begin);
-        at = u.begin + kb1;
-        if (tid == 0 && at >= line_hi) a.cuts[blockIdx.x] = make_cut(u, kb1, line_lo, per);
-        const int row0 = u.tile * RT + t * GROUP_ROWS;     // the group's first row
-        if (row0 >= u.rows * G) {                          // an empty second group
-          items += 2 * (kb1 - kb0);
-          continue;
-        }
-        // ---- Q: 16-byte chunks c of a row at c ^ (row % 8) of its 128-byte line ----
-        // (each warp its own threads' rows)
-        constexpr int CH = D / 8, RP = 32 / CH;            // chunks of a row, rows per pass
-        const int c = lane % CH;
-        const uint32_t dst0 = q_s + t * C::Q_BYTES + (c >> 3) * (GROUP_ROWS * 128);
-        uint4 w[CH];
+    constexpr int CH = D / 8, RP = 32 / CH;   // 16-byte chunks of a Q row, rows per pass of a warp
+    const int c = lane % CH;
+
+    // Q of a unit's group, first into registers, then into shared memory: chunk c of
+    // a row at c ^ (row % 8) of its 128-byte line, each warp its own threads' rows
+    auto has_rows = [&](const ChunkUnit& x) { return x.tile * RT + t * GROUP_ROWS < x.rows * G; };
+    auto q_load = [&](const ChunkUnit& x, uint4 (&w)[CH]) {
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
-          const int row = row0 + (warp & 3) * 32 + i * RP + lane / CH, q = row / G;
-          w[i] = make_uint4(0, 0, 0, 0);
-          if (q < u.rows)
-            w[i] = ldg_nc_v4(a.Q + (int64_t)(u.row0 + q) * a.ldq + (int64_t)(u.head * G + row % G) * D +
-                             c * 8);
-        }
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-          const int rr = (warp & 3) * 32 + i * RP + lane / CH;
-          if constexpr (Q8) {
-            // the row's largest value to [1, 2), for fp16
-            const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-            float big = 0.f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              big = fmaxf(big, fmaxf(fabsf(bf16lo(x[k])), fabsf(bf16hi(x[k]))));
-#pragma unroll
-            for (int o = CH / 2; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, o));
-            const int e = min(126, max(-126, (int)(__float_as_uint(big) >> 23) - 127));
-            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-            if (c == 0)
-              s_qs[t * GROUP_ROWS + rr] = a.sl2 * __uint_as_float((uint32_t)(127 + e) << 23);
-            w[i].x = pack_f16x2(bf16lo(x[0]) * down, bf16hi(x[0]) * down);
-            w[i].y = pack_f16x2(bf16lo(x[1]) * down, bf16hi(x[1]) * down);
-            w[i].z = pack_f16x2(bf16lo(x[2]) * down, bf16hi(x[2]) * down);
-            w[i].w = pack_f16x2(bf16lo(x[3]) * down, bf16hi(x[3]) * down);
-          }
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
-                           dst0 + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)),
-                       "r"(w[i].x), "r"(w[i].y), "r"(w[i].z), "r"(w[i].w)
-                       : "memory");
-        }
-        fence_async();
-        mbar_arrive(q_full(t));
-        __syncwarp();   // s_qs
-        const int q = (row0 + r) / G;
-        n_keys = u.n_keys;
-        lim = q < u.rows ? min(u.pos + q, n_keys - 1) : -1;            // keys 0 .. lim are read
-        lim_first = min(u.pos + u.tile * RT / G, n_keys - 1);          // by every row of the tile
-        // (not 0: it meets the masked scores' -infinity)
-        if constexpr (Q8) factor = fmaxf(s_qs[t * GROUP_ROWS + r], 1e-37f);
+      for (int i = 0; i < CH; ++i) {
+        const int row = x.tile * RT + t * GROUP_ROWS + (warp & 3) * 32 + i * RP + lane / CH;
+        const int q = a.by_group.quot(row);
+        w[i] = make_uint4(0, 0, 0, 0);
+        if (q < x.rows)
+          w[i] = ldg_nc_v4(a.Q + (int64_t)(x.row0 + q) * a.ldq + (int64_t)(x.head * G + row - q * G) * D +
+                           c * 8);
       }
+    };
+    auto q_store = [&](uint4 (&w)[CH]) {
+      const uint32_t dst0 = q_s + t * C::Q_BYTES + (c >> 3) * (GROUP_ROWS * 128);
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int rr = (warp & 3) * 32 + i * RP + lane / CH;
+        if constexpr (Q8) {
+          // the row's largest value to [1, 2), for fp16
+          const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+          float big = 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            big = fmaxf(big, fmaxf(fabsf(bf16lo(x[k])), fabsf(bf16hi(x[k]))));
+#pragma unroll
+          for (int o = CH / 2; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, o));
+          const int e = min(126, max(-126, (int)(__float_as_uint(big) >> 23) - 127));
+          const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+          // (not 0: it meets the masked scores' -infinity)
+          if (c == 0)
+            s_qs[t * GROUP_ROWS + rr] = fmaxf(a.sl2 * __uint_as_float((uint32_t)(127 + e) << 23), 1e-37f);
+          w[i].x = pack_f16x2(bf16lo(x[0]) * down, bf16hi(x[0]) * down);
+          w[i].y = pack_f16x2(bf16lo(x[1]) * down, bf16hi(x[1]) * down);
+          w[i].z = pack_f16x2(bf16lo(x[2]) * down, bf16hi(x[2]) * down);
+          w[i].w = pack_f16x2(bf16lo(x[3]) * down, bf16hi(x[3]) * down);
+        }
+        st_shared(dst0 + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), w[i].x, w[i].y, w[i].z, w[i].w);
+      }
+      fence_async();
+      mbar_arrive(q_full(t));
+      __syncwarp();   // s_qs
+    };
+    if (tid == 0 && line_lo >= line_hi) a.cuts[blockIdx.x].pieces = 0;
+    bool q_there = false;   // this piece's Q is in shared memory already
+    int piece = 0;
+    for (int64_t at = line_lo; at < line_hi; ++piece) {
+      const int kb0 = (int)(at - u.begin), kb1 = (int)min((int64_t)u.n_blocks, line_hi - u.begin);
+      const bool first = at == line_lo;
+      at = u.begin + kb1;
+      if (tid == 0 && at >= line_hi) a.cuts[blockIdx.x] = make_cut(u, kb1, line_lo, per);
+      if (!has_rows(u)) {   // an empty second group
+        items += 2 * (kb1 - kb0);
+        plan.next(u);
+        continue;
+      }
+      if (!q_there) {
+        uint4 w[CH];
+        q_load(u, w);
+        q_store(w);
+      }
+      const int row = u.tile * RT + t * GROUP_ROWS + r, q = a.by_group.quot(row);
+      const bool real = q < u.rows;
+      const int n_keys = u.n_keys;
+      const int lim = real ? min(u.pos + q, n_keys - 1) : -1;                         // keys 0 .. lim are read
+      const int lim_first = min(u.pos + a.by_group.quot(u.tile * RT), n_keys - 1);    // by every row of the tile
+      float factor = a.sl2;        // of the row's scores, to base 2
+      if constexpr (Q8) factor = s_qs[t * GROUP_ROWS + r];
+
       float ref = 0.f, l = 0.f;    // weights are 2^(score - ref)
       bool any = false;            // a key has been read
       for (int kb = kb0; kb < kb1; ++kb, items += 2) {
@@ -394,7 +422,7 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const ChunkArgs a, const int 
         tc_fence_after();
         float s[KB];
 #pragma unroll
-        for (int c = 0; c < KB; c += 32) tc_ld32(tS + c, s + c);
+        for (int x = 0; x < KB; x += 32) tc_ld32(tS + x, s + x);
         const uint32_t miss = s_miss[(items >> 1) & 7];
         const bool behind = key0 + KB - 1 > lim_first;   // the same for all rows of the tile
         const bool edge = behind || miss;
@@ -402,30 +430,30 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const ChunkArgs a, const int 
         wait_ld();
         if constexpr (Q8) {
 #pragma unroll
-          for (int c = 0; c < KB; c += 4) {
-            const float4 k4 = *reinterpret_cast<const float4*>(sc + c);
-            const float2 x = mul2(make_float2(s[c], s[c + 1]), make_float2(k4.x, k4.y));
-            const float2 y = mul2(make_float2(s[c + 2], s[c + 3]), make_float2(k4.z, k4.w));
-            s[c] = x.x;
-            s[c + 1] = x.y;
-            s[c + 2] = y.x;
-            s[c + 3] = y.y;
+          for (int x = 0; x < KB; x += 4) {
+            const float4 k4 = *reinterpret_cast<const float4*>(sc + x);
+            const float2 y = mul2(make_float2(s[x], s[x + 1]), make_float2(k4.x, k4.y));
+            const float2 z = mul2(make_float2(s[x + 2], s[x + 3]), make_float2(k4.z, k4.w));
+            s[x] = y.x;
+            s[x + 1] = y.y;
+            s[x + 2] = z.x;
+            s[x + 3] = z.y;
           }
         }
         if (edge) {
           const int last = lim - key0;   // columns past it are not read
 #pragma unroll
-          for (int c = 0; c < KB; ++c)
-            if (c > last || ((miss >> miss_bit<Q8>(c >> 4)) & 1u)) s[c] = -INFINITY;
+          for (int x = 0; x < KB; ++x)
+            if (x > last || ((miss >> miss_bit<Q8>(x >> 4)) & 1u)) s[x] = -INFINITY;
         }
         // eight chains: a single one would wait for itself 128 times
         float top8[8];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) top8[c] = fmaxf(s[c], s[c + 8]);
+        for (int i = 0; i < 8; ++i) top8[i] = fmaxf(s[i], s[i + 8]);
 #pragma unroll
-        for (int c = 16; c < KB; c += 16)
+        for (int x = 16; x < KB; x += 16)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) top8[i] = fmaxf(fmaxf(top8[i], s[c + i]), s[c + 8 + i]);
+          for (int i = 0; i < 8; ++i) top8[i] = fmaxf(fmaxf(top8[i], s[x + i]), s[x + 8 + i]);
         float top = fmaxf(fmaxf(fmaxf(top8[0], top8[1]), fmaxf(top8[2], top8[3])),
                           fmaxf(fmaxf(top8[4], top8[5]), fmaxf(top8[6], top8[7])));
         top = top == -INFINITY ? top : top * factor;
@@ -435,7 +463,7 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const ChunkArgs a, const int 
           top += fmaxf(fmaxf(lv.x, lv.y), fmaxf(lv.z, lv.w));
         }
         // ---- the reference, and the output that was formed with another ----
-        const bool grow = top > ref + GROWTH || (!any && top != -INFINITY);
+        const bool grow = top > ref + growth(Q8) || (!any && top != -INFINITY);
         if (__any_sync(~0u, grow)) {
           const float f = grow && any ? exp2_fast(ref - top) : 1.f;
           if (grow) {
@@ -444,15 +472,15 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const ChunkArgs a, const int 
           }
           l *= f;
           if (kb > kb0 && __any_sync(~0u, f != 1.f)) {
-#pragma unroll
-            for (int c = 0; c < D; c += 16) {
+#pragma unroll 1
+            for (int x = 0; x < D; x += 16) {
               float o[16];
               __syncwarp();
-              tc_ld16(tO + c, o);
+              tc_ld16(tO + x, o);
               wait_ld();
 #pragma unroll
               for (int i = 0; i < 16; ++i) o[i] *= f;
-              tc_st16(tO + c, reinterpret_cast<const uint32_t*>(o));
+              tc_st16(tO + x, reinterpret_cast<const uint32_t*>(o));
             }
           }
         }
@@ -462,28 +490,37 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const ChunkArgs a, const int 
           if (!gate.wait_warp(kv_full(st), ((items + 1) / STAGES) & 1)) break;
           const uint32_t v0 = ring_s + st * C::STAGE + r * 128;
           const bool past = key0 + r >= n_keys;
-          bool odd = false;
-#pragma unroll 4
+          uint32_t z = 0;   // 0 * x is NaN for what is not finite
+#pragma unroll 1
           for (int i = 0; i < D / 8; ++i) {
             const uint32_t at16 = v0 + (i >> 3) * (KB * 128) + (((i ^ r) & 7) << 4);
-            uint4 w = lds128(at16);
-            uint32_t x[4] = {w.x, w.y, w.z, w.w};
-            bool hit = past;
+            if (past) {
+              st_shared(at16, 0, 0, 0, 0);
+            } else {
+              const uint4 v = lds128(at16);
+              const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const bool lo = (x[k] & 0x7f80u) == 0x7f80u, hi = (x[k] & 0x7f800000u) == 0x7f800000u;
-              odd |= (lo || hi) && !past;
-              hit |= lo || hi;
-              if (past || lo) x[k] &= 0xffff0000u;
-              if (past || hi) x[k] &= 0x0000ffffu;
+              for (int k = 0; k < 4; ++k)
+                asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(z) : "r"(x[k]), "r"(0u));
             }
-            if (hit)
-              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at16), "r"(x[0]),
-                           "r"(x[1]), "r"(x[2]), "r"(x[3])
-                           : "memory");
           }
-          if (odd) s_odd[piece & 1] = piece + 1;
+          if ((z & 0x7fff7fffu) != 0) {   // hardly ever: take them out, add them at the end
+#pragma unroll 1
+            for (int i = 0; i < D / 8; ++i) {
+              const uint32_t at16 = v0 + (i >> 3) * (KB * 128) + (((i ^ r) & 7) << 4);
+              const uint4 v = lds128(at16);
+              uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                if ((x[k] & 0x7f80u) == 0x7f80u) x[k] &= 0xffff0000u;
+                if ((x[k] & 0x7f800000u) == 0x7f800000u) x[k] &= 0x0000ffffu;
+              }
+              st_shared(at16, x[0], x[1], x[2], x[3]);
+            }
+            s_odd[piece & 1] = piece + 1;
+          }
           fence_async();
+          __syncwarp();
         }
         // ---- weights, in place of the scores' first columns; the products with
         // the first half of V start while the second half is still here ----
@@ -493,84 +530,111 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const ChunkArgs a, const int 
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum[i] = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int c0 = 0; c0 < KB; c0 += 32) {
-          uint32_t w[16];
+        for (int x0 = 0; x0 < KB; x0 += 32) {
+          uint32_t pw[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int c = c0 + 2 * i;
-            float2 e = fma2(make_float2(s[c], s[c + 1]), f2, d2);
-            e.x = exp2_fast(e.x);
-            e.y = exp2_fast(e.y);
-            sum[i & 3] = add2(sum[i & 3], e);
+          for (int i = 0; i < 16; i += 2) {
+            const int x = x0 + 2 * i;
+            float2 e[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              e[k] = fma2(make_float2(s[x + 2 * k], s[x + 2 * k + 1]), f2, d2);
+              e[k].x = exp2_fast(e[k].x);
+              e[k].y = exp2_fast(e[k].y);
+              sum[(i + k) & 3] = add2(sum[(i + k) & 3], e[k]);
+            }
             if constexpr (Q8) {
-              e = mul2(e, *reinterpret_cast<const float2*>(sc + KB + c));
+              const float4 v4 = *reinterpret_cast<const float4*>(sc + KB + x);
+              e[0] = mul2(e[0], make_float2(v4.x, v4.y));
+              e[1] = mul2(e[1], make_float2(v4.z, v4.w));
               if (edge) {   // a key that is not read may have any scale
-                if (s[c] == -INFINITY) e.x = 0.f;
-                if (s[c + 1] == -INFINITY) e.y = 0.f;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  if (s[x + 2 * k] == -INFINITY) e[k].x = 0.f;
+                  if (s[x + 2 * k + 1] == -INFINITY) e[k].y = 0.f;
+                }
               }
-              w[i] = pack_f16x2(e.x, e.y);
+              pw[i] = pack_f16x2(e[0].x, e[0].y);
+              pw[i + 1] = pack_f16x2(e[1].x, e[1].y);
             } else {
-              w[i] = pack_bf16x2(e.x, e.y);
+              pw[i] = pack_bf16x2(e[0].x, e[0].y);
+              pw[i + 1] = pack_bf16x2(e[1].x, e[1].y);
             }
           }
-          tc_st16(tS + c0 / 2, w);
-          if (c0 == KB / 2 - 32 || c0 == KB - 32) {
+          // (the first half is announced late enough for its stores to have arrived)
+          if (x0 == KB / 2) {
             wait_st();
             tc_fence_before();
-            mbar_arrive(p_full(t, c0 >= KB / 2));
+            mbar_arrive(p_full(t, 0));
           }
+          tc_st16(tS + x0 / 2, pw);
         }
+        wait_st();
+        tc_fence_before();
+        mbar_arrive(p_full(t, 1));
         sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
         l += sum[0].x + sum[0].y;
       }
-      // ---- the piece's result ----
-      if (!gate.wait_warp(o_full(t), n_o & 1)) break;
+      // ---- the next piece's Q takes this one's place as soon as the products are
+      // through, so that its scores are formed while the result is written ----
+      const ChunkUnit done = u;
+      plan.next(u);
+      q_there = at < line_hi && has_rows(u);
+      bool through;
+      if (q_there) {
+        uint4 w[CH];
+        q_load(u, w);
+        through = gate.wait_warp(o_full(t), n_o & 1);
+        if (through) q_store(w);
+      } else {
+        through = gate.wait_warp(o_full(t), n_o & 1);
+      }
+      if (!through) break;
       ++n_o;
       tc_fence_after();
-      asm volatile("" ::: "memory");   // the unit's figures are looked up again, not kept through the loop
-      const auto u = plan.find(s_pre, begin);
-      const int row = u.tile * RT + t * GROUP_ROWS + r, q = row / G;
-      const bool real = q < u.rows;
-      const bool whole = kb0 == 0 && kb1 == u.n_blocks;
+      const bool whole = kb0 == 0 && kb1 == done.n_blocks;
       const bool odd = !Q8 && s_odd[piece & 1] == piece + 1;
       const float mul = whole ? (any ? 1.f / l : 0.f) : 1.f;
-      uint16_t* const out = a.O + ((int64_t)(u.row0 + q) * a.n_heads_q + u.head * G + row % G) * D;
-      const int64_t part_row =
-          (2 * (int64_t)blockIdx.x + (begin == line_lo ? 0 : 1)) * RT + t * GROUP_ROWS + r;
-#pragma unroll
-      for (int c = 0; c < D; c += 32) {
+      uint16_t* const out = a.O + ((int64_t)(done.row0 + q) * a.n_heads_q + done.head * G + row - q * G) * D;
+      const int64_t part_row = (2 * (int64_t)blockIdx.x + (first ? 0 : 1)) * RT + t * GROUP_ROWS + r;
+#pragma unroll 1
+      for (int x0 = 0; x0 < D; x0 += 32) {
         float o[32];
         __syncwarp();
-        tc_ld32(tO + c, o);
+        tc_ld32(tO + x0, o);
         wait_ld();
         if (odd && real) {
           // values that are not finite, of the keys this row reads in the blocks looked through
           const uint16_t* const vp = reinterpret_cast<const uint16_t*>(a.v);
           const int from = max(kb0, max(0, lim_first + 1) / KB) * KB;
           for (int key = from; key <= min(lim, kb1 * KB - 1); ++key) {
-            const int page = page_of(a.t, u.b, key);
+            const int page = page_of(a.t, done.b, key);
             if (page < 0) continue;
             const uint16_t* const x =
-                vp + pool_row(a.t, a.layer, a.n_heads_kv, page, u.head,
-                              (int)((uint32_t)key % (uint32_t)a.t.page_size)) * D + c;
+                vp + pool_row(a.t, a.layer, a.n_heads_kv, page, done.head,
+                              (int)((uint32_t)key % (uint32_t)a.t.page_size)) * D + x0;
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if ((x[i] & 0x7f80u) == 0x7f80u) o[i] += bf16_bits_to_f32(x[i]);
           }
         }
         if (real && whole) {
+          uint32_t b[16];
 #pragma unroll
-          for (int i = 0; i < 32; i += 8)
-            *reinterpret_cast<uint4*>(out + c + i) =
-                make_uint4(pack_bf16x2(o[i] * mul, o[i + 1] * mul),
-                           pack_bf16x2(o[i + 2] * mul, o[i + 3] * mul),
-                           pack_bf16x2(o[i + 4] * mul, o[i + 5] * mul),
-                           pack_bf16x2(o[i + 6] * mul, o[i + 7] * mul));
+          for (int i = 0; i < 16; ++i) b[i] = pack_bf16x2(o[2 * i] * mul, o[2 * i + 1] * mul);
+          if ((reinterpret_cast<uintptr_t>(a.O) & 31) == 0) {
+            st_global32(out + x0, b);
+            st_global32(out + x0 + 16, b + 8);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint4*>(out + x0 + 8 * i) =
+                  make_uint4(b[4 * i], b[4 * i + 1], b[4 * i + 2], b[4 * i + 3]);
+          }
         } else if (real) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            __stcg(reinterpret_cast<float4*>(a.part_o + part_row * D + c + i),
-                   make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]));
+          for (int i = 0; i < 32; i += 8)
+            st_global32(a.part_o + part_row * D + x0 + i, reinterpret_cast<const uint32_t*>(o + i));
         }
       }
       if (!whole && real)
@@ -598,19 +662,19 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const ChunkArgs a, const int 
         tc_commit(s_full(t));
       };
       for (int64_t at = line_lo; at < line_hi && ok;) {
-        const auto u = plan.find(s_pre, at);
         const int kb0 = (int)(at - u.begin), kb1 = (int)min((int64_t)u.n_blocks, line_hi - u.begin);
         at = u.begin + kb1;
         const int n = kb1 - kb0;
         const int groups = u.tile * RT + GROUP_ROWS < u.rows * G ? 2 : 1;
-        ok = gate.wait(kv_full(it % STAGES), (it / STAGES) & 1);
         for (int t = 0; t < groups && ok; ++t) {
           ok = gate.wait(q_full(t), n_q[t]++ & 1);
+          if (t == 0) ok = ok && gate.wait(kv_full(it % STAGES), (it / STAGES) & 1);
           tc_fence_after();
           if (ok) scores(t, it % STAGES);
         }
         if (!ok) break;
         tc_commit(kv_empty(it % STAGES));
+        plan.next(u);
         for (int i = 0; i < n && ok; ++i, it += 2) {
           const uint32_t vi = it + 1, ki = it + 2;
           for (int t = 0; t < groups && ok; ++t) {
@@ -628,17 +692,19 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const ChunkArgs a, const int 
             }
             if (!ok) break;
             ++n_p[t];
-            if (t == groups - 1) tc_commit(kv_empty(vi % STAGES));
             if (i + 1 < n) {
               if (t == 0) ok = gate.wait(kv_full(ki % STAGES), (ki / STAGES) & 1);
               if (!ok) break;
               tc_fence_after();
               scores(t, ki % STAGES);
-              if (t == groups - 1) tc_commit(kv_empty(ki % STAGES));
             } else {
               tc_commit(o_full(t));
             }
           }
+          if (!ok) break;
+          // stages are handed back together: each commit between products costs some cycles
+          tc_commit(kv_empty(vi % STAGES));
+          if (i + 1 < n) tc_commit(kv_empty(ki % STAGES));
         }
       }
     }
@@ -646,30 +712,29 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const ChunkArgs a, const int 
     // ------------------------------------------------------------ producers
     uint32_t it = 0;
     bool ok = true;
-    for (int64_t at = line_lo; at < line_hi && ok;) {
-      const auto u = plan.find(s_pre, at);
+    for (int64_t at = line_lo; at < line_hi && ok; plan.next(u)) {
       const int kb0 = (int)(at - u.begin), kb1 = (int)min((int64_t)u.n_blocks, line_hi - u.begin);
       at = u.begin + kb1;
       const int32_t* const pages = a.t.pages + (int64_t)u.b * a.t.width;
+      // pool row of a key, -1: none
+      auto row_of = [&](int key) {
+        if (key >= u.n_keys) return -1;
+        const int entry = a.by_page.quot(key), page = pages[entry];
+        if ((unsigned)page >= (unsigned)a.t.n_pages) return -1;
+        return (int)pool_row(a.t, a.layer, a.n_heads_kv, page, u.head, key - entry * a.t.page_size);
+      };
       if constexpr (!Q8) {
         // lanes 0..15 move K, 16..31 V: 64 columns (lane & 1) of the boxes (lane & 15) / 2, ..
         const int half = lane & 1, side = lane >> 4, b0 = (lane & 15) >> 1;
         const int n_box = KB / box;
+        int next = b0 < n_box ? row_of(kb0 * KB + b0 * box) : -1;
         for (int kb = kb0; kb < kb1 && ok; ++kb, it += 2) {
           // rows of the pool, one per box; past the pool (zeros) where there is no page
-          const int key = kb * KB + b0 * box;
-          int y = pool_rows;
-          bool here = false;
-          if (b0 < n_box && key < u.n_keys) {
-            const int page = pages[(uint32_t)key / (uint32_t)a.t.page_size];
-            here = (unsigned)page < (unsigned)a.t.n_pages;
-            if (here)
-              y = (int)pool_row(a.t, a.layer, a.n_heads_kv, page, u.head,
-                                (int)((uint32_t)key % (uint32_t)a.t.page_size));
-          }
+          const int key = kb * KB + b0 * box, y = next < 0 ? pool_rows : next;
           // 16-key parts without a page (those past the last key count as read past the end)
-          const unsigned gone = __ballot_sync(~0u, side == 0 && half == 0 && b0 < n_box && !here &&
+          const unsigned gone = __ballot_sync(~0u, side == 0 && half == 0 && b0 < n_box && next < 0 &&
                                                        key < u.n_keys);
+          next = kb + 1 < kb1 && b0 < n_box ? row_of(key + KB) : -1;   // a block ahead
 #pragma unroll
           for (int x = 0; x < 2; ++x) {   // K, then V
             const uint32_t item = it + x, st = item % STAGES;
@@ -679,8 +744,9 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const ChunkArgs a, const int 
             if (lane == 0) {
               if (x == 0) {
                 uint32_t miss = 0;
-                for (int b = 0; b < n_box; ++b)
-                  if ((gone >> (2 * b)) & 1u) miss |= ((1u << (box / 16)) - 1u) << (b * box / 16);
+                if (gone)
+                  for (int b = 0; b < n_box; ++b)
+                    if ((gone >> (2 * b)) & 1u) miss |= ((1u << (box / 16)) - 1u) << (b * box / 16);
                 s_miss[(item >> 1) & 7] = miss;
               }
               mbar_expect_tx(kv_full(st), C::STAGE);
@@ -692,92 +758,92 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const ChunkArgs a, const int 
           }
         }
       } else {
-        // CH lanes per key, 16 codes each; thread ptid looks up the pool row of key ptid
+        // CH lanes per key, 16 codes each; thread ptid looks up the pool row of key
+        // ptid.  Rows are looked up two blocks ahead of the conversion, codes and
+        // scales loaded one block ahead: no thread waits for what it has just asked for.
         constexpr int CH = D / 16, PASS = 128 / CH, N = KB / PASS;
         const int ptid = tid - 256, c = ptid % CH, k0 = ptid / CH;
-        uint4 w[N];
+        uint4 wk[N], wv[N];
+        float ksc = 0.f, vsc = 1.f;   // of key ptid of the next block
+        unsigned gone = 0;            // the warp's 32 keys: which stand on no page
         auto look_up = [&](int kb) {
-          const int key = kb * KB + ptid;
-          int row = -1;
-          if (key < u.n_keys) {
-            const int page = pages[(uint32_t)key / (uint32_t)a.t.page_size];
-            if ((unsigned)page < (unsigned)a.t.n_pages)
-              row = (int)pool_row(a.t, a.layer, a.n_heads_kv, page, u.head,
-                                  (int)((uint32_t)key % (uint32_t)a.t.page_size));
-          }
-          s_rows[kb & 1][ptid] = row;
-          return row;
+          if (kb < kb1) s_rows[(kb & 3) * KB + ptid] = row_of(kb * KB + ptid);
         };
-        auto load = [&](const void* pool, int kb) {
+        auto load = [&](const void* pool, uint4 (&w)[N], int kb) {
+          if (kb >= kb1) return;
           const uint8_t* const p = reinterpret_cast<const uint8_t*>(pool) + c * 16;
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            const int row = s_rows[kb & 1][i * PASS + k0];
+            const int row = s_rows[(kb & 3) * KB + i * PASS + k0];
             w[i] = row >= 0 ? ldg_nc_v4(p + (int64_t)row * D)
                             : make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
           }
         };
+        auto load_scales = [&](int kb) {
+          if (kb >= kb1) return;
+          const int row = s_rows[(kb & 3) * KB + ptid];
+          gone = __ballot_sync(~0u, row < 0 && kb * KB + ptid < u.n_keys);
+          ksc = row >= 0 ? a.ks[row] : 0.f;
+          vsc = row >= 0 ? a.vs[row] : 1.f;
+        };
+        auto put = [&](const uint4 (&w)[N], uint32_t dst) {
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const int key = i * PASS + k0;
+            const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            uint32_t h[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              h[2 * k] = codes2(v[k], 0x4140u);
+              h[2 * k + 1] = codes2(v[k], 0x4342u);
+            }
+            // 16 values are chunks 2 c, 2 c + 1 of the row; lanes of the second half of the
+            // row store theirs in the other order, so that eight lanes meet all banks
+            const uint32_t line = dst + (c >> 2) * (KB * 128) + key * 128;
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const int z = y ^ ((c >> 2) & 1);
+              st_shared(line + ((((c & 3) * 2 + z) ^ (key & 7)) << 4), z ? h[4] : h[0],
+                        z ? h[5] : h[1], z ? h[6] : h[2], z ? h[7] : h[3]);
+            }
+          }
+        };
         auto meet = [] { asm volatile("bar.sync 3, 128;" ::: "memory"); };
-        int row = look_up(kb0), next = -1;
+        meet();            // the piece before has read its rows
+        look_up(kb0);
+        look_up(kb0 + 1);
         meet();
-        load(a.k, kb0);
+        load(a.k, wk, kb0);
+        load(a.v, wv, kb0);
+        load_scales(kb0);
         // no thread leaves this loop early (they meet in it): after a wait ran out
         // they only go on writing to their own shared memory
-        for (int kb = kb0; kb < kb1; ++kb, it += 2, row = next) {
-          float ksc = 0.f, vsc = 1.f;
-          if (row >= 0) {
-            ksc = a.ks[row];
-            vsc = a.vs[row];
+        for (int kb = kb0; kb < kb1; ++kb, it += 2) {
+          look_up(kb + 2);
+          const uint32_t sk = it % STAGES, sv = (it + 1) % STAGES;
+          if (it >= STAGES) gate.wait(kv_empty(sk), ((it / STAGES) - 1) & 1);
+          float* const sc = s_scale + ((it >> 1) & 3) * C::SCALE_SLOT;
+          sc[ptid] = ksc;
+          sc[KB + ptid] = vsc;
+          // (at least 2^-80: the sums of weights stay in range)
+          const float big = warp_max(ksc != 0.f ? fmaxf(log2f(vsc), -80.f) : -80.f);
+          if (lane == 0) {
+            sc[2 * KB + warp - 8] = big;
+            // 16-key parts: bits 0 and 16 of the warp's 32 keys
+            reinterpret_cast<volatile uint8_t*>(s_miss + ((it >> 1) & 7))[warp - 8] =
+                (uint8_t)((gone & 1u) | ((gone >> 16) & 1u) << 1);
           }
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const uint32_t item = it + x, st = item % STAGES;
-            if (x == 0) next = kb + 1 < kb1 ? look_up(kb + 1) : -1;
-            if (item >= STAGES) gate.wait(kv_empty(st), ((item / STAGES) - 1) & 1);
-            if (x == 0) {
-              float* const sc = s_scale + ((item >> 1) & 3) * C::SCALE_SLOT;
-              sc[ptid] = ksc;
-              sc[KB + ptid] = vsc;
-              // (at least 2^-80: the sums of weights stay in range)
-              const float big = warp_max(row >= 0 ? fmaxf(log2f(vsc), -80.f) : -80.f);
-              if (lane == 0) sc[2 * KB + warp - 8] = big;
-              const unsigned gone = __ballot_sync(~0u, row < 0 && kb * KB + ptid < u.n_keys);
-              // 16-key parts: bits 0 and 16 of the warp's 32 keys
-              if (lane == 0)
-                reinterpret_cast<volatile uint8_t*>(s_miss + ((item >> 1) & 7))[warp - 8] =
-                    (uint8_t)((gone & 1u) | ((gone >> 16) & 1u) << 1);
-            }
-            const uint32_t dst = ring_s + st * C::STAGE;
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-              const int key = i * PASS + k0;
-              const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-              uint32_t h[8];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                h[2 * k] = codes2(v[k], 0x4140u);
-                h[2 * k + 1] = codes2(v[k], 0x4342u);
-              }
-              // 16 values are chunks 2 c, 2 c + 1 of the row; lanes of the second half of the
-              // row store theirs in the other order, so that eight lanes meet all banks
-              const uint32_t line = dst + (c >> 2) * (KB * 128) + key * 128;
-#pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                const int z = y ^ ((c >> 2) & 1);
-                const uint32_t p = line + ((((c & 3) * 2 + z) ^ (key & 7)) << 4);
-                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(p),
-                             "r"(z ? h[4] : h[0]), "r"(z ? h[5] : h[1]), "r"(z ? h[6] : h[2]),
-                             "r"(z ? h[7] : h[3])
-                             : "memory");
-              }
-            }
-            // the next item's codes are on their way while this one is used
-            if (x == 0) load(a.v, kb);
-            meet();
-            if (x == 1 && kb + 1 < kb1) load(a.k, kb + 1);
-            fence_async();
-            mbar_arrive(kv_full(st));
-          }
+          put(wk, ring_s + sk * C::STAGE);
+          fence_async();
+          mbar_arrive(kv_full(sk));
+          load(a.k, wk, kb + 1);
+          load_scales(kb + 1);
+          if (it + 1 >= STAGES) gate.wait(kv_empty(sv), (((it + 1) / STAGES) - 1) & 1);
+          put(wv, ring_s + sv * C::STAGE);
+          fence_async();
+          mbar_arrive(kv_full(sv));
+          load(a.v, wv, kb + 1);
+          meet();          // the rows of block kb + 2 are there
         }
       }
     }

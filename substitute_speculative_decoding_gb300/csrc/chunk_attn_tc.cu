@@ -199,6 +199,11 @@ __device__ __forceinline__ uint32_t codes2(uint32_t w, uint32_t sel) {
       : "r"(__byte_perm(w, 0x64646464u, sel)), "r"(0x64806480u));
   return r;
 }
+__device__ __forceinline__ bool elect_one() {   // by a whole warp: one lane
+  uint32_t x;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(x));
+  return x != 0;
+}
 __device__ __forceinline__ void fence_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -644,67 +649,87 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
       if (*s_dead) break;
     }
   } else if (warp >= 8 + (Q8 ? 4 : 0) && warp != 8) {
-    if (warp == C::MMA_WARP && lane == 0) {
+    if (warp == C::MMA_WARP) {
       // -------------------------------------------------------- MMA issuer
+      // The whole warp walks through this, with values that the compiler can see to be
+      // the same in all lanes, and elects the lane that issues: descriptors then stay in
+      // uniform registers (an issue from a lane of its own choice has to move them
+      // there each time, which took longer than the product).
       constexpr uint32_t id_s = idesc(KB, !Q8, false), id_o = idesc(D, !Q8, true);
+      const uint32_t tm = __shfl_sync(~0u, tmem, 0);
       uint32_t it = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
       bool ok = true;
       // descriptors of the first step; a step further is a constant in the address field
-      const uint64_t q_desc[2] = {desc_k(q_s), desc_k(q_s + C::Q_BYTES)};
-      const uint64_t k_desc = desc_k(ring_s), v_desc = desc_mn(ring_s);
-      auto scores = [&](int t, uint32_t stage) {
-        const uint64_t qd = q_desc[t], kd = k_desc + stage * (C::STAGE >> 4);
+      const uint64_t q_desc = desc_k(q_s), k_desc = desc_k(ring_s), v_desc = desc_mn(ring_s);
+      auto full = [&](uint32_t item) { return gate.wait_warp(kv_full(item % STAGES), (item / STAGES) & 1); };
+      auto scores = [&](int t, uint32_t item) {
+        if (elect_one()) {
+          const uint64_t qd = q_desc + t * (C::Q_BYTES >> 4), kd = k_desc + (item % STAGES) * (C::STAGE >> 4);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = ((k >> 2) * (KB * 128) + (k & 3) * 32) >> 4;
-          mma_ss(tmem + t * 128, qd + off, kd + off, id_s, k > 0);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = ((k >> 2) * (KB * 128) + (k & 3) * 32) >> 4;
+            mma_ss(tm + t * 128, qd + off, kd + off, id_s, k > 0);
+          }
+          tc_commit(s_full(t));
         }
-        tc_commit(s_full(t));
+        __syncwarp();
       };
-      for (int64_t at = line_lo; at < line_hi && ok;) {
+      // half h of a block's weights times half of V
+      auto output = [&](int t, uint32_t item, int h, bool add) {
+        if (elect_one()) {
+          const uint64_t vd = v_desc + (item % STAGES) * (C::STAGE >> 4);
+#pragma unroll
+          for (int k = 0; k < KB / 32; ++k) {
+            const int kk = h * (KB / 32) + k;
+            mma_ts(tm + 256 + t * 128, tm + t * 128 + kk * 8, vd + kk * (2048 >> 4), id_o,
+                   add || k > 0);
+          }
+        }
+        __syncwarp();
+      };
+      auto commit = [&](uint32_t bar) {
+        if (elect_one()) tc_commit(bar);
+        __syncwarp();
+      };
+      for (int64_t at = line_lo; at < line_hi && ok; plan.next(u)) {
         const int kb0 = (int)(at - u.begin), kb1 = (int)min((int64_t)u.n_blocks, line_hi - u.begin);
         at = u.begin + kb1;
-        const int n = kb1 - kb0;
-        const int groups = u.tile * RT + GROUP_ROWS < u.rows * G ? 2 : 1;
+        const int n = __shfl_sync(~0u, kb1 - kb0, 0);
+        const int groups = __shfl_sync(~0u, u.tile * RT + GROUP_ROWS < u.rows * G ? 2 : 1, 0);
         for (int t = 0; t < groups && ok; ++t) {
-          ok = gate.wait(q_full(t), n_q[t]++ & 1);
-          if (t == 0) ok = ok && gate.wait(kv_full(it % STAGES), (it / STAGES) & 1);
+          ok = gate.wait_warp(q_full(t), n_q[t]++ & 1);
+          if (t == 0) ok = ok && full(it);
           tc_fence_after();
-          if (ok) scores(t, it % STAGES);
+          if (ok) scores(t, it);
         }
         if (!ok) break;
-        tc_commit(kv_empty(it % STAGES));
-        plan.next(u);
+        commit(kv_empty(it % STAGES));
         for (int i = 0; i < n && ok; ++i, it += 2) {
           const uint32_t vi = it + 1, ki = it + 2;
-          for (int t = 0; t < groups && ok; ++t) {
-            if (t == 0) ok = gate.wait(kv_full(vi % STAGES), (vi / STAGES) & 1);
-            const uint64_t vd = v_desc + (vi % STAGES) * (C::STAGE >> 4);
+          ok = full(vi);
 #pragma unroll
-            for (int k = 0; k < KB / 16; ++k) {
-              if (k % (KB / 32) == 0) {   // half of the weights
-                ok = ok && gate.wait(p_full(t, k >= KB / 32), n_p[t] & 1);
-                if (!ok) break;
-                tc_fence_after();
-              }
-              mma_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8, vd + k * (2048 >> 4), id_o,
-                     i > 0 || k > 0);
-            }
+          for (int t = 0; t < 2; ++t) {
+            if (t == groups || !ok) break;
+            ok = gate.wait_warp(p_full(t, 0), n_p[t] & 1);
             if (!ok) break;
+            tc_fence_after();
+            output(t, vi, 0, i > 0);
+            ok = gate.wait_warp(p_full(t, 1), n_p[t] & 1);
+            if (!ok) break;
+            tc_fence_after();
+            output(t, vi, 1, true);
             ++n_p[t];
             if (i + 1 < n) {
-              if (t == 0) ok = gate.wait(kv_full(ki % STAGES), (ki / STAGES) & 1);
+              if (t == 0) ok = full(ki);
               if (!ok) break;
-              tc_fence_after();
-              scores(t, ki % STAGES);
+              scores(t, ki);
             } else {
-              tc_commit(o_full(t));
+              commit(o_full(t));
             }
           }
           if (!ok) break;
-          // stages are handed back together: each commit between products costs some cycles
-          tc_commit(kv_empty(vi % STAGES));
-          if (i + 1 < n) tc_commit(kv_empty(ki % STAGES));
+          commit(kv_empty(vi % STAGES));
+          if (i + 1 < n) commit(kv_empty(ki % STAGES));
         }
       }
     }

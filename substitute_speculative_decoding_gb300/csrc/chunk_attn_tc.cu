@@ -552,13 +552,6 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
               const float4 v4 = *reinterpret_cast<const float4*>(sc + KB + x);
               e[0] = mul2(e[0], make_float2(v4.x, v4.y));
               e[1] = mul2(e[1], make_float2(v4.z, v4.w));
-              if (edge) {   // a key that is not read may have any scale
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  if (s[x + 2 * k] == -INFINITY) e[k].x = 0.f;
-                  if (s[x + 2 * k + 1] == -INFINITY) e[k].y = 0.f;
-                }
-              }
               pw[i] = pack_f16x2(e[0].x, e[0].y);
               pw[i + 1] = pack_f16x2(e[1].x, e[1].y);
             } else {
@@ -810,6 +803,11 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
           gone = __ballot_sync(~0u, row < 0 && kb * KB + ptid < u.n_keys);
           ksc = row >= 0 ? a.ks[row] : 0.f;
           vsc = row >= 0 ? a.vs[row] : 1.f;
+          // a row that reads this key gets NaN by its score; weight 0 times it stays 0
+          if (!(vsc < INFINITY)) {
+            ksc = __int_as_float(0x7fc00000);
+            vsc = 1.f;
+          }
         };
         auto put = [&](const uint4 (&w)[N], uint32_t dst) {
 #pragma unroll

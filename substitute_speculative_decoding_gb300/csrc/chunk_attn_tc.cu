@@ -9,8 +9,8 @@
 //   warps 0-3, 4-7   softmax of rows 0-127 and 128-255, one row per thread (a
 //                    row's maximum and sum need no exchange between threads),
 //                    the Q tile's way into shared memory, and the results
-//   a producer       K and V blocks of 128 keys, one after the other, into a
-//                    ring: a TMA warp for a bf16 cache (boxes of as many keys
+//   a producer       blocks of 128 keys into a ring, V of one beside K of the next
+//                    (they are used together): a TMA warp for a bf16 cache (boxes of as many keys
 //                    as a page holds together), or four warps that turn 8-bit
 //                    codes into fp16 code - 128 on the way
 //   one MMA thread   S = Q K^T into tensor memory; then, once the group's weights
@@ -54,8 +54,9 @@ __device__ unsigned int g_chunk_timeouts;   // waits that ran out (never expecte
 
 template <int D, bool Q8>
 struct Cfg {
-  static constexpr int STAGE = KB * D * 2;               // K or V of a block, 16-bit values
-  static constexpr int STAGES = D == 64 ? 6 : Q8 ? 4 : 5;
+  static constexpr int HALF = KB * D * 2;                // K or V of a block, 16-bit values
+  static constexpr int SLOT = 2 * HALF;                  // V of a block, K of the next
+  static constexpr int SLOTS = D == 64 ? 3 : 2;         // (at most 3: four blocks' scales are kept)
   static constexpr int Q_BYTES = GROUP_ROWS * D * 2;     // of one group
   static constexpr int MMA_WARP = 8 + (Q8 ? 4 : 1);
   static constexpr int THREADS = Q8 ? 512 : 384;         // whole groups of four warps
@@ -74,9 +75,9 @@ struct Cfg {
   static constexpr int ROWS = Q8 ? 4 * KB * 4 : 0;       // pool rows of four blocks' keys
   static constexpr int TAIL = 256;                       // barriers, flags, TMEM address
   static constexpr int SMEM =
-      1024 + 2 * Q_BYTES + STAGES * STAGE + SCALES + QSCALES + ROWS + TAIL;
+      1024 + 2 * Q_BYTES + SLOTS * SLOT + SCALES + QSCALES + ROWS + TAIL;
   static_assert(SMEM <= 227 * 1024, "one CTA's shared memory");
-  static_assert(STAGES * STAGE >= (SUB_MAX_SEQS + 1) * 8, "the ring holds the running sums first");
+  static_assert(SLOTS * SLOT >= (SUB_MAX_SEQS + 1) * 8, "the ring holds the running sums first");
 };
 
 // ---------------------------------------------------------------- tcgen05 --
@@ -213,6 +214,7 @@ __device__ __forceinline__ void fence_async() {
 struct Gate {
   volatile int* dead;
   __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) const {
+    if (mbar_try_wait(bar, parity)) return true;
     for (uint32_t i = 0; i < (1u << 20); ++i) {
       if (mbar_try_wait(bar, parity)) return true;
       if ((i & 63) == 63 && *dead) return false;
@@ -265,30 +267,30 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::THREADS, 1)
 chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ChunkArgs a, const int box,
                 const int pool_rows) {
   using C = Cfg<D, Q8>;
-  constexpr int STAGES = C::STAGES;
+  constexpr int SLOTS = C::SLOTS;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* const base_p = smem_raw + (base - smem_u32(smem_raw));
   const uint32_t q_s = base, ring_s = base + 2 * C::Q_BYTES;
   int64_t* const s_pre = reinterpret_cast<int64_t*>(base_p + 2 * C::Q_BYTES);   // until the first copies
-  uint8_t* const after = base_p + 2 * C::Q_BYTES + STAGES * C::STAGE;
+  uint8_t* const after = base_p + 2 * C::Q_BYTES + SLOTS * C::SLOT;
   float* const s_scale = reinterpret_cast<float*>(after);                   // [4][SCALE_SLOT]
   float* const s_qs = reinterpret_cast<float*>(after + C::SCALES);          // [RT]
   int* const s_rows = reinterpret_cast<int*>(after + C::SCALES + C::QSCALES);   // [4][KB]
   uint8_t* const tail = after + C::SCALES + C::QSCALES + C::ROWS;
   const uint32_t bars = smem_u32(tail);
-  auto kv_full = [&](int s) { return bars + 8u * s; };
-  auto kv_empty = [&](int s) { return bars + 8u * (STAGES + s); };
-  auto q_full = [&](int t) { return bars + 8u * (2 * STAGES + t); };
-  auto s_full = [&](int t) { return bars + 8u * (2 * STAGES + 2 + t); };
-  auto p_full = [&](int t, int h) { return bars + 8u * (2 * STAGES + 4 + 2 * h + t); };
-  auto o_full = [&](int t) { return bars + 8u * (2 * STAGES + 8 + t); };
-  int* const flags = reinterpret_cast<int*>(tail + 8 * (2 * STAGES + 10));
+  auto kv_full = [&](uint32_t block) { return bars + 8u * (block % SLOTS); };
+  auto kv_empty = [&](uint32_t block) { return bars + 8u * (SLOTS + block % SLOTS); };
+  auto q_full = [&](int t) { return bars + 8u * (2 * SLOTS + t); };
+  auto s_full = [&](int t) { return bars + 8u * (2 * SLOTS + 2 + t); };
+  auto p_full = [&](int t) { return bars + 8u * (2 * SLOTS + 4 + t); };
+  auto o_full = [&](int t) { return bars + 8u * (2 * SLOTS + 6 + t); };
+  int* const flags = reinterpret_cast<int*>(tail + 8 * (2 * SLOTS + 8));
   volatile int* const s_dead = flags;            // a wait ran out
   volatile int* const s_odd = flags + 1;         // [2] piece (by parity) that met infinite values or NaN
   volatile uint32_t* const s_miss = reinterpret_cast<uint32_t*>(flags + 3);   // [8] blocks' missing 16-key parts
   uint32_t* const s_tmem = reinterpret_cast<uint32_t*>(flags + 11);
-  static_assert(8 * (2 * STAGES + 10) + 12 * 4 <= C::TAIL, "tail");
+  static_assert(8 * (2 * SLOTS + 8) + 12 * 4 <= C::TAIL, "tail");
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (warp == 0) {
@@ -299,15 +301,14 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (tid == 32) {
-    for (int s = 0; s < STAGES; ++s) {
-      mbar_init(kv_full(s), Q8 ? 128 : 1);
+    for (int s = 0; s < SLOTS; ++s) {
+      mbar_init(kv_full(s), Q8 ? 4 : 1);
       mbar_init(kv_empty(s), 1);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(q_full(t), GROUP_ROWS);
+      mbar_init(q_full(t), 4);   // one arrival for each warp of the group
       mbar_init(s_full(t), 1);
-      mbar_init(p_full(t, 0), GROUP_ROWS);
-      mbar_init(p_full(t, 1), GROUP_ROWS);
+      mbar_init(p_full(t), 4);
       mbar_init(o_full(t), 1);
     }
     *s_dead = 0;
@@ -344,7 +345,7 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + t * 128 + lanes, tO = tmem + 256 + t * 128 + lanes;
     uint32_t n_s = 0, n_o = 0;      // blocks and pieces seen by this group
-    uint32_t items = 0;             // ring items before this piece
+    uint32_t block = 0;             // of this CTA's part of the line
     constexpr int CH = D / 8, RP = 32 / CH;   // 16-byte chunks of a Q row, rows per pass of a warp
     const int c = lane % CH;
 
@@ -389,8 +390,8 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
         st_shared(dst0 + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), w[i].x, w[i].y, w[i].z, w[i].w);
       }
       fence_async();
-      mbar_arrive(q_full(t));
-      __syncwarp();   // s_qs
+      __syncwarp();   // (s_qs, too)
+      if (lane == 0) mbar_arrive(q_full(t));
     };
     if (tid == 0 && line_lo >= line_hi) a.cuts[blockIdx.x].pieces = 0;
     bool q_there = false;   // this piece's Q is in shared memory already
@@ -401,7 +402,7 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
       at = u.begin + kb1;
       if (tid == 0 && at >= line_hi) a.cuts[blockIdx.x] = make_cut(u, kb1, line_lo, per);
       if (!has_rows(u)) {   // an empty second group
-        items += 2 * (kb1 - kb0);
+        block += kb1 - kb0;
         plan.next(u);
         continue;
       }
@@ -420,7 +421,7 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
 
       float ref = 0.f, l = 0.f;    // weights are 2^(score - ref)
       bool any = false;            // a key has been read
-      for (int kb = kb0; kb < kb1; ++kb, items += 2) {
+      for (int kb = kb0; kb < kb1; ++kb, ++block) {
         const int key0 = kb * KB;
         if (!gate.wait_warp(s_full(t), n_s & 1)) break;
         ++n_s;
@@ -428,10 +429,10 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
         float s[KB];
 #pragma unroll
         for (int x = 0; x < KB; x += 32) tc_ld32(tS + x, s + x);
-        const uint32_t miss = s_miss[(items >> 1) & 7];
+        const uint32_t miss = s_miss[block & 7];
         const bool behind = key0 + KB - 1 > lim_first;   // the same for all rows of the tile
         const bool edge = behind || miss;
-        const float* const sc = s_scale + ((items >> 1) & 3) * C::SCALE_SLOT;
+        const float* const sc = s_scale + (block & 3) * C::SCALE_SLOT;
         wait_ld();
         if constexpr (Q8) {
 #pragma unroll
@@ -491,9 +492,8 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
         }
         if (!Q8 && behind && t == 0) {
           // V of the block: row r of it is this thread's
-          const uint32_t st = (items + 1) % STAGES;
-          if (!gate.wait_warp(kv_full(st), ((items + 1) / STAGES) & 1)) break;
-          const uint32_t v0 = ring_s + st * C::STAGE + r * 128;
+          if (!gate.wait_warp(kv_full(block + 1), ((block + 1) / SLOTS) & 1)) break;
+          const uint32_t v0 = ring_s + (block + 1) % SLOTS * C::SLOT + r * 128;
           const bool past = key0 + r >= n_keys;
           uint32_t z = 0;   // 0 * x is NaN for what is not finite
 #pragma unroll 1
@@ -527,8 +527,7 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
           fence_async();
           __syncwarp();
         }
-        // ---- weights, in place of the scores' first columns; the products with
-        // the first half of V start while the second half is still here ----
+        // ---- weights, in place of the scores' first columns ----
         const float shift = Q8 ? Q8_SHIFT - ref : -ref;
         const float2 f2 = make_float2(factor, factor), d2 = make_float2(shift, shift);
         float2 sum[4];
@@ -559,17 +558,12 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
               pw[i + 1] = pack_bf16x2(e[1].x, e[1].y);
             }
           }
-          // (the first half is announced late enough for its stores to have arrived)
-          if (x0 == KB / 2) {
-            wait_st();
-            tc_fence_before();
-            mbar_arrive(p_full(t, 0));
-          }
           tc_st16(tS + x0 / 2, pw);
         }
         wait_st();
         tc_fence_before();
-        mbar_arrive(p_full(t, 1));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(t));
         sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
         l += sum[0].x + sum[0].y;
       }
@@ -650,14 +644,13 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
       // there each time, which took longer than the product).
       constexpr uint32_t id_s = idesc(KB, !Q8, false), id_o = idesc(D, !Q8, true);
       const uint32_t tm = __shfl_sync(~0u, tmem, 0);
-      uint32_t it = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
-      bool ok = true;
+      uint32_t block = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
       // descriptors of the first step; a step further is a constant in the address field
-      const uint64_t q_desc = desc_k(q_s), k_desc = desc_k(ring_s), v_desc = desc_mn(ring_s);
-      auto full = [&](uint32_t item) { return gate.wait_warp(kv_full(item % STAGES), (item / STAGES) & 1); };
-      auto scores = [&](int t, uint32_t item) {
+      const uint64_t q_desc = desc_k(q_s), v_desc = desc_mn(ring_s), k_desc = desc_k(ring_s + C::HALF);
+      auto full = [&](uint32_t b) { return gate.wait_warp(kv_full(b), (b / SLOTS) & 1); };
+      auto scores = [&](int t, uint32_t b) {
         if (elect_one()) {
-          const uint64_t qd = q_desc + t * (C::Q_BYTES >> 4), kd = k_desc + (item % STAGES) * (C::STAGE >> 4);
+          const uint64_t qd = q_desc + t * (C::Q_BYTES >> 4), kd = k_desc + b % SLOTS * (C::SLOT >> 4);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const uint32_t off = ((k >> 2) * (KB * 128) + (k & 3) * 32) >> 4;
@@ -667,16 +660,12 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
         }
         __syncwarp();
       };
-      // half h of a block's weights times half of V
-      auto output = [&](int t, uint32_t item, int h, bool add) {
+      auto output = [&](int t, uint32_t b, bool add) {   // V of block b lies beside K of the next
         if (elect_one()) {
-          const uint64_t vd = v_desc + (item % STAGES) * (C::STAGE >> 4);
+          const uint64_t vd = v_desc + (b + 1) % SLOTS * (C::SLOT >> 4);
 #pragma unroll
-          for (int k = 0; k < KB / 32; ++k) {
-            const int kk = h * (KB / 32) + k;
-            mma_ts(tm + 256 + t * 128, tm + t * 128 + kk * 8, vd + kk * (2048 >> 4), id_o,
-                   add || k > 0);
-          }
+          for (int k = 0; k < KB / 16; ++k)
+            mma_ts(tm + 256 + t * 128, tm + t * 128 + k * 8, vd + k * (2048 >> 4), id_o, add || k > 0);
         }
         __syncwarp();
       };
@@ -684,6 +673,7 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
         if (elect_one()) tc_commit(bar);
         __syncwarp();
       };
+      bool ok = line_lo < line_hi && full(0);
       for (int64_t at = line_lo; at < line_hi && ok; plan.next(u)) {
         const int kb0 = (int)(at - u.begin), kb1 = (int)min((int64_t)u.n_blocks, line_hi - u.begin);
         at = u.begin + kb1;
@@ -691,161 +681,151 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
         const int groups = __shfl_sync(~0u, u.tile * RT + GROUP_ROWS < u.rows * G ? 2 : 1, 0);
         for (int t = 0; t < groups && ok; ++t) {
           ok = gate.wait_warp(q_full(t), n_q[t]++ & 1);
-          if (t == 0) ok = ok && full(it);
-          tc_fence_after();
-          if (ok) scores(t, it);
+          if (ok) scores(t, block);
         }
         if (!ok) break;
-        commit(kv_empty(it % STAGES));
-        for (int i = 0; i < n && ok; ++i, it += 2) {
-          const uint32_t vi = it + 1, ki = it + 2;
-          ok = full(vi);
+        commit(kv_empty(block));
+        for (int i = 0; i < n && ok; ++i, ++block) {
+          ok = full(block + 1);
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (t == groups || !ok) break;
-            ok = gate.wait_warp(p_full(t, 0), n_p[t] & 1);
+            ok = gate.wait_warp(p_full(t), n_p[t]++ & 1);
             if (!ok) break;
             tc_fence_after();
-            output(t, vi, 0, i > 0);
-            ok = gate.wait_warp(p_full(t, 1), n_p[t] & 1);
-            if (!ok) break;
-            tc_fence_after();
-            output(t, vi, 1, true);
-            ++n_p[t];
-            if (i + 1 < n) {
-              if (t == 0) ok = full(ki);
-              if (!ok) break;
-              scores(t, ki);
-            } else {
-              commit(o_full(t));
-            }
+            output(t, block, i > 0);
+            if (i + 1 < n) scores(t, block + 1);
+            else commit(o_full(t));
           }
-          if (!ok) break;
-          commit(kv_empty(vi % STAGES));
-          if (i + 1 < n) commit(kv_empty(ki % STAGES));
+          if (ok && i + 1 < n) commit(kv_empty(block + 1));
         }
       }
     }
   } else {
     // ------------------------------------------------------------ producers
-    uint32_t it = 0;
+    // Slot j of the ring holds V of block j - 1 and K of block j, across the units;
+    // the first has no V, the last no K.
+    const uint32_t n = (uint32_t)(line_hi > line_lo ? line_hi - line_lo : 0);
     bool ok = true;
-    for (int64_t at = line_lo; at < line_hi && ok; plan.next(u)) {
-      const int kb0 = (int)(at - u.begin), kb1 = (int)min((int64_t)u.n_blocks, line_hi - u.begin);
-      at = u.begin + kb1;
-      const int32_t* const pages = a.t.pages + (int64_t)u.b * a.t.width;
-      // pool row of a key, -1: none
-      auto row_of = [&](int key) {
-        if (key >= u.n_keys) return -1;
-        const int entry = a.by_page.quot(key), page = pages[entry];
-        if ((unsigned)page >= (unsigned)a.t.n_pages) return -1;
-        return (int)pool_row(a.t, a.layer, a.n_heads_kv, page, u.head, key - entry * a.t.page_size);
+    int kb = (int)(line_lo - u.begin);   // the next block to look up, of unit u
+    // pool row of key x of that block; -1: past the last key, -2: on no page
+    auto row_of = [&](int x) {
+      const int key = kb * KB + x;
+      if (key >= u.n_keys) return -1;
+      const int entry = a.by_page.quot(key), page = a.t.pages[(int64_t)u.b * a.t.width + entry];
+      if ((unsigned)page >= (unsigned)a.t.n_pages) return -2;
+      return (int)pool_row(a.t, a.layer, a.n_heads_kv, page, u.head, key - entry * a.t.page_size);
+    };
+    auto step = [&] {
+      if (++kb == u.n_blocks) {
+        plan.next(u);
+        kb = 0;
+      }
+    };
+    if constexpr (!Q8) {
+      // lanes 0..15 move K, 16..31 V: 64 columns (lane & 1) of the boxes (lane & 15) / 2, ..
+      const int half = lane & 1, side = lane >> 4, b0 = (lane & 15) >> 1;
+      const int n_box = KB / box;
+      const bool mine = b0 < n_box && half < D / 64;
+      int row = n > 0 && b0 < n_box ? row_of(b0 * box) : -1, before = -1;
+      for (uint32_t j = 0; j <= n && n > 0; ++j) {
+        // 16-key parts without a page (those past the last key count as read past the end)
+        const unsigned gone = __ballot_sync(~0u, side == 0 && half == 0 && row == -2);
+        // rows of the pool, one per box; past the pool (zeros) where there is no page
+        const int y = side ? before : row;
+        before = row;
+        if (j + 1 < n) {   // a block ahead
+          step();
+          row = b0 < n_box ? row_of(b0 * box) : -1;
+        }
+        if (j >= SLOTS) ok = gate.wait_warp(kv_empty(j), ((j / SLOTS) - 1) & 1);
+        if (!ok) break;
+        if (lane == 0) {
+          uint32_t miss = 0;
+          if (gone)
+            for (int b = 0; b < n_box; ++b)
+              if ((gone >> (2 * b)) & 1u) miss |= ((1u << (box / 16)) - 1u) << (b * box / 16);
+          if (j < n) s_miss[j & 7] = miss;
+          mbar_expect_tx(kv_full(j), (j > 0 ? C::HALF : 0) + (j < n ? C::HALF : 0));
+        }
+        __syncwarp();
+        if (mine && (side ? j > 0 : j < n))
+          tma_load_2d(ring_s + j % SLOTS * C::SLOT + (side ? 0 : C::HALF) + half * (KB * 128) +
+                          b0 * box * 128,
+                      side ? &maps.v : &maps.k, half * 64, y < 0 ? pool_rows : y, kv_full(j));
+      }
+    } else {
+      // CH lanes per key, 16 codes each; thread ptid looks up the pool row of key
+      // ptid.  Rows are looked up two blocks ahead of the conversion, codes and
+      // scales loaded one block ahead: no thread waits for what it has just asked for.
+      constexpr int CH = D / 16, PASS = 128 / CH, N = KB / PASS;
+      const int ptid = tid - 256, c = ptid % CH, k0 = ptid / CH;
+      uint4 wk[N], wv[N];
+      float ksc = 0.f, vsc = 1.f;   // of key ptid of the next block
+      unsigned gone = 0;            // the warp's 32 keys: which stand on no page
+      auto look_up = [&](uint32_t j) {   // called for j = 0, 1, ..
+        if (j >= n) return;
+        if (j > 0) step();
+        s_rows[(j & 3) * KB + ptid] = row_of(ptid);
       };
-      if constexpr (!Q8) {
-        // lanes 0..15 move K, 16..31 V: 64 columns (lane & 1) of the boxes (lane & 15) / 2, ..
-        const int half = lane & 1, side = lane >> 4, b0 = (lane & 15) >> 1;
-        const int n_box = KB / box;
-        int next = b0 < n_box ? row_of(kb0 * KB + b0 * box) : -1;
-        for (int kb = kb0; kb < kb1 && ok; ++kb, it += 2) {
-          // rows of the pool, one per box; past the pool (zeros) where there is no page
-          const int key = kb * KB + b0 * box, y = next < 0 ? pool_rows : next;
-          // 16-key parts without a page (those past the last key count as read past the end)
-          const unsigned gone = __ballot_sync(~0u, side == 0 && half == 0 && b0 < n_box && next < 0 &&
-                                                       key < u.n_keys);
-          next = kb + 1 < kb1 && b0 < n_box ? row_of(key + KB) : -1;   // a block ahead
+      auto load = [&](const void* pool, uint4 (&w)[N], uint32_t j) {
+        const uint8_t* const p = reinterpret_cast<const uint8_t*>(pool) + c * 16;
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {   // K, then V
-            const uint32_t item = it + x, st = item % STAGES;
-            if (item >= STAGES) ok = ok && gate.wait(kv_empty(st), ((item / STAGES) - 1) & 1);
-            ok = __all_sync(~0u, ok);
-            if (!ok) break;
-            if (lane == 0) {
-              if (x == 0) {
-                uint32_t miss = 0;
-                if (gone)
-                  for (int b = 0; b < n_box; ++b)
-                    if ((gone >> (2 * b)) & 1u) miss |= ((1u << (box / 16)) - 1u) << (b * box / 16);
-                s_miss[(item >> 1) & 7] = miss;
-              }
-              mbar_expect_tx(kv_full(st), C::STAGE);
-            }
-            __syncwarp();
-            if (side == x && b0 < n_box && half < D / 64)
-              tma_load_2d(ring_s + st * C::STAGE + half * (KB * 128) + b0 * box * 128,
-                          x ? &maps.v : &maps.k, half * 64, y, kv_full(st));
+        for (int i = 0; i < N; ++i) {
+          const int row = s_rows[(j & 3) * KB + i * PASS + k0];
+          w[i] = row >= 0 ? ldg_nc_v4(p + (int64_t)row * D)
+                          : make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
+        }
+      };
+      auto load_scales = [&](uint32_t j) {
+        const int row = s_rows[(j & 3) * KB + ptid];
+        gone = __ballot_sync(~0u, row == -2);
+        ksc = row >= 0 ? a.ks[row] : 0.f;
+        vsc = row >= 0 ? a.vs[row] : 1.f;
+        // a row that reads this key gets NaN by its score; weight 0 times it stays 0
+        if (!(vsc < INFINITY)) {
+          ksc = __int_as_float(0x7fc00000);
+          vsc = 1.f;
+        }
+      };
+      auto put = [&](const uint4 (&w)[N], uint32_t dst) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int key = i * PASS + k0;
+          const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+          uint32_t h[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            h[2 * k] = codes2(v[k], 0x4140u);
+            h[2 * k + 1] = codes2(v[k], 0x4342u);
+          }
+          // 16 values are chunks 2 c, 2 c + 1 of the row; lanes of the second half of the
+          // row store theirs in the other order, so that eight lanes meet all banks
+          const uint32_t line = dst + (c >> 2) * (KB * 128) + key * 128;
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int z = y ^ ((c >> 2) & 1);
+            st_shared(line + ((((c & 3) * 2 + z) ^ (key & 7)) << 4), z ? h[4] : h[0],
+                      z ? h[5] : h[1], z ? h[6] : h[2], z ? h[7] : h[3]);
           }
         }
-      } else {
-        // CH lanes per key, 16 codes each; thread ptid looks up the pool row of key
-        // ptid.  Rows are looked up two blocks ahead of the conversion, codes and
-        // scales loaded one block ahead: no thread waits for what it has just asked for.
-        constexpr int CH = D / 16, PASS = 128 / CH, N = KB / PASS;
-        const int ptid = tid - 256, c = ptid % CH, k0 = ptid / CH;
-        uint4 wk[N], wv[N];
-        float ksc = 0.f, vsc = 1.f;   // of key ptid of the next block
-        unsigned gone = 0;            // the warp's 32 keys: which stand on no page
-        auto look_up = [&](int kb) {
-          if (kb < kb1) s_rows[(kb & 3) * KB + ptid] = row_of(kb * KB + ptid);
-        };
-        auto load = [&](const void* pool, uint4 (&w)[N], int kb) {
-          if (kb >= kb1) return;
-          const uint8_t* const p = reinterpret_cast<const uint8_t*>(pool) + c * 16;
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const int row = s_rows[(kb & 3) * KB + i * PASS + k0];
-            w[i] = row >= 0 ? ldg_nc_v4(p + (int64_t)row * D)
-                            : make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
-          }
-        };
-        auto load_scales = [&](int kb) {
-          if (kb >= kb1) return;
-          const int row = s_rows[(kb & 3) * KB + ptid];
-          gone = __ballot_sync(~0u, row < 0 && kb * KB + ptid < u.n_keys);
-          ksc = row >= 0 ? a.ks[row] : 0.f;
-          vsc = row >= 0 ? a.vs[row] : 1.f;
-          // a row that reads this key gets NaN by its score; weight 0 times it stays 0
-          if (!(vsc < INFINITY)) {
-            ksc = __int_as_float(0x7fc00000);
-            vsc = 1.f;
-          }
-        };
-        auto put = [&](const uint4 (&w)[N], uint32_t dst) {
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const int key = i * PASS + k0;
-            const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-            uint32_t h[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              h[2 * k] = codes2(v[k], 0x4140u);
-              h[2 * k + 1] = codes2(v[k], 0x4342u);
-            }
-            // 16 values are chunks 2 c, 2 c + 1 of the row; lanes of the second half of the
-            // row store theirs in the other order, so that eight lanes meet all banks
-            const uint32_t line = dst + (c >> 2) * (KB * 128) + key * 128;
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const int z = y ^ ((c >> 2) & 1);
-              st_shared(line + ((((c & 3) * 2 + z) ^ (key & 7)) << 4), z ? h[4] : h[0],
-                        z ? h[5] : h[1], z ? h[6] : h[2], z ? h[7] : h[3]);
-            }
-          }
-        };
-        auto meet = [] { asm volatile("bar.sync 3, 128;" ::: "memory"); };
-        meet();            // the piece before has read its rows
-        look_up(kb0);
-        look_up(kb0 + 1);
-        meet();
-        load(a.k, wk, kb0);
-        load(a.v, wv, kb0);
-        load_scales(kb0);
-        // no thread leaves this loop early (they meet in it): after a wait ran out
-        // they only go on writing to their own shared memory
-        for (int kb = kb0; kb < kb1; ++kb, it += 2) {
-          look_up(kb + 2);
-          const uint32_t sk = it % STAGES, sv = (it + 1) % STAGES;
-          if (it >= STAGES) gate.wait(kv_empty(sk), ((it / STAGES) - 1) & 1);
-          float* const sc = s_scale + ((it >> 1) & 3) * C::SCALE_SLOT;
+      };
+      auto meet = [] { asm volatile("bar.sync 3, 128;" ::: "memory"); };
+      look_up(0);
+      look_up(1);
+      meet();
+      if (n > 0) {
+        load(a.k, wk, 0);
+        load_scales(0);
+      }
+      // no thread leaves this loop early (they meet in it): after a wait ran out
+      // they only go on writing to their own shared memory
+      for (uint32_t j = 0; j <= n && n > 0; ++j) {
+        look_up(j + 2);
+        if (j >= SLOTS) gate.wait(kv_empty(j), ((j / SLOTS) - 1) & 1);
+        const uint32_t slot = ring_s + j % SLOTS * C::SLOT;
+        if (j < n) {
+          float* const sc = s_scale + (j & 3) * C::SCALE_SLOT;
           sc[ptid] = ksc;
           sc[KB + ptid] = vsc;
           // (at least 2^-80: the sums of weights stay in range)
@@ -853,27 +833,27 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
           if (lane == 0) {
             sc[2 * KB + warp - 8] = big;
             // 16-key parts: bits 0 and 16 of the warp's 32 keys
-            reinterpret_cast<volatile uint8_t*>(s_miss + ((it >> 1) & 7))[warp - 8] =
+            reinterpret_cast<volatile uint8_t*>(s_miss + (j & 7))[warp - 8] =
                 (uint8_t)((gone & 1u) | ((gone >> 16) & 1u) << 1);
           }
-          put(wk, ring_s + sk * C::STAGE);
-          fence_async();
-          mbar_arrive(kv_full(sk));
-          load(a.k, wk, kb + 1);
-          load_scales(kb + 1);
-          if (it + 1 >= STAGES) gate.wait(kv_empty(sv), (((it + 1) / STAGES) - 1) & 1);
-          put(wv, ring_s + sv * C::STAGE);
-          fence_async();
-          mbar_arrive(kv_full(sv));
-          load(a.v, wv, kb + 1);
-          meet();          // the rows of block kb + 2 are there
+          put(wk, slot + C::HALF);
         }
+        if (j > 0) put(wv, slot);
+        fence_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(kv_full(j));
+        if (j < n) load(a.v, wv, j);
+        if (j + 1 < n) {
+          load(a.k, wk, j + 1);
+          load_scales(j + 1);
+        }
+        meet();          // the rows of block j + 2 are there
       }
     }
     if constexpr (!Q8) {
-      // after a wait ran out: copies of the last stages may still be under way
+      // after a wait ran out: copies into the slots may still be under way
       if (!ok && lane == 0)
-        for (int s = 0; s < STAGES; ++s)
+        for (int s = 0; s < SLOTS; ++s)
           for (uint32_t i = 0; i < (1u << 16) && !mbar_try_wait(kv_full(s), 0) && !mbar_try_wait(kv_full(s), 1); ++i) {
           }
     }

@@ -755,11 +755,12 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
                       side ? &maps.v : &maps.k, half * 64, y < 0 ? pool_rows : y, kv_full(j));
       }
     } else {
-      // CH lanes per key, 16 codes each; thread ptid looks up the pool row of key
-      // ptid.  Rows are looked up two blocks ahead of the conversion, codes and
-      // scales loaded one block ahead: no thread waits for what it has just asked for.
-      constexpr int CH = D / 16, PASS = 128 / CH, N = KB / PASS;
-      const int ptid = tid - 256, c = ptid % CH, k0 = ptid / CH;
+      // Four lanes take 64 codes of a key, a warp's load eight keys; thread ptid looks
+      // up the pool row of key ptid.  Rows are looked up two blocks ahead of the
+      // conversion, scales loaded one block ahead, and codes as soon as their
+      // registers are free, under the conversion of the other half.
+      constexpr int HV = D / 64, N = KB * HV / 32;   // halves of a row, loads per thread
+      const int ptid = tid - 256, c = ptid & 3, k0 = ptid >> 2;
       uint4 wk[N], wv[N];
       float ksc = 0.f, vsc = 1.f;   // of key ptid of the next block
       unsigned gone = 0;            // the warp's 32 keys: which stand on no page
@@ -771,10 +772,12 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
       auto load = [&](const void* pool, uint4 (&w)[N], uint32_t j) {
         const uint8_t* const p = reinterpret_cast<const uint8_t*>(pool) + c * 16;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int row = s_rows[(j & 3) * KB + i * PASS + k0];
-          w[i] = row >= 0 ? ldg_nc_v4(p + (int64_t)row * D)
-                          : make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
+        for (int i = 0; i < N; i += HV) {
+          const int row = s_rows[(j & 3) * KB + i / HV * 32 + k0];
+#pragma unroll
+          for (int h = 0; h < HV; ++h)
+            w[i + h] = row >= 0 ? ldg_nc_v4(p + (int64_t)row * D + h * 64)
+                                : make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
         }
       };
       auto load_scales = [&](uint32_t j) {
@@ -782,32 +785,20 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
         gone = __ballot_sync(~0u, row == -2);
         ksc = row >= 0 ? a.ks[row] : 0.f;
         vsc = row >= 0 ? a.vs[row] : 1.f;
-        // a row that reads this key gets NaN by its score; weight 0 times it stays 0
-        if (!(vsc < INFINITY)) {
-          ksc = __int_as_float(0x7fc00000);
-          vsc = 1.f;
-        }
       };
+      // 16 codes are chunks 2 c, 2 c + 1 of a half row's line; eight lanes' stores are
+      // those of two neighbouring keys, whose swizzles differ by one chunk: all banks
+      const uint32_t line = k0 * 128, x0 = (uint32_t)((2 * c) ^ (k0 & 7)) << 4;
       auto put = [&](const uint4 (&w)[N], uint32_t dst) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          const int key = i * PASS + k0;
+          const uint32_t at = dst + (i % HV) * (KB * 128) + i / HV * (32 * 128) + line;
           const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-          uint32_t h[8];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            h[2 * k] = codes2(v[k], 0x4140u);
-            h[2 * k + 1] = codes2(v[k], 0x4342u);
-          }
-          // 16 values are chunks 2 c, 2 c + 1 of the row; lanes of the second half of the
-          // row store theirs in the other order, so that eight lanes meet all banks
-          const uint32_t line = dst + (c >> 2) * (KB * 128) + key * 128;
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const int z = y ^ ((c >> 2) & 1);
-            st_shared(line + ((((c & 3) * 2 + z) ^ (key & 7)) << 4), z ? h[4] : h[0],
-                      z ? h[5] : h[1], z ? h[6] : h[2], z ? h[7] : h[3]);
-          }
+          for (int y = 0; y < 2; ++y)
+            st_shared(at + (x0 ^ (uint32_t)(y << 4)), codes2(v[2 * y], 0x4140u),
+                      codes2(v[2 * y], 0x4342u), codes2(v[2 * y + 1], 0x4140u),
+                      codes2(v[2 * y + 1], 0x4342u));
         }
       };
       auto meet = [] { asm volatile("bar.sync 3, 128;" ::: "memory"); };
@@ -825,28 +816,29 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
         if (j >= SLOTS) gate.wait(kv_empty(j), ((j / SLOTS) - 1) & 1);
         const uint32_t slot = ring_s + j % SLOTS * C::SLOT;
         if (j < n) {
+          put(wk, slot + C::HALF);
+          if (j + 1 < n) load(a.k, wk, j + 1);
+          // a row that reads a key whose scale of V is not finite gets NaN by its
+          // score; weight 0 times it stays 0
+          const bool fine = vsc < INFINITY;
           float* const sc = s_scale + (j & 3) * C::SCALE_SLOT;
-          sc[ptid] = ksc;
-          sc[KB + ptid] = vsc;
+          sc[ptid] = fine ? ksc : __int_as_float(0x7fc00000);
+          sc[KB + ptid] = fine ? vsc : 1.f;
           // (at least 2^-80: the sums of weights stay in range)
-          const float big = warp_max(ksc != 0.f ? fmaxf(log2f(vsc), -80.f) : -80.f);
+          const float big = warp_max(ksc != 0.f && fine ? fmaxf(log2f(vsc), -80.f) : -80.f);
           if (lane == 0) {
             sc[2 * KB + warp - 8] = big;
             // 16-key parts: bits 0 and 16 of the warp's 32 keys
             reinterpret_cast<volatile uint8_t*>(s_miss + (j & 7))[warp - 8] =
                 (uint8_t)((gone & 1u) | ((gone >> 16) & 1u) << 1);
           }
-          put(wk, slot + C::HALF);
+          if (j + 1 < n) load_scales(j + 1);
         }
         if (j > 0) put(wv, slot);
         fence_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(kv_full(j));
         if (j < n) load(a.v, wv, j);
-        if (j + 1 < n) {
-          load(a.k, wk, j + 1);
-          load_scales(j + 1);
-        }
         meet();          // the rows of block j + 2 are there
       }
     }

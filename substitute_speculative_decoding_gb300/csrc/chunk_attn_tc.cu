@@ -23,8 +23,13 @@
 // sum takes the unrounded weights) or fp16 for codes; a second product with
 // the rest would make the tensor cores half as slow again.
 //
-// The scale of v_j goes into the weights of codes (see chunk_attn.cu), as
-// 2^(s_ij + log2 vscale_j); the sum takes them divided by it.
+// Codes become fp16 values on the way, (code - 128) * scale relative to the power
+// of two of the block's largest scale, rounded once (half a step 2^-11, three bits
+// finer than the bf16 values of the other cache): the power of K's scales goes into
+// the scores' factor, that of V's into the weights.  (Scales applied to scores and weights,
+// column by column, would be exact, but cost every row 2 * 128 reads of shared
+// memory per block: the softmax then took 2.7 times as long.)  The scale enters in two fp16
+// parts, so that a row's values do not all share its rounding.
 //
 // V rows past the tile's last key hold anything, and so may keys of the chunk
 // that only later rows read.  In blocks that not all rows read to the end the first
@@ -33,6 +38,7 @@
 // read to its result (whatever is added to them, it stays infinite or NaN).
 #include <cuda.h>
 #include <cudaTypedefs.h>
+#include <cuda_fp16.h>
 #include <mutex>
 #include "chunk_attn.cuh"
 #include "tma.cuh"
@@ -56,21 +62,23 @@ template <int D, bool Q8>
 struct Cfg {
   static constexpr int HALF = KB * D * 2;                // K or V of a block, 16-bit values
   static constexpr int SLOT = 2 * HALF;                  // V of a block, K of the next
-  static constexpr int SLOTS = D == 64 ? 3 : 2;         // (at most 3: four blocks' scales are kept)
+  static constexpr int SLOTS = D == 64 ? 3 : 2;
   static constexpr int Q_BYTES = GROUP_ROWS * D * 2;     // of one group
-  static constexpr int MMA_WARP = 8 + (Q8 ? 4 : 1);
-  static constexpr int THREADS = Q8 ? 512 : 384;         // whole groups of four warps
+  static constexpr int CONV = Q8 ? 8 : 0;                // converter warps
+  static constexpr int MMA_WARP = 8 + (Q8 ? CONV : 1);
+  static constexpr int THREADS = Q8 ? 640 : 384;         // whole groups of four warps
   // registers by group of four warps, out of 65536 / THREADS each at the launch
   // (bf16: the producer and the MMA warp share one)
-  static constexpr int REGS_SOFTMAX = Q8 ? 176 : 192;
-  static constexpr int REGS_PROD = Q8 ? 80 : 120;
-  static constexpr int REGS_MMA = Q8 ? 80 : 120;
-  static_assert((2 * REGS_SOFTMAX + REGS_PROD + (Q8 ? REGS_MMA : 0)) * 128 <=
+  static constexpr int REGS_SOFTMAX = Q8 ? 160 : 192;
+  static constexpr int REGS_PROD = Q8 ? 64 : 120;
+  static constexpr int REGS_MMA = Q8 ? 32 : 120;
+  static_assert((2 * REGS_SOFTMAX + (Q8 ? CONV / 4 : 1) * REGS_PROD + (Q8 ? REGS_MMA : 0)) * 128 <=
                     65536 / THREADS / 8 * 8 * THREADS,
                 "the shares fit what the block is launched with");
-  // four blocks' scales of K, of V, and log2 of the largest of V by converter warp
-  static constexpr int SCALE_SLOT = 2 * KB + 4;
-  static constexpr int SCALES = Q8 ? 4 * SCALE_SLOT * 4 : 0;
+  // eight blocks' scales of K, of V, the largest of each by warp, and for the softmax
+  // the power of two of K's and the exponent of V's
+  static constexpr int SCALE_SLOT = 2 * KB + 12;
+  static constexpr int SCALES = Q8 ? 8 * SCALE_SLOT * 4 : 0;
   static constexpr int QSCALES = Q8 ? RT * 4 : 0;
   static constexpr int ROWS = Q8 ? 4 * KB * 4 : 0;       // pool rows of four blocks' keys
   static constexpr int TAIL = 256;                       // barriers, flags, TMEM address
@@ -173,11 +181,6 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.u) : "l"(x.u), "l"(y.u), "l"(z.u));
   return d.f;
 }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  F2 x{a}, y{b}, d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.u) : "l"(x.u), "l"(y.u));
-  return d.f;
-}
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   F2 x{a}, y{b}, d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.u) : "l"(x.u), "l"(y.u));
@@ -274,7 +277,7 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
   const uint32_t q_s = base, ring_s = base + 2 * C::Q_BYTES;
   int64_t* const s_pre = reinterpret_cast<int64_t*>(base_p + 2 * C::Q_BYTES);   // until the first copies
   uint8_t* const after = base_p + 2 * C::Q_BYTES + SLOTS * C::SLOT;
-  float* const s_scale = reinterpret_cast<float*>(after);                   // [4][SCALE_SLOT]
+  float* const s_scale = reinterpret_cast<float*>(after);                   // [8][SCALE_SLOT]
   float* const s_qs = reinterpret_cast<float*>(after + C::SCALES);          // [RT]
   int* const s_rows = reinterpret_cast<int*>(after + C::SCALES + C::QSCALES);   // [4][KB]
   uint8_t* const tail = after + C::SCALES + C::QSCALES + C::ROWS;
@@ -302,7 +305,7 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
   }
   if (tid == 32) {
     for (int s = 0; s < SLOTS; ++s) {
-      mbar_init(kv_full(s), Q8 ? 4 : 1);
+      mbar_init(kv_full(s), Q8 ? C::CONV : 1);
       mbar_init(kv_empty(s), 1);
     }
     for (int t = 0; t < 2; ++t) {
@@ -336,7 +339,7 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
   const Gate gate{s_dead};
   const int G = a.group;
   if (warp < 8) more_registers<C::REGS_SOFTMAX>();
-  else if (!Q8 || warp < 12) fewer_registers<C::REGS_PROD>();
+  else if (!Q8 || warp < 8 + C::CONV) fewer_registers<C::REGS_PROD>();
   else fewer_registers<C::REGS_MMA>();
 
   if (warp < 8) {
@@ -432,20 +435,14 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
         const uint32_t miss = s_miss[block & 7];
         const bool behind = key0 + KB - 1 > lim_first;   // the same for all rows of the tile
         const bool edge = behind || miss;
-        const float* const sc = s_scale + (block & 3) * C::SCALE_SLOT;
-        wait_ld();
+        // codes: the block's powers of two (not 0: it meets the masked scores' -infinity)
+        float f = factor, lv = 0.f;
         if constexpr (Q8) {
-#pragma unroll
-          for (int x = 0; x < KB; x += 4) {
-            const float4 k4 = *reinterpret_cast<const float4*>(sc + x);
-            const float2 y = mul2(make_float2(s[x], s[x + 1]), make_float2(k4.x, k4.y));
-            const float2 z = mul2(make_float2(s[x + 2], s[x + 3]), make_float2(k4.z, k4.w));
-            s[x] = y.x;
-            s[x + 1] = y.y;
-            s[x + 2] = z.x;
-            s[x + 3] = z.y;
-          }
+          const float2 pw = *reinterpret_cast<const float2*>(s_scale + (block & 7) * C::SCALE_SLOT + 2 * KB + 8);
+          f = fmaxf(factor * pw.x, 1e-37f);
+          lv = pw.y;
         }
+        wait_ld();
         if (edge) {
           const int last = lim - key0;   // columns past it are not read
 #pragma unroll
@@ -462,22 +459,18 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
           for (int i = 0; i < 8; ++i) top8[i] = fmaxf(fmaxf(top8[i], s[x + i]), s[x + 8 + i]);
         float top = fmaxf(fmaxf(fmaxf(top8[0], top8[1]), fmaxf(top8[2], top8[3])),
                           fmaxf(fmaxf(top8[4], top8[5]), fmaxf(top8[6], top8[7])));
-        top = top == -INFINITY ? top : top * factor;
-        if constexpr (Q8) {
-          // what is rounded to fp16 is the weight times the key's scale of V
-          const float4 lv = *reinterpret_cast<const float4*>(sc + 2 * KB);
-          top += fmaxf(fmaxf(lv.x, lv.y), fmaxf(lv.z, lv.w));
-        }
+        // what is rounded to fp16 is the weight times the power of two of V's scales
+        top = top == -INFINITY ? top : fmaf(top, f, lv);
         // ---- the reference, and the output that was formed with another ----
         const bool grow = top > ref + growth(Q8) || (!any && top != -INFINITY);
         if (__any_sync(~0u, grow)) {
-          const float f = grow && any ? exp2_fast(ref - top) : 1.f;
+          const float less = grow && any ? exp2_fast(ref - top) : 1.f;
           if (grow) {
             ref = top;
             any = true;
           }
-          l *= f;
-          if (kb > kb0 && __any_sync(~0u, f != 1.f)) {
+          l *= less;
+          if (kb > kb0 && __any_sync(~0u, less != 1.f)) {
 #pragma unroll 1
             for (int x = 0; x < D; x += 16) {
               float o[16];
@@ -485,7 +478,7 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
               tc_ld16(tO + x, o);
               wait_ld();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] *= f;
+              for (int i = 0; i < 16; ++i) o[i] *= less;
               tc_st16(tO + x, reinterpret_cast<const uint32_t*>(o));
             }
           }
@@ -528,8 +521,8 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
           __syncwarp();
         }
         // ---- weights, in place of the scores' first columns ----
-        const float shift = Q8 ? Q8_SHIFT - ref : -ref;
-        const float2 f2 = make_float2(factor, factor), d2 = make_float2(shift, shift);
+        const float shift = Q8 ? Q8_SHIFT + lv - ref : -ref;
+        const float2 f2 = make_float2(f, f), d2 = make_float2(shift, shift);
         float2 sum[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum[i] = make_float2(0.f, 0.f);
@@ -548,9 +541,6 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
               sum[(i + k) & 3] = add2(sum[(i + k) & 3], e[k]);
             }
             if constexpr (Q8) {
-              const float4 v4 = *reinterpret_cast<const float4*>(sc + KB + x);
-              e[0] = mul2(e[0], make_float2(v4.x, v4.y));
-              e[1] = mul2(e[1], make_float2(v4.z, v4.w));
               pw[i] = pack_f16x2(e[0].x, e[0].y);
               pw[i + 1] = pack_f16x2(e[1].x, e[1].y);
             } else {
@@ -565,7 +555,7 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full(t));
         sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
-        l += sum[0].x + sum[0].y;
+        l = fmaf(sum[0].x + sum[0].y, Q8 ? exp2_fast(-lv) : 1.f, l);
       }
       // ---- the next piece's Q takes this one's place as soon as the products are
       // through, so that its scores are formed while the result is written ----
@@ -635,7 +625,7 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
       tc_fence_before();   // O is read before the next piece's first weights are announced
       if (*s_dead) break;
     }
-  } else if (warp >= 8 + (Q8 ? 4 : 0) && warp != 8) {
+  } else if (Q8 ? warp >= 8 + C::CONV : warp > 8) {
     if (warp == C::MMA_WARP) {
       // -------------------------------------------------------- MMA issuer
       // The whole warp walks through this, with values that the compiler can see to be
@@ -759,21 +749,21 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
       // up the pool row of key ptid.  Rows are looked up two blocks ahead of the
       // conversion, scales loaded one block ahead, and codes as soon as their
       // registers are free, under the conversion of the other half.
-      constexpr int HV = D / 64, N = KB * HV / 32;   // halves of a row, loads per thread
+      constexpr int HV = D / 64, KEYS = C::CONV * 8, N = KB / KEYS * HV;   // halves of a row, keys per pass, loads
       const int ptid = tid - 256, c = ptid & 3, k0 = ptid >> 2;
       uint4 wk[N], wv[N];
-      float ksc = 0.f, vsc = 1.f;   // of key ptid of the next block
+      float ksc = 0.f, vsc = 0.f;   // of key ptid of the next block
       unsigned gone = 0;            // the warp's 32 keys: which stand on no page
       auto look_up = [&](uint32_t j) {   // called for j = 0, 1, ..
         if (j >= n) return;
         if (j > 0) step();
-        s_rows[(j & 3) * KB + ptid] = row_of(ptid);
+        if (ptid < KB) s_rows[(j & 3) * KB + ptid] = row_of(ptid);
       };
       auto load = [&](const void* pool, uint4 (&w)[N], uint32_t j) {
         const uint8_t* const p = reinterpret_cast<const uint8_t*>(pool) + c * 16;
 #pragma unroll
         for (int i = 0; i < N; i += HV) {
-          const int row = s_rows[(j & 3) * KB + i / HV * 32 + k0];
+          const int row = s_rows[(j & 3) * KB + i / HV * KEYS + k0];
 #pragma unroll
           for (int h = 0; h < HV; ++h)
             w[i + h] = row >= 0 ? ldg_nc_v4(p + (int64_t)row * D + h * 64)
@@ -781,65 +771,97 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
         }
       };
       auto load_scales = [&](uint32_t j) {
+        if (ptid >= KB) return;
         const int row = s_rows[(j & 3) * KB + ptid];
         gone = __ballot_sync(~0u, row == -2);
         ksc = row >= 0 ? a.ks[row] : 0.f;
-        vsc = row >= 0 ? a.vs[row] : 1.f;
+        vsc = row >= 0 ? a.vs[row] : 0.f;
+      };
+      auto store_scales = [&](uint32_t j) {
+        if (ptid >= KB) return;
+        // a row that reads a key whose scale of V is not finite gets NaN by its
+        // score; weight 0 times it stays 0
+        const bool fine = vsc < INFINITY;
+        float* const sc = s_scale + (j & 7) * C::SCALE_SLOT;
+        sc[ptid] = fine ? ksc : __int_as_float(0x7fc00000);
+        sc[KB + ptid] = fine ? vsc : 1.f;
+        const float kx = warp_max(ksc < INFINITY ? ksc : 0.f), vx = warp_max(fine ? vsc : 0.f);
+        if (lane == 0) {
+          sc[2 * KB + warp - 8] = kx;
+          sc[2 * KB + 4 + warp - 8] = vx;
+          // 16-key parts: bits 0 and 16 of the warp's 32 keys
+          reinterpret_cast<volatile uint8_t*>(s_miss + (j & 7))[warp - 8] =
+              (uint8_t)((gone & 1u) | ((gone >> 16) & 1u) << 1);
+        }
+      };
+      // exponent of a block's largest scale (V: at least -80, so that sums of weights
+      // stay in range)
+      auto exponent = [&](uint32_t j, int side) {
+        const float4 m = *reinterpret_cast<const float4*>(s_scale + (j & 7) * C::SCALE_SLOT + 2 * KB + 4 * side);
+        const float x = fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w));
+        return min(126, max(side ? -80 : -126, (int)(__float_as_uint(x) >> 23) - 127));
       };
       // 16 codes are chunks 2 c, 2 c + 1 of a half row's line; eight lanes' stores are
       // those of two neighbouring keys, whose swizzles differ by one chunk: all banks
       const uint32_t line = k0 * 128, x0 = (uint32_t)((2 * c) ^ (k0 & 7)) << 4;
-      auto put = [&](const uint4 (&w)[N], uint32_t dst) {
+      auto put = [&](const uint4 (&w)[N], uint32_t dst, uint32_t j, int side, int e) {
+        const float* const sc = s_scale + (j & 7) * C::SCALE_SLOT + side * KB + k0;
+        const float less = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          const uint32_t at = dst + (i % HV) * (KB * 128) + i / HV * (32 * 128) + line;
+          const float r = sc[i / HV * KEYS] * less;   // the scale relative to the power of two
+          const __half hi = __float2half_rn(r), lo = __float2half_rn(r - __half2float(hi));
+          const __half2 hi2 = __half2half2(hi), lo2 = __half2half2(lo);
+          auto value = [&](uint32_t word, uint32_t sel) {
+            const uint32_t x = codes2(word, sel);
+            const __half2 h = *reinterpret_cast<const __half2*>(&x);
+            const __half2 y = __hfma2(h, hi2, __hmul2(h, lo2));
+            return *reinterpret_cast<const uint32_t*>(&y);
+          };
+          const uint32_t at = dst + (i % HV) * (KB * 128) + i / HV * (KEYS * 128) + line;
           const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
           for (int y = 0; y < 2; ++y)
-            st_shared(at + (x0 ^ (uint32_t)(y << 4)), codes2(v[2 * y], 0x4140u),
-                      codes2(v[2 * y], 0x4342u), codes2(v[2 * y + 1], 0x4140u),
-                      codes2(v[2 * y + 1], 0x4342u));
+            st_shared(at + (x0 ^ (uint32_t)(y << 4)), value(v[2 * y], 0x4140u),
+                      value(v[2 * y], 0x4342u), value(v[2 * y + 1], 0x4140u),
+                      value(v[2 * y + 1], 0x4342u));
         }
       };
-      auto meet = [] { asm volatile("bar.sync 3, 128;" ::: "memory"); };
+      auto meet = [] { asm volatile("bar.sync 3, %0;" ::"n"(C::CONV * 32) : "memory"); };
       look_up(0);
       look_up(1);
       meet();
       if (n > 0) {
         load(a.k, wk, 0);
         load_scales(0);
+        store_scales(0);
       }
+      meet();
+      int ev = 0;   // exponent of the block's scales of V
       // no thread leaves this loop early (they meet in it): after a wait ran out
       // they only go on writing to their own shared memory
       for (uint32_t j = 0; j <= n && n > 0; ++j) {
         look_up(j + 2);
+        if (j + 1 < n) load_scales(j + 1);
         if (j >= SLOTS) gate.wait(kv_empty(j), ((j / SLOTS) - 1) & 1);
         const uint32_t slot = ring_s + j % SLOTS * C::SLOT;
+        const int ev_before = ev;
         if (j < n) {
-          put(wk, slot + C::HALF);
+          const int ek = exponent(j, 0);
+          ev = exponent(j, 1);
+          if (ptid == 0)
+            *reinterpret_cast<float2*>(s_scale + (j & 7) * C::SCALE_SLOT + 2 * KB + 8) =
+                make_float2(__uint_as_float((uint32_t)(127 + ek) << 23), (float)ev);
+          put(wk, slot + C::HALF, j, 0, ek);
           if (j + 1 < n) load(a.k, wk, j + 1);
-          // a row that reads a key whose scale of V is not finite gets NaN by its
-          // score; weight 0 times it stays 0
-          const bool fine = vsc < INFINITY;
-          float* const sc = s_scale + (j & 3) * C::SCALE_SLOT;
-          sc[ptid] = fine ? ksc : __int_as_float(0x7fc00000);
-          sc[KB + ptid] = fine ? vsc : 1.f;
-          // (at least 2^-80: the sums of weights stay in range)
-          const float big = warp_max(ksc != 0.f && fine ? fmaxf(log2f(vsc), -80.f) : -80.f);
-          if (lane == 0) {
-            sc[2 * KB + warp - 8] = big;
-            // 16-key parts: bits 0 and 16 of the warp's 32 keys
-            reinterpret_cast<volatile uint8_t*>(s_miss + (j & 7))[warp - 8] =
-                (uint8_t)((gone & 1u) | ((gone >> 16) & 1u) << 1);
-          }
-          if (j + 1 < n) load_scales(j + 1);
         }
-        if (j > 0) put(wv, slot);
+        if (j > 0) put(wv, slot, j - 1, 1, ev_before);
         fence_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(kv_full(j));
         if (j < n) load(a.v, wv, j);
-        meet();          // the rows of block j + 2 are there
+        if (j + 1 < n) store_scales(j + 1);
+        meet();          // the rows of block j + 2 and the scales of block j + 1 are there
       }
     }
     if constexpr (!Q8) {

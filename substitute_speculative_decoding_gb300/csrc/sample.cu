@@ -61,15 +61,20 @@ __device__ __forceinline__ void share(int groups, int rank, int size, int& lo, i
 
 // ------------------------------------------------------------- softmax --
 // p = exp((z - m) / T) / sum, with m the largest logit.  Bound by HBM: 4 bytes
-// in, 4 out.  A thread keeps NV groups in registers between the two passes
-// (groups past them, in rows longer than the cluster holds, are read again).
-// Each CTA sums relative to its own largest logit, so one cluster barrier
-// exchanges both, and a value is scaled by exp((m_cta - m) / T) / sum.
-template <int THREADS, int NV>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) probs_kernel(const float* logits, int64_t V, float c_hi,
-                                                        float c_lo, float* probs) {
+// in, 4 out.  The first pass keeps a running maximum and sum per thread, the
+// second reads the row again, from L2: a row's CTAs run at the same time, so
+// what is between the passes are a few dozen MB.  (Keeping a row in registers between
+// the passes left room for two CTAs per SM, and a cluster's copies, sums and
+// stores did not overlap enough: 4.1 TB/s on 576 rows of 128256.)  The CTAs exchange maxima
+// and sums in one cluster barrier.
+constexpr int PROBS_MLP = 4;
+
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS, 1536 / THREADS) probs_kernel(const float* logits, int64_t V,
+                                                                        float c_hi, float c_lo,
+                                                                        float* probs) {
   constexpr int WARPS = THREADS / 32;
-  __shared__ float s_m[WARPS], s_s[WARPS];
+  __shared__ float2 s_warp[WARPS];
   __shared__ float2 s_peer[MAX_CLUSTER];   // each CTA's (largest logit, sum), written by it
   cg::cluster_group cluster = cg::this_cluster();
   const int size = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -84,82 +89,71 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) probs_kernel(const fl
   share(r.groups(), rank, size, lo, hi);
   // exp(d / T) = 2^(d c), c = log2(e) / T in two parts: one rounding of d c
   auto expo = [&](float d) { return d == -INFINITY ? 0.f : exp2f(fmaf(d, c_hi, d * c_lo)); };
-  float4 x[NV];
+  auto merge = [&](float& m, float& s, float m2, float s2) {   // sums relative to their maxima
+    const float big = fmaxf(m, m2);
+    if (m2 == -INFINITY && s2 == 0.f) return;
+    s = (m == -INFINITY && s == 0.f ? 0.f : s * expo(m - big)) + s2 * expo(m2 - big);
+    m = big;
+  };
+  float m = -INFINITY, s = 0.f;
+  for (int g0 = lo + threadIdx.x; g0 < hi; g0 += PROBS_MLP * THREADS) {
+    float4 x[PROBS_MLP];
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int g = lo + threadIdx.x + j * THREADS;
-    x[j] = g < hi ? load_group(z, r, g, -INFINITY)
-                  : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    for (int k = 0; k < PROBS_MLP; ++k)
+      x[k] = g0 + k * THREADS < hi ? load_group(z, r, g0 + k * THREADS, -INFINITY)
+                                   : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    float big = m;
+#pragma unroll
+    for (int k = 0; k < PROBS_MLP; ++k)
+      big = fmaxf(fmaxf(big, fmaxf(x[k].x, x[k].y)), fmaxf(x[k].z, x[k].w));
+    // no logit above -infinity so far: every value is 0 whatever the reference
+    const float ref = big == -INFINITY ? 0.f : big;
+    s *= expo(m - ref);
+    m = big;
+#pragma unroll
+    for (int k = 0; k < PROBS_MLP; ++k)
+      s += (expo(x[k].x - ref) + expo(x[k].y - ref)) + (expo(x[k].z - ref) + expo(x[k].w - ref));
   }
-  auto max4 = [](const float4& v) { return fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)); };
-  float m = -INFINITY;
 #pragma unroll
-  for (int j = 0; j < NV; ++j) m = fmaxf(m, max4(x[j]));
-  for (int g = lo + threadIdx.x + NV * THREADS; g < hi; g += THREADS)
-    m = fmaxf(m, max4(load_group(z, r, g, -INFINITY)));
-  m = warp_max(m);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (lane == 0) s_m[warp] = m;
+  for (int o = 16; o; o >>= 1)
+    merge(m, s, __shfl_xor_sync(~0u, m, o), __shfl_xor_sync(~0u, s, o));
+  if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = make_float2(m, s);
   __syncthreads();
   m = -INFINITY;
-#pragma unroll
-  for (int w = 0; w < WARPS; ++w) m = fmaxf(m, s_m[w]);
-  // no logit above -infinity here: every value is 0 whatever the reference
-  const float ref = m == -INFINITY ? 0.f : m;
-  auto exp4 = [&](const float4& v) {
-    return make_float4(expo(v.x - ref), expo(v.y - ref), expo(v.z - ref), expo(v.w - ref));
-  };
-  float s = 0.f;
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    x[j] = exp4(x[j]);
-    s += (x[j].x + x[j].y) + (x[j].z + x[j].w);
-  }
-  for (int g = lo + threadIdx.x + NV * THREADS; g < hi; g += THREADS) {
-    const float4 e = exp4(load_group(z, r, g, -INFINITY));
-    s += (e.x + e.y) + (e.z + e.w);
-  }
-  s = warp_sum(s);
-  if (lane == 0) s_s[warp] = s;
-  __syncthreads();
   s = 0.f;
-#pragma unroll
-  for (int w = 0; w < WARPS; ++w) s += s_s[w];
-  float f;
-  if (size == 1) {
-    f = s == 0.f ? 0.f : 1.f / s;
-  } else {
+  for (int w = 0; w < WARPS; ++w) merge(m, s, s_warp[w].x, s_warp[w].y);
+  if (size > 1) {
     // every CTA writes its own into all of them, so that one barrier is enough:
     // nobody reads the memory of a CTA that may have ended
     cluster_all_here();
     if ((int)threadIdx.x < size) *cluster.map_shared_rank(&s_peer[rank], threadIdx.x) = make_float2(m, s);
     cluster.sync();
-    float big = -INFINITY, all = 0.f;
-    for (int i = 0; i < size; ++i) big = fmaxf(big, s_peer[i].x);
-    for (int i = 0; i < size; ++i) {
-      const float2 o = s_peer[i];
-      if (o.x != -INFINITY || o.y != 0.f) all += o.y * expo(o.x - big);
-    }
-    f = all == 0.f ? 0.f : expo(m - big) / all;
+    m = -INFINITY;
+    s = 0.f;
+    for (int i = 0; i < size; ++i) merge(m, s, s_peer[i].x, s_peer[i].y);
   }
-  auto put = [&](int g, const float4& v) {
-    const int64_t e = r.first(g);
-    if (r.whole(g)) {
-      *reinterpret_cast<float4*>(out + e) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
-      return;
+  const float ref = m == -INFINITY ? 0.f : m, f = s == 0.f ? 0.f : 1.f / s;
+  for (int g0 = lo + threadIdx.x; g0 < hi; g0 += PROBS_MLP * THREADS) {
+    float4 x[PROBS_MLP];
+#pragma unroll
+    for (int k = 0; k < PROBS_MLP; ++k)
+      if (g0 + k * THREADS < hi) x[k] = load_group(z, r, g0 + k * THREADS, -INFINITY);
+#pragma unroll
+    for (int k = 0; k < PROBS_MLP; ++k) {
+      const int g = g0 + k * THREADS;
+      if (g >= hi) break;
+      const int64_t e = r.first(g);
+      const float w[4] = {expo(x[k].x - ref) * f, expo(x[k].y - ref) * f, expo(x[k].z - ref) * f,
+                          expo(x[k].w - ref) * f};
+      if (r.whole(g)) {
+        __stcs(reinterpret_cast<float4*>(out + e), make_float4(w[0], w[1], w[2], w[3]));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (e + i >= 0 && e + i < V) out[e + i] = w[i];
+      }
     }
-    const float w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (e + i >= 0 && e + i < V) out[e + i] = w[i] * f;
-  };
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int g = lo + threadIdx.x + j * THREADS;
-    if (g < hi) put(g, x[j]);
   }
-  for (int g = lo + threadIdx.x + NV * THREADS; g < hi; g += THREADS)
-    put(g, exp4(load_group(z, r, g, -INFINITY)));
 }
 
 // ------------------------------------------------- draft verification --
@@ -193,7 +187,9 @@ __device__ __forceinline__ uint64_t warp_scan64(uint64_t v, int lane) {   // inc
 // One cluster per sequence.  Every warp repeats the acceptance tests (a few
 // numbers each), which name the row to sample from; then the row is read
 // once: weights as whole multiples of 2^-43, so that their sums do not depend
-// on the order and the sampled token is the same on any split.  Each warp sums
+// on the order and the sampled token is the same on any split.  (Formed in two
+// halves by fp32 additions that leave the whole number in the mantissa's low bits:
+// conversions to 64-bit integers run at a small fraction of that rate.)  Each warp sums
 // a contiguous part; the sums of all warps of the cluster name the one warp
 // whose part holds the number, and that warp alone reads its part again (from
 // L2) to find the token.  Bound by the latency of four dependent rounds of
@@ -247,11 +243,24 @@ __global__ void __launch_bounds__(VER_THREADS, 4) verify_kernel(VerifyArgs a) {
   const bool q_vec = q && ((reinterpret_cast<uintptr_t>(q) >> 2) & 3) == (unsigned)r.mis;
   int lo, hi;
   share(r.groups(), me, size * VER_WARPS, lo, hi);
+  // rint(x 2^43) = high 2^22 + low for x in [0, 1]: high = rint(x 2^21) in 23 bits over
+  // 2^23, low = rint(rest 2^22) in -2^21 .. 2^21 over 3 2^22
+  constexpr uint32_t HIGH0 = 0x4B000000u, LOW0 = 0x4B400000u;
+  auto halves = [&](float d, uint32_t& high, uint32_t& low) {
+    const float x = fminf(fmaxf(d, 0.f), 1.f);   // NaN counts as 0
+    const float h = fmaf(x, 0x1p21f, 8388608.f);
+    const float rest = fmaf(x, 0x1p21f, -(h - 8388608.f));   // exact
+    high = __float_as_uint(h);
+    low = __float_as_uint(fmaf(rest, 0x1p22f, 12582912.f));
+  };
   auto weights = [&](const float4& pv, const float4& qv, uint64_t (&w)[4]) {
     const float d[4] = {pv.x - qv.x, pv.y - qv.y, pv.z - qv.z, pv.w - qv.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[i] = __float2ull_rn(fminf(fmaxf(d[i], 0.f), 1.f) * 0x1p43f);   // NaN counts as 0
+    for (int i = 0; i < 4; ++i) {
+      uint32_t h, l;
+      halves(d[i], h, l);
+      w[i] = (uint64_t)(((int64_t)(h - HIGH0) << 22) + (int32_t)(l - LOW0));
+    }
   };
   auto load_q = [&](int g, bool diff) {
     if (!diff) return make_float4(0.f, 0.f, 0.f, 0.f);
@@ -263,7 +272,8 @@ __global__ void __launch_bounds__(VER_THREADS, 4) verify_kernel(VerifyArgs a) {
 
   bool alone = size > 1;   // the others may not run yet
   for (bool diff = refused;; diff = false) {
-    uint64_t mine = 0;
+    // sums of the halves, at most 2^9 values per lane (V <= 2^20): 2^30 of each
+    uint32_t high = 0, low = 0, count = 0;
     for (int g0 = lo + lane; g0 < hi; g0 += 32 * VER_MLP) {
       float4 pv[VER_MLP], qv[VER_MLP];
 #pragma unroll
@@ -277,12 +287,20 @@ __global__ void __launch_bounds__(VER_THREADS, 4) verify_kernel(VerifyArgs a) {
       }
 #pragma unroll
       for (int k = 0; k < VER_MLP; ++k) {
-        uint64_t w[4];
-        weights(pv[k], qv[k], w);
-        mine += (w[0] + w[1]) + (w[2] + w[3]);
+        const float d[4] = {pv[k].x - qv[k].x, pv[k].y - qv[k].y, pv[k].z - qv[k].z, pv[k].w - qv[k].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t h, l;
+          halves(d[i], h, l);
+          high += h;
+          low += l;
+        }
       }
+      count += 4 * VER_MLP;
     }
-    mine = warp_sum64(mine);
+    // (what the bits lie over goes with the wrapped-around sums)
+    const uint64_t mine = warp_sum64((uint64_t)(((int64_t)(high - count * HIGH0) << 22) +
+                                                (int32_t)(low - count * LOW0)));
     if (alone) cluster_all_here();
     alone = false;
     if (lane < size) *cluster.map_shared_rank(&s_sum[me], lane) = mine;
@@ -379,16 +397,13 @@ extern "C" int32_t sub_probs(const float* logits, int64_t rows, int64_t V, float
   const double c = 1.4426950408889634074 / (double)temperature;
   const float c_hi = (float)c, c_lo = (float)(c - (double)c_hi);
   const cudaStream_t st = as_stream(stream);
-  if (V <= 2048) {
-    SUB_CUDA_TRY(
-        launch_clusters(probs_kernel<128, 4>, rows, 1, 128, st, logits, V, c_hi, c_lo, probs));
+  if (V <= 2048) {   // a row of one round of loads
+    SUB_CUDA_TRY(launch_clusters(probs_kernel<128>, rows, 1, 128, st, logits, V, c_hi, c_lo, probs));
     return SUB_OK;
   }
-  // a CTA keeps 512 * 10 groups; few rows spread over more CTAs (two per SM)
-  int size = 1;
-  while (size < MAX_CLUSTER && (V > (int64_t)size * 512 * 40 - 4 || rows * size < 152)) size *= 2;
-  SUB_CUDA_TRY(
-      launch_clusters(probs_kernel<512, 10>, rows, size, 512, st, logits, V, c_hi, c_lo, probs));
+  // long rows over a cluster: rows in work at a time stay in L2, and few rows use more SMs
+  const int size = V <= 16384 && rows >= 608 ? 1 : MAX_CLUSTER;
+  SUB_CUDA_TRY(launch_clusters(probs_kernel<256>, rows, size, 256, st, logits, V, c_hi, c_lo, probs));
   return SUB_OK;
 }
 

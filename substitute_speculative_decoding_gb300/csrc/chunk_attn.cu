@@ -42,6 +42,7 @@
 namespace sub {
 namespace {
 
+constexpr int RT = 16;           // rows of a tile
 constexpr int WARPS = 8;
 constexpr int NT = WARPS * 32;
 constexpr int STAGES = 3;
@@ -116,21 +117,20 @@ struct Ring {
   static constexpr int BYTES = STAGES * STAGE;           // of one warp
 };
 
-template <int D, bool Q8, int MT>
+template <int D, bool Q8>
 constexpr int decode_smem() {
-  // a warp's partial result (MT * 16 rows of D floats, maxima and sums) reuses its ring
-  static_assert(Ring<D, Q8>::BYTES >= MT * 16 * (D + 2) * 4, "the ring holds the partial result");
+  // a warp's partial result (16 rows of D floats, maxima and sums) reuses its ring
+  static_assert(Ring<D, Q8>::BYTES >= RT * (D + 2) * 4, "the ring holds the partial result");
   return WARPS * Ring<D, Q8>::BYTES;
 }
 
 // ------------------------------------------------------------------ kernel --
-template <int D, bool Q8, int MT>
-__global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
+template <int D, bool Q8>
+__global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(const __grid_constant__ ChunkArgs a) {
   using R = Ring<D, Q8>;
-  constexpr int RT = MT * 16, KS = D / 16, ON = D / 8, KB = R::KB, SUBS = R::SUBS, TILES = KB / 8;
+  constexpr int KS = D / 16, ON = D / 8, KB = R::KB, SUBS = R::SUBS, TILES = KB / 8;
   extern __shared__ __align__(128) uint8_t smem[];
-  int64_t* const s_pre = reinterpret_cast<int64_t*>(smem);   // until the first copies
-  static_assert(decode_smem<D, Q8, MT>() >= (SUB_MAX_SEQS + 1) * 8, "the running sums fit");
+  __shared__ int64_t s_pre[SUB_MAX_SEQS + 1];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -140,19 +140,16 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
   plan.template scan<NT>(s_pre);
   const int64_t total = s_pre[a.t.n_seqs];
   const int64_t per = blocks_per_cta(total, gridDim.x, WARPS);
-  const int64_t line_lo = blockIdx.x * per, line_hi = min(total, line_lo + per);
   uint8_t* const ring = smem + warp * R::BYTES;
   const uint32_t ring_s = smem_u32(ring);
   // a lane's place in the first key of a step, of K and of V
   const uint8_t* const kp = reinterpret_cast<const uint8_t*>(a.k) + g * R::ROW + tig * 16;
   const uint8_t* const vp = reinterpret_cast<const uint8_t*>(a.v) + 2 * tig * R::ROW + g * R::VB;
   const int64_t page_rows = (int64_t)a.n_heads_kv * ps;
-  // from block to block of a warp
-  const int step_pages = a.by_page.quot(WARPS * KB), step_at = WARPS * KB - step_pages * ps;
+  const int64_t line_lo = blockIdx.x * per, line_hi = min(total, line_lo + per);
   ChunkUnit u;
   if (line_lo < line_hi) u = plan.find(s_pre, line_lo);
-  __syncthreads();
-
+  else if (tid == 0) a.cuts[blockIdx.x].pieces = 0;
   for (int64_t at = line_lo; at < line_hi; plan.next(u)) {
     const int kb0 = (int)(at - u.begin);
     const int kb1 = (int)min((int64_t)u.n_blocks, line_hi - u.begin);
@@ -160,30 +157,31 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
     const int32_t* const pages = a.t.pages + (int64_t)u.b * a.t.width;
     const int64_t row_base = ((int64_t)a.layer * a.t.n_pages * a.n_heads_kv + u.head) * ps;
 
-    // the next block to copy: first key, page-table entry and place in the page, and
-    // the pages of its steps (-1: none), read one block ahead of their use
-    struct {
-      int key, entry, at, page[SUBS];
-    } nx;
-    nx.key = (kb0 + warp) * KB;
-    nx.entry = a.by_page.quot(nx.key);
-    nx.at = nx.key - nx.entry * ps;
-    auto look_up = [&] {
-#pragma unroll
-      for (int s = 0; s < SUBS; ++s)
-        nx.page[s] = nx.key + 16 * s < u.n_keys ? pages[nx.entry + (nx.at + 16 * s >= ps ? 1 : 0)] : -1;
+    // Pool rows of the warp's next 32 16-key steps (-1: no page), one looked up by
+    // each lane, and of the 32 after them: a step's place is a shuffle away.
+    auto look_up = [&](int step) -> int64_t {
+      const int key = (kb0 + warp + step / SUBS * WARPS) * KB + step % SUBS * 16;
+      if (key >= u.n_keys || step >= n_mine * SUBS) return -1;
+      const int entry = a.by_page.quot(key), page = pages[entry];
+      if ((unsigned)page >= (unsigned)a.t.n_pages) return -1;
+      return row_base + (int64_t)page * page_rows + (key - entry * ps);
     };
+    int64_t places = look_up(lane), places2 = look_up(32 + lane);
     uint32_t missing = 0;   // bits SUBS * stage + step: no page there
-    auto issue = [&](int stage) {
+    auto issue = [&](int i, int stage) {
       const uint32_t dst = ring_s + stage * R::STAGE;
+      if (i > 0 && i % (32 / SUBS) == 0) {
+        places = places2;
+        places2 = look_up(i * SUBS + 32 + lane);
+      }
 #pragma unroll
       for (int s = 0; s < SUBS; ++s) {
-        const int place = nx.at + 16 * s - (nx.at + 16 * s >= ps ? ps : 0);
-        const bool have = (unsigned)nx.page[s] < (unsigned)a.t.n_pages;
-        const int left = have ? u.n_keys - (nx.key + 16 * s) : 0;   // keys of the step
+        const int64_t place = __shfl_sync(~0u, places, (i * SUBS + s) & 31);
+        const bool have = place >= 0;
+        const int64_t row0 = have ? place : 0;
+        const int left = have ? u.n_keys - ((kb0 + warp + i * WARPS) * KB + 16 * s) : 0;   // keys of the step
         const int bit = SUBS * stage + s;
         missing = (missing & ~(1u << bit)) | ((have ? 0u : 1u) << bit);
-        const int64_t row0 = row_base + (int64_t)(have ? nx.page[s] : 0) * page_rows + place;
         const uint8_t* const k0 = kp + row0 * R::ROW;
         const uint8_t* const v0 = vp + row0 * R::ROW;
         const uint32_t kd = dst + s * (2 * R::KI * 512) + lane * 16;
@@ -201,15 +199,15 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
               cp_async<R::VB>(vd + (kk * R::VH + c) * (32 * R::VB),
                               v0 + ((kk >> 1) * 8 + (kk & 1)) * R::ROW + c * 8 * R::VB);
         } else {   // zeros past the last key
-#pragma unroll
+#pragma unroll 1
           for (int h = 0; h < 2; ++h)
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < R::KI; ++c)
               cp_async_if<16>(kd + (h * R::KI + c) * 512, k0 + h * 8 * R::ROW + c * 64, a.k,
                               h * 8 + g < left);
-#pragma unroll
+#pragma unroll 1
           for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < R::VH; ++c)
               cp_async_if<R::VB>(vd + (kk * R::VH + c) * (32 * R::VB),
                                  v0 + ((kk >> 1) * 8 + (kk & 1)) * R::ROW + c * 8 * R::VB, a.k,
@@ -222,113 +220,80 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
         }
       }
     };
-    auto forward = [&] {
-      nx.key += WARPS * KB;
-      nx.entry += step_pages;
-      nx.at += step_at;
-      if (nx.at >= ps) {
-        nx.at -= ps;
-        ++nx.entry;
-      }
-    };
-    {
-      // the first blocks' pages are all asked for before the first is used
-      int page[STAGES + 1][SUBS], key = nx.key, entry = nx.entry, place = nx.at;
-#pragma unroll
-      for (int i = 0; i <= STAGES; ++i) {
-        look_up();
-#pragma unroll
-        for (int s = 0; s < SUBS; ++s) page[i][s] = nx.page[s];
-        forward();
-      }
-      nx.key = key;
-      nx.entry = entry;
-      nx.at = place;
-#pragma unroll
-      for (int i = 0; i <= STAGES; ++i) {
-#pragma unroll
-        for (int s = 0; s < SUBS; ++s) nx.page[s] = page[i][s];
-        if (i == STAGES) break;
-        if (i < n_mine) issue(i);
-        cp_commit();
-        forward();
-      }
+#pragma unroll 1
+    for (int i = 0; i < STAGES; ++i) {
+      if (i < n_mine) issue(i, i);
+      cp_commit();
     }
 
     // ---- Q fragments, and the rows' last visible key ----
-    uint32_t qf[MT][KS][4];
-    float qs[MT][2];    // factor of the row's scores
-    int lim[MT][2];     // keys 0 .. lim are read
+    uint32_t qf[KS][4];
+    float qs[2];    // factor of the row's scores
+    int lim[2];     // keys 0 .. lim are read
+    uint4 w[2][KS / 2];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      uint4 w[2][KS / 2];
+    for (int h = 0; h < 2; ++h) {
+      const int r = u.tile * RT + h * 8 + g;
+      const int q = a.by_group.quot(r);
+      const bool ok = q < u.rows;
+      lim[h] = ok ? min(u.pos + q, u.n_keys - 1) : -1;
+      const uint16_t* src = a.Q + (int64_t)(u.row0 + (ok ? q : 0)) * a.ldq +
+                            (int64_t)(u.head * G + r - q * G) * D;
+#pragma unroll
+      for (int c = 0; c < KS / 2; ++c) {
+        // bf16 cache: chunk tig + 4 c of 8 values; codes: half c & 1 of chunk tig + 4 (c / 2) of 16
+        const int d = Q8 ? ((tig + 4 * (c >> 1)) * 16 + (c & 1) * 8) : (tig + 4 * c) * 8;
+        w[h][c] = ok ? *reinterpret_cast<const uint4*>(src + d) : make_uint4(0, 0, 0, 0);
+      }
+    }
+    if constexpr (!Q8) {
+#pragma unroll
+      for (int c = 0; c < KS / 2; ++c) {
+        qf[2 * c][0] = w[0][c].x;
+        qf[2 * c][1] = w[1][c].x;
+        qf[2 * c][2] = w[0][c].y;
+        qf[2 * c][3] = w[1][c].y;
+        qf[2 * c + 1][0] = w[0][c].z;
+        qf[2 * c + 1][1] = w[1][c].z;
+        qf[2 * c + 1][2] = w[0][c].w;
+        qf[2 * c + 1][3] = w[1][c].w;
+      }
+      qs[0] = qs[1] = a.sl2;
+    } else {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int r = u.tile * RT + m * 16 + h * 8 + g;
-        const int q = a.by_group.quot(r);
-        const bool ok = q < u.rows;
-        lim[m][h] = ok ? min(u.pos + q, u.n_keys - 1) : -1;
-        const uint16_t* src = a.Q + (int64_t)(u.row0 + (ok ? q : 0)) * a.ldq +
-                              (int64_t)(u.head * G + r - q * G) * D;
+        // the row's largest value to [1, 2): an exponent in [-126, 126]
+        float big = 0.f;
 #pragma unroll
         for (int c = 0; c < KS / 2; ++c) {
-          // bf16 cache: chunk tig + 4 c of 8 values; codes: half c & 1 of chunk tig + 4 (c / 2) of 16
-          const int d = Q8 ? ((tig + 4 * (c >> 1)) * 16 + (c & 1) * 8) : (tig + 4 * c) * 8;
-          w[h][c] = ok ? *reinterpret_cast<const uint4*>(src + d) : make_uint4(0, 0, 0, 0);
+          const uint32_t x[4] = {w[h][c].x, w[h][c].y, w[h][c].z, w[h][c].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            big = fmaxf(big, fmaxf(fabsf(bf16lo(x[i])), fabsf(bf16hi(x[i]))));
         }
-      }
-      if constexpr (!Q8) {
+        big = fmaxf(big, __shfl_xor_sync(~0u, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(~0u, big, 2));
+        const int e = min(126, max(-126, (int)(__float_as_uint(big) >> 23) - 127));
+        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+        // (not 0: it meets the masked scores' -infinity)
+        qs[h] = fmaxf(a.sl2 * __uint_as_float((uint32_t)(127 + e) << 23), 1e-37f);
 #pragma unroll
         for (int c = 0; c < KS / 2; ++c) {
-          qf[m][2 * c][0] = w[0][c].x;
-          qf[m][2 * c][1] = w[1][c].x;
-          qf[m][2 * c][2] = w[0][c].y;
-          qf[m][2 * c][3] = w[1][c].y;
-          qf[m][2 * c + 1][0] = w[0][c].z;
-          qf[m][2 * c + 1][1] = w[1][c].z;
-          qf[m][2 * c + 1][2] = w[0][c].w;
-          qf[m][2 * c + 1][3] = w[1][c].w;
-        }
-        qs[m][0] = qs[m][1] = a.sl2;
-      } else {
+          const uint32_t x[4] = {w[h][c].x, w[h][c].y, w[h][c].z, w[h][c].w};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          // the row's largest value to [1, 2): an exponent in [-126, 126]
-          float big = 0.f;
-#pragma unroll
-          for (int c = 0; c < KS / 2; ++c) {
-            const uint32_t x[4] = {w[h][c].x, w[h][c].y, w[h][c].z, w[h][c].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              big = fmaxf(big, fmaxf(fabsf(bf16lo(x[i])), fabsf(bf16hi(x[i]))));
-          }
-          big = fmaxf(big, __shfl_xor_sync(~0u, big, 1));
-          big = fmaxf(big, __shfl_xor_sync(~0u, big, 2));
-          const int e = min(126, max(-126, (int)(__float_as_uint(big) >> 23) - 127));
-          const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-          // (not 0: it meets the masked scores' -infinity)
-          qs[m][h] = fmaxf(a.sl2 * __uint_as_float((uint32_t)(127 + e) << 23), 1e-37f);
-#pragma unroll
-          for (int c = 0; c < KS / 2; ++c) {
-            const uint32_t x[4] = {w[h][c].x, w[h][c].y, w[h][c].z, w[h][c].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              qf[m][2 * c + (i >> 1)][(i & 1) * 2 + h] =
-                  pack_f16x2(bf16lo(x[i]) * down, bf16hi(x[i]) * down);
-          }
+          for (int i = 0; i < 4; ++i)
+            qf[2 * c + (i >> 1)][(i & 1) * 2 + h] =
+                pack_f16x2(bf16lo(x[i]) * down, bf16hi(x[i]) * down);
         }
       }
     }
     const int lim_min = min(u.pos + a.by_group.quot(u.tile * RT), u.n_keys - 1);   // of the tile's first row
 
-    float o[MT][ON][4], mx[MT][2], l[MT][2];
+    float o[ON][4], mx[2], l[2];
+    mx[0] = mx[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      mx[m][0] = mx[m][1] = -INFINITY;
-      l[m][0] = l[m][1] = 0.f;
-#pragma unroll
-      for (int i = 0; i < ON; ++i) o[m][i][0] = o[m][i][1] = o[m][i][2] = o[m][i][3] = 0.f;
-    }
+    for (int i = 0; i < ON; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
     int stage = 0;
     for (int i = 0; i < n_mine; ++i) {
@@ -340,27 +305,22 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
       const bool edge = key0 + KB - 1 > lim_min || miss;
 
       // ---- S = Q K^T: n tile t holds keys key0 + 8 t .. + 7 ----
-      float s[MT][TILES][4];
+      float s[TILES][4];
 #pragma unroll
       for (int t = 0; t < TILES; ++t) {
-#pragma unroll
-        for (int m = 0; m < MT; ++m) s[m][t][0] = s[m][t][1] = s[m][t][2] = s[m][t][3] = 0.f;
+        s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
 #pragma unroll
         for (int c = 0; c < R::KI; ++c) {
           const uint4 w = *reinterpret_cast<const uint4*>(st + ((t * R::KI + c) * 32 + lane) * 16);
           if constexpr (!Q8) {
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              mma_bf16_16816(s[m][t], qf[m][2 * c], w.x, w.y);
-              mma_bf16_16816(s[m][t], qf[m][2 * c + 1], w.z, w.w);
-            }
+            mma_bf16_16816(s[t], qf[2 * c], w.x, w.y);
+            mma_bf16_16816(s[t], qf[2 * c + 1], w.z, w.w);
           } else {
             const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const uint32_t b0 = codes2(x[k], 0x4140u), b1 = codes2(x[k], 0x4342u);
-#pragma unroll
-              for (int m = 0; m < MT; ++m) mma_f16(s[m][t], qf[m][4 * c + k], b0, b1);
+              mma_f16(s[t], qf[4 * c + k], b0, b1);
             }
           }
         }
@@ -379,10 +339,7 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
           vsc[t][1] = vq.y;
           vmax = fmaxf(vmax, fmaxf(vq.x, vq.y));
 #pragma unroll
-          for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              s[m][t][e] *= e & 1 ? kq.y : kq.x;
+          for (int e = 0; e < 4; ++e) s[t][e] *= e & 1 ? kq.y : kq.x;
         }
         lv = fmaxf(log2_fast(vmax), -80.f) - 15.f;
       }
@@ -393,66 +350,61 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
           for (int e = 0; e < 4; ++e) {
             const int key = key0 + t * 8 + 2 * tig + (e & 1);
             const bool gone = (miss >> (t >> 1)) & 1u;
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-              if (gone || key > lim[m][e >> 1]) s[m][t][e] = -INFINITY;
+            if (gone || key > lim[e >> 1]) s[t][e] = -INFINITY;
           }
       }
-      uint32_t pf[MT][SUBS][4], pl[MT][SUBS][4];   // P of the 16-key steps (bf16: high and low part)
+      uint32_t pf[SUBS][4], pl[SUBS][4];   // P of the 16-key steps (bf16: high and low part)
+      float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        float top[2] = {-INFINITY, -INFINITY};
+      for (int t = 0; t < TILES; ++t)
 #pragma unroll
-        for (int t = 0; t < TILES; ++t)
+        for (int e = 0; e < 4; ++e) top[e >> 1] = fmaxf(top[e >> 1], s[t][e]);
+      top[0] = fmaf(top[0], qs[0], lv);
+      top[1] = fmaf(top[1], qs[1], lv);
+      if (__any_sync(~0u, top[0] > mx[0] || top[1] > mx[1])) {
+        float corr[2];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) top[e >> 1] = fmaxf(top[e >> 1], s[m][t][e]);
-        top[0] = fmaf(top[0], qs[m][0], lv);
-        top[1] = fmaf(top[1], qs[m][1], lv);
-        if (__any_sync(~0u, top[0] > mx[m][0] || top[1] > mx[m][1])) {
-          float corr[2];
+        for (int h = 0; h < 2; ++h) {
+          top[h] = fmaxf(top[h], __shfl_xor_sync(~0u, top[h], 1));
+          top[h] = fmaxf(top[h], __shfl_xor_sync(~0u, top[h], 2));
+          const float now = fmaxf(mx[h], top[h]);
+          corr[h] = now == -INFINITY ? 1.f : exp2_fast(mx[h] - now);
+          mx[h] = now;
+          l[h] *= corr[h];
+        }
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            top[h] = fmaxf(top[h], __shfl_xor_sync(~0u, top[h], 1));
-            top[h] = fmaxf(top[h], __shfl_xor_sync(~0u, top[h], 2));
-            const float now = fmaxf(mx[m][h], top[h]);
-            corr[h] = now == -INFINITY ? 1.f : exp2_fast(mx[m][h] - now);
-            mx[m][h] = now;
-            l[m][h] *= corr[h];
-          }
+        for (int n = 0; n < ON; ++n) {
+          o[n][0] *= corr[0];
+          o[n][1] *= corr[0];
+          o[n][2] *= corr[1];
+          o[n][3] *= corr[1];
+        }
+      }
+      // a row without a key so far keeps -infinity: subtract 0 there
+      const float ref[2] = {mx[0] == -INFINITY ? 0.f : mx[0],
+                            mx[1] == -INFINITY ? 0.f : mx[1]};
 #pragma unroll
-          for (int n = 0; n < ON; ++n) {
-            o[m][n][0] *= corr[0];
-            o[m][n][1] *= corr[0];
-            o[m][n][2] *= corr[1];
-            o[m][n][3] *= corr[1];
+      for (int t = 0; t < TILES; ++t) {
+        float p[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          p[e] = exp2_fast(fmaf(s[t][e], qs[e >> 1], -ref[e >> 1]));
+          l[e >> 1] += p[e];
+          if constexpr (Q8) {
+            // a masked key's scale may be anything
+            p[e] = edge && s[t][e] == -INFINITY ? 0.f : p[e] * vsc[t][e & 1];
           }
         }
-        // a row without a key so far keeps -infinity: subtract 0 there
-        const float ref[2] = {mx[m][0] == -INFINITY ? 0.f : mx[m][0],
-                              mx[m][1] == -INFINITY ? 0.f : mx[m][1]};
-#pragma unroll
-        for (int t = 0; t < TILES; ++t) {
-          float p[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            p[e] = exp2_fast(fmaf(s[m][t][e], qs[m][e >> 1], -ref[e >> 1]));
-            l[m][e >> 1] += p[e];
-            if constexpr (Q8) {
-              // a masked key's scale may be anything
-              p[e] = edge && s[m][t][e] == -INFINITY ? 0.f : p[e] * vsc[t][e & 1];
-            }
-          }
-          const int step = t >> 1, r0 = (t & 1) * 2;
-          if constexpr (Q8) {
-            pf[m][step][r0] = pack_f16x2(p[0], p[1]);
-            pf[m][step][r0 + 1] = pack_f16x2(p[2], p[3]);
-          } else {
-            const uint32_t a01 = pack_bf16x2(p[0], p[1]), a23 = pack_bf16x2(p[2], p[3]);
-            pf[m][step][r0] = a01;
-            pf[m][step][r0 + 1] = a23;
-            pl[m][step][r0] = pack_bf16x2(p[0] - bf16lo(a01), p[1] - bf16hi(a01));
-            pl[m][step][r0 + 1] = pack_bf16x2(p[2] - bf16lo(a23), p[3] - bf16hi(a23));
-          }
+        const int step = t >> 1, r0 = (t & 1) * 2;
+        if constexpr (Q8) {
+          pf[step][r0] = pack_f16x2(p[0], p[1]);
+          pf[step][r0 + 1] = pack_f16x2(p[2], p[3]);
+        } else {
+          const uint32_t a01 = pack_bf16x2(p[0], p[1]), a23 = pack_bf16x2(p[2], p[3]);
+          pf[step][r0] = a01;
+          pf[step][r0 + 1] = a23;
+          pl[step][r0] = pack_bf16x2(p[0] - bf16lo(a01), p[1] - bf16hi(a01));
+          pl[step][r0 + 1] = pack_bf16x2(p[2] - bf16lo(a23), p[3] - bf16hi(a23));
         }
       }
 
@@ -490,42 +442,36 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
                 const uint32_t b1 = __byte_perm(w[2][j], w[3][j], 0x5410u);
                 const uint32_t d0 = __byte_perm(w[0][j], w[1][j], 0x7632u);
                 const uint32_t d1 = __byte_perm(w[2][j], w[3][j], 0x7632u);
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                  mma_bf16_16816(o[m][c * 8 + 2 * j], pf[m][step], b0, b1);
-                  mma_bf16_16816(o[m][c * 8 + 2 * j + 1], pf[m][step], d0, d1);
-                  mma_bf16_16816(o[m][c * 8 + 2 * j], pl[m][step], b0, b1);
-                  mma_bf16_16816(o[m][c * 8 + 2 * j + 1], pl[m][step], d0, d1);
-                }
+                mma_bf16_16816(o[c * 8 + 2 * j], pf[step], b0, b1);
+                mma_bf16_16816(o[c * 8 + 2 * j + 1], pf[step], d0, d1);
+                mma_bf16_16816(o[c * 8 + 2 * j], pl[step], b0, b1);
+                mma_bf16_16816(o[c * 8 + 2 * j + 1], pl[step], d0, d1);
               }
             } else {
               // element by element: output columns 2 tig + e of n tile 8 c + 2 j + x
 #pragma unroll 1
               for (int key = 0; key < 16; ++key) {
                 const int kt = (key & 7) >> 1, kk = (key >> 3) * 2 + (key & 1);   // its lanes, its piece
+                float pr[2];
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                  float pr[2];
+                for (int h = 0; h < 2; ++h) {
+                  const uint32_t hi =
+                      __shfl_sync(~0u, key & 8 ? pf[step][2 + h] : pf[step][h], g * 4 + kt);
+                  const uint32_t lo =
+                      __shfl_sync(~0u, key & 8 ? pl[step][2 + h] : pl[step][h], g * 4 + kt);
+                  pr[h] = key & 1 ? bf16hi(hi) + bf16hi(lo) : bf16lo(hi) + bf16lo(lo);
+                }
 #pragma unroll
-                  for (int h = 0; h < 2; ++h) {
-                    const uint32_t hi =
-                        __shfl_sync(~0u, key & 8 ? pf[m][step][2 + h] : pf[m][step][h], g * 4 + kt);
-                    const uint32_t lo =
-                        __shfl_sync(~0u, key & 8 ? pl[m][step][2 + h] : pl[m][step][h], g * 4 + kt);
-                    pr[h] = key & 1 ? bf16hi(hi) + bf16hi(lo) : bf16lo(hi) + bf16lo(lo);
-                  }
+                for (int j = 0; j < 4; ++j) {
+                  const uint32_t mine = kk == 0 ? w[0][j] : kk == 1 ? w[1][j] : kk == 2 ? w[2][j] : w[3][j];
 #pragma unroll
-                  for (int j = 0; j < 4; ++j) {
-                    const uint32_t mine = kk == 0 ? w[0][j] : kk == 1 ? w[1][j] : kk == 2 ? w[2][j] : w[3][j];
+                  for (int e = 0; e < 2; ++e) {
+                    const uint32_t x = __shfl_sync(~0u, mine, (2 * tig + e) * 4 + kt);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                      const uint32_t x = __shfl_sync(~0u, mine, (2 * tig + e) * 4 + kt);
-#pragma unroll
-                      for (int h = 0; h < 2; ++h) {
-                        if (pr[h] == 0.f) continue;
-                        o[m][c * 8 + 2 * j][2 * h + e] += pr[h] * bf16lo(x);
-                        o[m][c * 8 + 2 * j + 1][2 * h + e] += pr[h] * bf16hi(x);
-                      }
+                    for (int h = 0; h < 2; ++h) {
+                      if (pr[h] == 0.f) continue;
+                      o[c * 8 + 2 * j][2 * h + e] += pr[h] * bf16lo(x);
+                      o[c * 8 + 2 * j + 1][2 * h + e] += pr[h] * bf16hi(x);
                     }
                   }
                 }
@@ -560,17 +506,14 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
             for (int x = 0; x < 4; ++x) {
               const uint32_t sel = x & 1 ? 0x4342u : 0x4140u;
               const uint32_t b0 = codes2(x < 2 ? a0 : a1, sel), b1 = codes2(x < 2 ? c0 : c1, sel);
-#pragma unroll
-              for (int m = 0; m < MT; ++m) mma_f16(o[m][4 * j + x], pf[m][step], b0, b1);
+              mma_f16(o[4 * j + x], pf[step], b0, b1);
             }
           }
         }
       }
       __syncwarp();   // the stage's scales were read by other lanes
-      if (i + STAGES < n_mine) issue(stage);
+      if (i + STAGES < n_mine) issue(i + STAGES, stage);
       cp_commit();
-      forward();
-      look_up();
       stage = stage + 1 == STAGES ? 0 : stage + 1;
     }
     cp_wait<0>();
@@ -580,29 +523,27 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
     constexpr int WSTRIDE = R::BYTES / 4;
     float* const wo = reinterpret_cast<float*>(ring);   // [RT][D], maxima [RT], sums [RT]
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int h = 0; h < 2; ++h) {
+      const int r = h * 8 + g;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = m * 16 + h * 8 + g;
+      for (int e = 0; e < 2; ++e) {
+        const int gg = 2 * tig + e;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int gg = 2 * tig + e;
-#pragma unroll
-          for (int n = 0; n < ON; n += 4) {
-            const int d = Q8 ? gg * (D / 8) + n : (n >> 3) * 64 + gg * 8 + (n & 7);
-            *reinterpret_cast<float4*>(wo + r * D + d) =
-                make_float4(o[m][n][2 * h + e], o[m][n + 1][2 * h + e], o[m][n + 2][2 * h + e],
-                            o[m][n + 3][2 * h + e]);
-          }
-        }
-        float ls = l[m][h];
-        ls += __shfl_xor_sync(~0u, ls, 1);
-        ls += __shfl_xor_sync(~0u, ls, 2);
-        if (tig == 0) {
-          wo[RT * D + r] = mx[m][h];
-          wo[RT * D + RT + r] = ls;
+        for (int n = 0; n < ON; n += 4) {
+          const int d = Q8 ? gg * (D / 8) + n : (n >> 3) * 64 + gg * 8 + (n & 7);
+          *reinterpret_cast<float4*>(wo + r * D + d) =
+              make_float4(o[n][2 * h + e], o[n + 1][2 * h + e], o[n + 2][2 * h + e],
+                          o[n + 3][2 * h + e]);
         }
       }
+      float ls = l[h];
+      ls += __shfl_xor_sync(~0u, ls, 1);
+      ls += __shfl_xor_sync(~0u, ls, 2);
+      if (tig == 0) {
+        wo[RT * D + r] = mx[h];
+        wo[RT * D + RT + r] = ls;
+      }
+    }
     __syncthreads();
     const bool whole = kb0 == 0 && kb1 == u.n_blocks;
     // a CTA's first piece goes to its slot 0, its last to slot 1
@@ -643,7 +584,6 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
     at = u.begin + kb1;
     if (tid == 0 && at >= line_hi) a.cuts[blockIdx.x] = make_cut(u, kb1, line_lo, per);
   }
-  if (tid == 0 && line_lo >= line_hi) a.cuts[blockIdx.x].pieces = 0;
 }
 
 // ------------------------------------------------------------------- joins --
@@ -651,76 +591,73 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(ChunkArgs a) {
 // lanes hold the pieces' maxima and sums, then four columns each.  A few dependent
 // rounds of reads from L2, at the end of every call: what it needs to know
 // lies ready in the list of cuts.
-constexpr int JOIN_WARPS = 4, JOIN_MAX = 5;   // warps per CTA; 32 * JOIN_MAX pieces at most
+constexpr int JOIN_WARPS = 4;   // per CTA
 constexpr int join_rows(int rt) { return rt <= 32 ? JOIN_WARPS : 4 * JOIN_WARPS; }   // per CTA
 
 template <int D, int RT>
-__global__ void __launch_bounds__(JOIN_WARPS * 32) chunk_join_kernel(ChunkArgs a) {
+__global__ void __launch_bounds__(JOIN_WARPS * 32) chunk_join_kernel(const __grid_constant__ ChunkArgs a) {
   pdl_wait();
   pdl_trigger();
-  const ChunkCut c = a.cuts[blockIdx.x];
+  const int part = blockIdx.x;
+  const ChunkCut c = a.cuts[part];
   if (c.pieces == 0) return;
   constexpr int LANES = D / 4, PER = 32 / LANES;   // lanes per piece, pieces per load
+  constexpr int AHEAD = 8;                          // loads in flight
   const int lane = threadIdx.x & 31, n = c.pieces;
-  const int d = (lane % LANES) * 4, part = lane / LANES;
-  auto slot = [&](int i) { return i == 0 ? c.first : 2 * ((int)blockIdx.x + i); };
+  const int d = (lane % LANES) * 4, mine = lane / LANES;
+  auto slot = [&](int i) { return (int64_t)(i == 0 ? c.first : 2 * (part + i)); };
   const FastDiv by = a.by_group;
-  for (int r = blockIdx.y * join_rows(RT) + (threadIdx.x >> 5); r < (int)(blockIdx.y + 1) * join_rows(RT);
-       r += JOIN_WARPS) {
+  const int r0 = blockIdx.y * join_rows(RT);
+#pragma unroll 1
+  for (int r = r0 + (threadIdx.x >> 5); r < r0 + join_rows(RT); r += JOIN_WARPS) {
     const int row = c.tile * RT + r, q = by.quot(row);
     if (q >= c.rows) break;
-    auto piece = [&](int i) {
-      return __ldcg(reinterpret_cast<const float4*>(a.part_o + ((int64_t)slot(i) * RT + r) * D + d));
-    };
-    // the first pieces' columns are on their way with the maxima
-    constexpr int AHEAD = 8;
+    // pieces from i0 on, PER at a time: their columns, asked for together
     float4 v[AHEAD];
+    auto load = [&](int i0) {
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i)
-      v[i] = i * PER + part < n ? piece(i * PER + part) : make_float4(0.f, 0.f, 0.f, 0.f);
-    float2 ml[JOIN_MAX];
-    float big = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < JOIN_MAX; ++k) {
-      const int i = k * 32 + lane;
-      ml[k] = i < n ? __ldcg(a.part_ml + (int64_t)slot(i) * RT + r) : make_float2(-INFINITY, 0.f);
-      big = fmaxf(big, ml[k].x);
-    }
-    big = warp_max(big);
-    float sum = 0.f;
-#pragma unroll
-    for (int k = 0; k < JOIN_MAX; ++k) {
-      ml[k].x = ml[k].x == -INFINITY ? 0.f : exp2_fast(ml[k].x - big);   // the piece's weight
-      sum = fmaf(ml[k].x, ml[k].y, sum);
-    }
-    sum = warp_sum(sum);
-    float x[4] = {0.f, 0.f, 0.f, 0.f};
-    auto add = [&](float f, const float4& y) {
-      x[0] = fmaf(f, y.x, x[0]);
-      x[1] = fmaf(f, y.y, x[1]);
-      x[2] = fmaf(f, y.z, x[2]);
-      x[3] = fmaf(f, y.w, x[3]);
+      for (int k = 0; k < AHEAD; ++k) {
+        const int i = i0 + k * PER + mine;
+        v[k] = i < n ? __ldcg(reinterpret_cast<const float4*>(a.part_o + (slot(i) * RT + r) * D + d))
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
     };
+    load(0);   // on their way with the maxima
+    auto stats = [&](int i) {
+      return i < n ? __ldcg(a.part_ml + slot(i) * RT + r) : make_float2(-INFINITY, 0.f);
+    };
+    const float2 first = stats(lane);
+    float big = first.x;
+#pragma unroll 1
+    for (int i = 32 + lane; i - lane < n; i += 32) big = fmaxf(big, stats(i).x);
+    big = warp_max(big);
+    auto weight = [&](float m) { return m == -INFINITY ? 0.f : exp2_fast(m - big); };
+    float sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int base = 0; base < n; base += 32) {
+      const float2 ml = base == 0 ? first : stats(base + lane);
+      const float w = weight(ml.x);   // of piece base + lane, 0 if it is not there
+      sum = fmaf(w, ml.y, sum);
+#pragma unroll 1
+      for (int i0 = 0; i0 < 32 && base + i0 < n; i0 += AHEAD * PER) {
+        if (base + i0 > 0) load(base + i0);
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i)   // a piece that is not there has weight 0
-      add(__shfl_sync(~0u, ml[0].x, i * PER + part), v[i]);
-#pragma unroll
-    for (int k = 0; k < JOIN_MAX; ++k) {
-      if (k * 32 >= n) break;
-#pragma unroll 8
-      for (int i0 = k == 0 ? AHEAD * PER : 0; i0 < 32; i0 += PER) {
-        if (k * 32 + i0 >= n) break;
-        const int i = k * 32 + i0 + part;
-        const float f = __shfl_sync(~0u, ml[k].x, i0 + part);
-        if (i < n) add(f, piece(i));
+        for (int k = 0; k < AHEAD; ++k) {
+          const float f = __shfl_sync(~0u, w, i0 + k * PER + mine);
+          x[0] = fmaf(f, v[k].x, x[0]);
+          x[1] = fmaf(f, v[k].y, x[1]);
+          x[2] = fmaf(f, v[k].z, x[2]);
+          x[3] = fmaf(f, v[k].w, x[3]);
+        }
       }
     }
+    sum = warp_sum(sum);
     if constexpr (PER == 2) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[e] += __shfl_xor_sync(~0u, x[e], 16);
     }
     const float inv = big == -INFINITY ? 0.f : 1.f / sum;
-    if (part == 0)
+    if (mine == 0)
       *reinterpret_cast<uint2*>(
           a.O + ((int64_t)(c.row0 + q) * a.n_heads_q + c.head * a.group + row - q * a.group) * D + d) =
           make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
@@ -742,37 +679,36 @@ int sm_count() {
 
 template <int D, int RT>
 int32_t launch_join(const ChunkArgs& a, int n_ctas, cudaStream_t st) {
-  SUB_CHECK_ARG(n_ctas <= 32 * JOIN_MAX, "chunk_attn: more SMs than the join was built for");
   SUB_CUDA_TRY(launch_k(chunk_join_kernel<D, RT>, dim3(n_ctas, RT / join_rows(RT)),
                         dim3(JOIN_WARPS * 32), 0, st, a));
   return SUB_OK;
 }
 
-template <int D, bool Q8, int MT>
+template <int D, bool Q8>
 int32_t launch_decode(const ChunkArgs& a, int n_ctas, cudaStream_t st) {
   static std::once_flag once;
   static cudaError_t err = cudaSuccess;
-  constexpr int SMEM = decode_smem<D, Q8, MT>();
+  constexpr int SMEM = decode_smem<D, Q8>();
   std::call_once(once, [] {
-    err = cudaFuncSetAttribute(chunk_attn_kernel<D, Q8, MT>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    err = cudaFuncSetAttribute(chunk_attn_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               SMEM);
   });
   SUB_CUDA_TRY(err);
-  SUB_CUDA_TRY(launch_k(chunk_attn_kernel<D, Q8, MT>, dim3(n_ctas), dim3(NT), SMEM, st, a));
-  return launch_join<D, MT * 16>(a, n_ctas, st);
+  SUB_CUDA_TRY(launch_k(chunk_attn_kernel<D, Q8>, dim3(n_ctas), dim3(NT), SMEM, st, a));
+  return launch_join<D, RT>(a, n_ctas, st);
 }
 
-// Partial results, two per CTA, and the list of cuts.
-int64_t part_bytes(int n_ctas, int rows, int d) {
-  return (int64_t)n_ctas * (2 * rows * (d + 2) * 4 + (int64_t)sizeof(ChunkCut));
-}
-
-// Rows of a tile, by the rows that a sequence has on average (rows and
-// sequences are known here, lengths only on the device): the smallest that
-// holds them, since a tile streams all its keys.
+// Rows of a tile, by the rows that a sequence has on average (rows and sequences are
+// known here, lengths only on the device).  Up to 16, the warps' kernel streams
+// the keys once; above, its tiles would read them again, and the tensor-core kernel
+// takes over (28 rows, 4000 keys, 8 sequences: 31 us against 37 for tiles of 32
+// rows that way).
 int tile_rows(int group, int n_seqs, int n_rows) {
-  const int64_t rows = (int64_t)n_rows * group;
-  return rows <= 16 * (int64_t)n_seqs ? 16 : rows <= 32 * (int64_t)n_seqs ? 32 : CHUNK_TC_ROWS;
+  return (int64_t)n_rows * group <= RT * (int64_t)n_seqs ? RT : CHUNK_TC_ROWS;
+}
+// Partial results, two per CTA, and the list of cuts.
+int64_t part_bytes(int rows, int d) {
+  return (int64_t)sm_count() * (2 * rows * (d + 2) * 4 + (int64_t)sizeof(ChunkCut));
 }
 
 template <class Cache>
@@ -818,23 +754,22 @@ int32_t chunk_attn(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q, const Cach
     SUB_TRY(scratch.alloc((size_t)need));
     workspace = scratch.p;
   }
-  const int n_ctas = sm_count();
-  a.part_o = reinterpret_cast<float*>(workspace);
   const int rt = tile_rows(a.group, a.t.n_seqs, a.t.n_rows);
-  a.part_ml = reinterpret_cast<float2*>(a.part_o + (int64_t)n_ctas * 2 * rt * kv->head_dim);
-  a.cuts = reinterpret_cast<ChunkCut*>(a.part_ml + (int64_t)n_ctas * 2 * rt);
   const int64_t pool_rows =
       (int64_t)kv->n_layers * kv->n_pages * kv->n_heads_kv * kv->page_size;
-  if (rt == CHUNK_TC_ROWS && chunk_tc_fits(pool_rows)) {
+  const bool tensor_cores = rt == CHUNK_TC_ROWS && chunk_tc_fits(pool_rows);
+  const int n_ctas = sm_count();
+  const int part_rows = tensor_cores ? CHUNK_TC_ROWS : RT;
+  a.part_o = reinterpret_cast<float*>(workspace);
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + (int64_t)n_ctas * 2 * part_rows * kv->head_dim);
+  a.cuts = reinterpret_cast<ChunkCut*>(a.part_ml + (int64_t)n_ctas * 2 * part_rows);
+  if (tensor_cores) {
     SUB_TRY(launch_chunk_tc(a, Q8, kv->head_dim, pool_rows, n_ctas, st));
     return kv->head_dim == 128 ? launch_join<128, CHUNK_TC_ROWS>(a, n_ctas, st)
                                : launch_join<64, CHUNK_TC_ROWS>(a, n_ctas, st);
   }
-  if (rt == 16)
-    return kv->head_dim == 128 ? launch_decode<128, Q8, 1>(a, n_ctas, st)
-                               : launch_decode<64, Q8, 1>(a, n_ctas, st);
-  return kv->head_dim == 128 ? launch_decode<128, Q8, 2>(a, n_ctas, st)
-                             : launch_decode<64, Q8, 2>(a, n_ctas, st);
+  return kv->head_dim == 128 ? launch_decode<128, Q8>(a, n_ctas, st)
+                             : launch_decode<64, Q8>(a, n_ctas, st);
 }
 
 }  // namespace
@@ -850,8 +785,8 @@ extern "C" int32_t sub_chunk_attn_workspace(int32_t n_heads_q, int32_t n_heads_k
   SUB_CHECK_ARG(n_heads_kv >= 1 && n_heads_q >= 1 && n_heads_q % n_heads_kv == 0,
                 "Hq must be a multiple of Hkv");
   SUB_CHECK_ARG(n_seqs >= 1 && n_seqs <= SUB_MAX_SEQS && n_rows >= 0, "bad batch sizes");
-  *bytes = n_rows ? part_bytes(sm_count(), tile_rows(n_heads_q / n_heads_kv, n_seqs, n_rows),
-                               head_dim) : 0;
+  const int rt = tile_rows(n_heads_q / n_heads_kv, n_seqs, n_rows);
+  *bytes = n_rows ? part_bytes(rt, head_dim) : 0;
   return SUB_OK;
 }
 

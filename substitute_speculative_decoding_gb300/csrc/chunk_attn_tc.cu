@@ -24,12 +24,13 @@
 // the rest would make the tensor cores half as slow again.
 //
 // Codes become fp16 values on the way, (code - 128) * scale relative to the power
-// of two of the block's largest scale, rounded once (half a step 2^-11, three bits
+// of two of the block's largest scale, rounded to half a step of 2^-11 (three bits
 // finer than the bf16 values of the other cache): the power of K's scales goes into
 // the scores' factor, that of V's into the weights.  (Scales applied to scores and weights,
 // column by column, would be exact, but cost every row 2 * 128 reads of shared
-// memory per block: the softmax then took 2.7 times as long.)  The scale enters in two fp16
-// parts, so that a row's values do not all share its rounding.
+// memory per block: the softmax then took 2.7 times as long.)  K's scale enters in two
+// fp16 parts, so that its rounding is not common to all terms of a score; V's in one,
+// like a rounding of the weight.
 //
 // V rows past the tile's last key hold anything, and so may keys of the chunk
 // that only later rows read.  In blocks that not all rows read to the end the first
@@ -815,7 +816,7 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
           auto value = [&](uint32_t word, uint32_t sel) {
             const uint32_t x = codes2(word, sel);
             const __half2 h = *reinterpret_cast<const __half2*>(&x);
-            const __half2 y = __hfma2(h, hi2, __hmul2(h, lo2));
+            const __half2 y = side ? __hmul2(h, hi2) : __hfma2(h, hi2, __hmul2(h, lo2));
             return *reinterpret_cast<const uint32_t*>(&y);
           };
           const uint32_t at = dst + (i % HV) * (KB * 128) + i / HV * (KEYS * 128) + line;

@@ -8,7 +8,7 @@
 // no scratch.  Rows are read in aligned groups of four values whatever V is:
 // a row that starts `mis` values past a 16-byte boundary has groups
 // [4 g - mis, 4 g - mis + 4), of which the first and last may be partial.
-#include <algorithm>
+#include <cmath>
 #include <cooperative_groups.h>
 #include "common.cuh"
 
@@ -22,19 +22,23 @@ constexpr int64_t MAX_V = 1 << 20;
 
 struct Row {
   int64_t V;
-  int mis;
+  int mis, n;               // groups
+  int inner, n_inner;       // whole ones: n_inner from `inner` on
   __device__ Row(const float* z, int64_t v)
-      : V(v), mis((int)((reinterpret_cast<uintptr_t>(z) >> 2) & 3)) {}
-  __device__ int groups() const { return (int)((V + mis + 3) / 4); }
+      : V(v), mis((int)((reinterpret_cast<uintptr_t>(z) >> 2) & 3)) {
+    n = (int)((V + mis + 3) / 4);
+    inner = mis ? 1 : 0;
+    n_inner = max(0, n - ((V + mis) % 4 ? 1 : 0) - inner);
+  }
   __device__ int64_t first(int g) const { return (int64_t)g * 4 - mis; }   // may be < 0 in group 0
-  __device__ bool whole(int g) const { return first(g) >= 0 && first(g) + 4 <= V; }
+  __device__ bool whole(int g) const { return (unsigned)(g - inner) < (unsigned)n_inner; }
 };
 
 // Group g of row z; `none` where the row has no value.
 template <bool VEC = true>
 __device__ __forceinline__ float4 load_group(const float* z, const Row& r, int g, float none) {
+  if (VEC && r.whole(g)) return *(reinterpret_cast<const float4*>(z - r.mis) + g);
   const int64_t e = r.first(g);
-  if (VEC && r.whole(g)) return *reinterpret_cast<const float4*>(z + e);
   float4 x;
   x.x = e >= 0 && e < r.V ? z[e] : none;
   x.y = e + 1 >= 0 && e + 1 < r.V ? z[e + 1] : none;
@@ -52,6 +56,32 @@ __device__ __forceinline__ void cluster_all_here() {
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
 
+// Two fp32 operations in one instruction.
+union F2 {
+  float2 f;
+  uint64_t u;
+};
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  F2 x{a}, y{b}, z{c}, d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.u) : "l"(x.u), "l"(y.u), "l"(z.u));
+  return d.f;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  F2 x{a}, y{b}, d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.u) : "l"(x.u), "l"(y.u));
+  return d.f;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  F2 x{a}, y{b}, d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.u) : "l"(x.u), "l"(y.u));
+  return d.f;
+}
+__device__ __forceinline__ float exp2_fast(float x) {   // 2 ulp; flushes below 2^-126
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // A CTA's share of a row's groups.
 __device__ __forceinline__ void share(int groups, int rank, int size, int& lo, int& hi) {
   const int per = (groups + size - 1) / size;
@@ -67,10 +97,8 @@ __device__ __forceinline__ void share(int groups, int rank, int size, int& lo, i
 // the passes left room for two CTAs per SM, and a cluster's copies, sums and
 // stores did not overlap enough: 4.1 TB/s on 576 rows of 128256.)  The CTAs exchange maxima
 // and sums in one cluster barrier.
-constexpr int PROBS_MLP = 4;
-
-template <int THREADS>
-__global__ void __launch_bounds__(THREADS, 1536 / THREADS) probs_kernel(const float* logits, int64_t V,
+template <int THREADS, int MLP>   // MLP: groups a thread loads in one round
+__global__ void __launch_bounds__(THREADS, THREADS > 512 ? 1 : 1280 / THREADS) probs_kernel(const float* logits, int64_t V,
                                                                         float c_hi, float c_lo,
                                                                         float* probs) {
   constexpr int WARPS = THREADS / 32;
@@ -86,9 +114,17 @@ __global__ void __launch_bounds__(THREADS, 1536 / THREADS) probs_kernel(const fl
   float* out = probs + row * V;
   const Row r(z, V);
   int lo, hi;
-  share(r.groups(), rank, size, lo, hi);
-  // exp(d / T) = 2^(d c), c = log2(e) / T in two parts: one rounding of d c
-  auto expo = [&](float d) { return d == -INFINITY ? 0.f : exp2f(fmaf(d, c_hi, d * c_lo)); };
+  share(r.n, rank, size, lo, hi);
+  // exp(d / T) = 2^(d c), c = log2(e) / T in two parts: one rounding of d c.  (Both
+  // are positive, so that d = -infinity gives 0.)
+  auto expo = [&](float d) { return exp2_fast(fmaf(d, c_hi, d * c_lo)); };
+  const float2 hi2 = make_float2(c_hi, c_hi), lo2 = make_float2(c_lo, c_lo);
+  auto expo4 = [&](const float4& x, float minus) {   // of x + minus, two at a time
+    const float2 r2 = make_float2(minus, minus);
+    const float2 a = add2(make_float2(x.x, x.y), r2), b = add2(make_float2(x.z, x.w), r2);
+    const float2 ea = fma2(a, hi2, mul2(a, lo2)), eb = fma2(b, hi2, mul2(b, lo2));
+    return make_float4(exp2_fast(ea.x), exp2_fast(ea.y), exp2_fast(eb.x), exp2_fast(eb.y));
+  };
   auto merge = [&](float& m, float& s, float m2, float s2) {   // sums relative to their maxima
     const float big = fmaxf(m, m2);
     if (m2 == -INFINITY && s2 == 0.f) return;
@@ -96,23 +132,25 @@ __global__ void __launch_bounds__(THREADS, 1536 / THREADS) probs_kernel(const fl
     m = big;
   };
   float m = -INFINITY, s = 0.f;
-  for (int g0 = lo + threadIdx.x; g0 < hi; g0 += PROBS_MLP * THREADS) {
-    float4 x[PROBS_MLP];
+  float4 x[MLP];
+  for (int g0 = lo + threadIdx.x; g0 < hi; g0 += MLP * THREADS) {
 #pragma unroll
-    for (int k = 0; k < PROBS_MLP; ++k)
+    for (int k = 0; k < MLP; ++k)
       x[k] = g0 + k * THREADS < hi ? load_group(z, r, g0 + k * THREADS, -INFINITY)
                                    : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
     float big = m;
 #pragma unroll
-    for (int k = 0; k < PROBS_MLP; ++k)
+    for (int k = 0; k < MLP; ++k)
       big = fmaxf(fmaxf(big, fmaxf(x[k].x, x[k].y)), fmaxf(x[k].z, x[k].w));
     // no logit above -infinity so far: every value is 0 whatever the reference
     const float ref = big == -INFINITY ? 0.f : big;
     s *= expo(m - ref);
     m = big;
 #pragma unroll
-    for (int k = 0; k < PROBS_MLP; ++k)
-      s += (expo(x[k].x - ref) + expo(x[k].y - ref)) + (expo(x[k].z - ref) + expo(x[k].w - ref));
+    for (int k = 0; k < MLP; ++k) {
+      const float4 e = expo4(x[k], -ref);
+      s += (e.x + e.y) + (e.z + e.w);
+    }
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1)
@@ -133,24 +171,24 @@ __global__ void __launch_bounds__(THREADS, 1536 / THREADS) probs_kernel(const fl
     for (int i = 0; i < size; ++i) merge(m, s, s_peer[i].x, s_peer[i].y);
   }
   const float ref = m == -INFINITY ? 0.f : m, f = s == 0.f ? 0.f : 1.f / s;
-  for (int g0 = lo + threadIdx.x; g0 < hi; g0 += PROBS_MLP * THREADS) {
-    float4 x[PROBS_MLP];
+  const bool again = hi - lo > MLP * THREADS;   // a single round is still in registers
+  for (int g0 = lo + threadIdx.x; g0 < hi; g0 += MLP * THREADS) {
 #pragma unroll
-    for (int k = 0; k < PROBS_MLP; ++k)
-      if (g0 + k * THREADS < hi) x[k] = load_group(z, r, g0 + k * THREADS, -INFINITY);
+    for (int k = 0; k < MLP; ++k)
+      if (again && g0 + k * THREADS < hi) x[k] = load_group(z, r, g0 + k * THREADS, -INFINITY);
 #pragma unroll
-    for (int k = 0; k < PROBS_MLP; ++k) {
+    for (int k = 0; k < MLP; ++k) {
       const int g = g0 + k * THREADS;
       if (g >= hi) break;
-      const int64_t e = r.first(g);
-      const float w[4] = {expo(x[k].x - ref) * f, expo(x[k].y - ref) * f, expo(x[k].z - ref) * f,
-                          expo(x[k].w - ref) * f};
+      const float4 e = expo4(x[k], -ref);
+      const float w[4] = {e.x * f, e.y * f, e.z * f, e.w * f};
       if (r.whole(g)) {
-        __stcs(reinterpret_cast<float4*>(out + e), make_float4(w[0], w[1], w[2], w[3]));
+        __stcs(reinterpret_cast<float4*>(out - r.mis) + g, make_float4(w[0], w[1], w[2], w[3]));
       } else {
+        const int64_t at = r.first(g);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (e + i >= 0 && e + i < V) out[e + i] = w[i];
+          if (at + i >= 0 && at + i < V) out[at + i] = w[i];
       }
     }
   }
@@ -242,7 +280,7 @@ __global__ void __launch_bounds__(VER_THREADS, 4) verify_kernel(VerifyArgs a) {
   const Row r(p, a.V);
   const bool q_vec = q && ((reinterpret_cast<uintptr_t>(q) >> 2) & 3) == (unsigned)r.mis;
   int lo, hi;
-  share(r.groups(), me, size * VER_WARPS, lo, hi);
+  share(r.n, me, size * VER_WARPS, lo, hi);
   // rint(x 2^43) = high 2^22 + low for x in [0, 1]: high = rint(x 2^21) in 23 bits over
   // 2^23, low = rint(rest 2^22) in -2^21 .. 2^21 over 3 2^22
   constexpr uint32_t HIGH0 = 0x4B000000u, LOW0 = 0x4B400000u;
@@ -395,15 +433,25 @@ extern "C" int32_t sub_probs(const float* logits, int64_t rows, int64_t V, float
   SUB_CHECK_ARG(logits && probs, "null pointer");
   SUB_CHECK_ARG(aligned16(logits) && aligned16(probs), "logits and probs must be 16-byte aligned");
   const double c = 1.4426950408889634074 / (double)temperature;
-  const float c_hi = (float)c, c_lo = (float)(c - (double)c_hi);
+  float c_hi = (float)c;
+  if ((double)c_hi >= c) c_hi = std::nextafterf(c_hi, 0.f);
+  const float c_lo = (float)(c - (double)c_hi);
   const cudaStream_t st = as_stream(stream);
-  if (V <= 2048) {   // a row of one round of loads
-    SUB_CUDA_TRY(launch_clusters(probs_kernel<128>, rows, 1, 128, st, logits, V, c_hi, c_lo, probs));
+  // A round of a CTA's loads takes 16 values per thread.  Rows of one round: one
+  // small CTA.  Longer ones: a cluster whose CTAs need two rounds at most, or as many
+  // CTAs as there are SMs (448 rows of 5000: 9 us, against 23 us as clusters of eight).
+  // The few rows that leave SMs idle get CTAs that hold a share in registers, if it
+  // fits, and skip the second reading (1 row of 152064: 9 us against 12).
+  if (V <= 2048) {
+    SUB_CUDA_TRY(launch_clusters(probs_kernel<128, 4>, rows, 1, 128, st, logits, V, c_hi, c_lo, probs));
     return SUB_OK;
   }
-  // long rows over a cluster: rows in work at a time stay in L2, and few rows use more SMs
-  const int size = V <= 16384 && rows >= 608 ? 1 : MAX_CLUSTER;
-  SUB_CUDA_TRY(launch_clusters(probs_kernel<256>, rows, size, 256, st, logits, V, c_hi, c_lo, probs));
+  int size = 1;
+  while (size < MAX_CLUSTER && (V > size * 8192 || (rows * size < 152 && V > size * 4096))) size *= 2;
+  if (rows * size <= 152 && V > size * 4096 && V <= size * 20480 - 4)
+    SUB_CUDA_TRY(launch_clusters(probs_kernel<1024, 5>, rows, size, 1024, st, logits, V, c_hi, c_lo, probs));
+  else
+    SUB_CUDA_TRY(launch_clusters(probs_kernel<256, 4>, rows, size, 256, st, logits, V, c_hi, c_lo, probs));
   return SUB_OK;
 }
 

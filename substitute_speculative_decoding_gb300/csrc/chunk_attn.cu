@@ -119,9 +119,14 @@ struct Ring {
 
 template <int D, bool Q8>
 constexpr int decode_smem() {
-  // a warp's partial result (16 rows of D floats, maxima and sums) reuses its ring
-  static_assert(Ring<D, Q8>::BYTES >= RT * (D + 2) * 4, "the ring holds the partial result");
+  static_assert(Ring<D, Q8>::STAGE >= RT * D * 4, "a stage holds a warp's partial result");
   return WARPS * Ring<D, Q8>::BYTES;
+}
+
+// A barrier of two warps.
+__device__ __forceinline__ void bar_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void bar_arrive(int id) {
+  asm volatile("bar.arrive %0, 64;" ::"r"(id) : "memory");
 }
 
 // ------------------------------------------------------------------ kernel --
@@ -131,6 +136,8 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(const __grid_constant
   constexpr int KS = D / 16, ON = D / 8, KB = R::KB, SUBS = R::SUBS, TILES = KB / 8;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t s_pre[SUB_MAX_SEQS + 1];
+  __shared__ int s_at[WARPS];          // their stages
+  __shared__ float4 s_ml[WARPS][32];   // maxima and sums of the warps' partial results, by lane
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -140,46 +147,63 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(const __grid_constant
   plan.template scan<NT>(s_pre);
   const int64_t total = s_pre[a.t.n_seqs];
   const int64_t per = blocks_per_cta(total, gridDim.x, WARPS);
-  uint8_t* const ring = smem + warp * R::BYTES;
+  const uint8_t* const ring = smem + warp * R::BYTES;
   const uint32_t ring_s = smem_u32(ring);
   // a lane's place in the first key of a step, of K and of V
   const uint8_t* const kp = reinterpret_cast<const uint8_t*>(a.k) + g * R::ROW + tig * 16;
   const uint8_t* const vp = reinterpret_cast<const uint8_t*>(a.v) + 2 * tig * R::ROW + g * R::VB;
   const int64_t page_rows = (int64_t)a.n_heads_kv * ps;
   const int64_t line_lo = blockIdx.x * per, line_hi = min(total, line_lo + per);
-  ChunkUnit u;
-  if (line_lo < line_hi) u = plan.find(s_pre, line_lo);
-  else if (tid == 0) a.cuts[blockIdx.x].pieces = 0;
-  for (int64_t at = line_lo; at < line_hi; plan.next(u)) {
-    const int kb0 = (int)(at - u.begin);
-    const int kb1 = (int)min((int64_t)u.n_blocks, line_hi - u.begin);
-    const int n_mine = (kb1 - kb0 - warp + WARPS - 1) / WARPS;   // blocks kb0 + warp + i * WARPS
-    const int32_t* const pages = a.t.pages + (int64_t)u.b * a.t.width;
-    const int64_t row_base = ((int64_t)a.layer * a.t.n_pages * a.n_heads_kv + u.head) * ps;
+  if (line_lo >= line_hi) {
+    if (tid == 0) a.cuts[blockIdx.x].pieces = 0;
+    return;
+  }
+  ChunkUnit u = plan.find(s_pre, line_lo);
 
-    // Pool rows of the warp's next 32 16-key steps (-1: no page), one looked up by
-    // each lane, and of the 32 after them: a step's place is a shuffle away.
-    auto look_up = [&](int step) -> int64_t {
-      const int key = (kb0 + warp + step / SUBS * WARPS) * KB + step % SUBS * 16;
-      if (key >= u.n_keys || step >= n_mine * SUBS) return -1;
-      const int entry = a.by_page.quot(key), page = pages[entry];
-      if ((unsigned)page >= (unsigned)a.t.n_pages) return -1;
-      return row_base + (int64_t)page * page_rows + (key - entry * ps);
-    };
-    int64_t places = look_up(lane), places2 = look_up(32 + lane);
-    uint32_t missing = 0;   // bits SUBS * stage + step: no page there
-    auto issue = [&](int i, int stage) {
+  // ---- the loads: the warp's blocks of all its units, one after the other ----
+  // unit f, of which the warp reads blocks f0 + warp + i * WARPS, i < fn
+  ChunkUnit f = u;
+  int f0, fn, fi;
+  const int32_t* pages;
+  int64_t row_base, places, places2;
+  // Pool rows of the warp's next 32 16-key steps (-1: no page), one looked up by
+  // each lane, and of the 32 after them: a step's place is a shuffle away.
+  auto look_up = [&](int step) -> int64_t {
+    const int key = (f0 + warp + step / SUBS * WARPS) * KB + step % SUBS * 16;
+    if (key >= f.n_keys || step >= fn * SUBS) return -1;
+    const int entry = a.by_page.quot(key), page = pages[entry];
+    if ((unsigned)page >= (unsigned)a.t.n_pages) return -1;
+    return row_base + (int64_t)page * page_rows + (key - entry * ps);
+  };
+  auto open = [&](int64_t at) {
+    for (;;) {
+      f0 = (int)(at - f.begin);
+      const int f1 = (int)min((int64_t)f.n_blocks, line_hi - f.begin);
+      fn = (f1 - f0 - warp + WARPS - 1) / WARPS;
+      fi = 0;
+      at = f.begin + f1;
+      if (fn > 0 || at >= line_hi) break;
+      plan.next(f);
+    }
+    pages = a.t.pages + (int64_t)f.b * a.t.width;
+    row_base = ((int64_t)a.layer * a.t.n_pages * a.n_heads_kv + f.head) * ps;
+    places = look_up(lane);
+    places2 = look_up(32 + lane);
+  };
+  uint32_t missing = 0;   // bits SUBS * stage + step: no page there
+  auto feed = [&](int stage) {
+    if (fi < fn) {
       const uint32_t dst = ring_s + stage * R::STAGE;
-      if (i > 0 && i % (32 / SUBS) == 0) {
+      if (fi > 0 && fi % (32 / SUBS) == 0) {
         places = places2;
-        places2 = look_up(i * SUBS + 32 + lane);
+        places2 = look_up(fi * SUBS + 32 + lane);
       }
 #pragma unroll
       for (int s = 0; s < SUBS; ++s) {
-        const int64_t place = __shfl_sync(~0u, places, (i * SUBS + s) & 31);
+        const int64_t place = __shfl_sync(~0u, places, (fi * SUBS + s) & 31);
         const bool have = place >= 0;
         const int64_t row0 = have ? place : 0;
-        const int left = have ? u.n_keys - ((kb0 + warp + i * WARPS) * KB + 16 * s) : 0;   // keys of the step
+        const int left = have ? f.n_keys - ((f0 + warp + fi * WARPS) * KB + 16 * s) : 0;   // keys of the step
         const int bit = SUBS * stage + s;
         missing = (missing & ~(1u << bit)) | ((have ? 0u : 1u) << bit);
         const uint8_t* const k0 = kp + row0 * R::ROW;
@@ -219,12 +243,26 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(const __grid_constant
                          (lane < 16 ? a.ks : a.vs) + row0 + key, a.ks, key < left);
         }
       }
-    };
-#pragma unroll 1
-    for (int i = 0; i < STAGES; ++i) {
-      if (i < n_mine) issue(i, i);
-      cp_commit();
+      if (++fi == fn) {
+        const int64_t end = f.begin + min((int64_t)f.n_blocks, line_hi - f.begin);
+        if (end < line_hi) {
+          plan.next(f);
+          open(end);
+        }
+      }
     }
+    cp_commit();
+  };
+  open(line_lo);
+#pragma unroll 1
+  for (int i = 0; i < STAGES - 1; ++i) feed(i);
+
+  int stage = 0;          // of the next block
+  int owed = 0;           // the barrier after which the last partial result has been read
+  for (int64_t at = line_lo; at < line_hi; plan.next(u)) {
+    const int kb0 = (int)(at - u.begin);
+    const int kb1 = (int)min((int64_t)u.n_blocks, line_hi - u.begin);
+    const int n_mine = (kb1 - kb0 - warp + WARPS - 1) / WARPS;   // blocks kb0 + warp + i * WARPS
 
     // ---- Q fragments, and the rows' last visible key ----
     uint32_t qf[KS][4];
@@ -295,8 +333,10 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(const __grid_constant
 #pragma unroll
     for (int i = 0; i < ON; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
-    int stage = 0;
+    if (owed) bar_sync(owed);
+    owed = 0;
     for (int i = 0; i < n_mine; ++i) {
+      feed(stage == 0 ? STAGES - 1 : stage - 1);   // the stage that was read last
       cp_wait<STAGES - 1>();
       __syncwarp();
       const int key0 = (kb0 + warp + i * WARPS) * KB;
@@ -512,78 +552,99 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(const __grid_constant
         }
       }
       __syncwarp();   // the stage's scales were read by other lanes
-      if (i + STAGES < n_mine) issue(i + STAGES, stage);
-      cp_commit();
       stage = stage + 1 == STAGES ? 0 : stage + 1;
     }
-    cp_wait<0>();
-    __syncwarp();
 
-    // ---- the warps' results into their rings, then joined in warp order ----
-    constexpr int WSTRIDE = R::BYTES / 4;
-    float* const wo = reinterpret_cast<float*>(ring);   // [RT][D], maxima [RT], sums [RT]
+    // ---- the warps' results, joined pairwise: 4 .. 7 into 0 .. 3, 2, 3 into 0, 1, 1 into 0 ----
+    // A result travels through the stage that its warp has read last, fragments as
+    // they are; the loads of the next unit stay on their way meanwhile.
+    auto slot_of = [&](int w, int st) {
+      return reinterpret_cast<float4*>(smem + w * R::BYTES + st * R::STAGE);
+    };
+#pragma unroll 1
+    for (int r = WARPS / 2; r > 0; r >>= 1) {
+      if (warp >= 2 * r) break;
+      const int there = warp & (r - 1);                    // the pair (there, there + r)
+      const int full = r + there, free = WARPS - 1 + full;   // its barriers, 1 .. 14
+      if (warp >= r) {
+        if (n_mine > 0) {
+          float4* const out = slot_of(warp, stage == 0 ? STAGES - 1 : stage - 1) + lane;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = h * 8 + g;
+          for (int n = 0; n < ON; ++n) out[n * 32] = make_float4(o[n][0], o[n][1], o[n][2], o[n][3]);
+          s_ml[warp][lane] = make_float4(mx[0], mx[1], l[0], l[1]);
+          s_at[warp] = stage == 0 ? STAGES - 1 : stage - 1;
+        }
+        bar_arrive(full);
+        owed = free;
+        break;
+      }
+      bar_sync(full);
+      const int w = warp + r;
+      if (kb1 - kb0 > w) {   // it had blocks
+        const float4 ml = s_ml[w][lane];
+        const float4* const in = slot_of(w, s_at[w]) + lane;
+        const float m[2] = {ml.x, ml.y};
+        float c0[2], c1[2];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int gg = 2 * tig + e;
+        for (int h = 0; h < 2; ++h) {
+          const float big = fmaxf(mx[h], m[h]);
+          c0[h] = big == -INFINITY ? 1.f : exp2_fast(mx[h] - big);
+          c1[h] = big == -INFINITY ? 1.f : exp2_fast(m[h] - big);
+          mx[h] = big;
+          l[h] = l[h] * c0[h] + (h ? ml.w : ml.z) * c1[h];
+        }
 #pragma unroll
-        for (int n = 0; n < ON; n += 4) {
-          const int d = Q8 ? gg * (D / 8) + n : (n >> 3) * 64 + gg * 8 + (n & 7);
-          *reinterpret_cast<float4*>(wo + r * D + d) =
-              make_float4(o[n][2 * h + e], o[n + 1][2 * h + e], o[n + 2][2 * h + e],
-                          o[n + 3][2 * h + e]);
+        for (int n = 0; n < ON; ++n) {
+          const float4 v = in[n * 32];
+          o[n][0] = o[n][0] * c0[0] + v.x * c1[0];
+          o[n][1] = o[n][1] * c0[0] + v.y * c1[0];
+          o[n][2] = o[n][2] * c0[1] + v.z * c1[1];
+          o[n][3] = o[n][3] * c0[1] + v.w * c1[1];
         }
       }
-      float ls = l[h];
-      ls += __shfl_xor_sync(~0u, ls, 1);
-      ls += __shfl_xor_sync(~0u, ls, 2);
-      if (tig == 0) {
-        wo[RT * D + r] = mx[h];
-        wo[RT * D + RT + r] = ls;
+      bar_arrive(free);
+    }
+    if (warp == 0) {
+      const bool whole = kb0 == 0 && kb1 == u.n_blocks;
+      // a CTA's first piece goes to its slot 0, its last to slot 1
+      const int64_t slot = 2 * (int64_t)blockIdx.x + (at == line_lo ? 0 : 1);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        l[h] += __shfl_xor_sync(~0u, l[h], 1);
+        l[h] += __shfl_xor_sync(~0u, l[h], 2);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = h * 8 + g, row = u.tile * RT + r, q = a.by_group.quot(row);
+        if (q >= u.rows) continue;
+        const float inv = mx[h] == -INFINITY ? 0.f : 1.f / l[h];
+        uint16_t* const to =
+            a.O + ((int64_t)(u.row0 + q) * a.n_heads_q + u.head * G + row - q * G) * D;
+        float* const part = a.part_o + (slot * RT + r) * D;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int n = 0; n < ON; n += 8) {   // columns d .. d + 7
+            const int d = Q8 ? (2 * tig + e) * (D / 8) + n : n * 8 + (2 * tig + e) * 8;
+            float x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = o[n + k][2 * h + e];
+            if (whole) {
+              *reinterpret_cast<uint4*>(to + d) =
+                  make_uint4(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv),
+                             pack_bf16x2(x[4] * inv, x[5] * inv), pack_bf16x2(x[6] * inv, x[7] * inv));
+            } else {
+              __stcg(reinterpret_cast<float4*>(part + d), make_float4(x[0], x[1], x[2], x[3]));
+              __stcg(reinterpret_cast<float4*>(part + d + 4), make_float4(x[4], x[5], x[6], x[7]));
+            }
+          }
+        if (!whole && tig == 0) __stcg(a.part_ml + slot * RT + r, make_float2(mx[h], l[h]));
       }
     }
-    __syncthreads();
-    const bool whole = kb0 == 0 && kb1 == u.n_blocks;
-    // a CTA's first piece goes to its slot 0, its last to slot 1
-    const int64_t slot = 2 * (int64_t)blockIdx.x + (at == line_lo ? 0 : 1);
-    const float* const all = reinterpret_cast<const float*>(smem);
-    for (int idx = tid; idx < RT * (D / 4); idx += NT) {
-      const int r = idx / (D / 4), d = (idx % (D / 4)) * 4;
-      const int row = u.tile * RT + r, q = a.by_group.quot(row);
-      if (q >= u.rows) continue;
-      float big = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) big = fmaxf(big, all[w * WSTRIDE + RT * D + r]);
-      float sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) {
-        const float* const pw = all + w * WSTRIDE;
-        const float mw = pw[RT * D + r];
-        if (mw == -INFINITY) continue;
-        const float f = exp2_fast(mw - big);
-        const float4 v = *reinterpret_cast<const float4*>(pw + r * D + d);
-        sum = fmaf(f, pw[RT * D + RT + r], sum);
-        x[0] = fmaf(f, v.x, x[0]);
-        x[1] = fmaf(f, v.y, x[1]);
-        x[2] = fmaf(f, v.z, x[2]);
-        x[3] = fmaf(f, v.w, x[3]);
-      }
-      if (whole) {
-        const float inv = big == -INFINITY ? 0.f : 1.f / sum;
-        *reinterpret_cast<uint2*>(a.O + ((int64_t)(u.row0 + q) * a.n_heads_q + u.head * G + row - q * G) * D + d) =
-            make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
-      } else {
-        __stcg(reinterpret_cast<float4*>(a.part_o + (slot * RT + r) * D + d),
-               make_float4(x[0], x[1], x[2], x[3]));
-        if (d == 0) __stcg(a.part_ml + slot * RT + r, make_float2(big, sum));
-      }
-    }
-    __syncthreads();
     at = u.begin + kb1;
     if (tid == 0 && at >= line_hi) a.cuts[blockIdx.x] = make_cut(u, kb1, line_lo, per);
   }
+  if (owed) bar_sync(owed);
 }
 
 // ------------------------------------------------------------------- joins --

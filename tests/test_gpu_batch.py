@@ -307,6 +307,19 @@ def test_later_keys_do_not_reach_earlier_rows(sub, n, bad):
     assert torch.isfinite(torch.cat([o[early], o[n:]])).all()
 
 
+@pytest.mark.parametrize("bits,d", [(16, 128), (16, 64), (8, 128), (8, 64)])
+@pytest.mark.parametrize("n", [1, 3, 40])
+def test_a_key_that_is_not_a_number_is_not_lost(sub, bits, d, n):
+    """A NaN in K that rows read, alone in its block for the first of them."""
+    c = Case(sub, [(128, n), (20, 1)], 8, 2, d, bits=bits, seed=6)
+    pg, pl = int(c.table[0, 128 // 16]), 128 % 16
+    where = c.pools[0] if bits == 16 else c.scales[0]
+    where[c.layer, pg, 0, pl] = float("nan")
+    o = sub.chunk_attn(c.q.to(DEV), c.kv, c.layer, c.batch)
+    assert torch.isnan(o[:n, :4]).all()
+    assert torch.isfinite(o[:n, 4:]).all() and torch.isfinite(o[n:]).all()
+
+
 def test_scales_and_queries_of_any_size_in_an_8_bit_cache(sub):
     """Scales over 2^-60 .. 2^60 and queries of 2^-90 .. 2^60: sums stay in range."""
     for n in (1, 140):

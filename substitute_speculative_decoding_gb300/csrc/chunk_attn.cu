@@ -347,22 +347,32 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(const __grid_constant
       // ---- S = Q K^T: n tile t holds keys key0 + 8 t .. + 7 ----
       float s[TILES][4];
 #pragma unroll
-      for (int t = 0; t < TILES; ++t) {
-        s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+      for (int t = 0; t < TILES; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
 #pragma unroll
-        for (int c = 0; c < R::KI; ++c) {
-          const uint4 w = *reinterpret_cast<const uint4*>(st + ((t * R::KI + c) * 32 + lane) * 16);
-          if constexpr (!Q8) {
-            mma_bf16_16816(s[t], qf[2 * c], w.x, w.y);
-            mma_bf16_16816(s[t], qf[2 * c + 1], w.z, w.w);
-          } else {
-            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+      for (int c = 0; c < R::KI; ++c) {   // (the tiles in turn: their sums do not wait for each other)
+        uint32_t w[TILES][4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t b0 = codes2(x[k], 0x4140u), b1 = codes2(x[k], 0x4342u);
+        for (int t = 0; t < TILES; ++t) {
+          const uint4 x = *reinterpret_cast<const uint4*>(st + ((t * R::KI + c) * 32 + lane) * 16);
+          w[t][0] = x.x;
+          w[t][1] = x.y;
+          w[t][2] = x.z;
+          w[t][3] = x.w;
+        }
+        if constexpr (!Q8) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int t = 0; t < TILES; ++t)
+              mma_bf16_16816(s[t], qf[2 * c + k], w[t][2 * k], w[t][2 * k + 1]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int t = 0; t < TILES; ++t) {
+              const uint32_t b0 = codes2(w[t][k], 0x4140u), b1 = codes2(w[t][k], 0x4342u);
               mma_f16(s[t], qf[4 * c + k], b0, b1);
             }
-          }
         }
       }
 

@@ -770,13 +770,15 @@ int32_t launch_decode(const ChunkArgs& a, int n_ctas, cudaStream_t st) {
 }
 
 // Rows of a tile, by the rows that a sequence has on average (rows and sequences are
-// known here, lengths only on the device).  Up to 16, the warps' kernel streams
-// the keys once; above, its tiles would read them again, and the tensor-core kernel
-// takes over (28 rows, 4000 keys, 8 sequences: 31 us against 37 for tiles of 32
-// rows that way).
-int tile_rows(int group, int n_seqs, int n_rows) {
-  return (int64_t)n_rows * group <= RT * (int64_t)n_seqs ? RT : CHUNK_TC_ROWS;
+// known here, lengths only on the device).  The warps' kernel reads the keys again
+// for every tile of 16 rows, the tensor-core kernel once for 256.  bf16: 16 rows
+// (8 sequences over 4000 keys: 32 rows 39 us by the tensor cores, 42 here, 64 rows 39
+// and 63).  Codes, which the tensor-core kernel has to convert first: 64 rows (32 rows
+// 51 and 34, 64 rows 53 and 49).
+int tile_rows(int group, int n_seqs, int n_rows, bool codes) {
+  return (int64_t)n_rows * group <= (codes ? 4 : 1) * RT * (int64_t)n_seqs ? RT : CHUNK_TC_ROWS;
 }
+
 // Partial results, two per CTA, and the list of cuts.
 int64_t part_bytes(int rows, int d) {
   return (int64_t)sm_count() * (2 * rows * (d + 2) * 4 + (int64_t)sizeof(ChunkCut));
@@ -825,7 +827,7 @@ int32_t chunk_attn(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q, const Cach
     SUB_TRY(scratch.alloc((size_t)need));
     workspace = scratch.p;
   }
-  const int rt = tile_rows(a.group, a.t.n_seqs, a.t.n_rows);
+  const int rt = tile_rows(a.group, a.t.n_seqs, a.t.n_rows, Q8);
   const int64_t pool_rows =
       (int64_t)kv->n_layers * kv->n_pages * kv->n_heads_kv * kv->page_size;
   const bool tensor_cores = rt == CHUNK_TC_ROWS && chunk_tc_fits(pool_rows);
@@ -856,7 +858,7 @@ extern "C" int32_t sub_chunk_attn_workspace(int32_t n_heads_q, int32_t n_heads_k
   SUB_CHECK_ARG(n_heads_kv >= 1 && n_heads_q >= 1 && n_heads_q % n_heads_kv == 0,
                 "Hq must be a multiple of Hkv");
   SUB_CHECK_ARG(n_seqs >= 1 && n_seqs <= SUB_MAX_SEQS && n_rows >= 0, "bad batch sizes");
-  const int rt = tile_rows(n_heads_q / n_heads_kv, n_seqs, n_rows);
+  const int rt = tile_rows(n_heads_q / n_heads_kv, n_seqs, n_rows, false);   // the larger one
   *bytes = n_rows ? part_bytes(rt, head_dim) : 0;
   return SUB_OK;
 }

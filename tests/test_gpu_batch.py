@@ -88,7 +88,7 @@ class Case:
         scale is at least 2^11, so one that falls below fp16's normal numbers is off by at
         most half of 2^-24, 2^-36 of the largest: per key, 2^-36 of the largest |v|
         (which matters in a column where the largest weights meet codes 128).
-        Tiles of many rows (more than 16 per sequence and KV head) round the values of
+        Tiles of many rows (more than 64 per sequence and KV head) round the values of
         codes to fp16, too (2^-11): V's scale and V's value, K in every term of a score,
         and with 2^-25 of the block's largest scale where that is below fp16's normal
         numbers."""
@@ -108,7 +108,7 @@ class Case:
                 top = (np.abs(q) * big).sum(-1, keepdims=True) * sc
             c = (2.0 ** -8 if self.bits == 16 else 2.0 ** -11) + \
                 2 * (self.d / 16 + 4) * 2.0 ** -22 * top + (len(k) / 16 + 4) * 2.0 ** -22
-            if self.bits == 8 and self.batch.n_rows * self.hq > 16 * self.hkv * len(self.seqs):
+            if self.bits == 8 and self.batch.n_rows * self.hq > 64 * self.hkv * len(self.seqs):
                 c = c + 2 * 2.0 ** -11 + 2 * 2.0 ** -11 * top
             err = np.abs(np32(o[r0:r0 + n]).astype(np.float64) - ref)
             bound = 2.0 ** -8 * np.abs(ref) + c * w + 1e-30

@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(const __grid_constant
 // rounds of reads from L2, at the end of every call: what it needs to know
 // lies ready in the list of cuts.
 constexpr int JOIN_WARPS = 4;   // per CTA
-constexpr int join_rows(int rt) { return rt <= 32 ? JOIN_WARPS : 4 * JOIN_WARPS; }   // per CTA
+constexpr int join_split(int rt) { return rt == RT ? RT / JOIN_WARPS : 16; }   // CTAs per tile
 
 template <int D, int RT>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) chunk_join_kernel(const __grid_constant__ ChunkArgs a) {
@@ -678,9 +678,9 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) chunk_join_kernel(const __gri
   const int d = (lane % LANES) * 4, mine = lane / LANES;
   auto slot = [&](int i) { return (int64_t)(i == 0 ? c.first : 2 * (part + i)); };
   const FastDiv by = a.by_group;
-  const int r0 = blockIdx.y * join_rows(RT);
+  // (a tile's CTAs in turn: its last rows are often unused)
 #pragma unroll 1
-  for (int r = r0 + (threadIdx.x >> 5); r < r0 + join_rows(RT); r += JOIN_WARPS) {
+  for (int r = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5); r < RT; r += gridDim.y * JOIN_WARPS) {
     const int row = c.tile * RT + r, q = by.quot(row);
     if (q >= c.rows) break;
     // pieces from i0 on, PER at a time: their columns, asked for together
@@ -750,7 +750,7 @@ int sm_count() {
 
 template <int D, int RT>
 int32_t launch_join(const ChunkArgs& a, int n_ctas, cudaStream_t st) {
-  SUB_CUDA_TRY(launch_k(chunk_join_kernel<D, RT>, dim3(n_ctas, RT / join_rows(RT)),
+  SUB_CUDA_TRY(launch_k(chunk_join_kernel<D, RT>, dim3(n_ctas, join_split(RT)),
                         dim3(JOIN_WARPS * 32), 0, st, a));
   return SUB_OK;
 }

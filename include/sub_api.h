@@ -295,7 +295,7 @@ typedef struct {
  * a < 2^-100: scale 1, codes 128; a row that is not finite: scale NaN, codes
  * 128.  The value is (code - 128) * scale.
  * Codes lie like the values of sub_kv_cache ([layer][page][head][page_size]
- * [head_dim]), scales like them without the last axis. */
+ * [head_dim]), scales like them without the last axis; both 16-byte aligned. */
 typedef struct {
   uint8_t* k;
   uint8_t* v;

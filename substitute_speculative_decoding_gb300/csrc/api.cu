@@ -55,7 +55,7 @@ extern "C" int32_t sub_pipeline_timeouts(uint32_t* out) {
   unsigned int a = 0, b = 0, c = 0;
   SUB_TRY(gemv_tma_timeouts(&a));
   SUB_TRY(gemm_tc_timeouts(&b));
-  SUB_TRY(chunk_tc_timeouts(&c));
+  SUB_TRY(chunk_attn_timeouts(&c));
   *out = a + b + c;
   return SUB_OK;
 }

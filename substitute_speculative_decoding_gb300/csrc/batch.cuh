@@ -81,4 +81,10 @@ inline int32_t make_seq_table(const Cache* kv, int32_t layer, const sub_batch* b
   return SUB_OK;
 }
 
+inline int32_t check_scales(const sub_kv8_cache* kv) {
+  SUB_CHECK_ARG(kv && kv->k_scale && kv->v_scale, "null pointer");
+  SUB_CHECK_ARG(aligned16(kv->k_scale) && aligned16(kv->v_scale), "the scales must be 16-byte aligned");
+  return SUB_OK;
+}
+
 }  // namespace sub

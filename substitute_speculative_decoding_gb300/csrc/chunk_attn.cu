@@ -38,40 +38,29 @@
 #include <mutex>
 #include <type_traits>
 #include "chunk_attn.cuh"
+#include "tma.cuh"
 
 namespace sub {
 namespace {
+
+using namespace tmah;
 
 constexpr int RT = 16;           // rows of a tile
 constexpr int WARPS = 8;
 constexpr int NT = WARPS * 32;
 constexpr int STAGES = 3;
 
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-  return (uint32_t)__cvta_generic_to_shared(p);
-}
-// 16, 8 or 4 bytes; `_if`: zeros if not, with `any` an address that may be read.
-template <int N>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
-  if constexpr (N == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(dst), "l"(src), "n"(N)
-                 : "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_if(uint32_t dst, const void* src, const void* any, bool yes) {
-  if constexpr (N == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(yes ? src : any),
-                 "r"(yes ? 16 : 0) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;\n" ::"r"(dst),
-                 "l"(yes ? src : any), "n"(N), "r"(yes ? N : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+__device__ unsigned int g_decode_timeouts;   // waits that ran out (never expected)
+
+struct PageMaps {
+  CUtensorMap k, v;   // [pages and heads, page_size, D], boxes of 16 keys x 128 (or 64) bytes
+};
+// bytes: a multiple of 16, both addresses on 16-byte boundaries
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -109,18 +98,21 @@ struct Ring {
   static constexpr int KB = !Q8 && D == 128 ? 16 : 32;   // keys per block of a warp
   static constexpr int SUBS = KB / 16;                   // 16-key steps; a step lies in one page
   static constexpr int ROW = D * (Q8 ? 1 : 2);           // bytes of a row
+  static constexpr int LINE = ROW < 128 ? ROW : 128;     // a box is 16 lines: 16 keys' columns
+  static constexpr int BOX = 16 * LINE, H = ROW / LINE;  // boxes side by side
   static constexpr int KI = ROW / 64;                    // 16-byte chunks of a key per lane
-  static constexpr int VB = Q8 ? D / 8 : 16;             // bytes of a V piece
-  static constexpr int VH = Q8 ? 1 : D / 64;             // pieces per key and lane
   static constexpr int K_BYTES = KB * ROW;
-  static constexpr int STAGE = 2 * K_BYTES + (Q8 ? 2 * KB * 4 : 0);
+  static constexpr int STAGE = 2 * K_BYTES;
   static constexpr int BYTES = STAGES * STAGE;           // of one warp
+  static constexpr int SCALES = Q8 ? 2 * KB * 4 : 0;     // of one stage
+  static constexpr int OPS = 2 * H + (Q8 ? 2 : 0);       // copies of a 16-key step
 };
 
 template <int D, bool Q8>
 constexpr int decode_smem() {
   static_assert(Ring<D, Q8>::STAGE >= RT * D * 4, "a stage holds a warp's partial result");
-  return WARPS * Ring<D, Q8>::BYTES;
+  static_assert(Ring<D, Q8>::SUBS * Ring<D, Q8>::OPS <= 32, "a lane per copy");
+  return 1024 + WARPS * (Ring<D, Q8>::BYTES + STAGES * Ring<D, Q8>::SCALES);
 }
 
 // A barrier of two warps.
@@ -131,16 +123,25 @@ __device__ __forceinline__ void bar_arrive(int id) {
 
 // ------------------------------------------------------------------ kernel --
 template <int D, bool Q8>
-__global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(const __grid_constant__ ChunkArgs a) {
+__global__ void __launch_bounds__(NT, 1)
+chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__ ChunkArgs a) {
   using R = Ring<D, Q8>;
   constexpr int KS = D / 16, ON = D / 8, KB = R::KB, SUBS = R::SUBS, TILES = KB / 8;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = smem_raw + (-smem_u32(smem_raw) & 1023u);   // as the boxes' swizzle wants it
   __shared__ int64_t s_pre[SUB_MAX_SEQS + 1];
   __shared__ int s_at[WARPS];          // their stages
   __shared__ float4 s_ml[WARPS][32];   // maxima and sums of the warps' partial results, by lane
+  __shared__ __align__(8) uint64_t s_bar[WARPS][STAGES];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid < WARPS * STAGES) mbar_init(smem_u32(&s_bar[0][0] + tid), 1);
+  if (tid == 0) {
+    tma_prefetch_desc(&maps.k);
+    tma_prefetch_desc(&maps.v);
+  }
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, tig = lane & 3;
   const int G = a.group, ps = a.t.page_size;
   const ChunkPlan<RT, KB> plan(a);
@@ -148,11 +149,19 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(const __grid_constant
   const int64_t total = s_pre[a.t.n_seqs];
   const int64_t per = blocks_per_cta(total, gridDim.x, WARPS);
   const uint8_t* const ring = smem + warp * R::BYTES;
-  const uint32_t ring_s = smem_u32(ring);
-  // a lane's place in the first key of a step, of K and of V
-  const uint8_t* const kp = reinterpret_cast<const uint8_t*>(a.k) + g * R::ROW + tig * 16;
-  const uint8_t* const vp = reinterpret_cast<const uint8_t*>(a.v) + 2 * tig * R::ROW + g * R::VB;
-  const int64_t page_rows = (int64_t)a.n_heads_kv * ps;
+  const float* const scales =
+      reinterpret_cast<const float*>(smem + WARPS * R::BYTES + warp * (STAGES * R::SCALES));
+  const uint32_t ring_s = smem_u32(ring), scales_s = smem_u32(scales), bar_s = smem_u32(s_bar[warp]);
+  // Where a lane's operands lie in a box, 16-byte chunks swizzled by the line: K of key
+  // g, its chunks 2 tig, 2 tig + 1 (of four: tig), V of keys 2 tig, 2 tig + 1, its piece g
+  int k_at[2], v_at[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int r = 2 * tig + x;
+    k_at[x] = R::LINE == 128 ? g * 128 + ((r ^ g) * 16) : g * 64 + ((tig ^ (g >> 1)) * 16);
+    v_at[x] = R::LINE == 128 ? r * 128 + ((g ^ r) * 16)
+                             : r * 64 + (((g >> 1) ^ tig) * 16) + (g & 1) * 8;
+  }
   const int64_t line_lo = blockIdx.x * per, line_hi = min(total, line_lo + per);
   if (line_lo >= line_hi) {
     if (tid == 0) a.cuts[blockIdx.x].pieces = 0;
@@ -165,15 +174,15 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(const __grid_constant
   ChunkUnit f = u;
   int f0, fn, fi;
   const int32_t* pages;
-  int64_t row_base, places, places2;
-  // Pool rows of the warp's next 32 16-key steps (-1: no page), one looked up by
+  int places, places2;
+  // (page, head) of the warp's next 32 16-key steps (-1: no page), one looked up by
   // each lane, and of the 32 after them: a step's place is a shuffle away.
-  auto look_up = [&](int step) -> int64_t {
+  auto look_up = [&](int step) {
     const int key = (f0 + warp + step / SUBS * WARPS) * KB + step % SUBS * 16;
     if (key >= f.n_keys || step >= fn * SUBS) return -1;
-    const int entry = a.by_page.quot(key), page = pages[entry];
+    const int page = pages[a.by_page.quot(key)];
     if ((unsigned)page >= (unsigned)a.t.n_pages) return -1;
-    return row_base + (int64_t)page * page_rows + (key - entry * ps);
+    return (a.layer * a.t.n_pages + page) * a.n_heads_kv + f.head;
   };
   auto open = [&](int64_t at) {
     for (;;) {
@@ -186,61 +195,42 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(const __grid_constant
       plan.next(f);
     }
     pages = a.t.pages + (int64_t)f.b * a.t.width;
-    row_base = ((int64_t)a.layer * a.t.n_pages * a.n_heads_kv + f.head) * ps;
     places = look_up(lane);
     places2 = look_up(32 + lane);
   };
   uint32_t missing = 0;   // bits SUBS * stage + step: no page there
+  uint32_t phase = 0;     // of the stages' barriers
+  uint32_t coming = 0;    // stages with copies under way
+  bool dead = false;      // a wait ran out: no more copies, no more waits
+  const int my_step = min(lane / R::OPS, SUBS - 1), my_op = lane - my_step * R::OPS;   // op >= OPS: none
   auto feed = [&](int stage) {
-    if (fi < fn) {
-      const uint32_t dst = ring_s + stage * R::STAGE;
+    if (fi < fn && !dead) {
       if (fi > 0 && fi % (32 / SUBS) == 0) {
         places = places2;
         places2 = look_up(fi * SUBS + 32 + lane);
       }
+      const int place = __shfl_sync(~0u, places, (fi * SUBS + my_step) & 31);
+      const unsigned have = __ballot_sync(~0u, place >= 0);
+      uint32_t gone = 0;
 #pragma unroll
-      for (int s = 0; s < SUBS; ++s) {
-        const int64_t place = __shfl_sync(~0u, places, (fi * SUBS + s) & 31);
-        const bool have = place >= 0;
-        const int64_t row0 = have ? place : 0;
-        const int left = have ? f.n_keys - ((f0 + warp + fi * WARPS) * KB + 16 * s) : 0;   // keys of the step
-        const int bit = SUBS * stage + s;
-        missing = (missing & ~(1u << bit)) | ((have ? 0u : 1u) << bit);
-        const uint8_t* const k0 = kp + row0 * R::ROW;
-        const uint8_t* const v0 = vp + row0 * R::ROW;
-        const uint32_t kd = dst + s * (2 * R::KI * 512) + lane * 16;
-        const uint32_t vd = dst + R::K_BYTES + s * (4 * R::VH * 32 * R::VB) + lane * R::VB;
-        if (left >= 16) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int c = 0; c < R::KI; ++c)
-              cp_async<16>(kd + (h * R::KI + c) * 512, k0 + h * 8 * R::ROW + c * 64);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-            for (int c = 0; c < R::VH; ++c)
-              cp_async<R::VB>(vd + (kk * R::VH + c) * (32 * R::VB),
-                              v0 + ((kk >> 1) * 8 + (kk & 1)) * R::ROW + c * 8 * R::VB);
-        } else {   // zeros past the last key
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h)
-#pragma unroll 1
-            for (int c = 0; c < R::KI; ++c)
-              cp_async_if<16>(kd + (h * R::KI + c) * 512, k0 + h * 8 * R::ROW + c * 64, a.k,
-                              h * 8 + g < left);
-#pragma unroll 1
-          for (int kk = 0; kk < 4; ++kk)
-#pragma unroll 1
-            for (int c = 0; c < R::VH; ++c)
-              cp_async_if<R::VB>(vd + (kk * R::VH + c) * (32 * R::VB),
-                                 v0 + ((kk >> 1) * 8 + (kk & 1)) * R::ROW + c * 8 * R::VB, a.k,
-                                 (kk >> 1) * 8 + 2 * tig + (kk & 1) < left);
-        }
-        if constexpr (Q8) {   // 16 scales of K, 16 of V
-          const int key = lane & 15;
-          cp_async_if<4>(dst + 2 * R::K_BYTES + ((lane >> 4) * KB + s * 16 + key) * 4,
-                         (lane < 16 ? a.ks : a.vs) + row0 + key, a.ks, key < left);
+      for (int s = 0; s < SUBS; ++s) gone |= (~(have >> (s * R::OPS)) & 1u) << s;
+      missing = (missing & ~(((1u << SUBS) - 1u) << (SUBS * stage))) | gone << (SUBS * stage);
+      const uint32_t bar = bar_s + stage * 8;
+      coming |= 1u << stage;
+      if (lane == 0)
+        mbar_expect_tx(bar, (SUBS - __popc(gone)) * (32 * R::ROW + (Q8 ? 128 : 0)));
+      __syncwarp();
+      if (place >= 0 && my_op < R::OPS) {
+        const int key = (f0 + warp + fi * WARPS) * KB + my_step * 16;
+        const int at = key - a.by_page.quot(key) * ps;
+        if (my_op < 2 * R::H) {
+          const int side = my_op / R::H, h = my_op % R::H;
+          tma_load_3d(ring_s + stage * R::STAGE + side * R::K_BYTES + (my_step * R::H + h) * R::BOX,
+                      side ? &maps.v : &maps.k, h * 64, at, place, bar);
+        } else {   // 16 scales of K, 16 of V
+          const int side = my_op - 2 * R::H;
+          bulk_load(scales_s + stage * R::SCALES + (side * KB + my_step * 16) * 4,
+                    (side ? a.vs : a.ks) + (int64_t)place * ps + at, 64, bar);
         }
       }
       if (++fi == fn) {
@@ -251,7 +241,6 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(const __grid_constant
         }
       }
     }
-    cp_commit();
   };
   open(line_lo);
 #pragma unroll 1
@@ -279,8 +268,9 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(const __grid_constant
                             (int64_t)(u.head * G + r - q * G) * D;
 #pragma unroll
       for (int c = 0; c < KS / 2; ++c) {
-        // bf16 cache: chunk tig + 4 c of 8 values; codes: half c & 1 of chunk tig + 4 (c / 2) of 16
-        const int d = Q8 ? ((tig + 4 * (c >> 1)) * 16 + (c & 1) * 8) : (tig + 4 * c) * 8;
+        // the chunk that K's c-th (bf16, 8 values), (c / 2)-th (codes, 16) operands come from
+        const int i = Q8 ? c >> 1 : c, chunk = R::KI == 1 ? tig : 8 * (i >> 1) + 2 * tig + (i & 1);
+        const int d = Q8 ? chunk * 16 + (c & 1) * 8 : chunk * 8;
         w[h][c] = ok ? *reinterpret_cast<const uint4*>(src + d) : make_uint4(0, 0, 0, 0);
       }
     }
@@ -333,12 +323,23 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(const __grid_constant
 #pragma unroll
     for (int i = 0; i < ON; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
-    if (owed) bar_sync(owed);
+    if (owed) {
+      bar_sync(owed);
+      fence_async();   // the copies to come follow the stores of the partial result
+      __syncwarp();
+    }
     owed = 0;
     for (int i = 0; i < n_mine; ++i) {
       feed(stage == 0 ? STAGES - 1 : stage - 1);   // the stage that was read last
-      cp_wait<STAGES - 1>();
-      __syncwarp();
+      if (!dead) {
+        if (__all_sync(~0u, mbar_wait_polls(bar_s + stage * 8, (phase >> stage) & 1u, 1u << 20))) {
+          phase ^= 1u << stage;
+          coming &= ~(1u << stage);
+        } else {
+          dead = true;
+          if (lane == 0) atomicAdd(&g_decode_timeouts, 1u);
+        }
+      }
       const int key0 = (kb0 + warp + i * WARPS) * KB;
       const uint8_t* const st = ring + stage * R::STAGE;
       const uint32_t miss = (missing >> (SUBS * stage)) & ((1u << SUBS) - 1u);
@@ -353,7 +354,8 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(const __grid_constant
         uint32_t w[TILES][4];
 #pragma unroll
         for (int t = 0; t < TILES; ++t) {
-          const uint4 x = *reinterpret_cast<const uint4*>(st + ((t * R::KI + c) * 32 + lane) * 16);
+          const uint4 x = *reinterpret_cast<const uint4*>(
+              st + ((t >> 1) * R::H + (c >> 1)) * R::BOX + (t & 1) * 8 * R::LINE + k_at[c & 1]);
           w[t][0] = x.x;
           w[t][1] = x.y;
           w[t][2] = x.z;
@@ -377,9 +379,10 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(const __grid_constant
       }
 
       // ---- weights of the lane's keys 8 t + 2 tig + {0, 1} ----
-      float vsc[TILES][2], lv = 0.f;
+      float vsc[TILES][2], lv[2] = {0.f, 0.f};
+      auto shift = [](float vmax) { return fmaxf(log2_fast(vmax), -80.f) - 15.f; };
       if constexpr (Q8) {
-        const float* const sc = reinterpret_cast<const float*>(st + 2 * R::K_BYTES);
+        const float* const sc = scales + stage * (R::SCALES / 4);
         float vmax = 0.f;
 #pragma unroll
         for (int t = 0; t < TILES; ++t) {
@@ -391,7 +394,7 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(const __grid_constant
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[t][e] *= e & 1 ? kq.y : kq.x;
         }
-        lv = fmaxf(log2_fast(vmax), -80.f) - 15.f;
+        lv[0] = lv[1] = shift(vmax);
       }
       if (edge) {
 #pragma unroll
@@ -402,6 +405,18 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(const __grid_constant
             const bool gone = (miss >> (t >> 1)) & 1u;
             if (gone || key > lim[e >> 1]) s[t][e] = -INFINITY;
           }
+        if constexpr (Q8) {   // the scales of keys that a row does not read may be anything
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float vmax = 0.f;
+#pragma unroll
+            for (int t = 0; t < TILES; ++t)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (s[t][2 * h + e] != -INFINITY) vmax = fmaxf(vmax, vsc[t][e]);
+            lv[h] = shift(vmax);
+          }
+        }
       }
       uint32_t pf[SUBS][4], pl[SUBS][4];   // P of the 16-key steps (bf16: high and low part)
       float top[2] = {-INFINITY, -INFINITY};
@@ -409,8 +424,8 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(const __grid_constant
       for (int t = 0; t < TILES; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) top[e >> 1] = fmaxf(top[e >> 1], s[t][e]);
-      top[0] = fmaf(top[0], qs[0], lv);
-      top[1] = fmaf(top[1], qs[1], lv);
+      top[0] = fmaf(top[0], qs[0], lv[0]);
+      top[1] = fmaf(top[1], qs[1], lv[1]);
       if (__any_sync(~0u, top[0] > mx[0] || top[1] > mx[1])) {
         float corr[2];
 #pragma unroll
@@ -464,12 +479,13 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(const __grid_constant
       for (int step = 0; step < SUBS; ++step) {
         if constexpr (!Q8) {
 #pragma unroll
-          for (int c = 0; c < R::VH; ++c) {   // d(g, 8 c + j) = 64 c + 8 g + j
+          for (int c = 0; c < R::H; ++c) {   // d(g, 8 c + j) = 64 c + 8 g + j
             uint32_t w[4][4];
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
               const uint4 x =
-                  *reinterpret_cast<const uint4*>(sv + (((step * 4 + kk) * R::VH + c) * 32 + lane) * 16);
+                  *reinterpret_cast<const uint4*>(sv + (step * R::H + c) * R::BOX + (kk >> 1) * 8 * R::LINE +
+                                                  v_at[kk & 1]);
               w[kk][0] = x.x;
               w[kk][1] = x.y;
               w[kk][2] = x.z;
@@ -529,11 +545,11 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(const __grid_constant
             }
           }
         } else {
-          constexpr int WN = R::VB / 4;   // d(g, n) = g * (D / 8) + n
+          constexpr int WN = D / 32;   // d(g, n) = g * (D / 8) + n
           uint32_t w[4][WN];
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
-            const uint8_t* const src = sv + ((step * 4 + kk) * 32 + lane) * R::VB;
+            const uint8_t* const src = sv + step * R::BOX + (kk >> 1) * 8 * R::LINE + v_at[kk & 1];
             if constexpr (WN == 4) {
               const uint4 x = *reinterpret_cast<const uint4*>(src);
               w[kk][0] = x.x;
@@ -655,6 +671,8 @@ __global__ void __launch_bounds__(NT, 1) chunk_attn_kernel(const __grid_constant
     if (tid == 0 && at >= line_hi) a.cuts[blockIdx.x] = make_cut(u, kb1, line_lo, per);
   }
   if (owed) bar_sync(owed);
+  for (int st = 0; dead && st < STAGES; ++st)   // the copies that are still under way
+    if ((coming >> st) & 1u) mbar_wait_polls(bar_s + st * 8, (phase >> st) & 1u, 1u << 16);
 }
 
 // ------------------------------------------------------------------- joins --
@@ -765,7 +783,11 @@ int32_t launch_decode(const ChunkArgs& a, int n_ctas, cudaStream_t st) {
                                SMEM);
   });
   SUB_CUDA_TRY(err);
-  SUB_CUDA_TRY(launch_k(chunk_attn_kernel<D, Q8>, dim3(n_ctas), dim3(NT), SMEM, st, a));
+  PageMaps maps;
+  if (!chunk_page_map(&maps.k, a.k, a.t, (int64_t)a.n_layers * a.n_heads_kv, D, Q8) ||
+      !chunk_page_map(&maps.v, a.v, a.t, (int64_t)a.n_layers * a.n_heads_kv, D, Q8))
+    return fail(SUB_ECUDA, "chunk_attn: the cache's tensor map was refused");
+  SUB_CUDA_TRY(launch_k(chunk_attn_kernel<D, Q8>, dim3(n_ctas), dim3(NT), SMEM, st, maps, a));
   return launch_join<D, RT>(a, n_ctas, st);
 }
 
@@ -808,6 +830,7 @@ int32_t chunk_attn(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q, const Cach
   a.ks = ks;
   a.vs = vs;
   a.layer = layer;
+  a.n_layers = kv->n_layers;
   a.n_heads_q = n_heads_q;
   a.n_heads_kv = kv->n_heads_kv;
   a.group = n_heads_q / kv->n_heads_kv;
@@ -846,6 +869,15 @@ int32_t chunk_attn(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q, const Cach
 }
 
 }  // namespace
+
+int32_t chunk_attn_timeouts(unsigned int* out) {
+  unsigned int tc = 0;
+  SUB_TRY(chunk_tc_timeouts(&tc));
+  SUB_CUDA_TRY(cudaMemcpyFromSymbol(out, g_decode_timeouts, sizeof(unsigned int)));
+  *out += tc;
+  return SUB_OK;
+}
+
 }  // namespace sub
 
 using namespace sub;
@@ -875,7 +907,7 @@ extern "C" int32_t sub_chunk_attn8(const sub_bf16* Q, int64_t ldq, int32_t n_hea
                                    const sub_kv8_cache* kv, int32_t layer, const sub_batch* batch,
                                    float softmax_scale, sub_bf16* O, void* workspace,
                                    int64_t workspace_bytes, void* stream) {
-  SUB_CHECK_ARG(kv && kv->k_scale && kv->v_scale, "null pointer");
+  SUB_TRY(check_scales(kv));
   return chunk_attn(Q, ldq, n_heads_q, kv, kv->k_scale, kv->v_scale, layer, batch, softmax_scale,
                     O, workspace, workspace_bytes, stream);
 }

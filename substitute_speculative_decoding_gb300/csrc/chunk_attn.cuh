@@ -1,5 +1,6 @@
 // Attention of a batch's new rows over a paged cache (see chunk_attn.cu).
 #pragma once
+#include <cuda.h>
 #include "batch.cuh"
 
 namespace sub {
@@ -30,7 +31,7 @@ struct ChunkArgs {
   const void* v;
   const float* ks;       // scales of the codes
   const float* vs;
-  int layer, n_heads_q, n_heads_kv, group;   // group = Hq / Hkv
+  int layer, n_layers, n_heads_q, n_heads_kv, group;   // group = Hq / Hkv
   FastDiv by_group, by_page;
   float sl2;             // softmax scale * log2(e): scores in base 2
   // partial results of units cut between CTAs: two per CTA
@@ -216,5 +217,9 @@ bool chunk_tc_fits(int64_t pool_rows);   // rows of head_dim values in a pool
 int32_t launch_chunk_tc(const ChunkArgs& a, bool q8, int head_dim, int64_t pool_rows, int n_ctas,
                         cudaStream_t st);
 int32_t chunk_tc_timeouts(unsigned int* out);
+// Waits that ran out in either kernel.
+int32_t chunk_attn_timeouts(unsigned int* out);
+// Tensor map of a pool by (page and head, place, column), in boxes of 16 places.
+bool chunk_page_map(CUtensorMap* m, const void* pool, const SeqTable& t, int64_t heads, int d, bool codes);
 
 }  // namespace sub

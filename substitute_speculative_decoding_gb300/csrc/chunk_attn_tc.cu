@@ -209,9 +209,6 @@ __device__ __forceinline__ bool elect_one() {   // by a whole warp: one lane
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(x));
   return x != 0;
 }
-__device__ __forceinline__ void fence_async() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
 
 // Bounded wait.  One that runs out is counted and ends the CTA's work: every
 // later wait returns at once, nothing more is issued, and the results are not valid.
@@ -929,6 +926,19 @@ int32_t launch(const ChunkArgs& a, int64_t rows, int n_ctas, cudaStream_t st) {
 }
 
 }  // namespace
+
+bool chunk_page_map(CUtensorMap* m, const void* pool, const SeqTable& t, int64_t heads, int d, bool codes) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const int size = codes ? 1 : 2, line = d * size < 128 ? d * size : 128;
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)t.page_size, (cuuint64_t)(heads * t.n_pages)};
+  const cuuint64_t strides[2] = {(cuuint64_t)d * size, (cuuint64_t)d * size * t.page_size};
+  const cuuint32_t boxes[3] = {(cuuint32_t)(line / size), 16, 1}, es[3] = {1, 1, 1};
+  return fn(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+            const_cast<void*>(pool), dims, strides, boxes, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            line == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 bool chunk_tc_fits(int64_t pool_rows) { return pool_rows < (1ll << 31) - 4096; }
 

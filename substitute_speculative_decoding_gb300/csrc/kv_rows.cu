@@ -190,11 +190,6 @@ int32_t append(const sub_bf16* K, int64_t ldk, const sub_bf16* V, int64_t ldv, c
   return SUB_OK;
 }
 
-int32_t check_scales(const sub_kv8_cache* kv) {
-  SUB_CHECK_ARG(kv && kv->k_scale && kv->v_scale, "null pointer");
-  return SUB_OK;
-}
-
 }  // namespace
 }  // namespace sub
 

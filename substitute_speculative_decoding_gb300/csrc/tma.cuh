@@ -53,6 +53,11 @@ __device__ __forceinline__ uint32_t mbar_wait_polls(uint32_t bar, uint32_t parit
   return 0;   // gave up
 }
 
+// Stores of this thread before copies into the same shared memory.
+__device__ __forceinline__ void fence_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 // 2-D tiled TMA load of one box at (x, y) (x in elements of the innermost
 // dimension) into shared memory, completing bytes on the mbarrier.
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y,

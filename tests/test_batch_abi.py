@@ -89,8 +89,9 @@ def test_bad_caches_and_batches_are_refused(s, q8):
             assert r == s.SUB_EINVAL and word in s._lib.sub_last_error(), bad
     if q8:
         for name in ("k_scale", "v_scale"):
-            for r in calls(s, True, cache(s, True, **{name: None}), rows(s)):
-                assert r == s.SUB_EINVAL
+            for at, word in ((None, b"null"), (4100, b"aligned")):
+                for r in calls(s, True, cache(s, True, **{name: at}), rows(s)):
+                    assert r == s.SUB_EINVAL and word in s._lib.sub_last_error()
 
 
 def test_an_empty_batch_needs_nothing(s):

@@ -35,6 +35,7 @@
 // and where its value is infinite or NaN (bf16 only, and only in blocks that
 // not all rows read to the end), the block's products with V are formed one by
 // one without the keys of weight zero.
+#include <algorithm>
 #include <mutex>
 #include <type_traits>
 #include "chunk_attn.cuh"
@@ -45,7 +46,7 @@ namespace {
 
 using namespace tmah;
 
-constexpr int RT = 16;           // rows of a tile
+constexpr int WIDE = 16, NARROW = 8;   // rows of a tile
 constexpr int WARPS = 8;
 constexpr int NT = WARPS * 32;
 constexpr int STAGES = 3;
@@ -110,9 +111,16 @@ struct Ring {
 
 template <int D, bool Q8>
 constexpr int decode_smem() {
-  static_assert(Ring<D, Q8>::STAGE >= RT * D * 4, "a stage holds a warp's partial result");
+  static_assert(Ring<D, Q8>::STAGE >= WIDE * D * 4, "a stage holds a warp's partial result");
   static_assert(Ring<D, Q8>::SUBS * Ring<D, Q8>::OPS <= 32, "a lane per copy");
   return 1024 + WARPS * (Ring<D, Q8>::BYTES + STAGES * Ring<D, Q8>::SCALES);
+}
+
+// The 8x8 matrix of 16-bit values whose row g the lanes (g, .) hold, turned over.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 
 // A barrier of two warps.
@@ -122,11 +130,15 @@ __device__ __forceinline__ void bar_arrive(int id) {
 }
 
 // ------------------------------------------------------------------ kernel --
-template <int D, bool Q8>
+template <int D, bool Q8, int RT>
 __global__ void __launch_bounds__(NT, 1)
 chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__ ChunkArgs a) {
   using R = Ring<D, Q8>;
-  constexpr int KS = D / 16, ON = D / 8, KB = R::KB, SUBS = R::SUBS, TILES = KB / 8;
+  constexpr int KS = D / 16, KB = R::KB, SUBS = R::SUBS;
+  // Scores in accumulators of 8 keys x 16 rows, or turned over, of 16 keys x 8 rows;
+  // results of 8 columns x 16 rows, or 16 columns x 8 rows
+  constexpr bool TURNED = RT == NARROW;
+  constexpr int TILES = TURNED ? SUBS : KB / 8, ON = TURNED ? D / 16 : D / 8;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + (-smem_u32(smem_raw) & 1023u);   // as the boxes' swizzle wants it
   __shared__ int64_t s_pre[SUB_MAX_SEQS + 1];
@@ -253,48 +265,53 @@ chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__
     const int kb1 = (int)min((int64_t)u.n_blocks, line_hi - u.begin);
     const int n_mine = (kb1 - kb0 - warp + WARPS - 1) / WARPS;   // blocks kb0 + warp + i * WARPS
 
-    // ---- Q fragments, and the rows' last visible key ----
-    uint32_t qf[KS][4];
+    // Element i of accumulator t: which of the lane's two rows, which of its two keys
+    auto row_of = [](int i) { return TURNED ? i & 1 : i >> 1; };
+    auto key_of = [](int i) { return TURNED ? i >> 1 : i & 1; };
+    auto tile_row = [&](int h) { return TURNED ? 2 * tig + h : h * 8 + g; };
+    auto block_key = [&](int t, int x) { return TURNED ? 16 * t + 8 * x + g : 8 * t + 2 * tig + x; };
+
+    // ---- Q fragments (of rows g, g + 8, or as the other operand, of row g) ----
+    uint32_t qf[KS][TURNED ? 2 : 4];
     float qs[2];    // factor of the row's scores
     int lim[2];     // keys 0 .. lim are read
-    uint4 w[2][KS / 2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+      const int q = a.by_group.quot(u.tile * RT + tile_row(h));
+      lim[h] = q < u.rows ? min(u.pos + q, u.n_keys - 1) : -1;
+      qs[h] = a.sl2;
+    }
+#pragma unroll
+    for (int h = 0; h < (TURNED ? 1 : 2); ++h) {
       const int r = u.tile * RT + h * 8 + g;
       const int q = a.by_group.quot(r);
       const bool ok = q < u.rows;
-      lim[h] = ok ? min(u.pos + q, u.n_keys - 1) : -1;
       const uint16_t* src = a.Q + (int64_t)(u.row0 + (ok ? q : 0)) * a.ldq +
                             (int64_t)(u.head * G + r - q * G) * D;
+      uint4 w[KS / 2];
 #pragma unroll
       for (int c = 0; c < KS / 2; ++c) {
         // the chunk that K's c-th (bf16, 8 values), (c / 2)-th (codes, 16) operands come from
         const int i = Q8 ? c >> 1 : c, chunk = R::KI == 1 ? tig : 8 * (i >> 1) + 2 * tig + (i & 1);
         const int d = Q8 ? chunk * 16 + (c & 1) * 8 : chunk * 8;
-        w[h][c] = ok ? *reinterpret_cast<const uint4*>(src + d) : make_uint4(0, 0, 0, 0);
+        w[c] = ok ? *reinterpret_cast<const uint4*>(src + d) : make_uint4(0, 0, 0, 0);
       }
-    }
-    if constexpr (!Q8) {
+      // registers of row g: 0 and 2 of a row operand, 0 and 1 of a column operand
+      if constexpr (!Q8) {
 #pragma unroll
-      for (int c = 0; c < KS / 2; ++c) {
-        qf[2 * c][0] = w[0][c].x;
-        qf[2 * c][1] = w[1][c].x;
-        qf[2 * c][2] = w[0][c].y;
-        qf[2 * c][3] = w[1][c].y;
-        qf[2 * c + 1][0] = w[0][c].z;
-        qf[2 * c + 1][1] = w[1][c].z;
-        qf[2 * c + 1][2] = w[0][c].w;
-        qf[2 * c + 1][3] = w[1][c].w;
-      }
-      qs[0] = qs[1] = a.sl2;
-    } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
+        for (int c = 0; c < KS / 2; ++c) {
+          constexpr int UP = TURNED ? 1 : 2;
+          qf[2 * c][h] = w[c].x;
+          qf[2 * c][UP + h] = w[c].y;
+          qf[2 * c + 1][h] = w[c].z;
+          qf[2 * c + 1][UP + h] = w[c].w;
+        }
+      } else {
         // the row's largest value to [1, 2): an exponent in [-126, 126]
         float big = 0.f;
 #pragma unroll
         for (int c = 0; c < KS / 2; ++c) {
-          const uint32_t x[4] = {w[h][c].x, w[h][c].y, w[h][c].z, w[h][c].w};
+          const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             big = fmaxf(big, fmaxf(fabsf(bf16lo(x[i])), fabsf(bf16hi(x[i]))));
@@ -307,15 +324,26 @@ chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__
         qs[h] = fmaxf(a.sl2 * __uint_as_float((uint32_t)(127 + e) << 23), 1e-37f);
 #pragma unroll
         for (int c = 0; c < KS / 2; ++c) {
-          const uint32_t x[4] = {w[h][c].x, w[h][c].y, w[h][c].z, w[h][c].w};
+          const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            qf[2 * c + (i >> 1)][(i & 1) * 2 + h] =
+            qf[2 * c + (i >> 1)][(i & 1) * (TURNED ? 1 : 2) + h] =
                 pack_f16x2(bf16lo(x[i]) * down, bf16hi(x[i]) * down);
         }
       }
     }
+    if constexpr (TURNED && Q8) {
+      const float mine = qs[0];   // of row g
+      qs[0] = __shfl_sync(~0u, mine, 8 * tig);
+      qs[1] = __shfl_sync(~0u, mine, 8 * tig + 4);
+    }
     const int lim_min = min(u.pos + a.by_group.quot(u.tile * RT), u.n_keys - 1);   // of the tile's first row
+    // largest value over the lanes that share their rows
+    auto row_max = [](float x) {
+#pragma unroll
+      for (int d = TURNED ? 4 : 1; d < (TURNED ? 32 : 4); d *= 2) x = fmaxf(x, __shfl_xor_sync(~0u, x, d));
+      return x;
+    };
 
     float o[ON][4], mx[2], l[2];
     mx[0] = mx[1] = -INFINITY;
@@ -345,15 +373,16 @@ chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__
       const uint32_t miss = (missing >> (SUBS * stage)) & ((1u << SUBS) - 1u);
       const bool edge = key0 + KB - 1 > lim_min || miss;
 
-      // ---- S = Q K^T: n tile t holds keys key0 + 8 t .. + 7 ----
+      // ---- S = Q K^T, or K Q^T ----
       float s[TILES][4];
 #pragma unroll
       for (int t = 0; t < TILES; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+      // w[t]: the lane's chunk of key g of keys 8 t .. + 7
 #pragma unroll
       for (int c = 0; c < R::KI; ++c) {   // (the tiles in turn: their sums do not wait for each other)
-        uint32_t w[TILES][4];
+        uint32_t w[KB / 8][4];
 #pragma unroll
-        for (int t = 0; t < TILES; ++t) {
+        for (int t = 0; t < KB / 8; ++t) {
           const uint4 x = *reinterpret_cast<const uint4*>(
               st + ((t >> 1) * R::H + (c >> 1)) * R::BOX + (t & 1) * 8 * R::LINE + k_at[c & 1]);
           w[t][0] = x.x;
@@ -361,24 +390,30 @@ chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__
           w[t][2] = x.z;
           w[t][3] = x.w;
         }
-        if constexpr (!Q8) {
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
+        for (int k = 0; k < (Q8 ? 4 : 2); ++k) {
+          uint32_t b[KB / 8][2];   // 16 values' two operand registers
 #pragma unroll
-            for (int t = 0; t < TILES; ++t)
-              mma_bf16_16816(s[t], qf[2 * c + k], w[t][2 * k], w[t][2 * k + 1]);
-        } else {
+          for (int t = 0; t < KB / 8; ++t) {
+            b[t][0] = Q8 ? codes2(w[t][k], 0x4140u) : w[t][2 * (k & 1)];
+            b[t][1] = Q8 ? codes2(w[t][k], 0x4342u) : w[t][2 * (k & 1) + 1];
+          }
+          const auto& qk = qf[(Q8 ? 4 : 2) * c + k];
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int t = 0; t < TILES; ++t) {
-              const uint32_t b0 = codes2(w[t][k], 0x4140u), b1 = codes2(w[t][k], 0x4342u);
-              mma_f16(s[t], qf[4 * c + k], b0, b1);
+          for (int t = 0; t < TILES; ++t) {
+            if constexpr (TURNED) {
+              const uint32_t kf[4] = {b[2 * t][0], b[2 * t + 1][0], b[2 * t][1], b[2 * t + 1][1]};
+              if constexpr (Q8) mma_f16(s[t], kf, qk[0], qk[1]);
+              else mma_bf16_16816(s[t], kf, qk[0], qk[1]);
+            } else {
+              if constexpr (Q8) mma_f16(s[t], qk, b[t][0], b[t][1]);
+              else mma_bf16_16816(s[t], qk, b[t][0], b[t][1]);
             }
+          }
         }
       }
 
-      // ---- weights of the lane's keys 8 t + 2 tig + {0, 1} ----
+      // ---- weights ----
       float vsc[TILES][2], lv[2] = {0.f, 0.f};
       auto shift = [](float vmax) { return fmaxf(log2_fast(vmax), -80.f) - 15.f; };
       if constexpr (Q8) {
@@ -386,13 +421,24 @@ chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__
         float vmax = 0.f;
 #pragma unroll
         for (int t = 0; t < TILES; ++t) {
-          const float2 kq = *reinterpret_cast<const float2*>(sc + t * 8 + 2 * tig);
-          const float2 vq = *reinterpret_cast<const float2*>(sc + KB + t * 8 + 2 * tig);
-          vsc[t][0] = vq.x;
-          vsc[t][1] = vq.y;
-          vmax = fmaxf(vmax, fmaxf(vq.x, vq.y));
+          float ksc[2];
+          if constexpr (TURNED) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[t][e] *= e & 1 ? kq.y : kq.x;
+            for (int x = 0; x < 2; ++x) {
+              ksc[x] = sc[block_key(t, x)];
+              vsc[t][x] = sc[KB + block_key(t, x)];
+            }
+          } else {
+            const float2 kq = *reinterpret_cast<const float2*>(sc + block_key(t, 0));
+            const float2 vq = *reinterpret_cast<const float2*>(sc + KB + block_key(t, 0));
+            ksc[0] = kq.x;
+            ksc[1] = kq.y;
+            vsc[t][0] = vq.x;
+            vsc[t][1] = vq.y;
+          }
+          vmax = fmaxf(vmax, fmaxf(vsc[t][0], vsc[t][1]));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[t][e] *= ksc[key_of(e)];
         }
         lv[0] = lv[1] = shift(vmax);
       }
@@ -401,66 +447,61 @@ chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__
         for (int t = 0; t < TILES; ++t)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int key = key0 + t * 8 + 2 * tig + (e & 1);
-            const bool gone = (miss >> (t >> 1)) & 1u;
-            if (gone || key > lim[e >> 1]) s[t][e] = -INFINITY;
+            const int x = block_key(t, key_of(e));
+            const bool gone = (miss >> (TURNED ? t : t >> 1)) & 1u;
+            if (gone || key0 + x > lim[row_of(e)]) s[t][e] = -INFINITY;
           }
         if constexpr (Q8) {   // the scales of keys that a row does not read may be anything
+          float vmax[2] = {0.f, 0.f};
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float vmax = 0.f;
+          for (int t = 0; t < TILES; ++t)
 #pragma unroll
-            for (int t = 0; t < TILES; ++t)
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                if (s[t][2 * h + e] != -INFINITY) vmax = fmaxf(vmax, vsc[t][e]);
-            lv[h] = shift(vmax);
-          }
+            for (int e = 0; e < 4; ++e)
+              if (s[t][e] != -INFINITY) vmax[row_of(e)] = fmaxf(vmax[row_of(e)], vsc[t][key_of(e)]);
+          lv[0] = shift(vmax[0]);
+          lv[1] = shift(vmax[1]);
         }
       }
-      uint32_t pf[SUBS][4], pl[SUBS][4];   // P of the 16-key steps (bf16: high and low part)
       float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
       for (int t = 0; t < TILES; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) top[e >> 1] = fmaxf(top[e >> 1], s[t][e]);
+        for (int e = 0; e < 4; ++e) top[row_of(e)] = fmaxf(top[row_of(e)], s[t][e]);
       top[0] = fmaf(top[0], qs[0], lv[0]);
       top[1] = fmaf(top[1], qs[1], lv[1]);
       if (__any_sync(~0u, top[0] > mx[0] || top[1] > mx[1])) {
         float corr[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          top[h] = fmaxf(top[h], __shfl_xor_sync(~0u, top[h], 1));
-          top[h] = fmaxf(top[h], __shfl_xor_sync(~0u, top[h], 2));
-          const float now = fmaxf(mx[h], top[h]);
+          const float now = fmaxf(mx[h], row_max(top[h]));
           corr[h] = now == -INFINITY ? 1.f : exp2_fast(mx[h] - now);
           mx[h] = now;
           l[h] *= corr[h];
         }
 #pragma unroll
-        for (int n = 0; n < ON; ++n) {
-          o[n][0] *= corr[0];
-          o[n][1] *= corr[0];
-          o[n][2] *= corr[1];
-          o[n][3] *= corr[1];
-        }
+        for (int n = 0; n < ON; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[n][e] *= corr[row_of(e)];
       }
       // a row without a key so far keeps -infinity: subtract 0 there
       const float ref[2] = {mx[0] == -INFINITY ? 0.f : mx[0],
                             mx[1] == -INFINITY ? 0.f : mx[1]};
+      // P of the 16-key steps as operands (bf16: high and low part), and, turned over, as
+      // they are held: [.. + 2 ..]
+      uint32_t pf[SUBS][4], pl[SUBS][4];
 #pragma unroll
       for (int t = 0; t < TILES; ++t) {
         float p[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          p[e] = exp2_fast(fmaf(s[t][e], qs[e >> 1], -ref[e >> 1]));
-          l[e >> 1] += p[e];
+          p[e] = exp2_fast(fmaf(s[t][e], qs[row_of(e)], -ref[row_of(e)]));
+          l[row_of(e)] += p[e];
           if constexpr (Q8) {
             // a masked key's scale may be anything
-            p[e] = edge && s[t][e] == -INFINITY ? 0.f : p[e] * vsc[t][e & 1];
+            p[e] = edge && s[t][e] == -INFINITY ? 0.f : p[e] * vsc[t][key_of(e)];
           }
         }
-        const int step = t >> 1, r0 = (t & 1) * 2;
+        const int step = TURNED ? t : t >> 1, r0 = TURNED ? 2 : (t & 1) * 2;
         if constexpr (Q8) {
           pf[step][r0] = pack_f16x2(p[0], p[1]);
           pf[step][r0 + 1] = pack_f16x2(p[2], p[3]);
@@ -471,9 +512,17 @@ chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__
           pl[step][r0] = pack_bf16x2(p[0] - bf16lo(a01), p[1] - bf16hi(a01));
           pl[step][r0 + 1] = pack_bf16x2(p[2] - bf16lo(a23), p[3] - bf16hi(a23));
         }
+        if constexpr (TURNED) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            pf[step][x] = transposed(pf[step][2 + x]);
+            if constexpr (!Q8) pl[step][x] = transposed(pl[step][2 + x]);
+          }
+        }
       }
 
-      // ---- O += P V: n tile n, column g is column d(g, n) of the head ----
+      // ---- O += P V, or V^T P^T: n tile n, column g is column d(g, n) of the head ----
+      // (turned over, two n tiles are one of 16 columns)
       const uint8_t* const sv = st + R::K_BYTES;
 #pragma unroll
       for (int step = 0; step < SUBS; ++step) {
@@ -483,9 +532,8 @@ chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__
             uint32_t w[4][4];
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
-              const uint4 x =
-                  *reinterpret_cast<const uint4*>(sv + (step * R::H + c) * R::BOX + (kk >> 1) * 8 * R::LINE +
-                                                  v_at[kk & 1]);
+              const uint4 x = *reinterpret_cast<const uint4*>(
+                  sv + (step * R::H + c) * R::BOX + (kk >> 1) * 8 * R::LINE + v_at[kk & 1]);
               w[kk][0] = x.x;
               w[kk][1] = x.y;
               w[kk][2] = x.z;
@@ -508,36 +556,54 @@ chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__
                 const uint32_t b1 = __byte_perm(w[2][j], w[3][j], 0x5410u);
                 const uint32_t d0 = __byte_perm(w[0][j], w[1][j], 0x7632u);
                 const uint32_t d1 = __byte_perm(w[2][j], w[3][j], 0x7632u);
-                mma_bf16_16816(o[c * 8 + 2 * j], pf[step], b0, b1);
-                mma_bf16_16816(o[c * 8 + 2 * j + 1], pf[step], d0, d1);
-                mma_bf16_16816(o[c * 8 + 2 * j], pl[step], b0, b1);
-                mma_bf16_16816(o[c * 8 + 2 * j + 1], pl[step], d0, d1);
+                if constexpr (TURNED) {
+                  const uint32_t vf[4] = {b0, d0, b1, d1};
+                  mma_bf16_16816(o[c * 4 + j], vf, pf[step][0], pf[step][1]);
+                  mma_bf16_16816(o[c * 4 + j], vf, pl[step][0], pl[step][1]);
+                } else {
+                  mma_bf16_16816(o[c * 8 + 2 * j], pf[step], b0, b1);
+                  mma_bf16_16816(o[c * 8 + 2 * j + 1], pf[step], d0, d1);
+                  mma_bf16_16816(o[c * 8 + 2 * j], pl[step], b0, b1);
+                  mma_bf16_16816(o[c * 8 + 2 * j + 1], pl[step], d0, d1);
+                }
               }
-            } else {
-              // element by element: output columns 2 tig + e of n tile 8 c + 2 j + x
+            } else {   // element by element
 #pragma unroll 1
               for (int key = 0; key < 16; ++key) {
                 const int kt = (key & 7) >> 1, kk = (key >> 3) * 2 + (key & 1);   // its lanes, its piece
                 float pr[2];
+                if constexpr (TURNED) {
+                  const int from = (key & 7) * 4 + tig;
+                  const uint32_t hi = __shfl_sync(~0u, key & 8 ? pf[step][3] : pf[step][2], from);
+                  const uint32_t lo = __shfl_sync(~0u, key & 8 ? pl[step][3] : pl[step][2], from);
+                  pr[0] = bf16lo(hi) + bf16lo(lo);
+                  pr[1] = bf16hi(hi) + bf16hi(lo);
+                } else {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const uint32_t hi =
-                      __shfl_sync(~0u, key & 8 ? pf[step][2 + h] : pf[step][h], g * 4 + kt);
-                  const uint32_t lo =
-                      __shfl_sync(~0u, key & 8 ? pl[step][2 + h] : pl[step][h], g * 4 + kt);
-                  pr[h] = key & 1 ? bf16hi(hi) + bf16hi(lo) : bf16lo(hi) + bf16lo(lo);
+                  for (int h = 0; h < 2; ++h) {
+                    const uint32_t hi =
+                        __shfl_sync(~0u, key & 8 ? pf[step][2 + h] : pf[step][h], g * 4 + kt);
+                    const uint32_t lo =
+                        __shfl_sync(~0u, key & 8 ? pl[step][2 + h] : pl[step][h], g * 4 + kt);
+                    pr[h] = key & 1 ? bf16hi(hi) + bf16hi(lo) : bf16lo(hi) + bf16lo(lo);
+                  }
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                   const uint32_t mine = kk == 0 ? w[0][j] : kk == 1 ? w[1][j] : kk == 2 ? w[2][j] : w[3][j];
 #pragma unroll
-                  for (int e = 0; e < 2; ++e) {
-                    const uint32_t x = __shfl_sync(~0u, mine, (2 * tig + e) * 4 + kt);
+                  for (int e = 0; e < (TURNED ? 1 : 2); ++e) {   // column g, or columns 2 tig + e
+                    const uint32_t x = __shfl_sync(~0u, mine, (TURNED ? g : 2 * tig + e) * 4 + kt);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                       if (pr[h] == 0.f) continue;
-                      o[c * 8 + 2 * j][2 * h + e] += pr[h] * bf16lo(x);
-                      o[c * 8 + 2 * j + 1][2 * h + e] += pr[h] * bf16hi(x);
+                      if constexpr (TURNED) {
+                        o[c * 4 + j][h] += pr[h] * bf16lo(x);
+                        o[c * 4 + j][2 + h] += pr[h] * bf16hi(x);
+                      } else {
+                        o[c * 8 + 2 * j][2 * h + e] += pr[h] * bf16lo(x);
+                        o[c * 8 + 2 * j + 1][2 * h + e] += pr[h] * bf16hi(x);
+                      }
                     }
                   }
                 }
@@ -568,16 +634,27 @@ chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__
             const uint32_t a1 = __byte_perm(w[0][j], w[1][j], 0x7362u);
             const uint32_t c0 = __byte_perm(w[2][j], w[3][j], 0x5140u);
             const uint32_t c1 = __byte_perm(w[2][j], w[3][j], 0x7362u);
+            uint32_t b[4][2];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               const uint32_t sel = x & 1 ? 0x4342u : 0x4140u;
-              const uint32_t b0 = codes2(x < 2 ? a0 : a1, sel), b1 = codes2(x < 2 ? c0 : c1, sel);
-              mma_f16(o[4 * j + x], pf[step], b0, b1);
+              b[x][0] = codes2(x < 2 ? a0 : a1, sel);
+              b[x][1] = codes2(x < 2 ? c0 : c1, sel);
+            }
+            if constexpr (TURNED) {
+#pragma unroll
+              for (int x = 0; x < 4; x += 2) {
+                const uint32_t vf[4] = {b[x][0], b[x + 1][0], b[x][1], b[x + 1][1]};
+                mma_f16(o[2 * j + (x >> 1)], vf, pf[step][0], pf[step][1]);
+              }
+            } else {
+#pragma unroll
+              for (int x = 0; x < 4; ++x) mma_f16(o[4 * j + x], pf[step], b[x][0], b[x][1]);
             }
           }
         }
       }
-      __syncwarp();   // the stage's scales were read by other lanes
+      __syncwarp();   // the stage was read by other lanes
       stage = stage + 1 == STAGES ? 0 : stage + 1;
     }
 
@@ -622,10 +699,9 @@ chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__
 #pragma unroll
         for (int n = 0; n < ON; ++n) {
           const float4 v = in[n * 32];
-          o[n][0] = o[n][0] * c0[0] + v.x * c1[0];
-          o[n][1] = o[n][1] * c0[0] + v.y * c1[0];
-          o[n][2] = o[n][2] * c0[1] + v.z * c1[1];
-          o[n][3] = o[n][3] * c0[1] + v.w * c1[1];
+          const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[n][e] = o[n][e] * c0[row_of(e)] + x[e] * c1[row_of(e)];
         }
       }
       bar_arrive(free);
@@ -635,26 +711,26 @@ chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__
       // a CTA's first piece goes to its slot 0, its last to slot 1
       const int64_t slot = 2 * (int64_t)blockIdx.x + (at == line_lo ? 0 : 1);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        l[h] += __shfl_xor_sync(~0u, l[h], 1);
-        l[h] += __shfl_xor_sync(~0u, l[h], 2);
-      }
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int d = TURNED ? 4 : 1; d < (TURNED ? 32 : 4); d *= 2) l[h] += __shfl_xor_sync(~0u, l[h], d);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int r = h * 8 + g, row = u.tile * RT + r, q = a.by_group.quot(row);
+        const int r = tile_row(h), row = u.tile * RT + r, q = a.by_group.quot(row);
         if (q >= u.rows) continue;
         const float inv = mx[h] == -INFINITY ? 0.f : 1.f / l[h];
         uint16_t* const to =
             a.O + ((int64_t)(u.row0 + q) * a.n_heads_q + u.head * G + row - q * G) * D;
         float* const part = a.part_o + (slot * RT + r) * D;
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+        for (int e = 0; e < (TURNED ? 1 : 2); ++e)   // column g, or columns 2 tig + e
 #pragma unroll
-          for (int n = 0; n < ON; n += 8) {   // columns d .. d + 7
-            const int d = Q8 ? (2 * tig + e) * (D / 8) + n : n * 8 + (2 * tig + e) * 8;
+          for (int n = 0; n < D / 8; n += 8) {   // columns d .. d + 7
+            const int gg = TURNED ? g : 2 * tig + e, d = Q8 ? gg * (D / 8) + n : n * 8 + gg * 8;
             float x[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = o[n + k][2 * h + e];
+            for (int k = 0; k < 8; ++k)
+              x[k] = TURNED ? o[(n + k) >> 1][(k & 1) * 2 + h] : o[TURNED ? 0 : n + k][2 * h + e];
             if (whole) {
               *reinterpret_cast<uint4*>(to + d) =
                   make_uint4(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv),
@@ -664,7 +740,8 @@ chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__
               __stcg(reinterpret_cast<float4*>(part + d + 4), make_float4(x[4], x[5], x[6], x[7]));
             }
           }
-        if (!whole && tig == 0) __stcg(a.part_ml + slot * RT + r, make_float2(mx[h], l[h]));
+        if (!whole && (TURNED ? g : tig) == 0)
+          __stcg(a.part_ml + slot * RT + r, make_float2(mx[h], l[h]));
       }
     }
     at = u.begin + kb1;
@@ -681,7 +758,7 @@ chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__
 // rounds of reads from L2, at the end of every call: what it needs to know
 // lies ready in the list of cuts.
 constexpr int JOIN_WARPS = 4;   // per CTA
-constexpr int join_split(int rt) { return rt == RT ? RT / JOIN_WARPS : 16; }   // CTAs per tile
+constexpr int join_split(int rt) { return rt <= WIDE ? rt / JOIN_WARPS : 16; }   // CTAs per tile
 
 template <int D, int RT>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) chunk_join_kernel(const __grid_constant__ ChunkArgs a) {
@@ -773,13 +850,13 @@ int32_t launch_join(const ChunkArgs& a, int n_ctas, cudaStream_t st) {
   return SUB_OK;
 }
 
-template <int D, bool Q8>
+template <int D, bool Q8, int RT>
 int32_t launch_decode(const ChunkArgs& a, int n_ctas, cudaStream_t st) {
   static std::once_flag once;
   static cudaError_t err = cudaSuccess;
   constexpr int SMEM = decode_smem<D, Q8>();
   std::call_once(once, [] {
-    err = cudaFuncSetAttribute(chunk_attn_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    err = cudaFuncSetAttribute(chunk_attn_kernel<D, Q8, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                SMEM);
   });
   SUB_CUDA_TRY(err);
@@ -787,7 +864,7 @@ int32_t launch_decode(const ChunkArgs& a, int n_ctas, cudaStream_t st) {
   if (!chunk_page_map(&maps.k, a.k, a.t, (int64_t)a.n_layers * a.n_heads_kv, D, Q8) ||
       !chunk_page_map(&maps.v, a.v, a.t, (int64_t)a.n_layers * a.n_heads_kv, D, Q8))
     return fail(SUB_ECUDA, "chunk_attn: the cache's tensor map was refused");
-  SUB_CUDA_TRY(launch_k(chunk_attn_kernel<D, Q8>, dim3(n_ctas), dim3(NT), SMEM, st, maps, a));
+  SUB_CUDA_TRY(launch_k(chunk_attn_kernel<D, Q8, RT>, dim3(n_ctas), dim3(NT), SMEM, st, maps, a));
   return launch_join<D, RT>(a, n_ctas, st);
 }
 
@@ -798,7 +875,8 @@ int32_t launch_decode(const ChunkArgs& a, int n_ctas, cudaStream_t st) {
 // and 63).  Codes, which the tensor-core kernel has to convert first: 64 rows (32 rows
 // 51 and 34, 64 rows 53 and 49).
 int tile_rows(int group, int n_seqs, int n_rows, bool codes) {
-  return (int64_t)n_rows * group <= (codes ? 4 : 1) * RT * (int64_t)n_seqs ? RT : CHUNK_TC_ROWS;
+  const int64_t rows = (int64_t)n_rows * group, seqs = n_seqs;
+  return rows <= NARROW * seqs ? NARROW : rows <= (codes ? 4 : 1) * WIDE * seqs ? WIDE : CHUNK_TC_ROWS;
 }
 
 // Partial results, two per CTA, and the list of cuts.
@@ -855,7 +933,7 @@ int32_t chunk_attn(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q, const Cach
       (int64_t)kv->n_layers * kv->n_pages * kv->n_heads_kv * kv->page_size;
   const bool tensor_cores = rt == CHUNK_TC_ROWS && chunk_tc_fits(pool_rows);
   const int n_ctas = sm_count();
-  const int part_rows = tensor_cores ? CHUNK_TC_ROWS : RT;
+  const int part_rows = tensor_cores ? CHUNK_TC_ROWS : std::min(rt, WIDE);
   a.part_o = reinterpret_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float2*>(a.part_o + (int64_t)n_ctas * 2 * part_rows * kv->head_dim);
   a.cuts = reinterpret_cast<ChunkCut*>(a.part_ml + (int64_t)n_ctas * 2 * part_rows);
@@ -864,8 +942,11 @@ int32_t chunk_attn(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q, const Cach
     return kv->head_dim == 128 ? launch_join<128, CHUNK_TC_ROWS>(a, n_ctas, st)
                                : launch_join<64, CHUNK_TC_ROWS>(a, n_ctas, st);
   }
-  return kv->head_dim == 128 ? launch_decode<128, Q8>(a, n_ctas, st)
-                             : launch_decode<64, Q8>(a, n_ctas, st);
+  if (rt == NARROW)
+    return kv->head_dim == 128 ? launch_decode<128, Q8, NARROW>(a, n_ctas, st)
+                               : launch_decode<64, Q8, NARROW>(a, n_ctas, st);
+  return kv->head_dim == 128 ? launch_decode<128, Q8, WIDE>(a, n_ctas, st)
+                             : launch_decode<64, Q8, WIDE>(a, n_ctas, st);
 }
 
 }  // namespace

@@ -307,6 +307,23 @@ def test_later_keys_do_not_reach_earlier_rows(sub, n, bad):
     assert torch.isfinite(torch.cat([o[early], o[n:]])).all()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_later_keys_do_not_reach_earlier_rows_in_small_tiles(sub, d, bad):
+    """The same for at most 8 rows per sequence and KV head."""
+    c = Case(sub, [(45, 4), (20, 1), (33, 1)], 4, 2, d, seed=8)
+    clean = sub.chunk_attn(c.q.to(DEV), c.kv, c.layer, c.batch).clone()
+    pg, pl = int(c.table[0, 47 // 16]), 47 % 16
+    c.pools[1][c.layer, pg, 1, pl, 5] = bad
+    c.pools[0][c.layer, pg, 0, pl, 7] = bad
+    o = sub.chunk_attn(c.q.to(DEV), c.kv, c.layer, c.batch)
+    assert torch.equal(torch.cat([o[:2], o[4:]]), torch.cat([clean[:2], clean[4:]]))
+    assert not torch.isfinite(o[2:4, 2:, 5]).any()
+    other = [x for x in range(d) if x != 5]
+    assert (o[2:4, 2:, other] - clean[2:4, 2:, other]).abs().max() < 0.05
+    assert not torch.isfinite(o[2:4, :2]).all()
+
+
 @pytest.mark.parametrize("bits,d", [(16, 128), (16, 64), (8, 128), (8, 64)])
 @pytest.mark.parametrize("n", [1, 3, 40])
 def test_a_key_that_is_not_a_number_is_not_lost(sub, bits, d, n):

@@ -869,14 +869,17 @@ int32_t launch_decode(const ChunkArgs& a, int n_ctas, cudaStream_t st) {
 }
 
 // Rows of a tile, by the rows that a sequence has on average (rows and sequences are
-// known here, lengths only on the device).  The warps' kernel reads the keys again
-// for every tile of 16 rows, the tensor-core kernel once for 256.  bf16: 16 rows
-// (8 sequences over 4000 keys: 32 rows 39 us by the tensor cores, 42 here, 64 rows 39
-// and 63).  Codes, which the tensor-core kernel has to convert first: 64 rows (32 rows
-// 51 and 34, 64 rows 53 and 49).
-int tile_rows(int group, int n_seqs, int n_rows, bool codes) {
+// known here, lengths only on the device) and the most keys that one may have.  The
+// warps' kernel reads the keys again for every tile, the tensor-core kernel once for 256
+// rows, but it starts later and wants blocks of 128 keys.  bf16: 16 rows, and 32 up to
+// 4096 keys (32 rows of 1 sequence over 1000 keys 15 us here, 19 by the tensor cores; of
+// 8 over 4000 37 and 36; of 1 over 16000 33 and 29; 64 rows of 8 over 4000 54 and
+// 37).  Codes, which the tensor-core kernel has to convert first: 64 rows (32 rows
+// of 8 sequences over 4000 keys 34 and 51, 64 rows 49 and 53, 112 rows 43 and 38).
+int tile_rows(int group, int n_seqs, int n_rows, bool codes, int64_t keys) {
   const int64_t rows = (int64_t)n_rows * group, seqs = n_seqs;
-  return rows <= NARROW * seqs ? NARROW : rows <= (codes ? 4 : 1) * WIDE * seqs ? WIDE : CHUNK_TC_ROWS;
+  const int tiles = codes ? 4 : keys <= 4096 ? 2 : 1;
+  return rows <= NARROW * seqs ? NARROW : rows <= tiles * WIDE * seqs ? WIDE : CHUNK_TC_ROWS;
 }
 
 // Partial results, two per CTA, and the list of cuts.
@@ -928,7 +931,8 @@ int32_t chunk_attn(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q, const Cach
     SUB_TRY(scratch.alloc((size_t)need));
     workspace = scratch.p;
   }
-  const int rt = tile_rows(a.group, a.t.n_seqs, a.t.n_rows, Q8);
+  const int rt = tile_rows(a.group, a.t.n_seqs, a.t.n_rows, Q8,
+                           batch->max_keys ? std::min(batch->max_keys, kv->capacity) : kv->capacity);
   const int64_t pool_rows =
       (int64_t)kv->n_layers * kv->n_pages * kv->n_heads_kv * kv->page_size;
   const bool tensor_cores = rt == CHUNK_TC_ROWS && chunk_tc_fits(pool_rows);
@@ -971,7 +975,7 @@ extern "C" int32_t sub_chunk_attn_workspace(int32_t n_heads_q, int32_t n_heads_k
   SUB_CHECK_ARG(n_heads_kv >= 1 && n_heads_q >= 1 && n_heads_q % n_heads_kv == 0,
                 "Hq must be a multiple of Hkv");
   SUB_CHECK_ARG(n_seqs >= 1 && n_seqs <= SUB_MAX_SEQS && n_rows >= 0, "bad batch sizes");
-  const int rt = tile_rows(n_heads_q / n_heads_kv, n_seqs, n_rows, false);   // the larger one
+  const int rt = tile_rows(n_heads_q / n_heads_kv, n_seqs, n_rows, false, INT64_MAX);   // the largest of them
   *bytes = n_rows ? part_bytes(rt, head_dim) : 0;
   return SUB_OK;
 }

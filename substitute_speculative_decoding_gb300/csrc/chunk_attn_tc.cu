@@ -716,7 +716,8 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
       const int n_box = KB / box;
       const bool mine = b0 < n_box && half < D / 64;
       int row = n > 0 && b0 < n_box ? row_of(b0 * box) : -1, before = -1;
-      for (uint32_t j = 0; j <= n && n > 0; ++j) {
+      uint32_t j = 0;
+      for (; j <= n && n > 0; ++j) {
         // 16-key parts without a page (those past the last key count as read past the end)
         const unsigned gone = __ballot_sync(~0u, side == 0 && half == 0 && row == -2);
         // rows of the pool, one per box; past the pool (zeros) where there is no page
@@ -742,6 +743,9 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
                           b0 * box * 128,
                       side ? &maps.v : &maps.k, half * 64, y < 0 ? pool_rows : y, kv_full(j));
       }
+      // the copies issued last: none may be under way when the CTA ends, whatever its consumers did
+      for (uint32_t i = j > SLOTS ? j - SLOTS : 0; i < j; ++i)
+        mbar_wait_polls(kv_full(i), (i / SLOTS) & 1, 1u << 20);
     } else {
       // Four lanes take 64 codes of a key, a warp's load eight keys; thread ptid looks
       // up the pool row of key ptid.  Rows are looked up two blocks ahead of the
@@ -861,13 +865,6 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
         if (j + 1 < n) store_scales(j + 1);
         meet();          // the rows of block j + 2 and the scales of block j + 1 are there
       }
-    }
-    if constexpr (!Q8) {
-      // after a wait ran out: copies into the slots may still be under way
-      if (!ok && lane == 0)
-        for (int s = 0; s < SLOTS; ++s)
-          for (uint32_t i = 0; i < (1u << 16) && !mbar_try_wait(kv_full(s), 0) && !mbar_try_wait(kv_full(s), 1); ++i) {
-          }
     }
   }
   tc_fence_before();

@@ -64,8 +64,8 @@ const char* sub_version(void);
  * Unset (the default) costs one getenv per allocation or copy. */
 
 /* Pipeline waits that ran out on the current device since the library was
- * loaded.  Every wait inside the TMA-streamed GEMV and the tensor-core GEMM
- * (mbarrier phases, the grid-wide counters) is bounded: one that runs out
+ * loaded.  Every wait inside the TMA-streamed GEMV, the tensor-core GEMM and the
+ * attention of batches (mbarrier phases, the grid-wide counters) is bounded: one that runs out
  * bumps this count and lets the kernel finish with wrong numbers instead of
  * hanging.  A correct run leaves it at 0; a non-zero value means the results
  * of that run are invalid.  *out receives the count. */
@@ -335,7 +335,10 @@ int32_t sub_kv8_read(const sub_kv8_cache* kv, int32_t layer, const sub_batch* ba
  * whatever they hold) does not change it.
  * Hq % Hkv == 0, Hq / Hkv <= 64; head_dim 64 or 128.  Which sequences share
  * the batch, and max_keys, move a row's result by rounding only; the same call
- * gives the same bits.  workspace: sub_chunk_attn_workspace(...) bytes of
+ * gives the same bits.  Rounding: the weights to bf16 or better; of codes, when a
+ * sequence has more than 64 rows per KV head on average, also the values, to fp16
+ * relative to the largest scale among 128 neighbouring keys (a key whose scale is
+ * less than 2^-14 of that keeps fewer bits).  workspace: sub_chunk_attn_workspace(...) bytes of
  * device memory, 32-byte aligned, used by this call alone until it is done
  * (its contents do not matter); NULL: drawn from the stream's memory pool. */
 int32_t sub_chunk_attn(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q, const sub_kv_cache* kv,

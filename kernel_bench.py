@@ -24,6 +24,11 @@ than the 129 MB L2):
               "draft_level" (the second of two runs)
   verify_pass one target forward over a 385-node tree (offloaded layers streamed),
               inside the NVTX range "verify_pass"
+  batch_decode, batch_decode8  attention of one new row of each of 128 sequences of 500
+              to 2000 keys, 32/8 heads, d 128, bf16 or 8-bit cache
+  batch_chunk, batch_chunk8    attention of 1024 new rows behind 7000 keys, same heads
+  batch_probs, batch_verify    probabilities of 576 rows of 128256 logits; verification of
+              64 sequences' 8 drafted tokens against them
 Prints one JSON line: milliseconds per launch and algorithmic GB/s, TFLOP/s.
 """
 from __future__ import annotations
@@ -99,6 +104,37 @@ def _model_pass(case):
         out["ms"] = e0.elapsed_time(e1)
     m.close()
     return out
+
+
+def _batch_attn(bits, lens, n_new, iters):
+    """Attention of the last n_new of each sequence's positions, two caches in turn."""
+    hq, hkv, d, page, dev = 32, 8, 128, 64, "cuda"
+    width = -(-max(lens) // page)
+    n_pages = len(lens) * width
+    table = torch.randperm(n_pages, generator=torch.Generator().manual_seed(0))
+    table = table.view(len(lens), width).to(torch.int32).to(dev)
+    start = torch.arange(len(lens) + 1, dtype=torch.int32, device=dev) * n_new
+    pos = torch.tensor([n - n_new for n in lens], dtype=torch.int32, device=dev)
+    batch = sub.batch(start, pos, len(lens) * n_new, max(lens))
+    shape = (1, n_pages, hkv, page, d)
+    caches = []
+    for _ in range(2):
+        if bits == 16:
+            caches.append(sub.paged_kv(*(torch.randn(shape, device=dev, dtype=torch.bfloat16)
+                                         for _ in range(2)), table))
+        else:
+            codes = [torch.randint(1, 256, shape, device=dev, dtype=torch.uint8) for _ in range(2)]
+            caches.append(sub.paged_kv8(*codes, *(torch.rand(shape[:4], device=dev) / 64 + 1e-3
+                                                  for _ in range(2)), table))
+    q = torch.randn(len(lens) * n_new, hq, d, device=dev).to(torch.bfloat16)
+    o = torch.empty_like(q)
+    ws = torch.empty(sub.chunk_attn_workspace(hq, hkv, d, len(lens), len(lens) * n_new),
+                     dtype=torch.uint8, device=dev)
+    ms = _time(lambda i: sub.chunk_attn(q, caches[i % 2], 0, batch, out=o, workspace=ws), iters)
+    row = d * 4 if bits == 16 else d * 2 + 8
+    byt = sum(lens) * hkv * row + 4 * q.numel()
+    flops = sum(4 * hq * d * (n_new * n - n_new * (n_new - 1) // 2) for n in lens)
+    return dict(ms=ms, gbs=byt / ms / 1e6, tflops=flops / ms / 1e9)
 
 
 def main():
@@ -253,6 +289,26 @@ def main():
         ms = _time(lambda i: sub.tree_attn(q, caches[i % nc][0], 0, lkv, lkv, n_tree, anc=an,
                                            depth=dp), max(a.iters, nc))
         byt = kv_bytes + 4 * 8 * hq * d
+        res.update(ms=ms, gbs=byt / ms / 1e6)
+    elif a.case in ("batch_decode", "batch_decode8"):
+        lens = [500 + (1500 * i) // 127 for i in range(128)]
+        res.update(_batch_attn(8 if a.case.endswith("8") else 16, lens, 1, a.iters))
+    elif a.case in ("batch_chunk", "batch_chunk8"):
+        res.update(_batch_attn(8 if a.case.endswith("8") else 16, [8024], 1024, a.iters))
+    elif a.case in ("batch_probs", "batch_verify"):
+        b, n, v = 64, 8, 128256
+        z = torch.randn(b * (n + 1), v, device=dev)
+        out = torch.empty_like(z)
+        if a.case == "batch_probs":
+            ms = _time(lambda i: sub.probs(z, 0.6, out=out), a.iters)
+            byt = 8 * z.numel()
+        else:
+            p = sub.probs(z, 0.6, out=out).view(b, n + 1, v)
+            q = sub.probs(torch.randn(b * n, v, device=dev), 0.6).view(b, n, v)
+            draft = q.argmax(-1).to(torch.int32)
+            u = torch.rand(b, n + 1, device=dev)
+            ms = _time(lambda i: sub.verify_sample(p, q, draft, u), a.iters)
+            byt = 8 * b * v
         res.update(ms=ms, gbs=byt / ms / 1e6)
     elif a.case in ("draft_level", "verify_pass"):
         res.update(_model_pass(a.case))

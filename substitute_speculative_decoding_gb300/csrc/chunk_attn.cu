@@ -7,22 +7,35 @@
 // same tile, so a key is read once for all of them.
 //
 // Bound by HBM: a row tile of 16 does 64 flops per byte of a bf16 cache,
-// mma.sync covers that many times over, and what counts is bytes in flight and
-// instructions per key.  So each of eight warps streams blocks of 16 or 32 keys (8
-// KB) on its own, through a private ring of shared memory that its lanes fill with
-// cp.async and read themselves: a lane copies exactly the 16-byte pieces that it will
-// use as matrix operands, so there is no barrier, no swizzle and no ldmatrix in
-// the loop.  That works because a dot product may take its terms in any order, if
-// Q is laid out the same way: lane (g, tig) holds, of key g of an 8-key group, the
-// 16-byte chunks tig, tig + 4, .. of the row, and of V, for its four keys of a
-// 16-key step, the columns that make its B fragments for the n tiles of eight
-// chunk-wise permuted columns.
+// mma.sync covers that many times over, and what counts is bytes in flight.  So
+// each of eight warps streams blocks of 16 or 32 keys (8 KB; 4 KB of codes of 64
+// columns) on its own, through a private ring of three stages that bulk tensor copies
+// fill, one lane per 2 KB box, over all its units of work one after the other.  (The same
+// loop with 16-byte cp.async copies, sixteen per lane and block, ran at 5.1 TB/s
+// on 32 sequences of up to 16384 keys and left a quarter of the SMs a fifth slower
+// than the rest; the copies alone now take 203 us, 6.7 TB/s, and the kernel
+// 218.)  No barrier in the loop, no ldmatrix: a dot product may take its terms
+// in any order, if Q is laid out the same way, so lane (g, tig) reads, of key g of an
+// 8-key group, the 16-byte chunks 2 tig, 2 tig + 1 of each 128 bytes, and of V, for
+// its four keys of a 16-key step, the chunk that makes its B fragments for the n tiles of
+// eight chunk-wise permuted columns; the boxes' swizzle spreads both over all banks.
+//
+// At most 8 rows are a tile of their own, with both products turned over (S^T = K Q^T,
+// O^T = V^T P^T): half the matrix instructions, exponentials and accumulators of 16
+// rows.  The turned weights are already the next product's operand but for an
+// 8x8 transposition.
+//
+// Measured: 32 rows of 32 sequences of up to 16384 keys 218 us (1.37 GB, 6.3 TB/s);
+// codes, 2 sequences of 65536 47 us (4.5 TB/s); 128 of up to 2000 keys 126 us (5.2
+// TB/s), codes 95 (3.6); 1 sequence of 64 keys 10 us, a launch, its dependent
+// reads and the join.  Over codes the conversions and, on short caches, the
+// change of units show: the same loads without the products take 43 and 75 us.
 //
 // 8-bit codes c stand for (c - 128) * scale, and both products take c - 128 in
 // fp16, exactly: the bytes 0x64, c are 1024 + c, a byte permute and a subtraction
 // for two of them.  The scale of k_j multiplies the score, and the scale of v_j
 // goes into e_ij before it is rounded to fp16.
-// The running maximum includes log2 of the largest vscale in reach, minus 15, so
+// The running maximum includes log2 of the largest vscale that the row reads, minus 15, so
 // that what is rounded reaches 2^15 at most, and fp16's smallest step, 2^-24, is
 // 2^-39 of the largest; the sum takes the unscaled e_ij, in fp32, relative to the
 // same maximum (log2(vscale) counts as at least -80, which keeps it in range).  Q
@@ -31,10 +44,11 @@
 // cache P = hi + lo, two bf16 products, keeps it to 2^-17; in fp16 one product keeps
 // 2^-12.
 //
-// A key that a row must not read can still hold anything.  Its score is replaced,
-// and where its value is infinite or NaN (bf16 only, and only in blocks that
-// not all rows read to the end), the block's products with V are formed one by
-// one without the keys of weight zero.
+// A key that a row must not read can still hold anything, and so can a box past the
+// last key or of a page that is not there.  Its score is replaced, and where its
+// value is infinite or NaN (bf16 only, and only in blocks that not all rows read
+// to the end), the block's products with V are formed one by one without the keys of
+// weight zero.
 #include <algorithm>
 #include <mutex>
 #include <type_traits>
@@ -142,8 +156,8 @@ chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + (-smem_u32(smem_raw) & 1023u);   // as the boxes' swizzle wants it
   __shared__ int64_t s_pre[SUB_MAX_SEQS + 1];
-  __shared__ int s_at[WARPS];          // their stages
   __shared__ float4 s_ml[WARPS][32];   // maxima and sums of the warps' partial results, by lane
+  __shared__ int s_at[WARPS];          // the stages that these lie in
   __shared__ __align__(8) uint64_t s_bar[WARPS][STAGES];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid < WARPS * STAGES) mbar_init(smem_u32(&s_bar[0][0] + tid), 1);
@@ -278,7 +292,7 @@ chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int q = a.by_group.quot(u.tile * RT + tile_row(h));
-      lim[h] = q < u.rows ? min(u.pos + q, u.n_keys - 1) : -1;
+      lim[h] = q < u.rows ? last_key(u.pos, q, u.n_keys) : -1;
       qs[h] = a.sl2;
     }
 #pragma unroll
@@ -337,7 +351,7 @@ chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__
       qs[0] = __shfl_sync(~0u, mine, 8 * tig);
       qs[1] = __shfl_sync(~0u, mine, 8 * tig + 4);
     }
-    const int lim_min = min(u.pos + a.by_group.quot(u.tile * RT), u.n_keys - 1);   // of the tile's first row
+    const int lim_min = last_key(u.pos, a.by_group.quot(u.tile * RT), u.n_keys);   // of the tile's first row
     // largest value over the lanes that share their rows
     auto row_max = [](float x) {
 #pragma unroll

@@ -66,16 +66,19 @@ __device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
   return (int64_t)q;
 }
 
+// Last key that row q of a sequence reads, of n_keys.  (pos may be anything.)
+__device__ __forceinline__ int last_key(int pos, int q, int n_keys) {
+  return (int)min((int64_t)pos + q, (int64_t)n_keys - 1);
+}
+
 // ---------------------------------------------------------------- work plan --
 // A unit of work is one tile of RT rows -- (row, head in group) pairs of one
 // KV head of one sequence -- over all the keys its last row reads, in blocks of
 // KB keys.  All units' blocks, sequence by sequence, KV head by KV head, tile by
 // tile, form one line that the CTAs share evenly, so that any mix of lengths
 // fills the GPU; a unit cut between CTAs is joined afterwards from their
-// partial results, in order.  (Smaller parts handed out as CTAs come free, four per
-// CTA, cost at every start what they gained at the end: 274 us against 275 for 32
-// sequences of up to 16384 keys, 87 against 62 for 2.)  Every CTA works its part out by
-// itself from the lengths on the device: the place of its first unit from running sums over the
+// partial results, in order.  Every CTA works its part out by itself from
+// the lengths on the device: the place of its first unit from running sums over the
 // sequences, the others one after the other.
 struct ChunkUnit {
   int b, head, tile;      // sequence, KV head, tile

@@ -3,7 +3,12 @@
 //
 // The same sums as chunk_attn.cu, in tiles of 256 (row, head in group) pairs x
 // 128 keys.  Bound by the tensor cores and, close behind, by the exponentials: a
-// tile pair costs 4 * 512 cycles of tcgen05.mma, and 2 * 128 * 128 exponentials.
+// block costs four products of 128 x 128 x D and 2 * 128 * 128 exponentials.
+// Measured: 2048 rows of 32 heads behind 14336 keys 341 us, 1512 TFLOP/s, 0.78 of a
+// plain bf16 matrix product of the library; over codes three prompts of 1537 rows of 28
+// heads behind up to 2600 keys 213 us, 593 TFLOP/s, where the converter warps' share of the
+// issue slots bounds it (1024 rows behind 7000 keys: 197 us, 122 with the
+// conversions left out).
 // So two groups of 128 rows alternate: while the tensor cores form one group's
 // scores or output, the four warps of the other turn scores into weights.
 //   warps 0-3, 4-7   softmax of rows 0-127 and 128-255, one row per thread (a
@@ -11,9 +16,9 @@
 //                    the Q tile's way into shared memory, and the results
 //   a producer       blocks of 128 keys into a ring, V of one beside K of the next
 //                    (they are used together): a TMA warp for a bf16 cache (boxes of as many keys
-//                    as a page holds together), or four warps that turn 8-bit
-//                    codes into fp16 code - 128 on the way
-//   one MMA thread   S = Q K^T into tensor memory; then, once the group's weights
+//                    as a page holds together), or eight warps that turn 8-bit
+//                    codes into fp16 values on the way
+//   one MMA warp     S = Q K^T into tensor memory; then, once the group's weights
 //                    are there, O += P V with P read from tensor memory (in
 //                    place of S, as bf16 or fp16 pairs) and S of the next block
 // O stays in tensor memory.  It is rescaled only when a row's maximum has grown
@@ -233,7 +238,7 @@ struct Gate {
 };
 
 // Bit of a block's 16-key part in its word of missing pages: the TMA warp writes
-// the word, the four converter warps a byte each.
+// the word, each converter warp that looks keys up a byte.
 template <bool Q8>
 __device__ constexpr int miss_bit(int part) {
   return Q8 ? 8 * (part >> 1) + (part & 1) : part;
@@ -415,8 +420,8 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
       const int row = u.tile * RT + t * GROUP_ROWS + r, q = a.by_group.quot(row);
       const bool real = q < u.rows;
       const int n_keys = u.n_keys;
-      const int lim = real ? min(u.pos + q, n_keys - 1) : -1;                         // keys 0 .. lim are read
-      const int lim_first = min(u.pos + a.by_group.quot(u.tile * RT), n_keys - 1);    // by every row of the tile
+      const int lim = real ? last_key(u.pos, q, n_keys) : -1;                         // keys 0 .. lim are read
+      const int lim_first = last_key(u.pos, a.by_group.quot(u.tile * RT), n_keys);    // by every row of the tile
       float factor = a.sl2;        // of the row's scores, to base 2
       if constexpr (Q8) factor = s_qs[t * GROUP_ROWS + r];
 

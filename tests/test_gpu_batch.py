@@ -307,6 +307,19 @@ def test_later_keys_do_not_reach_earlier_rows(sub, n, bad):
     assert torch.isfinite(torch.cat([o[early], o[n:]])).all()
 
 
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("n", [2, 12, 40])
+def test_positions_at_the_end_of_int32(sub, bits, n):
+    """Rows beyond the capacity read all of it, however far beyond."""
+    c = Case(sub, [(64 - n, n)], 8, 2, 64, bits=bits, seed=9)
+    q = c.q.to(DEV)
+    o = [sub.chunk_attn(q, c.kv, c.layer,
+                        sub.batch(c.start.to(DEV), torch.tensor([pos], dtype=torch.int32, device=DEV), n))
+         for pos in (c.kv.capacity, 2 ** 31 - 2)]
+    assert torch.isfinite(o[0]).all() and o[0].abs().min(-1).values.max() > 0
+    assert torch.equal(o[0], o[1])
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("bad", [float("inf"), float("nan")])
 def test_later_keys_do_not_reach_earlier_rows_in_small_tiles(sub, d, bad):

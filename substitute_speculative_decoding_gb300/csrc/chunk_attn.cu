@@ -309,7 +309,7 @@ chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__
         // the chunk that K's c-th (bf16, 8 values), (c / 2)-th (codes, 16) operands come from
         const int i = Q8 ? c >> 1 : c, chunk = R::KI == 1 ? tig : 8 * (i >> 1) + 2 * tig + (i & 1);
         const int d = Q8 ? chunk * 16 + (c & 1) * 8 : chunk * 8;
-        w[c] = ok ? *reinterpret_cast<const uint4*>(src + d) : make_uint4(0, 0, 0, 0);
+        w[c] = ok ? ldg_cg_v4(src + d) : make_uint4(0, 0, 0, 0);
       }
       // registers of row g: 0 and 2 of a row operand, 0 and 1 of a column operand
       if constexpr (!Q8) {
@@ -780,7 +780,13 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) chunk_join_kernel(const __gri
   pdl_wait();
   pdl_trigger();
   const int part = blockIdx.x;
-  const ChunkCut c = a.cuts[part];
+  union {
+    int4 w[2];
+    ChunkCut cut;
+  } x;
+  x.w[0] = __ldcg(reinterpret_cast<const int4*>(a.cuts + part));
+  x.w[1] = __ldcg(reinterpret_cast<const int4*>(a.cuts + part) + 1);
+  const ChunkCut c = x.cut;
   if (c.pieces == 0) return;
   constexpr int LANES = D / 4, PER = 32 / LANES;   // lanes per piece, pieces per load
   constexpr int AHEAD = 8;                          // loads in flight

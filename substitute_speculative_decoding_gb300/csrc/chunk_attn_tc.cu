@@ -365,7 +365,7 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
         const int q = a.by_group.quot(row);
         w[i] = make_uint4(0, 0, 0, 0);
         if (q < x.rows)
-          w[i] = ldg_nc_v4(a.Q + (int64_t)(x.row0 + q) * a.ldq + (int64_t)(x.head * G + row - q * G) * D +
+          w[i] = ldg_cg_v4(a.Q + (int64_t)(x.row0 + q) * a.ldq + (int64_t)(x.head * G + row - q * G) * D +
                            c * 8);
       }
     };
@@ -599,8 +599,10 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
                 vp + pool_row(a.t, a.layer, a.n_heads_kv, page, done.head,
                               (int)((uint32_t)key % (uint32_t)a.t.page_size)) * D + x0;
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if ((x[i] & 0x7f80u) == 0x7f80u) o[i] += bf16_bits_to_f32(x[i]);
+            for (int i = 0; i < 32; ++i) {
+              const uint16_t bits = __ldcg(x + i);
+              if ((bits & 0x7f80u) == 0x7f80u) o[i] += bf16_bits_to_f32(bits);
+            }
           }
         }
         if (real && whole) {
@@ -773,7 +775,7 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
           const int row = s_rows[(j & 3) * KB + i / HV * KEYS + k0];
 #pragma unroll
           for (int h = 0; h < HV; ++h)
-            w[i + h] = row >= 0 ? ldg_nc_v4(p + (int64_t)row * D + h * 64)
+            w[i + h] = row >= 0 ? ldg_cg_v4(p + (int64_t)row * D + h * 64)
                                 : make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
         }
       };
@@ -781,8 +783,8 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
         if (ptid >= KB) return;
         const int row = s_rows[(j & 3) * KB + ptid];
         gone = __ballot_sync(~0u, row == -2);
-        ksc = row >= 0 ? a.ks[row] : 0.f;
-        vsc = row >= 0 ? a.vs[row] : 0.f;
+        ksc = row >= 0 ? __ldcg(a.ks + row) : 0.f;
+        vsc = row >= 0 ? __ldcg(a.vs + row) : 0.f;
       };
       auto store_scales = [&](uint32_t j) {
         if (ptid >= KB) return;

@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(ROW_WARPS * 32) append_kernel(RowArgs a) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int h = h0 + u * PER + sub;
-      w[u] = h < a.n_heads_kv ? ldg_nc_v4(src + h * D + l * 8) : make_uint4(0, 0, 0, 0);
+      w[u] = h < a.n_heads_kv ? ldg_cg_v4(src + h * D + l * 8) : make_uint4(0, 0, 0, 0);
     }
   };
   load(0);   // on its way while the row's place is looked up
@@ -149,8 +149,8 @@ __global__ void __launch_bounds__(ROW_WARPS * 32) read_kernel(RowArgs a) {
       s[u] = 0.f;
       if (p.page >= 0 && h < a.n_heads_kv) {
         const int64_t r = pool_row(a.t, a.layer, a.n_heads_kv, p.page, h, p.at);
-        w[u] = *(reinterpret_cast<const uint2*>(pool) + r * LANES + l);
-        s[u] = a.scale[side][r];
+        w[u] = __ldcg(reinterpret_cast<const uint2*>(pool) + r * LANES + l);
+        s[u] = __ldcg(a.scale[side] + r);
       }
     }
 #pragma unroll

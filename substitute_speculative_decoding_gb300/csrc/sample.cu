@@ -34,16 +34,17 @@ struct Row {
   __device__ bool whole(int g) const { return (unsigned)(g - inner) < (unsigned)n_inner; }
 };
 
-// Group g of row z; `none` where the row has no value.
+// Group g of row z, through L2 (the kernel just before may have written it); `none`
+// where the row has no value.
 template <bool VEC = true>
 __device__ __forceinline__ float4 load_group(const float* z, const Row& r, int g, float none) {
-  if (VEC && r.whole(g)) return *(reinterpret_cast<const float4*>(z - r.mis) + g);
+  if (VEC && r.whole(g)) return __ldcg(reinterpret_cast<const float4*>(z - r.mis) + g);
   const int64_t e = r.first(g);
   float4 x;
-  x.x = e >= 0 && e < r.V ? z[e] : none;
-  x.y = e + 1 >= 0 && e + 1 < r.V ? z[e + 1] : none;
-  x.z = e + 2 >= 0 && e + 2 < r.V ? z[e + 2] : none;
-  x.w = e + 3 < r.V ? z[e + 3] : none;
+  x.x = e >= 0 && e < r.V ? __ldcg(z + e) : none;
+  x.y = e + 1 >= 0 && e + 1 < r.V ? __ldcg(z + e + 1) : none;
+  x.z = e + 2 >= 0 && e + 2 < r.V ? __ldcg(z + e + 2) : none;
+  x.w = e + 3 < r.V ? __ldcg(z + e + 3) : none;
   return x;
 }
 
@@ -242,7 +243,7 @@ __global__ void __launch_bounds__(VER_THREADS, 4) verify_kernel(VerifyArgs a) {
   if (size > 1) cluster_here();
   pdl_wait();
   pdl_trigger();
-  const float uf = a.u[b * (n + 1) + n];
+  const float uf = __ldcg(a.u + b * (n + 1) + n);
 
   // ---- the longest accepted prefix ----
   int acc = n;
@@ -251,11 +252,11 @@ __global__ void __launch_bounds__(VER_THREADS, 4) verify_kernel(VerifyArgs a) {
     const int i = i0 + lane;
     bool stop = i < n, bad = false;
     if (i < n) {
-      const int x = a.draft[b * n + i];
+      const int x = __ldcg(a.draft + b * n + i);
       if (x >= 0 && x < a.V) {
-        const float ui = a.u[b * (n + 1) + i];
-        const double pv = a.p[(b * (n + 1) + i) * a.V + x];
-        const double qv = a.q ? a.q[(b * n + i) * a.V + x] : 1.f;
+        const float ui = __ldcg(a.u + b * (n + 1) + i);
+        const double pv = __ldcg(a.p + (b * (n + 1) + i) * a.V + x);
+        const double qv = a.q ? __ldcg(a.q + (b * n + i) * a.V + x) : 1.f;
         bad = !((double)ui * qv < pv);   // 48-bit product: exact
         stop = bad;
       }
@@ -270,13 +271,13 @@ __global__ void __launch_bounds__(VER_THREADS, 4) verify_kernel(VerifyArgs a) {
   }
   if (rank == 0) {
     for (int i = threadIdx.x; i <= n; i += VER_THREADS)
-      if (i != acc) a.tokens[b * (n + 1) + i] = i < acc ? a.draft[b * n + i] : -1;
+      if (i != acc) a.tokens[b * (n + 1) + i] = i < acc ? __ldcg(a.draft + b * n + i) : -1;
     if (threadIdx.x == 0) a.n_accepted[b] = acc;
   }
 
   const float* p = a.p + (b * (n + 1) + acc) * a.V;
   const float* q = a.q ? a.q + (b * n + acc) * a.V : nullptr;   // read after a rejection only
-  const int64_t x = refused ? a.draft[b * n + acc] : -1;
+  const int64_t x = refused ? __ldcg(a.draft + b * n + acc) : -1;
   const Row r(p, a.V);
   const bool q_vec = q && ((reinterpret_cast<uintptr_t>(q) >> 2) & 3) == (unsigned)r.mis;
   int lo, hi;

@@ -308,6 +308,30 @@ def test_later_keys_do_not_reach_earlier_rows(sub, n, bad):
 
 
 @pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("n", [1, 4, 40])
+def test_operators_right_after_each_other(sub, bits, n):
+    """Each call sees all that the one just before it wrote, with no pause between:
+    rows, then attention; logits' probabilities, then verification."""
+    c = Case(sub, [(100, n), (37, n), (1500, n)], 8, 2, 128, bits=bits, seed=10)
+    q, g = c.q.to(DEV), torch.Generator(device=DEV).manual_seed(1)
+    append = sub.kv_append if bits == 16 else sub.kv8_append
+    rows = [torch.randn(3 * n, 2, 128, device=DEV, generator=g).to(BF) for _ in range(8)]
+    z = torch.randn(3, 3, 5000, device=DEV, generator=g)
+    draft = torch.randint(0, 5000, (3, 2), device=DEV, generator=g, dtype=torch.int32)
+    u = torch.rand(3, 3, device=DEV, generator=g)
+    p = torch.empty_like(z)
+    o = torch.empty_like(q)
+    for i in range(24):
+        append(rows[i % 8], rows[(3 * i + 1) % 8], c.kv, c.layer, c.batch)
+        sub.chunk_attn(q, c.kv, c.layer, c.batch, out=o)
+        sub.probs(z[i % 3], 0.3 + 0.1 * i, out=p[i % 3])
+        tokens, _ = sub.verify_sample(p[i % 3][None], None, draft[:1], u[:1])
+        torch.cuda.synchronize()
+        assert torch.equal(o, sub.chunk_attn(q, c.kv, c.layer, c.batch)), i
+        assert torch.equal(tokens, sub.verify_sample(p[i % 3][None], None, draft[:1], u[:1])[0])
+
+
+@pytest.mark.parametrize("bits", [16, 8])
 @pytest.mark.parametrize("n", [2, 12, 40])
 def test_positions_at_the_end_of_int32(sub, bits, n):
     """Rows beyond the capacity read all of it, however far beyond."""

@@ -72,12 +72,13 @@ struct Cfg {
   static constexpr int Q_BYTES = GROUP_ROWS * D * 2;     // of one group
   static constexpr int CONV = Q8 ? 8 : 0;                // converter warps
   static constexpr int MMA_WARP = 8 + (Q8 ? CONV : 1);
+  static constexpr int PLAN = Q8 ? 2 : 0;                // then warps that look the keys up
   static constexpr int THREADS = Q8 ? 640 : 384;         // whole groups of four warps
   // registers by group of four warps, out of 65536 / THREADS each at the launch
   // (bf16: the producer and the MMA warp share one)
   static constexpr int REGS_SOFTMAX = Q8 ? 160 : 192;
-  static constexpr int REGS_PROD = Q8 ? 64 : 120;
-  static constexpr int REGS_MMA = Q8 ? 32 : 120;
+  static constexpr int REGS_PROD = Q8 ? 56 : 120;
+  static constexpr int REGS_MMA = Q8 ? 48 : 120;
   static_assert((2 * REGS_SOFTMAX + (Q8 ? CONV / 4 : 1) * REGS_PROD + (Q8 ? REGS_MMA : 0)) * 128 <=
                     65536 / THREADS / 8 * 8 * THREADS,
                 "the shares fit what the block is launched with");
@@ -238,7 +239,7 @@ struct Gate {
 };
 
 // Bit of a block's 16-key part in its word of missing pages: the TMA warp writes
-// the word, each converter warp that looks keys up a byte.
+// the word, the warps that look keys up a byte per 32 keys.
 template <bool Q8>
 __device__ constexpr int miss_bit(int part) {
   return Q8 ? 8 * (part >> 1) + (part & 1) : part;
@@ -250,6 +251,12 @@ __device__ __forceinline__ void more_registers() {
 template <int N>
 __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Converters and the warps that look keys up, once per block.
+template <int WARPS>
+__device__ __forceinline__ void meet_planners() {
+  asm volatile("bar.sync 3, %0;" ::"n"(WARPS * 32) : "memory");
 }
 
 struct Maps {
@@ -341,6 +348,25 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
   __syncthreads();
   const Gate gate{s_dead};
   const int G = a.group;
+  // Slot j of the ring holds V of block j - 1 and K of block j, across the units;
+  // the first has no V, the last no K.
+  const uint32_t n = (uint32_t)(line_hi > line_lo ? line_hi - line_lo : 0);
+  int kb = (int)(line_lo - u.begin);   // the next block to look up, of unit u
+  // pool row of key x of that block; -1: past the last key, -2: on no page
+  auto row_of = [&](int x) {
+    const int key = kb * KB + x;
+    if (key >= u.n_keys) return -1;
+    const int entry = a.by_page.quot(key), page = a.t.pages[(int64_t)u.b * a.t.width + entry];
+    if ((unsigned)page >= (unsigned)a.t.n_pages) return -2;
+    return (int)pool_row(a.t, a.layer, a.n_heads_kv, page, u.head, key - entry * a.t.page_size);
+  };
+  auto step = [&] {
+    if (++kb == u.n_blocks) {
+      plan.next(u);
+      kb = 0;
+    }
+  };
+
   if (warp < 8) more_registers<C::REGS_SOFTMAX>();
   else if (!Q8 || warp < 8 + C::CONV) fewer_registers<C::REGS_PROD>();
   else fewer_registers<C::REGS_MMA>();
@@ -695,28 +721,75 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
           if (ok && i + 1 < n) commit(kv_empty(block + 1));
         }
       }
+    } else if (Q8 && warp <= C::MMA_WARP + C::PLAN) {
+      // ------------------------------------- pool rows and scales of the keys
+      // Two blocks, and one block, ahead of the conversion.  (By the converters
+      // themselves, four of the eight took half as long again for a block as the others.)
+      constexpr int KEYS = KB / 64;   // per lane: keys x0, x0 + 32
+      static_assert(C::PLAN != 1 && KEYS == 2, "two warps, two keys per lane");
+      const int pw = warp - C::MMA_WARP - 1, x0 = pw * 64 + lane;
+      float ksc[KEYS], vsc[KEYS];
+      unsigned gone[KEYS];            // of 32 keys: which stand on no page
+      auto look_up = [&](uint32_t j) {   // called for j = 0, 1, ..
+        if (j >= n) return;
+        if (j > 0) step();
+        int row[KEYS];
+#pragma unroll
+        for (int h = 0; h < KEYS; ++h) row[h] = row_of(x0 + 32 * h);
+#pragma unroll
+        for (int h = 0; h < KEYS; ++h) s_rows[(j & 3) * KB + x0 + 32 * h] = row[h];
+      };
+      auto load_scales = [&](uint32_t j) {
+        if (j >= n) return;
+#pragma unroll
+        for (int h = 0; h < KEYS; ++h) {
+          const int row = s_rows[(j & 3) * KB + x0 + 32 * h];
+          gone[h] = __ballot_sync(~0u, row == -2);
+          ksc[h] = row >= 0 ? __ldcg(a.ks + row) : 0.f;
+          vsc[h] = row >= 0 ? __ldcg(a.vs + row) : 0.f;
+        }
+      };
+      auto store_scales = [&](uint32_t j) {
+        if (j >= n) return;
+        float* const sc = s_scale + (j & 7) * C::SCALE_SLOT;
+        float kx = 0.f, vx = 0.f;
+#pragma unroll
+        for (int h = 0; h < KEYS; ++h) {
+          // a row that reads a key whose scale of V is not finite gets NaN by its
+          // score; weight 0 times it stays 0
+          const bool fine = vsc[h] < INFINITY;
+          sc[x0 + 32 * h] = fine ? ksc[h] : __int_as_float(0x7fc00000);
+          sc[KB + x0 + 32 * h] = fine ? vsc[h] : 1.f;
+          kx = fmaxf(kx, ksc[h] < INFINITY ? ksc[h] : 0.f);
+          vx = fmaxf(vx, fine ? vsc[h] : 0.f);
+        }
+        kx = warp_max(kx);
+        vx = warp_max(vx);
+        if (lane == 0) {
+          sc[2 * KB + pw] = kx;
+          sc[2 * KB + 4 + pw] = vx;
+#pragma unroll
+          for (int h = 0; h < KEYS; ++h)   // 16-key parts: bits 0 and 16 of 32 keys
+            reinterpret_cast<volatile uint8_t*>(s_miss + (j & 7))[2 * pw + h] =
+                (uint8_t)((gone[h] & 1u) | ((gone[h] >> 16) & 1u) << 1);
+        }
+      };
+      look_up(0);
+      look_up(1);
+      meet_planners<C::CONV + C::PLAN>();
+      load_scales(0);
+      store_scales(0);
+      meet_planners<C::CONV + C::PLAN>();
+      for (uint32_t j = 0; j <= n && n > 0; ++j) {
+        load_scales(j + 1);
+        look_up(j + 2);
+        store_scales(j + 1);
+        meet_planners<C::CONV + C::PLAN>();
+      }
     }
   } else {
     // ------------------------------------------------------------ producers
-    // Slot j of the ring holds V of block j - 1 and K of block j, across the units;
-    // the first has no V, the last no K.
-    const uint32_t n = (uint32_t)(line_hi > line_lo ? line_hi - line_lo : 0);
     bool ok = true;
-    int kb = (int)(line_lo - u.begin);   // the next block to look up, of unit u
-    // pool row of key x of that block; -1: past the last key, -2: on no page
-    auto row_of = [&](int x) {
-      const int key = kb * KB + x;
-      if (key >= u.n_keys) return -1;
-      const int entry = a.by_page.quot(key), page = a.t.pages[(int64_t)u.b * a.t.width + entry];
-      if ((unsigned)page >= (unsigned)a.t.n_pages) return -2;
-      return (int)pool_row(a.t, a.layer, a.n_heads_kv, page, u.head, key - entry * a.t.page_size);
-    };
-    auto step = [&] {
-      if (++kb == u.n_blocks) {
-        plan.next(u);
-        kb = 0;
-      }
-    };
     if constexpr (!Q8) {
       // lanes 0..15 move K, 16..31 V: 64 columns (lane & 1) of the boxes (lane & 15) / 2, ..
       const int half = lane & 1, side = lane >> 4, b0 = (lane & 15) >> 1;
@@ -754,20 +827,11 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
       for (uint32_t i = j > SLOTS ? j - SLOTS : 0; i < j; ++i)
         mbar_wait_polls(kv_full(i), (i / SLOTS) & 1, 1u << 20);
     } else {
-      // Four lanes take 64 codes of a key, a warp's load eight keys; thread ptid looks
-      // up the pool row of key ptid.  Rows are looked up two blocks ahead of the
-      // conversion, scales loaded one block ahead, and codes as soon as their
+      // Four lanes take 64 codes of a key, a warp's load eight keys, as soon as their
       // registers are free, under the conversion of the other half.
       constexpr int HV = D / 64, KEYS = C::CONV * 8, N = KB / KEYS * HV;   // halves of a row, keys per pass, loads
       const int ptid = tid - 256, c = ptid & 3, k0 = ptid >> 2;
       uint4 wk[N], wv[N];
-      float ksc = 0.f, vsc = 0.f;   // of key ptid of the next block
-      unsigned gone = 0;            // the warp's 32 keys: which stand on no page
-      auto look_up = [&](uint32_t j) {   // called for j = 0, 1, ..
-        if (j >= n) return;
-        if (j > 0) step();
-        if (ptid < KB) s_rows[(j & 3) * KB + ptid] = row_of(ptid);
-      };
       auto load = [&](const void* pool, uint4 (&w)[N], uint32_t j) {
         const uint8_t* const p = reinterpret_cast<const uint8_t*>(pool) + c * 16;
 #pragma unroll
@@ -779,35 +843,11 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
                                 : make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
         }
       };
-      auto load_scales = [&](uint32_t j) {
-        if (ptid >= KB) return;
-        const int row = s_rows[(j & 3) * KB + ptid];
-        gone = __ballot_sync(~0u, row == -2);
-        ksc = row >= 0 ? __ldcg(a.ks + row) : 0.f;
-        vsc = row >= 0 ? __ldcg(a.vs + row) : 0.f;
-      };
-      auto store_scales = [&](uint32_t j) {
-        if (ptid >= KB) return;
-        // a row that reads a key whose scale of V is not finite gets NaN by its
-        // score; weight 0 times it stays 0
-        const bool fine = vsc < INFINITY;
-        float* const sc = s_scale + (j & 7) * C::SCALE_SLOT;
-        sc[ptid] = fine ? ksc : __int_as_float(0x7fc00000);
-        sc[KB + ptid] = fine ? vsc : 1.f;
-        const float kx = warp_max(ksc < INFINITY ? ksc : 0.f), vx = warp_max(fine ? vsc : 0.f);
-        if (lane == 0) {
-          sc[2 * KB + warp - 8] = kx;
-          sc[2 * KB + 4 + warp - 8] = vx;
-          // 16-key parts: bits 0 and 16 of the warp's 32 keys
-          reinterpret_cast<volatile uint8_t*>(s_miss + (j & 7))[warp - 8] =
-              (uint8_t)((gone & 1u) | ((gone >> 16) & 1u) << 1);
-        }
-      };
       // exponent of a block's largest scale (V: at least -80, so that sums of weights
       // stay in range)
       auto exponent = [&](uint32_t j, int side) {
-        const float4 m = *reinterpret_cast<const float4*>(s_scale + (j & 7) * C::SCALE_SLOT + 2 * KB + 4 * side);
-        const float x = fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w));
+        const float2 m = *reinterpret_cast<const float2*>(s_scale + (j & 7) * C::SCALE_SLOT + 2 * KB + 4 * side);
+        const float x = fmaxf(m.x, m.y);
         return min(126, max(side ? -80 : -126, (int)(__float_as_uint(x) >> 23) - 127));
       };
       // 16 codes are chunks 2 c, 2 c + 1 of a half row's line; eight lanes' stores are
@@ -836,22 +876,13 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
                       value(v[2 * y + 1], 0x4342u));
         }
       };
-      auto meet = [] { asm volatile("bar.sync 3, %0;" ::"n"(C::CONV * 32) : "memory"); };
-      look_up(0);
-      look_up(1);
-      meet();
-      if (n > 0) {
-        load(a.k, wk, 0);
-        load_scales(0);
-        store_scales(0);
-      }
-      meet();
+      meet_planners<C::CONV + C::PLAN>();
+      if (n > 0) load(a.k, wk, 0);
+      meet_planners<C::CONV + C::PLAN>();
       int ev = 0;   // exponent of the block's scales of V
       // no thread leaves this loop early (they meet in it): after a wait ran out
       // they only go on writing to their own shared memory
       for (uint32_t j = 0; j <= n && n > 0; ++j) {
-        look_up(j + 2);
-        if (j + 1 < n) load_scales(j + 1);
         if (j >= SLOTS) gate.wait(kv_empty(j), ((j / SLOTS) - 1) & 1);
         const uint32_t slot = ring_s + j % SLOTS * C::SLOT;
         const int ev_before = ev;
@@ -869,8 +900,7 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
         __syncwarp();
         if (lane == 0) mbar_arrive(kv_full(j));
         if (j < n) load(a.v, wv, j);
-        if (j + 1 < n) store_scales(j + 1);
-        meet();          // the rows of block j + 2 and the scales of block j + 1 are there
+        meet_planners<C::CONV + C::PLAN>();   // the rows of block j + 2 and the scales of block j + 1 are there
       }
     }
   }

@@ -197,7 +197,10 @@ chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__
   ChunkUnit u = plan.find(s_pre, line_lo);
 
   // ---- the loads: the warp's blocks of all its units, one after the other ----
-  // unit f, of which the warp reads blocks f0 + warp + i * WARPS, i < fn
+  // unit f, of which the warp reads blocks f0 + mine + i * WARPS, i < fn.  The last warps
+  // come first: the first ones join the results, and a remainder of the blocks
+  // goes to those that do not.
+  const int mine = WARPS - 1 - warp;
   ChunkUnit f = u;
   int f0, fn, fi;
   const int32_t* pages;
@@ -205,7 +208,7 @@ chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__
   // (page, head) of the warp's next 32 16-key steps (-1: no page), one looked up by
   // each lane, and of the 32 after them: a step's place is a shuffle away.
   auto look_up = [&](int step) {
-    const int key = (f0 + warp + step / SUBS * WARPS) * KB + step % SUBS * 16;
+    const int key = (f0 + mine + step / SUBS * WARPS) * KB + step % SUBS * 16;
     if (key >= f.n_keys || step >= fn * SUBS) return -1;
     const int page = pages[a.by_page.quot(key)];
     if ((unsigned)page >= (unsigned)a.t.n_pages) return -1;
@@ -215,7 +218,7 @@ chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__
     for (;;) {
       f0 = (int)(at - f.begin);
       const int f1 = (int)min((int64_t)f.n_blocks, line_hi - f.begin);
-      fn = (f1 - f0 - warp + WARPS - 1) / WARPS;
+      fn = (f1 - f0 - mine + WARPS - 1) / WARPS;
       fi = 0;
       at = f.begin + f1;
       if (fn > 0 || at >= line_hi) break;
@@ -248,7 +251,7 @@ chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__
         mbar_expect_tx(bar, (SUBS - __popc(gone)) * (32 * R::ROW + (Q8 ? 128 : 0)));
       __syncwarp();
       if (place >= 0 && my_op < R::OPS) {
-        const int key = (f0 + warp + fi * WARPS) * KB + my_step * 16;
+        const int key = (f0 + mine + fi * WARPS) * KB + my_step * 16;
         const int at = key - a.by_page.quot(key) * ps;
         if (my_op < 2 * R::H) {
           const int side = my_op / R::H, h = my_op % R::H;
@@ -278,7 +281,7 @@ chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__
   for (int64_t at = line_lo; at < line_hi; plan.next(u)) {
     const int kb0 = (int)(at - u.begin);
     const int kb1 = (int)min((int64_t)u.n_blocks, line_hi - u.begin);
-    const int n_mine = (kb1 - kb0 - warp + WARPS - 1) / WARPS;   // blocks kb0 + warp + i * WARPS
+    const int n_mine = (kb1 - kb0 - mine + WARPS - 1) / WARPS;   // blocks kb0 + mine + i * WARPS
 
     // Element i of accumulator t: which of the lane's two rows, which of its two keys
     auto row_of = [](int i) { return TURNED ? i & 1 : i >> 1; };
@@ -383,7 +386,7 @@ chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__
           if (lane == 0) atomicAdd(&g_decode_timeouts, 1u);
         }
       }
-      const int key0 = (kb0 + warp + i * WARPS) * KB;
+      const int key0 = (kb0 + mine + i * WARPS) * KB;
       const uint8_t* const st = ring + stage * R::STAGE;
       const uint32_t miss = (missing >> (SUBS * stage)) & ((1u << SUBS) - 1u);
       const bool edge = key0 + KB - 1 > lim_min || miss;
@@ -674,8 +677,8 @@ chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__
     }
 
     // ---- the warps' results, joined pairwise: 4 .. 7 into 0 .. 3, 2, 3 into 0, 1, 1 into 0 ----
-    // A result travels through the stage that its warp has read last, fragments as
-    // they are; the loads of the next unit stay on their way meanwhile.
+    // A result travels through the stage that its warp has read last (or not yet filled),
+    // fragments as they are; the loads of the next unit stay on their way meanwhile.
     auto slot_of = [&](int w, int st) {
       return reinterpret_cast<float4*>(smem + w * R::BYTES + st * R::STAGE);
     };
@@ -685,7 +688,7 @@ chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__
       const int there = warp & (r - 1);                    // the pair (there, there + r)
       const int full = r + there, free = WARPS - 1 + full;   // its barriers, 1 .. 14
       if (warp >= r) {
-        if (n_mine > 0) {
+        if (kb1 - kb0 > 2 * r - 1 - warp) {   // there is one, its own or joined
           float4* const out = slot_of(warp, stage == 0 ? STAGES - 1 : stage - 1) + lane;
 #pragma unroll
           for (int n = 0; n < ON; ++n) out[n * 32] = make_float4(o[n][0], o[n][1], o[n][2], o[n][3]);
@@ -698,7 +701,7 @@ chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__
       }
       bar_sync(full);
       const int w = warp + r;
-      if (kb1 - kb0 > w) {   // it had blocks
+      if (kb1 - kb0 > 2 * r - 1 - w) {   // it has one
         const float4 ml = s_ml[w][lane];
         const float4* const in = slot_of(w, s_at[w]) + lane;
         const float m[2] = {ml.x, ml.y};

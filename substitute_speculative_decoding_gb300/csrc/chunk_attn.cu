@@ -14,7 +14,7 @@
 // loop with 16-byte cp.async copies, sixteen per lane and block, ran at 5.1 TB/s
 // on 32 sequences of up to 16384 keys and left a quarter of the SMs a fifth slower
 // than the rest; the copies alone now take 203 us, 6.7 TB/s, and the kernel
-// 218.)  No barrier in the loop, no ldmatrix: a dot product may take its terms
+// 217.)  No barrier in the loop, no ldmatrix: a dot product may take its terms
 // in any order, if Q is laid out the same way, so lane (g, tig) reads, of key g of an
 // 8-key group, the 16-byte chunks 2 tig, 2 tig + 1 of each 128 bytes, and of V, for
 // its four keys of a 16-key step, the chunk that makes its B fragments for the n tiles of
@@ -25,12 +25,13 @@
 // rows.  The turned weights are already the next product's operand but for an
 // 8x8 transposition.
 //
-// Measured: 32 rows of 32 sequences of up to 16384 keys 218 us (1.37 GB, 6.3 TB/s);
-// codes, 2 sequences of 65536 47 us (4.5 TB/s); 128 of up to 2000 keys 126 us (5.2
-// TB/s), codes 95 (3.6); 1 sequence of 64 keys 10 us, a launch, its dependent
-// reads and the join.  Over codes the conversions and, on short caches, the
-// change of units show: the same loads without the products take 43 and 75 us.  (Twelve
-// warps with two stages each: 46 and 90 us, but 13 us on the short call.)
+// Measured, 40 or 32 query heads of 8 KV heads of 128: 32 sequences of up to 16384 keys
+// 217 us (1.37 GB, 6.3 TB/s); codes, 2 of up to 65001 47 us (4.5 TB/s); 128 of up to
+// 2000 keys 123 us (5.4 TB/s), codes 90 (3.8); 1 sequence of 512 keys of 2 heads of 64
+// 10 us, two launches and their dependent reads.  Over codes the conversions and, on
+// short caches, the change of units show: the same loads without the products take 43
+// and 75 us.  (Twelve warps with two stages each gained 4% there and cost the
+// short call 2.6 us; Q read a unit ahead gained nothing.)
 //
 // 8-bit codes c stand for (c - 128) * scale, and both products take c - 128 in
 // fp16, exactly: the bytes 0x64, c are 1024 + c, a byte permute and a subtraction
@@ -899,7 +900,8 @@ int32_t launch_decode(const ChunkArgs& a, int n_ctas, cudaStream_t st) {
 // 4096 keys (32 rows of 1 sequence over 1000 keys 15 us here, 19 by the tensor cores; of
 // 8 over 4000 37 and 36; of 1 over 16000 33 and 29; 64 rows of 8 over 4000 54 and
 // 37).  Codes, which the tensor-core kernel has to convert first: 64 rows (32 rows
-// of 8 sequences over 4000 keys 34 and 51, 64 rows 49 and 53, 112 rows 43 and 38).
+// of 8 sequences over 4000 keys 34 and 46, 56 rows of 4 KV heads 29 and 33, 64 rows 48
+// and 47; 48 rows of 2 over 64000 109 and 122).
 int tile_rows(int group, int n_seqs, int n_rows, bool codes, int64_t keys) {
   const int64_t rows = (int64_t)n_rows * group, seqs = n_seqs;
   const int tiles = codes ? 4 : keys <= 4096 ? 2 : 1;

@@ -6,9 +6,9 @@
 // block costs four products of 128 x 128 x D and 2 * 128 * 128 exponentials.
 // Measured: 2048 rows of 32 heads behind 14336 keys 341 us, 1512 TFLOP/s, 0.78 of a
 // plain bf16 matrix product of the library; over codes three prompts of 1537 rows of 28
-// heads behind up to 2600 keys 213 us, 593 TFLOP/s, where the converter warps' share of the
-// issue slots bounds it (1024 rows behind 7000 keys: 197 us, 122 with the
-// conversions left out).
+// heads behind up to 2600 keys 184 us, 686 TFLOP/s, bounded by the converter warps: a
+// block takes 4000 cycles, 3200 of them in its conversion, against 2700 over bf16
+// (1024 rows behind 7000 keys: 157 us against 115).
 // So two groups of 128 rows alternate: while the tensor cores form one group's
 // scores or output, the four warps of the other turn scores into weights.
 //   warps 0-3, 4-7   softmax of rows 0-127 and 128-255, one row per thread (a
@@ -18,6 +18,7 @@
 //                    (they are used together): a TMA warp for a bf16 cache (boxes of as many keys
 //                    as a page holds together), or eight warps that turn 8-bit
 //                    codes into fp16 values on the way
+//   two warps        (codes) that look the blocks' keys up and gather their scales ahead
 //   one MMA warp     S = Q K^T into tensor memory; then, once the group's weights
 //                    are there, O += P V with P read from tensor memory (in
 //                    place of S, as bf16 or fp16 pairs) and S of the next block

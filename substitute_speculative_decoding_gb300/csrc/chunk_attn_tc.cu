@@ -6,7 +6,7 @@
 // block costs four products of 128 x 128 x D and 2 * 128 * 128 exponentials.
 // Measured: 2048 rows of 32 heads behind 14336 keys 341 us, 1512 TFLOP/s, 0.78 of a
 // plain bf16 matrix product of the library; over codes three prompts of 1537 rows of 28
-// heads behind up to 2600 keys 184 us, 686 TFLOP/s, bounded by the converter warps: a
+// heads behind up to 2600 keys 196 us, 645 TFLOP/s, bounded by the converter warps: a
 // block takes 4000 cycles, 3200 of them in its conversion, against 2700 over bf16
 // (1024 rows behind 7000 keys: 157 us against 115).
 // So two groups of 128 rows alternate: while the tensor cores form one group's
@@ -36,7 +36,14 @@
 // column by column, would be exact, but cost every row 2 * 128 reads of shared
 // memory per block: the softmax then took 2.7 times as long.)  K's scale enters in two
 // fp16 parts, so that its rounding is not common to all terms of a score; V's in one,
-// like a rounding of the weight.
+// like a rounding of the weight.  Values are up to 2^15, near the end of fp16: a scale
+// may be 2^-21 of the block's largest before it loses a bit.
+//
+// That power of two is a choice for all rows, so it may come from keys that all
+// rows read, only.  In a block that not all rows read to its end the operands are the bare
+// codes, and each row applies the scales of its own keys, column by column, with the
+// largest of those for its power of two: one or two blocks of a tile, which take about
+// 6000 cycles more (the prompts 196 us; 179 with one power of two there, too).
 //
 // V rows past the tile's last key hold anything, and so may keys of the chunk
 // that only later rows read.  In blocks that not all rows read to the end the first
@@ -62,6 +69,10 @@ constexpr int GROUP_ROWS = 128;
 // the reference and 2^15 at most, so that fp16's smallest step is 2^-35 of the former
 constexpr float growth(bool q8) { return q8 ? 4.f : 8.f; }
 constexpr float Q8_SHIFT = 11.f;
+// log2 of what the values formed from codes are relative to the scales' power of two, and
+// the least exponents of that of K and of V (V: sums of weights times 2^-(VALUE_MIN -
+// VALUE_UP) stay in range)
+constexpr int VALUE_UP = 7, KEY_MIN = VALUE_UP - 126, VALUE_MIN = VALUE_UP - 80;
 
 __device__ unsigned int g_chunk_timeouts;   // waits that ran out (never expected)
 
@@ -83,8 +94,9 @@ struct Cfg {
   static_assert((2 * REGS_SOFTMAX + (Q8 ? CONV / 4 : 1) * REGS_PROD + (Q8 ? REGS_MMA : 0)) * 128 <=
                     65536 / THREADS / 8 * 8 * THREADS,
                 "the shares fit what the block is launched with");
-  // eight blocks' scales of K, of V, the largest of each by warp, and for the softmax
-  // the power of two of K's and the exponent of V's
+  // eight blocks' scales of K, of V; the largest of K's by warp, whether operands are the
+  // bare codes by warp, the largest of V's by warp; for the softmax the power of two of
+  // K's and the exponent of V's
   static constexpr int SCALE_SLOT = 2 * KB + 12;
   static constexpr int SCALES = Q8 ? 8 * SCALE_SLOT * 4 : 0;
   static constexpr int QSCALES = Q8 ? RT * 4 : 0;
@@ -459,41 +471,18 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
         if (!gate.wait_warp(s_full(t), n_s & 1)) break;
         ++n_s;
         tc_fence_after();
-        float s[KB];
-#pragma unroll
-        for (int x = 0; x < KB; x += 32) tc_ld32(tS + x, s + x);
         const uint32_t miss = s_miss[block & 7];
         const bool behind = key0 + KB - 1 > lim_first;   // the same for all rows of the tile
-        const bool edge = behind || miss;
-        // codes: the block's powers of two (not 0: it meets the masked scores' -infinity)
-        float f = factor, lv = 0.f;
-        if constexpr (Q8) {
-          const float2 pw = *reinterpret_cast<const float2*>(s_scale + (block & 7) * C::SCALE_SLOT + 2 * KB + 8);
-          f = fmaxf(factor * pw.x, 1e-37f);
-          lv = pw.y;
-        }
-        wait_ld();
-        if (edge) {
-          const int last = lim - key0;   // columns past it are not read
+        const int last = lim - key0;                     // columns past it are not read
+        const float* const sc = s_scale + (block & 7) * C::SCALE_SLOT;
+        float lv = 0.f;   // log2 of what V's scales add to the weights
+        float2 sum[4];
 #pragma unroll
-          for (int x = 0; x < KB; ++x)
-            if (x > last || ((miss >> miss_bit<Q8>(x >> 4)) & 1u)) s[x] = -INFINITY;
-        }
-        // eight chains: a single one would wait for itself 128 times
-        float top8[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) top8[i] = fmaxf(s[i], s[i + 8]);
-#pragma unroll
-        for (int x = 16; x < KB; x += 16)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) top8[i] = fmaxf(fmaxf(top8[i], s[x + i]), s[x + 8 + i]);
-        float top = fmaxf(fmaxf(fmaxf(top8[0], top8[1]), fmaxf(top8[2], top8[3])),
-                          fmaxf(fmaxf(top8[4], top8[5]), fmaxf(top8[6], top8[7])));
-        // what is rounded to fp16 is the weight times the power of two of V's scales
-        top = top == -INFINITY ? top : fmaf(top, f, lv);
-        // ---- the reference, and the output that was formed with another ----
-        const bool grow = top > ref + growth(Q8) || (!any && top != -INFINITY);
-        if (__any_sync(~0u, grow)) {
+        for (int i = 0; i < 4; ++i) sum[i] = make_float2(0.f, 0.f);
+        // the reference, and the output that was formed with another
+        auto raise = [&](float top) {
+          const bool grow = top > ref + growth(Q8) || (!any && top != -INFINITY);
+          if (!__any_sync(~0u, grow)) return;
           const float less = grow && any ? exp2_fast(ref - top) : 1.f;
           if (grow) {
             ref = top;
@@ -512,73 +501,163 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
               tc_st16(tO + x, reinterpret_cast<const uint32_t*>(o));
             }
           }
-        }
-        if (!Q8 && behind && t == 0) {
-          // V of the block: row r of it is this thread's
-          if (!gate.wait_warp(kv_full(block + 1), ((block + 1) / SLOTS) & 1)) break;
-          const uint32_t v0 = ring_s + (block + 1) % SLOTS * C::SLOT + r * 128;
-          const bool past = key0 + r >= n_keys;
-          uint32_t z = 0;   // 0 * x is NaN for what is not finite
+        };
+        if (Q8 && behind) {
+          // Bare codes: this row's scales, in two walks over the columns.  (As loops: the
+          // code of all 128 columns at once, which a tile runs once or twice, was fetched
+          // again each time: the prompts took 229 us, against 196.)
+          const float f = fmaxf(factor * (1.f / (1 << VALUE_UP)), 1e-37f);
+          float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, vmax4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-          for (int i = 0; i < D / 8; ++i) {
-            const uint32_t at16 = v0 + (i >> 3) * (KB * 128) + (((i ^ r) & 7) << 4);
-            if (past) {
-              st_shared(at16, 0, 0, 0, 0);
-            } else {
-              const uint4 v = lds128(at16);
-              const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+          for (int x0 = 0; x0 < KB; x0 += 32) {
+            float s[32];
+            __syncwarp();
+            tc_ld32(tS + x0, s);
+            wait_ld();
+            const uint32_t gone = miss >> miss_bit<Q8>(x0 >> 4);
+            const int end = last - x0;
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(z) : "r"(x[k]), "r"(0u));
+            for (int x = 0; x < 32; x += 4) {
+              const float4 k4 = *reinterpret_cast<const float4*>(sc + x0 + x);
+              const float4 v4 = *reinterpret_cast<const float4*>(sc + KB + x0 + x);
+              const float kk[4] = {k4.x, k4.y, k4.z, k4.w}, vv[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const bool unread = x + i > end;
+                s[x + i] = unread ? -INFINITY : s[x + i] * kk[i];
+                vmax4[i] = fmaxf(vmax4[i], unread ? 0.f : vv[i]);   // (0 where there is no page)
+              }
             }
+            if (gone & 3u) {
+#pragma unroll
+              for (int x = 0; x < 32; ++x)
+                if ((gone >> miss_bit<Q8>(x >> 4)) & 1u) s[x] = -INFINITY;
+            }
+#pragma unroll
+            for (int x = 0; x < 32; ++x) top4[x & 3] = fmaxf(top4[x & 3], s[x]);
+            tc_st16(tS + x0, reinterpret_cast<const uint32_t*>(s));
+            tc_st16(tS + x0 + 16, reinterpret_cast<const uint32_t*>(s + 16));
           }
-          if ((z & 0x7fff7fffu) != 0) {   // hardly ever: take them out, add them at the end
+          wait_st();
+          const float vmax = fmaxf(fmaxf(vmax4[0], vmax4[1]), fmaxf(vmax4[2], vmax4[3]));
+          const int e = max(VALUE_MIN, (int)(__float_as_uint(vmax) >> 23) - 127) + 1;   // vmax < 2^e
+          const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+          raise(top == -INFINITY ? top : fmaf(top, f, (float)(e - VALUE_UP)));
+          const float shift = Q8_SHIFT - (float)VALUE_UP - ref;
+          lv = (float)-VALUE_UP;
+#pragma unroll 1
+          for (int x0 = 0; x0 < KB; x0 += 32) {
+            float s[32];
+            __syncwarp();
+            tc_ld32(tS + x0, s);
+            wait_ld();
+            uint32_t pw[16];
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const float4 v = *reinterpret_cast<const float4*>(sc + KB + x0 + 2 * i);   // all finite
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const float2 w = make_float2(exp2_fast(fmaf(s[2 * (i + k)], f, shift)),
+                                             exp2_fast(fmaf(s[2 * (i + k) + 1], f, shift)));
+                sum[(i + k) & 3] = add2(sum[(i + k) & 3], w);
+                pw[i + k] = pack_f16x2(w.x * (k ? v.z : v.x), w.y * (k ? v.w : v.y));
+              }
+            }
+            tc_st16(tS + x0 / 2, pw);   // over columns that are read already
+          }
+        } else {
+          const bool edge = behind || miss;
+          float s[KB];
+#pragma unroll
+          for (int x = 0; x < KB; x += 32) tc_ld32(tS + x, s + x);
+          float f = factor;
+          if constexpr (Q8) {   // the block's powers of two (not 0: it meets the masked scores' -infinity)
+            const float2 pw = *reinterpret_cast<const float2*>(sc + 2 * KB + 8);
+            f = fmaxf(factor * pw.x, 1e-37f);
+            lv = pw.y;
+          }
+          wait_ld();
+          if (edge) {
+#pragma unroll
+            for (int x = 0; x < KB; ++x)
+              if (x > last || ((miss >> miss_bit<Q8>(x >> 4)) & 1u)) s[x] = -INFINITY;
+          }
+          // eight chains: a single one would wait for itself 128 times
+          float top8[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) top8[i] = fmaxf(s[i], s[i + 8]);
+#pragma unroll
+          for (int x = 16; x < KB; x += 16)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top8[i] = fmaxf(fmaxf(top8[i], s[x + i]), s[x + 8 + i]);
+          const float top = fmaxf(fmaxf(fmaxf(top8[0], top8[1]), fmaxf(top8[2], top8[3])),
+                                  fmaxf(fmaxf(top8[4], top8[5]), fmaxf(top8[6], top8[7])));
+          // what is rounded to fp16 is the weight times the power of two of V's scales
+          raise(top == -INFINITY ? top : fmaf(top, f, lv));
+          if (!Q8 && behind && t == 0) {
+            // V of the block: row r of it is this thread's
+            if (!gate.wait_warp(kv_full(block + 1), ((block + 1) / SLOTS) & 1)) break;
+            const uint32_t v0 = ring_s + (block + 1) % SLOTS * C::SLOT + r * 128;
+            const bool past = key0 + r >= n_keys;
+            uint32_t z = 0;   // 0 * x is NaN for what is not finite
 #pragma unroll 1
             for (int i = 0; i < D / 8; ++i) {
               const uint32_t at16 = v0 + (i >> 3) * (KB * 128) + (((i ^ r) & 7) << 4);
-              const uint4 v = lds128(at16);
-              uint32_t x[4] = {v.x, v.y, v.z, v.w};
+              if (past) {
+                st_shared(at16, 0, 0, 0, 0);
+              } else {
+                const uint4 v = lds128(at16);
+                const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                if ((x[k] & 0x7f80u) == 0x7f80u) x[k] &= 0xffff0000u;
-                if ((x[k] & 0x7f800000u) == 0x7f800000u) x[k] &= 0x0000ffffu;
+                for (int k = 0; k < 4; ++k)
+                  asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(z) : "r"(x[k]), "r"(0u));
               }
-              st_shared(at16, x[0], x[1], x[2], x[3]);
             }
-            s_odd[piece & 1] = piece + 1;
+            if ((z & 0x7fff7fffu) != 0) {   // hardly ever: take them out, add them at the end
+#pragma unroll 1
+              for (int i = 0; i < D / 8; ++i) {
+                const uint32_t at16 = v0 + (i >> 3) * (KB * 128) + (((i ^ r) & 7) << 4);
+                const uint4 v = lds128(at16);
+                uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  if ((x[k] & 0x7f80u) == 0x7f80u) x[k] &= 0xffff0000u;
+                  if ((x[k] & 0x7f800000u) == 0x7f800000u) x[k] &= 0x0000ffffu;
+                }
+                st_shared(at16, x[0], x[1], x[2], x[3]);
+              }
+              s_odd[piece & 1] = piece + 1;
+            }
+            fence_async();
+            __syncwarp();
           }
-          fence_async();
-          __syncwarp();
-        }
-        // ---- weights, in place of the scores' first columns ----
-        const float shift = Q8 ? Q8_SHIFT + lv - ref : -ref;
-        const float2 f2 = make_float2(f, f), d2 = make_float2(shift, shift);
-        float2 sum[4];
+          // ---- weights, in place of the scores' first columns ----
+          const float shift = Q8 ? Q8_SHIFT + lv - ref : -ref;
+          const float2 f2 = make_float2(f, f), d2 = make_float2(shift, shift);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum[i] = make_float2(0.f, 0.f);
+          for (int x0 = 0; x0 < KB; x0 += 32) {
+            uint32_t pw[16];
 #pragma unroll
-        for (int x0 = 0; x0 < KB; x0 += 32) {
-          uint32_t pw[16];
+            for (int i = 0; i < 16; i += 2) {
+              const int x = x0 + 2 * i;
+              float2 e[2];
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            const int x = x0 + 2 * i;
-            float2 e[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              e[k] = fma2(make_float2(s[x + 2 * k], s[x + 2 * k + 1]), f2, d2);
-              e[k].x = exp2_fast(e[k].x);
-              e[k].y = exp2_fast(e[k].y);
-              sum[(i + k) & 3] = add2(sum[(i + k) & 3], e[k]);
+              for (int k = 0; k < 2; ++k) {
+                e[k] = fma2(make_float2(s[x + 2 * k], s[x + 2 * k + 1]), f2, d2);
+                e[k].x = exp2_fast(e[k].x);
+                e[k].y = exp2_fast(e[k].y);
+                sum[(i + k) & 3] = add2(sum[(i + k) & 3], e[k]);
+              }
+              if constexpr (Q8) {
+                pw[i] = pack_f16x2(e[0].x, e[0].y);
+                pw[i + 1] = pack_f16x2(e[1].x, e[1].y);
+              } else {
+                pw[i] = pack_bf16x2(e[0].x, e[0].y);
+                pw[i + 1] = pack_bf16x2(e[1].x, e[1].y);
+              }
             }
-            if constexpr (Q8) {
-              pw[i] = pack_f16x2(e[0].x, e[0].y);
-              pw[i + 1] = pack_f16x2(e[1].x, e[1].y);
-            } else {
-              pw[i] = pack_bf16x2(e[0].x, e[0].y);
-              pw[i + 1] = pack_bf16x2(e[1].x, e[1].y);
-            }
+            tc_st16(tS + x0 / 2, pw);
           }
-          tc_st16(tS + x0 / 2, pw);
         }
         wait_st();
         tc_fence_before();
@@ -731,9 +810,12 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
       const int pw = warp - C::MMA_WARP - 1, x0 = pw * 64 + lane;
       float ksc[KEYS], vsc[KEYS];
       unsigned gone[KEYS];            // of 32 keys: which stand on no page
+      uint32_t bare = 0;              // bit j % 32: not all rows read block j to its end
       auto look_up = [&](uint32_t j) {   // called for j = 0, 1, ..
         if (j >= n) return;
         if (j > 0) step();
+        const bool behind = kb * KB + KB - 1 > last_key(u.pos, a.by_group.quot(u.tile * RT), u.n_keys);
+        bare = (bare & ~(1u << (j & 31))) | (uint32_t)behind << (j & 31);
         int row[KEYS];
 #pragma unroll
         for (int h = 0; h < KEYS; ++h) row[h] = row_of(x0 + 32 * h);
@@ -768,6 +850,7 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
         vx = warp_max(vx);
         if (lane == 0) {
           sc[2 * KB + pw] = kx;
+          sc[2 * KB + 2 + pw] = (float)((bare >> (j & 31)) & 1u);
           sc[2 * KB + 4 + pw] = vx;
 #pragma unroll
           for (int h = 0; h < KEYS; ++h)   // 16-key parts: bits 0 and 16 of 32 keys
@@ -844,22 +927,23 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
                                 : make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
         }
       };
-      // exponent of a block's largest scale (V: at least -80, so that sums of weights
-      // stay in range)
+      // exponent of a block's largest scale
       auto exponent = [&](uint32_t j, int side) {
         const float2 m = *reinterpret_cast<const float2*>(s_scale + (j & 7) * C::SCALE_SLOT + 2 * KB + 4 * side);
         const float x = fmaxf(m.x, m.y);
-        return min(126, max(side ? -80 : -126, (int)(__float_as_uint(x) >> 23) - 127));
+        return min(126, max(side ? VALUE_MIN : KEY_MIN, (int)(__float_as_uint(x) >> 23) - 127));
       };
       // 16 codes are chunks 2 c, 2 c + 1 of a half row's line; eight lanes' stores are
       // those of two neighbouring keys, whose swizzles differ by one chunk: all banks
       const uint32_t line = k0 * 128, x0 = (uint32_t)((2 * c) ^ (k0 & 7)) << 4;
       auto put = [&](const uint4 (&w)[N], uint32_t dst, uint32_t j, int side, int e) {
-        const float* const sc = s_scale + (j & 7) * C::SCALE_SLOT + side * KB + k0;
-        const float less = __uint_as_float((uint32_t)(127 - e) << 23);
+        const float* const sc = s_scale + (j & 7) * C::SCALE_SLOT;
+        const float less = __uint_as_float((uint32_t)(127 + VALUE_UP - e) << 23);
+        const bool bare = sc[2 * KB + 2] != 0.f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          const float r = sc[i / HV * KEYS] * less;   // the scale relative to the power of two
+          // the scale relative to the power of two; bare codes: a power of two
+          const float r = bare ? (float)(1 << VALUE_UP) : sc[side * KB + k0 + i / HV * KEYS] * less;
           const __half hi = __float2half_rn(r), lo = __float2half_rn(r - __half2float(hi));
           const __half2 hi2 = __half2half2(hi), lo2 = __half2half2(lo);
           auto value = [&](uint32_t word, uint32_t sel) {
@@ -892,7 +976,7 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
           ev = exponent(j, 1);
           if (ptid == 0)
             *reinterpret_cast<float2*>(s_scale + (j & 7) * C::SCALE_SLOT + 2 * KB + 8) =
-                make_float2(__uint_as_float((uint32_t)(127 + ek) << 23), (float)ev);
+                make_float2(__uint_as_float((uint32_t)(127 + ek - VALUE_UP) << 23), (float)(ev - VALUE_UP));
           put(wk, slot + C::HALF, j, 0, ek);
           if (j + 1 < n) load(a.k, wk, j + 1);
         }

@@ -1,0 +1,39 @@
+"""Serving batches where a result depends on what lies beside it: scales of keys
+that a row does not read, weights' second halves, probabilities below the
+normal numbers, tensors at any address, caches of one sequence, batches of unlike
+and of very many sequences."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import batch as ob
+from test_gpu_batch import BF, DEV, Case, np32
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def sub():
+    import substitute_speculative_decoding_gb300 as s
+    return s
+
+
+# ------------------------------------------------- scales of unread keys --
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [4, 20, 40, 300])
+@pytest.mark.parametrize("side", [0, 1])
+def test_scales_of_later_keys_leave_earlier_rows_as_they_are(sub, d, n, side):
+    """The largest finite scales in an 8-bit cache, of keys that only the last two rows
+    read: the rows before them keep their bits, whichever tiles the batch gets."""
+    c = Case(sub, [(45, n), (20, 2)], 8, 2, d, bits=8, seed=3)
+    q = c.q.to(DEV)
+    at = 45 + n - 2
+    pg, pl = int(c.table[0, at // 16]), at % 16
+    clean = sub.chunk_attn(q, c.kv, c.layer, c.batch)
+    c.check(clean)
+    one = c.scales[side][c.layer, pg, :, pl].clone()
+    for f in (2.0 ** 16, 2.0 ** 24, 2.0 ** 30, 2.0 ** 100):
+        c.scales[side][c.layer, pg, :, pl] = one * f
+        o = sub.chunk_attn(q, c.kv, c.layer, c.batch)
+        assert torch.equal(o[:n - 2], clean[:n - 2]) and torch.equal(o[n:], clean[n:]), f
+        assert not torch.equal(o[n - 2:n], clean[n - 2:n])

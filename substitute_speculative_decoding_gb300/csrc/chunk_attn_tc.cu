@@ -313,10 +313,13 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
   auto o_full = [&](int t) { return bars + 8u * (2 * SLOTS + 6 + t); };
   int* const flags = reinterpret_cast<int*>(tail + 8 * (2 * SLOTS + 8));
   volatile int* const s_dead = flags;            // a wait ran out
-  volatile int* const s_odd = flags + 1;         // [2] piece (by parity) that met infinite values or NaN
-  volatile uint32_t* const s_miss = reinterpret_cast<uint32_t*>(flags + 3);   // [8] blocks' missing 16-key parts
-  uint32_t* const s_tmem = reinterpret_cast<uint32_t*>(flags + 11);
-  static_assert(8 * (2 * SLOTS + 8) + 12 * 4 <= C::TAIL, "tail");
+  // [group][2] the piece that met infinite values or NaN, for each group by the parity of
+  // the pieces that it takes part in: the first group, which finds them, gets two such pieces
+  // ahead of the second only after the second is through with the older one
+  volatile int* const s_odd = flags + 1;
+  volatile uint32_t* const s_miss = reinterpret_cast<uint32_t*>(flags + 5);   // [8] blocks' missing 16-key parts
+  uint32_t* const s_tmem = reinterpret_cast<uint32_t*>(flags + 13);
+  static_assert(8 * (2 * SLOTS + 8) + 14 * 4 <= C::TAIL, "tail");
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (warp == 0) {
@@ -338,7 +341,7 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
       mbar_init(o_full(t), 1);
     }
     *s_dead = 0;
-    s_odd[0] = s_odd[1] = 0;
+    for (int i = 0; i < 4; ++i) s_odd[i] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (!Q8 && tid == 64) {
@@ -396,7 +399,8 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
 
     // Q of a unit's group, first into registers, then into shared memory: chunk c of
     // a row at c ^ (row % 8) of its 128-byte line, each warp its own threads' rows
-    auto has_rows = [&](const ChunkUnit& x) { return x.tile * RT + t * GROUP_ROWS < x.rows * G; };
+    auto group_has_rows = [&](const ChunkUnit& x, int g) { return x.tile * RT + g * GROUP_ROWS < x.rows * G; };
+    auto has_rows = [&](const ChunkUnit& x) { return group_has_rows(x, t); };
     auto q_load = [&](const ChunkUnit& x, uint4 (&w)[CH]) {
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
@@ -441,6 +445,7 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
     if (tid == 0 && line_lo >= line_hi) a.cuts[blockIdx.x].pieces = 0;
     bool q_there = false;   // this piece's Q is in shared memory already
     int piece = 0;
+    int both = 0;   // pieces so far that the second group took part in
     for (int64_t at = line_lo; at < line_hi; ++piece) {
       const int kb0 = (int)(at - u.begin), kb1 = (int)min((int64_t)u.n_blocks, line_hi - u.begin);
       const bool first = at == line_lo;
@@ -627,6 +632,7 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
                 st_shared(at16, x[0], x[1], x[2], x[3]);
               }
               s_odd[piece & 1] = piece + 1;
+              if (group_has_rows(u, 1)) s_odd[2 + (both & 1)] = piece + 1;
             }
             fence_async();
             __syncwarp();
@@ -684,7 +690,8 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
       ++n_o;
       tc_fence_after();
       const bool whole = kb0 == 0 && kb1 == done.n_blocks;
-      const bool odd = !Q8 && s_odd[piece & 1] == piece + 1;
+      const bool odd = !Q8 && s_odd[t ? 2 + (both & 1) : piece & 1] == piece + 1;
+      both += group_has_rows(done, 1);
       const float mul = whole ? (any ? 1.f / l : 0.f) : 1.f;
       uint16_t* const out = a.O + ((int64_t)(done.row0 + q) * a.n_heads_q + done.head * G + row - q * G) * D;
       const int64_t part_row = (2 * (int64_t)blockIdx.x + (first ? 0 : 1)) * RT + t * GROUP_ROWS + r;

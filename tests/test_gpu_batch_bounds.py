@@ -37,3 +37,25 @@ def test_scales_of_later_keys_leave_earlier_rows_as_they_are(sub, d, n, side):
         o = sub.chunk_attn(q, c.kv, c.layer, c.batch)
         assert torch.equal(o[:n - 2], clean[:n - 2]) and torch.equal(o[n:], clean[n:]), f
         assert not torch.equal(o[n - 2:n], clean[n - 2:n])
+
+
+# ------------------------------------------ infinities, tile after tile --
+def test_infinite_values_of_neighbouring_tiles_are_all_kept(sub):
+    """Tiles whose second half is empty between tiles where both halves read an infinite
+    value, several to a CTA: every row from the second on of each long sequence has it."""
+    rows = [50, 25, 50, 25, 25, 40] * 100          # times 4 heads: 200, 100, .. of 256 rows
+    seqs = [(3 + b % 5, n) for b, n in enumerate(rows)]
+    c = Case(sub, seqs, 8, 2, 64, page=64, seed=21)
+    q = c.q.to(DEV)
+    clean = sub.chunk_attn(q, c.kv, c.layer, c.batch)
+    assert torch.isfinite(clean).all()
+    want = torch.ones(clean.shape, dtype=torch.bool)
+    for b, (p, n) in enumerate(seqs):
+        if n > 30:
+            at = p + 1                             # the second row's own key
+            c.pools[1][c.layer, int(c.table[b, 0]), 1, at, 5] = float("inf")
+            want[int(c.start[b]) + 1:int(c.start[b]) + n, 4:, 5] = False
+    for _ in range(5):
+        o = sub.chunk_attn(q, c.kv, c.layer, c.batch)
+        assert torch.equal(torch.isfinite(o).cpu(), want)
+        assert torch.equal(o.cpu()[want], clean.cpu()[want])

@@ -791,7 +791,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) chunk_join_kernel(const __gri
   x.w[0] = __ldcg(reinterpret_cast<const int4*>(a.cuts + part));
   x.w[1] = __ldcg(reinterpret_cast<const int4*>(a.cuts + part) + 1);
   const ChunkCut c = x.cut;
-  if (c.pieces == 0) return;
+  if (!cut_stands(c, part, gridDim.x, a.t.n_rows, a.n_heads_kv, a.group, RT)) return;
   constexpr int LANES = D / 4, PER = 32 / LANES;   // lanes per piece, pieces per load
   constexpr int AHEAD = 8;                          // loads in flight
   const int lane = threadIdx.x & 31, n = c.pieces;

@@ -48,6 +48,15 @@ struct __align__(16) ChunkCut {
   int pad[2];
 };
 
+// Whether CTA part's entry names pieces, rows and a head that there are: what the join goes
+// by lies in memory that only kernels which ran to their end have written.
+__host__ __device__ inline bool cut_stands(const ChunkCut& c, int part, int n_ctas, int n_rows,
+                                           int n_heads_kv, int group, int tile_rows) {
+  return c.pieces >= 2 && c.pieces <= n_ctas - part && (c.first == 2 * part || c.first == 2 * part + 1) &&
+         c.row0 >= 0 && c.rows >= 1 && c.row0 <= n_rows && c.rows <= n_rows - c.row0 && c.head >= 0 &&
+         c.head < n_heads_kv && c.tile >= 0 && (int64_t)c.tile * tile_rows < (int64_t)c.rows * group;
+}
+
 // Quotients of line positions, nearly always of 32 bits.  (The compiler's 64-bit
 // division takes a few hundred cycles and instructions; this one's rare case is slow
 // but small.)

@@ -442,7 +442,8 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
       __syncwarp();   // (s_qs, too)
       if (lane == 0) mbar_arrive(q_full(t));
     };
-    if (tid == 0 && line_lo >= line_hi) a.cuts[blockIdx.x].pieces = 0;
+    // (also for a CTA that stops early because a wait ran out)
+    if (tid == 0) a.cuts[blockIdx.x].pieces = 0;
     bool q_there = false;   // this piece's Q is in shared memory already
     int piece = 0;
     int both = 0;   // pieces so far that the second group took part in

@@ -335,7 +335,7 @@ int32_t sub_kv8_read(const sub_kv8_cache* kv, int32_t layer, const sub_batch* ba
  * whatever they hold) does not change it.
  * Hq % Hkv == 0, Hq / Hkv <= 64; head_dim 64 or 128.  Which sequences share
  * the batch, and max_keys, move a row's result by rounding only; the same call
- * gives the same bits.  Rounding: the weights to bf16 or better (over codes, a weight
+ * gives the same bits.  Rounding: the weights to 2^-16 (over codes, a weight
  * times V's scale to fp16, and to 2^-36 of the row's largest weight times the largest
  * scale of V that it reads); of codes, when a sequence has more than 64 rows per KV head on average,
  * also the values, to fp16 relative to the largest scale among 128 neighbouring keys

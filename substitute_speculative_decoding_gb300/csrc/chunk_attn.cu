@@ -897,9 +897,9 @@ int32_t launch_decode(const ChunkArgs& a, int n_ctas, cudaStream_t st) {
 // known here, lengths only on the device) and the most keys that one may have.  The
 // warps' kernel reads the keys again for every tile, the tensor-core kernel once for 256
 // rows, but it starts later and wants blocks of 128 keys.  bf16: 16 rows, and 32 up to
-// 4096 keys (32 rows of 1 sequence over 1000 keys 15 us here, 19 by the tensor cores; of
-// 8 over 4000 37 and 36; of 1 over 16000 33 and 29; 64 rows of 8 over 4000 54 and
-// 37).  Codes, which the tensor-core kernel has to convert first: 64 rows (32 rows
+// 4096 keys (32 rows of 1 sequence over 1000 keys 12 us here, 16 by the tensor cores; of
+// 8 over 4000 43 and 41; of 1 over 16000 28 and 28; 20 rows of 8 over 16000 167 and
+// 109).  Codes, which the tensor-core kernel has to convert first: 64 rows (32 rows
 // of 8 sequences over 4000 keys 34 and 46, 56 rows of 4 KV heads 29 and 33, 64 rows 48
 // and 47; 48 rows of 2 over 64000 109 and 122).
 int tile_rows(int group, int n_seqs, int n_rows, bool codes, int64_t keys) {

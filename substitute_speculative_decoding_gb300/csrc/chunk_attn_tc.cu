@@ -2,10 +2,11 @@
 // prompt, on the 5th-generation tensor cores.
 //
 // The same sums as chunk_attn.cu, in tiles of 256 (row, head in group) pairs x
-// 128 keys.  Bound by the tensor cores and, close behind, by the exponentials: a
-// block costs four products of 128 x 128 x D and 2 * 128 * 128 exponentials.
-// Measured: 2048 rows of 32 heads behind 14336 keys 341 us, 1512 TFLOP/s, 0.78 of a
-// plain bf16 matrix product of the library; over codes three prompts of 1537 rows of 28
+// 128 keys.  Bound by the tensor cores: a block costs six products of 128 x 128 x D
+// (codes: four) and 2 * 128 * 128 exponentials.
+// Measured: 2048 rows of 32 heads behind 14336 keys 483 us, 1070 TFLOP/s (0.55 of a
+// plain bf16 matrix product of the library) that are counted, 1600 with the
+// weights' second halves; over codes three prompts of 1537 rows of 28
 // heads behind up to 2600 keys 196 us, 645 TFLOP/s, bounded by the converter warps: a
 // block takes 4000 cycles, 3200 of them in its conversion, against 2700 over bf16
 // (1024 rows behind 7000 keys: 157 us against 115).
@@ -21,13 +22,15 @@
 //   two warps        (codes) that look the blocks' keys up and gather their scales ahead
 //   one MMA warp     S = Q K^T into tensor memory; then, once the group's weights
 //                    are there, O += P V with P read from tensor memory (in
-//                    place of S, as bf16 or fp16 pairs) and S of the next block
+//                    place of S, as two bf16 halves or as fp16) and S of the next block
 // O stays in tensor memory.  It is rescaled only when a row's maximum has grown
 // by more than 2^8 (codes: 2^4) since the weights' reference was set: until then the
 // weights exceed 1 by at most that factor, which costs a floating-point value nothing.
-// P is rounded once, to bf16 (half a step 2^-8 relative, random over the keys; the
-// sum takes the unrounded weights) or fp16 for codes; a second product with
-// the rest would make the tensor cores half as slow again.
+// Over a bf16 cache P = hi + lo, two bf16 products, like in the few rows' kernel (2^-16 of
+// a weight): a token's row rounds alike, whether it is decoded, verified or part
+// of a prompt.  (One product, P rounded to bf16, took 362 us of the 2048 rows; its error
+// against 64 bits was a third more, as much as the result's own rounding.)  Over codes P
+// is rounded once, to fp16, three bits finer; the sums take the unrounded weights.
 //
 // Codes become fp16 values on the way, (code - 128) * scale relative to the power
 // of two of the block's largest scale, rounded to half a step of 2^-11 (three bits
@@ -643,7 +646,7 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
           const float2 f2 = make_float2(f, f), d2 = make_float2(shift, shift);
 #pragma unroll
           for (int x0 = 0; x0 < KB; x0 += 32) {
-            uint32_t pw[16];
+            uint32_t pw[16], rest[16];
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
               const int x = x0 + 2 * i;
@@ -655,15 +658,20 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
                 e[k].y = exp2_fast(e[k].y);
                 sum[(i + k) & 3] = add2(sum[(i + k) & 3], e[k]);
               }
-              if constexpr (Q8) {
-                pw[i] = pack_f16x2(e[0].x, e[0].y);
-                pw[i + 1] = pack_f16x2(e[1].x, e[1].y);
-              } else {
-                pw[i] = pack_bf16x2(e[0].x, e[0].y);
-                pw[i + 1] = pack_bf16x2(e[1].x, e[1].y);
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                if constexpr (Q8) {
+                  pw[i + k] = pack_f16x2(e[k].x, e[k].y);
+                } else {
+                  const uint32_t w = pack_bf16x2(e[k].x, e[k].y);
+                  pw[i + k] = w;
+                  const float2 r = add2(e[k], make_float2(-bf16lo(w), -bf16hi(w)));
+                  rest[i + k] = pack_bf16x2(r.x, r.y);
+                }
               }
             }
             tc_st16(tS + x0 / 2, pw);
+            if constexpr (!Q8) tc_st16(tS + KB / 2 + x0 / 2, rest);
           }
         }
         wait_st();
@@ -773,8 +781,11 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
         if (elect_one()) {
           const uint64_t vd = v_desc + (b + 1) % SLOTS * (C::SLOT >> 4);
 #pragma unroll
-          for (int k = 0; k < KB / 16; ++k)
+          for (int k = 0; k < KB / 16; ++k) {
             mma_ts(tm + 256 + t * 128, tm + t * 128 + k * 8, vd + k * (2048 >> 4), id_o, add || k > 0);
+            if constexpr (!Q8)   // the weights' second halves
+              mma_ts(tm + 256 + t * 128, tm + t * 128 + KB / 2 + k * 8, vd + k * (2048 >> 4), id_o, true);
+          }
         }
         __syncwarp();
       };

@@ -59,3 +59,32 @@ def test_infinite_values_of_neighbouring_tiles_are_all_kept(sub):
         o = sub.chunk_attn(q, c.kv, c.layer, c.batch)
         assert torch.equal(torch.isfinite(o).cpu(), want)
         assert torch.equal(o.cpu()[want], clean.cpu()[want])
+
+
+# --------------------------------------------------------- both halves --
+def _check_tight(c, o):
+    """As Case.check for a bf16 cache, with the weights in two bf16 halves: the second
+    half's rounding is half a step of half a step, 2^-16 of the weight.  The result's own
+    rounding counts as what it is, half the distance of bf16 numbers there."""
+    for b, (p, n) in enumerate(c.seqs):
+        r0 = int(c.start[b])
+        q, k, v = np32(c.q[r0:r0 + n]), c.values(0, b), c.values(1, b)
+        ref, w = ob.chunk_attention(q, k, v, p)
+        top = (np.abs(q) * np.repeat(np.abs(k).max(0), c.hq // c.hkv, 0)).sum(-1, keepdims=True)
+        e = 2.0 ** -16 + 2 * (c.d / 16 + 4) * 2.0 ** -22 * top * c.d ** -0.5 + \
+            (len(k) / 16 + 4) * 2.0 ** -22
+        mag = np.abs(ref) + e * w
+        half = 2.0 ** (np.floor(np.log2(np.maximum(mag, 1e-30))) - 8)
+        err = np.abs(np32(o[r0:r0 + n]).astype(np.float64) - ref)
+        assert np.all(err <= half + e * w), (b, float((err / (half + e * w)).max()))
+
+
+@pytest.mark.parametrize("kw", [dict(seqs=[(300, 1), (17, 2)], hq=8, hkv=2, d=128),
+                                dict(seqs=[(300, 4), (17, 3)], hq=8, hkv=2, d=64),
+                                dict(seqs=[(700, 9), (90, 12)], hq=28, hkv=4, d=128, page=48),
+                                dict(seqs=[(77, 300), (500, 1)], hq=8, hkv=2, d=128, page=64),
+                                dict(seqs=[(0, 130)], hq=8, hkv=8, d=64, page=32)])
+def test_weights_over_a_bf16_cache_keep_two_halves(sub, kw):
+    """In every tile: a token's row comes out alike whatever else the batch holds."""
+    c = Case(sub, seed=17, **kw)
+    _check_tight(c, sub.chunk_attn(c.q.to(DEV), c.kv, c.layer, c.batch))

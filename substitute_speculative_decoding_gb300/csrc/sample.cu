@@ -82,6 +82,11 @@ __device__ __forceinline__ float exp2_fast(float x) {   // 2 ulp; flushes below 
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+__device__ __forceinline__ float exp2_small(float x) {   // the same, down to 2^-149
+  float r;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 
 // A CTA's share of a row's groups.
 __device__ __forceinline__ void share(int groups, int rank, int size, int& lo, int& hi) {
@@ -120,11 +125,11 @@ __global__ void __launch_bounds__(THREADS, THREADS > 512 ? 1 : 1280 / THREADS) p
   // are positive, so that d = -infinity gives 0.)
   auto expo = [&](float d) { return exp2_fast(fmaf(d, c_hi, d * c_lo)); };
   const float2 hi2 = make_float2(c_hi, c_hi), lo2 = make_float2(c_lo, c_lo);
-  auto expo4 = [&](const float4& x, float minus) {   // of x + minus, two at a time
+  auto exponents = [&](const float4& x, float minus) {   // of x + minus, two at a time
     const float2 r2 = make_float2(minus, minus);
     const float2 a = add2(make_float2(x.x, x.y), r2), b = add2(make_float2(x.z, x.w), r2);
     const float2 ea = fma2(a, hi2, mul2(a, lo2)), eb = fma2(b, hi2, mul2(b, lo2));
-    return make_float4(exp2_fast(ea.x), exp2_fast(ea.y), exp2_fast(eb.x), exp2_fast(eb.y));
+    return make_float4(ea.x, ea.y, eb.x, eb.y);
   };
   auto merge = [&](float& m, float& s, float m2, float s2) {   // sums relative to their maxima
     const float big = fmaxf(m, m2);
@@ -149,8 +154,8 @@ __global__ void __launch_bounds__(THREADS, THREADS > 512 ? 1 : 1280 / THREADS) p
     m = big;
 #pragma unroll
     for (int k = 0; k < MLP; ++k) {
-      const float4 e = expo4(x[k], -ref);
-      s += (e.x + e.y) + (e.z + e.w);
+      const float4 e = exponents(x[k], -ref);   // (the sum is at least 1: no term below 2^-126 counts)
+      s += (exp2_fast(e.x) + exp2_fast(e.y)) + (exp2_fast(e.z) + exp2_fast(e.w));
     }
   }
 #pragma unroll
@@ -181,8 +186,9 @@ __global__ void __launch_bounds__(THREADS, THREADS > 512 ? 1 : 1280 / THREADS) p
     for (int k = 0; k < MLP; ++k) {
       const int g = g0 + k * THREADS;
       if (g >= hi) break;
-      const float4 e = expo4(x[k], -ref);
-      const float w[4] = {e.x * f, e.y * f, e.z * f, e.w * f};
+      const float4 e = exponents(x[k], -ref);
+      const float w[4] = {exp2_small(e.x) * f, exp2_small(e.y) * f, exp2_small(e.z) * f,
+                          exp2_small(e.w) * f};
       if (r.whole(g)) {
         __stcs(reinterpret_cast<float4*>(out - r.mis) + g, make_float4(w[0], w[1], w[2], w[3]));
       } else {

@@ -88,3 +88,21 @@ def test_weights_over_a_bf16_cache_keep_two_halves(sub, kw):
     """In every tile: a token's row comes out alike whatever else the batch holds."""
     c = Case(sub, seed=17, **kw)
     _check_tight(c, sub.chunk_attn(c.q.to(DEV), c.kv, c.layer, c.batch))
+
+
+# -------------------------------------------------------- probabilities --
+@pytest.mark.parametrize("v", [9, 5000, 152064])
+@pytest.mark.parametrize("t", [0.5, 1.0])
+def test_probabilities_below_the_normal_numbers(sub, v, t):
+    """They are kept down to fp32's smallest step: two roundings to it (the
+    exponential, the product with 1 / sum), each off by a step at most."""
+    g = torch.Generator().manual_seed(v)
+    z = -(85 + 25 * torch.rand(2, v, generator=g)) * t
+    z[:, 0] = 0
+    z[1, v - 1] = 0
+    p = sub.probs(z.to(DEV), t).cpu().numpy().astype(np.float64)
+    ref = ob.probs(z.numpy(), t)
+    tiny = (ref > 2.0 ** -148) & (ref < 2.0 ** -126)
+    assert tiny.sum() >= 2 and np.all(p[ref > 2.0 ** -146] > 0)
+    rel = 2.0 ** -24 * (2.5 * 110 + 2.5 * 110 + 400 + 12)
+    assert np.all(np.abs(p - ref) <= rel * ref + 2.0 ** -148)

@@ -356,9 +356,10 @@ int32_t sub_chunk_attn_workspace(int32_t n_heads_q, int32_t n_heads_kv, int32_t 
                                  int32_t n_seqs, int32_t n_rows, int64_t* bytes);
 
 /* probs[r, v] = exp(z[r, v] / T) / sum_w exp(z[r, w] / T) for fp32 logits z
- * [rows, V], sums in fp32; probs [rows, V] may be the logits themselves.
- * -infinity entries get 0, a row of nothing else gets zeros.  1 <= V <= 2^20,
- * temperature in [1e-6, 1e6]; logits and probs 16-byte aligned. */
+ * [rows, V], sums in fp32; probs [rows, V] is the logits themselves or lies apart
+ * from them.  -infinity entries get 0, a row of nothing else gets zeros.
+ * 1 <= V <= 2^20, temperature in [1e-6, 1e6]; any addresses (fastest where logits and
+ * probs are alike modulo 16 bytes). */
 int32_t sub_probs(const float* logits, int64_t rows, int64_t V, float temperature, float* probs,
                   void* stream);
 
@@ -378,8 +379,9 @@ int32_t sub_probs(const float* logits, int64_t rows, int64_t V, float temperatur
  * to 0 gives token 0.
  * tokens [n_seqs, n_draft + 1] gets the accepted tokens, the sampled one, then
  * -1; n_accepted [n_seqs] how many were accepted.  n_draft >= 0 (0: plain
- * sampling from p, draft and q may be NULL), 1 <= V <= 2^20; p and q 16-byte
- * aligned. */
+ * sampling from p, draft and q may be NULL), 1 <= V <= 2^20.  Any addresses
+ * (fastest where p and q are alike modulo 16 bytes); the outputs lie apart from
+ * the inputs. */
 int32_t sub_verify_sample(const float* p, const float* q, const int32_t* draft, const float* u,
                           int32_t n_seqs, int32_t n_draft, int64_t V, int32_t* tokens,
                           int32_t* n_accepted, void* stream);

@@ -9,6 +9,7 @@
 // a row that starts `mis` values past a 16-byte boundary has groups
 // [4 g - mis, 4 g - mis + 4), of which the first and last may be partial.
 #include <cmath>
+#include <type_traits>
 #include <cooperative_groups.h>
 #include "common.cuh"
 
@@ -178,27 +179,31 @@ __global__ void __launch_bounds__(THREADS, THREADS > 512 ? 1 : 1280 / THREADS) p
   }
   const float ref = m == -INFINITY ? 0.f : m, f = s == 0.f ? 0.f : 1.f / s;
   const bool again = hi - lo > MLP * THREADS;   // a single round is still in registers
-  for (int g0 = lo + threadIdx.x; g0 < hi; g0 += MLP * THREADS) {
+  auto store = [&](auto alike) {   // probabilities lie like the logits: stored in fours
+    for (int g0 = lo + threadIdx.x; g0 < hi; g0 += MLP * THREADS) {
 #pragma unroll
-    for (int k = 0; k < MLP; ++k)
-      if (again && g0 + k * THREADS < hi) x[k] = load_group(z, r, g0 + k * THREADS, -INFINITY);
+      for (int k = 0; k < MLP; ++k)
+        if (again && g0 + k * THREADS < hi) x[k] = load_group(z, r, g0 + k * THREADS, -INFINITY);
 #pragma unroll
-    for (int k = 0; k < MLP; ++k) {
-      const int g = g0 + k * THREADS;
-      if (g >= hi) break;
-      const float4 e = exponents(x[k], -ref);
-      const float w[4] = {exp2_small(e.x) * f, exp2_small(e.y) * f, exp2_small(e.z) * f,
-                          exp2_small(e.w) * f};
-      if (r.whole(g)) {
-        __stcs(reinterpret_cast<float4*>(out - r.mis) + g, make_float4(w[0], w[1], w[2], w[3]));
-      } else {
-        const int64_t at = r.first(g);
+      for (int k = 0; k < MLP; ++k) {
+        const int g = g0 + k * THREADS;
+        if (g >= hi) break;
+        const float4 e = exponents(x[k], -ref);
+        const float w[4] = {exp2_small(e.x) * f, exp2_small(e.y) * f, exp2_small(e.z) * f,
+                            exp2_small(e.w) * f};
+        if (decltype(alike)::value && r.whole(g)) {
+          __stcs(reinterpret_cast<float4*>(out - r.mis) + g, make_float4(w[0], w[1], w[2], w[3]));
+        } else {
+          const int64_t at = r.first(g);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (at + i >= 0 && at + i < V) out[at + i] = w[i];
+          for (int i = 0; i < 4; ++i)
+            if (at + i >= 0 && at + i < V) out[at + i] = w[i];
+        }
       }
     }
-  }
+  };
+  if (((reinterpret_cast<uintptr_t>(z) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0) store(std::true_type{});
+  else store(std::false_type{});
 }
 
 // ------------------------------------------------- draft verification --
@@ -425,6 +430,13 @@ cudaError_t launch_clusters(void (*kern)(KArgs...), int64_t rows, int size, int 
   return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
 }
 
+// Whether a and b, of that many values of 4 bytes, have any in common (none at NULL).
+bool overlap(const void* a, __int128 n_a, const void* b, __int128 n_b) {
+  const __int128 x = (__int128)reinterpret_cast<uintptr_t>(a), y = (__int128)reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + 4 * n_b && y < x + 4 * n_a;
+}
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+
 }  // namespace
 }  // namespace sub
 
@@ -438,7 +450,9 @@ extern "C" int32_t sub_probs(const float* logits, int64_t rows, int64_t V, float
                 "temperature must be in [1e-6, 1e6]");
   if (rows == 0) return SUB_OK;
   SUB_CHECK_ARG(logits && probs, "null pointer");
-  SUB_CHECK_ARG(aligned16(logits) && aligned16(probs), "logits and probs must be 16-byte aligned");
+  SUB_CHECK_ARG(aligned4(logits) && aligned4(probs), "logits and probs must be 4-byte aligned");
+  SUB_CHECK_ARG(probs == logits || !overlap(logits, rows * V, probs, rows * V),
+                "probs must be the logits or lie apart from them");
   const double c = 1.4426950408889634074 / (double)temperature;
   float c_hi = (float)c;
   if ((double)c_hi >= c) c_hi = std::nextafterf(c_hi, 0.f);
@@ -470,7 +484,19 @@ extern "C" int32_t sub_verify_sample(const float* p, const float* q, const int32
   SUB_CHECK_ARG(V >= 1 && V <= MAX_V, "V must be in [1, 2^20]");
   if (n_seqs == 0) return SUB_OK;
   SUB_CHECK_ARG(p && u && tokens && n_accepted && (draft || n_draft == 0), "null pointer");
-  SUB_CHECK_ARG(aligned16(p) && aligned16(q), "p and q must be 16-byte aligned");
+  SUB_CHECK_ARG(aligned4(p) && aligned4(q) && aligned4(draft) && aligned4(u) && aligned4(tokens) &&
+                    aligned4(n_accepted),
+                "pointers must be 4-byte aligned");
+  const __int128 chain = n_draft, seqs = n_seqs;
+  for (int i = 0; i < 2; ++i) {
+    const void* const out = i ? (const void*)n_accepted : tokens;
+    const __int128 n = i ? seqs : seqs * (chain + 1);
+    SUB_CHECK_ARG(!overlap(out, n, p, seqs * (chain + 1) * V) && !overlap(out, n, q, seqs * chain * V) &&
+                      !overlap(out, n, draft, seqs * chain) && !overlap(out, n, u, seqs * (chain + 1)),
+                  "tokens and n_accepted must lie apart from the inputs");
+  }
+  SUB_CHECK_ARG(!overlap(tokens, seqs * (chain + 1), n_accepted, seqs),
+                "tokens and n_accepted must lie apart");
   VerifyArgs a{p, q, draft, u, n_draft, V, tokens, n_accepted};
   // rows one CTA reads in a few rounds need no cluster
   const int size = V <= 8192 ? 1 : MAX_CLUSTER;

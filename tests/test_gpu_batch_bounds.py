@@ -106,3 +106,50 @@ def test_probabilities_below_the_normal_numbers(sub, v, t):
     assert tiny.sum() >= 2 and np.all(p[ref > 2.0 ** -146] > 0)
     rel = 2.0 ** -24 * (2.5 * 110 + 2.5 * 110 + 400 + 12)
     assert np.all(np.abs(p - ref) <= rel * ref + 2.0 ** -148)
+
+
+# ------------------------------------------------------------ addresses --
+def _at(t, off):
+    """The same values, `off` values past a 16-byte boundary."""
+    flat = torch.zeros(t.numel() + 8, dtype=t.dtype, device=t.device)
+    view = flat[off:off + t.numel()].view(t.shape)
+    return view.copy_(t)
+
+
+@pytest.mark.parametrize("v", [7, 5001, 128255])
+def test_probs_at_any_address(sub, v):
+    """Where the logits lie decides which four values are summed first, so their address
+    moves a result within test_probs' bound (span / T at most 40 here); where the
+    probabilities go moves nothing."""
+    z = 2.5 * torch.randn(3, v, device=DEV, generator=torch.Generator(device=DEV).manual_seed(v))
+    ref = ob.probs(z.cpu().numpy(), 0.7)
+    assert float(z.max() - z.min()) / 0.7 < 40
+    bound = 2.0 ** -24 * (2.5 * 40 + 2.5 * 40 + 400 + 12) * ref + 2.0 ** -126
+    want = sub.probs(z, 0.7)
+    assert torch.equal(sub.probs(z[1:2], 0.7), want[1:2])
+    for i in range(4):
+        want = sub.probs(_at(z, i), 0.7)
+        assert np.all(np.abs(want.cpu().numpy().astype(np.float64) - ref) <= bound)
+        for j in range(4):
+            flat = torch.full((3 * v + 16,), 5.0, device=DEV)
+            out = flat[8 + j:8 + j + 3 * v].view(3, v)
+            assert sub.probs(_at(z, i), 0.7, out=out) is out and torch.equal(out, want)
+            assert torch.all(flat[:8 + j] == 5) and torch.all(flat[8 + j + 3 * v:] == 5)
+        own = _at(z, i)
+        assert torch.equal(sub.probs(own, 0.7, out=own), want)
+
+
+@pytest.mark.parametrize("v", [7, 5001, 128255])
+def test_verify_sample_at_any_address(sub, v):
+    g = torch.Generator(device=DEV).manual_seed(v)
+    p = torch.softmax(2.5 * torch.randn(4, 3, v, device=DEV, generator=g), -1)
+    q = torch.softmax(p.log()[:, :2] + 0.4 * torch.randn(4, 2, v, device=DEV, generator=g), -1)
+    draft = q.argmax(-1).to(torch.int32)
+    u = torch.rand(4, 3, device=DEV, generator=g)
+    tok, acc = sub.verify_sample(p, q, draft, u)
+    t1, a1 = sub.verify_sample(p[1:2], q[1:2], draft[1:2], u[1:2])
+    assert torch.equal(t1, tok[1:2]) and torch.equal(a1, acc[1:2])
+    for i in range(4):
+        for j in range(4):
+            t, a = sub.verify_sample(_at(p, i), _at(q, j), draft, u)
+            assert torch.equal(t, tok) and torch.equal(a, acc)

@@ -351,7 +351,7 @@ int32_t sub_chunk_attn8(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q,
                         float softmax_scale, sub_bf16* O, void* workspace,
                         int64_t workspace_bytes, void* stream);
 /* *bytes = workspace that one sub_chunk_attn / sub_chunk_attn8 call of these
- * sizes may need (0: none). */
+ * sizes on the current device may need (0: none). */
 int32_t sub_chunk_attn_workspace(int32_t n_heads_q, int32_t n_heads_kv, int32_t head_dim,
                                  int32_t n_seqs, int32_t n_rows, int64_t* bytes);
 

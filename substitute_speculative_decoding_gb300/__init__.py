@@ -498,12 +498,21 @@ def kv8_read(kv: KV8Cache, layer: int, batch: Batch, out=None, stream=None):
     return k, v
 
 
-@functools.lru_cache(maxsize=4096)
 def chunk_attn_workspace(n_heads_q: int, n_heads_kv: int, head_dim: int, n_seqs: int,
                          n_rows: int) -> int:
-    """Bytes of workspace that a chunk_attn call of these sizes may need."""
+    """Bytes of workspace that a chunk_attn call of these sizes on the current device may
+    need."""
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    return _workspace_bytes(dev, n_heads_q, n_heads_kv, head_dim, n_seqs, n_rows)
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(device: int, *sizes) -> int:
+    if device >= 0 and torch.cuda.current_device() != device:
+        with torch.cuda.device(device):
+            return _workspace_bytes(device, *sizes)
     n = _i64()
-    _check(_chunk_attn_workspace(n_heads_q, n_heads_kv, head_dim, n_seqs, n_rows, C.byref(n)))
+    _check(_chunk_attn_workspace(*sizes, C.byref(n)))
     return n.value
 
 
@@ -523,7 +532,7 @@ def chunk_attn(q, kv, layer: int, batch: Batch, scale=None, out=None, workspace=
         out = _new((n, hq, d), torch.bfloat16, dev, stream, True)
     at = _dense(out, torch.bfloat16, (n, hq, d), "out", dev)
     if workspace is None:
-        size = chunk_attn_workspace(hq, kv.n_heads_kv, d, batch.n_seqs, n)
+        size = _workspace_bytes(dev.index, hq, kv.n_heads_kv, d, batch.n_seqs, n)
         workspace = _new(size, torch.uint8, dev, stream, False)
     else:
         size = workspace.numel()

@@ -43,6 +43,17 @@ int32_t check_launch(const char* what) {
   return SUB_OK;
 }
 
+int device_sms() {
+  static std::atomic<int> count[MAX_DEVICES];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+  const bool known = dev >= 0 && dev < MAX_DEVICES;
+  if (known && (n = count[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 152;
+  if (known) count[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
 }  // namespace sub
 
 using namespace sub;

@@ -52,7 +52,6 @@
 // to the end), the block's products with V are formed one by one without the keys of
 // weight zero.
 #include <algorithm>
-#include <mutex>
 #include <type_traits>
 #include "chunk_attn.cuh"
 #include "tma.cuh"
@@ -856,18 +855,6 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) chunk_join_kernel(const __gri
 }
 
 // -------------------------------------------------------------------- host --
-int sm_count() {
-  static int n = 0;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-      n = 152;
-  });
-  return n;
-}
-
 template <int D, int RT>
 int32_t launch_join(const ChunkArgs& a, int n_ctas, cudaStream_t st) {
   SUB_CUDA_TRY(launch_k(chunk_join_kernel<D, RT>, dim3(n_ctas, join_split(RT)),
@@ -877,14 +864,11 @@ int32_t launch_join(const ChunkArgs& a, int n_ctas, cudaStream_t st) {
 
 template <int D, bool Q8, int RT>
 int32_t launch_decode(const ChunkArgs& a, int n_ctas, cudaStream_t st) {
-  static std::once_flag once;
-  static cudaError_t err = cudaSuccess;
   constexpr int SMEM = decode_smem<D, Q8>();
-  std::call_once(once, [] {
-    err = cudaFuncSetAttribute(chunk_attn_kernel<D, Q8, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               SMEM);
-  });
-  SUB_CUDA_TRY(err);
+  SUB_CUDA_TRY(once_per_device([] {
+    return cudaFuncSetAttribute(chunk_attn_kernel<D, Q8, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                SMEM);
+  }));
   PageMaps maps;
   if (!chunk_page_map(&maps.k, a.k, a.t, (int64_t)a.n_layers * a.n_heads_kv, D, Q8) ||
       !chunk_page_map(&maps.v, a.v, a.t, (int64_t)a.n_layers * a.n_heads_kv, D, Q8))
@@ -910,7 +894,7 @@ int tile_rows(int group, int n_seqs, int n_rows, bool codes, int64_t keys) {
 
 // Partial results, two per CTA, and the list of cuts.
 int64_t part_bytes(int rows, int d) {
-  return (int64_t)sm_count() * (2 * rows * (d + 2) * 4 + (int64_t)sizeof(ChunkCut));
+  return (int64_t)device_sms() * (2 * rows * (d + 2) * 4 + (int64_t)sizeof(ChunkCut));
 }
 
 template <class Cache>
@@ -962,7 +946,7 @@ int32_t chunk_attn(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q, const Cach
   const int64_t pool_rows =
       (int64_t)kv->n_layers * kv->n_pages * kv->n_heads_kv * kv->page_size;
   const bool tensor_cores = rt == CHUNK_TC_ROWS && chunk_tc_fits(pool_rows);
-  const int n_ctas = sm_count();
+  const int n_ctas = device_sms();
   const int part_rows = tensor_cores ? CHUNK_TC_ROWS : std::min(rt, WIDE);
   a.part_o = reinterpret_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float2*>(a.part_o + (int64_t)n_ctas * 2 * part_rows * kv->head_dim);

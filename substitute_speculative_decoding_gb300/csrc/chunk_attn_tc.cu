@@ -1045,13 +1045,10 @@ bool pool_map(CUtensorMap* m, const void* pool, int64_t rows, int d, int box) {
 template <int D, bool Q8>
 int32_t launch(const ChunkArgs& a, int64_t rows, int n_ctas, cudaStream_t st) {
   using C = Cfg<D, Q8>;
-  static std::once_flag once;
-  static cudaError_t err = cudaSuccess;
-  std::call_once(once, [] {
-    err = cudaFuncSetAttribute(chunk_tc_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               C::SMEM);
-  });
-  SUB_CUDA_TRY(err);
+  SUB_CUDA_TRY(once_per_device([] {
+    return cudaFuncSetAttribute(chunk_tc_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                C::SMEM);
+  }));
   Maps maps;
   memset(&maps, 0, sizeof(maps));
   int box = 16;

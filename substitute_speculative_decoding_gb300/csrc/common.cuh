@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
+#include <atomic>
 #include <string>
 #include <cstring>
 #include "../../include/sub_api.h"
@@ -41,6 +42,25 @@ struct StreamScratch {
     if (p) cudaFreeAsync(p, st);
   }
 };
+
+// f, which prepares the current device (a kernel's attributes belong to the device that is
+// current when they are set), once for each device: every place that calls this has
+// its own record.  Threads that meet here may both call f; a failure is not remembered.
+constexpr int MAX_DEVICES = 64;   // beyond: f at every call
+template <class F>
+cudaError_t once_per_device(F f) {
+  static std::atomic<bool> done[MAX_DEVICES];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool known = dev >= 0 && dev < MAX_DEVICES;
+  if (known && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = f();
+  if (e == cudaSuccess && known) done[dev].store(true, std::memory_order_release);
+  return e;
+}
+
+int device_sms();   // SMs of the current device
 
 // ------------------------------------------- programmatic dependent launch --
 // Kernels of the decode path are launched with programmatic stream

@@ -468,8 +468,9 @@ extern "C" int32_t sub_probs(const float* logits, int64_t rows, int64_t V, float
     return SUB_OK;
   }
   int size = 1;
-  while (size < MAX_CLUSTER && (V > size * 8192 || (rows * size < 152 && V > size * 4096))) size *= 2;
-  if (rows * size <= 152 && V > size * 4096 && V <= size * 20480 - 4)
+  const int sms = device_sms();
+  while (size < MAX_CLUSTER && (V > size * 8192 || (rows * size < sms && V > size * 4096))) size *= 2;
+  if (rows * size <= sms && V > size * 4096 && V <= size * 20480 - 4)
     SUB_CUDA_TRY(launch_clusters(probs_kernel<1024, 5>, rows, size, 1024, st, logits, V, c_hi, c_lo, probs));
   else
     SUB_CUDA_TRY(launch_clusters(probs_kernel<256, 4>, rows, size, 256, st, logits, V, c_hi, c_lo, probs));

@@ -422,8 +422,8 @@ def _paged(struct, dtype, k, v, page_table, scales=()):
     at += [_dense(x, torch.float32, shape[:4], n, dev) for x, n in scales]
     at.append(_dense(page_table, torch.int32, page_table.shape, "page_table", dev))
     kv = struct(*at, nl, h, d, ps, npg, page_table.shape[1] * ps)
-    kv.keep, kv.device, kv.n_seqs = (k, v, page_table, *scales), dev, page_table.shape[0]
-    kv.ref = C.byref(kv)
+    kv.keep = (k, v, page_table, *(x for x, _ in scales))
+    kv.device, kv.n_seqs = dev, page_table.shape[0]
     return kv
 
 
@@ -453,7 +453,6 @@ def batch(start, pos, n_rows: int, max_keys: int = 0) -> Batch:
     b = Batch(_dense(start, torch.int32, (n + 1,), "start", dev),
               _dense(pos, torch.int32, (n,), "pos", dev), n, n_rows, max_keys)
     b.keep, b.device = (start, pos), dev
-    b.ref = C.byref(b)
     return b
 
 
@@ -480,7 +479,7 @@ def _append_rows(fn, k, v, kv, layer, batch, stream):
     dev = _same(kv, batch)
     n, h, d = batch.n_rows, kv.n_heads_kv, kv.head_dim
     ldk, ldv = _rows(k, n, h, d, "k", dev), _rows(v, n, h, d, "v", dev)
-    _run(fn, dev, stream, k.data_ptr(), ldk, v.data_ptr(), ldv, kv.ref, layer, batch.ref)
+    _run(fn, dev, stream, k.data_ptr(), ldk, v.data_ptr(), ldv, kv, layer, batch)
 
 
 def kv8_read(kv: KV8Cache, layer: int, batch: Batch, out=None, stream=None):
@@ -492,7 +491,7 @@ def kv8_read(kv: KV8Cache, layer: int, batch: Batch, out=None, stream=None):
         out = (_new(shape, torch.bfloat16, dev, stream, True),
                _new(shape, torch.bfloat16, dev, stream, True))
     k, v = out
-    _run(_kv8_read, dev, stream, kv.ref, layer, batch.ref,
+    _run(_kv8_read, dev, stream, kv, layer, batch,
          _dense(k, torch.bfloat16, shape, "out[0]", dev),
          _dense(v, torch.bfloat16, shape, "out[1]", dev))
     return k, v
@@ -538,7 +537,7 @@ def chunk_attn(q, kv, layer: int, batch: Batch, scale=None, out=None, workspace=
         size = workspace.numel()
         _dense(workspace, torch.uint8, workspace.shape, "workspace", dev)
     _run(_chunk_attn8 if type(kv) is KV8Cache else _chunk_attn, dev, stream, q.data_ptr(), ldq, hq,
-         kv.ref, layer, batch.ref, d ** -0.5 if scale is None else scale, at,
+         kv, layer, batch, d ** -0.5 if scale is None else scale, at,
          workspace.data_ptr() or None, size)
     return out
 

@@ -893,8 +893,12 @@ int tile_rows(int group, int n_seqs, int n_rows, bool codes, int64_t keys) {
 }
 
 // Partial results, two per CTA, and the list of cuts.
-int64_t part_bytes(int rows, int d) {
-  return (int64_t)device_sms() * (2 * rows * (d + 2) * 4 + (int64_t)sizeof(ChunkCut));
+int64_t part_bytes(int n_ctas, int rows, int d) {
+  return (int64_t)n_ctas * (2 * rows * (d + 2) * 4 + (int64_t)sizeof(ChunkCut));
+}
+// What a call of these sizes may need: the largest tiles that it may get.
+int64_t work_bytes(int n_ctas, int group, int d, int n_seqs, int n_rows) {
+  return n_rows ? part_bytes(n_ctas, tile_rows(group, n_seqs, n_rows, false, INT64_MAX), d) : 0;
 }
 
 template <class Cache>
@@ -930,9 +934,8 @@ int32_t chunk_attn(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q, const Cach
   // (a scale of 0 must not meet the masked scores' -infinity)
   a.sl2 = fmaxf(softmax_scale, 1e-30f) * 1.4426950408889634f;
   const cudaStream_t st = as_stream(stream);
-  int64_t need = 0;
-  SUB_TRY(sub_chunk_attn_workspace(n_heads_q, kv->n_heads_kv, kv->head_dim, a.t.n_seqs, a.t.n_rows,
-                                   &need));
+  const int n_ctas = device_sms();
+  const int64_t need = work_bytes(n_ctas, a.group, kv->head_dim, a.t.n_seqs, a.t.n_rows);
   StreamScratch scratch(st);
   if (workspace) {
     SUB_CHECK_ARG((reinterpret_cast<uintptr_t>(workspace) & 31) == 0 && workspace_bytes >= need,
@@ -946,7 +949,6 @@ int32_t chunk_attn(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q, const Cach
   const int64_t pool_rows =
       (int64_t)kv->n_layers * kv->n_pages * kv->n_heads_kv * kv->page_size;
   const bool tensor_cores = rt == CHUNK_TC_ROWS && chunk_tc_fits(pool_rows);
-  const int n_ctas = device_sms();
   const int part_rows = tensor_cores ? CHUNK_TC_ROWS : std::min(rt, WIDE);
   a.part_o = reinterpret_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float2*>(a.part_o + (int64_t)n_ctas * 2 * part_rows * kv->head_dim);
@@ -985,8 +987,7 @@ extern "C" int32_t sub_chunk_attn_workspace(int32_t n_heads_q, int32_t n_heads_k
   SUB_CHECK_ARG(n_heads_kv >= 1 && n_heads_q >= 1 && n_heads_q % n_heads_kv == 0,
                 "Hq must be a multiple of Hkv");
   SUB_CHECK_ARG(n_seqs >= 1 && n_seqs <= SUB_MAX_SEQS && n_rows >= 0, "bad batch sizes");
-  const int rt = tile_rows(n_heads_q / n_heads_kv, n_seqs, n_rows, false, INT64_MAX);   // the largest of them
-  *bytes = n_rows ? part_bytes(rt, head_dim) : 0;
+  *bytes = work_bytes(device_sms(), n_heads_q / n_heads_kv, head_dim, n_seqs, n_rows);
   return SUB_OK;
 }
 

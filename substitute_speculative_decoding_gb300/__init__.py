@@ -37,12 +37,16 @@ _i32, _i64, _u64, _f32 = C.c_int32, C.c_int64, C.c_uint64, C.c_float
 
 
 class KVCache(C.Structure):
+    """sub_kv_cache.  device: where its tensors are; n_seqs: rows of its page table."""
+    device, n_seqs = None, 1
     _fields_ = [("k", _vp), ("v", _vp), ("page_table", _vp), ("n_layers", _i32),
                 ("n_heads_kv", _i32), ("head_dim", _i32), ("page_size", _i32),
                 ("n_pages", _i32), ("capacity", _i64)]
 
 
 class KV8Cache(C.Structure):
+    """sub_kv8_cache, with the same."""
+    device, n_seqs = None, 1
     _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("page_table", _vp),
                 ("n_layers", _i32), ("n_heads_kv", _i32), ("head_dim", _i32),
                 ("page_size", _i32), ("n_pages", _i32), ("capacity", _i64)]
@@ -356,6 +360,7 @@ def make_kv(n_layers, n_heads_kv, head_dim, capacity, page_size=64, device="cuda
     pt = pt.to(device)
     st = KVCache(k.data_ptr(), v.data_ptr(), pt.data_ptr(), n_layers, n_heads_kv, head_dim,
                  page_size, n_pages, n_pages * page_size)
+    st.device = k.device
     return st, (k, v, pt)
 
 
@@ -457,11 +462,11 @@ def batch(start, pos, n_rows: int, max_keys: int = 0) -> Batch:
 
 
 def _same(kv, b):
-    if kv.device != b.device:
+    if kv.device != b.device and kv.device is not None:   # None: a struct filled by hand
         _refuse("the batch and the cache must be on one device")
     if kv.n_seqs != b.n_seqs:
         _refuse("page_table and batch must have the same number of sequences")
-    return kv.device
+    return b.device
 
 
 def kv_append(k, v, kv: KVCache, layer: int, batch: Batch, stream=None):
@@ -668,6 +673,7 @@ class Model:
         h = _vp()
         _check(_model_create(C.byref(d), C.byref(h)))
         self.handle = h
+        self.device = torch.device("cuda", torch.cuda.current_device())   # of its pools
 
     def close(self):
         """Destroy the model and drop the tensors it pointed into (the pinned
@@ -690,8 +696,10 @@ class Model:
         return b.value
 
     def kv(self) -> KVCache:
+        """The cache of the model's one sequence.  Keeps the model; not valid after close()."""
         kv = KVCache()
         _check(_model_kv(self.handle, C.byref(kv)))
+        kv.keep, kv.device = (self,), self.device
         return kv
 
     def forward(self, which: int, tokens, slot0: int, n_prefix: int, depth=None, anc=None,

@@ -1,5 +1,5 @@
 """Handles of batched calls on the host (no GPU needed): they let go of their tensors
-when they are dropped."""
+when they are dropped; the caches of one sequence are such handles, too."""
 import gc
 import weakref
 
@@ -43,3 +43,15 @@ def test_a_dropped_handle_frees_its_tensors_at_once(s):
             assert [r() for r in kept] == [None] * len(kept)
     finally:
         gc.enable()
+
+
+def test_a_cache_of_one_sequence_is_a_cache_for_batches(s):
+    kv, (k, _, _) = s.make_kv(1, 2, 64, 40, page_size=16, device="cpu")
+    one, two = (s.Batch(4096, 4096, n, 4, 0) for n in (1, 2))
+    one.device = two.device = k.device
+    assert s._same(kv, one) == k.device
+    with pytest.raises(s.SubError):
+        s._same(kv, two)
+    kv.device = torch.device("cuda", 1)
+    with pytest.raises(s.SubError):
+        s._same(kv, one)

@@ -153,3 +153,45 @@ def test_verify_sample_at_any_address(sub, v):
         for j in range(4):
             t, a = sub.verify_sample(_at(p, i), _at(q, j), draft, u)
             assert torch.equal(t, tok) and torch.equal(a, acc)
+
+
+# ------------------------------------------- caches of one sequence --
+def test_a_cache_of_one_sequence_takes_batches(sub):
+    """make_kv's cache: the same rows and results as a paged_kv of its tensors."""
+    kv, (k, v, pt) = sub.make_kv(2, 2, 64, 100, page_size=16, shuffle_seed=1)
+    g = torch.Generator(device=DEV).manual_seed(0)
+    rows = [torch.randn(90, 2, 64, device=DEV, generator=g).to(BF) for _ in range(2)]
+    q = torch.randn(90, 8, 64, device=DEV, generator=g).to(BF)
+    b = sub.batch(torch.tensor([0, 90], dtype=torch.int32, device=DEV),
+                  torch.tensor([0], dtype=torch.int32, device=DEV), 90)
+    sub.kv_append(*rows, kv, 1, b)
+    o = sub.chunk_attn(q, kv, 1, b)
+    k2, v2 = torch.zeros_like(k), torch.zeros_like(v)
+    other = sub.paged_kv(k2, v2, pt[None])
+    sub.kv_append(*rows, other, 1, b)
+    assert torch.equal(k, k2) and torch.equal(v, v2) and k.any()
+    assert torch.equal(o, sub.chunk_attn(q, other, 1, b))
+    two = sub.batch(torch.tensor([0, 45, 90], dtype=torch.int32, device=DEV),
+                    torch.tensor([0, 0], dtype=torch.int32, device=DEV), 90)
+    with pytest.raises(sub.SubError):
+        sub.chunk_attn(q, kv, 1, two)
+
+
+def test_a_model_s_cache_takes_batches(sub):
+    import synthetic
+    cfg = synthetic.CONFIGS["tiny"]
+    m = sub.Model(cfg, synthetic.make_model(cfg, norm_gain_std=0.1), max_seq=128, max_depth=4,
+                  max_width=2, max_prompt=32)
+    m.generate(synthetic.make_prompt(cfg), 4, depth=2, width=2)
+    kv = m.kv()
+    g = torch.Generator(device=DEV).manual_seed(0)
+    n, h, d = 6, kv.n_heads_kv, kv.head_dim
+    rows = [torch.randn(n, h, d, device=DEV, generator=g).to(BF) for _ in range(2)]
+    q = torch.randn(n, 2 * h, d, device=DEV, generator=g).to(BF)
+    b = sub.batch(torch.tensor([0, n], dtype=torch.int32, device=DEV),
+                  torch.tensor([0], dtype=torch.int32, device=DEV), n)
+    sub.kv_append(*rows, kv, 0, b)
+    o = sub.chunk_attn(q, kv, 0, b)
+    ref, w = ob.chunk_attention(np32(q), np32(rows[0]), np32(rows[1]), 0)
+    assert np.all(np.abs(np32(o) - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 1e-4) * w)
+    m.close()

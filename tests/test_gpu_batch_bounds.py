@@ -195,3 +195,56 @@ def test_a_model_s_cache_takes_batches(sub):
     ref, w = ob.chunk_attention(np32(q), np32(rows[0]), np32(rows[1]), 0)
     assert np.all(np.abs(np32(o) - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 1e-4) * w)
     m.close()
+
+
+# ------------------------------------------------------ unlike sequences --
+@pytest.mark.parametrize("bits", [16, 8])
+def test_one_prompt_among_single_rows(sub, bits):
+    """The batch's average picks another kernel than its longest sequence would, and
+    the other way round."""
+    many = [(100 + 9 * b, 1) for b in range(40)]
+    for seqs in (many + [(30, 90)], many[:3] + [(64, 200)], [(5, 300)] + many[:1]):
+        c = Case(sub, seqs, 8, 2, 64, bits=bits, seed=12)
+        o = sub.chunk_attn(c.q.to(DEV), c.kv, c.layer, c.batch)
+        c.check(o)
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("n_seqs", [33, 1023, 1024])
+def test_as_many_sequences_as_a_batch_takes(sub, bits, n_seqs):
+    """Rows find their sequence and the work its place with every entry of start used;
+    some sequences are empty."""
+    seqs = [(b % 13, (b * 5) % 3) for b in range(n_seqs - 1)] + [(7, 2)]
+    c = Case(sub, seqs, 2, 1, 64, bits=bits, layers=1, layer=0, seed=13, pad=2)
+    lo, hi = int(c.start[0]), int(c.start[-1])
+    if bits == 16:
+        for t in c.pools:
+            t.nan_to_num_(nan=3.0)
+    want = [t.clone() for t in c.pools]
+    rows = [torch.zeros(c.batch.n_rows, 1, 64, dtype=BF) for _ in range(2)]
+    for b, (p, n) in enumerate(seqs):
+        for new, side in zip(rows, (c.k, c.v)):
+            new[int(c.start[b]):int(c.start[b]) + n] = side[b][p:]
+        for t in c.pools if n else ():        # cleared, to be written again
+            t[0, int(c.table[b, 0]), :, p] = 1
+    append = sub.kv_append if bits == 16 else sub.kv8_append
+    append(rows[0].to(DEV), rows[1].to(DEV), c.kv, 0, c.batch)
+    assert all(torch.equal(got, ref) for got, ref in zip(c.pools, want))
+    o = torch.full((c.batch.n_rows, 2, 64), 7.0, dtype=BF, device=DEV)
+    sub.chunk_attn(c.q.to(DEV), c.kv, 0, c.batch, out=o)
+    c.check(o)
+    assert torch.all(o[:lo] == 7) and torch.all(o[hi:] == 7)
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+def test_a_thousand_prompts(sub, bits):
+    """The same for the tiles of many rows, on one page that all sequences share."""
+    n_seqs, n = 1024, 33
+    c = Case(sub, [(5, n)], 4, 1, 64, page=48, bits=bits, layers=1, layer=0, seed=14)
+    table = c.table_d[:, :1].expand(n_seqs, 1).contiguous()
+    kv = sub.paged_kv(*c.pools, table) if bits == 16 else sub.paged_kv8(*c.pools, *c.scales, table)
+    start = torch.arange(n_seqs + 1, dtype=torch.int32, device=DEV) * n
+    b = sub.batch(start, torch.full((n_seqs,), 5, dtype=torch.int32, device=DEV), n_seqs * n)
+    o = sub.chunk_attn(c.q.to(DEV).repeat(n_seqs, 1, 1), kv, 0, b).view(n_seqs, n, 4, 64)
+    c.check(o[0])
+    assert torch.equal(o, o[:1].expand_as(o))

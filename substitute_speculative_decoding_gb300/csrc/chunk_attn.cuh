@@ -52,9 +52,12 @@ struct __align__(16) ChunkCut {
 // by lies in memory that only kernels which ran to their end have written.
 __host__ __device__ inline bool cut_stands(const ChunkCut& c, int part, int n_ctas, int n_rows,
                                            int n_heads_kv, int group, int tile_rows) {
-  return c.pieces >= 2 && c.pieces <= n_ctas - part && (c.first == 2 * part || c.first == 2 * part + 1) &&
-         c.row0 >= 0 && c.rows >= 1 && c.row0 <= n_rows && c.rows <= n_rows - c.row0 && c.head >= 0 &&
-         c.head < n_heads_kv && c.tile >= 0 && (int64_t)c.tile * tile_rows < (int64_t)c.rows * group;
+  // (a negative value is a large one; rows * group < 2^31, tile_rows is a power of two)
+  const uint32_t row0 = c.row0, rows = c.rows, all = n_rows;
+  return ((uint32_t)c.pieces - 2u < (uint32_t)(n_ctas - part - 1)) &
+         ((uint32_t)c.first - 2u * part < 2u) & (row0 <= all) & (rows - 1u < all - row0) &
+         ((uint32_t)c.head < (uint32_t)n_heads_kv) &
+         ((uint32_t)c.tile <= (rows * group - 1u) / (uint32_t)tile_rows);
 }
 
 // Quotients of line positions, nearly always of 32 bits.  (The compiler's 64-bit
@@ -73,6 +76,18 @@ __device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
     }
   }
   return (int64_t)q;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+// Codes in two bytes of w as fp16 code - 128.
+__device__ __forceinline__ uint32_t codes2(uint32_t w, uint32_t sel) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(__byte_perm(w, 0x64646464u, sel)), "r"(0x64806480u));
+  return r;
 }
 
 // Last key that row q of a sequence reads, of n_keys.  (pos may be anything.)

@@ -53,11 +53,9 @@
 // group's warps look through V: rows past the end and values that are not
 // finite become 0, and if there were any of these, each row adds those that it does
 // read to its result (whatever is added to them, it stays infinite or NaN).
-#include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_fp16.h>
-#include <mutex>
 #include "chunk_attn.cuh"
+#include "gemv.cuh"
 #include "tma.cuh"
 
 namespace sub {
@@ -194,38 +192,6 @@ __device__ __forceinline__ void tc_st16(uint32_t t, const uint32_t* r) {
       : "memory");
 }
 
-// Two fp32 operations in one instruction.
-union F2 {
-  float2 f;
-  uint64_t u;
-};
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  F2 x{a}, y{b}, z{c}, d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.u) : "l"(x.u), "l"(y.u), "l"(z.u));
-  return d.f;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  F2 x{a}, y{b}, d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.u) : "l"(x.u), "l"(y.u));
-  return d.f;
-}
-__device__ __forceinline__ float exp2_fast(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-  return r;
-}
-__device__ __forceinline__ uint32_t codes2(uint32_t w, uint32_t sel) {
-  uint32_t r;
-  asm("sub.rn.f16x2 %0, %1, %2;"
-      : "=r"(r)
-      : "r"(__byte_perm(w, 0x64646464u, sel)), "r"(0x64806480u));
-  return r;
-}
 __device__ __forceinline__ bool elect_one() {   // by a whole warp: one lane
   uint32_t x;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(x));
@@ -1017,31 +983,6 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
 }
 
 // -------------------------------------------------------------------- host --
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  return fn;
-}
-
-bool pool_map(CUtensorMap* m, const void* pool, int64_t rows, int d, int box) {
-  auto fn = encode_fn();
-  if (!fn) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)d * 2};
-  const cuuint32_t boxes[2] = {64, (cuuint32_t)box}, es[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(pool), dims, strides, boxes,
-            es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int D, bool Q8>
 int32_t launch(const ChunkArgs& a, int64_t rows, int n_ctas, cudaStream_t st) {
   using C = Cfg<D, Q8>;
@@ -1053,7 +994,10 @@ int32_t launch(const ChunkArgs& a, int64_t rows, int n_ctas, cudaStream_t st) {
   memset(&maps, 0, sizeof(maps));
   int box = 16;
   while (box < KB && a.t.page_size % (2 * box) == 0) box *= 2;
-  if (!Q8 && (!pool_map(&maps.k, a.k, rows, D, box) || !pool_map(&maps.v, a.v, rows, D, box)))
+  auto pool_map = [&](CUtensorMap* m, const void* pool) {
+    return make_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pool, D, rows, D * 2, 64, box, 128);
+  };
+  if (!Q8 && (!pool_map(&maps.k, a.k) || !pool_map(&maps.v, a.v)))
     return fail(SUB_ECUDA, "chunk_attn: the cache's tensor map was refused");
   SUB_CUDA_TRY(launch_k(chunk_tc_kernel<D, Q8>, dim3(n_ctas), dim3(C::THREADS), C::SMEM, st, maps, a,
                         box, (int)rows));

@@ -58,32 +58,7 @@ __device__ __forceinline__ void cluster_all_here() {
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
 
-// Two fp32 operations in one instruction.
-union F2 {
-  float2 f;
-  uint64_t u;
-};
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  F2 x{a}, y{b}, z{c}, d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.u) : "l"(x.u), "l"(y.u), "l"(z.u));
-  return d.f;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  F2 x{a}, y{b}, d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.u) : "l"(x.u), "l"(y.u));
-  return d.f;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  F2 x{a}, y{b}, d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.u) : "l"(x.u), "l"(y.u));
-  return d.f;
-}
-__device__ __forceinline__ float exp2_fast(float x) {   // 2 ulp; flushes below 2^-126
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ float exp2_small(float x) {   // the same, down to 2^-149
+__device__ __forceinline__ float exp2_small(float x) {   // as exp2_fast, down to 2^-149
   float r;
   asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;

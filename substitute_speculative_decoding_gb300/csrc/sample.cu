@@ -80,9 +80,8 @@ __device__ __forceinline__ void share(int groups, int rank, int size, int& lo, i
 // stores did not overlap enough: 4.1 TB/s on 576 rows of 128256.)  The CTAs exchange maxima
 // and sums in one cluster barrier.
 template <int THREADS, int MLP>   // MLP: groups a thread loads in one round
-__global__ void __launch_bounds__(THREADS, THREADS > 512 ? 1 : 1280 / THREADS) probs_kernel(const float* logits, int64_t V,
-                                                                        float c_hi, float c_lo,
-                                                                        float* probs) {
+__global__ void __launch_bounds__(THREADS, 1280 / THREADS)
+probs_kernel(const float* logits, int64_t V, float c_hi, float c_lo, float* probs) {
   constexpr int WARPS = THREADS / 32;
   __shared__ float2 s_warp[WARPS];
   __shared__ float2 s_peer[MAX_CLUSTER];   // each CTA's (largest logit, sum), written by it
@@ -435,9 +434,7 @@ extern "C" int32_t sub_probs(const float* logits, int64_t rows, int64_t V, float
   const cudaStream_t st = as_stream(stream);
   // A round of a CTA's loads takes 16 values per thread.  Rows of one round: one
   // small CTA.  Longer ones: a cluster whose CTAs need two rounds at most, or as many
-  // CTAs as there are SMs (448 rows of 5000: 9 us, against 23 us as clusters of eight).
-  // The few rows that leave SMs idle get CTAs that hold a share in registers, if it
-  // fits, and skip the second reading (1 row of 152064: 9 us against 12).
+  // CTAs as there are SMs (448 rows of 5000: 7 us, against 22 as clusters of eight).
   if (V <= 2048) {
     SUB_CUDA_TRY(launch_clusters(probs_kernel<128, 4>, rows, 1, 128, st, logits, V, c_hi, c_lo, probs));
     return SUB_OK;
@@ -445,10 +442,7 @@ extern "C" int32_t sub_probs(const float* logits, int64_t rows, int64_t V, float
   int size = 1;
   const int sms = device_sms();
   while (size < MAX_CLUSTER && (V > size * 8192 || (rows * size < sms && V > size * 4096))) size *= 2;
-  if (rows * size <= sms && V > size * 4096 && V <= size * 20480 - 4)
-    SUB_CUDA_TRY(launch_clusters(probs_kernel<1024, 5>, rows, size, 1024, st, logits, V, c_hi, c_lo, probs));
-  else
-    SUB_CUDA_TRY(launch_clusters(probs_kernel<256, 4>, rows, size, 256, st, logits, V, c_hi, c_lo, probs));
+  SUB_CUDA_TRY(launch_clusters(probs_kernel<256, 4>, rows, size, 256, st, logits, V, c_hi, c_lo, probs));
   return SUB_OK;
 }
 

@@ -6,7 +6,7 @@
 // running maximum m_i.  The Hq / Hkv query heads of a KV head are rows of the
 // same tile, so a key is read once for all of them.
 //
-// Bound by HBM: a row tile of 16 does 64 flops per byte of a bf16 cache,
+// Bound by HBM: a row tile of 16 does 16 flops per byte of a bf16 cache,
 // mma.sync covers that many times over, and what counts is bytes in flight.  So
 // each of eight warps streams blocks of 16 or 32 keys (8 KB; 4 KB of codes of 64
 // columns) on its own, through a private ring of three stages that bulk tensor copies
@@ -14,7 +14,7 @@
 // loop with 16-byte cp.async copies, sixteen per lane and block, ran at 5.1 TB/s
 // on 32 sequences of up to 16384 keys and left a quarter of the SMs a fifth slower
 // than the rest; the copies alone now take 203 us, 6.7 TB/s, and the kernel
-// 217.)  No barrier in the loop, no ldmatrix: a dot product may take its terms
+// 215.)  No barrier in the loop, no ldmatrix: a dot product may take its terms
 // in any order, if Q is laid out the same way, so lane (g, tig) reads, of key g of an
 // 8-key group, the 16-byte chunks 2 tig, 2 tig + 1 of each 128 bytes, and of V, for
 // its four keys of a 16-key step, the chunk that makes its B fragments for the n tiles of
@@ -26,12 +26,12 @@
 // 8x8 transposition.
 //
 // Measured, 40 or 32 query heads of 8 KV heads of 128: 32 sequences of up to 16384 keys
-// 217 us (1.37 GB, 6.3 TB/s); codes, 2 of up to 65001 47 us (4.5 TB/s); 128 of up to
-// 2000 keys 123 us (5.4 TB/s), codes 90 (3.8); 1 sequence of 512 keys of 2 heads of 64
-// 10 us, two launches and their dependent reads.  Over codes the conversions and, on
-// short caches, the change of units show: the same loads without the products take 43
-// and 75 us.  (Twelve warps with two stages each gained 4% there and cost the
-// short call 2.6 us; Q read a unit ahead gained nothing.)
+// 215 us (1.37 GB, 6.35 TB/s); codes, 2 of up to 65001 44 us (4.8 TB/s); 128 of up to
+// 2000 keys 116 us (5.7 TB/s), codes 96 (3.5); 1 sequence of 512 keys of 2 heads of 64
+// 7.5 us, two launches and their dependent reads.  Over codes the conversions and, on
+// short caches, the change of units show: the same loads without the products took four
+// fifths of the time of the 128 sequences.  (Twelve warps with two stages each gained 4%
+// there and cost the short call a quarter; Q read a unit ahead gained nothing.)
 //
 // 8-bit codes c stand for (c - 128) * scale, and both products take c - 128 in
 // fp16, exactly: the bytes 0x64, c are 1024 + c, a byte permute and a subtraction
@@ -867,9 +867,9 @@ int32_t launch_decode(const ChunkArgs& a, int n_ctas, cudaStream_t st) {
 // rows, but it starts later and wants blocks of 128 keys.  bf16: 16 rows, and 32 up to
 // 4096 keys (32 rows of 1 sequence over 1000 keys 12 us here, 16 by the tensor cores; of
 // 8 over 4000 43 and 41; of 1 over 16000 28 and 28; 20 rows of 8 over 16000 167 and
-// 109).  Codes, which the tensor-core kernel has to convert first: 64 rows (32 rows
-// of 8 sequences over 4000 keys 34 and 46, 56 rows of 4 KV heads 29 and 33, 64 rows 48
-// and 47; 48 rows of 2 over 64000 109 and 122).
+// 108; 48 of 8 over 4000 60 and 42).  Codes, which the tensor-core kernel has to convert
+// first, with a rounding: 64 rows (32 rows of 8 sequences over 4000 keys 37 and 53, 56
+// rows of 4 KV heads 36 and 37, 64 rows 62 and 55; 48 rows of 2 over 64000 147 and 150).
 int tile_rows(int group, int n_seqs, int n_rows, bool codes, int64_t keys) {
   const int64_t rows = (int64_t)n_rows * group, seqs = n_seqs;
   const int tiles = codes ? 4 : keys <= 4096 ? 2 : 1;

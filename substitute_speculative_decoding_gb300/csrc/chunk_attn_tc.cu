@@ -4,12 +4,13 @@
 // The same sums as chunk_attn.cu, in tiles of 256 (row, head in group) pairs x
 // 128 keys.  Bound by the tensor cores: a block costs six products of 128 x 128 x D
 // (codes: four) and 2 * 128 * 128 exponentials.
-// Measured: 2048 rows of 32 heads behind 14336 keys 483 us, 1070 TFLOP/s (0.55 of a
-// plain bf16 matrix product of the library) that are counted, 1600 with the
-// weights' second halves; over codes three prompts of 1537 rows of 28
-// heads behind up to 2600 keys 196 us, 645 TFLOP/s, bounded by the converter warps: a
-// block takes 4000 cycles, 3200 of them in its conversion, against 2700 over bf16
-// (1024 rows behind 7000 keys: 157 us against 115).
+// Measured: 2048 rows of 32 heads behind 14336 keys 470 to 484 us, 1070 TFLOP/s (0.55 of
+// a plain bf16 matrix product of the library) that are counted, 1600 with the
+// weights' second halves; over codes three prompts of up to 1537 rows of 28
+// heads behind up to 2600 keys 196 us, 645 TFLOP/s, bounded by the converter warps: of a
+// block's 4000 cycles 3200 are its conversion.  1024 rows of 32 heads behind 7000 keys:
+// 138 us, over codes 146.  (The softmax warps' registers hold a row's 128 scores and
+// little else: 370 to 640 bytes per thread are spilled.)
 // So two groups of 128 rows alternate: while the tensor cores form one group's
 // scores or output, the four warps of the other turn scores into weights.
 //   warps 0-3, 4-7   softmax of rows 0-127 and 128-255, one row per thread (a

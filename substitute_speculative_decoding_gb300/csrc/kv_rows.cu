@@ -13,11 +13,13 @@
 // lanes hold one (row, head), 16 bytes each, so a warp's load covers 512
 // contiguous bytes of a token's row, the largest value is a shuffle away, and a
 // warp takes one token: its sequence is searched once for all heads.  K and V
-// go to different warps (together in one, with half the warps, 12288 rows of 8 heads
-// took 29 us instead of 27 to be written and read, 64 rows 10.4 instead of 9.1).
-// Measured: 12288 rows of 8 heads of 128, K and V, written as codes in 15 us and read
-// back in 11 (76 MB each, 5.1 and 6.9 TB/s, the codes' reading from L2); 64 rows 9 us
-// for both, two launches and their dependent reads.
+// go to different warps (together in one, with half the warps, both calls took 7% longer
+// on 8403 rows of 8 heads and 14% on 64).
+// Measured: 8403 rows of 8 heads of 128, K and V, written as codes in 14.5 us and read
+// back in 10.9 (52 MB each, 3.6 and 4.8 TB/s, the codes' reading from L2), copied as bf16 in
+// 12.3 (69 MB, 5.6 TB/s); 64 rows 3.0, 2.4 and 2.1 us, their dependent reads.  What
+// is left to the floor (15.4 us for codes both ways) is the lookup of each row's sequence,
+// position and page before its stores.
 #include <algorithm>
 #include "batch.cuh"
 

@@ -326,6 +326,47 @@ int32_t sub_kv8_append(const sub_bf16* K, int64_t ldk, const sub_bf16* V, int64_
 int32_t sub_kv8_read(const sub_kv8_cache* kv, int32_t layer, const sub_batch* batch, sub_bf16* K,
                      sub_bf16* V, void* stream);
 
+/* The rotation of position embeddings: pair i (elements i and i + head_dim / 2 of a
+ * head) turns by freqs[i] radians per position.  step[i] is that as a fraction of a whole
+ * turn in units of 2^-64, so that a position's angle is one whole-number product whose
+ * overflow drops the whole turns: exact at any position. */
+typedef struct {
+  uint64_t step[64];   /* [head_dim / 2] */
+  int32_t head_dim;
+} sub_rope;
+/* Fill *rope: freqs_host [head_dim / 2], each in [0, 1e6] radians, or NULL for
+ * theta^(-2 i / head_dim), theta in [1, 1e12]. */
+int32_t sub_rope_init(int32_t head_dim, double theta, const double* freqs_host, sub_rope* rope);
+
+/* sub_kv_append / sub_kv8_append with the rotation on the way: the batch's new rows K are
+ * turned to their positions and rounded (to bf16, or to codes: there the fp32 values are
+ * quantised), V is written as it is, and Q ([n_rows, Hq, head_dim] bf16, rows ldq
+ * elements apart), turned alike, goes to Q_out (rows ldo elements apart; rows of no
+ * sequence are left as they are).  Q_out may be Q itself and has nothing else in common with the
+ * inputs; n_heads_q = 0: no Q (NULL, NULL).  at [n_rows]: the position that a row is turned
+ * to, where it is not the one that it stands at (nodes of a tree: the depth counts); NULL: that
+ * one.  Any int32 is a position. */
+int32_t sub_kv_append_rope(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q, const sub_bf16* K,
+                           int64_t ldk, const sub_bf16* V, int64_t ldv, const sub_kv_cache* kv,
+                           int32_t layer, const sub_batch* batch, const sub_rope* rope,
+                           const int32_t* at, sub_bf16* Q_out, int64_t ldo, void* stream);
+int32_t sub_kv8_append_rope(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q, const sub_bf16* K,
+                            int64_t ldk, const sub_bf16* V, int64_t ldv, const sub_kv8_cache* kv,
+                            int32_t layer, const sub_batch* batch, const sub_rope* rope,
+                            const int32_t* at, sub_bf16* Q_out, int64_t ldo, void* stream);
+
+/* Move rows of K and V within their sequences, in all layers (the commit of a tree's
+ * accepted path, for a batch): the row at position from[b, i] goes to position to[b] + i, for
+ * i < count[b] (clamped to [0, n_max]).  All of a sequence's rows are read before any is
+ * written.  from [n_seqs, n_max], to and count [n_seqs] on the device; n_seqs rows of the page
+ * table; n_max <= SUB_MAX_MOVE.  Positions on no page are skipped, as source or as
+ * destination.  No sequence may read a place that another one writes, nor two write the same. */
+#define SUB_MAX_MOVE 128
+int32_t sub_kv_move(const sub_kv_cache* kv, int32_t n_seqs, const int32_t* to, const int32_t* from,
+                    int32_t n_max, const int32_t* count, void* stream);
+int32_t sub_kv8_move(const sub_kv8_cache* kv, int32_t n_seqs, const int32_t* to,
+                     const int32_t* from, int32_t n_max, const int32_t* count, void* stream);
+
 /* Attention of the batch's new rows over the paged cache, which already holds
  * their own K and V: row i of sequence b (Q [n_rows, Hq, head_dim] bf16, rows
  * ldq elements apart, a multiple of 8) reads the keys at positions
@@ -354,6 +395,52 @@ int32_t sub_chunk_attn8(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q,
  * sizes on the current device may need (0: none). */
 int32_t sub_chunk_attn_workspace(int32_t n_heads_q, int32_t n_heads_kv, int32_t head_dim,
                                  int32_t n_seqs, int32_t n_rows, int64_t* bytes);
+
+/* sub_chunk_attn / sub_chunk_attn8 for nodes of trees ("Low-Bit Shadow" report 6.3,
+ * SpecInfer, for a batch): row i of sequence b reads the key at position t <= pos[b] + i if
+ * t < base[b] (its committed tokens), or if bit t - base[b] of its mask is set (its path in
+ * the tree, itself included: nodes lie in slot order behind the committed tokens, parents
+ * before children).  base [n_seqs]; mask [n_rows, mask_words] int32, bit s % 32 of word
+ * s / 32 for slot s; slots past the words are not read; 1 <= mask_words <= SUB_MASK_WORDS.
+ * What the masks of other rows, or of no row, leave unread does not change a row's result.
+ * All else, the workspace and its size included, as there. */
+#define SUB_MASK_WORDS 64
+int32_t sub_chunk_tree_attn(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q,
+                            const sub_kv_cache* kv, int32_t layer, const sub_batch* batch,
+                            const int32_t* base, const int32_t* mask, int32_t mask_words,
+                            float softmax_scale, sub_bf16* O, void* workspace,
+                            int64_t workspace_bytes, void* stream);
+int32_t sub_chunk_tree_attn8(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q,
+                             const sub_kv8_cache* kv, int32_t layer, const sub_batch* batch,
+                             const int32_t* base, const int32_t* mask, int32_t mask_words,
+                             float softmax_scale, sub_bf16* O, void* workspace,
+                             int64_t workspace_bytes, void* stream);
+
+/* The best n_best continuations of each sequence's beams by one token (a level of a batch's
+ * draft trees: "Low-Bit Shadow" report 6.3/6.4; a step of a beam search).  Beam j of sequence
+ * b has score[b, j] and logits [b, j, V]; continuation (j, v) scores
+ *   score[b, j] + z_v / T - log sum_w exp(z_w / T).
+ * token, parent, score_out [n_seqs, n_best] get the best ones in falling order (ties: the
+ * smaller beam, then the larger logit, then the smaller token): token, beam, and the score
+ * rounded to fp32.  The order is decided in 64 bits, the sums of exp are fp32 terms.
+ * A beam whose score is not finite, or whose logits hold +infinity or nothing above
+ * -infinity, has no continuations; a logit of -infinity or NaN is none either.  Places
+ * that stay empty get token -1, parent -1, score -infinity.
+ * state [n_seqs, n_beams, state_words] int32 (NULL: none): state_out [n_seqs, n_best,
+ * state_words] gets the rows of the parents, reordered with them (zeros in empty places).
+ * slot >= 0: bit slot + r of the r-th row is set in it, as sub_chunk_tree_attn's masks have it
+ * (slot + n_best <= 32 * state_words); -1: none.
+ * 1 <= n_beams, n_best <= SUB_MAX_BEAMS; 1 <= V <= 2^20; temperature in [1e-6, 1e6]; any
+ * 4-byte aligned addresses; the outputs lie apart from the inputs and from each other.  workspace:
+ * sub_beam_workspace(...) bytes of device memory, 32-byte aligned, used by this call alone
+ * until it is done; NULL: drawn from the stream's memory pool. */
+#define SUB_MAX_BEAMS 64
+int32_t sub_beam_select(const float* logits, const float* score, int32_t n_seqs, int32_t n_beams,
+                        int64_t V, float temperature, int32_t n_best, const int32_t* state,
+                        int32_t state_words, int32_t slot, int32_t* token, int32_t* parent,
+                        float* score_out, int32_t* state_out, void* workspace,
+                        int64_t workspace_bytes, void* stream);
+int32_t sub_beam_workspace(int32_t n_seqs, int32_t n_beams, int64_t V, int64_t* bytes);
 
 /* probs[r, v] = exp(z[r, v] / T) / sum_w exp(z[r, w] / T) for fp32 logits z
  * [rows, V], sums in fp32; probs [rows, V] is the logits themselves or lies apart

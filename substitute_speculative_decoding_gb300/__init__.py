@@ -57,6 +57,11 @@ class Batch(C.Structure):
                 ("max_keys", _i64)]
 
 
+class Rope(C.Structure):
+    """sub_rope: the rotation of position embeddings."""
+    _fields_ = [("step", _u64 * 64), ("head_dim", _i32)]
+
+
 class Tree(C.Structure):
     _fields_ = [("token", _vp), ("parent", _vp), ("depth", _vp), ("score", _vp), ("anc", _vp),
                 ("width", _i32), ("max_depth", _i32)]
@@ -136,6 +141,21 @@ _chunk_attn8 = _decl("sub_chunk_attn8", [_vp, _i64, _i32, _KV8, _i32, _BATCH, _f
                                          _i64, _vp])
 _chunk_attn_workspace = _decl("sub_chunk_attn_workspace", [_i32, _i32, _i32, _i32, _i32,
                                                            C.POINTER(_i64)])
+_ROPE = C.POINTER(Rope)
+_rope_init = _decl("sub_rope_init", [_i32, C.c_double, C.POINTER(C.c_double), _ROPE])
+_kv_append_rope = _decl("sub_kv_append_rope", [_vp, _i64, _i32, _vp, _i64, _vp, _i64, _KV, _i32,
+                                               _BATCH, _ROPE, _vp, _vp, _i64, _vp])
+_kv8_append_rope = _decl("sub_kv8_append_rope", [_vp, _i64, _i32, _vp, _i64, _vp, _i64, _KV8, _i32,
+                                                 _BATCH, _ROPE, _vp, _vp, _i64, _vp])
+_kv_move = _decl("sub_kv_move", [_KV, _i32, _vp, _vp, _i32, _vp, _vp])
+_kv8_move = _decl("sub_kv8_move", [_KV8, _i32, _vp, _vp, _i32, _vp, _vp])
+_chunk_tree_attn = _decl("sub_chunk_tree_attn", [_vp, _i64, _i32, _KV, _i32, _BATCH, _vp, _vp, _i32,
+                                                 _f32, _vp, _vp, _i64, _vp])
+_chunk_tree_attn8 = _decl("sub_chunk_tree_attn8", [_vp, _i64, _i32, _KV8, _i32, _BATCH, _vp, _vp,
+                                                   _i32, _f32, _vp, _vp, _i64, _vp])
+_beam_select = _decl("sub_beam_select", [_vp, _vp, _i32, _i32, _i64, _f32, _i32, _vp, _i32, _i32,
+                                         _vp, _vp, _vp, _vp, _vp, _i64, _vp])
+_beam_workspace = _decl("sub_beam_workspace", [_i32, _i32, _i64, C.POINTER(_i64)])
 _probs = _decl("sub_probs", [_vp, _i64, _i64, _f32, _vp, _vp])
 _verify_sample = _decl("sub_verify_sample", [_vp, _vp, _vp, _vp, _i32, _i32, _i64, _vp, _vp, _vp])
 _model_create = _decl("sub_model_create", [C.POINTER(ModelDesc), C.POINTER(_vp)])
@@ -158,7 +178,10 @@ EXPORTED = ["sub_last_error", "sub_version", "sub_pipeline_timeouts", "sub_bound
             "sub_bf16_gemm", "sub_tree_attn", "sub_draft_expand", "sub_verify_accept",
             "sub_verify_accept_static",
             "sub_kv_compact", "sub_kv_append", "sub_kv8_append", "sub_kv8_read", "sub_chunk_attn",
-            "sub_chunk_attn8", "sub_chunk_attn_workspace", "sub_probs", "sub_verify_sample",
+            "sub_chunk_attn8", "sub_chunk_attn_workspace", "sub_rope_init",
+            "sub_kv_append_rope", "sub_kv8_append_rope", "sub_kv_move", "sub_kv8_move",
+            "sub_chunk_tree_attn", "sub_chunk_tree_attn8", "sub_beam_select", "sub_beam_workspace",
+            "sub_probs", "sub_verify_sample",
             "sub_model_create", "sub_model_destroy", "sub_model_memory",
             "sub_model_forward", "sub_model_kv", "sub_generate", "sub_prefill",
             "sub_decode_cycles", "sub_decode_read", "sub_cycle_info"]
@@ -487,6 +510,65 @@ def _append_rows(fn, k, v, kv, layer, batch, stream):
     _run(fn, dev, stream, k.data_ptr(), ldk, v.data_ptr(), ldv, kv, layer, batch)
 
 
+def rope(head_dim: int, theta: float = 10000.0, freqs=None) -> Rope:
+    """The rotation of position embeddings: pair (i, i + head_dim / 2) of a head turns by
+    freqs[i] radians per position (a sequence of head_dim / 2 numbers; without it
+    theta ** (-2 i / head_dim))."""
+    r = Rope()
+    f = None
+    if freqs is not None:
+        f = [float(x) for x in freqs]
+        if 2 * len(f) != head_dim:
+            _refuse("freqs: must be head_dim / 2 numbers")
+        f = (C.c_double * len(f))(*f)
+    _check(_rope_init(head_dim, theta, f, C.byref(r)))
+    return r
+
+
+def kv_append_rope(q, k, v, kv, layer: int, batch: Batch, rope: Rope, at=None, q_out=None,
+                   stream=None):
+    """Turn the batch's new rows q, k (bf16 [n_rows, heads, head_dim], rows may be strided)
+    to their positions and write k and v into one layer of a paged_kv or paged_kv8 cache
+    -> q turned.  at: int32 [n_rows], positions to turn to (None: where the rows stand;
+    nodes of a tree: by their depth).  q_out may be q; rows of no sequence are left as
+    they are in it, zero without.  q None: nothing but the cache is written."""
+    dev = _same(kv, batch)
+    n, h, d = batch.n_rows, kv.n_heads_kv, kv.head_dim
+    ldk, ldv = _rows(k, n, h, d, "k", dev), _rows(v, n, h, d, "v", dev)
+    qa = oa = None
+    hq = ldq = ldo = 0
+    if q is not None:
+        if q.dim() != 3:
+            _refuse("q: must be [n_rows, n_heads_q, head_dim]")
+        hq = q.shape[1]
+        ldq = _rows(q, n, hq, d, "q", dev)
+        if q_out is None:
+            q_out = _new((n, hq, d), torch.bfloat16, dev, stream, True)
+        ldo = _rows(q_out, n, hq, d, "q_out", dev)
+        qa, oa = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        _refuse("q_out without q")
+    _run(_kv8_append_rope if type(kv) is KV8Cache else _kv_append_rope, dev, stream, qa, ldq, hq,
+         k.data_ptr(), ldk, v.data_ptr(), ldv, kv, layer, batch, rope,
+         None if at is None else _dense(at, torch.int32, (n,), "at", dev), oa, ldo)
+    return q_out
+
+
+def kv_move(kv, to, src, count, stream=None):
+    """Move rows of a paged_kv or paged_kv8 cache within their sequences, in all layers: the
+    row at position src[b, i] goes to position to[b] + i, for i < count[b] (int32 [n_seqs,
+    n_max], [n_seqs], [n_seqs]; n_max <= 128).  All are read before any is written."""
+    dev = _gpu(src, "src")
+    if kv.device != dev and kv.device is not None:
+        _refuse("src and the cache must be on one device")
+    if src.dim() != 2 or src.shape[0] != kv.n_seqs:
+        _refuse("src: must be [n_seqs, n_max]")
+    n, most = src.shape
+    _run(_kv8_move if type(kv) is KV8Cache else _kv_move, dev, stream, kv, n,
+         _dense(to, torch.int32, (n,), "to", dev), _dense(src, torch.int32, (n, most), "src", dev),
+         most, _dense(count, torch.int32, (n,), "count", dev))
+
+
 def kv8_read(kv: KV8Cache, layer: int, batch: Batch, out=None, stream=None):
     """The values at the batch's positions -> (k, v) bf16 [n_rows, n_heads_kv,
     head_dim].  Rows of no sequence are left as they are in `out`, zero without."""
@@ -527,6 +609,11 @@ def chunk_attn(q, kv, layer: int, batch: Batch, scale=None, out=None, workspace=
     their own keys already -> bf16 [n_rows, n_heads_q, head_dim].  Rows of no
     sequence are left as they are in `out`, zero without.  workspace: a uint8
     tensor of chunk_attn_workspace bytes; allocated by torch if not given."""
+    return _attend(_chunk_attn8 if type(kv) is KV8Cache else _chunk_attn, q, kv, layer, batch, (),
+                   scale, out, workspace, stream)
+
+
+def _attend(fn, q, kv, layer, batch, extra, scale, out, workspace, stream):
     dev = _same(kv, batch)
     if q.dim() != 3:
         _refuse("q: must be [n_rows, n_heads_q, head_dim]")
@@ -541,10 +628,75 @@ def chunk_attn(q, kv, layer: int, batch: Batch, scale=None, out=None, workspace=
     else:
         size = workspace.numel()
         _dense(workspace, torch.uint8, workspace.shape, "workspace", dev)
-    _run(_chunk_attn8 if type(kv) is KV8Cache else _chunk_attn, dev, stream, q.data_ptr(), ldq, hq,
-         kv, layer, batch, d ** -0.5 if scale is None else scale, at,
-         workspace.data_ptr() or None, size)
+    _run(fn, dev, stream, q.data_ptr(), ldq, hq, kv, layer, batch, *extra,
+         d ** -0.5 if scale is None else scale, at, workspace.data_ptr() or None, size)
     return out
+
+
+def chunk_tree_attn(q, kv, layer: int, batch: Batch, base, mask, scale=None, out=None,
+                    workspace=None, stream=None):
+    """chunk_attn for nodes of trees: row i of sequence b reads the keys up to its own
+    position that are committed (before base[b], int32 [n_seqs]) or whose slot, counted from
+    base[b], is set in its mask (int32 [n_rows, words], bit s % 32 of word s / 32: its path,
+    itself included)."""
+    dev = _same(kv, batch)
+    if mask.dim() != 2:
+        _refuse("mask: must be [n_rows, words]")
+    words = mask.shape[1]
+    extra = (_dense(base, torch.int32, (batch.n_seqs,), "base", dev),
+             _dense(mask, torch.int32, (batch.n_rows, words), "mask", dev), words)
+    return _attend(_chunk_tree_attn8 if type(kv) is KV8Cache else _chunk_tree_attn, q, kv, layer,
+                   batch, extra, scale, out, workspace, stream)
+
+
+def beam_workspace(n_seqs: int, n_beams: int, vocab: int) -> int:
+    """Bytes of workspace that a beam_select call of these sizes needs."""
+    n = _i64()
+    _check(_beam_workspace(n_seqs, n_beams, vocab, C.byref(n)))
+    return n.value
+
+
+def beam_select(logits, score, n_best: int, temperature: float = 1.0, state=None, slot: int = -1,
+                out=None, workspace=None, stream=None):
+    """The best continuations of each sequence's beams by one token: logits fp32 [n_seqs,
+    n_beams, V], score fp32 [n_seqs, n_beams] (-inf: no beam) -> (token, parent int32, score
+    fp32 [n_seqs, n_best]) in falling order of score + log_softmax(logits / temperature); -1,
+    -1, -inf where there are fewer.  With state (int32 [n_seqs, n_beams, words]) also the
+    parents' states [n_seqs, n_best, words]; slot >= 0 sets bit slot + r in the r-th of them
+    (chunk_tree_attn's masks of a tree's next level)."""
+    dev = _gpu(logits, "logits")
+    if logits.dim() != 3:
+        _refuse("logits: must be [n_seqs, n_beams, V]")
+    b, n, v = logits.shape
+    words = 0
+    if state is not None:
+        if state.dim() != 3:
+            _refuse("state: must be [n_seqs, n_beams, words]")
+        words = state.shape[2]
+    kinds = (torch.int32, torch.int32, torch.float32) + (torch.int32,) * (state is not None)
+    shapes = ((b, n_best),) * 3 + ((b, n_best, words),) * (state is not None)
+    if out is None:
+        if n_best < 1:
+            _refuse("n_best must be at least 1")
+        out = tuple(_new(s, t, dev, stream, False) for s, t in zip(shapes, kinds))
+    if len(out) != len(kinds):
+        _refuse("out: must be token, parent, score and, with state, the new states")
+    at = [_dense(x, t, s, f"out[{i}]", dev) for i, (x, s, t) in enumerate(zip(out, shapes, kinds))]
+    size = _beam_bytes(b, n, v)
+    if workspace is None:
+        workspace = _new(size, torch.uint8, dev, stream, False)
+    else:
+        size = workspace.numel()
+        _dense(workspace, torch.uint8, workspace.shape, "workspace", dev)
+    _run(_beam_select, dev, stream, _dense(logits, torch.float32, (b, n, v), "logits", dev),
+         _dense(score, torch.float32, (b, n), "score", dev), b, n, v, temperature, n_best,
+         None if state is None else _dense(state, torch.int32, (b, n, words), "state", dev), words,
+         slot, at[0], at[1], at[2], at[3] if state is not None else None,
+         workspace.data_ptr() or None, size)
+    return tuple(out)
+
+
+_beam_bytes = functools.lru_cache(maxsize=4096)(beam_workspace)
 
 
 def probs(logits, temperature: float = 1.0, out=None, stream=None):

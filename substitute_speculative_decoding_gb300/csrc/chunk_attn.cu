@@ -129,7 +129,7 @@ __device__ __forceinline__ void bar_arrive(int id) {
 }
 
 // ------------------------------------------------------------------ kernel --
-template <int D, bool Q8, int RT>
+template <int D, bool Q8, int RT, bool TREE>
 __global__ void __launch_bounds__(NT, 1)
 chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__ ChunkArgs a) {
   using R = Ring<D, Q8>;
@@ -277,10 +277,13 @@ chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__
     uint32_t qf[KS][TURNED ? 2 : 4];
     float qs[2];    // factor of the row's scores
     int lim[2];     // keys 0 .. lim are read
+    const uint32_t* mask[2];   // TREE: those behind the committed ones as it says
+    const int base = TREE ? tree_base(a, u.b) : 0;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int q = a.by_group.quot(u.tile * RT + tile_row(h));
       lim[h] = q < u.rows ? last_key(u.pos, q, u.n_keys) : -1;
+      if constexpr (TREE) mask[h] = a.mask + (int64_t)(u.row0 + min(q, u.rows - 1)) * a.words;
       qs[h] = a.sl2;
     }
 #pragma unroll
@@ -339,7 +342,7 @@ chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__
       qs[0] = __shfl_sync(~0u, mine, 8 * tig);
       qs[1] = __shfl_sync(~0u, mine, 8 * tig + 4);
     }
-    const int lim_min = last_key(u.pos, a.by_group.quot(u.tile * RT), u.n_keys);   // of the tile's first row
+    const int lim_min = plan.template common<TREE>(u);
     // largest value over the lanes that share their rows
     auto row_max = [](float x) {
 #pragma unroll
@@ -445,13 +448,16 @@ chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__
         lv[0] = lv[1] = shift(vmax);
       }
       if (edge) {
+        uint32_t seen[2];   // the block's keys that the rows' masks leave
+#pragma unroll
+        for (int h = 0; h < 2; ++h) seen[h] = TREE ? mask_window(mask[h], a.words, key0 - base) : ~0u;
 #pragma unroll
         for (int t = 0; t < TILES; ++t)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int x = block_key(t, key_of(e));
             const bool gone = (miss >> (TURNED ? t : t >> 1)) & 1u;
-            if (gone || key0 + x > lim[row_of(e)]) s[t][e] = -INFINITY;
+            if (gone || key0 + x > lim[row_of(e)] || !((seen[row_of(e)] >> x) & 1u)) s[t][e] = -INFINITY;
           }
         if constexpr (Q8) {   // the scales of keys that a row does not read may be anything
           float vmax[2] = {0.f, 0.f};
@@ -846,19 +852,27 @@ int32_t launch_join(const ChunkArgs& a, int n_ctas, cudaStream_t st) {
   return SUB_OK;
 }
 
-template <int D, bool Q8, int RT>
+template <int D, bool Q8, int RT, bool TREE>
 int32_t launch_decode(const ChunkArgs& a, int n_ctas, cudaStream_t st) {
   constexpr int SMEM = decode_smem<D, Q8>();
   SUB_CUDA_TRY(once_per_device([] {
-    return cudaFuncSetAttribute(chunk_attn_kernel<D, Q8, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                SMEM);
+    return cudaFuncSetAttribute(chunk_attn_kernel<D, Q8, RT, TREE>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   }));
   PageMaps maps;
   if (!chunk_page_map(&maps.k, a.k, a.t, (int64_t)a.n_layers * a.n_heads_kv, D, Q8) ||
       !chunk_page_map(&maps.v, a.v, a.t, (int64_t)a.n_layers * a.n_heads_kv, D, Q8))
     return fail(SUB_ECUDA, "chunk_attn: the cache's tensor map was refused");
-  SUB_CUDA_TRY(launch_k(chunk_attn_kernel<D, Q8, RT>, dim3(n_ctas), dim3(NT), SMEM, st, maps, a));
+  SUB_CUDA_TRY(launch_k(chunk_attn_kernel<D, Q8, RT, TREE>, dim3(n_ctas), dim3(NT), SMEM, st, maps, a));
   return launch_join<D, RT>(a, n_ctas, st);
+}
+template <bool Q8, bool TREE>
+int32_t launch_rows(const ChunkArgs& a, int d, int rt, int n_ctas, cudaStream_t st) {
+  if (rt == NARROW)
+    return d == 128 ? launch_decode<128, Q8, NARROW, TREE>(a, n_ctas, st)
+                    : launch_decode<64, Q8, NARROW, TREE>(a, n_ctas, st);
+  return d == 128 ? launch_decode<128, Q8, WIDE, TREE>(a, n_ctas, st)
+                  : launch_decode<64, Q8, WIDE, TREE>(a, n_ctas, st);
 }
 
 // Rows of a tile, by the rows that a sequence has on average (rows and sequences are
@@ -889,9 +903,8 @@ template <class Cache>
 int32_t chunk_attn(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q, const Cache* kv,
                    const float* ks, const float* vs, int32_t layer, const sub_batch* batch,
                    float softmax_scale, sub_bf16* O, void* workspace, int64_t workspace_bytes,
-                   void* stream) {
+                   void* stream, ChunkArgs a = ChunkArgs{}) {
   constexpr bool Q8 = std::is_same<Cache, sub_kv8_cache>::value;
-  ChunkArgs a{};
   SUB_TRY(make_seq_table(kv, layer, batch, &a.t));
   SUB_CHECK_ARG(n_heads_q >= 1 && n_heads_q % kv->n_heads_kv == 0 &&
                     n_heads_q / kv->n_heads_kv <= 64,
@@ -942,11 +955,20 @@ int32_t chunk_attn(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q, const Cach
     return kv->head_dim == 128 ? launch_join<128, CHUNK_TC_ROWS>(a, n_ctas, st)
                                : launch_join<64, CHUNK_TC_ROWS>(a, n_ctas, st);
   }
-  if (rt == NARROW)
-    return kv->head_dim == 128 ? launch_decode<128, Q8, NARROW>(a, n_ctas, st)
-                               : launch_decode<64, Q8, NARROW>(a, n_ctas, st);
-  return kv->head_dim == 128 ? launch_decode<128, Q8, WIDE>(a, n_ctas, st)
-                             : launch_decode<64, Q8, WIDE>(a, n_ctas, st);
+  return a.mask ? launch_rows<Q8, true>(a, kv->head_dim, rt, n_ctas, st)
+                : launch_rows<Q8, false>(a, kv->head_dim, rt, n_ctas, st);
+}
+
+int32_t tree_args(const int32_t* base, const int32_t* mask, int32_t words, const sub_batch* batch,
+                  ChunkArgs* a) {
+  SUB_CHECK_ARG(batch && base && (mask || batch->n_rows == 0), "null pointer");
+  SUB_CHECK_ARG(words >= 1 && words <= SUB_MASK_WORDS, "mask_words must be in [1, SUB_MASK_WORDS]");
+  SUB_CHECK_ARG(((reinterpret_cast<uintptr_t>(base) | reinterpret_cast<uintptr_t>(mask)) & 3) == 0,
+                "base and mask must be 4-byte aligned");
+  a->base = base;
+  a->mask = reinterpret_cast<const uint32_t*>(mask);
+  a->words = words;
+  return SUB_OK;
 }
 
 }  // namespace
@@ -990,4 +1012,27 @@ extern "C" int32_t sub_chunk_attn8(const sub_bf16* Q, int64_t ldq, int32_t n_hea
   SUB_TRY(check_scales(kv));
   return chunk_attn(Q, ldq, n_heads_q, kv, kv->k_scale, kv->v_scale, layer, batch, softmax_scale,
                     O, workspace, workspace_bytes, stream);
+}
+
+extern "C" int32_t sub_chunk_tree_attn(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q,
+                                       const sub_kv_cache* kv, int32_t layer, const sub_batch* batch,
+                                       const int32_t* base, const int32_t* mask, int32_t mask_words,
+                                       float softmax_scale, sub_bf16* O, void* workspace,
+                                       int64_t workspace_bytes, void* stream) {
+  ChunkArgs a{};
+  SUB_TRY(tree_args(base, mask, mask_words, batch, &a));
+  return chunk_attn(Q, ldq, n_heads_q, kv, nullptr, nullptr, layer, batch, softmax_scale, O,
+                    workspace, workspace_bytes, stream, a);
+}
+
+extern "C" int32_t sub_chunk_tree_attn8(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q,
+                                        const sub_kv8_cache* kv, int32_t layer, const sub_batch* batch,
+                                        const int32_t* base, const int32_t* mask, int32_t mask_words,
+                                        float softmax_scale, sub_bf16* O, void* workspace,
+                                        int64_t workspace_bytes, void* stream) {
+  ChunkArgs a{};
+  SUB_TRY(tree_args(base, mask, mask_words, batch, &a));
+  SUB_TRY(check_scales(kv));
+  return chunk_attn(Q, ldq, n_heads_q, kv, kv->k_scale, kv->v_scale, layer, batch, softmax_scale,
+                    O, workspace, workspace_bytes, stream, a);
 }

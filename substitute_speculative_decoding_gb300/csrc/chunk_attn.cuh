@@ -38,6 +38,11 @@ struct ChunkArgs {
   float* part_o;         // [2 n_ctas][rows][D], relative to the maxima of
   float2* part_ml;       // [2 n_ctas][rows] (largest score, sum)
   struct ChunkCut* cuts; // [n_ctas]
+  // nodes of trees (null: none): keys before base[b] are read by all rows up to their own
+  // position, those from it on by the rows in whose mask their bit is set
+  const int32_t* base;   // [n_seqs]
+  const uint32_t* mask;  // [n_rows][words]
+  int words;
 };
 
 // The unit of work (below) that is cut first at the end of a CTA's part, for the
@@ -95,6 +100,17 @@ __device__ __forceinline__ int last_key(int pos, int q, int n_keys) {
   return (int)min((int64_t)pos + q, (int64_t)n_keys - 1);
 }
 
+// First position behind the committed keys of sequence b.  (Whatever base holds, slots
+// counted from it fit 32 bits; below -4096 all of them lie past any mask.)
+__device__ __forceinline__ int tree_base(const ChunkArgs& a, int b) { return max(a.base[b], -4096); }
+// Bits of the 32 keys from slot `at` on in a row's mask: the committed keys before slot 0
+// are set, none are past its words.  (Through L2: the kernel just before may have written it.)
+__device__ __forceinline__ uint32_t mask_window(const uint32_t* mask, int words, int at) {
+  auto word = [&](int i) { return i < 0 ? ~0u : i < words ? __ldcg(mask + i) : 0u; };
+  const int i = at >> 5;
+  return __funnelshift_r(word(i), at & 31 ? word(i + 1) : 0u, at & 31);
+}
+
 // ---------------------------------------------------------------- work plan --
 // A unit of work is one tile of RT rows -- (row, head in group) pairs of one
 // KV head of one sequence -- over all the keys its last row reads, in blocks of
@@ -130,6 +146,12 @@ struct ChunkPlan {
     u.row0 = seq_first(a.t, u.b);
     u.rows = seq_rows(a.t, u.b);
     u.pos = a.t.pos[u.b];
+  }
+  // last key that all rows of the tile read
+  template <bool TREE>
+  __device__ int common(const ChunkUnit& u) const {
+    const int last = last_key(u.pos, a.by_group.quot(u.tile * RT), u.n_keys);
+    return TREE ? min(last, tree_base(a, u.b) - 1) : last;
   }
   __device__ void measure(ChunkUnit& u) const {
     u.n_keys = keys(u.pos, u.rows, u.tile);
@@ -238,7 +260,7 @@ __device__ __forceinline__ ChunkCut make_cut(const ChunkUnit& u, int kb1, int64_
 }
 
 // The kernel for many rows per sequence (chunk_attn_tc.cu): its tiles, and the
-// fewest blocks a CTA takes.
+// fewest blocks a CTA takes.  (Trees: a.mask.)
 constexpr int CHUNK_TC_ROWS = 256, CHUNK_TC_KEYS = 128, CHUNK_TC_LEAST = 2;
 bool chunk_tc_fits(int64_t pool_rows);   // rows of head_dim values in a pool
 int32_t launch_chunk_tc(const ChunkArgs& a, bool q8, int head_dim, int64_t pool_rows, int n_ctas,

@@ -258,7 +258,7 @@ __device__ __forceinline__ void st_global32(void* p, const uint32_t* r) {
 }
 
 // ------------------------------------------------------------------ kernel --
-template <int D, bool Q8>
+template <int D, bool Q8, bool TREE>
 __global__ void __launch_bounds__(Cfg<D, Q8>::THREADS, 1)
 chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ChunkArgs a, const int box,
                 const int pool_rows) {
@@ -436,7 +436,11 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
       const bool real = q < u.rows;
       const int n_keys = u.n_keys;
       const int lim = real ? last_key(u.pos, q, n_keys) : -1;                         // keys 0 .. lim are read
-      const int lim_first = last_key(u.pos, a.by_group.quot(u.tile * RT), n_keys);    // by every row of the tile
+      const int lim_first = plan.template common<TREE>(u);                            // by every row of the tile
+      // TREE: the keys behind the committed ones that the row reads
+      const int base = TREE ? tree_base(a, u.b) : 0;
+      const uint32_t* const mask = TREE ? a.mask + (int64_t)(u.row0 + min(q, u.rows - 1)) * a.words : nullptr;
+      auto seen = [&](int key) { return TREE ? mask_window(mask, a.words, key - base) : ~0u; };   // of 32 keys
       float factor = a.sl2;        // of the row's scores, to base 2
       if constexpr (Q8) factor = s_qs[t * GROUP_ROWS + r];
 
@@ -490,7 +494,7 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
             __syncwarp();
             tc_ld32(tS + x0, s);
             wait_ld();
-            const uint32_t gone = miss >> miss_bit<Q8>(x0 >> 4);
+            const uint32_t gone = miss >> miss_bit<Q8>(x0 >> 4), read = seen(key0 + x0);
             const int end = last - x0;
 #pragma unroll
             for (int x = 0; x < 32; x += 4) {
@@ -499,7 +503,7 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
               const float kk[4] = {k4.x, k4.y, k4.z, k4.w}, vv[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const bool unread = x + i > end;
+                const bool unread = x + i > end || !((read >> (x + i)) & 1u);
                 s[x + i] = unread ? -INFINITY : s[x + i] * kk[i];
                 vmax4[i] = fmaxf(vmax4[i], unread ? 0.f : vv[i]);   // (0 where there is no page)
               }
@@ -557,6 +561,15 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
 #pragma unroll
             for (int x = 0; x < KB; ++x)
               if (x > last || ((miss >> miss_bit<Q8>(x >> 4)) & 1u)) s[x] = -INFINITY;
+            if (TREE && behind) {
+#pragma unroll
+              for (int x0 = 0; x0 < KB; x0 += 32) {
+                const uint32_t read = seen(key0 + x0);
+#pragma unroll
+                for (int x = 0; x < 32; ++x)
+                  if (!((read >> x) & 1u)) s[x0 + x] = -INFINITY;
+              }
+            }
           }
           // eight chains: a single one would wait for itself 128 times
           float top8[8];
@@ -683,7 +696,7 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
           const int from = max(kb0, max(0, lim_first + 1) / KB) * KB;
           for (int key = from; key <= min(lim, kb1 * KB - 1); ++key) {
             const int page = page_of(a.t, done.b, key);
-            if (page < 0) continue;
+            if (page < 0 || !(seen(key) & 1u)) continue;
             const uint16_t* const x =
                 vp + pool_row(a.t, a.layer, a.n_heads_kv, page, done.head,
                               (int)((uint32_t)key % (uint32_t)a.t.page_size)) * D + x0;
@@ -800,7 +813,7 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
       auto look_up = [&](uint32_t j) {   // called for j = 0, 1, ..
         if (j >= n) return;
         if (j > 0) step();
-        const bool behind = kb * KB + KB - 1 > last_key(u.pos, a.by_group.quot(u.tile * RT), u.n_keys);
+        const bool behind = kb * KB + KB - 1 > plan.template common<TREE>(u);
         bare = (bare & ~(1u << (j & 31))) | (uint32_t)behind << (j & 31);
         int row[KEYS];
 #pragma unroll
@@ -826,7 +839,7 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
         for (int h = 0; h < KEYS; ++h) {
           // a row that reads a key whose scale of V is not finite gets NaN by its
           // score; weight 0 times it stays 0
-          const bool fine = vsc[h] < INFINITY;
+          const bool fine = fabsf(vsc[h]) < INFINITY;
           sc[x0 + 32 * h] = fine ? ksc[h] : __int_as_float(0x7fc00000);
           sc[KB + x0 + 32 * h] = fine ? vsc[h] : 1.f;
           kx = fmaxf(kx, ksc[h] < INFINITY ? ksc[h] : 0.f);
@@ -984,12 +997,12 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
 }
 
 // -------------------------------------------------------------------- host --
-template <int D, bool Q8>
+template <int D, bool Q8, bool TREE>
 int32_t launch(const ChunkArgs& a, int64_t rows, int n_ctas, cudaStream_t st) {
   using C = Cfg<D, Q8>;
   SUB_CUDA_TRY(once_per_device([] {
-    return cudaFuncSetAttribute(chunk_tc_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                C::SMEM);
+    return cudaFuncSetAttribute(chunk_tc_kernel<D, Q8, TREE>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   }));
   Maps maps;
   memset(&maps, 0, sizeof(maps));
@@ -1000,7 +1013,7 @@ int32_t launch(const ChunkArgs& a, int64_t rows, int n_ctas, cudaStream_t st) {
   };
   if (!Q8 && (!pool_map(&maps.k, a.k) || !pool_map(&maps.v, a.v)))
     return fail(SUB_ECUDA, "chunk_attn: the cache's tensor map was refused");
-  SUB_CUDA_TRY(launch_k(chunk_tc_kernel<D, Q8>, dim3(n_ctas), dim3(C::THREADS), C::SMEM, st, maps, a,
+  SUB_CUDA_TRY(launch_k(chunk_tc_kernel<D, Q8, TREE>, dim3(n_ctas), dim3(C::THREADS), C::SMEM, st, maps, a,
                         box, (int)rows));
   return SUB_OK;
 }
@@ -1024,10 +1037,11 @@ bool chunk_tc_fits(int64_t pool_rows) { return pool_rows < (1ll << 31) - 4096; }
 
 int32_t launch_chunk_tc(const ChunkArgs& a, bool q8, int head_dim, int64_t pool_rows, int n_ctas,
                         cudaStream_t st) {
-  if (q8) return head_dim == 128 ? launch<128, true>(a, pool_rows, n_ctas, st)
-                                 : launch<64, true>(a, pool_rows, n_ctas, st);
-  return head_dim == 128 ? launch<128, false>(a, pool_rows, n_ctas, st)
-                         : launch<64, false>(a, pool_rows, n_ctas, st);
+  auto k = a.mask ? (q8 ? (head_dim == 128 ? launch<128, true, true> : launch<64, true, true>)
+                        : (head_dim == 128 ? launch<128, false, true> : launch<64, false, true>))
+                  : (q8 ? (head_dim == 128 ? launch<128, true, false> : launch<64, true, false>)
+                        : (head_dim == 128 ? launch<128, false, false> : launch<64, false, false>));
+  return k(a, pool_rows, n_ctas, st);
 }
 
 int32_t chunk_tc_timeouts(unsigned int* out) {

@@ -1,0 +1,115 @@
+// Rows of a paged cache moved within their sequences, in all layers: the commit of
+// the accepted paths of a batch's draft trees ("SubSpec: Using the Target Model's Own
+// Low-Bit Shadow as Its Draft Model", 4.1 point 2 and 6.3).
+//
+// Memory bound, or at a few rows bound by the chain count -> position -> page ->
+// row of dependent reads, so a CTA takes one side of one layer of a sequence and
+// looks its rows' places up once for all heads.  In place: a destination may be
+// a later row's source, so all rows of a head are in registers before the first
+// of them is written (8 chunks of 16 bytes for each of 256 threads hold
+// SUB_MAX_MOVE rows of 256 bytes); several heads at a time where the rows are fewer.
+#include "batch.cuh"
+
+namespace sub {
+namespace {
+
+constexpr int MOVE_THREADS = 256, MOVE_CHUNKS = 8;
+
+struct MoveArgs {
+  SeqTable t;               // start, pos: none
+  int n_heads_kv, n_max;
+  const int32_t *to, *from, *count;
+  void* pool[2];
+  float* scale[2];
+};
+
+// LANES: 16-byte chunks of a row
+template <int LANES, bool Q8>
+__global__ void __launch_bounds__(MOVE_THREADS) move_kernel(const __grid_constant__ MoveArgs a) {
+  static_assert(SUB_MAX_MOVE * LANES <= MOVE_THREADS * MOVE_CHUNKS, "a head's rows fit the registers");
+  __shared__ int64_t s_from[SUB_MAX_MOVE], s_to[SUB_MAX_MOVE];   // rows of the pool, of head 0; -1: not moved
+  pdl_wait();
+  pdl_trigger();
+  const int b = blockIdx.x, layer = blockIdx.y, side = blockIdx.z, tid = threadIdx.x;
+  const int n = min(max(__ldcg(a.count + b), 0), a.n_max);
+  if (n == 0) return;
+  if (tid < n) {
+    const int64_t x = __ldcg(a.from + (int64_t)b * a.n_max + tid), y = (int64_t)__ldcg(a.to + b) + tid;
+    const int px = page_of(a.t, b, x), py = page_of(a.t, b, y);
+    const bool ok = px >= 0 && py >= 0;
+    const uint32_t ps = a.t.page_size;
+    s_from[tid] = ok ? pool_row(a.t, layer, a.n_heads_kv, px, 0, (int)((uint32_t)x % ps)) : -1;
+    s_to[tid] = ok ? pool_row(a.t, layer, a.n_heads_kv, py, 0, (int)((uint32_t)y % ps)) : -1;
+  }
+  __syncthreads();
+  uint4* const pool = reinterpret_cast<uint4*>(a.pool[side]);
+  const int per_head = n * LANES, ps = a.t.page_size;
+  const int together = MOVE_THREADS * MOVE_CHUNKS / per_head;   // heads
+  for (int h0 = 0; h0 < a.n_heads_kv; h0 += together) {
+    const int items = min(together, a.n_heads_kv - h0) * per_head;
+    uint4 w[MOVE_CHUNKS];
+    float sc[MOVE_CHUNKS];
+    auto each = [&](auto f) {
+#pragma unroll
+      for (int k = 0; k < MOVE_CHUNKS; ++k) {
+        const int i = k * MOVE_THREADS + tid;
+        if (i >= items) break;
+        const int h = i / per_head, r = (i - h * per_head) / LANES, c = i % LANES;
+        if (s_from[r] >= 0) f(k, r, (int64_t)(h0 + h) * ps, c);
+      }
+    };
+    each([&](int k, int r, int64_t head, int c) {
+      w[k] = __ldcg(pool + (s_from[r] + head) * LANES + c);
+      if (Q8 && c == 0) sc[k] = __ldcg(a.scale[side] + s_from[r] + head);
+    });
+    __syncthreads();
+    each([&](int k, int r, int64_t head, int c) {
+      pool[(s_to[r] + head) * LANES + c] = w[k];
+      if (Q8 && c == 0) a.scale[side][s_to[r] + head] = sc[k];
+    });
+  }
+}
+
+template <class Cache>
+int32_t move(const Cache* kv, int32_t n_seqs, const int32_t* to, const int32_t* from, int32_t n_max,
+             const int32_t* count, MoveArgs a, bool q8, void* stream) {
+  SUB_CHECK_ARG(kv && kv->k && kv->v && kv->page_table, "null pointer");
+  // (no rows of a batch here: start and pos are not read)
+  const sub_batch none{kv->page_table, kv->page_table, n_seqs, 0, 0};
+  SUB_TRY(make_seq_table(kv, 0, &none, &a.t));
+  SUB_CHECK_ARG(kv->n_layers <= 65535, "n_layers out of range");
+  SUB_CHECK_ARG(n_max >= 0 && n_max <= SUB_MAX_MOVE, "n_max must be in [0, SUB_MAX_MOVE]");
+  if (n_max == 0) return SUB_OK;
+  SUB_CHECK_ARG(to && from && count, "null pointer");
+  a.t.start = a.t.pos = nullptr;
+  a.n_heads_kv = kv->n_heads_kv;
+  a.n_max = n_max;
+  a.to = to;
+  a.from = from;
+  a.count = count;
+  a.pool[0] = kv->k;
+  a.pool[1] = kv->v;
+  auto k = kv->head_dim == 128 ? (q8 ? move_kernel<8, true> : move_kernel<16, false>)
+                               : (q8 ? move_kernel<4, true> : move_kernel<8, false>);
+  SUB_CUDA_TRY(launch_k(k, dim3(n_seqs, kv->n_layers, 2), dim3(MOVE_THREADS), 0, as_stream(stream), a));
+  return SUB_OK;
+}
+
+}  // namespace
+}  // namespace sub
+
+using namespace sub;
+
+extern "C" int32_t sub_kv_move(const sub_kv_cache* kv, int32_t n_seqs, const int32_t* to, const int32_t* from,
+                               int32_t n_max, const int32_t* count, void* stream) {
+  return move(kv, n_seqs, to, from, n_max, count, MoveArgs{}, false, stream);
+}
+
+extern "C" int32_t sub_kv8_move(const sub_kv8_cache* kv, int32_t n_seqs, const int32_t* to,
+                                const int32_t* from, int32_t n_max, const int32_t* count, void* stream) {
+  SUB_TRY(check_scales(kv));
+  MoveArgs a{};
+  a.scale[0] = kv->k_scale;
+  a.scale[1] = kv->v_scale;
+  return move(kv, n_seqs, to, from, n_max, count, a, true, stream);
+}

@@ -21,7 +21,7 @@
 // is left to the floor (15.4 us for codes both ways) is the lookup of each row's sequence,
 // position and page before its stores.
 #include <algorithm>
-#include "batch.cuh"
+#include "kv_rows.cuh"
 
 namespace sub {
 namespace {
@@ -37,39 +37,6 @@ struct RowArgs {
   float* scale[2];
   uint16_t* dst[2];         // rows read back
 };
-
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
-// Row of this warp, its sequence and the page of its position.
-struct Place {
-  int row, page, at;
-  bool in_seq;
-};
-__device__ __forceinline__ Place find_place(const SeqTable& t, int row, int lane) {
-  Place p{row, -1, 0, false};
-  if (row >= t.n_rows) return p;
-  const int b = row_seq(t, row, lane);
-  if (b < 0) return p;
-  p.in_seq = true;
-  const int64_t x = (int64_t)t.pos[b] + (row - seq_first(t, b));
-  p.page = page_of(t, b, x);
-  p.at = p.page < 0 ? 0 : (int)((uint32_t)x % (uint32_t)t.page_size);
-  return p;
-}
-
-// 8 bf16 values in a uint4 to fp32.
-__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
-  const uint32_t r[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = bf16lo(r[i]);
-    x[2 * i + 1] = bf16hi(r[i]);
-  }
-}
 
 template <int D, bool Q8>
 __global__ void __launch_bounds__(ROW_WARPS * 32) append_kernel(RowArgs a) {
@@ -109,20 +76,11 @@ __global__ void __launch_bounds__(ROW_WARPS * 32) append_kernel(RowArgs a) {
         for (int i = 0; i < 8; ++i) big = max_nan(big, fabsf(x[i]));
 #pragma unroll
         for (int o = LANES / 2; o; o >>= 1) big = max_nan(big, __shfl_xor_sync(~0u, big, o));
-        float s = 1.f, t = 0.f;
-        if (!(big < INFINITY)) {
-          s = __int_as_float(0x7fc00000);   // NaN or infinity somewhere in the row
-        } else if (big >= 0x1p-100f) {
-          s = __fdiv_rn(big, 127.f);
-          t = __fdiv_rn(127.f, big);
-        }
-        uint32_t c[2] = {0, 0};
-#pragma unroll
-        for (int i = 0; i < 8; ++i)   // |x t| <= 127 (1 + 2^-22): the code needs no clamp
-          c[i >> 2] |= (uint32_t)(t == 0.f ? 128 : 128 + __float2int_rn(__fmul_rn(x[i], t)))
-                       << (8 * (i & 3));
+        float s, t;
+        row_scale(big, s, t);
+        const uint2 c = codes8(x, t);
         if (ok) {
-          *(reinterpret_cast<uint2*>(a.pool[side]) + r * LANES + l) = make_uint2(c[0], c[1]);
+          *(reinterpret_cast<uint2*>(a.pool[side]) + r * LANES + l) = c;
           if (l == 0) a.scale[side][r] = s;
         }
       }

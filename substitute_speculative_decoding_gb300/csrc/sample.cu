@@ -5,71 +5,13 @@
 // Both pass once over rows of V values.  A row belongs to one thread-block
 // cluster, so that a single row still streams through several SMs, and the
 // CTAs agree on the row's sums through distributed shared memory: one launch,
-// no scratch.  Rows are read in aligned groups of four values whatever V is:
-// a row that starts `mis` values past a 16-byte boundary has groups
-// [4 g - mis, 4 g - mis + 4), of which the first and last may be partial.
+// no scratch.
 #include <cmath>
 #include <type_traits>
-#include <cooperative_groups.h>
-#include "common.cuh"
+#include "rows.cuh"
 
 namespace sub {
 namespace {
-
-namespace cg = cooperative_groups;
-
-constexpr int MAX_CLUSTER = 8;        // the portable size
-constexpr int64_t MAX_V = 1 << 20;
-
-struct Row {
-  int64_t V;
-  int mis, n;               // groups
-  int inner, n_inner;       // whole ones: n_inner from `inner` on
-  __device__ Row(const float* z, int64_t v)
-      : V(v), mis((int)((reinterpret_cast<uintptr_t>(z) >> 2) & 3)) {
-    n = (int)((V + mis + 3) / 4);
-    inner = mis ? 1 : 0;
-    n_inner = max(0, n - ((V + mis) % 4 ? 1 : 0) - inner);
-  }
-  __device__ int64_t first(int g) const { return (int64_t)g * 4 - mis; }   // may be < 0 in group 0
-  __device__ bool whole(int g) const { return (unsigned)(g - inner) < (unsigned)n_inner; }
-};
-
-// Group g of row z, through L2 (the kernel just before may have written it); `none`
-// where the row has no value.
-template <bool VEC = true>
-__device__ __forceinline__ float4 load_group(const float* z, const Row& r, int g, float none) {
-  if (VEC && r.whole(g)) return __ldcg(reinterpret_cast<const float4*>(z - r.mis) + g);
-  const int64_t e = r.first(g);
-  float4 x;
-  x.x = e >= 0 && e < r.V ? __ldcg(z + e) : none;
-  x.y = e + 1 >= 0 && e + 1 < r.V ? __ldcg(z + e + 1) : none;
-  x.z = e + 2 >= 0 && e + 2 < r.V ? __ldcg(z + e + 2) : none;
-  x.w = e + 3 < r.V ? __ldcg(z + e + 3) : none;
-  return x;
-}
-
-// The CTAs of a cluster write into each other's shared memory once all of them
-// run: each says so at its start, and asks before its first write.
-__device__ __forceinline__ void cluster_here() {
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_all_here() {
-  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ float exp2_small(float x) {   // as exp2_fast, down to 2^-149
-  float r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-// A CTA's share of a row's groups.
-__device__ __forceinline__ void share(int groups, int rank, int size, int& lo, int& hi) {
-  const int per = (groups + size - 1) / size;
-  lo = min(groups, rank * per);
-  hi = min(groups, lo + per);
-}
 
 // ------------------------------------------------------------- softmax --
 // p = exp((z - m) / T) / sum, with m the largest logit.  Bound by HBM: 4 bytes
@@ -81,7 +23,7 @@ __device__ __forceinline__ void share(int groups, int rank, int size, int& lo, i
 // and sums in one cluster barrier.
 template <int THREADS, int MLP>   // MLP: groups a thread loads in one round
 __global__ void __launch_bounds__(THREADS, 1280 / THREADS)
-probs_kernel(const float* logits, int64_t V, float c_hi, float c_lo, float* probs) {
+probs_kernel(const float* logits, int64_t V, Sharpen sharp, float* probs) {
   constexpr int WARPS = THREADS / 32;
   __shared__ float2 s_warp[WARPS];
   __shared__ float2 s_peer[MAX_CLUSTER];   // each CTA's (largest logit, sum), written by it
@@ -96,22 +38,9 @@ probs_kernel(const float* logits, int64_t V, float c_hi, float c_lo, float* prob
   const Row r(z, V);
   int lo, hi;
   share(r.n, rank, size, lo, hi);
-  // exp(d / T) = 2^(d c), c = log2(e) / T in two parts: one rounding of d c.  (Both
-  // are positive, so that d = -infinity gives 0.)
-  auto expo = [&](float d) { return exp2_fast(fmaf(d, c_hi, d * c_lo)); };
-  const float2 hi2 = make_float2(c_hi, c_hi), lo2 = make_float2(c_lo, c_lo);
-  auto exponents = [&](const float4& x, float minus) {   // of x + minus, two at a time
-    const float2 r2 = make_float2(minus, minus);
-    const float2 a = add2(make_float2(x.x, x.y), r2), b = add2(make_float2(x.z, x.w), r2);
-    const float2 ea = fma2(a, hi2, mul2(a, lo2)), eb = fma2(b, hi2, mul2(b, lo2));
-    return make_float4(ea.x, ea.y, eb.x, eb.y);
-  };
-  auto merge = [&](float& m, float& s, float m2, float s2) {   // sums relative to their maxima
-    const float big = fmaxf(m, m2);
-    if (m2 == -INFINITY && s2 == 0.f) return;
-    s = (m == -INFINITY && s == 0.f ? 0.f : s * expo(m - big)) + s2 * expo(m2 - big);
-    m = big;
-  };
+  auto expo = [&](float d) { return sharp.expo(d); };
+  auto exponents = [&](const float4& x, float minus) { return sharp.exponents(x, minus); };
+  auto merge = [&](float& m, float& s, float m2, float s2) { sharp.merge(m, s, m2, s2); };
   float m = -INFINITY, s = 0.f;
   float4 x[MLP];
   for (int g0 = lo + threadIdx.x; g0 < hi; g0 += MLP * THREADS) {
@@ -385,32 +314,6 @@ __global__ void __launch_bounds__(VER_THREADS, 4) verify_kernel(VerifyArgs a) {
   }
 }
 
-template <typename... KArgs, typename... Args>
-cudaError_t launch_clusters(void (*kern)(KArgs...), int64_t rows, int size, int threads,
-                            cudaStream_t st, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(rows * size));
-  cfg.blockDim = dim3(threads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = size;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
-}
-
-// Whether a and b, of that many values of 4 bytes, have any in common (none at NULL).
-bool overlap(const void* a, __int128 n_a, const void* b, __int128 n_b) {
-  const __int128 x = (__int128)reinterpret_cast<uintptr_t>(a), y = (__int128)reinterpret_cast<uintptr_t>(b);
-  return a && b && x < y + 4 * n_b && y < x + 4 * n_a;
-}
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
-
 }  // namespace
 }  // namespace sub
 
@@ -427,22 +330,19 @@ extern "C" int32_t sub_probs(const float* logits, int64_t rows, int64_t V, float
   SUB_CHECK_ARG(aligned4(logits) && aligned4(probs), "logits and probs must be 4-byte aligned");
   SUB_CHECK_ARG(probs == logits || !overlap(logits, rows * V, probs, rows * V),
                 "probs must be the logits or lie apart from them");
-  const double c = 1.4426950408889634074 / (double)temperature;
-  float c_hi = (float)c;
-  if ((double)c_hi >= c) c_hi = std::nextafterf(c_hi, 0.f);
-  const float c_lo = (float)(c - (double)c_hi);
+  const Sharpen sharp = make_sharpen(temperature);
   const cudaStream_t st = as_stream(stream);
   // A round of a CTA's loads takes 16 values per thread.  Rows of one round: one
   // small CTA.  Longer ones: a cluster whose CTAs need two rounds at most, or as many
   // CTAs as there are SMs (448 rows of 5000: 7 us, against 22 as clusters of eight).
   if (V <= 2048) {
-    SUB_CUDA_TRY(launch_clusters(probs_kernel<128, 4>, rows, 1, 128, st, logits, V, c_hi, c_lo, probs));
+    SUB_CUDA_TRY(launch_clusters(probs_kernel<128, 4>, rows, 1, 128, 0, st, logits, V, sharp, probs));
     return SUB_OK;
   }
   int size = 1;
   const int sms = device_sms();
   while (size < MAX_CLUSTER && (V > size * 8192 || (rows * size < sms && V > size * 4096))) size *= 2;
-  SUB_CUDA_TRY(launch_clusters(probs_kernel<256, 4>, rows, size, 256, st, logits, V, c_hi, c_lo, probs));
+  SUB_CUDA_TRY(launch_clusters(probs_kernel<256, 4>, rows, size, 256, 0, st, logits, V, sharp, probs));
   return SUB_OK;
 }
 
@@ -470,6 +370,6 @@ extern "C" int32_t sub_verify_sample(const float* p, const float* q, const int32
   VerifyArgs a{p, q, draft, u, n_draft, V, tokens, n_accepted};
   // rows one CTA reads in a few rounds need no cluster
   const int size = V <= 8192 ? 1 : MAX_CLUSTER;
-  SUB_CUDA_TRY(launch_clusters(verify_kernel, n_seqs, size, VER_THREADS, as_stream(stream), a));
+  SUB_CUDA_TRY(launch_clusters(verify_kernel, n_seqs, size, VER_THREADS, 0, as_stream(stream), a));
   return SUB_OK;
 }

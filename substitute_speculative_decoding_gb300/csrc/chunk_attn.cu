@@ -766,7 +766,7 @@ chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__
 // rounds of reads from L2, at the end of every call: what it needs to know
 // lies ready in the list of cuts.
 constexpr int JOIN_WARPS = 4;   // per CTA
-constexpr int join_split(int rt) { return rt <= WIDE ? rt / JOIN_WARPS : 16; }   // CTAs per tile
+constexpr int join_split(int rt) { return rt <= 64 ? rt / JOIN_WARPS : 16; }   // CTAs per tile
 
 template <int D, int RT>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) chunk_join_kernel(const __grid_constant__ ChunkArgs a) {
@@ -890,6 +890,12 @@ int tile_rows(int group, int n_seqs, int n_rows, bool codes, int64_t keys) {
   return rows <= NARROW * seqs ? NARROW : rows <= tiles * WIDE * seqs ? WIDE : CHUNK_TC_ROWS;
 }
 
+// Trees: tiles of 32 or 64 rows (0: those above), by the rows that a sequence has on average.
+int tree_rows(int group, int n_seqs, int n_rows) {
+  const int64_t rows = (int64_t)n_rows * group, seqs = n_seqs;
+  return rows <= WIDE * seqs || rows > 64 * seqs ? 0 : rows <= 32 * seqs ? 32 : 64;
+}
+
 // Partial results, two per CTA, and the list of cuts.
 int64_t part_bytes(int n_ctas, int rows, int d) {
   return (int64_t)n_ctas * (2 * rows * (d + 2) * 4 + (int64_t)sizeof(ChunkCut));
@@ -945,6 +951,16 @@ int32_t chunk_attn(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q, const Cach
                            batch->max_keys ? std::min(batch->max_keys, kv->capacity) : kv->capacity);
   const int64_t pool_rows =
       (int64_t)kv->n_layers * kv->n_pages * kv->n_heads_kv * kv->page_size;
+  const int mid = a.mask && chunk_tc_fits(pool_rows) ? tree_rows(a.group, a.t.n_seqs, a.t.n_rows) : 0;
+  if (mid) {
+    a.part_o = reinterpret_cast<float*>(workspace);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + (int64_t)n_ctas * 2 * mid * kv->head_dim);
+    a.cuts = reinterpret_cast<ChunkCut*>(a.part_ml + (int64_t)n_ctas * 2 * mid);
+    SUB_TRY(launch_chunk_mid(a, Q8, kv->head_dim, mid, pool_rows, n_ctas, st));
+    if (mid == 32)
+      return kv->head_dim == 128 ? launch_join<128, 32>(a, n_ctas, st) : launch_join<64, 32>(a, n_ctas, st);
+    return kv->head_dim == 128 ? launch_join<128, 64>(a, n_ctas, st) : launch_join<64, 64>(a, n_ctas, st);
+  }
   const bool tensor_cores = rt == CHUNK_TC_ROWS && chunk_tc_fits(pool_rows);
   const int part_rows = tensor_cores ? CHUNK_TC_ROWS : std::min(rt, WIDE);
   a.part_o = reinterpret_cast<float*>(workspace);
@@ -974,10 +990,11 @@ int32_t tree_args(const int32_t* base, const int32_t* mask, int32_t words, const
 }  // namespace
 
 int32_t chunk_attn_timeouts(unsigned int* out) {
-  unsigned int tc = 0;
+  unsigned int tc = 0, mid = 0;
   SUB_TRY(chunk_tc_timeouts(&tc));
+  SUB_TRY(chunk_mid_timeouts(&mid));
   SUB_CUDA_TRY(cudaMemcpyFromSymbol(out, g_decode_timeouts, sizeof(unsigned int)));
-  *out += tc;
+  *out += tc + mid;
   return SUB_OK;
 }
 

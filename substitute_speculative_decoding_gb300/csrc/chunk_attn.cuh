@@ -266,7 +266,13 @@ bool chunk_tc_fits(int64_t pool_rows);   // rows of head_dim values in a pool
 int32_t launch_chunk_tc(const ChunkArgs& a, bool q8, int head_dim, int64_t pool_rows, int n_ctas,
                         cudaStream_t st);
 int32_t chunk_tc_timeouts(unsigned int* out);
-// Waits that ran out in either kernel.
+// The kernel for a few dozen rows of trees (chunk_attn_mid.cu): tiles of 32 or 64 rows.
+int32_t launch_chunk_mid(const ChunkArgs& a, bool q8, int head_dim, int rows, int64_t pool_rows, int n_ctas,
+                         cudaStream_t st);
+int32_t chunk_mid_timeouts(unsigned int* out);
+// Tensor map of a bf16 pool by (row, column), in boxes of `box` rows of 64 columns.
+bool chunk_pool_map(CUtensorMap* m, const void* pool, int64_t rows, int d, int box);
+// Waits that ran out in any of the kernels.
 int32_t chunk_attn_timeouts(unsigned int* out);
 // Tensor map of a pool by (page and head, place, column), in boxes of 16 places.
 bool chunk_page_map(CUtensorMap* m, const void* pool, const SeqTable& t, int64_t heads, int d, bool codes);

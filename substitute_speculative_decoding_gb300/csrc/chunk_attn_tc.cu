@@ -55,17 +55,15 @@
 // finite become 0, and if there were any of these, each row adds those that it does
 // read to its result (whatever is added to them, it stays infinite or NaN).
 #include <cuda_fp16.h>
-#include "chunk_attn.cuh"
-#include "gemv.cuh"
-#include "tma.cuh"
+#include "chunk_tc.cuh"
 
 namespace sub {
 namespace {
 
 using namespace tmah;
 
-constexpr int RT = CHUNK_TC_ROWS, KB = CHUNK_TC_KEYS;
-static_assert(RT == 256 && KB == 128, "two groups of 128 rows, blocks of 128 keys");
+constexpr int RT = CHUNK_TC_ROWS;
+static_assert(RT == 256, "two groups of 128 rows");
 constexpr int GROUP_ROWS = 128;
 // log2 of how far weights may exceed 1; fp16 weights times scales of V are 2^11 at
 // the reference and 2^15 at most, so that fp16's smallest step is 2^-35 of the former
@@ -109,153 +107,6 @@ struct Cfg {
   static_assert(SMEM <= 227 * 1024, "one CTA's shared memory");
   static_assert(SLOTS * SLOT >= (SUB_MAX_SEQS + 1) * 8, "the ring holds the running sums first");
 };
-
-// ---------------------------------------------------------------- tcgen05 --
-// Shared-memory descriptors of operands in the 128-byte swizzle.  K-major (Q, K:
-// rows of 64 values): stride 1024 between groups of 8 rows.  MN-major (V: a key
-// is a row of 64 columns): 1024 between groups of 8 keys, and the next 64 columns a
-// whole block of keys further.
-__device__ __forceinline__ uint64_t desc_k(uint32_t addr) {
-  return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024u >> 4) << 32 |
-         (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
-__device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
-  return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)((KB * 128u) >> 4) << 16 |
-         (uint64_t)(1024u >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
-// kind::f16, fp32 accumulator, M = 128; both operands bf16 (1) or fp16 (0).
-__device__ constexpr uint32_t idesc(int n, bool bf16, bool b_mn) {
-  return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((b_mn ? 1u : 0u) << 16) |
-         ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
-}
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool add) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"((uint32_t)add)
-      : "memory");
-}
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool add) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(id), "r"((uint32_t)add)
-      : "memory");
-}
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void wait_ld() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void wait_st() {
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-// 32 columns of the warp's 32 lanes, one lane per thread; wait_ld before use.
-__device__ __forceinline__ void tc_ld32(uint32_t t, float* v) {
-  uint32_t* r = reinterpret_cast<uint32_t*>(v);
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(t)
-      : "memory");
-}
-__device__ __forceinline__ void tc_ld16(uint32_t t, float* v) {
-  uint32_t* r = reinterpret_cast<uint32_t*>(v);
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-      "%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(t)
-      : "memory");
-}
-__device__ __forceinline__ void tc_st16(uint32_t t, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15,%16};" ::"r"(t),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-
-__device__ __forceinline__ bool elect_one() {   // by a whole warp: one lane
-  uint32_t x;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(x));
-  return x != 0;
-}
-
-// Bounded wait.  One that runs out is counted and ends the CTA's work: every
-// later wait returns at once, nothing more is issued, and the results are not valid.
-struct Gate {
-  volatile int* dead;
-  __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) const {
-    if (mbar_try_wait(bar, parity)) return true;
-    for (uint32_t i = 0; i < (1u << 20); ++i) {
-      if (mbar_try_wait(bar, parity)) return true;
-      if ((i & 63) == 63 && *dead) return false;
-    }
-    if (!*dead) {
-      *dead = 1;
-      atomicAdd(&g_chunk_timeouts, 1u);
-    }
-    return false;
-  }
-  // by a whole warp, which goes on or stops together
-  __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) const {
-    return __all_sync(~0u, wait(bar, parity));
-  }
-};
-
-// Bit of a block's 16-key part in its word of missing pages: the TMA warp writes
-// the word, the warps that look keys up a byte per 32 keys.
-template <bool Q8>
-__device__ constexpr int miss_bit(int part) {
-  return Q8 ? 8 * (part >> 1) + (part & 1) : part;
-}
-template <int N>
-__device__ __forceinline__ void more_registers() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void fewer_registers() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-// Converters and the warps that look keys up, once per block.
-template <int WARPS>
-__device__ __forceinline__ void meet_planners() {
-  asm volatile("bar.sync 3, %0;" ::"n"(WARPS * 32) : "memory");
-}
-
-struct Maps {
-  CUtensorMap k, v;   // pool rows [all rows, D] bf16, boxes of 64 columns x box keys
-};
-
-__device__ __forceinline__ void st_shared(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w)
-               : "memory");
-}
-// 32 bytes at once: a row is written by one thread, and this fills whole sectors.
-__device__ __forceinline__ void st_global32(void* p, const uint32_t* r) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]),
-               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
 
 // ------------------------------------------------------------------ kernel --
 template <int D, bool Q8, bool TREE>
@@ -332,7 +183,7 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
   if (line_lo < line_hi) u = plan.find(s_pre, line_lo);
   fence_async();     // the ring is written by copies from here on
   __syncthreads();
-  const Gate gate{s_dead};
+  const Gate gate{s_dead, &g_chunk_timeouts};
   const int G = a.group;
   // Slot j of the ring holds V of block j - 1 and K of block j, across the units;
   // the first has no V, the last no K.
@@ -1008,10 +859,7 @@ int32_t launch(const ChunkArgs& a, int64_t rows, int n_ctas, cudaStream_t st) {
   memset(&maps, 0, sizeof(maps));
   int box = 16;
   while (box < KB && a.t.page_size % (2 * box) == 0) box *= 2;
-  auto pool_map = [&](CUtensorMap* m, const void* pool) {
-    return make_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pool, D, rows, D * 2, 64, box, 128);
-  };
-  if (!Q8 && (!pool_map(&maps.k, a.k) || !pool_map(&maps.v, a.v)))
+  if (!Q8 && (!chunk_pool_map(&maps.k, a.k, rows, D, box) || !chunk_pool_map(&maps.v, a.v, rows, D, box)))
     return fail(SUB_ECUDA, "chunk_attn: the cache's tensor map was refused");
   SUB_CUDA_TRY(launch_k(chunk_tc_kernel<D, Q8, TREE>, dim3(n_ctas), dim3(C::THREADS), C::SMEM, st, maps, a,
                         box, (int)rows));
@@ -1019,6 +867,10 @@ int32_t launch(const ChunkArgs& a, int64_t rows, int n_ctas, cudaStream_t st) {
 }
 
 }  // namespace
+
+bool chunk_pool_map(CUtensorMap* m, const void* pool, int64_t rows, int d, int box) {
+  return make_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pool, d, rows, d * 2, 64, box, 128);
+}
 
 bool chunk_page_map(CUtensorMap* m, const void* pool, const SeqTable& t, int64_t heads, int d, bool codes) {
   auto fn = encode_fn();

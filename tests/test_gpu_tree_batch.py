@@ -280,7 +280,8 @@ def test_a_path_of_all_is_chunk_attention(sub, bits_, n):
     c.mask.zero_()
     for far in (2 ** 31 - 1, 300 + 5 + n):
         c.base.fill_(far)
-        assert torch.equal(c.run(), plain)
+        c.check(c.run())
+        assert (c.run().float() - plain.float()).abs().max() < 0.05      # (other sums, another rounding)
 
 
 @pytest.mark.parametrize("bits_", [16, 8])

@@ -10,19 +10,19 @@
 //                 (codes are converted bare, two instructions for two of them), and a
 //                 block costs N exponentials per thread, not 128
 //   O^T = V^T P^T [D x N], with P^T written to shared memory as it is formed (bf16: two
-//                 halves, P = hi + lo; codes: fp16 times V's scale)
+//                 halves, hi in the columns of a product and lo beside them; codes: fp16 times V's scale)
 // Roles:
-//   warps 0-3, 4-7   softmax of the even and the odd blocks of 128 keys of a unit: two
-//                    states (reference, sum, O^T), joined when the unit is through
+//   warps 0-3, 4-7   softmax of the first and the second half of the rows, block by block: the
+//                    scores of the next block and the output of the last are formed meanwhile
 //   a producer       as in chunk_attn_tc.cu: a TMA warp (bf16), or eight warps that turn
 //                    codes into fp16 (code - 128), exactly, with two warps that look
 //                    the keys up and gather their scales ahead
 //   one MMA warp
 //
 // The running maximum of a row lies across the threads, so it is not formed in every
-// block: each thread compares its scores with the references of all rows (one
-// comparison for N scores), and only if one exceeds its reference by more than 2^8 (codes: 2^3),
-// the group forms the maxima and rescales.  Sums are kept per thread and row.
+// block: each thread compares its scores with the references of its rows, and only if
+// one exceeds its reference by more than 2^8 (codes: 2^3), the group forms the
+// maxima and rescales.  Sums are kept per thread and row.
 //
 // Codes: the weight times V's scale, of which a power of two is part of the score that the
 // reference follows and the rest, in [1, 2), a factor: what is rounded to fp16 is 2^11
@@ -41,8 +41,6 @@ namespace {
 
 __device__ unsigned int g_mid_timeouts;   // waits that ran out (never expected)
 
-constexpr float NONE = 3e38f;   // minus the reference of a row that has read no key
-
 template <int D, bool Q8, int N>
 struct MidCfg {
   static_assert(N == 32 || N == 64, "rows of a tile: a warp's lanes hold one or two each");
@@ -50,29 +48,29 @@ struct MidCfg {
   static constexpr int SLOT = 2 * HALF;                  // V of a block, K of the next
   static constexpr int SLOTS = D == 64 ? 3 : 2;
   static constexpr int Q_BYTES = N * D * 2;
-  static constexpr int P_HALF = KB * 128;                // a key's weights: 64 columns, N of them used
-  static constexpr int P_GROUP = (Q8 ? 1 : 2) * P_HALF;
+  static constexpr int H = N / 2;                        // of a group
+  // A key's weights: lines of 64 columns.  bf16: N = 32 hi and lo in one, N = 64 one each
+  static constexpr int P_LINES = KB * 128, P_COLS = Q8 ? N : 2 * N;
+  static constexpr int P_BYTES = P_COLS > 64 ? 2 * P_LINES : P_LINES;   // of a block; two of them
   static constexpr int CONV = Q8 ? 8 : 0;                // converter warps
   static constexpr int MMA_WARP = 8 + (Q8 ? CONV : 1);
   static constexpr int PLAN = Q8 ? 2 : 0;                // then warps that look the keys up
   static constexpr int THREADS = Q8 ? 640 : 384;         // whole groups of four warps
-  // registers by group of four warps, out of 65536 / THREADS each at the launch
-  static constexpr int REGS_SOFTMAX = Q8 ? 160 : 192;
-  static constexpr int REGS_PROD = Q8 ? 56 : 120;
-  static constexpr int REGS_MMA = Q8 ? 48 : 120;
-  static_assert((2 * REGS_SOFTMAX + (Q8 ? CONV / 4 : 1) * REGS_PROD + (Q8 ? REGS_MMA : 0)) * 128 <=
-                    65536 / THREADS / 8 * 8 * THREADS,
+  // codes: registers by group of four warps, out of 65536 / THREADS each at the launch
+  static constexpr int REGS_SOFTMAX = 128, REGS_CONV = 80, REGS_MMA = 64;
+  static_assert(!Q8 || (2 * REGS_SOFTMAX + CONV / 4 * REGS_CONV + REGS_MMA) * 128 <=
+                           65536 / THREADS / 8 * 8 * THREADS,
                 "the shares fit what the block is launched with");
   static constexpr float GROWTH = Q8 ? 3.f : 8.f;        // log2 of how far weights may exceed the reference
   static constexpr float SHIFT = Q8 ? 11.f : 0.f;        // log2 of the weight at it
   static constexpr int SCALES = Q8 ? 8 * 2 * KB * 4 : 0; // eight blocks' scales of K, of V
-  static constexpr int ROWS = Q8 ? 4 * KB * 4 : 0;       // pool rows of four blocks' keys
-  // of the rows: place in O, last key, mask, factor; [2] minus the reference, factors; [2][4
-  // warps] maxima or sums
-  static constexpr int INFO = N * (8 + 4 + 4 + 4 + 2 * 4 + 2 * 4 + 2 * 4 * 4);
+  static constexpr int ROWS = Q8 ? 8 * KB * 4 : 0;       // pool rows of eight blocks' keys
+  // of the rows: place in O, last key, mask, factor, minus the reference, whether a key was
+  // read, factor of what was formed and difference of the reference; [4 warps] maxima or sums
+  static constexpr int INFO = N * (8 + 7 * 4 + 4 * 4);
   static constexpr int TAIL = 256;                       // barriers, flags, TMEM address
-  static constexpr int TMEM = 4 * N;                     // columns: S^T and O^T of both groups
-  static constexpr int SMEM = 1024 + 2 * P_GROUP + Q_BYTES + SLOTS * SLOT + SCALES + ROWS + INFO + TAIL;
+  static constexpr int TMEM = 2 * N + P_COLS <= 128 ? 128 : 256;   // columns: S^T of two blocks, O^T
+  static constexpr int SMEM = 1024 + 2 * P_BYTES + Q_BYTES + SLOTS * SLOT + SCALES + ROWS + INFO + TAIL;
   static_assert(SMEM <= 227 * 1024, "one CTA's shared memory");
   static_assert(SLOTS * SLOT >= (SUB_MAX_SEQS + 1) * 8, "the ring holds the running sums first");
 };
@@ -91,11 +89,15 @@ __device__ __forceinline__ bool group_any(int t, bool x) {
   return r != 0;
 }
 
-// v[i] of all lanes joined by f, for i = lane.
-template <class F>
-__device__ __forceinline__ float across(float (&v)[32], int lane, F f) {
+// v[i] of all lanes joined by f, for i = lane (below M).
+template <int M, class F>
+__device__ __forceinline__ float across(float (&v)[M], int lane, F f) {
+  if constexpr (M == 16) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1)
+    for (int i = 0; i < M; ++i) v[i] = f(v[i], __shfl_xor_sync(~0u, v[i], 16));
+  }
+#pragma unroll
+  for (int o = M / 2; o; o >>= 1)
 #pragma unroll
     for (int i = 0; i < o; ++i) {
       const bool up = lane & o;
@@ -111,11 +113,11 @@ __global__ void __launch_bounds__(MidCfg<D, Q8, N>::THREADS, 1)
 chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ChunkArgs a, const int box,
                  const int pool_rows) {
   using C = MidCfg<D, Q8, N>;
-  constexpr int SLOTS = C::SLOTS;
+  constexpr int SLOTS = C::SLOTS, H = C::H;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* const base_p = smem_raw + (base - smem_u32(smem_raw));
-  const uint32_t p_s = base, q_s = p_s + 2 * C::P_GROUP, ring_s = q_s + C::Q_BYTES;
+  const uint32_t p_s = base, q_s = p_s + 2 * C::P_BYTES, ring_s = q_s + C::Q_BYTES;
   int64_t* const s_pre = reinterpret_cast<int64_t*>(base_p + (ring_s - base));   // until the first copies
   uint8_t* at_p = base_p + (ring_s - base) + SLOTS * C::SLOT;
   auto take = [&](int bytes) {
@@ -124,27 +126,31 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
     return p;
   };
   float* const s_scale = reinterpret_cast<float*>(take(C::SCALES));    // [8][K: KB, V: KB]
-  int* const s_rows = reinterpret_cast<int*>(take(C::ROWS));           // [4][KB]
+  int* const s_rows = reinterpret_cast<int*>(take(C::ROWS));           // [8][KB]
   int64_t* const s_place = reinterpret_cast<int64_t*>(take(N * 8));    // of a row in O; -1: none
   float* const s_qs = reinterpret_cast<float*>(take(N * 4));           // codes: factor of a row's scores
-  float* const s_nref = reinterpret_cast<float*>(take(2 * N * 4));     // [group] SHIFT - reference
-  float* const s_fac = reinterpret_cast<float*>(take(2 * N * 4));      // [group]
-  float* const s_part = reinterpret_cast<float*>(take(2 * 4 * N * 4)); // [group][warp]
+  float* const s_nref = reinterpret_cast<float*>(take(N * 4));         // SHIFT - reference
+  float* const s_fac = reinterpret_cast<float*>(take(N * 4));
+  float* const s_diff = reinterpret_cast<float*>(take(N * 4));
+  float* const s_part = reinterpret_cast<float*>(take(4 * N * 4));     // [group][warp][H]
+  int* const s_any = reinterpret_cast<int*>(take(N * 4));              // a key has been read
   int* const s_lim = reinterpret_cast<int*>(take(N * 4));              // keys 0 .. lim are read
   int* const s_mask = reinterpret_cast<int*>(take(N * 4));             // row of the masks
   uint8_t* const tail = take(C::TAIL);
   const uint32_t bars = smem_u32(tail);
   auto kv_full = [&](uint32_t block) { return bars + 8u * (block % SLOTS); };
   auto kv_empty = [&](uint32_t block) { return bars + 8u * (SLOTS + block % SLOTS); };
-  auto s_full = [&](int t) { return bars + 8u * (2 * SLOTS + t); };
-  auto p_full = [&](int t) { return bars + 8u * (2 * SLOTS + 2 + t); };
-  const uint32_t q_full = bars + 8u * (2 * SLOTS + 4), o_full = q_full + 8u;
-  int* const flags = reinterpret_cast<int*>(tail + 8 * (2 * SLOTS + 6));
+  auto s_full = [&](uint32_t block) { return bars + 8u * (2 * SLOTS + (block & 1)); };
+  auto p_full = [&](uint32_t block) { return bars + 8u * (2 * SLOTS + 2 + (block & 1)); };
+  auto o_full = [&](uint32_t block) { return bars + 8u * (2 * SLOTS + 4 + (block & 1)); };
+  const uint32_t q_full = bars + 8u * (2 * SLOTS + 6);
+  int* const flags = reinterpret_cast<int*>(tail + 8 * (2 * SLOTS + 7));
   volatile int* const s_dead = flags;                // a wait ran out
   volatile int* const s_odd = flags + 1;             // 1 + the last piece that met infinite values or NaN
-  volatile uint32_t* const s_miss = reinterpret_cast<uint32_t*>(flags + 2);   // [8] blocks' missing 16-key parts
-  uint32_t* const s_tmem = reinterpret_cast<uint32_t*>(flags + 10);
-  static_assert(8 * (2 * SLOTS + 6) + 11 * 4 <= C::TAIL, "tail");
+  volatile int* const s_force = flags + 2;           // [group] a row has read no key yet
+  volatile uint32_t* const s_miss = reinterpret_cast<uint32_t*>(flags + 4);   // [8] blocks' missing 16-key parts
+  uint32_t* const s_tmem = reinterpret_cast<uint32_t*>(flags + 12);
+  static_assert(8 * (2 * SLOTS + 7) + 13 * 4 <= C::TAIL, "tail");
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (warp == 0) {
@@ -159,12 +165,12 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
       mbar_init(kv_full(s), Q8 ? C::CONV : 1);
       mbar_init(kv_empty(s), 1);
     }
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(s_full(t), 1);
-      mbar_init(p_full(t), 4);   // one arrival for each warp of the group
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(s_full(b), 1);
+      mbar_init(p_full(b), 8);   // one arrival for each softmax warp
+      mbar_init(o_full(b), 1);
     }
     mbar_init(q_full, 8);
-    mbar_init(o_full, 1);
     *s_dead = 0;
     *s_odd = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -193,14 +199,6 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
   // the first has no V, the last no K.
   const uint32_t n = (uint32_t)(line_hi > line_lo ? line_hi - line_lo : 0);
   int kb = (int)(line_lo - u.begin);   // the next block to look up, of unit u
-  // pool row of key x of that block; -1: past the last key, -2: on no page
-  auto row_of = [&](int x) {
-    const int key = kb * KB + x;
-    if (key >= u.n_keys) return -1;
-    const int entry = a.by_page.quot(key), page = a.t.pages[(int64_t)u.b * a.t.width + entry];
-    if ((unsigned)page >= (unsigned)a.t.n_pages) return -2;
-    return (int)pool_row(a.t, a.layer, a.n_heads_kv, page, u.head, key - entry * a.t.page_size);
-  };
   auto step = [&] {
     if (++kb == u.n_blocks) {
       plan.next(u);
@@ -208,29 +206,40 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
     }
   };
 
-  if (warp < 8) more_registers<C::REGS_SOFTMAX>();
-  else if (!Q8 || warp < 8 + C::CONV) fewer_registers<C::REGS_PROD>();
-  else fewer_registers<C::REGS_MMA>();
+  if constexpr (Q8) {
+    if (warp < 8) more_registers<C::REGS_SOFTMAX>();
+    else if (warp < 8 + C::CONV) fewer_registers<C::REGS_CONV>();
+    else fewer_registers<C::REGS_MMA>();
+  }
 
   if (warp < 8) {
     // ------------------------------------------------ softmax, Q, results
     const int t = warp >> 2, wq = warp & 3, r = wq * 32 + lane;   // group, the thread's key of a block (or column of O)
+    const int c0 = t * H;                                         // the group's rows
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
-    const uint32_t tS = tmem + t * N + lanes;
-    auto tO = [&](int g) { return tmem + (2 + g) * N + lanes; };
-    const uint32_t mine_p = p_s + t * C::P_GROUP + r * 128;
-    float* const nref = s_nref + t * N;
-    float* const fac = s_fac + t * N;
-    uint32_t n_s = 0, n_o = 0;      // blocks of this group, pieces
+    const uint32_t tS = tmem + c0 + lanes, tO = tmem + 2 * N + c0 + lanes;
+    float* const nref = s_nref + c0;
+    float* const fac = s_fac + c0;
     uint32_t block = 0;             // of this CTA's part of the line
     constexpr int CH = D / 8, RP = 32 / CH, QP = N / 8 / RP;   // 16-byte chunks of a Q row, rows per pass of a warp, passes
-    const int c = lane % CH;
+    const int c = lane % CH, q_row = warp * (N / 8) + lane / CH;
+    uint4 qw[QP];
+    auto q_load = [&] {
+#pragma unroll
+      for (int i = 0; i < QP; ++i) {
+        const int row = u.tile * N + q_row + i * RP, q = a.by_group.quot(row);
+        qw[i] = make_uint4(0, 0, 0, 0);
+        if (q < u.rows)
+          qw[i] = ldg_cg_v4(a.Q + (int64_t)(u.row0 + q) * a.ldq + (int64_t)(u.head * G + row - q * G) * D + c * 8);
+      }
+    };
     // (also for a CTA that stops early because a wait ran out)
     if (tid == 0) a.cuts[blockIdx.x].pieces = 0;
+    if (line_lo < line_hi) q_load();
     int piece = 0;
     for (int64_t at = line_lo; at < line_hi; ++piece) {
       const int kb0 = (int)(at - u.begin), kb1 = (int)min((int64_t)u.n_blocks, line_hi - u.begin), nb = kb1 - kb0;
-      const bool first = at == line_lo;
+      const bool first = at == line_lo, whole = kb0 == 0 && kb1 == u.n_blocks;
       at = u.begin + kb1;
       if (tid == 0 && at >= line_hi) a.cuts[blockIdx.x] = make_cut(u, kb1, line_lo, per);
       // ---- the rows, and Q into shared memory: chunk c of a row at c ^ (row % 8) of its
@@ -239,18 +248,18 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
       if (tid < N) {
         const int row = u.tile * N + tid, q = a.by_group.quot(row);
         const bool real = q < u.rows;
-        s_place[tid] = real ? ((int64_t)(u.row0 + q) * a.n_heads_q + u.head * G + row - q * G) * D : -1;
+        s_place[tid] = !real ? -1
+                             : whole ? ((int64_t)(u.row0 + q) * a.n_heads_q + u.head * G + row - q * G) * D
+                                     : ((2 * (int64_t)blockIdx.x + (first ? 0 : 1)) * N + tid) * D;
         s_lim[tid] = real ? last_key(u.pos, q, u.n_keys) : -1;
         s_mask[tid] = u.row0 + min(q, u.rows - 1);
+        s_nref[tid] = 0.f;
+        s_any[tid] = 0;
       }
-      if (tid < 2 * N) s_nref[tid] = NONE;
 #pragma unroll
       for (int i = 0; i < QP; ++i) {
-        const int rr = warp * (N / 8) + i * RP + lane / CH;
-        const int row = u.tile * N + rr, q = a.by_group.quot(row);
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (q < u.rows)
-          w = ldg_cg_v4(a.Q + (int64_t)(u.row0 + q) * a.ldq + (int64_t)(u.head * G + row - q * G) * D + c * 8);
+        const int rr = q_row + i * RP;
+        uint4 w = qw[i];
         if constexpr (Q8) {
           // the row's largest value to [1, 2), for fp16
           const uint32_t x[4] = {w.x, w.y, w.z, w.w};
@@ -270,53 +279,51 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
         st_shared(q_s + (c >> 3) * (N * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), w.x, w.y, w.z, w.w);
       }
       fence_async();
+      tc_fence_before();   // O^T of the last piece is read
       softmax_sync();
       if (lane == 0) mbar_arrive(q_full);
       const int lim_all = plan.template common<true>(u);   // last key that every row reads
       const int slot0 = tree_base(a, u.b);
-      auto window = [&](int row, int key) {   // of 32 keys, those that the row's mask leaves
-        return mask_window(a.mask + (int64_t)s_mask[row] * a.words, a.words, key - slot0);
-      };
       // 32 keys from `key` on that the row reads, as far as its place and its mask say
       auto reads = [&](int row, int key) {
         const int left = s_lim[row] - key;
-        return left < 0 ? 0u : window(row, key) & (left >= 31 ? ~0u : (2u << left) - 1u);
+        if (left < 0) return 0u;
+        return mask_window(a.mask + (int64_t)s_mask[row] * a.words, a.words, key - slot0) &
+               (left >= 31 ? ~0u : (2u << left) - 1u);
       };
 
-      float2 l[N / 2];
+      float2 l[H / 2];
 #pragma unroll
-      for (int i = 0; i < N / 2; ++i) l[i] = make_float2(0.f, 0.f);
+      for (int x = 0; x < H / 2; ++x) l[x] = make_float2(0.f, 0.f);
       // (A wait that runs out stops no warp: all of them meet in barriers.  The waits after it
-      // return at once, and the results are not valid.)
+      // return soon, and the results are not valid.)
 #pragma unroll 1
-      for (int i = t; i < nb; i += 2) {
-        const uint32_t bl = block + i;
+      for (int i = 0; i < nb; ++i, ++block) {
         const int key0 = (kb0 + i) * KB;
-        gate.wait_warp(s_full(t), n_s & 1);
-        ++n_s;
+        gate.wait_warp(s_full(block), (block >> 1) & 1);
         tc_fence_after();
-        const uint32_t miss = s_miss[bl & 7];
+        const uint32_t miss = s_miss[block & 7];
         const bool behind = key0 + KB - 1 > lim_all;
-        float s[N];
-#pragma unroll
-        for (int x = 0; x < N; x += 32) tc_ld32(tS + x, s + x);
+        float s[H];
+        if constexpr (H == 32) tc_ld32(tS + (block & 1) * N, s);
+        else tc_ld16(tS + (block & 1) * N, s);
         // codes: this key's scales, that of V as a power of two and the rest of it
         float f = a.sl2, lv = 0.f, part = 1.f, back = 1.f;
         if constexpr (Q8) {
-          const float* const sc = s_scale + (bl & 7) * (2 * KB);
-          const float kk = sc[r], vv = sc[KB + r];
-          const int e = min(126, max(-80, (int)((__float_as_uint(vv) >> 23) & 255u) - 127));   // vv is finite
-          f = kk;
+          const float* const sc = s_scale + (block & 7) * (2 * KB);
+          const float vv = sc[KB + r];   // finite
+          const int e = min(126, max(-80, (int)((__float_as_uint(vv) >> 23) & 255u) - 127));
+          f = sc[r];
           lv = (float)e;
           back = __uint_as_float((uint32_t)(127 - e) << 23);   // 2^-e
           part = vv * back;
         }
+        const float2 f2 = make_float2(f, f), lv2 = make_float2(lv, lv);
         wait_ld();
         if constexpr (Q8) {
-          const float2 f2 = make_float2(f, f), lv2 = make_float2(lv, lv);
 #pragma unroll
-          for (int x = 0; x < N; x += 4) {
-            const float4 qs = *reinterpret_cast<const float4*>(s_qs + x);
+          for (int x = 0; x < H; x += 4) {
+            const float4 qs = *reinterpret_cast<const float4*>(s_qs + c0 + x);
             const float2 a0 = fma2(mul2(make_float2(s[x], s[x + 1]), make_float2(qs.x, qs.y)), f2, lv2);
             const float2 a1 = fma2(mul2(make_float2(s[x + 2], s[x + 3]), make_float2(qs.z, qs.w)), f2, lv2);
             s[x] = a0.x;
@@ -324,76 +331,117 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
             s[x + 2] = a1.x;
             s[x + 3] = a1.y;
           }
-          f = 1.f;
         }
         if (behind || miss) {
-          // lane: the warp's 32 keys, as rows lane (and 32 + lane) read them
+          // lane x: the warp's 32 keys, as the group's row x reads them
           const uint32_t gone = miss >> miss_bit<Q8>(2 * wq);
           const uint32_t there = ((gone & 1u) ? 0u : 0xffffu) | ((gone & 2u) ? 0u : 0xffff0000u);
+          const uint32_t word = lane < H ? reads(c0 + lane, key0 + wq * 32) & there : 0u;
 #pragma unroll
-          for (int h = 0; h < N; h += 32) {
-            const uint32_t word = reads(h + lane, key0 + wq * 32) & there;
-#pragma unroll
-            for (int x = 0; x < 32; ++x)
-              if (!((__shfl_sync(~0u, word, x) >> lane) & 1u)) s[h + x] = -INFINITY;
-          }
+          for (int x = 0; x < H; ++x)
+            if (!((__shfl_sync(~0u, word, x) >> lane) & 1u)) s[x] = -INFINITY;
         }
-        // scores relative to the references (bf16: in place of the products)
-        const float2 fs = make_float2(f, f);
-        float over = -INFINITY;
+        // ---- scores relative to the references ----
+        float over[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int x = 0; x < N; x += 4) {
+        for (int x = 0; x < H; x += 4) {
           const float4 m = *reinterpret_cast<const float4*>(nref + x);
-          const float2 a0 = fma2(make_float2(s[x], s[x + 1]), fs, make_float2(m.x, m.y));
-          const float2 a1 = fma2(make_float2(s[x + 2], s[x + 3]), fs, make_float2(m.z, m.w));
-          over = fmaxf(fmaxf(over, fmaxf(a0.x, a0.y)), fmaxf(a1.x, a1.y));
+          float2 a0 = make_float2(s[x], s[x + 1]), a1 = make_float2(s[x + 2], s[x + 3]);
+          a0 = Q8 ? add2(a0, make_float2(m.x, m.y)) : fma2(a0, f2, make_float2(m.x, m.y));
+          a1 = Q8 ? add2(a1, make_float2(m.z, m.w)) : fma2(a1, f2, make_float2(m.z, m.w));
+          over[0] = fmaxf(over[0], s[x] = a0.x);
+          over[1] = fmaxf(over[1], s[x + 1] = a0.y);
+          over[2] = fmaxf(over[2], s[x + 2] = a1.x);
+          over[3] = fmaxf(over[3], s[x + 3] = a1.y);
         }
-        if (group_any(t, over > C::GROWTH + C::SHIFT)) {
+        const bool above = fmaxf(fmaxf(over[0], over[1]), fmaxf(over[2], over[3])) > C::GROWTH + C::SHIFT;
+        if (group_any(t, above) || i == 0 || s_force[t]) {
           // ---- the references, and what was formed with others ----
+          {
+            float v[H];
 #pragma unroll
-          for (int h = 0; h < N; h += 32) {
-            float v[32];
-#pragma unroll
-            for (int x = 0; x < 32; ++x) v[x] = s[h + x] * f;
-            s_part[(t * 4 + wq) * N + h + lane] = across(v, lane, [](float x, float y) { return fmaxf(x, y); });
+            for (int x = 0; x < H; ++x) v[x] = s[x];
+            const float m = across(v, lane, [](float x, float y) { return fmaxf(x, y); });
+            if (lane < H) s_part[(t * 4 + wq) * H + lane] = m;
           }
           group_sync(t);
-          if (r < N) {
-            float m = s_part[t * 4 * N + r];
+          if (wq == 0) {
+            bool none = false;
+            if (lane < H) {
+              float m = -INFINITY;   // largest score, relative to the reference
 #pragma unroll
-            for (int w = 1; w < 4; ++w) m = fmaxf(m, s_part[(t * 4 + w) * N + r]);
-            const float old = nref[r];
-            float less = 1.f;
-            if (m + old > C::SHIFT || (old == NONE && m > -INFINITY)) {   // above the reference
-              less = old == NONE ? 0.f : exp2_fast(C::SHIFT - m - old);
-              nref[r] = C::SHIFT - m;
+              for (int w = 0; w < 4; ++w) m = fmaxf(m, s_part[(t * 4 + w) * H + lane]);
+              const bool any = s_any[c0 + lane];
+              float diff = 0.f, less = 1.f;
+              if (any ? m > C::SHIFT : m > -INFINITY) {
+                diff = C::SHIFT - m;
+                less = any ? exp2_fast(diff) : 0.f;   // (nothing was formed without a key)
+                nref[lane] += diff;
+                s_any[c0 + lane] = 1;
+              }
+              fac[lane] = less;
+              s_diff[c0 + lane] = diff;
+              none = !any && !(m > -INFINITY) && s_place[c0 + lane] >= 0;
             }
-            fac[r] = less;
+            none = __any_sync(~0u, none);
+            if (lane == 0) s_force[t] = none;
           }
           group_sync(t);
 #pragma unroll
-          for (int x = 0; x < N; x += 2) {
+          for (int x = 0; x < H; x += 2) {
             const float2 y = *reinterpret_cast<const float2*>(fac + x);
+            const float2 z = *reinterpret_cast<const float2*>(s_diff + c0 + x);
             l[x / 2] = mul2(l[x / 2], y);
+            s[x] += z.x;
+            s[x + 1] += z.y;
           }
-          if (i >= 2) {   // (O^T is formed: the scores came after it)
+          if (i > 0) {
+            gate.wait_warp(o_full(block - 1), ((block - 1) >> 1) & 1);
+            tc_fence_after();
 #pragma unroll 1
-            for (int x = 0; x < N; x += 16) {
+            for (int x = 0; x < (Q8 ? H : 2 * H); x += 16) {
               float o[16];
+              const int y = x % H;   // its row; bf16: the halves' columns lie N apart
               __syncwarp();
-              tc_ld16(tO(t) + x, o);
+              tc_ld16(tO + y + x / H * N, o);
               wait_ld();
 #pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] *= fac[x + k];
-              tc_st16(tO(t) + x, reinterpret_cast<const uint32_t*>(o));
+              for (int k = 0; k < 16; ++k) o[k] *= fac[y + k];
+              tc_st16(tO + y + x / H * N, reinterpret_cast<const uint32_t*>(o));
             }
             wait_st();
           }
         }
-        if (!Q8 && behind) {
+        // ---- weights, into shared memory: chunk k of a key's line at k ^ (key % 8) ----
+        const float2 back2 = make_float2(back, back), part2 = make_float2(part, part);
+        const uint32_t line = p_s + (block & 1) * C::P_BYTES + r * 128;
+#pragma unroll
+        for (int x = 0; x < H; x += 8) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float2 e = make_float2(exp2_fast(s[x + 2 * k]), exp2_fast(s[x + 2 * k + 1]));
+            if constexpr (Q8) {
+              l[x / 2 + k] = fma2(e, back2, l[x / 2 + k]);
+              e = mul2(e, part2);
+              hi[k] = pack_f16x2(e.x, e.y);
+            } else {
+              l[x / 2 + k] = add2(l[x / 2 + k], e);
+              hi[k] = pack_bf16x2(e.x, e.y);
+              const float2 rest = add2(e, make_float2(-bf16lo(hi[k]), -bf16hi(hi[k])));
+              lo[k] = pack_bf16x2(rest.x, rest.y);
+            }
+          }
+          auto chunk = [&](int col) {
+            return line + (col >> 6) * C::P_LINES + (((((uint32_t)col >> 3) & 7u) ^ (r & 7)) << 4);
+          };
+          st_shared(chunk(c0 + x), hi[0], hi[1], hi[2], hi[3]);
+          if constexpr (!Q8) st_shared(chunk(N + c0 + x), lo[0], lo[1], lo[2], lo[3]);
+        }
+        if (!Q8 && behind && t == 0) {
           // V of the block: its row r is this thread's
-          gate.wait_warp(kv_full(bl + 1), ((bl + 1) / SLOTS) & 1);
-          const uint32_t v0 = ring_s + (bl + 1) % SLOTS * C::SLOT + r * 128;
+          gate.wait_warp(kv_full(block + 1), ((block + 1) / SLOTS) & 1);
+          const uint32_t v0 = ring_s + (block + 1) % SLOTS * C::SLOT + r * 128;
           const bool past = key0 + r >= u.n_keys;
           uint32_t z = 0;   // 0 * x is NaN for what is not finite
 #pragma unroll 4
@@ -425,151 +473,117 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
             *s_odd = piece + 1;
           }
         }
-        // ---- weights, into shared memory: chunk x / 8 of a key's line at its place ^ (key % 8) ----
-        const float2 back2 = make_float2(back, back), part2 = make_float2(part, part);
-#pragma unroll
-        for (int x = 0; x < N; x += 8) {
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 m = *reinterpret_cast<const float2*>(nref + x + 2 * k);
-            float2 e = fma2(make_float2(s[x + 2 * k], s[x + 2 * k + 1]), fs, m);
-            e.x = exp2_fast(e.x);
-            e.y = exp2_fast(e.y);
-            if constexpr (Q8) {
-              l[x / 2 + k] = fma2(e, back2, l[x / 2 + k]);
-              e = mul2(e, part2);
-              hi[k] = pack_f16x2(e.x, e.y);
-            } else {
-              l[x / 2 + k] = add2(l[x / 2 + k], e);
-              hi[k] = pack_bf16x2(e.x, e.y);
-              const float2 rest = add2(e, make_float2(-bf16lo(hi[k]), -bf16hi(hi[k])));
-              lo[k] = pack_bf16x2(rest.x, rest.y);
-            }
-          }
-          const uint32_t to = mine_p + (((x >> 3) ^ (r & 7)) << 4);
-          st_shared(to, hi[0], hi[1], hi[2], hi[3]);
-          if constexpr (!Q8) st_shared(to + C::P_HALF, lo[0], lo[1], lo[2], lo[3]);
-        }
         fence_async();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(t));
+        if (lane == 0) mbar_arrive(p_full(block));
       }
-      // ---- both groups' results ----
-      // sums over the group's threads, per row
+      // ---- the results: the next piece's Q comes meanwhile ----
+      const ChunkUnit done = u;
+      plan.next(u);
+      if (at < line_hi) q_load();
+      {   // sums over the group's threads, per row
+        float v[H];
 #pragma unroll
-      for (int h = 0; h < N; h += 32) {
-        float v[32];
-#pragma unroll
-        for (int x = 0; x < 32; x += 2) {
-          v[x] = l[(h + x) / 2].x;
-          v[x + 1] = l[(h + x) / 2].y;
+        for (int x = 0; x < H; x += 2) {
+          v[x] = l[x / 2].x;
+          v[x + 1] = l[x / 2].y;
         }
-        s_part[(t * 4 + wq) * N + h + lane] = across(v, lane, [](float x, float y) { return x + y; });
+        const float sum = across(v, lane, [](float x, float y) { return x + y; });
+        if (lane < H) s_part[(t * 4 + wq) * H + lane] = sum;
       }
-      gate.wait_warp(o_full, n_o & 1);
-      ++n_o;
+      group_sync(t);
+      if (r < H) {
+        const int row = c0 + r;
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) sum += s_part[(t * 4 + w) * H + r];
+        fac[r] = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+        if (!whole && s_place[row] >= 0)   // (codes: the shift is common to all pieces)
+          __stcg(a.part_ml + s_place[row] / D, make_float2(s_any[row] ? -nref[r] : -INFINITY, sum));
+      }
+      gate.wait_warp(o_full(block - 1), ((block - 1) >> 1) & 1);
       tc_fence_after();
-      softmax_sync();
-      const bool whole = kb0 == 0 && kb1 == u.n_blocks;
-      const int64_t part0 = (2 * (int64_t)blockIdx.x + (first ? 0 : 1)) * N;
-      if (tid < N) {
-        const float m0 = s_nref[tid], m1 = s_nref[N + tid], ref = fminf(m0, m1);   // minus: the larger reference
-        float sum[2] = {0.f, 0.f};
-#pragma unroll
-        for (int w = 0; w < 8; ++w) sum[w >> 2] += s_part[w * N + tid];
-        const float c0 = m0 == NONE ? 0.f : exp2_fast(ref - m0), c1 = m1 == NONE ? 0.f : exp2_fast(ref - m1);
-        const float both = sum[0] * c0 + sum[1] * c1;
-        const float inv = !whole ? 1.f : both == 0.f ? 0.f : 1.f / both;
-        s_fac[tid] = c0 * inv;
-        s_fac[N + tid] = c1 * inv;
-        if (!whole && s_place[tid] >= 0)
-          __stcg(a.part_ml + part0 + tid, make_float2(both == 0.f ? -INFINITY : -ref, both));
-      }
-      softmax_sync();
+      group_sync(t);
       const bool odd = !Q8 && *s_odd == piece + 1;
-      // O^T: the thread's column of D (r), this group's half of the rows
+      // O^T: the thread's column of D (r), the group's rows
 #pragma unroll 1
-      for (int x0 = t * (N / 2); x0 < (t + 1) * (N / 2); x0 += 16) {
-        float o[16], o1[16];
+      for (int x0 = 0; x0 < H; x0 += 16) {
+        float o[16];
         __syncwarp();
-        tc_ld16(tO(0) + x0, o);
-        if (nb > 1) tc_ld16(tO(1) + x0, o1);
-        wait_ld();
+        tc_ld16(tO + x0, o);
+        if constexpr (!Q8) {
+          float lo[16];
+          tc_ld16(tO + N + x0, lo);
+          wait_ld();
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          o[k] *= s_fac[x0 + k];
-          if (nb > 1) o[k] = fmaf(o1[k], s_fac[N + x0 + k], o[k]);
+          for (int k = 0; k < 16; ++k) o[k] += lo[k];
+        } else {
+          wait_ld();
         }
         if (odd && r < D) {
           // values that are not finite, of the keys that a row reads in the blocks looked through
           const uint16_t* const vp = reinterpret_cast<const uint16_t*>(a.v);
 #pragma unroll 1
-          for (int key = max(kb0, max(0, lim_all + 1) / KB) * KB; key < min(u.n_keys, kb1 * KB); ++key) {
-            const int page = page_of(a.t, u.b, key);
+          for (int key = max(kb0, max(0, lim_all + 1) / KB) * KB; key < min(done.n_keys, kb1 * KB); ++key) {
+            const int page = page_of(a.t, done.b, key);
             if (page < 0) continue;
             const uint16_t x = __ldcg(
-                vp + pool_row(a.t, a.layer, a.n_heads_kv, page, u.head,
+                vp + pool_row(a.t, a.layer, a.n_heads_kv, page, done.head,
                               (int)((uint32_t)key % (uint32_t)a.t.page_size)) * D + r);
             if ((x & 0x7f80u) != 0x7f80u) continue;
 #pragma unroll
             for (int k = 0; k < 16; ++k)
-              if (reads(x0 + k, key) & 1u) o[k] += bf16_bits_to_f32(x);
+              if (reads(c0 + x0 + k, key) & 1u) o[k] += bf16_bits_to_f32(x);
           }
         }
         if (r < D) {
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
-            const int64_t place = s_place[x0 + k];
+            const int64_t place = s_place[c0 + x0 + k];
             if (place < 0) continue;
-            if (whole) a.O[place + r] = f32_to_bf16_bits(o[k]);
-            else __stcg(a.part_o + (part0 + x0 + k) * D + r, o[k]);
+            if (whole) a.O[place + r] = f32_to_bf16_bits(o[k] * fac[x0 + k]);
+            else __stcg(a.part_o + place + r, o[k]);
           }
         }
       }
-      tc_fence_before();   // O^T is read before the next piece's Q is announced
-      block += nb;
-      plan.next(u);
     }
   } else if (Q8 ? warp >= 8 + C::CONV : warp > 8) {
     if (warp == C::MMA_WARP) {
       // -------------------------------------------------------- MMA issuer
       // The whole warp walks through this, with values that the compiler can see to be
       // the same in all lanes, and elects the lane that issues (chunk_attn_tc.cu).
-      constexpr uint32_t id_s = idesc(N, !Q8, false), id_o = idesc(N, !Q8, true, true);
+      constexpr uint32_t id_s = idesc(N, !Q8, false), id_o = idesc(C::P_COLS, !Q8, true, true);
       const uint32_t tm = __shfl_sync(~0u, tmem, 0);
-      uint32_t block = 0, n_q = 0, n_p[2] = {0, 0};
+      uint32_t block = 0, n_q = 0;
       // descriptors of the first step; a step further is a constant in the address field
       const uint64_t q_desc = desc_k(q_s), p_desc = desc_mn(p_s), v_desc = desc_mn(ring_s),
                      k_desc = desc_k(ring_s + C::HALF);
+      static_assert(C::P_LINES == KB * 128, "the next 64 columns lie where desc_mn says");
       auto full = [&](uint32_t b) { return gate.wait_warp(kv_full(b), (b / SLOTS) & 1); };
-      auto commit = [&](uint32_t bar) {
-        if (elect_one()) tc_commit(bar);
-        __syncwarp();
-      };
-      auto scores = [&](int t, uint32_t b) {
+      auto scores = [&](uint32_t b) {
         if (elect_one()) {
           const uint64_t kd = k_desc + b % SLOTS * (C::SLOT >> 4);
+          const uint32_t to = tm + (b & 1) * N;
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            mma_ss(tm + t * N, kd + (((k >> 2) * (KB * 128) + (k & 3) * 32) >> 4),
+            mma_ss(to, kd + (((k >> 2) * (KB * 128) + (k & 3) * 32) >> 4),
                    q_desc + (((k >> 2) * (N * 128) + (k & 3) * 32) >> 4), id_s, k > 0);
-          tc_commit(s_full(t));
+          tc_commit(s_full(b));
         }
         __syncwarp();
       };
       // V of block b lies beside K of the next.  (D = 64: lanes 64 .. 127 are formed from what lies
       // behind V, and not read.)
-      auto output = [&](int t, uint32_t b, bool add) {
+      auto output = [&](uint32_t b, bool add, bool last) {
         if (elect_one()) {
-          const uint64_t vd = v_desc + (b + 1) % SLOTS * (C::SLOT >> 4), pd = p_desc + t * (C::P_GROUP >> 4);
+          const uint64_t vd = v_desc + (b + 1) % SLOTS * (C::SLOT >> 4), pd = p_desc + (b & 1) * (C::P_BYTES >> 4);
 #pragma unroll
-          for (int k = 0; k < KB / 16; ++k) {
-            mma_ss(tm + (2 + t) * N, vd + k * (2048 >> 4), pd + k * (2048 >> 4), id_o, add || k > 0);
-            if constexpr (!Q8)   // the weights' second halves
-              mma_ss(tm + (2 + t) * N, vd + k * (2048 >> 4), pd + ((C::P_HALF + k * 2048) >> 4), id_o, true);
-          }
+          for (int k = 0; k < KB / 16; ++k)
+            mma_ss(tm + 2 * N, vd + k * (2048 >> 4), pd + k * (2048 >> 4), id_o, add || k > 0);
+          // (the last slot's K is the next unit's first)
+          if (!last) tc_commit(kv_empty(b + 1));
+          tc_commit(o_full(b));
         }
         __syncwarp();
       };
@@ -578,58 +592,67 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
         const int kb0 = (int)(at - u.begin), kb1 = (int)min((int64_t)u.n_blocks, line_hi - u.begin);
         at = u.begin + kb1;
         const int nb = __shfl_sync(~0u, kb1 - kb0, 0);
-        ok = gate.wait_warp(q_full, n_q++ & 1);
+        ok = gate.wait_warp(q_full, n_q++ & 1) && full(block);
+        if (!ok) break;
         tc_fence_after();
-        for (int i = 0; i < 2 && i < nb && ok; ++i) {
-          ok = full(block + i);
-          if (!ok) break;
-          scores(i, block + i);
-          // (V of the block before, of another unit, has been used)
-          if (i == 0) commit(kv_empty(block));
+        scores(block);
+        if (elect_one()) tc_commit(kv_empty(block));   // (V of the block before has been used)
+        __syncwarp();
+        if (nb > 1) {
+          ok = full(block + 1);
+          if (ok) scores(block + 1);
         }
-        for (int i = 0; i < nb && ok; i += 2) {
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (i + t >= nb || !ok) break;
-            ok = full(block + i + t + 1) && gate.wait_warp(p_full(t), n_p[t]++ & 1);
-            if (!ok) break;
-            tc_fence_after();
-            output(t, block + i + t, i > 0);
-            if (i + t + 1 < nb) commit(kv_empty(block + i + t + 1));
-            if (i + t + 2 < nb) {
-              ok = full(block + i + t + 2);
-              if (ok) scores(t, block + i + t + 2);
-            }
+        for (int i = 0; i < nb && ok; ++i, ++block) {
+          ok = full(block + 1) && gate.wait_warp(p_full(block), (block >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          output(block, i > 0, i + 1 == nb);
+          if (i + 2 < nb) {
+            ok = full(block + 2);
+            if (ok) scores(block + 2);
           }
         }
-        if (ok) commit(o_full);
-        block += nb;
       }
     } else if (Q8 && warp <= C::MMA_WARP + C::PLAN) {
       // ------------------------------------- pool rows and scales of the keys
-      // Two blocks, and one block, ahead of the conversion.
+      // Each block's page numbers are asked for in one round, its rows formed in the next and
+      // announced three blocks ahead of the conversion, its scales asked for then and stored
+      // in the round after: no round waits for what it asks for.
       constexpr int KEYS = KB / 64;   // per lane: keys x0, x0 + 32
-      static_assert(C::PLAN != 1 && KEYS == 2, "two warps, two keys per lane");
+      static_assert(!Q8 || (C::PLAN == 2 && KEYS == 2), "two warps, two keys per lane");
       const int pw = warp - C::MMA_WARP - 1, x0 = pw * 64 + lane;
+      int page[KEYS], place[KEYS], head = 0;   // place -1: past the last key
+      int row[KEYS];                  // of the block whose scales come next
       float ksc[KEYS], vsc[KEYS];
       unsigned gone[KEYS];            // of 32 keys: which stand on no page
-      auto look_up = [&](uint32_t j) {   // called for j = 0, 1, ..
+      auto ask_pages = [&](uint32_t j) {   // called for j = 0, 1, ..
         if (j >= n) return;
         if (j > 0) step();
-        int row[KEYS];
+        head = u.head;
 #pragma unroll
-        for (int h = 0; h < KEYS; ++h) row[h] = row_of(x0 + 32 * h);
-#pragma unroll
-        for (int h = 0; h < KEYS; ++h) s_rows[(j & 3) * KB + x0 + 32 * h] = row[h];
+        for (int h = 0; h < KEYS; ++h) {
+          const int key = kb * KB + x0 + 32 * h, entry = a.by_page.quot(key);
+          place[h] = key >= u.n_keys ? -1 : key - entry * a.t.page_size;
+          page[h] = key >= u.n_keys ? 0 : a.t.pages[(int64_t)u.b * a.t.width + entry];
+        }
       };
-      auto load_scales = [&](uint32_t j) {
+      auto form_rows = [&](uint32_t j) {
+        if (j >= n) return;
+#pragma unroll
+        for (int h = 0; h < KEYS; ++h)
+          s_rows[(j & 7) * KB + x0 + 32 * h] =
+              place[h] < 0 ? -1
+                           : (unsigned)page[h] >= (unsigned)a.t.n_pages
+                                 ? -2
+                                 : (int)pool_row(a.t, a.layer, a.n_heads_kv, page[h], head, place[h]);
+      };
+      auto ask_scales = [&](uint32_t j) {
         if (j >= n) return;
 #pragma unroll
         for (int h = 0; h < KEYS; ++h) {
-          const int row = s_rows[(j & 3) * KB + x0 + 32 * h];
-          gone[h] = __ballot_sync(~0u, row == -2);
-          ksc[h] = row >= 0 ? __ldcg(a.ks + row) : 0.f;
-          vsc[h] = row >= 0 ? __ldcg(a.vs + row) : 0.f;
+          row[h] = s_rows[(j & 7) * KB + x0 + 32 * h];
+          ksc[h] = row[h] >= 0 ? __ldcg(a.ks + row[h]) : 0.f;
+          vsc[h] = row[h] >= 0 ? __ldcg(a.vs + row[h]) : 0.f;
         }
       };
       auto store_scales = [&](uint32_t j) {
@@ -642,6 +665,7 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
           const bool fine = fabsf(vsc[h]) < INFINITY;
           sc[x0 + 32 * h] = fine ? ksc[h] : __int_as_float(0x7fc00000);
           sc[KB + x0 + 32 * h] = fine ? vsc[h] : 1.f;
+          gone[h] = __ballot_sync(~0u, row[h] == -2);
         }
         if (lane == 0) {
 #pragma unroll
@@ -650,16 +674,21 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
                 (uint8_t)((gone[h] & 1u) | ((gone[h] >> 16) & 1u) << 1);
         }
       };
-      look_up(0);
-      look_up(1);
-      meet_planners<C::CONV + C::PLAN>();
-      load_scales(0);
+      for (uint32_t j = 0; j < 3; ++j) {
+        ask_pages(j);
+        form_rows(j);
+      }
+      meet_planners<C::CONV + C::PLAN>();   // rows 0, 1, 2
+      ask_scales(0);
       store_scales(0);
-      meet_planners<C::CONV + C::PLAN>();
+      ask_scales(1);
+      ask_pages(3);
+      meet_planners<C::CONV + C::PLAN>();   // scales 0
       for (uint32_t j = 0; j <= n && n > 0; ++j) {
-        load_scales(j + 1);
-        look_up(j + 2);
         store_scales(j + 1);
+        form_rows(j + 3);
+        ask_scales(j + 2);
+        ask_pages(j + 4);
         meet_planners<C::CONV + C::PLAN>();
       }
     }
@@ -671,6 +700,14 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
       const int half = lane & 1, side = lane >> 4, b0 = (lane & 15) >> 1;
       const int n_box = KB / box;
       const bool mine = b0 < n_box && half < D / 64;
+      // pool row of key x of the next block; -1: past the last key, -2: on no page
+      auto row_of = [&](int x) {
+        const int key = kb * KB + x;
+        if (key >= u.n_keys) return -1;
+        const int entry = a.by_page.quot(key), page = a.t.pages[(int64_t)u.b * a.t.width + entry];
+        if ((unsigned)page >= (unsigned)a.t.n_pages) return -2;
+        return (int)pool_row(a.t, a.layer, a.n_heads_kv, page, u.head, key - entry * a.t.page_size);
+      };
       int row = n > 0 && b0 < n_box ? row_of(b0 * box) : -1, before = -1;
       uint32_t j = 0;
       for (; j <= n && n > 0; ++j) {
@@ -679,10 +716,6 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
         // rows of the pool, one per box; past the pool (zeros) where there is no page
         const int y = side ? before : row;
         before = row;
-        if (j + 1 < n) {   // a block ahead
-          step();
-          row = b0 < n_box ? row_of(b0 * box) : -1;
-        }
         if (j >= SLOTS) ok = gate.wait_warp(kv_empty(j), ((j / SLOTS) - 1) & 1);
         if (!ok) break;
         if (lane == 0) {
@@ -698,21 +731,25 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
           tma_load_2d(ring_s + j % SLOTS * C::SLOT + (side ? 0 : C::HALF) + half * (KB * 128) +
                           b0 * box * 128,
                       side ? &maps.v : &maps.k, half * 64, y < 0 ? pool_rows : y, kv_full(j));
+        if (j + 1 < n) {   // a block ahead
+          step();
+          row = b0 < n_box ? row_of(b0 * box) : -1;
+        }
       }
       // the copies issued last: none may be under way when the CTA ends, whatever its consumers did
       for (uint32_t i = j > SLOTS ? j - SLOTS : 0; i < j; ++i)
         mbar_wait_polls(kv_full(i), (i / SLOTS) & 1, 1u << 20);
     } else {
-      // Four lanes take 64 codes of a key, a warp's load eight keys, as soon as their
-      // registers are free, under the conversion of the other half.
+      // Four lanes take 64 codes of a key, a warp's load eight keys, two blocks ahead of
+      // their conversion.
       constexpr int HV = D / 64, KEYS = C::CONV * 8, L = KB / KEYS * HV;   // halves of a row, keys per pass, loads
       const int ptid = tid - 256, c = ptid & 3, k0 = ptid >> 2;
-      uint4 wk[L], wv[L];
+      uint4 wk[2][L], wv[2][L];
       auto load = [&](const void* pool, uint4 (&w)[L], uint32_t j) {
         const uint8_t* const p = reinterpret_cast<const uint8_t*>(pool) + c * 16;
 #pragma unroll
         for (int i = 0; i < L; i += HV) {
-          const int row = s_rows[(j & 3) * KB + i / HV * KEYS + k0];
+          const int row = s_rows[(j & 7) * KB + i / HV * KEYS + k0];
 #pragma unroll
           for (int h = 0; h < HV; ++h)
             w[i + h] = row >= 0 ? ldg_cg_v4(p + (int64_t)row * D + h * 64)
@@ -734,23 +771,32 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
         }
       };
       meet_planners<C::CONV + C::PLAN>();
-      if (n > 0) load(a.k, wk, 0);
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (n > x) {
+          load(a.k, wk[x], x);
+          load(a.v, wv[x], x);
+        }
       meet_planners<C::CONV + C::PLAN>();
       // no thread leaves this loop early (they meet in it): after a wait ran out
       // they only go on writing to their own shared memory
-      for (uint32_t j = 0; j <= n && n > 0; ++j) {
-        if (j >= SLOTS) gate.wait(kv_empty(j), ((j / SLOTS) - 1) & 1);
-        const uint32_t slot = ring_s + j % SLOTS * C::SLOT;
-        if (j < n) {
-          put(wk, slot + C::HALF);
-          if (j + 1 < n) load(a.k, wk, j + 1);
+      for (uint32_t j0 = 0; j0 <= n && n > 0; j0 += 2) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t j = j0 + x;
+          if (j > n) break;
+          if (j >= SLOTS) gate.wait(kv_empty(j), ((j / SLOTS) - 1) & 1);
+          const uint32_t slot = ring_s + j % SLOTS * C::SLOT;
+          if (j < n) put(wk[x], slot + C::HALF);
+          if (j > 0) put(wv[1 - x], slot);
+          fence_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(kv_full(j));
+          // (rows up to block j + 2 are there)
+          if (j + 2 < n) load(a.k, wk[x], j + 2);
+          if (j > 0 && j + 1 < n) load(a.v, wv[1 - x], j + 1);
+          meet_planners<C::CONV + C::PLAN>();   // and those of block j + 3 and the scales of block j + 1
         }
-        if (j > 0) put(wv, slot);
-        fence_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(kv_full(j));
-        if (j < n) load(a.v, wv, j);
-        meet_planners<C::CONV + C::PLAN>();   // the rows of block j + 2 and the scales of block j + 1 are there
       }
     }
   }

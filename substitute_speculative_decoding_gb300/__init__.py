@@ -438,6 +438,26 @@ def _run(fn, device, stream, *args):
         _check(code)
 
 
+def _run_scratch(fn, device, stream, size, *args):
+    """_run with `size` bytes of workspace that the call's stream has to itself, as the last
+    arguments.  From torch's allocator without a tensor around it: among driver calls
+    torch.empty costs the host 5 us, this 2."""
+    i = device.index
+    if torch._C._cuda_getDevice() != i:
+        with torch.cuda.device(i):
+            return _run_scratch(fn, device, stream, size, *args)
+    if size == 0:
+        return _run(fn, device, stream, *args, None, 0)
+    st = torch._C._cuda_getCurrentRawStream(i) if stream is None else stream.cuda_stream
+    p = torch._C._cuda_cudaCachingAllocator_raw_alloc(size, st)
+    try:
+        code = fn(*args, p, size, st)
+    finally:
+        torch._C._cuda_cudaCachingAllocator_raw_delete(p)
+    if code != SUB_OK:
+        _check(code)
+
+
 def _paged(struct, dtype, k, v, page_table, scales=()):
     dev = _gpu(k, "k")
     if k.dim() != 5:
@@ -622,14 +642,13 @@ def _attend(fn, q, kv, layer, batch, extra, scale, out, workspace, stream):
     if out is None:
         out = _new((n, hq, d), torch.bfloat16, dev, stream, True)
     at = _dense(out, torch.bfloat16, (n, hq, d), "out", dev)
+    args = (q.data_ptr(), ldq, hq, kv, layer, batch, *extra, d ** -0.5 if scale is None else scale, at)
     if workspace is None:
         size = _workspace_bytes(dev.index, hq, kv.n_heads_kv, d, batch.n_seqs, n)
-        workspace = _new(size, torch.uint8, dev, stream, False)
+        _run_scratch(fn, dev, stream, size, *args)
     else:
-        size = workspace.numel()
-        _dense(workspace, torch.uint8, workspace.shape, "workspace", dev)
-    _run(fn, dev, stream, q.data_ptr(), ldq, hq, kv, layer, batch, *extra,
-         d ** -0.5 if scale is None else scale, at, workspace.data_ptr() or None, size)
+        ws = _dense(workspace, torch.uint8, workspace.shape, "workspace", dev)
+        _run(fn, dev, stream, *args, ws or None, workspace.numel())
     return out
 
 
@@ -682,17 +701,15 @@ def beam_select(logits, score, n_best: int, temperature: float = 1.0, state=None
     if len(out) != len(kinds):
         _refuse("out: must be token, parent, score and, with state, the new states")
     at = [_dense(x, t, s, f"out[{i}]", dev) for i, (x, s, t) in enumerate(zip(out, shapes, kinds))]
-    size = _beam_bytes(b, n, v)
+    args = (_dense(logits, torch.float32, (b, n, v), "logits", dev),
+            _dense(score, torch.float32, (b, n), "score", dev), b, n, v, temperature, n_best,
+            None if state is None else _dense(state, torch.int32, (b, n, words), "state", dev), words,
+            slot, at[0], at[1], at[2], at[3] if state is not None else None)
     if workspace is None:
-        workspace = _new(size, torch.uint8, dev, stream, False)
+        _run_scratch(_beam_select, dev, stream, _beam_bytes(b, n, v), *args)
     else:
-        size = workspace.numel()
-        _dense(workspace, torch.uint8, workspace.shape, "workspace", dev)
-    _run(_beam_select, dev, stream, _dense(logits, torch.float32, (b, n, v), "logits", dev),
-         _dense(score, torch.float32, (b, n), "score", dev), b, n, v, temperature, n_best,
-         None if state is None else _dense(state, torch.int32, (b, n, words), "state", dev), words,
-         slot, at[0], at[1], at[2], at[3] if state is not None else None,
-         workspace.data_ptr() or None, size)
+        ws = _dense(workspace, torch.uint8, workspace.shape, "workspace", dev)
+        _run(_beam_select, dev, stream, *args, ws or None, workspace.numel())
     return tuple(out)
 
 

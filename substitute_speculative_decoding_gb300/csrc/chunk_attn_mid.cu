@@ -6,18 +6,21 @@
 // every key once per tile of 16; the kernel of 256 rows (chunk_attn_tc.cu) gives each
 // row a thread, and 224 of them are idle.  Here both products are turned over, so that
 // the keys take the tensor cores' 128 lanes and the N = 32 or 64 rows their columns:
-//   S^T = K Q^T   [128 keys x N], a key per thread: its scales and its masks are the thread's own
-//                 (codes are converted bare, two instructions for two of them), and a
-//                 block costs N exponentials per thread, not 128
+//   S^T = K Q^T   [128 keys x N], a key per thread: its scales and its masks are the thread's own,
+//                 and a block costs N exponentials per thread, not 128
 //   O^T = V^T P^T [D x N], with P^T written to shared memory as it is formed (bf16: two
 //                 halves, hi in the columns of a product and lo beside them; codes: fp16 times V's scale)
 // Roles:
 //   warps 0-3, 4-7   softmax of the first and the second half of the rows, block by block: the
 //                    scores of the next block and the output of the last are formed meanwhile
-//   a producer       as in chunk_attn_tc.cu: a TMA warp (bf16), or eight warps that turn
-//                    codes into fp16 (code - 128), exactly, with two warps that look
-//                    the keys up and gather their scales ahead
+//   two warps        copies (TMA) of K and of V into rings of blocks of 128 keys, in boxes of as many
+//                    keys as a page holds together; the pages of two blocks are looked up ahead
 //   one MMA warp
+//   warps 8-11, 12-15   codes: K and V into fp16 (code - 128, exactly; two instructions for two of
+//                    them), K into tensor memory, a key per lane, V into shared memory.  (Codes
+//                    loaded straight into registers, 64 KB of them under way, queue for the 29 KB that
+//                    shared memory leaves to L1: 16 sequences of 32 heads, 10000 keys on average,
+//                    took 136 us.)
 //
 // The running maximum of a row lies across the threads, so it is not formed in every
 // block: each thread compares its scores with the references of its rows, and only if
@@ -44,36 +47,49 @@ __device__ unsigned int g_mid_timeouts;   // waits that ran out (never expected)
 template <int D, bool Q8, int N>
 struct MidCfg {
   static_assert(N == 32 || N == 64, "rows of a tile: a warp's lanes hold one or two each");
-  static constexpr int HALF = KB * D * 2;                // K or V of a block, 16-bit values
-  static constexpr int SLOT = 2 * HALF;                  // V of a block, K of the next
-  static constexpr int SLOTS = D == 64 ? 3 : 2;
+  static constexpr int TILE = KB * D * 2;                // K or V of a block, 16-bit values
+  static constexpr int SLOTS = !Q8 && D == 64 ? 4 : 2;   // of V, bf16: and of K
+  static constexpr int CODES = Q8 ? KB * D : 0;          // K or V of a block, codes
+  static constexpr int RAW = Q8 ? D == 64 ? 4 : 3 : 0;   // blocks of codes
   static constexpr int Q_BYTES = N * D * 2;
   static constexpr int H = N / 2;                        // of a group
   // A key's weights: lines of 64 columns.  bf16: N = 32 hi and lo in one, N = 64 one each
   static constexpr int P_LINES = KB * 128, P_COLS = Q8 ? N : 2 * N;
   static constexpr int P_BYTES = P_COLS > 64 ? 2 * P_LINES : P_LINES;   // of a block; two of them
-  static constexpr int CONV = Q8 ? 8 : 0;                // converter warps
-  static constexpr int MMA_WARP = 8 + (Q8 ? CONV : 1);
-  static constexpr int PLAN = Q8 ? 2 : 0;                // then warps that look the keys up
-  static constexpr int THREADS = Q8 ? 640 : 384;         // whole groups of four warps
+  static constexpr int COPY_WARP = Q8 ? 16 : 8;          // K's; the next is V's
+  static constexpr int MMA_WARP = COPY_WARP + 2;
+  static constexpr int THREADS = (MMA_WARP + 2) * 32;    // whole groups of four warps
   // codes: registers by group of four warps, out of 65536 / THREADS each at the launch
   static constexpr int REGS_SOFTMAX = 128, REGS_CONV = 80, REGS_MMA = 64;
-  static_assert(!Q8 || (2 * REGS_SOFTMAX + CONV / 4 * REGS_CONV + REGS_MMA) * 128 <=
-                           65536 / THREADS / 8 * 8 * THREADS,
+  static_assert(!Q8 || (2 * REGS_SOFTMAX + 2 * REGS_CONV + REGS_MMA) * 128 <= 65536 / THREADS / 8 * 8 * THREADS,
                 "the shares fit what the block is launched with");
   static constexpr float GROWTH = Q8 ? 3.f : 8.f;        // log2 of how far weights may exceed the reference
   static constexpr float SHIFT = Q8 ? 11.f : 0.f;        // log2 of the weight at it
-  static constexpr int SCALES = Q8 ? 8 * 2 * KB * 4 : 0; // eight blocks' scales of K, of V
-  static constexpr int ROWS = Q8 ? 8 * KB * 4 : 0;       // pool rows of eight blocks' keys
+  // Eight blocks' scales of K, of V.  (K's copies run at most RAW + SLOTS blocks ahead of the scores
+  // that are formed, and those one ahead of the softmax.)
+  static constexpr int SCALES = Q8 ? 8 * 2 * KB * 4 : 0;
+  static_assert(RAW + SLOTS + 1 < 8, "scales are read before their place is written again");
   // of the rows: place in O, last key, mask, factor, minus the reference, whether a key was
   // read, factor of what was formed and difference of the reference; [4 warps] maxima or sums
   static constexpr int INFO = N * (8 + 7 * 4 + 4 * 4);
-  static constexpr int TAIL = 256;                       // barriers, flags, TMEM address
-  static constexpr int TMEM = 2 * N + P_COLS <= 128 ? 128 : 256;   // columns: S^T of two blocks, O^T
-  static constexpr int SMEM = 1024 + 2 * P_BYTES + Q_BYTES + SLOTS * SLOT + SCALES + ROWS + INFO + TAIL;
+  static constexpr int TAIL = 512;                       // barriers, flags, TMEM address
+  static constexpr int RING = (Q8 ? 1 : 2) * SLOTS * TILE + 2 * RAW * CODES;
+  // columns: S^T of two blocks, O^T, codes: K of two blocks
+  static constexpr int TM_O = 2 * N, TM_K = TM_O + P_COLS, COLS = TM_K + (Q8 ? D : 0);
+  static constexpr int TMEM = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
+  static constexpr int SMEM = 1024 + 2 * P_BYTES + Q_BYTES + RING + SCALES + INFO + TAIL;
   static_assert(SMEM <= 227 * 1024, "one CTA's shared memory");
-  static_assert(SLOTS * SLOT >= (SUB_MAX_SEQS + 1) * 8, "the ring holds the running sums first");
+  static_assert(RING >= (SUB_MAX_SEQS + 1) * 8, "the ring holds the running sums first");
 };
+
+// Untiled copy: both addresses 16-byte aligned.  (A tiled one would want its place in shared memory
+// at 128 bytes, and 16 scales are 64.)
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, int bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar)
+      : "memory");
+}
 
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 4, 256;" ::: "memory"); }
 __device__ __forceinline__ void group_sync(int t) { asm volatile("bar.sync %0, 128;" ::"r"(t + 1) : "memory"); }
@@ -117,16 +133,18 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* const base_p = smem_raw + (base - smem_u32(smem_raw));
-  const uint32_t p_s = base, q_s = p_s + 2 * C::P_BYTES, ring_s = q_s + C::Q_BYTES;
-  int64_t* const s_pre = reinterpret_cast<int64_t*>(base_p + (ring_s - base));   // until the first copies
-  uint8_t* at_p = base_p + (ring_s - base) + SLOTS * C::SLOT;
+  // (V's ring is followed by another: at D = 64 the product reads 64 columns past a block, for lanes
+  // that nobody reads)
+  const uint32_t p_s = base, q_s = p_s + 2 * C::P_BYTES, v_s = q_s + C::Q_BYTES, k_s = v_s + SLOTS * C::TILE,
+                 raw_s = v_s + SLOTS * C::TILE;   // bf16: K's blocks; codes: K's, then V's
+  int64_t* const s_pre = reinterpret_cast<int64_t*>(base_p + (v_s - base));   // until the first copies
+  uint8_t* at_p = base_p + (v_s - base) + C::RING;
   auto take = [&](int bytes) {
     uint8_t* const p = at_p;
     at_p += bytes;
     return p;
   };
   float* const s_scale = reinterpret_cast<float*>(take(C::SCALES));    // [8][K: KB, V: KB]
-  int* const s_rows = reinterpret_cast<int*>(take(C::ROWS));           // [8][KB]
   int64_t* const s_place = reinterpret_cast<int64_t*>(take(N * 8));    // of a row in O; -1: none
   float* const s_qs = reinterpret_cast<float*>(take(N * 4));           // codes: factor of a row's scores
   float* const s_nref = reinterpret_cast<float*>(take(N * 4));         // SHIFT - reference
@@ -138,19 +156,28 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
   int* const s_mask = reinterpret_cast<int*>(take(N * 4));             // row of the masks
   uint8_t* const tail = take(C::TAIL);
   const uint32_t bars = smem_u32(tail);
-  auto kv_full = [&](uint32_t block) { return bars + 8u * (block % SLOTS); };
-  auto kv_empty = [&](uint32_t block) { return bars + 8u * (SLOTS + block % SLOTS); };
-  auto s_full = [&](uint32_t block) { return bars + 8u * (2 * SLOTS + (block & 1)); };
-  auto p_full = [&](uint32_t block) { return bars + 8u * (2 * SLOTS + 2 + (block & 1)); };
-  auto o_full = [&](uint32_t block) { return bars + 8u * (2 * SLOTS + 4 + (block & 1)); };
-  const uint32_t q_full = bars + 8u * (2 * SLOTS + 6);
-  int* const flags = reinterpret_cast<int*>(tail + 8 * (2 * SLOTS + 7));
+  constexpr int BARS = 4 * SLOTS + 4 * C::RAW + 7;
+  auto ring = [&](int which, uint32_t block) { return bars + 8u * (which * SLOTS + block % SLOTS); };
+  auto k_full = [&](uint32_t block) { return ring(0, block); };
+  auto k_empty = [&](uint32_t block) { return ring(1, block); };
+  auto v_full = [&](uint32_t block) { return ring(2, block); };
+  auto v_empty = [&](uint32_t block) { return ring(3, block); };
+  auto raw_full = [&](int side, uint32_t block) {   // codes of K, of V
+    return bars + 8u * (4 * SLOTS + 2 * side * C::RAW + block % max(C::RAW, 1));
+  };
+  auto raw_empty = [&](int side, uint32_t block) { return raw_full(side, block) + 8u * C::RAW; };
+  auto pair = [&](int which, uint32_t block) { return bars + 8u * (BARS - 7 + 2 * which + (block & 1)); };
+  auto s_full = [&](uint32_t block) { return pair(0, block); };
+  auto p_full = [&](uint32_t block) { return pair(1, block); };
+  auto o_full = [&](uint32_t block) { return pair(2, block); };
+  const uint32_t q_full = bars + 8u * (BARS - 1);
+  int* const flags = reinterpret_cast<int*>(tail + 8 * BARS);
   volatile int* const s_dead = flags;                // a wait ran out
   volatile int* const s_odd = flags + 1;             // 1 + the last piece that met infinite values or NaN
   volatile int* const s_force = flags + 2;           // [group] a row has read no key yet
   volatile uint32_t* const s_miss = reinterpret_cast<uint32_t*>(flags + 4);   // [8] blocks' missing 16-key parts
   uint32_t* const s_tmem = reinterpret_cast<uint32_t*>(flags + 12);
-  static_assert(8 * (2 * SLOTS + 7) + 13 * 4 <= C::TAIL, "tail");
+  static_assert(8 * BARS + 13 * 4 <= C::TAIL, "tail");
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (warp == 0) {
@@ -161,10 +188,17 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (tid == 32) {
-    for (int s = 0; s < SLOTS; ++s) {
-      mbar_init(kv_full(s), Q8 ? C::CONV : 1);
-      mbar_init(kv_empty(s), 1);
+    for (int i = 0; i < SLOTS; ++i) {
+      mbar_init(k_full(i), Q8 ? 4 : 1);   // an arrival for each warp, or the copies'
+      mbar_init(v_full(i), Q8 ? 4 : 1);
+      mbar_init(k_empty(i), 1);
+      mbar_init(v_empty(i), 1);
     }
+    for (int i = 0; i < C::RAW; ++i)
+      for (int side = 0; side < 2; ++side) {
+        mbar_init(raw_full(side, i), 1);
+        mbar_init(raw_empty(side, i), 4);
+      }
     for (int b = 0; b < 2; ++b) {
       mbar_init(s_full(b), 1);
       mbar_init(p_full(b), 8);   // one arrival for each softmax warp
@@ -175,7 +209,7 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
     *s_odd = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (!Q8 && tid == 64) {
+  if (tid == 64) {
     tma_prefetch_desc(&maps.k);
     tma_prefetch_desc(&maps.v);
   }
@@ -195,9 +229,7 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
   __syncthreads();
   const Gate gate{s_dead, &g_mid_timeouts};
   const int G = a.group;
-  // Slot j of the ring holds V of block j - 1 and K of block j, across the units;
-  // the first has no V, the last no K.
-  const uint32_t n = (uint32_t)(line_hi > line_lo ? line_hi - line_lo : 0);
+  const uint32_t n = (uint32_t)(line_hi > line_lo ? line_hi - line_lo : 0);   // blocks, across the units
   int kb = (int)(line_lo - u.begin);   // the next block to look up, of unit u
   auto step = [&] {
     if (++kb == u.n_blocks) {
@@ -208,7 +240,7 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
 
   if constexpr (Q8) {
     if (warp < 8) more_registers<C::REGS_SOFTMAX>();
-    else if (warp < 8 + C::CONV) fewer_registers<C::REGS_CONV>();
+    else if (warp < C::COPY_WARP) fewer_registers<C::REGS_CONV>();
     else fewer_registers<C::REGS_MMA>();
   }
 
@@ -217,7 +249,7 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
     const int t = warp >> 2, wq = warp & 3, r = wq * 32 + lane;   // group, the thread's key of a block (or column of O)
     const int c0 = t * H;                                         // the group's rows
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
-    const uint32_t tS = tmem + c0 + lanes, tO = tmem + 2 * N + c0 + lanes;
+    const uint32_t tS = tmem + c0 + lanes, tO = tmem + C::TM_O + c0 + lanes;
     float* const nref = s_nref + c0;
     float* const fac = s_fac + c0;
     uint32_t block = 0;             // of this CTA's part of the line
@@ -311,9 +343,13 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
         float f = a.sl2, lv = 0.f, part = 1.f, back = 1.f;
         if constexpr (Q8) {
           const float* const sc = s_scale + (block & 7) * (2 * KB);
-          const float vv = sc[KB + r];   // finite
+          // a row that reads a key whose scale of V is not finite gets NaN by its score; weight 0
+          // times it stays 0
+          float vv = sc[KB + r];
+          const bool fine = fabsf(vv) < INFINITY;
+          vv = fine ? vv : 1.f;
           const int e = min(126, max(-80, (int)((__float_as_uint(vv) >> 23) & 255u) - 127));
-          f = sc[r];
+          f = fine ? sc[r] : __int_as_float(0x7fc00000);
           lv = (float)e;
           back = __uint_as_float((uint32_t)(127 - e) << 23);   // 2^-e
           part = vv * back;
@@ -334,7 +370,7 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
         }
         if (behind || miss) {
           // lane x: the warp's 32 keys, as the group's row x reads them
-          const uint32_t gone = miss >> miss_bit<Q8>(2 * wq);
+          const uint32_t gone = miss >> (2 * wq);
           const uint32_t there = ((gone & 1u) ? 0u : 0xffffu) | ((gone & 2u) ? 0u : 0xffff0000u);
           const uint32_t word = lane < H ? reads(c0 + lane, key0 + wq * 32) & there : 0u;
 #pragma unroll
@@ -440,8 +476,8 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
         }
         if (!Q8 && behind && t == 0) {
           // V of the block: its row r is this thread's
-          gate.wait_warp(kv_full(block + 1), ((block + 1) / SLOTS) & 1);
-          const uint32_t v0 = ring_s + (block + 1) % SLOTS * C::SLOT + r * 128;
+          gate.wait_warp(v_full(block), (block / SLOTS) & 1);
+          const uint32_t v0 = v_s + block % SLOTS * C::TILE + r * 128;
           const bool past = key0 + r >= u.n_keys;
           uint32_t z = 0;   // 0 * x is NaN for what is not finite
 #pragma unroll 4
@@ -548,256 +584,176 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
         }
       }
     }
-  } else if (Q8 ? warp >= 8 + C::CONV : warp > 8) {
-    if (warp == C::MMA_WARP) {
-      // -------------------------------------------------------- MMA issuer
-      // The whole warp walks through this, with values that the compiler can see to be
-      // the same in all lanes, and elects the lane that issues (chunk_attn_tc.cu).
-      constexpr uint32_t id_s = idesc(N, !Q8, false), id_o = idesc(C::P_COLS, !Q8, true, true);
-      const uint32_t tm = __shfl_sync(~0u, tmem, 0);
-      uint32_t block = 0, n_q = 0;
-      // descriptors of the first step; a step further is a constant in the address field
-      const uint64_t q_desc = desc_k(q_s), p_desc = desc_mn(p_s), v_desc = desc_mn(ring_s),
-                     k_desc = desc_k(ring_s + C::HALF);
-      static_assert(C::P_LINES == KB * 128, "the next 64 columns lie where desc_mn says");
-      auto full = [&](uint32_t b) { return gate.wait_warp(kv_full(b), (b / SLOTS) & 1); };
-      auto scores = [&](uint32_t b) {
-        if (elect_one()) {
-          const uint64_t kd = k_desc + b % SLOTS * (C::SLOT >> 4);
-          const uint32_t to = tm + (b & 1) * N;
+  } else if (warp < C::COPY_WARP) {
+    // ------------------------------------------------------ codes into fp16
+    // A key per thread.  Chunk c of a row of codes lies at c ^ (row % 8) of its 128-byte line, or of
+    // its half of one: eight lanes read all banks.
+    if constexpr (Q8) {
+      const int side = (warp - 8) >> 2, key = (warp & 3) * 32 + lane;   // K, V
+      const uint32_t raw0 = raw_s + side * (C::RAW * C::CODES) + key * D, turn = D == 128 ? key & 7 : (key >> 1) & 3;
+      const uint32_t tK = tmem + C::TM_K + ((uint32_t)((warp & 3) * 32) << 16);
+      for (uint32_t j = 0; j < n; ++j) {
+        if (!gate.wait_warp(raw_full(side, j), (j / C::RAW) & 1)) break;
+        if (j >= SLOTS && !gate.wait_warp(side ? v_empty(j) : k_empty(j), ((j / SLOTS) - 1) & 1)) break;
+        if (side == 0) tc_fence_after();
+        const uint32_t raw = raw0 + j % C::RAW * C::CODES;
+        const uint32_t to = v_s + j % SLOTS * C::TILE + key * 128;
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            mma_ss(to, kd + (((k >> 2) * (KB * 128) + (k & 3) * 32) >> 4),
-                   q_desc + (((k >> 2) * (N * 128) + (k & 3) * 32) >> 4), id_s, k > 0);
-          tc_commit(s_full(b));
-        }
-        __syncwarp();
-      };
-      // V of block b lies beside K of the next.  (D = 64: lanes 64 .. 127 are formed from what lies
-      // behind V, and not read.)
-      auto output = [&](uint32_t b, bool add, bool last) {
-        if (elect_one()) {
-          const uint64_t vd = v_desc + (b + 1) % SLOTS * (C::SLOT >> 4), pd = p_desc + (b & 1) * (C::P_BYTES >> 4);
+        for (int c = 0; c < D / 16; c += 2) {
+          uint32_t x[16];
 #pragma unroll
-          for (int k = 0; k < KB / 16; ++k)
-            mma_ss(tm + 2 * N, vd + k * (2048 >> 4), pd + k * (2048 >> 4), id_o, add || k > 0);
-          // (the last slot's K is the next unit's first)
-          if (!last) tc_commit(kv_empty(b + 1));
-          tc_commit(o_full(b));
-        }
-        __syncwarp();
-      };
-      bool ok = true;
-      for (int64_t at = line_lo; at < line_hi && ok; plan.next(u)) {
-        const int kb0 = (int)(at - u.begin), kb1 = (int)min((int64_t)u.n_blocks, line_hi - u.begin);
-        at = u.begin + kb1;
-        const int nb = __shfl_sync(~0u, kb1 - kb0, 0);
-        ok = gate.wait_warp(q_full, n_q++ & 1) && full(block);
-        if (!ok) break;
-        tc_fence_after();
-        scores(block);
-        if (elect_one()) tc_commit(kv_empty(block));   // (V of the block before has been used)
-        __syncwarp();
-        if (nb > 1) {
-          ok = full(block + 1);
-          if (ok) scores(block + 1);
-        }
-        for (int i = 0; i < nb && ok; ++i, ++block) {
-          ok = full(block + 1) && gate.wait_warp(p_full(block), (block >> 1) & 1);
-          if (!ok) break;
-          tc_fence_after();
-          output(block, i > 0, i + 1 == nb);
-          if (i + 2 < nb) {
-            ok = full(block + 2);
-            if (ok) scores(block + 2);
+          for (int h = 0; h < 2; ++h) {
+            const uint4 w = lds128(raw + (((c + h) ^ turn) << 4));
+            const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              x[8 * h + 2 * y] = codes2(v[y], 0x4140u);
+              x[8 * h + 2 * y + 1] = codes2(v[y], 0x4342u);
+            }
+          }
+          if (side == 0) {
+            tc_st16(tK + (j & 1) * (D / 2) + c * 8, x);
+          } else {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {   // 16-byte chunks 2 c .. 2 c + 3 of the row
+              const int f = 2 * c + h;
+              st_shared(to + (f >> 3) * (KB * 128) + (((f & 7) ^ (key & 7)) << 4), x[4 * h], x[4 * h + 1],
+                        x[4 * h + 2], x[4 * h + 3]);
+            }
           }
         }
-      }
-    } else if (Q8 && warp <= C::MMA_WARP + C::PLAN) {
-      // ------------------------------------- pool rows and scales of the keys
-      // Each block's page numbers are asked for in one round, its rows formed in the next and
-      // announced three blocks ahead of the conversion, its scales asked for then and stored
-      // in the round after: no round waits for what it asks for.
-      constexpr int KEYS = KB / 64;   // per lane: keys x0, x0 + 32
-      static_assert(!Q8 || (C::PLAN == 2 && KEYS == 2), "two warps, two keys per lane");
-      const int pw = warp - C::MMA_WARP - 1, x0 = pw * 64 + lane;
-      int page[KEYS], place[KEYS], head = 0;   // place -1: past the last key
-      int row[KEYS];                  // of the block whose scales come next
-      float ksc[KEYS], vsc[KEYS];
-      unsigned gone[KEYS];            // of 32 keys: which stand on no page
-      auto ask_pages = [&](uint32_t j) {   // called for j = 0, 1, ..
-        if (j >= n) return;
-        if (j > 0) step();
-        head = u.head;
-#pragma unroll
-        for (int h = 0; h < KEYS; ++h) {
-          const int key = kb * KB + x0 + 32 * h, entry = a.by_page.quot(key);
-          place[h] = key >= u.n_keys ? -1 : key - entry * a.t.page_size;
-          page[h] = key >= u.n_keys ? 0 : a.t.pages[(int64_t)u.b * a.t.width + entry];
-        }
-      };
-      auto form_rows = [&](uint32_t j) {
-        if (j >= n) return;
-#pragma unroll
-        for (int h = 0; h < KEYS; ++h)
-          s_rows[(j & 7) * KB + x0 + 32 * h] =
-              place[h] < 0 ? -1
-                           : (unsigned)page[h] >= (unsigned)a.t.n_pages
-                                 ? -2
-                                 : (int)pool_row(a.t, a.layer, a.n_heads_kv, page[h], head, place[h]);
-      };
-      auto ask_scales = [&](uint32_t j) {
-        if (j >= n) return;
-#pragma unroll
-        for (int h = 0; h < KEYS; ++h) {
-          row[h] = s_rows[(j & 7) * KB + x0 + 32 * h];
-          ksc[h] = row[h] >= 0 ? __ldcg(a.ks + row[h]) : 0.f;
-          vsc[h] = row[h] >= 0 ? __ldcg(a.vs + row[h]) : 0.f;
-        }
-      };
-      auto store_scales = [&](uint32_t j) {
-        if (j >= n) return;
-        float* const sc = s_scale + (j & 7) * (2 * KB);
-#pragma unroll
-        for (int h = 0; h < KEYS; ++h) {
-          // a row that reads a key whose scale of V is not finite gets NaN by its
-          // score; weight 0 times it stays 0
-          const bool fine = fabsf(vsc[h]) < INFINITY;
-          sc[x0 + 32 * h] = fine ? ksc[h] : __int_as_float(0x7fc00000);
-          sc[KB + x0 + 32 * h] = fine ? vsc[h] : 1.f;
-          gone[h] = __ballot_sync(~0u, row[h] == -2);
-        }
-        if (lane == 0) {
-#pragma unroll
-          for (int h = 0; h < KEYS; ++h)   // 16-key parts: bits 0 and 16 of 32 keys
-            reinterpret_cast<volatile uint8_t*>(s_miss + (j & 7))[2 * pw + h] =
-                (uint8_t)((gone[h] & 1u) | ((gone[h] >> 16) & 1u) << 1);
-        }
-      };
-      for (uint32_t j = 0; j < 3; ++j) {
-        ask_pages(j);
-        form_rows(j);
-      }
-      meet_planners<C::CONV + C::PLAN>();   // rows 0, 1, 2
-      ask_scales(0);
-      store_scales(0);
-      ask_scales(1);
-      ask_pages(3);
-      meet_planners<C::CONV + C::PLAN>();   // scales 0
-      for (uint32_t j = 0; j <= n && n > 0; ++j) {
-        store_scales(j + 1);
-        form_rows(j + 3);
-        ask_scales(j + 2);
-        ask_pages(j + 4);
-        meet_planners<C::CONV + C::PLAN>();
-      }
-    }
-  } else {
-    // ------------------------------------------------------------ producers
-    bool ok = true;
-    if constexpr (!Q8) {
-      // lanes 0..15 move K, 16..31 V: 64 columns (lane & 1) of the boxes (lane & 15) / 2, ..
-      const int half = lane & 1, side = lane >> 4, b0 = (lane & 15) >> 1;
-      const int n_box = KB / box;
-      const bool mine = b0 < n_box && half < D / 64;
-      // pool row of key x of the next block; -1: past the last key, -2: on no page
-      auto row_of = [&](int x) {
-        const int key = kb * KB + x;
-        if (key >= u.n_keys) return -1;
-        const int entry = a.by_page.quot(key), page = a.t.pages[(int64_t)u.b * a.t.width + entry];
-        if ((unsigned)page >= (unsigned)a.t.n_pages) return -2;
-        return (int)pool_row(a.t, a.layer, a.n_heads_kv, page, u.head, key - entry * a.t.page_size);
-      };
-      int row = n > 0 && b0 < n_box ? row_of(b0 * box) : -1, before = -1;
-      uint32_t j = 0;
-      for (; j <= n && n > 0; ++j) {
-        // 16-key parts without a page (those past the last key count as read past the end)
-        const unsigned gone = __ballot_sync(~0u, side == 0 && half == 0 && row == -2);
-        // rows of the pool, one per box; past the pool (zeros) where there is no page
-        const int y = side ? before : row;
-        before = row;
-        if (j >= SLOTS) ok = gate.wait_warp(kv_empty(j), ((j / SLOTS) - 1) & 1);
-        if (!ok) break;
-        if (lane == 0) {
-          uint32_t miss = 0;
-          if (gone)
-            for (int b = 0; b < n_box; ++b)
-              if ((gone >> (2 * b)) & 1u) miss |= ((1u << (box / 16)) - 1u) << (b * box / 16);
-          if (j < n) s_miss[j & 7] = miss;
-          mbar_expect_tx(kv_full(j), (j > 0 ? C::HALF : 0) + (j < n ? C::HALF : 0));
+        if (side == 0) {
+          wait_st();
+          tc_fence_before();
+        } else {
+          fence_async();
         }
         __syncwarp();
-        if (mine && (side ? j > 0 : j < n))
-          tma_load_2d(ring_s + j % SLOTS * C::SLOT + (side ? 0 : C::HALF) + half * (KB * 128) +
-                          b0 * box * 128,
-                      side ? &maps.v : &maps.k, half * 64, y < 0 ? pool_rows : y, kv_full(j));
-        if (j + 1 < n) {   // a block ahead
-          step();
-          row = b0 < n_box ? row_of(b0 * box) : -1;
+        if (lane == 0) {
+          mbar_arrive(raw_empty(side, j));
+          mbar_arrive(side ? v_full(j) : k_full(j));
         }
       }
-      // the copies issued last: none may be under way when the CTA ends, whatever its consumers did
-      for (uint32_t i = j > SLOTS ? j - SLOTS : 0; i < j; ++i)
-        mbar_wait_polls(kv_full(i), (i / SLOTS) & 1, 1u << 20);
-    } else {
-      // Four lanes take 64 codes of a key, a warp's load eight keys, two blocks ahead of
-      // their conversion.
-      constexpr int HV = D / 64, KEYS = C::CONV * 8, L = KB / KEYS * HV;   // halves of a row, keys per pass, loads
-      const int ptid = tid - 256, c = ptid & 3, k0 = ptid >> 2;
-      uint4 wk[2][L], wv[2][L];
-      auto load = [&](const void* pool, uint4 (&w)[L], uint32_t j) {
-        const uint8_t* const p = reinterpret_cast<const uint8_t*>(pool) + c * 16;
+    }
+  } else if (warp < C::MMA_WARP) {
+    // --------------------------------------------------------------- copies
+    const int side = warp - C::COPY_WARP;   // K, V
+    constexpr int DEPTH = Q8 ? C::RAW : SLOTS;
+    auto full = [&](uint32_t j) { return Q8 ? raw_full(side, j) : side ? v_full(j) : k_full(j); };
+    auto empty = [&](uint32_t j) { return Q8 ? raw_empty(side, j) : side ? v_empty(j) : k_empty(j); };
+    // lane: a box of the block; bf16: 64 columns of it, codes: its codes, or K's or V's scales
+    const int b0 = lane & 7, what = lane >> 3, n_box = KB / box;
+    const bool mine = b0 < n_box && what < (Q8 ? side ? 1 : 3 : D / 64);
+    // Each box's page is asked for two blocks ahead of its copy.
+    int page[2], place[2], head[2];   // place -1: past the last key
+    auto ask = [&](uint32_t j, int x) {   // called for j = 0, 1, ..
+      if (j >= n) return;
+      if (j > 0) step();
+      const int key = kb * KB + b0 * box, entry = a.by_page.quot(key);
+      const bool there = b0 < n_box && key < u.n_keys;
+      place[x] = there ? key - entry * a.t.page_size : -1;
+      page[x] = there ? a.t.pages[(int64_t)u.b * a.t.width + entry] : 0;
+      head[x] = u.head;
+    };
+    ask(0, 0);
+    ask(1, 1);
+    bool ok = true;
+    uint32_t j = 0;
+    while (j < n && ok) {
 #pragma unroll
-        for (int i = 0; i < L; i += HV) {
-          const int row = s_rows[(j & 7) * KB + i / HV * KEYS + k0];
-#pragma unroll
-          for (int h = 0; h < HV; ++h)
-            w[i + h] = row >= 0 ? ldg_cg_v4(p + (int64_t)row * D + h * 64)
-                                : make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
+      for (int x = 0; x < 2; ++x) {
+        if (j >= n) break;
+        if (j >= DEPTH) ok = gate.wait_warp(empty(j), ((j / DEPTH) - 1) & 1);
+        if (!ok) break;
+        const bool past = place[x] < 0, none = !past && (unsigned)page[x] >= (unsigned)a.t.n_pages;
+        // past the pool (zeros) where there is no page
+        const int row = past || none
+                            ? pool_rows
+                            : (int)pool_row(a.t, a.layer, a.n_heads_kv, page[x], head[x], place[x]);
+        if (side == 0) {   // the block's 16-key parts without a page
+          const unsigned gone = __ballot_sync(~0u, none && what == 0);
+          if (lane == 0) {
+            uint32_t miss = 0;
+            if (gone)
+              for (int b = 0; b < n_box; ++b)
+                if ((gone >> b) & 1u) miss |= ((1u << (box / 16)) - 1u) << (b * box / 16);
+            s_miss[j & 7] = miss;
+          }
         }
-      };
-      // 16 codes are chunks 2 c, 2 c + 1 of a half row's line; eight lanes' stores are
-      // those of two neighbouring keys, whose swizzles differ by one chunk: all banks
-      const uint32_t line = k0 * 128, x0 = (uint32_t)((2 * c) ^ (k0 & 7)) << 4;
-      auto put = [&](const uint4 (&w)[L], uint32_t dst) {
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-          const uint32_t at = dst + (i % HV) * (KB * 128) + i / HV * (KEYS * 128) + line;
-          const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-          for (int y = 0; y < 2; ++y)
-            st_shared(at + (x0 ^ (uint32_t)(y << 4)), codes2(v[2 * y], 0x4140u), codes2(v[2 * y], 0x4342u),
-                      codes2(v[2 * y + 1], 0x4140u), codes2(v[2 * y + 1], 0x4342u));
+        // scales come where there are some; elsewhere what lies there is not used
+        const unsigned scales = Q8 && side == 0 ? __popc(__ballot_sync(~0u, mine && what && !past && !none)) : 0;
+        if (lane == 0) mbar_expect_tx(full(j), Q8 ? C::CODES + scales * (box * 4) : C::TILE);
+        __syncwarp();
+        if (mine) {
+          if constexpr (Q8) {
+            if (what == 0)
+              tma_load_2d(raw_s + (side * C::RAW + j % C::RAW) * C::CODES + b0 * box * D, side ? &maps.v : &maps.k,
+                          0, row, full(j));
+            else if (!past && !none)
+              bulk_load(smem_u32(s_scale + (j & 7) * (2 * KB) + (what - 1) * KB + b0 * box),
+                        (what == 1 ? a.ks : a.vs) + row, box * 4, full(j));
+          } else {
+            tma_load_2d((side ? v_s : k_s) + j % SLOTS * C::TILE + what * (KB * 128) + b0 * box * 128,
+                        side ? &maps.v : &maps.k, what * 64, row, full(j));
+          }
         }
-      };
-      meet_planners<C::CONV + C::PLAN>();
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-        if (n > x) {
-          load(a.k, wk[x], x);
-          load(a.v, wv[x], x);
-        }
-      meet_planners<C::CONV + C::PLAN>();
-      // no thread leaves this loop early (they meet in it): after a wait ran out
-      // they only go on writing to their own shared memory
-      for (uint32_t j0 = 0; j0 <= n && n > 0; j0 += 2) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint32_t j = j0 + x;
-          if (j > n) break;
-          if (j >= SLOTS) gate.wait(kv_empty(j), ((j / SLOTS) - 1) & 1);
-          const uint32_t slot = ring_s + j % SLOTS * C::SLOT;
-          if (j < n) put(wk[x], slot + C::HALF);
-          if (j > 0) put(wv[1 - x], slot);
-          fence_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(kv_full(j));
-          // (rows up to block j + 2 are there)
-          if (j + 2 < n) load(a.k, wk[x], j + 2);
-          if (j > 0 && j + 1 < n) load(a.v, wv[1 - x], j + 1);
-          meet_planners<C::CONV + C::PLAN>();   // and those of block j + 3 and the scales of block j + 1
-        }
+        ++j;
+        ask(j + 1, x);
       }
+    }
+    // the copies issued last: none may be under way when the CTA ends, whatever its consumers did
+    for (uint32_t i = j > DEPTH ? j - DEPTH : 0; i < j; ++i) mbar_wait_polls(full(i), (i / DEPTH) & 1, 1u << 20);
+  } else if (warp == C::MMA_WARP) {
+    // ---------------------------------------------------------- MMA issuer
+    // The whole warp walks through this, with values that the compiler can see to be
+    // the same in all lanes, and elects the lane that issues (chunk_attn_tc.cu).
+    constexpr uint32_t id_s = idesc(N, !Q8, false), id_o = idesc(C::P_COLS, !Q8, true, true);
+    const uint32_t tm = __shfl_sync(~0u, tmem, 0);
+    uint32_t block = 0, n_q = 0;
+    // descriptors of the first step; a step further is a constant in the address field
+    const uint64_t q_desc = desc_k(q_s), p_desc = desc_mn(p_s), v_desc = desc_mn(v_s), k_desc = desc_k(k_s);
+    static_assert(C::P_LINES == KB * 128, "the next 64 columns lie where desc_mn says");
+    auto scores = [&](uint32_t b) {
+      if (!gate.wait_warp(k_full(b), (b / SLOTS) & 1)) return false;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t to = tm + (b & 1) * N;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t qd = q_desc + (((k >> 2) * (N * 128) + (k & 3) * 32) >> 4);
+          if constexpr (Q8)
+            mma_ts(to, tm + C::TM_K + (b & 1) * (D / 2) + k * 8, qd, id_s, k > 0);
+          else
+            mma_ss(to, k_desc + b % SLOTS * (C::TILE >> 4) + (((k >> 2) * (KB * 128) + (k & 3) * 32) >> 4), qd,
+                   id_s, k > 0);
+        }
+        tc_commit(s_full(b));
+        tc_commit(k_empty(b));
+      }
+      __syncwarp();
+      return true;
+    };
+    auto output = [&](uint32_t b, bool add) {
+      if (!gate.wait_warp(v_full(b), (b / SLOTS) & 1) || !gate.wait_warp(p_full(b), (b >> 1) & 1)) return false;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t vd = v_desc + b % SLOTS * (C::TILE >> 4), pd = p_desc + (b & 1) * (C::P_BYTES >> 4);
+#pragma unroll
+        for (int k = 0; k < KB / 16; ++k)
+          mma_ss(tm + C::TM_O, vd + k * (2048 >> 4), pd + k * (2048 >> 4), id_o, add || k > 0);
+        tc_commit(v_empty(b));
+        tc_commit(o_full(b));
+      }
+      __syncwarp();
+      return true;
+    };
+    bool ok = true;
+    for (int64_t at = line_lo; at < line_hi && ok; plan.next(u)) {
+      const int kb0 = (int)(at - u.begin), kb1 = (int)min((int64_t)u.n_blocks, line_hi - u.begin);
+      at = u.begin + kb1;
+      const int nb = __shfl_sync(~0u, kb1 - kb0, 0);
+      ok = gate.wait_warp(q_full, n_q++ & 1) && scores(block) && (nb == 1 || scores(block + 1));
+      for (int i = 0; i < nb && ok; ++i, ++block) ok = output(block, i > 0) && (i + 2 >= nb || scores(block + 2));
     }
   }
   tc_fence_before();
@@ -809,6 +765,10 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
 }
 
 // -------------------------------------------------------------------- host --
+// Rows of codes, in boxes of `box` rows.
+bool code_map(CUtensorMap* m, const void* pool, int64_t rows, int d, int box) {
+  return make_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, pool, d, rows, d, d, box, d);
+}
 template <int D, bool Q8, int N>
 int32_t launch(const ChunkArgs& a, int64_t rows, int n_ctas, cudaStream_t st) {
   using C = MidCfg<D, Q8, N>;
@@ -817,11 +777,14 @@ int32_t launch(const ChunkArgs& a, int64_t rows, int n_ctas, cudaStream_t st) {
                                 C::SMEM);
   }));
   Maps maps;
-  memset(&maps, 0, sizeof(maps));
   int box = 16;
   while (box < KB && a.t.page_size % (2 * box) == 0) box *= 2;
-  if (!Q8 && (!chunk_pool_map(&maps.k, a.k, rows, D, box) || !chunk_pool_map(&maps.v, a.v, rows, D, box)))
-    return fail(SUB_ECUDA, "chunk_tree_attn: the cache's tensor map was refused");
+  bool fine;
+  if constexpr (Q8)
+    fine = code_map(&maps.k, a.k, rows, D, box) && code_map(&maps.v, a.v, rows, D, box);
+  else
+    fine = chunk_pool_map(&maps.k, a.k, rows, D, box) && chunk_pool_map(&maps.v, a.v, rows, D, box);
+  if (!fine) return fail(SUB_ECUDA, "chunk_tree_attn: the cache's tensor map was refused");
   SUB_CUDA_TRY(launch_k(chunk_mid_kernel<D, Q8, N>, dim3(n_ctas), dim3(C::THREADS), C::SMEM, st, maps, a,
                         box, (int)rows));
   return SUB_OK;

@@ -692,15 +692,16 @@ def beam_select(logits, score, n_best: int, temperature: float = 1.0, state=None
         if state.dim() != 3:
             _refuse("state: must be [n_seqs, n_beams, words]")
         words = state.shape[2]
-    kinds = (torch.int32, torch.int32, torch.float32) + (torch.int32,) * (state is not None)
     shapes = ((b, n_best),) * 3 + ((b, n_best, words),) * (state is not None)
     if out is None:
         if n_best < 1:
             _refuse("n_best must be at least 1")
-        out = tuple(_new(s, t, dev, stream, False) for s, t in zip(shapes, kinds))
-    if len(out) != len(kinds):
-        _refuse("out: must be token, parent, score and, with state, the new states")
-    at = [_dense(x, t, s, f"out[{i}]", dev) for i, (x, s, t) in enumerate(zip(out, shapes, kinds))]
+        out = tuple(_new(s, t, dev, stream, False) for s, t in zip(shapes, _BEAM_TYPES))
+        at = [x.data_ptr() for x in out]
+    else:
+        if len(out) != len(shapes):
+            _refuse("out: must be token, parent, score and, with state, the new states")
+        at = [_dense(x, t, s, f"out[{i}]", dev) for i, (x, s, t) in enumerate(zip(out, shapes, _BEAM_TYPES))]
     args = (_dense(logits, torch.float32, (b, n, v), "logits", dev),
             _dense(score, torch.float32, (b, n), "score", dev), b, n, v, temperature, n_best,
             None if state is None else _dense(state, torch.int32, (b, n, words), "state", dev), words,
@@ -713,6 +714,7 @@ def beam_select(logits, score, n_best: int, temperature: float = 1.0, state=None
     return tuple(out)
 
 
+_BEAM_TYPES = (torch.int32, torch.int32, torch.float32, torch.int32)
 _beam_bytes = functools.lru_cache(maxsize=4096)(beam_workspace)
 
 

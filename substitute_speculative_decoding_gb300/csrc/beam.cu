@@ -8,13 +8,16 @@
 // all that can be chosen, and only their scores are formed.  Two launches:
 //
 // scan   one pass over the logits, bound by HBM: per CTA the running maximum and sum
-//        of exp, and the largest logit of every block of 128.
+//        of exp, and the largest logit of every block of 128.  512 rows of 128256: 47 us,
+//        5.6 TB/s, whatever the loads in flight (2 to 16 per thread) and CTAs per row.
 // pick   one cluster per sequence, a CTA per beam (or several): the k largest of the
 //        block maxima name k blocks that hold all of the k largest logits (a logit
 //        above which there are fewer than k others cannot lie in a block that k others
 //        exceed), which are read again, from L2; the beams' lists meet in the
 //        cluster's first CTA, where each candidate finds its place by bisection in the
-//        others' lists.  Bound by latency: some ten dependent steps.
+//        others' lists.  Bound by latency: some ten dependent steps, 8 us after the scan
+//        of 8 rows.  (16 us before the log of the sum had a warp of its own and the
+//        bisections several lanes and whole numbers to compare.)
 //
 // (Every CTA keeping the best of its part while it streams would need no second
 // reading, but a sorted list per thread costs the scan its loads in flight.)
@@ -110,69 +113,108 @@ __global__ void __launch_bounds__(SCAN_THREADS, 4) scan_kernel(const __grid_cons
 }
 
 // ------------------------------------------------------------------- pick --
-constexpr int PARTS = 128;   // a selection's threshold comes from the largest keys of so many parts
-static_assert(SUB_MAX_BEAMS <= PARTS && PICK_THREADS == 2 * PARTS, "two threads per part");
+// A selection's threshold comes from the largest keys of 64 parts (n_best up to 16: fewer
+// comparisons) or 128; `1 << part_threads` threads form a part.
+__host__ __device__ inline int part_threads(int k) { return k <= 16 ? 2 : 1; }
+static_assert(SUB_MAX_BEAMS <= PICK_THREADS / 2 && PICK_THREADS == 256, "parts for the largest n_best");
 
-// most keys that select() may have to compare with each other: n keys, the k largest
-__host__ __device__ inline int survivors(int n, int k) {
-  const int per = 2 * ((n + PICK_THREADS - 1) / PICK_THREADS);
-  return n < k * per ? n : k * per;
+// most keys that select() may have to compare with each other: n keys, the k largest, `per`
+// in a thread's hands
+__host__ __device__ inline int survivors(int n, int k, int per) {
+  const int most = k * (per << part_threads(k));
+  return n < most ? n : most;
+}
+constexpr int PICK_WARPS = PICK_THREADS / 32;
+__host__ __device__ inline int per_block_key(int n) { return (n + PICK_THREADS - 1) / PICK_THREADS; }
+__host__ __device__ inline int per_logit(int k) { return (k + PICK_WARPS - 1) / PICK_WARPS * 4; }
+
+__device__ __forceinline__ void pick_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ bool pick_any(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 q, %1, 0;\n barrier.cta.red.or.pred p, 1, 256, q;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
 }
 
 // The k largest of n keys in shared memory (all unlike; 0: none) to out, in falling order,
-// zeros behind them.  The k-th largest of 128 parts' largest keys is a threshold that k
-// keys reach and few others pass; those are ranked by counting.  By the whole CTA.
-__device__ void select(const uint64_t* keys, int n, int k, uint64_t* out, uint64_t* list, uint64_t* s_top,
-                       int* s_count) {
-  const int tid = threadIdx.x;
-  uint64_t best = 0;
-  for (int i = tid; i < n; i += PICK_THREADS) best = max(best, keys[i]);
-  best = max(best, (uint64_t)__shfl_xor_sync(~0u, (unsigned long long)best, 1));
-  if (!(tid & 1)) s_top[tid >> 1] = best;
+// zeros behind them; best: the largest of those that the thread wrote there.  The k-th
+// largest of the parts' largest keys is a threshold that k keys reach and few others
+// pass; those are ranked by counting, eight lanes for each.  By the first PICK_THREADS threads.
+__device__ void select(const uint64_t* keys, int n, int k, uint64_t best, uint64_t* out, uint64_t* list,
+                       uint64_t* s_top, int* s_count) {
+  const int tid = threadIdx.x, lg = part_threads(k), parts = PICK_THREADS >> lg;
+  for (int o = 1; o < 1 << lg; o <<= 1)
+    best = max(best, (uint64_t)__shfl_xor_sync(~0u, (unsigned long long)best, o));
   if (tid == 0) *s_count = 0;
   if (tid < k) out[tid] = 0;
-  __syncthreads();
-  int above = 0;   // parts whose largest key is above this one's; the two threads count a half each
+  const int at = tid & ((1 << lg) - 1), share = parts >> lg;   // of the comparisons
+  if (at == 0) s_top[tid >> lg] = best;
+  pick_sync();
+  int above = 0;   // parts whose largest key is above this one's
 #pragma unroll 8
-  for (int i = 0; i < PARTS / 2; ++i) above += s_top[2 * i + (tid & 1)] > best;
-  above += __shfl_xor_sync(~0u, above, 1);
+  for (int i = 0; i < share; i += 2) {
+    const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(s_top + at * share + i);
+    above += (x.x > best) + (x.y > best);
+  }
+  for (int o = 1; o < 1 << lg; o <<= 1) above += __shfl_xor_sync(~0u, above, o);
   // fewer than k parts with a key at all: every key is a candidate
   const bool mine = above == k - 1 && best != 0;
   uint64_t least = 1;
-  if (__syncthreads_or(mine)) {
-    if (mine && !(tid & 1)) s_top[0] = best;
-    __syncthreads();
+  if (pick_any(mine)) {
+    if (mine && at == 0) s_top[0] = best;
+    pick_sync();
     least = s_top[0];
   }
   for (int i = tid; i < n; i += PICK_THREADS)
     if (keys[i] >= least) list[atomicAdd(s_count, 1)] = keys[i];
-  __syncthreads();
+  pick_sync();
   const int found = *s_count;
-  for (int i = tid; i < found; i += PICK_THREADS) {
-    const uint64_t x = list[i];
+  for (int i0 = 0; i0 < found; i0 += PICK_THREADS / 8) {
+    const int i = i0 + (tid >> 3);
+    const uint64_t x = i < found ? list[i] : 0;
     int rank = 0;
-    for (int j = 0; j < found && rank < k; ++j) rank += list[j] > x;
-    if (rank < k) out[rank] = x;
+    for (int j = tid & 7; j < found; j += 8) rank += list[j] > x;
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) rank += __shfl_xor_sync(~0u, rank, o);
+    if ((tid & 7) == 0 && i < found && rank < k) out[rank] = x;
   }
-  __syncthreads();
+  pick_sync();
 }
 
 struct PickShared {
-  size_t list, cand_score, cand_token, bytes;   // offsets; the keys come first
+  size_t list, cand_key, cand_token, bytes;   // offsets; the keys come first
 };
 __host__ __device__ inline PickShared pick_shared(int n_blocks, int n_beams, int k) {
   const int n = n_blocks > k * 128 ? n_blocks : k * 128;
   PickShared p;
   p.list = (size_t)n * 8;
-  p.cand_score = p.list + (size_t)max(survivors(n_blocks, k), survivors(k * 128, k)) * 8;
-  p.cand_token = p.cand_score + (size_t)n_beams * k * 8;
+  p.cand_key = p.list + (size_t)max(survivors(n_blocks, k, per_block_key(n_blocks)),
+                                    survivors(k * 128, k, per_logit(k))) * 8;
+  p.cand_token = p.cand_key + (size_t)n_beams * k * 8;
   p.bytes = p.cand_token + (size_t)n_beams * k * 4;
   return p;
 }
 
-__global__ void __launch_bounds__(PICK_THREADS) pick_kernel(const __grid_constant__ BeamArgs a) {
+// Scores in whole numbers that compare as they do (a comparison of doubles takes ten times as
+// long), and back.
+__device__ __forceinline__ int64_t order_key(double x) {
+  const int64_t b = __double_as_longlong(x + 0.);   // (-0 and 0 are one value)
+  return b ^ (int64_t)((uint64_t)(b >> 63) >> 1);
+}
+__device__ __forceinline__ double order_value(int64_t k) {
+  return __longlong_as_double(k ^ (int64_t)((uint64_t)(k >> 63) >> 1));
+}
+
+// The first eight warps select; the ninth forms the log of the sum meanwhile, in 64 bits
+// (exponentials, a logarithm and a division of doubles: 10000 cycles when it came first).
+__global__ void __launch_bounds__(PICK_THREADS + 32) pick_kernel(const __grid_constant__ BeamArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ uint64_t s_top[PARTS], s_out[SUB_MAX_BEAMS];
+  __shared__ __align__(16) uint64_t s_top[PICK_THREADS / 2];
+  __shared__ uint64_t s_out[SUB_MAX_BEAMS];
   __shared__ int s_found, s_count[SUB_MAX_BEAMS];   // of the first CTA: candidates of each beam
   __shared__ int s_parent[SUB_MAX_BEAMS];
   __shared__ double s_lse;
@@ -184,7 +226,7 @@ __global__ void __launch_bounds__(PICK_THREADS) pick_kernel(const __grid_constan
   const PickShared at = pick_shared(a.n_blocks, a.n_beams, k);
   uint64_t* const keys = reinterpret_cast<uint64_t*>(smem);
   uint64_t* const list = reinterpret_cast<uint64_t*>(smem + at.list);
-  double* const cand_score = reinterpret_cast<double*>(smem + at.cand_score);
+  int64_t* const cand_key = reinterpret_cast<int64_t*>(smem + at.cand_key);
   int32_t* const cand_token = reinterpret_cast<int32_t*>(smem + at.cand_token);
   pdl_wait();
   pdl_trigger();
@@ -195,98 +237,117 @@ __global__ void __launch_bounds__(PICK_THREADS) pick_kernel(const __grid_constan
     const Row r(z, a.V);
     const int blocks = (r.n + BLOCK_GROUPS - 1) / BLOCK_GROUPS;
     const float score = __ldcg(a.score + row);
-    int n_cand = 0;
-    if (alive(score)) {
-      // ---- the log of the sum, by the first warp ----
-      if (warp == 0) {
-        float m = -INFINITY;
-        for (int c = lane; c < a.n_chunks; c += 32) m = fmaxf(m, __ldcg(a.part + row * a.n_chunks + c).x);
-        m = warp_max(m);
-        double s = 0.;
-        for (int c = lane; c < a.n_chunks; c += 32) {
-          const float2 p = __ldcg(a.part + row * a.n_chunks + c);
-          if (p.x != -INFINITY) s += (double)p.y * exp(((double)p.x - (double)m) / (double)a.temp);
-        }
+    uint64_t key = 0;    // the thread's candidate
+    double zt = 0.;
+    if (!alive(score)) {
+      // no candidates
+    } else if (warp == PICK_WARPS) {
+      // ---- the log of the sum ----
+      static_assert(MAX_CHUNKS == 64, "two per lane");
+      float2 p[2];
 #pragma unroll
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
-        if (lane == 0)   // not finite: no continuations
-          s_lse = fabsf(m) < INFINITY ? (double)m / (double)a.temp + log(s) : (double)INFINITY;
-      }
+      for (int h = 0; h < 2; ++h)
+        p[h] = lane + 32 * h < a.n_chunks ? __ldcg(a.part + row * a.n_chunks + lane + 32 * h)
+                                          : make_float2(-INFINITY, 0.f);
+      const float m = warp_max(fmaxf(p[0].x, p[1].x));
+      const bool finite = fabsf(m) < INFINITY;
+      const double top = (double)m / (double)a.temp, per = 1. / (double)a.temp;
+      double e[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        e[h] = p[h].x == -INFINITY || !finite ? 0. : (double)p[h].y * exp(((double)p[h].x - (double)m) * per);
+      double s = e[0] + e[1];
+#pragma unroll
+      for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+      if (lane == 0) s_lse = finite ? top + log(s) : (double)INFINITY;   // not finite: no continuations
+    } else {
       // ---- the blocks that hold the k largest logits ----
+      uint64_t best = 0;
       for (int i = tid; i < blocks; i += PICK_THREADS) {
         const float x = __ldcg(a.top + row * a.n_blocks + i);
-        keys[i] = x == -INFINITY ? 0 : rank_key(x, (uint32_t)i);
+        const uint64_t y = x == -INFINITY ? 0 : rank_key(x, (uint32_t)i);
+        keys[i] = y;
+        best = max(best, y);
       }
-      __syncthreads();
-      select(keys, blocks, k, s_out, list, s_top, &s_found);
+      select(keys, blocks, k, best, s_out, list, s_top, &s_found);
       // ---- their logits ----
       constexpr int AHEAD = 4;
-      for (int i0 = warp; i0 < k; i0 += PICK_THREADS / 32 * AHEAD) {
+      best = 0;
+      for (int i0 = warp; i0 < k; i0 += PICK_WARPS * AHEAD) {
         float4 x[AHEAD];
         int g[AHEAD];
 #pragma unroll
         for (int u = 0; u < AHEAD; ++u) {
-          const int i = i0 + u * (PICK_THREADS / 32);
-          const uint64_t key = i < k ? s_out[i] : 0;
-          g[u] = key ? (int)rank_idx(key) * BLOCK_GROUPS + lane : r.n;
+          const int i = i0 + u * PICK_WARPS;
+          const uint64_t y = i < k ? s_out[i] : 0;
+          g[u] = y ? (int)rank_idx(y) * BLOCK_GROUPS + lane : r.n;
           x[u] = g[u] < r.n ? load_group(z, r, g[u], -INFINITY)
                             : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
         }
 #pragma unroll
         for (int u = 0; u < AHEAD; ++u) {
-          const int i = i0 + u * (PICK_THREADS / 32);
+          const int i = i0 + u * PICK_WARPS;
           if (i >= k) break;
           const float v[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {   // (elements before and past the row are -infinity)
             const float c = clean(v[e]);
-            keys[i * 128 + e * 32 + lane] = c == -INFINITY ? 0 : rank_key(c, (uint32_t)(r.first(g[u]) + e));
+            const uint64_t y = c == -INFINITY ? 0 : rank_key(c, (uint32_t)(r.first(g[u]) + e));
+            keys[i * 128 + e * 32 + lane] = y;
+            best = max(best, y);
           }
         }
       }
-      __syncthreads();
-      select(keys, k * 128, k, s_out, list, s_top, &s_found);
-      if (s_lse < (double)INFINITY)
-        while (n_cand < k && s_out[n_cand]) ++n_cand;
+      pick_sync();   // s_out is read
+      select(keys, k * 128, k, best, s_out, list, s_top, &s_found);
+      if (tid < k) key = s_out[tid];
+      if (key) zt = (double)key_float((uint32_t)(key >> 32)) / (double)a.temp;
     }
+    __syncthreads();   // s_lse is there
     // ---- scores, to the cluster's first CTA ----
     if (alone) cluster_all_here();
     alone = false;
-    if (tid < n_cand) {
-      const uint64_t key = s_out[tid];
-      const double x = ((double)score + (double)key_float((uint32_t)(key >> 32)) / (double)a.temp) - s_lse;
-      *cluster.map_shared_rank(cand_score + j * k + tid, 0) = x;
+    if (key && !(s_lse < (double)INFINITY)) key = 0;
+    if (key) {
+      *cluster.map_shared_rank(cand_key + j * k + tid, 0) = order_key(((double)score + zt) - s_lse);
       *cluster.map_shared_rank(cand_token + j * k + tid, 0) = (int32_t)rank_idx(key);
     }
+    const int n_cand = __syncthreads_count(key != 0);   // s_out and s_lse are read
     if (tid == 0) *cluster.map_shared_rank(s_count + j, 0) = n_cand;
-    __syncthreads();   // s_out and s_lse are read
   }
   if (size > 1) cluster.sync();
+  else __syncthreads();
   if (rank != 0) return;
 
-  // ---- the first CTA: every candidate's place among all ----
+  // ---- the first CTA: every candidate's place among all, by 2^lg lanes for each ----
   if (tid < SUB_MAX_BEAMS) s_parent[tid] = -1;
   __syncthreads();
-  for (int i = tid; i < a.n_beams * k; i += PICK_THREADS) {
-    const int j = i / k, c = i - j * k;
-    if (c >= s_count[j]) continue;
-    const double x = cand_score[i];
-    int place = c;   // of its own beam's, so many come first
-    for (int o = 0; o < a.n_beams && place < k; ++o) {
-      if (o == j) continue;
-      int lo = 0, hi = s_count[o];   // its candidates that come before this one
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        const double y = cand_score[o * k + mid];
-        if (y > x || (y == x && o < j)) lo = mid + 1;
-        else hi = mid;
+  int lg = 0;
+  while (lg < 3 && (a.n_beams * k) << (lg + 1) <= PICK_THREADS) ++lg;
+  const int part = tid & ((1 << lg) - 1), total = a.n_beams * k;
+  for (int i0 = 0; i0 < total && warp < PICK_WARPS; i0 += PICK_THREADS >> lg) {
+    const int i = i0 + (tid >> lg), j = i / k, c = i - j * k;
+    const bool there = i < total && c < s_count[min(j, a.n_beams - 1)];
+    const int64_t x = there ? cand_key[i] : 0;
+    int place = 0;
+    if (there)
+      for (int o = part; o < a.n_beams && place < k; o += 1 << lg) {
+        if (o == j) continue;
+        int lo = 0, hi = s_count[o];   // its candidates that come before this one
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          const int64_t y = cand_key[o * k + mid];
+          if (y > x || (y == x && o < j)) lo = mid + 1;
+          else hi = mid;
+        }
+        place += lo;
       }
-      place += lo;
-    }
-    if (place >= k) continue;
+    for (int o = 1; o < 1 << lg; o <<= 1) place += __shfl_xor_sync(~0u, place, o);
+    place += c;   // of its own beam's, so many come first
+    if (!there || part != 0 || place >= k) continue;
     a.token[b * k + place] = cand_token[i];
     a.parent[b * k + place] = j;
-    a.score_out[b * k + place] = (float)x;
+    a.score_out[b * k + place] = (float)order_value(x);
     s_parent[place] = j;
   }
   __syncthreads();
@@ -297,7 +358,7 @@ __global__ void __launch_bounds__(PICK_THREADS) pick_kernel(const __grid_constan
   }
   // ---- the parents' states ----
   if (a.state_out)
-    for (int64_t i = tid; i < (int64_t)k * a.words; i += PICK_THREADS) {
+    for (int64_t i = tid; i < (int64_t)k * a.words; i += PICK_THREADS + 32) {
       const int p = (int)(i / a.words), w = (int)(i - (int64_t)p * a.words), j = s_parent[p];
       int32_t x = j < 0 ? 0 : __ldcg(a.state + (b * a.n_beams + j) * a.words + w);
       if (j >= 0 && a.slot >= 0 && (a.slot + p) >> 5 == w) x |= (int32_t)(1u << ((a.slot + p) & 31));
@@ -396,7 +457,7 @@ extern "C" int32_t sub_beam_select(const float* logits, const float* score, int3
   }));
   SUB_CUDA_TRY(launch_k(scan_kernel, dim3((unsigned)rows, a.n_chunks), dim3(SCAN_THREADS), 0, st, a));
   const int size = n_beams < MAX_CLUSTER ? n_beams : MAX_CLUSTER;
-  SUB_CUDA_TRY(launch_clusters(pick_kernel, n_seqs, size, PICK_THREADS,
+  SUB_CUDA_TRY(launch_clusters(pick_kernel, n_seqs, size, PICK_THREADS + 32,
                                pick_shared(a.n_blocks, n_beams, n_best).bytes, st, a));
   return SUB_OK;
 }

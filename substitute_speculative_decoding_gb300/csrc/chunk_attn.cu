@@ -890,10 +890,20 @@ int tile_rows(int group, int n_seqs, int n_rows, bool codes, int64_t keys) {
   return rows <= NARROW * seqs ? NARROW : rows <= tiles * WIDE * seqs ? WIDE : CHUNK_TC_ROWS;
 }
 
-// Trees: tiles of 32 or 64 rows (0: those above), by the rows that a sequence has on average.
-int tree_rows(int group, int n_seqs, int n_rows) {
+// Trees: tiles of 32 or 64 rows of the kernel with the keys on the lanes (0: the others), by
+// the rows that a sequence has on average.  It starts 1 to 2 us later than the warps' kernel
+// (22 rows over 600 keys 12 us and 10), reads the keys once where that one has several tiles
+// (32 rows of 16 sequences over 10000 keys 116 and 157 us, over codes 86 and 149), and does
+// not outlast the 256 rows' kernel until 128 rows or so (98 rows of 8 sequences 32 and 41 us,
+// 132 of 1 25 and 32, 188 of 8 90 and 81; over codes 98 rows 42 and 46, 100 rows 83 and 81).
+// 64 rows take longer per key than 32 (those 32 rows of 16 sequences 119 and 115 us), but
+// a sequence of 36 rows would make two tiles of 32: they are taken where all sequences may
+// have as many rows, as the levels of trees have, or few do (28 rows on average, of 20
+// or 36: 183 us with 32, 116 with 64).
+int tree_rows(int group, int n_seqs, int n_rows, int64_t keys) {
   const int64_t rows = (int64_t)n_rows * group, seqs = n_seqs;
-  return rows <= WIDE * seqs || rows > 64 * seqs ? 0 : rows <= 32 * seqs ? 32 : 64;
+  if (rows <= WIDE * seqs || rows > 128 * seqs || (rows <= 32 * seqs && keys <= 1024)) return 0;
+  return rows <= 24 * seqs || (rows <= 32 * seqs && n_rows % n_seqs == 0) ? 32 : 64;
 }
 
 // Partial results, two per CTA, and the list of cuts.
@@ -947,11 +957,11 @@ int32_t chunk_attn(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q, const Cach
     SUB_TRY(scratch.alloc((size_t)need));
     workspace = scratch.p;
   }
-  const int rt = tile_rows(a.group, a.t.n_seqs, a.t.n_rows, Q8,
-                           batch->max_keys ? std::min(batch->max_keys, kv->capacity) : kv->capacity);
+  const int64_t keys = batch->max_keys ? std::min(batch->max_keys, kv->capacity) : kv->capacity;
+  const int rt = tile_rows(a.group, a.t.n_seqs, a.t.n_rows, Q8, keys);
   const int64_t pool_rows =
       (int64_t)kv->n_layers * kv->n_pages * kv->n_heads_kv * kv->page_size;
-  const int mid = a.mask && chunk_tc_fits(pool_rows) ? tree_rows(a.group, a.t.n_seqs, a.t.n_rows) : 0;
+  const int mid = a.mask && chunk_tc_fits(pool_rows) ? tree_rows(a.group, a.t.n_seqs, a.t.n_rows, keys) : 0;
   if (mid) {
     a.part_o = reinterpret_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float2*>(a.part_o + (int64_t)n_ctas * 2 * mid * kv->head_dim);

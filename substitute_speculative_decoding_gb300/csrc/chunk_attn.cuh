@@ -111,6 +111,17 @@ __device__ __forceinline__ uint32_t mask_window(const uint32_t* mask, int words,
   return __funnelshift_r(word(i), at & 31 ? word(i + 1) : 0u, at & 31);
 }
 
+// The same for 128 keys, asked for together.
+__device__ __forceinline__ void mask_windows(const uint32_t* mask, int words, int at, uint32_t (&w)[4]) {
+  const int i = at >> 5;
+  uint32_t x[5];
+#pragma unroll
+  for (int k = 0; k < 5; ++k)
+    x[k] = i + k < 0 ? ~0u : i + k < words && (k < 4 || (at & 31)) ? __ldcg(mask + i + k) : 0u;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(x[k], x[k + 1], at & 31);
+}
+
 // ---------------------------------------------------------------- work plan --
 // A unit of work is one tile of RT rows -- (row, head in group) pairs of one
 // KV head of one sequence -- over all the keys its last row reads, in blocks of
@@ -266,7 +277,7 @@ bool chunk_tc_fits(int64_t pool_rows);   // rows of head_dim values in a pool
 int32_t launch_chunk_tc(const ChunkArgs& a, bool q8, int head_dim, int64_t pool_rows, int n_ctas,
                         cudaStream_t st);
 int32_t chunk_tc_timeouts(unsigned int* out);
-// The kernel for a few dozen rows of trees (chunk_attn_mid.cu): tiles of 32 or 64 rows.
+// The kernel for 17 to 128 rows of trees (chunk_attn_mid.cu): tiles of 32 or 64 rows.
 int32_t launch_chunk_mid(const ChunkArgs& a, bool q8, int head_dim, int rows, int64_t pool_rows, int n_ctas,
                          cudaStream_t st);
 int32_t chunk_mid_timeouts(unsigned int* out);

@@ -324,6 +324,7 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
                (left >= 31 ? ~0u : (2u << left) - 1u);
       };
 
+      bool force = true;   // a row has read no key yet
       float2 l[H / 2];
 #pragma unroll
       for (int x = 0; x < H / 2; ++x) l[x] = make_float2(0.f, 0.f);
@@ -332,10 +333,13 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
 #pragma unroll 1
       for (int i = 0; i < nb; ++i, ++block) {
         const int key0 = (kb0 + i) * KB;
+        const bool behind = key0 + KB - 1 > lim_all;
+        // lane x: the warp's 32 keys, as the group's row x reads them
+        uint32_t word = ~0u;
+        if (behind && lane < H) word = reads(c0 + lane, key0 + wq * 32);
         gate.wait_warp(s_full(block), (block >> 1) & 1);
         tc_fence_after();
         const uint32_t miss = s_miss[block & 7];
-        const bool behind = key0 + KB - 1 > lim_all;
         float s[H];
         if constexpr (H == 32) tc_ld32(tS + (block & 1) * N, s);
         else tc_ld16(tS + (block & 1) * N, s);
@@ -369,10 +373,8 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
           }
         }
         if (behind || miss) {
-          // lane x: the warp's 32 keys, as the group's row x reads them
           const uint32_t gone = miss >> (2 * wq);
-          const uint32_t there = ((gone & 1u) ? 0u : 0xffffu) | ((gone & 2u) ? 0u : 0xffff0000u);
-          const uint32_t word = lane < H ? reads(c0 + lane, key0 + wq * 32) & there : 0u;
+          word &= ((gone & 1u) ? 0u : 0xffffu) | ((gone & 2u) ? 0u : 0xffff0000u);
 #pragma unroll
           for (int x = 0; x < H; ++x)
             if (!((__shfl_sync(~0u, word, x) >> lane) & 1u)) s[x] = -INFINITY;
@@ -391,7 +393,7 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
           over[3] = fmaxf(over[3], s[x + 3] = a1.y);
         }
         const bool above = fmaxf(fmaxf(over[0], over[1]), fmaxf(over[2], over[3])) > C::GROWTH + C::SHIFT;
-        if (group_any(t, above) || i == 0 || s_force[t]) {
+        if (group_any(t, above || force)) {
           // ---- the references, and what was formed with others ----
           {
             float v[H];
@@ -423,6 +425,7 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
             if (lane == 0) s_force[t] = none;
           }
           group_sync(t);
+          force = s_force[t];
 #pragma unroll
           for (int x = 0; x < H; x += 2) {
             const float2 y = *reinterpret_cast<const float2*>(fac + x);
@@ -474,14 +477,15 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
           st_shared(chunk(c0 + x), hi[0], hi[1], hi[2], hi[3]);
           if constexpr (!Q8) st_shared(chunk(N + c0 + x), lo[0], lo[1], lo[2], lo[3]);
         }
-        if (!Q8 && behind && t == 0) {
-          // V of the block: its row r is this thread's
+        if (!Q8 && behind) {
+          // V of the block: half of its row r is this thread's
+          const int k0 = t * (D / 16);
           gate.wait_warp(v_full(block), (block / SLOTS) & 1);
           const uint32_t v0 = v_s + block % SLOTS * C::TILE + r * 128;
           const bool past = key0 + r >= u.n_keys;
           uint32_t z = 0;   // 0 * x is NaN for what is not finite
 #pragma unroll 4
-          for (int k = 0; k < D / 8; ++k) {
+          for (int k = k0; k < k0 + D / 16; ++k) {
             const uint32_t at16 = v0 + (k >> 3) * (KB * 128) + (((k ^ r) & 7) << 4);
             if (past) {
               st_shared(at16, 0, 0, 0, 0);
@@ -495,7 +499,7 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
           }
           if ((z & 0x7fff7fffu) != 0) {   // hardly ever: take them out, add them at the end
 #pragma unroll 1
-            for (int k = 0; k < D / 8; ++k) {
+            for (int k = k0; k < k0 + D / 16; ++k) {
               const uint32_t at16 = v0 + (k >> 3) * (KB * 128) + (((k ^ r) & 7) << 4);
               const uint4 v = lds128(at16);
               uint32_t x[4] = {v.x, v.y, v.z, v.w};
@@ -641,9 +645,7 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
     constexpr int DEPTH = Q8 ? C::RAW : SLOTS;
     auto full = [&](uint32_t j) { return Q8 ? raw_full(side, j) : side ? v_full(j) : k_full(j); };
     auto empty = [&](uint32_t j) { return Q8 ? raw_empty(side, j) : side ? v_empty(j) : k_empty(j); };
-    // lane: a box of the block; bf16: 64 columns of it, codes: its codes, or K's or V's scales
-    const int b0 = lane & 7, what = lane >> 3, n_box = KB / box;
-    const bool mine = b0 < n_box && what < (Q8 ? side ? 1 : 3 : D / 64);
+    const int b0 = lane & 7, n_box = KB / box;   // a box of the block
     // Each box's page is asked for two blocks ahead of its copy.
     int page[2], place[2], head[2];   // place -1: past the last key
     auto ask = [&](uint32_t j, int x) {   // called for j = 0, 1, ..
@@ -671,7 +673,7 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
                             ? pool_rows
                             : (int)pool_row(a.t, a.layer, a.n_heads_kv, page[x], head[x], place[x]);
         if (side == 0) {   // the block's 16-key parts without a page
-          const unsigned gone = __ballot_sync(~0u, none && what == 0);
+          const unsigned gone = __ballot_sync(~0u, none && lane < n_box);
           if (lane == 0) {
             uint32_t miss = 0;
             if (gone)
@@ -681,21 +683,30 @@ chunk_mid_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chun
           }
         }
         // scales come where there are some; elsewhere what lies there is not used
-        const unsigned scales = Q8 && side == 0 ? __popc(__ballot_sync(~0u, mine && what && !past && !none)) : 0;
-        if (lane == 0) mbar_expect_tx(full(j), Q8 ? C::CODES + scales * (box * 4) : C::TILE);
+        const unsigned some = Q8 && side == 0 ? __ballot_sync(~0u, lane < n_box && !past && !none) : 0;
+        const uint32_t bar = full(j);
+        if (lane == 0) mbar_expect_tx(bar, Q8 ? C::CODES + __popc(some) * (2 * box * 4) : C::TILE);
         __syncwarp();
-        if (mine) {
-          if constexpr (Q8) {
-            if (what == 0)
-              tma_load_2d(raw_s + (side * C::RAW + j % C::RAW) * C::CODES + b0 * box * D, side ? &maps.v : &maps.k,
-                          0, row, full(j));
-            else if (!past && !none)
-              bulk_load(smem_u32(s_scale + (j & 7) * (2 * KB) + (what - 1) * KB + b0 * box),
-                        (what == 1 ? a.ks : a.vs) + row, box * 4, full(j));
-          } else {
-            tma_load_2d((side ? v_s : k_s) + j % SLOTS * C::TILE + what * (KB * 128) + b0 * box * 128,
-                        side ? &maps.v : &maps.k, what * 64, row, full(j));
+        // one lane issues them all, with values that are the same in all lanes
+        const CUtensorMap* const map = side ? &maps.v : &maps.k;
+#pragma unroll 1
+        for (int b = 0; b < n_box; ++b) {
+          const int y = __shfl_sync(~0u, row, b);
+          if (elect_one()) {
+            if constexpr (Q8) {
+              tma_load_2d(raw_s + (side * C::RAW + j % C::RAW) * C::CODES + b * box * D, map, 0, y, bar);
+              if ((some >> b) & 1u) {
+                const uint32_t to = smem_u32(s_scale + (j & 7) * (2 * KB) + b * box);
+                bulk_load(to, a.ks + y, box * 4, bar);
+                bulk_load(to + KB * 4, a.vs + y, box * 4, bar);
+              }
+            } else {
+              const uint32_t to = (side ? v_s : k_s) + j % SLOTS * C::TILE + b * box * 128;
+#pragma unroll
+              for (int h = 0; h < D / 64; ++h) tma_load_2d(to + h * (KB * 128), map, h * 64, y, bar);
+            }
           }
+          __syncwarp();
         }
         ++j;
         ask(j + 1, x);

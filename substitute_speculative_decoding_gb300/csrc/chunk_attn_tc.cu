@@ -299,11 +299,15 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
       bool any = false;            // a key has been read
       for (int kb = kb0; kb < kb1; ++kb, ++block) {
         const int key0 = kb * KB;
+        const bool behind = key0 + KB - 1 > lim_first;   // the same for all rows of the tile
+        // TREE: the block's keys that the row's mask has, on their way during the wait.  (Asked for
+        // where they are used, with no register free, they came one after the other: 3 us per block.)
+        uint32_t win[4] = {~0u, ~0u, ~0u, ~0u};
+        if (TREE && behind) mask_windows(mask, a.words, key0 - base, win);
         if (!gate.wait_warp(s_full(t), n_s & 1)) break;
         ++n_s;
         tc_fence_after();
         const uint32_t miss = s_miss[block & 7];
-        const bool behind = key0 + KB - 1 > lim_first;   // the same for all rows of the tile
         const int last = lim - key0;                     // columns past it are not read
         const float* const sc = s_scale + (block & 7) * C::SCALE_SLOT;
         float lv = 0.f;   // log2 of what V's scales add to the weights
@@ -345,7 +349,8 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
             __syncwarp();
             tc_ld32(tS + x0, s);
             wait_ld();
-            const uint32_t gone = miss >> miss_bit<Q8>(x0 >> 4), read = seen(key0 + x0);
+            const uint32_t gone = miss >> miss_bit<Q8>(x0 >> 4);
+            const uint32_t read = !TREE ? ~0u : x0 < 64 ? x0 ? win[1] : win[0] : x0 == 64 ? win[2] : win[3];
             const int end = last - x0;
 #pragma unroll
             for (int x = 0; x < 32; x += 4) {
@@ -408,18 +413,20 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
             lv = pw.y;
           }
           wait_ld();
-          if (edge) {
+          if (edge && !TREE) {
 #pragma unroll
             for (int x = 0; x < KB; ++x)
               if (x > last || ((miss >> miss_bit<Q8>(x >> 4)) & 1u)) s[x] = -INFINITY;
-            if (TREE && behind) {
+          } else if (edge) {
 #pragma unroll
-              for (int x0 = 0; x0 < KB; x0 += 32) {
-                const uint32_t read = seen(key0 + x0);
+            for (int x0 = 0; x0 < KB; x0 += 32) {
+              const uint32_t gone = miss >> miss_bit<Q8>(x0 >> 4);
+              const int end = last - x0;   // columns past it are not read
+              const uint32_t read = win[x0 / 32] & (end >= 31 ? ~0u : end < 0 ? 0u : (2u << end) - 1u) &
+                                    ~((gone & 1u) * 0xffffu) & ~((gone >> 1 & 1u) * 0xffff0000u);
 #pragma unroll
-                for (int x = 0; x < 32; ++x)
-                  if (!((read >> x) & 1u)) s[x0 + x] = -INFINITY;
-              }
+              for (int x = 0; x < 32; ++x)
+                if (!((read >> x) & 1u)) s[x0 + x] = -INFINITY;
             }
           }
           // eight chains: a single one would wait for itself 128 times

@@ -270,6 +270,21 @@ def test_many_ctas_and_wide_masks(sub, bits_, n):
 
 
 @pytest.mark.parametrize("bits_", [16, 8])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page", [16, 48, 64, 128])
+@pytest.mark.parametrize("trees", [[(900, 9, 8), (0, 0, 8), (33, 1, 8)], [(129, 17, 7), (1500, 0, 9), (5, 0, 2)],
+                                   [(700, 3, 16)], [(260, 0, 31), (90, 40, 20), (0, 0, 45)]])
+def test_a_few_dozen_rows(sub, bits_, d, page, trees):
+    """Rows of one tile or two of the kernel with the keys on the lanes (which wants room
+    for more than 1024 of them), in boxes of all sizes."""
+    c = TreeCase(sub, trees, 8, 2, d, page=page, bits=bits_, kind="any", seed=page + d, width=70)
+    c.table_d[0, 2] = -1
+    see = [c.see(b) for b in range(len(trees))]
+    see[0][:, 2 * page:3 * page] = False
+    c.check_tree(c.run(), see=see)
+
+
+@pytest.mark.parametrize("bits_", [16, 8])
 @pytest.mark.parametrize("n", [2, 8, 60])
 def test_a_path_of_all_is_chunk_attention(sub, bits_, n):
     """Masks with all bits, and a base behind all keys."""

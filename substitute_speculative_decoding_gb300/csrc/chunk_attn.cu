@@ -158,7 +158,7 @@ chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__
   const ChunkPlan<RT, KB> plan(a);
   plan.template scan<NT>(s_pre);
   const int64_t total = s_pre[a.t.n_seqs];
-  const int64_t per = blocks_per_cta(total, gridDim.x, WARPS);
+  const int64_t per = blocks_per_cta(total, gridDim.x, TREE ? plan.least(total, WARPS) : WARPS);
   const uint8_t* const ring = smem + warp * R::BYTES;
   const float* const scales =
       reinterpret_cast<const float*>(smem + WARPS * R::BYTES + warp * (STAGES * R::SCALES));
@@ -891,18 +891,17 @@ int tile_rows(int group, int n_seqs, int n_rows, bool codes, int64_t keys) {
 }
 
 // Trees: tiles of 32 or 64 rows of the kernel with the keys on the lanes (0: the others), by
-// the rows that a sequence has on average.  It starts 1 to 2 us later than the warps' kernel
-// (22 rows over 600 keys 12 us and 10), reads the keys once where that one has several tiles
-// (32 rows of 16 sequences over 10000 keys 116 and 157 us, over codes 86 and 149), and does
-// not outlast the 256 rows' kernel until 128 rows or so (98 rows of 8 sequences 32 and 41 us,
-// 132 of 1 25 and 32, 188 of 8 90 and 81; over codes 98 rows 42 and 46, 100 rows 83 and 81).
-// 64 rows take longer per key than 32 (those 32 rows of 16 sequences 119 and 115 us), but
-// a sequence of 36 rows would make two tiles of 32: they are taken where all sequences may
-// have as many rows, as the levels of trees have, or few do (28 rows on average, of 20
-// or 36: 183 us with 32, 116 with 64).
-int tree_rows(int group, int n_seqs, int n_rows, int64_t keys) {
+// the rows that a sequence has on average.  It reads the keys once where the warps' kernel has
+// several tiles (32 rows of 16 sequences over 10000 keys 116 and 157 us, over codes 86 and 149; of
+// 1 over 1000 13 and 12), and does not outlast the 256 rows' kernel until 128 rows or so
+// (98 rows of 8 sequences 32 and 41 us, 132 of 1 25 and 32, 188 of 8 90 and 81; over codes 98
+// rows 42 and 46, 100 rows 83 and 81).  64 rows take longer per key than 32 (those 32
+// rows of 16 sequences 119 and 115 us), but a sequence of 36 rows would make two tiles of 32:
+// they are taken where all sequences may have as many rows, as the levels of trees have,
+// or few do (28 rows on average, of 20 or 36: 183 us with 32, 116 with 64).
+int tree_rows(int group, int n_seqs, int n_rows) {
   const int64_t rows = (int64_t)n_rows * group, seqs = n_seqs;
-  if (rows <= WIDE * seqs || rows > 128 * seqs || (rows <= 32 * seqs && keys <= 1024)) return 0;
+  if (rows <= WIDE * seqs || rows > 128 * seqs) return 0;
   return rows <= 24 * seqs || (rows <= 32 * seqs && n_rows % n_seqs == 0) ? 32 : 64;
 }
 
@@ -961,7 +960,7 @@ int32_t chunk_attn(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q, const Cach
   const int rt = tile_rows(a.group, a.t.n_seqs, a.t.n_rows, Q8, keys);
   const int64_t pool_rows =
       (int64_t)kv->n_layers * kv->n_pages * kv->n_heads_kv * kv->page_size;
-  const int mid = a.mask && chunk_tc_fits(pool_rows) ? tree_rows(a.group, a.t.n_seqs, a.t.n_rows, keys) : 0;
+  const int mid = a.mask && chunk_tc_fits(pool_rows) ? tree_rows(a.group, a.t.n_seqs, a.t.n_rows) : 0;
   if (mid) {
     a.part_o = reinterpret_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float2*>(a.part_o + (int64_t)n_ctas * 2 * mid * kv->head_dim);

@@ -200,6 +200,13 @@ struct ChunkPlan {
     __syncthreads();
   }
 
+  // Fewest blocks of a CTA, `most` where there are so many: where units are shorter, about a unit for
+  // each CTA.  (Eight units of one block, one after the other in one CTA, took 25 us, in eight 8.7.)
+  __device__ int least(int64_t total, int most) const {
+    const int64_t units = (int64_t)a.n_heads_kv * max((int64_t)a.t.n_seqs, ((int64_t)a.t.n_rows * a.group + RT - 1) / RT);
+    return (int)min((int64_t)most, max((int64_t)1, quot(total, units)));
+  }
+
   // the unit that block `at` (< pre[n_seqs]) of the line belongs to; by a whole warp
   __device__ ChunkUnit find(const int64_t* pre, int64_t at) const {
     const int lane = threadIdx.x & 31;

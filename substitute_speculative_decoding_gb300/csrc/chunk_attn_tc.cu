@@ -177,7 +177,7 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
   const int64_t total = s_pre[a.t.n_seqs];
-  const int64_t per = blocks_per_cta(total, gridDim.x, CHUNK_TC_LEAST);
+  const int64_t per = blocks_per_cta(total, gridDim.x, TREE ? plan.least(total, CHUNK_TC_LEAST) : CHUNK_TC_LEAST);
   const int64_t line_lo = blockIdx.x * per, line_hi = min(total, line_lo + per);
   ChunkUnit u;
   if (line_lo < line_hi) u = plan.find(s_pre, line_lo);

@@ -173,12 +173,12 @@ chunk_attn_kernel(const __grid_constant__ PageMaps maps, const __grid_constant__
     v_at[x] = R::LINE == 128 ? r * 128 + ((g ^ r) * 16)
                              : r * 64 + (((g >> 1) ^ tig) * 16) + (g & 1) * 8;
   }
-  const int64_t line_lo = blockIdx.x * per, line_hi = min(total, line_lo + per);
+  int64_t line_lo, line_hi;
+  ChunkUnit u = plan.template part<TREE>(s_pre, total, per, line_lo, line_hi);
   if (line_lo >= line_hi) {
     if (tid == 0) a.cuts[blockIdx.x].pieces = 0;
     return;
   }
-  ChunkUnit u = plan.find(s_pre, line_lo);
 
   // ---- the loads: the warp's blocks of all its units, one after the other ----
   // unit f, of which the warp reads blocks f0 + mine + i * WARPS, i < fn.  The last warps
@@ -864,7 +864,7 @@ int32_t launch_decode(const ChunkArgs& a, int n_ctas, cudaStream_t st) {
       !chunk_page_map(&maps.v, a.v, a.t, (int64_t)a.n_layers * a.n_heads_kv, D, Q8))
     return fail(SUB_ECUDA, "chunk_attn: the cache's tensor map was refused");
   SUB_CUDA_TRY(launch_k(chunk_attn_kernel<D, Q8, RT, TREE>, dim3(n_ctas), dim3(NT), SMEM, st, maps, a));
-  return launch_join<D, RT>(a, n_ctas, st);
+  return a.whole ? SUB_OK : launch_join<D, RT>(a, n_ctas, st);
 }
 template <bool Q8, bool TREE>
 int32_t launch_rows(const ChunkArgs& a, int d, int rt, int n_ctas, cudaStream_t st) {
@@ -957,6 +957,10 @@ int32_t chunk_attn(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q, const Cach
     workspace = scratch.p;
   }
   const int64_t keys = batch->max_keys ? std::min(batch->max_keys, kv->capacity) : kv->capacity;
+  // Trees over few keys: no unit is cut, which saves the second launch, 2 us of the host's time too
+  // (8 rows of 2 heads over 500 keys 8.1 us, cut 8.7, over 1000 10.3 and 8.6; of 8 sequences of 8
+  // heads, 32 rows, 14.2 and 15.7 over 1000, 19.9 and 17.3 over 2000).
+  a.whole = a.mask && (keys <= 640 || (keys <= 1024 && 3 * a.t.n_seqs * a.n_heads_kv >= n_ctas));
   const int rt = tile_rows(a.group, a.t.n_seqs, a.t.n_rows, Q8, keys);
   const int64_t pool_rows =
       (int64_t)kv->n_layers * kv->n_pages * kv->n_heads_kv * kv->page_size;
@@ -966,6 +970,7 @@ int32_t chunk_attn(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q, const Cach
     a.part_ml = reinterpret_cast<float2*>(a.part_o + (int64_t)n_ctas * 2 * mid * kv->head_dim);
     a.cuts = reinterpret_cast<ChunkCut*>(a.part_ml + (int64_t)n_ctas * 2 * mid);
     SUB_TRY(launch_chunk_mid(a, Q8, kv->head_dim, mid, pool_rows, n_ctas, st));
+    if (a.whole) return SUB_OK;
     if (mid == 32)
       return kv->head_dim == 128 ? launch_join<128, 32>(a, n_ctas, st) : launch_join<64, 32>(a, n_ctas, st);
     return kv->head_dim == 128 ? launch_join<128, 64>(a, n_ctas, st) : launch_join<64, 64>(a, n_ctas, st);
@@ -977,6 +982,7 @@ int32_t chunk_attn(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q, const Cach
   a.cuts = reinterpret_cast<ChunkCut*>(a.part_ml + (int64_t)n_ctas * 2 * part_rows);
   if (tensor_cores) {
     SUB_TRY(launch_chunk_tc(a, Q8, kv->head_dim, pool_rows, n_ctas, st));
+    if (a.whole) return SUB_OK;
     return kv->head_dim == 128 ? launch_join<128, CHUNK_TC_ROWS>(a, n_ctas, st)
                                : launch_join<64, CHUNK_TC_ROWS>(a, n_ctas, st);
   }

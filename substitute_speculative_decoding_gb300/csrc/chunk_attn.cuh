@@ -43,6 +43,7 @@ struct ChunkArgs {
   const int32_t* base;   // [n_seqs]
   const uint32_t* mask;  // [n_rows][words]
   int words;
+  bool whole;            // no unit is cut (below), and nothing is left to join
 };
 
 // The unit of work (below) that is cut first at the end of a CTA's part, for the
@@ -241,6 +242,28 @@ struct ChunkPlan {
       u.begin += __shfl_sync(~0u, run, 31);
     }
     measure(u);
+    return u;
+  }
+
+  // A CTA's blocks [lo, hi) of the line, and the unit that they begin with: its share of `per`, or,
+  // a.whole, all blocks of the units that begin there.
+  template <bool TREE>
+  __device__ ChunkUnit part(const int64_t* pre, int64_t total, int64_t per, int64_t& lo, int64_t& hi) const {
+    lo = blockIdx.x * per;
+    hi = min(total, lo + per);
+    ChunkUnit u;
+    if (lo >= hi) return u;
+    u = find(pre, lo);
+    if (TREE && a.whole) {
+      if (u.begin < lo) {
+        next(u);
+        lo = u.begin;
+      }
+      if (hi < total) {
+        const ChunkUnit v = find(pre, hi);
+        if (v.begin < hi) hi = v.begin + v.n_blocks;
+      }
+    }
     return u;
   }
 

@@ -178,9 +178,8 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
   const uint32_t tmem = *s_tmem;
   const int64_t total = s_pre[a.t.n_seqs];
   const int64_t per = blocks_per_cta(total, gridDim.x, TREE ? plan.least(total, CHUNK_TC_LEAST) : CHUNK_TC_LEAST);
-  const int64_t line_lo = blockIdx.x * per, line_hi = min(total, line_lo + per);
-  ChunkUnit u;
-  if (line_lo < line_hi) u = plan.find(s_pre, line_lo);
+  int64_t line_lo, line_hi;
+  ChunkUnit u = plan.template part<TREE>(s_pre, total, per, line_lo, line_hi);
   fence_async();     // the ring is written by copies from here on
   __syncthreads();
   const Gate gate{s_dead, &g_chunk_timeouts};

@@ -19,6 +19,8 @@
 //        of 8 rows.  (16 us before the log of the sum had a warp of its own and the
 //        bisections several lanes and whole numbers to compare.)
 //
+// Rows that a cluster reads in a moment take both in one launch (beam_kernel).
+//
 // (Every CTA keeping the best of its part while it streams would need no second
 // reading, but a sorted list per thread costs the scan its loads in flight.)
 //
@@ -59,20 +61,13 @@ __device__ __forceinline__ bool alive(float score) { return fabsf(score) < INFIN
 // NaN is no logit; -0 and 0 are one value
 __device__ __forceinline__ float clean(float z) { return fmaxf(z, -INFINITY) + 0.f; }
 
-__global__ void __launch_bounds__(SCAN_THREADS, 4) scan_kernel(const __grid_constant__ BeamArgs a) {
-  __shared__ float2 s_warp[SCAN_WARPS];
-  pdl_wait();
-  pdl_trigger();
+// A warp's part of blocks lo .. hi of a row, eight at a time: the largest logit of each to top(block,
+// value), and into m, s the largest of all and the sum of exp relative to it.  (A row that is not
+// alive is left with its first loads under way.)
+template <class F>
+__device__ __forceinline__ void scan_blocks(const BeamArgs& a, const float* z, const Row& r, int lo, int hi,
+                                            bool live, float& m, float& s, F top) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t row = blockIdx.x;
-  const float* const z = a.logits + row * a.V;
-  const Row r(z, a.V);
-  const int blocks = (r.n + BLOCK_GROUPS - 1) / BLOCK_GROUPS;
-  int lo, hi;
-  share(blocks, blockIdx.y, a.n_chunks, lo, hi);
-  const float live = __ldcg(a.score + row);
-  float* const top = a.top + row * a.n_blocks;
-  float m = -INFINITY, s = 0.f;
   for (int b0 = lo + warp * SCAN_MLP; b0 < hi; b0 += SCAN_WARPS * SCAN_MLP) {
     float4 x[SCAN_MLP];
 #pragma unroll
@@ -81,7 +76,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 4) scan_kernel(const __grid_cons
       x[k] = b0 + k < hi && g < r.n ? load_group(z, r, g, -INFINITY)
                                     : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
     }
-    if (!alive(live)) break;   // (the whole CTA, with its first loads under way)
+    if (!live) break;   // (the whole CTA)
     float big = m;
     uint32_t mine = 0;
 #pragma unroll
@@ -92,7 +87,7 @@ __global__ void __launch_bounds__(SCAN_THREADS, 4) scan_kernel(const __grid_cons
       const uint32_t all = __reduce_max_sync(~0u, float_key(t));
       if (lane == k) mine = all;
     }
-    if (lane < SCAN_MLP && b0 + lane < hi) top[b0 + lane] = key_float(mine);
+    if (lane < SCAN_MLP && b0 + lane < hi) top(b0 + lane, key_float(mine));
     // no logit above -infinity so far: every value is 0 whatever the reference
     const float ref = big == -INFINITY ? 0.f : big;
     s *= a.sharp.expo(m - ref);
@@ -103,11 +98,27 @@ __global__ void __launch_bounds__(SCAN_THREADS, 4) scan_kernel(const __grid_cons
       s += (exp2_fast(e.x) + exp2_fast(e.y)) + (exp2_fast(e.z) + exp2_fast(e.w));
     }
   }
-  if (!alive(live)) return;
+  if (!live) return;
 #pragma unroll
   for (int o = 16; o; o >>= 1)
     a.sharp.merge(m, s, __shfl_xor_sync(~0u, m, o), __shfl_xor_sync(~0u, s, o));
-  if (lane == 0) s_warp[warp] = make_float2(m, s);
+}
+
+__global__ void __launch_bounds__(SCAN_THREADS, 4) scan_kernel(const __grid_constant__ BeamArgs a) {
+  __shared__ float2 s_warp[SCAN_WARPS];
+  pdl_wait();
+  pdl_trigger();
+  const int64_t row = blockIdx.x;
+  const float* const z = a.logits + row * a.V;
+  const Row r(z, a.V);
+  int lo, hi;
+  share((r.n + BLOCK_GROUPS - 1) / BLOCK_GROUPS, blockIdx.y, a.n_chunks, lo, hi);
+  const bool live = alive(__ldcg(a.score + row));
+  float* const top = a.top + row * a.n_blocks;
+  float m = -INFINITY, s = 0.f;
+  scan_blocks(a, z, r, lo, hi, live, m, s, [&](int block, float x) { top[block] = x; });
+  if (!live) return;
+  if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = make_float2(m, s);
   __syncthreads();
   if (threadIdx.x) return;
   for (int w = 1; w < SCAN_WARPS; ++w) a.sharp.merge(m, s, s_warp[w].x, s_warp[w].y);
@@ -211,15 +222,138 @@ __device__ __forceinline__ double order_value(int64_t k) {
   return __longlong_as_double(k ^ (int64_t)((uint64_t)(k >> 63) >> 1));
 }
 
+struct PickState {   // of a CTA
+  __align__(16) uint64_t top[PICK_THREADS / 2];
+  uint64_t out[SUB_MAX_BEAMS];
+  int found, count[SUB_MAX_BEAMS];   // of the first CTA: candidates of each beam
+  int parent[SUB_MAX_BEAMS];
+  double lse;
+};
+
+// The log of a row's sum, from the parts' maxima and sums that the lanes hold, two each.  By a warp.
+__device__ __forceinline__ double log_sum(const BeamArgs& a, const float2 (&p)[2]) {
+  const float m = warp_max(fmaxf(p[0].x, p[1].x));
+  const bool finite = fabsf(m) < INFINITY;
+  const double top = (double)m / (double)a.temp, per = 1. / (double)a.temp;
+  double e[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    e[h] = p[h].x == -INFINITY || !finite ? 0. : (double)p[h].y * exp(((double)p[h].x - (double)m) * per);
+  double s = e[0] + e[1];
+#pragma unroll
+  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+  return finite ? top + log(s) : (double)INFINITY;   // not finite: no continuations
+}
+
+// The k largest logits of a row, in falling order, to st.out, from the keys of its blocks; best: the
+// largest that the thread wrote there.  By the first PICK_THREADS threads.
+__device__ void best_of_row(const float* z, const Row& r, int blocks, int k, uint64_t best, uint64_t* keys,
+                            uint64_t* list, PickState& st) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // ---- the blocks that hold them ----
+  select(keys, blocks, k, best, st.out, list, st.top, &st.found);
+  // ---- their logits ----
+  constexpr int AHEAD = 4;
+  best = 0;
+  for (int i0 = warp; i0 < k; i0 += PICK_WARPS * AHEAD) {
+    float4 x[AHEAD];
+    int g[AHEAD];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      const int i = i0 + u * PICK_WARPS;
+      const uint64_t y = i < k ? st.out[i] : 0;
+      g[u] = y ? (int)rank_idx(y) * BLOCK_GROUPS + lane : r.n;
+      x[u] = g[u] < r.n ? load_group(z, r, g[u], -INFINITY)
+                        : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    }
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      const int i = i0 + u * PICK_WARPS;
+      if (i >= k) break;
+      const float v[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {   // (elements before and past the row are -infinity)
+        const float c = clean(v[e]);
+        const uint64_t y = c == -INFINITY ? 0 : rank_key(c, (uint32_t)(r.first(g[u]) + e));
+        keys[i * 128 + e * 32 + lane] = y;
+        best = max(best, y);
+      }
+    }
+  }
+  pick_sync();   // st.out is read
+  select(keys, k * 128, k, best, st.out, list, st.top, &st.found);
+}
+
+// A beam's candidates, one per thread (key 0: none), to the cluster's first CTA.  By the whole CTA.
+__device__ __forceinline__ void send(const BeamArgs& a, int j, float score, uint64_t key, int64_t* cand_key,
+                                     int32_t* cand_token, PickState& st) {
+  cg::cluster_group cluster = cg::this_cluster();
+  const int tid = threadIdx.x;
+  if (key && !(st.lse < (double)INFINITY)) key = 0;
+  if (key) {
+    const double zt = (double)key_float((uint32_t)(key >> 32)) / (double)a.temp;
+    *cluster.map_shared_rank(cand_key + j * a.n_best + tid, 0) = order_key(((double)score + zt) - st.lse);
+    *cluster.map_shared_rank(cand_token + j * a.n_best + tid, 0) = (int32_t)rank_idx(key);
+  }
+  const int n_cand = __syncthreads_count(key != 0);   // st.out and st.lse are read
+  if (tid == 0) *cluster.map_shared_rank(st.count + j, 0) = n_cand;
+}
+
+// The first CTA: every candidate's place among all, by 2^lg lanes for each, and the outputs.
+__device__ void place_all(const BeamArgs& a, int64_t b, const int64_t* cand_key, const int32_t* cand_token,
+                          PickState& st) {
+  const int tid = threadIdx.x, k = a.n_best;
+  if (tid < SUB_MAX_BEAMS) st.parent[tid] = -1;
+  __syncthreads();
+  int lg = 0;
+  while (lg < 3 && (a.n_beams * k) << (lg + 1) <= PICK_THREADS) ++lg;
+  const int part = tid & ((1 << lg) - 1), total = a.n_beams * k;
+  for (int i0 = 0; i0 < total && tid < PICK_THREADS; i0 += PICK_THREADS >> lg) {
+    const int i = i0 + (tid >> lg), j = i / k, c = i - j * k;
+    const bool there = i < total && c < st.count[min(j, a.n_beams - 1)];
+    const int64_t x = there ? cand_key[i] : 0;
+    int place = 0;
+    if (there)
+      for (int o = part; o < a.n_beams && place < k; o += 1 << lg) {
+        if (o == j) continue;
+        int lo = 0, hi = st.count[o];   // its candidates that come before this one
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          const int64_t y = cand_key[o * k + mid];
+          if (y > x || (y == x && o < j)) lo = mid + 1;
+          else hi = mid;
+        }
+        place += lo;
+      }
+    for (int o = 1; o < 1 << lg; o <<= 1) place += __shfl_xor_sync(~0u, place, o);
+    place += c;   // of its own beam's, so many come first
+    if (!there || part != 0 || place >= k) continue;
+    a.token[b * k + place] = cand_token[i];
+    a.parent[b * k + place] = j;
+    a.score_out[b * k + place] = (float)order_value(x);
+    st.parent[place] = j;
+  }
+  __syncthreads();
+  if (tid < k && st.parent[tid] < 0) {
+    a.token[b * k + tid] = -1;
+    a.parent[b * k + tid] = -1;
+    a.score_out[b * k + tid] = -INFINITY;
+  }
+  // ---- the parents' states ----
+  if (a.state_out)
+    for (int64_t i = tid; i < (int64_t)k * a.words; i += PICK_THREADS + 32) {
+      const int p = (int)(i / a.words), w = (int)(i - (int64_t)p * a.words), j = st.parent[p];
+      int32_t x = j < 0 ? 0 : __ldcg(a.state + (b * a.n_beams + j) * a.words + w);
+      if (j >= 0 && a.slot >= 0 && (a.slot + p) >> 5 == w) x |= (int32_t)(1u << ((a.slot + p) & 31));
+      a.state_out[b * k * a.words + i] = x;
+    }
+}
+
 // The first eight warps select; the ninth forms the log of the sum meanwhile, in 64 bits
 // (exponentials, a logarithm and a division of doubles: 10000 cycles when it came first).
 __global__ void __launch_bounds__(PICK_THREADS + 32) pick_kernel(const __grid_constant__ BeamArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ __align__(16) uint64_t s_top[PICK_THREADS / 2];
-  __shared__ uint64_t s_out[SUB_MAX_BEAMS];
-  __shared__ int s_found, s_count[SUB_MAX_BEAMS];   // of the first CTA: candidates of each beam
-  __shared__ int s_parent[SUB_MAX_BEAMS];
-  __shared__ double s_lse;
+  __shared__ PickState st;
   cg::cluster_group cluster = cg::this_cluster();
   const int size = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int64_t b = blockIdx.x / size;
@@ -240,30 +374,18 @@ __global__ void __launch_bounds__(PICK_THREADS + 32) pick_kernel(const __grid_co
     const int blocks = (r.n + BLOCK_GROUPS - 1) / BLOCK_GROUPS;
     const float score = __ldcg(a.score + row);
     uint64_t key = 0;    // the thread's candidate
-    double zt = 0.;
     if (!alive(score)) {
       // no candidates
     } else if (warp == PICK_WARPS) {
-      // ---- the log of the sum ----
       static_assert(MAX_CHUNKS == 64, "two per lane");
       float2 p[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         p[h] = lane + 32 * h < a.n_chunks ? __ldcg(a.part + row * a.n_chunks + lane + 32 * h)
                                           : make_float2(-INFINITY, 0.f);
-      const float m = warp_max(fmaxf(p[0].x, p[1].x));
-      const bool finite = fabsf(m) < INFINITY;
-      const double top = (double)m / (double)a.temp, per = 1. / (double)a.temp;
-      double e[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        e[h] = p[h].x == -INFINITY || !finite ? 0. : (double)p[h].y * exp(((double)p[h].x - (double)m) * per);
-      double s = e[0] + e[1];
-#pragma unroll
-      for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
-      if (lane == 0) s_lse = finite ? top + log(s) : (double)INFINITY;   // not finite: no continuations
+      const double lse = log_sum(a, p);
+      if (lane == 0) st.lse = lse;
     } else {
-      // ---- the blocks that hold the k largest logits ----
       uint64_t best = 0;
       for (int i = tid; i < blocks; i += PICK_THREADS) {
         const float x = __ldcg(a.top + row * a.n_blocks + i);
@@ -271,101 +393,86 @@ __global__ void __launch_bounds__(PICK_THREADS + 32) pick_kernel(const __grid_co
         keys[i] = y;
         best = max(best, y);
       }
-      select(keys, blocks, k, best, s_out, list, s_top, &s_found);
-      // ---- their logits ----
-      constexpr int AHEAD = 4;
-      best = 0;
-      for (int i0 = warp; i0 < k; i0 += PICK_WARPS * AHEAD) {
-        float4 x[AHEAD];
-        int g[AHEAD];
-#pragma unroll
-        for (int u = 0; u < AHEAD; ++u) {
-          const int i = i0 + u * PICK_WARPS;
-          const uint64_t y = i < k ? s_out[i] : 0;
-          g[u] = y ? (int)rank_idx(y) * BLOCK_GROUPS + lane : r.n;
-          x[u] = g[u] < r.n ? load_group(z, r, g[u], -INFINITY)
-                            : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-        }
-#pragma unroll
-        for (int u = 0; u < AHEAD; ++u) {
-          const int i = i0 + u * PICK_WARPS;
-          if (i >= k) break;
-          const float v[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {   // (elements before and past the row are -infinity)
-            const float c = clean(v[e]);
-            const uint64_t y = c == -INFINITY ? 0 : rank_key(c, (uint32_t)(r.first(g[u]) + e));
-            keys[i * 128 + e * 32 + lane] = y;
-            best = max(best, y);
-          }
-        }
-      }
-      pick_sync();   // s_out is read
-      select(keys, k * 128, k, best, s_out, list, s_top, &s_found);
-      if (tid < k) key = s_out[tid];
-      if (key) zt = (double)key_float((uint32_t)(key >> 32)) / (double)a.temp;
+      best_of_row(z, r, blocks, k, best, keys, list, st);
+      if (tid < k) key = st.out[tid];
     }
-    __syncthreads();   // s_lse is there
-    // ---- scores, to the cluster's first CTA ----
+    __syncthreads();   // st.lse is there
     if (alone) cluster_all_here();
     alone = false;
-    if (key && !(s_lse < (double)INFINITY)) key = 0;
-    if (key) {
-      *cluster.map_shared_rank(cand_key + j * k + tid, 0) = order_key(((double)score + zt) - s_lse);
-      *cluster.map_shared_rank(cand_token + j * k + tid, 0) = (int32_t)rank_idx(key);
-    }
-    const int n_cand = __syncthreads_count(key != 0);   // s_out and s_lse are read
-    if (tid == 0) *cluster.map_shared_rank(s_count + j, 0) = n_cand;
+    send(a, j, score, key, cand_key, cand_token, st);
   }
   if (size > 1) cluster.sync();
   else __syncthreads();
-  if (rank != 0) return;
+  if (rank == 0) place_all(a, b, cand_key, cand_token, st);
+}
 
-  // ---- the first CTA: every candidate's place among all, by 2^lg lanes for each ----
-  if (tid < SUB_MAX_BEAMS) s_parent[tid] = -1;
-  __syncthreads();
-  int lg = 0;
-  while (lg < 3 && (a.n_beams * k) << (lg + 1) <= PICK_THREADS) ++lg;
-  const int part = tid & ((1 << lg) - 1), total = a.n_beams * k;
-  for (int i0 = 0; i0 < total && warp < PICK_WARPS; i0 += PICK_THREADS >> lg) {
-    const int i = i0 + (tid >> lg), j = i / k, c = i - j * k;
-    const bool there = i < total && c < s_count[min(j, a.n_beams - 1)];
-    const int64_t x = there ? cand_key[i] : 0;
-    int place = 0;
-    if (there)
-      for (int o = part; o < a.n_beams && place < k; o += 1 << lg) {
-        if (o == j) continue;
-        int lo = 0, hi = s_count[o];   // its candidates that come before this one
-        while (lo < hi) {
-          const int mid = (lo + hi) >> 1;
-          const int64_t y = cand_key[o * k + mid];
-          if (y > x || (y == x && o < j)) lo = mid + 1;
-          else hi = mid;
-        }
-        place += lo;
-      }
-    for (int o = 1; o < 1 << lg; o <<= 1) place += __shfl_xor_sync(~0u, place, o);
-    place += c;   // of its own beam's, so many come first
-    if (!there || part != 0 || place >= k) continue;
-    a.token[b * k + place] = cand_token[i];
-    a.parent[b * k + place] = j;
-    a.score_out[b * k + place] = (float)order_value(x);
-    s_parent[place] = j;
-  }
-  __syncthreads();
-  if (tid < k && s_parent[tid] < 0) {
-    a.token[b * k + tid] = -1;
-    a.parent[b * k + tid] = -1;
-    a.score_out[b * k + tid] = -INFINITY;
-  }
-  // ---- the parents' states ----
-  if (a.state_out)
-    for (int64_t i = tid; i < (int64_t)k * a.words; i += PICK_THREADS + 32) {
-      const int p = (int)(i / a.words), w = (int)(i - (int64_t)p * a.words), j = s_parent[p];
-      int32_t x = j < 0 ? 0 : __ldcg(a.state + (b * a.n_beams + j) * a.words + w);
-      if (j >= 0 && a.slot >= 0 && (a.slot + p) >> 5 == w) x |= (int32_t)(1u << ((a.slot + p) & 31));
-      a.state_out[b * k * a.words + i] = x;
+// Both in one launch, where a cluster has a CTA for each beam, or `team` of them: these share the
+// row's scan, and the first of them goes on with what the others left in its shared memory.
+__global__ void __launch_bounds__(PICK_THREADS + 32, 3) beam_kernel(const __grid_constant__ BeamArgs a, const int team) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ PickState st;
+  __shared__ float2 s_warp[SCAN_WARPS], s_part[2 * MAX_CLUSTER];
+  static_assert(SCAN_THREADS == PICK_THREADS && 2 * MAX_CLUSTER <= 32, "the same warps, a part per lane");
+  cg::cluster_group cluster = cg::this_cluster();
+  const int size = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int64_t b = blockIdx.x / size;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = a.n_best;
+  const int j = rank / team, member = rank - j * team, first = rank - member;   // beam, CTA of its team
+  if (size > 1) cluster_here();
+  const PickShared at = pick_shared(a.n_blocks, a.n_beams, k);
+  uint64_t* const keys = reinterpret_cast<uint64_t*>(smem);
+  uint64_t* const list = reinterpret_cast<uint64_t*>(smem + at.list);
+  int64_t* const cand_key = reinterpret_cast<int64_t*>(smem + at.cand_key);
+  int32_t* const cand_token = reinterpret_cast<int32_t*>(smem + at.cand_token);
+  uint64_t* const team_keys = cluster.map_shared_rank(keys, first);
+  pdl_wait();
+  pdl_trigger();
+  const int64_t row = b * a.n_beams + j;
+  const float* const z = a.logits + row * a.V;
+  const Row r(z, a.V);
+  const int blocks = (r.n + BLOCK_GROUPS - 1) / BLOCK_GROUPS;
+  const float score = __ldcg(a.score + row);
+  const bool live = alive(score);
+  if (size > 1) cluster_all_here();   // before the first write to another CTA
+  if (warp < PICK_WARPS) {
+    int lo, hi;
+    share(blocks, member, team, lo, hi);
+    float m = -INFINITY, s = 0.f;
+    scan_blocks(a, z, r, lo, hi, live, m, s, [&](int block, float x) {
+      team_keys[block] = x == -INFINITY ? 0 : rank_key(x, (uint32_t)block);
+    });
+    if (lane == 0) s_warp[warp] = make_float2(m, s);
+    pick_sync();
+    if (tid == 0) {
+      for (int w = 1; w < SCAN_WARPS; ++w) a.sharp.merge(m, s, s_warp[w].x, s_warp[w].y);
+      *cluster.map_shared_rank(s_part + member, first) = make_float2(m, s);
     }
+  }
+  if (size > 1) {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    if (member != 0) return;   // (nobody reads or writes its shared memory)
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  } else {
+    __syncthreads();
+  }
+  uint64_t key = 0;   // the thread's candidate
+  if (!live) {
+    // no candidates
+  } else if (warp == PICK_WARPS) {
+    const float2 p[2] = {lane < team ? s_part[lane] : make_float2(-INFINITY, 0.f), make_float2(-INFINITY, 0.f)};
+    const double lse = log_sum(a, p);
+    if (lane == 0) st.lse = lse;
+  } else {
+    uint64_t best = 0;
+    for (int i = tid; i < blocks; i += PICK_THREADS) best = max(best, keys[i]);
+    best_of_row(z, r, blocks, k, best, keys, list, st);
+    if (tid < k) key = st.out[tid];
+  }
+  __syncthreads();   // st.lse is there
+  send(a, j, score, key, cand_key, cand_token, st);
+  if (size > 1) cluster.sync();   // (of the CTAs that are left)
+  else __syncthreads();
+  if (rank == 0) place_all(a, b, cand_key, cand_token, st);
 }
 
 // Blocks of the longest layout of a row, and bytes of a call's workspace.
@@ -393,9 +500,12 @@ int largest_cluster() {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const bool placed =
-      cudaFuncSetAttribute(pick_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
-      cudaOccupancyMaxActiveClusters(&n, pick_kernel, &cfg) == cudaSuccess && n > 0;
+  auto allows = [&](auto kernel) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PICK_SMEM) == cudaSuccess &&
+           cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0;
+  };
+  const bool placed = allows(pick_kernel) && allows(beam_kernel);
   if (!placed) cudaGetLastError();   // (not an error of the call)
   n = placed ? 2 * MAX_CLUSTER : MAX_CLUSTER;
   if (known) size[dev].store(n, std::memory_order_relaxed);
@@ -483,11 +593,21 @@ extern "C" int32_t sub_beam_select(const float* logits, const float* score, int3
   a.part = reinterpret_cast<float2*>(workspace);
   a.top = reinterpret_cast<float*>(a.part + rows * MAX_CHUNKS);
   SUB_CUDA_TRY(once_per_device([] {
-    return cudaFuncSetAttribute(pick_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PICK_SMEM);
+    cudaError_t e = cudaFuncSetAttribute(pick_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PICK_SMEM);
+    return e != cudaSuccess ? e : cudaFuncSetAttribute(beam_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PICK_SMEM);
   }));
+  const size_t bytes = pick_shared(a.n_blocks, n_beams, n_best).bytes;
+  const int most = largest_cluster();
+  // One launch where a CTA of a cluster has 80 blocks at most: 3 us less of the host's time, and as
+  // long on the GPU (1 beam of 152064 logits 9.7 us and 9.5; 16 trees of 5 beams of 5000 13.0 and 13.8;
+  // but 4 beams of 152064, 297 blocks per CTA, 13.3 and 10.4, and 64 trees of 8 of 128256 87 and 59: a
+  // cluster's SMs are few, and wait for 16 to be free at once).
+  if (a.n_blocks <= 80 * (most / n_beams)) {
+    const int team = (int)std::min<int64_t>(most / n_beams, cdiv(a.n_blocks, round));   // a round of loads each
+    SUB_CUDA_TRY(launch_clusters(beam_kernel, n_seqs, team * n_beams, PICK_THREADS + 32, bytes, st, a, team));
+    return SUB_OK;
+  }
   SUB_CUDA_TRY(launch_k(scan_kernel, dim3((unsigned)rows, a.n_chunks), dim3(SCAN_THREADS), 0, st, a));
-  const int size = std::min(n_beams, n_beams > MAX_CLUSTER ? largest_cluster() : MAX_CLUSTER);
-  SUB_CUDA_TRY(launch_clusters(pick_kernel, n_seqs, size, PICK_THREADS + 32,
-                               pick_shared(a.n_blocks, n_beams, n_best).bytes, st, a));
+  SUB_CUDA_TRY(launch_clusters(pick_kernel, n_seqs, std::min(n_beams, most), PICK_THREADS + 32, bytes, st, a));
   return SUB_OK;
 }

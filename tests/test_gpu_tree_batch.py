@@ -471,7 +471,7 @@ def beams(sub, z, score, k, temp=1.0, state=None, slot=-1, **kw):
 
 
 @pytest.mark.parametrize("shape", [(1, 1, 1), (1, 1, 7), (3, 2, 33), (2, 5, 128), (2, 8, 1000), (5, 3, 5001),
-                                   (1, 8, 20011), (2, 64, 513), (1, 16, 65537), (3, 13, 700), (2, 31, 5000)])
+                                   (1, 8, 20011), (2, 64, 513), (1, 16, 65537), (3, 13, 700), (2, 31, 5000), (2, 1, 152064), (3, 3, 50003)])
 @pytest.mark.parametrize("k", [1, 3, 8, 64])
 @pytest.mark.parametrize("temp", [0.2, 1.0])
 def test_beam_select(sub, shape, k, temp):

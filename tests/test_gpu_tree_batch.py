@@ -228,6 +228,10 @@ class TreeCase(Case):
             assert np.all(err <= bound), (b, float((err / bound).max()))
 
 
+# Further columns of the page table: with room for many keys, rows go to the kernels of long sequences,
+# and units are cut
+WIDTHS = [0, 30000]
+
 TREES = [dict(trees=[(0, 0, 1)], hq=4, hkv=2, d=64),
          dict(trees=[(511, 9, 8)], hq=4, hkv=2, d=64),
          dict(trees=[(31, 0, 1), (32, 1, 1), (0, 3, 1), (60, 8, 1), (1000, 40, 1)], hq=28, hkv=4, d=128, page=64),
@@ -246,8 +250,9 @@ TREES = [dict(trees=[(0, 0, 1)], hq=4, hkv=2, d=64),
 @pytest.mark.parametrize("kw", TREES)
 @pytest.mark.parametrize("bits_", [16, 8])
 @pytest.mark.parametrize("kind", ["tree", "any"])
-def test_tree_attn(sub, kw, bits_, kind):
-    c = TreeCase(sub, bits=bits_, kind=kind, seed=len(kw["trees"]) + bits_, **kw)
+@pytest.mark.parametrize("width", WIDTHS)
+def test_tree_attn(sub, kw, bits_, kind, width):
+    c = TreeCase(sub, bits=bits_, kind=kind, seed=len(kw["trees"]) + bits_, width=width, **kw)
     o = torch.full((c.batch.n_rows, c.hq, c.d), 7.0, dtype=BF, device=DEV)
     c.run(out=o)
     c.check_tree(o)
@@ -260,12 +265,15 @@ def test_tree_attn(sub, kw, bits_, kind):
 
 @pytest.mark.parametrize("bits_", [16, 8])
 @pytest.mark.parametrize("n", [1, 8, 40, 300])
-def test_many_ctas_and_wide_masks(sub, bits_, n):
+@pytest.mark.parametrize("width", WIDTHS)
+def test_many_ctas_and_wide_masks(sub, bits_, n, width):
     """Many CTAs on one sequence's keys beside short ones, masks of 64 words, and masks that
     end before the new rows' own slots."""
-    c = TreeCase(sub, [(9000, 1700, n), (64, 0, n), (0, 31, n)], 4, 1, 128, page=64, bits=bits_, seed=n, words=64)
+    c = TreeCase(sub, [(9000, 1700, n), (64, 0, n), (0, 31, n)], 4, 1, 128, page=64, bits=bits_, seed=n, words=64,
+                 width=width)
     c.check_tree(c.run())
-    c = TreeCase(sub, [(900, 60, n), (64, 0, n), (0, 0, n)], 4, 1, 128, page=64, bits=bits_, seed=n, words=1)
+    c = TreeCase(sub, [(900, 60, n), (64, 0, n), (0, 0, n)], 4, 1, 128, page=64, bits=bits_, seed=n, words=1,
+                 width=width)
     c.check_tree(c.run(scale=0.3), scale=0.3)
 
 
@@ -286,9 +294,11 @@ def test_a_few_dozen_rows(sub, bits_, d, page, trees):
 
 @pytest.mark.parametrize("bits_", [16, 8])
 @pytest.mark.parametrize("n", [2, 8, 60])
-def test_a_path_of_all_is_chunk_attention(sub, bits_, n):
+@pytest.mark.parametrize("width", WIDTHS)
+def test_a_path_of_all_is_chunk_attention(sub, bits_, n, width):
     """Masks with all bits, and a base behind all keys."""
-    c = TreeCase(sub, [(300, 5, n), (40, 0, n), (0, 0, n)], 8, 2, 128, page=48, bits=bits_, seed=4)
+    c = TreeCase(sub, [(300, 5, n), (40, 0, n), (0, 0, n)], 8, 2, 128, page=48, bits=bits_, seed=4,
+                 width=width)
     c.check(sub.chunk_attn(c.q.to(DEV), c.kv, c.layer, c.batch))
     c.mask.fill_(-1)
     c.check(c.run())
@@ -299,9 +309,10 @@ def test_a_path_of_all_is_chunk_attention(sub, bits_, n):
 
 
 @pytest.mark.parametrize("bits_", [16, 8])
-@pytest.mark.parametrize("n", [1, 4, 150])
-def test_rows_that_read_nothing(sub, bits_, n):
-    c = TreeCase(sub, [(0, 3, n), (50, 0, n), (0, 0, n)], 8, 2, 128, bits=bits_, kind="none")
+@pytest.mark.parametrize("n", [1, 4, 8, 150])
+@pytest.mark.parametrize("width", WIDTHS)
+def test_rows_that_read_nothing(sub, bits_, n, width):
+    c = TreeCase(sub, [(0, 3, n), (50, 0, n), (0, 0, n)], 8, 2, 128, bits=bits_, kind="none", width=width)
     o = c.run()
     c.check_tree(o)
     assert torch.all(o[:n] == 0) and torch.all(o[2 * n:] == 0) and torch.isfinite(o).all()
@@ -319,9 +330,10 @@ def test_rows_that_read_nothing(sub, bits_, n):
 
 
 @pytest.mark.parametrize("bits_", [16, 8])
-@pytest.mark.parametrize("n", [8, 150])
-def test_missing_pages_under_a_tree(sub, bits_, n):
-    c = TreeCase(sub, [(200, 9, n), (64, 0, n)], 8, 2, 128, bits=bits_, seed=2)
+@pytest.mark.parametrize("n", [3, 8, 150])
+@pytest.mark.parametrize("width", WIDTHS)
+def test_missing_pages_under_a_tree(sub, bits_, n, width):
+    c = TreeCase(sub, [(200, 9, n), (64, 0, n)], 8, 2, 128, bits=bits_, seed=2, width=width)
     c.table_d[0, 3] = -1
     c.table_d[0, 13] = c.kv.n_pages           # slots 8 .. 23
     c.table_d[1] = -7
@@ -333,10 +345,11 @@ def test_missing_pages_under_a_tree(sub, bits_, n):
 @pytest.mark.parametrize("bits_", [16, 8])
 @pytest.mark.parametrize("n", [2, 8, 33, 260])
 @pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
-def test_slots_that_a_row_does_not_read_hold_anything(sub, bits_, n, bad):
+@pytest.mark.parametrize("width", WIDTHS)
+def test_slots_that_a_row_does_not_read_hold_anything(sub, bits_, n, bad, width):
     """Infinities and NaN in K, V (codes: in their scales) of slots off a row's path."""
     base, first = 45, 40
-    c = TreeCase(sub, [(base, first, n), (20, 0, 2)], 8, 2, 128, bits=bits_, seed=3)
+    c = TreeCase(sub, [(base, first, n), (20, 0, 2)], 8, 2, 128, bits=bits_, seed=3, width=width)
     clean = c.run().clone()
     hurt = np.zeros(first + n, bool)
     hurt[[5, 17, 38, first + n - 2]] = True
@@ -371,11 +384,12 @@ def test_slots_that_a_row_does_not_read_hold_anything(sub, bits_, n, bad):
                     assert not have[i, h, x], (i, h, s)
 
 
-def test_strides_streams_workspaces_and_graphs(sub):
+@pytest.mark.parametrize("width", WIDTHS)
+def test_strides_streams_workspaces_and_graphs(sub, width):
     """Strided queries; a call on another stream with a given workspace; a captured call
     replayed with other masks, bases and queries."""
     for bits_, n in ((16, 3), (8, 3), (16, 70), (8, 70)):
-        c = TreeCase(sub, [(90, 4, n), (13, 0, n)], 8, 2, 64, page=32, bits=bits_, seed=1)
+        c = TreeCase(sub, [(90, 4, n), (13, 0, n)], 8, 2, 64, page=32, bits=bits_, seed=1, width=width)
         wide = torch.randn(c.batch.n_rows, 12, 64, device=DEV).to(BF)
         wide[:, :8] = c.q.to(DEV)
         ws = torch.empty(sub.chunk_attn_workspace(8, 2, 64, 2, c.batch.n_rows), dtype=torch.uint8, device=DEV)
@@ -388,7 +402,8 @@ def test_strides_streams_workspaces_and_graphs(sub):
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
             sub.chunk_tree_attn(wide[:, :8], c.kv, c.layer, c.batch, c.base, c.mask, out=o, workspace=ws)
-        other = TreeCase(sub, [(90, 4, n), (13, 0, n)], 8, 2, 64, page=32, bits=bits_, kind="any", seed=1)
+        other = TreeCase(sub, [(90, 4, n), (13, 0, n)], 8, 2, 64, page=32, bits=bits_, kind="any", seed=1,
+                         width=width)
         c.mask.copy_(other.mask)
         c.masks = other.masks
         o.zero_()
@@ -400,8 +415,8 @@ def test_strides_streams_workspaces_and_graphs(sub):
 def test_workspaces_of_the_calls_own(sub):
     """Without a workspace: on another stream beside work of this one, and in two captured
     graphs of one memory pool, replayed in turn; chunk_attn and beam_select alike."""
-    cases = [TreeCase(sub, [(3000, 4, n), (13, 0, n)], 8, 2, 64, page=32, bits=bits_, seed=n)
-             for bits_, n in ((16, 3), (8, 3), (16, 8), (8, 20), (16, 70), (8, 70))]
+    cases = [TreeCase(sub, [(3000, 4, n), (13, 0, n)], 8, 2, 64, page=32, bits=bits_, seed=n, width=width)
+             for bits_, n, width in ((16, 3, 0), (8, 3, 9000), (16, 8, 0), (8, 20, 0), (16, 70, 9000), (8, 70, 9000))]
     z = torch.randn(3, 5, 4000, device=DEV)
     score = -torch.rand(3, 5, device=DEV).cumsum(1)
     want = [c.run() for c in cases]

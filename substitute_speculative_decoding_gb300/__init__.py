@@ -629,12 +629,11 @@ def chunk_attn(q, kv, layer: int, batch: Batch, scale=None, out=None, workspace=
     their own keys already -> bf16 [n_rows, n_heads_q, head_dim].  Rows of no
     sequence are left as they are in `out`, zero without.  workspace: a uint8
     tensor of chunk_attn_workspace bytes; allocated by torch if not given."""
-    return _attend(_chunk_attn8 if type(kv) is KV8Cache else _chunk_attn, q, kv, layer, batch, (),
-                   scale, out, workspace, stream)
+    return _attend(_chunk_attn8 if type(kv) is KV8Cache else _chunk_attn, q, kv, layer, batch,
+                   _same(kv, batch), (), scale, out, workspace, stream)
 
 
-def _attend(fn, q, kv, layer, batch, extra, scale, out, workspace, stream):
-    dev = _same(kv, batch)
+def _attend(fn, q, kv, layer, batch, dev, extra, scale, out, workspace, stream):
     if q.dim() != 3:
         _refuse("q: must be [n_rows, n_heads_q, head_dim]")
     n, hq, d = batch.n_rows, q.shape[1], kv.head_dim
@@ -665,7 +664,7 @@ def chunk_tree_attn(q, kv, layer: int, batch: Batch, base, mask, scale=None, out
     extra = (_dense(base, torch.int32, (batch.n_seqs,), "base", dev),
              _dense(mask, torch.int32, (batch.n_rows, words), "mask", dev), words)
     return _attend(_chunk_tree_attn8 if type(kv) is KV8Cache else _chunk_tree_attn, q, kv, layer,
-                   batch, extra, scale, out, workspace, stream)
+                   batch, dev, extra, scale, out, workspace, stream)
 
 
 def beam_workspace(n_seqs: int, n_beams: int, vocab: int) -> int:

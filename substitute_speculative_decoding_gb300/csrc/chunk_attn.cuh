@@ -307,7 +307,7 @@ bool chunk_tc_fits(int64_t pool_rows);   // rows of head_dim values in a pool
 int32_t launch_chunk_tc(const ChunkArgs& a, bool q8, int head_dim, int64_t pool_rows, int n_ctas,
                         cudaStream_t st);
 int32_t chunk_tc_timeouts(unsigned int* out);
-// The kernel for 17 to 128 rows of trees (chunk_attn_mid.cu): tiles of 32 or 64 rows.
+// The kernel with the keys on the lanes, for trees (chunk_attn_mid.cu): tiles of 32 or 64 rows.
 int32_t launch_chunk_mid(const ChunkArgs& a, bool q8, int head_dim, int rows, int64_t pool_rows, int n_ctas,
                          cudaStream_t st);
 int32_t chunk_mid_timeouts(unsigned int* out);

@@ -1,5 +1,5 @@
-// Attention of tree nodes over a paged cache, a few dozen rows per KV head: the
-// nodes of a draft tree's level, times the heads of a group.
+// Attention of tree nodes over a paged cache, a few dozen rows per KV head (the nodes of
+// a draft tree's level, times the heads of a group), or more over short caches.
 //
 // Bound by HBM, if the work per key stays small: 32 rows do 32 flops per byte of a bf16
 // cache.  The kernel of 16 rows (chunk_attn.cu) would read and, over codes, convert
@@ -32,6 +32,11 @@
 // at the reference and below 2^15, its smallest step 2^-36 of the reference.  The
 // sum takes the weight itself, in fp32.  Rows' scores thus take nothing from keys
 // that they do not read, whose scales may be anything.
+//
+// Measured, heads of 128: 32 rows of each of 16 sequences and 8 KV heads over 10000 keys on average
+// 116 us (0.67 GB, 5.8 TB/s), over codes 86 (4.0 TB/s); 56 rows of 32 sequences and 4 KV heads over
+// 5100 68 us (5.1 TB/s); 33 nodes of 1 sequence and 8 KV heads over 500 keys 14.  A block of 128 keys
+// takes 2200 cycles over codes, of which the issue slots are busy 1240; a bf16 block at HBM's rate 2800.
 //
 // V of a block that not all rows read to its end may hold anything where it is not read: values that
 // are not finite are taken out by the thread whose key it is, and added at the end to

@@ -86,6 +86,9 @@ int32_t move(const Cache* kv, int32_t n_seqs, const int32_t* to, const int32_t* 
   SUB_CHECK_ARG(n_max >= 0 && n_max <= SUB_MAX_MOVE, "n_max must be in [0, SUB_MAX_MOVE]");
   if (n_max == 0) return SUB_OK;
   SUB_CHECK_ARG(to && from && count, "null pointer");
+  SUB_CHECK_ARG(((reinterpret_cast<uintptr_t>(to) | reinterpret_cast<uintptr_t>(from) |
+                  reinterpret_cast<uintptr_t>(count)) & 3) == 0,
+                "to, from and count must be 4-byte aligned");
   a.t.start = a.t.pos = nullptr;
   a.n_heads_kv = kv->n_heads_kv;
   a.n_max = n_max;

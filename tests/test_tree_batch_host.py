@@ -116,13 +116,13 @@ def test_bad_rows_are_refused(s, turn):
     bad = [rope(q=None), rope(out=None), rope(k=None), rope(v=None), rope(kv=None), rope(b=None),
            rope(r=None), rope(r=C.byref(other)), rope(hq=-1), rope(hq=1 << 16), rope(ldq=504),
            rope(ldq=516), rope(ldo=504, q=C.c_void_p(8192)), rope(ldk=248), rope(ldv=252), rope(q=ODD),
-           rope(k=ODD), rope(out=ODD), rope(layer=2), rope(ldq=1024), rope(ldo=1024)]
+           rope(k=ODD), rope(out=ODD), rope(at=OFF), rope(layer=2), rope(ldq=1024), rope(ldo=1024)]
     bad += [attn(base=None), attn(mask=None), attn(words=0), attn(words=65), attn(base=OFF), attn(mask=OFF),
             attn(q=None), attn(out=None), attn(ldq=504), attn(hq=7), attn(hq=0), attn(scale=-1.0),
             attn(scale=float("nan")), attn(q=ODD), attn(ws=P, size=16), attn(ws=ODD, size=1 << 40),
             s._chunk_tree_attn(P, 512, 8, kv, 0, None, P, P, 1, 0.1, P, None, 0, None)]
     bad += [move(n=0), move(n=1025), move(to=None), move(src=None), move(count=None), move(most=-1),
-            move(most=129), move(kv=None)]
+            move(most=129), move(kv=None), move(to=OFF), move(src=OFF), move(count=OFF)]
     assert bad == [s.SUB_EINVAL] * len(bad)
 
 

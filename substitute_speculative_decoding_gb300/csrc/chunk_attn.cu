@@ -992,8 +992,8 @@ int32_t chunk_attn(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q, const Cach
   a.part_ml = reinterpret_cast<float2*>(a.part_o + (int64_t)n_ctas * 2 * part_rows * kv->head_dim);
   a.cuts = reinterpret_cast<ChunkCut*>(a.part_ml + (int64_t)n_ctas * 2 * part_rows);
   if (tensor_cores) {
+    a.whole = false;   // (short caches hardly come here, and the search cost 1 us of 70)
     SUB_TRY(launch_chunk_tc(a, Q8, kv->head_dim, pool_rows, n_ctas, st));
-    if (a.whole) return SUB_OK;
     return kv->head_dim == 128 ? launch_join<128, CHUNK_TC_ROWS>(a, n_ctas, st)
                                : launch_join<64, CHUNK_TC_ROWS>(a, n_ctas, st);
   }

@@ -179,7 +179,7 @@ chunk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Chunk
   const int64_t total = s_pre[a.t.n_seqs];
   const int64_t per = blocks_per_cta(total, gridDim.x, TREE ? plan.least(total, CHUNK_TC_LEAST) : CHUNK_TC_LEAST);
   int64_t line_lo, line_hi;
-  ChunkUnit u = plan.template part<TREE>(s_pre, total, per, line_lo, line_hi);
+  ChunkUnit u = plan.template part<false>(s_pre, total, per, line_lo, line_hi);
   fence_async();     // the ring is written by copies from here on
   __syncthreads();
   const Gate gate{s_dead, &g_chunk_timeouts};

@@ -328,14 +328,14 @@ int32_t sub_kv8_read(const sub_kv8_cache* kv, int32_t layer, const sub_batch* ba
 
 /* The rotation of position embeddings: pair i (elements i and i + head_dim / 2 of a
  * head) turns by freqs[i] radians per position.  step[i] is that as a fraction of a whole
- * turn in units of 2^-64, so that a position's angle is one whole-number product whose
- * overflow drops the whole turns: exact at any position. */
+ * turn in units of 2^-64, to the nearest, so that a position's angle is one whole-number product
+ * whose overflow drops the whole turns: right to 2^-34 of a turn at any position. */
 typedef struct {
   uint64_t step[64];   /* [head_dim / 2] */
   int32_t head_dim;
 } sub_rope;
 /* Fill *rope: freqs_host [head_dim / 2], each in [0, 1e6] radians, or NULL for
- * theta^(-2 i / head_dim), theta in [1, 1e12]. */
+ * theta^(-2 i / head_dim), rounded to a double like any other frequency, theta in [1, 1e12]. */
 int32_t sub_rope_init(int32_t head_dim, double theta, const double* freqs_host, sub_rope* rope);
 
 /* sub_kv_append / sub_kv8_append with the rotation on the way: the batch's new rows K are

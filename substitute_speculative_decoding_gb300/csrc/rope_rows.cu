@@ -3,9 +3,10 @@
 // Pair (x1, x2) = elements (i, i + D / 2) of a head becomes (x1 cos - x2 sin,
 // x2 cos + x1 sin) of the angle at * freqs[i].  Angles of far positions lose their
 // fraction of a turn in fp32 (at 10^5 radians a step is 2^-7), so they are formed in
-// whole numbers: step[i] is the frequency in turns times 2^64, and the product's overflow is
-// the whole turns.  One 64-bit multiplication then gives the fraction to 2^-32 of a
-// turn and better, and sincospi takes it without another reduction.
+// whole numbers: step[i] is the frequency in turns times 2^64, right in all of its bits, and
+// the product's overflow is the whole turns.  One 64-bit multiplication then gives the
+// fraction to 2^-32 of a turn and better (2^-65 times a position below 2^31, and half a step
+// of the 2^-32 that are kept), and sincospi takes it without another reduction.
 //
 // Memory bound: q is read and written, K read and written, V copied.  A warp takes
 // one token's K, or V, or 16 heads of its q; D / 16 lanes hold a head, each the two
@@ -130,6 +131,31 @@ __global__ void __launch_bounds__(ROPE_WARPS * 32) rope_append_kernel(const __gr
   }
 }
 
+// freq / (2 pi) in units of 2^-64, without its whole turns, to the nearest.  (A quotient of
+// doubles has 53 bits before the whole turns drop out: of a frequency of 10^6 that is 2^-36 of a turn,
+// and 10^5 positions on 2^-20.)  freq, finite and below 2^20, is m 2^e in whole numbers, so its
+// whole turns and its fraction lie in m times 1 / (2 pi) to 192 bits, which is below
+// 2^-64 of a unit short.
+uint64_t turn_step(double freq) {
+  constexpr uint64_t INV_2PI[3] = {0x36d8a5664f10e410u, 0x7f09d5f47d4d3770u, 0x28be60db9391054au};   // low word first
+  if (freq == 0.) return 0;
+  int e;
+  const uint64_t m = (uint64_t)std::ldexp(std::frexp(freq, &e), 53);
+  uint64_t w[5] = {0, 0, 0, 0, 0};   // m / (2 pi) in units of 2^-192
+  unsigned __int128 sum = 0;
+  for (int i = 0; i < 3; ++i) {
+    sum += (unsigned __int128)m * INV_2PI[i];
+    w[i] = (uint64_t)sum;
+    sum >>= 64;
+  }
+  w[3] = (uint64_t)sum;
+  const int shift = 128 + 53 - e;   // from there to the result, 161 at least
+  if (shift > 256) return 0;
+  const int at = shift / 64, by = shift % 64;   // at = 4: by = 0
+  const uint64_t x = by ? w[at] >> by | w[at + 1] << (64 - by) : w[at];
+  return x + (w[(shift - 1) / 64] >> (shift - 1) % 64 & 1);
+}
+
 template <bool Q8, class Cache>
 int32_t append_rope(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q, const sub_bf16* K, int64_t ldk,
                     const sub_bf16* V, int64_t ldv, const Cache* kv, int32_t layer, const sub_batch* batch,
@@ -186,11 +212,8 @@ extern "C" int32_t sub_rope_init(int32_t head_dim, double theta, const double* f
     SUB_CHECK_ARG(freqs_host[i] >= 0.0 && freqs_host[i] <= 1e6, "freqs must be in [0, 1e6] radians");
   memset(rope, 0, sizeof(*rope));
   rope->head_dim = head_dim;
-  for (int i = 0; i < n; ++i) {
-    const double turns =
-        (freqs_host ? freqs_host[i] : std::pow(theta, -2.0 * i / head_dim)) / 6.283185307179586476925;
-    rope->step[i] = (uint64_t)std::nearbyint((turns - std::floor(turns)) * 0x1p64);   // below 2^64: 53 bits below 1
-  }
+  for (int i = 0; i < n; ++i)
+    rope->step[i] = turn_step(freqs_host ? freqs_host[i] : std::pow(theta, -2.0 * i / head_dim));
   return SUB_OK;
 }
 

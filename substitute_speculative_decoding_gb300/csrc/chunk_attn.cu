@@ -52,7 +52,6 @@
 // to the end), the block's products with V are formed one by one without the keys of
 // weight zero.
 #include <algorithm>
-#include <cmath>
 #include <type_traits>
 #include "chunk_attn.cuh"
 #include "tma.cuh"
@@ -889,30 +888,6 @@ int tile_rows(int group, int n_seqs, int n_rows, bool codes, int64_t keys) {
   const int64_t rows = (int64_t)n_rows * group, seqs = n_seqs;
   const int tiles = codes ? 4 : keys <= 4096 ? 2 : 1;
   return rows <= NARROW * seqs ? NARROW : rows <= tiles * WIDE * seqs ? WIDE : CHUNK_TC_ROWS;
-}
-
-// Trees: tiles of 32 or 64 rows of the kernel with the keys on the lanes (0: the others), by
-// the rows that a sequence has on average.  It reads the keys once where the warps' kernel has
-// several tiles (32 rows of 16 sequences over 10000 keys 116 and 157 us, over codes 86 and 149; of
-// 1 over 1000 13 and 12).  Against the 256 rows' kernel (two groups of 128, one of them idle in a
-// smaller tile): it needs more blocks of 128 keys per CTA, and is faster by the block and by the
-// call; the numbers in us were fitted to 83 shapes of 56 to 2695 rows, of which six are not
-// within 5% of the faster kernel (7 to 30% behind).  132 rows of 1 sequence over 500 keys 14 and 24 us,
-// 903 of 1 over 2000 23 and 34, 188 of 8 over 8000 90 and 81; over codes 175 of 8 over 2000 32
-// and 37, over 16000 105 and 85.  64 rows take longer per key than 32 (those 32 rows of 16
-// sequences 119 and 115 us), but a sequence of 36 rows would make two tiles of 32: they are taken
-// where all sequences may have as many rows, as the levels of trees have, or few do (28 rows on
-// average, of 20 or 36: 183 us with 32, 116 with 64).
-int tree_rows(int group, int n_seqs, int n_rows, int n_heads_kv, int64_t keys, bool codes, int n_ctas) {
-  const double rows = (double)n_rows * group / n_seqs;
-  const bool alike = n_rows % n_seqs == 0;
-  if (rows <= WIDE) return 0;
-  auto blocks = [&](int tile) {   // per CTA; a sequence's last tile is half full where rows differ
-    return (alike ? std::ceil(rows / tile) : std::max(1., rows / tile + 0.5)) * n_seqs * n_heads_kv *
-           (double)cdiv(keys, CHUNK_TC_KEYS) / n_ctas;
-  };
-  if ((codes ? 1.25 : 1.15) * blocks(64) > (codes ? 4 : 11) + 1.5 * blocks(128)) return 0;
-  return rows <= 24 || (rows <= 32 && alike) ? 32 : 64;
 }
 
 // Partial results, two per CTA, and the list of cuts.

@@ -1,5 +1,6 @@
 // Attention of a batch's new rows over a paged cache (see chunk_attn.cu).
 #pragma once
+#include <cmath>
 #include <cuda.h>
 #include "batch.cuh"
 
@@ -313,6 +314,31 @@ int32_t launch_chunk_mid(const ChunkArgs& a, bool q8, int head_dim, int rows, in
 int32_t chunk_mid_timeouts(unsigned int* out);
 // Tensor map of a bf16 pool by (row, column), in boxes of `box` rows of 64 columns.
 bool chunk_pool_map(CUtensorMap* m, const void* pool, int64_t rows, int d, int box);
+// Trees: tiles of 32 or 64 rows of the kernel with the keys on the lanes (0: the others), by
+// the rows that a sequence has on average.  It reads the keys once where the warps' kernel has
+// several tiles (32 rows of 16 sequences over 10000 keys 116 and 157 us, over codes 86 and 149; of
+// 1 over 1000 13 and 12).  Against the 256 rows' kernel (two groups of 128, one of them idle in a
+// smaller tile): it needs more blocks of 128 keys per CTA, and is faster by the block and by the
+// call; the numbers in us were fitted to 83 shapes of 56 to 2695 rows, of which six are not
+// within 5% of the faster kernel (7 to 30% behind).  132 rows of 1 sequence over 500 keys 14 and 24 us,
+// 903 of 1 over 2000 23 and 34, 188 of 8 over 8000 90 and 81; over codes 175 of 8 over 2000 32
+// and 37, over 16000 105 and 85.
+// Whether sequences have as many rows each is not known here, and rows of no sequence
+// are counted in n_rows: the average is taken in whole rows, which fewer than n_seqs of those do
+// not change.  From 24 to 32 rows: a tile of 64 costs levels of 8 nodes in 4 heads 3 to 5% of long
+// calls and 20% of short ones (16 sequences over 5000 keys 64 and 67 us, over 1300 25 and 29; over
+// codes 54 and 76), a tile of 32 costs sequences of 20 and of 36 rows, whose average is 28, 15 to
+// 40% of long calls (16 sequences over 5000 keys 77 and 67 us, 48 of them 229 and 165; over 1300
+// 30 and 29; over codes 72 and 75, 176 and 181).  So: 64 over a bf16 cache, from 48 blocks per CTA on.
+inline int tree_rows(int group, int n_seqs, int n_rows, int n_heads_kv, int64_t keys, bool codes, int n_ctas) {
+  // (not above the average: call by call, the workspace's rows go by that)
+  const double rows = n_rows < n_seqs ? (double)n_rows * group / n_seqs : (double)(n_rows / n_seqs) * group;
+  if (rows <= 16) return 0;
+  const double read_once = (double)n_seqs * n_heads_kv * (double)cdiv(keys, CHUNK_TC_KEYS) / n_ctas;
+  auto blocks = [&](int tile) { return std::ceil(rows / tile) * read_once; };   // per CTA
+  if ((codes ? 1.25 : 1.15) * blocks(64) > (codes ? 4 : 11) + 1.5 * blocks(128)) return 0;
+  return rows <= 24 || (rows <= 32 && (codes || read_once < 48)) ? 32 : 64;
+}
 // Waits that ran out in any of the kernels.
 int32_t chunk_attn_timeouts(unsigned int* out);
 // Tensor map of a pool by (page and head, place, column), in boxes of 16 places.

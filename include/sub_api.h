@@ -422,7 +422,9 @@ int32_t sub_chunk_tree_attn8(const sub_bf16* Q, int64_t ldq, int32_t n_heads_q,
  *   score[b, j] + z_v / T - log sum_w exp(z_w / T).
  * token, parent, score_out [n_seqs, n_best] get the best ones in falling order (ties: the
  * smaller beam, then the larger logit, then the smaller token): token, beam, and the score
- * rounded to fp32.  The order is decided in 64 bits, the sums of exp are fp32 terms.
+ * rounded to fp32.  A beam's own continuations are in exact order.  Scores are formed and
+ * compared in 64 bits, the sums of exp are of fp32 terms, right to 2^-16, as a rule to 2^-20:
+ * continuations of two beams whose scores are closer than that may change places.
  * A beam whose score is not finite, or whose logits hold +infinity or nothing above
  * -infinity, has no continuations; a logit of -infinity or NaN is none either.  Places
  * that stay empty get token -1, parent -1, score -infinity.

@@ -24,10 +24,14 @@
 // (Every CTA keeping the best of its part while it streams would need no second
 // reading, but a sorted list per thread costs the scan its loads in flight.)
 //
-// Rounding: terms of the sums of exp are fp32 relative to the largest logit, partial
-// sums of a thread and a CTA too; the CTAs' sums are joined, and the scores formed and
-// compared, in 64 bits, so that where two beams' candidates meet, only the error of the
-// sums (2^-23 or so) can exchange them.
+// Rounding: within a beam the order is that of the logits, exactly.  Between beams it is that of
+// scores formed and compared in 64 bits, from sums whose terms and whose parts within a CTA are fp32
+// (the CTAs' parts are joined in 64 bits).  A term 2^-e of the largest has an exponent rounded twice,
+// 2^-23 e of it, which matters up to e = 20 or so, where 2^20 terms weigh as much as the largest one:
+// 2^-19.6 of the sum.  Each exponential adds 2^-22, of a term and of a maximum that has changed, each
+// addition 2^-24: below 2^-16 if all point one way, 2^-20 as they come.  Two beams' candidates that
+// are closer than that can change places; those of equal rows, too, whose first values lie
+// unlike far from a 16-byte boundary, as their terms are added in another order.
 #include <algorithm>
 #include <atomic>
 #include "rows.cuh"

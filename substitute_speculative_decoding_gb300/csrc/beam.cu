@@ -605,7 +605,8 @@ extern "C" int32_t sub_beam_select(const float* logits, const float* score, int3
   // One launch where a CTA of a cluster has 80 blocks at most: 3 us less of the host's time, and as
   // long on the GPU (1 beam of 152064 logits 9.7 us and 9.5; 16 trees of 5 beams of 5000 13.0 and 13.8;
   // but 4 beams of 152064, 297 blocks per CTA, 13.3 and 10.4, and 64 trees of 8 of 128256 87 and 59: a
-  // cluster's SMs are few, and wait for 16 to be free at once).
+  // cluster's SMs are few, and wait for 16 to be free at once).  More than 16 sequences that the rule
+  // sends here were not timed.
   if (a.n_blocks <= 80 * (most / n_beams)) {
     const int team = (int)std::min<int64_t>(most / n_beams, cdiv(a.n_blocks, round));   // a round of loads each
     SUB_CUDA_TRY(launch_clusters(beam_kernel, n_seqs, team * n_beams, PICK_THREADS + 32, bytes, st, a, team));

@@ -37,6 +37,8 @@
 // 116 us (0.67 GB, 5.8 TB/s), over codes 86 (4.0 TB/s); 56 rows of 32 sequences and 4 KV heads over
 // 5100 68 us (5.1 TB/s); 33 nodes of 1 sequence and 8 KV heads over 500 keys 14.  A block of 128 keys
 // takes 2200 cycles over codes, of which the issue slots are busy 1240; a bf16 block at HBM's rate 2800.
+// All at pages of 64.  Pages of 16, and of 48, come in boxes of 16 keys, 24 copies of K's side of a block of
+// codes, which one lane issues in turn: the 86 us are 128 there (bf16, 56 rows: 70 and 69).
 //
 // V of a block that not all rows read to its end may hold anything where it is not read: values that
 // are not finite are taken out by the thread whose key it is, and added at the end to
